@@ -12,6 +12,9 @@ API (shapes follow the FlashQLA skill page, "Core API" / "Low-Level API"):
 * ``chunk_gated_delta_rule_bwd(q, k, v, g_cumsum, beta, A, do, ...) -> (dq, dk, dv, dbeta, dg, dh0)``
 * ``chunk_gated_delta_rule(q, k, v, g, beta, ...) -> (o, final_state)`` (autograd)
 * ``prepare_chunks(cu_seqlens, chunk_size=64) -> (chunk_indices, chunk_offsets, total_chunks)``
+
+Around the recurrence (``layer_ops``): ``rms_norm``, ``short_conv`` and ``selective_scan``, each with ``*_fwd`` and
+``*_bwd`` and, for the last two, ``*_step`` for single tokens.
 """
 
 from __future__ import annotations
@@ -22,40 +25,16 @@ from typing import Optional
 import torch
 
 from . import _lib
+from ._args import _DT, _check, _check_cu, _cu, _ptr, _stream
+from .layer_ops import (rms_norm, rms_norm_bwd, rms_norm_fwd, selective_scan, selective_scan_bwd, selective_scan_fwd,
+                        selective_scan_step, short_conv, short_conv_bwd, short_conv_fwd, short_conv_step)
 
 __all__ = ["chunk_gated_delta_rule", "chunk_gated_delta_rule_fwd", "chunk_gated_delta_rule_bwd", "saved_buffer",
-           "recurrent_gated_delta_rule", "prepare_chunks", "GdrError", "problem", "workspace_bytes"]
+           "recurrent_gated_delta_rule", "prepare_chunks", "GdrError", "problem", "workspace_bytes", "rms_norm",
+           "rms_norm_fwd", "rms_norm_bwd", "short_conv", "short_conv_fwd", "short_conv_bwd", "short_conv_step",
+           "selective_scan", "selective_scan_fwd", "selective_scan_bwd", "selective_scan_step"]
 
 GdrError = _lib.GdrError
-
-_DT = {torch.bfloat16: _lib.GDR_BF16, torch.float16: _lib.GDR_FP16, torch.float32: _lib.GDR_FP32}
-
-
-def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
-
-
-def _stream(device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-
-
-def _check(t, name, shape=None, dtype=None, like=None, optional=False, contiguous=True):
-    """The library reads and writes every tensor through a raw device pointer as a contiguous row-major array
-    of the problem's shape: anything else is refused here, before a kernel could read past its end."""
-    if t is None:
-        if optional:
-            return
-        raise ValueError(f"{name} is required")
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, the other tensors on {like.device}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
 
 
 def _check_tokens(q, k, v, g=None, beta=None):
@@ -75,13 +54,6 @@ def _check_state(t, name, p, v_first, like):
     # (states are copied to contiguous fp32 by the callers below when they are not already)
     if t is not None:
         _check(t, name, _state_shape(p, v_first), None, like, contiguous=False)
-
-
-def _check_cu(cu, q):
-    if cu is not None:
-        _check(cu, "cu_seqlens", (cu.numel(),), torch.int32, q)
-        if q.shape[0] != 1:
-            raise ValueError("a packed batch (cu_seqlens) has B = 1")
 
 
 def _check_saved(saved, p, q):
@@ -143,14 +115,6 @@ def workspace_bytes(p: _lib.Problem, backward: bool, saved=None) -> int:
 def _state_shape(p, v_first):
     N = p.num_seqs if p.cu_seqlens else p.B
     return (N, p.Hv, p.V, p.K) if v_first else (N, p.Hv, p.K, p.V)
-
-
-def _cu(cu_seqlens):
-    if cu_seqlens is None:
-        return None
-    if cu_seqlens.dtype != torch.int32:
-        cu_seqlens = cu_seqlens.to(torch.int32)
-    return cu_seqlens.contiguous()
 
 
 def saved_buffer(q, v, g, scale=None, cu_seqlens=None, use_qk_l2norm_in_kernel=False, state_v_first=False,

@@ -9,7 +9,7 @@ import threading
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libgdr.so")
 
-GDR_BF16, GDR_FP16, GDR_FP32 = 0, 1, 2
+GDR_BF16, GDR_FP16, GDR_FP32, GDR_E4M3 = 0, 1, 2, 3
 GDR_L2NORM_QK = 1 << 0
 GDR_STATE_V_FIRST = 1 << 1
 GDR_GATE_IN_KERNEL = 1 << 8
@@ -17,6 +17,8 @@ GDR_BETA_SIGMOID_IN_KERNEL = 1 << 9
 GDR_ALLOW_NEG_EIGVAL = 1 << 10
 GDR_INTER_CARD_CP = 1 << 11
 GDR_CHUNK = 64
+GDR_CONV_SILU = 1 << 0
+GDR_SCAN_DT_SOFTPLUS = 1 << 0
 
 STATUS_NAMES = {
     0: "GDR_OK", 1: "GDR_ERR_NULL", 2: "GDR_ERR_SHAPE", 3: "GDR_ERR_DTYPE", 4: "GDR_ERR_UNSUPPORTED",
@@ -28,7 +30,10 @@ STATUS_NAMES = {
 EXPORTS = ["gdr_max_chunks", "gdr_prepare_chunks", "gdr_fwd_workspace_size", "gdr_bwd_workspace_size",
            "gdr_fwd", "gdr_bwd", "gdr_get_error", "gdr_status_string", "gdr_version", "gdr_profile_enable",
            "gdr_profile_read", "gdr_fwd_noalloc", "gdr_saved_bytes", "gdr_saved_workspace_size", "gdr_fwd_ex",
-           "gdr_bwd_ex", "gdr_decode", "gdr_debug_set_wait_polls", "gdr_last_cuda_error"]
+           "gdr_bwd_ex", "gdr_decode", "gdr_debug_set_wait_polls", "gdr_last_cuda_error",
+           "gdr_norm_fwd", "gdr_norm_bwd_workspace_size", "gdr_norm_bwd",
+           "gdr_conv_fwd", "gdr_conv_step", "gdr_conv_bwd_workspace_size", "gdr_conv_bwd",
+           "gdr_scan_saved_bytes", "gdr_scan_workspace_size", "gdr_scan_fwd", "gdr_scan_step", "gdr_scan_bwd"]
 
 
 class Problem(ctypes.Structure):
@@ -37,6 +42,31 @@ class Problem(ctypes.Structure):
         ("K", ctypes.c_int), ("V", ctypes.c_int), ("dtype", ctypes.c_int), ("gate_dtype", ctypes.c_int),
         ("scale", ctypes.c_float), ("cu_seqlens", ctypes.c_void_p), ("num_seqs", ctypes.c_int),
         ("flags", ctypes.c_uint), ("num_segments", ctypes.c_int),
+    ]
+
+
+class NormProblem(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("x_ld", ctypes.c_int64), ("D", ctypes.c_int), ("dtype", ctypes.c_int),
+        ("weight_dtype", ctypes.c_int), ("residual_dtype", ctypes.c_int), ("y_dtype", ctypes.c_int),
+        ("scale_group", ctypes.c_int), ("eps", ctypes.c_float),
+    ]
+
+
+class ConvProblem(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int), ("W", ctypes.c_int), ("x_ld", ctypes.c_int64),
+        ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int), ("cu_seqlens", ctypes.c_void_p),
+        ("num_seqs", ctypes.c_int), ("flags", ctypes.c_uint),
+    ]
+
+
+class ScanProblem(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("T", ctypes.c_int), ("D", ctypes.c_int), ("N", ctypes.c_int), ("G", ctypes.c_int),
+        ("x_ld", ctypes.c_int64), ("dt_ld", ctypes.c_int64), ("z_ld", ctypes.c_int64), ("b_ld", ctypes.c_int64),
+        ("c_ld", ctypes.c_int64), ("dtype", ctypes.c_int), ("cu_seqlens", ctypes.c_void_p),
+        ("num_seqs", ctypes.c_int), ("flags", ctypes.c_uint),
     ]
 
 
@@ -105,6 +135,19 @@ def load() -> ctypes.CDLL:
         lib.gdr_profile_read.restype = i32
         lib.gdr_debug_set_wait_polls.argtypes = [ctypes.c_longlong]
         lib.gdr_debug_set_wait_polls.restype = i32
+        size_p = ctypes.POINTER(ctypes.c_size_t)
+        norm, conv, scan = (ctypes.POINTER(s) for s in (NormProblem, ConvProblem, ScanProblem))
+        for name, args in (
+                ("gdr_norm_fwd", [norm] + [P] * 7), ("gdr_norm_bwd_workspace_size", [norm, size_p]),
+                ("gdr_norm_bwd", [norm] + [P] * 8 + [ctypes.c_size_t, P]),
+                ("gdr_conv_fwd", [conv] + [P] * 7), ("gdr_conv_step", [conv] + [P] * 6),
+                ("gdr_conv_bwd_workspace_size", [conv, size_p]),
+                ("gdr_conv_bwd", [conv] + [P] * 11 + [ctypes.c_size_t, P]),
+                ("gdr_scan_saved_bytes", [scan, size_p]), ("gdr_scan_workspace_size", [scan, i32, size_p]),
+                ("gdr_scan_fwd", [scan] + [P] * 13 + [ctypes.c_size_t, P]), ("gdr_scan_step", [scan] + [P] * 11),
+                ("gdr_scan_bwd", [scan] + [P] * 22 + [ctypes.c_size_t, P])):
+            fn = getattr(lib, name)
+            fn.argtypes, fn.restype = args, i32
         lib.gdr_version.argtypes = []
         lib.gdr_version.restype = i32
         _lib = lib

@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "host.h"
 #include "launch.h"
 #include "tmap.h"
 
@@ -156,6 +157,8 @@ long long g_wait_polls = -1;  // gdr_debug_set_wait_polls (< 0: every wait keeps
 int g_dev_ok[kMaxDevices];           // 0 unknown, 1 ok, 2 wrong arch
 unsigned *g_err_ptr[kMaxDevices];    // device address of the error word
 
+}  // namespace
+
 gdr_status device_state(unsigned **err) {
     int dev = 0;
     cudaError_t ce = cudaGetDevice(&dev);
@@ -182,12 +185,11 @@ gdr_status device_state(unsigned **err) {
     return GDR_OK;
 }
 
+namespace {
+
 // the gate / beta activation options
 constexpr unsigned kActFlags = GDR_GATE_IN_KERNEL | GDR_BETA_SIGMOID_IN_KERNEL | GDR_ALLOW_NEG_EIGVAL;
 
-inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-inline size_t esize(gdr_dtype d) { return d == GDR_FP32 ? 4 : 2; }
 
 gdr_status check_problem(const gdr_problem *p) {
     if (!p) return GDR_ERR_NULL;
@@ -457,16 +459,13 @@ gdr_status check_ws(const Layout &L, void *ws, size_t bytes) {
     return GDR_OK;
 }
 
-gdr_status cuda_status(cudaError_t e) { return e == cudaSuccess ? GDR_OK : cuda_fail(e); }
-
 // ---- per-kernel timing: event pairs recorded around each launch while enabled
-enum KernelId {
-    K_PREP = 0, K_WY_FWD, K_CHAIN_FWD, K_CHAIN_FWD_RECOMPUTE, K_CHAIN_BWD, K_CHAIN_PAIR, K_BWD_CHUNK, K_CHUNK_P,
-    K_CHAIN_REV, K_GATE_ACT, K_PAD, K_ONECHUNK, K_COUNT
-};
 const char *const kKernelNames[K_COUNT] = {"prep_chunks", "wy_fwd",     "chain_fwd", "chain_fwd_recompute",
                                            "chain_bwd",   "chain_pair", "bwd_chunk", "chunk_p",
-                                           "chain_rev",   "gate_act",   "pad",       "onechunk_dg"};
+                                           "chain_rev",   "gate_act",   "pad",       "onechunk_dg",
+                                           "norm_fwd",    "norm_bwd",   "conv_fwd",  "conv_bwd",
+                                           "scan_local",  "scan_join",  "scan_fwd",  "scan_step",
+                                           "scan_bwd",    "reduce"};
 struct Pending {
     int id;
     cudaEvent_t a, b;
@@ -491,19 +490,22 @@ cudaEvent_t prof_event() {
     return e;
 }
 
-// Launch through f, bracketed by events when profiling is on.
-template <typename F>
-gdr_status timed(int id, cudaStream_t s, F &&f) {
-    cudaEvent_t a = nullptr, b = nullptr;
+}  // namespace
+
+gdr_status cuda_status(cudaError_t e) { return e == cudaSuccess ? GDR_OK : cuda_fail(e); }
+
+void prof_begin(cudaStream_t s, cudaEvent_t *a, cudaEvent_t *b) {
     {
         std::lock_guard<std::mutex> lk(g_prof.mu);
         if (g_prof.on) {
-            a = prof_event();
-            b = prof_event();
+            *a = prof_event();
+            *b = prof_event();
         }
     }
-    if (a) cudaEventRecord(a, s);
-    const cudaError_t e = f();
+    if (*a) cudaEventRecord(*a, s);
+}
+
+gdr_status prof_end(int id, cudaStream_t s, cudaEvent_t a, cudaEvent_t b, cudaError_t e) {
     if (b) {
         cudaEventRecord(b, s);
         std::lock_guard<std::mutex> lk(g_prof.mu);
@@ -513,6 +515,8 @@ gdr_status timed(int id, cudaStream_t s, F &&f) {
     if (st != GDR_OK) g_last_where = kKernelNames[id];
     return st;
 }
+
+namespace {
 
 // Build the varlen chunk tables in the workspace (no-op for dense batches).
 gdr_status tables(const gdr_problem *p, Args &a, char *ws, const Layout &L, cudaStream_t s) {

@@ -170,4 +170,8 @@ cudaError_t launch_bwd_chunk_tc(const Args &a, const void *q, const void *k, con
                                 const void *delta, const void *ddelta, void *dq, void *dk, void *dv, void *dg,
                                 void *dbeta, cudaStream_t s);
 
+// out[c] = sum over r < parts of part[r stride + c], c < cols, in a fixed order; out in bf16 / fp16 or fp32.
+cudaError_t launch_reduce_rows(const float *part, long long parts, long long stride, int cols, void *out, bool bf16,
+                               bool out_f32, cudaStream_t s);
+
 }  // namespace gdr

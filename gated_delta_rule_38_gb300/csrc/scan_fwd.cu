@@ -1,0 +1,309 @@
+// Forward of the selective state space scan (per channel d, N states; delta = softplus(dt + bias) or dt + bias):
+//
+//   h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t,   y_t = (C_t . h_t + D x_t) silu(z_t)
+//
+// The work is N exponentials and about 4 N fp32 operations a token and channel against 8 bytes of traffic, so at
+// N = 16 the kernels are bound by the special-function and fp32 pipes, not by HBM (this chip does 32 ex2 and 128 fp32
+// lanes a clock and SM: at least 4 clocks a quarter-SM for 32 (t, d, n) elements on either pipe).
+//
+// A block walks a segment of one row's tokens for a block of channels: it stages tiles of tokens in shared memory
+// (steps and inputs in fp32, each (token, channel) converted once, loads of the next tile in flight), runs the
+// recurrence with all states in registers, and writes the tile's outputs as whole vectors.  When rows x channel
+// blocks do not fill the chip the token axis is cut into segments: a first pass leaves every segment's end state from
+// a zero start and its sum of delta, a scan over the segments joins them (a segment multiplies its start state by
+// exp(A sum delta)), and the second pass starts from the joined states.
+#include "scan.cuh"
+
+namespace gdr {
+namespace scan {
+namespace {
+
+template <int L>
+struct Fwd {
+    static constexpr int NP = 4 * L;                    // padded states
+    static constexpr int CB = 512 / L;                  // channels a block
+    static constexpr int TT = L >= 4 ? 16 : 4 * L;      // tokens a tile
+    static constexpr int NVEC = TT * CB / 8;            // 8-channel vectors of a tile
+    static constexpr int VPT = NVEC > 128 ? NVEC / 128 : 1;
+    static constexpr int BPT = TT * NP > 128 ? TT * NP / 128 : 1;
+};
+
+template <int L>
+struct FwdSmem {
+    float delta[Fwd<L>::TT][Fwd<L>::CB];
+    float u[Fwd<L>::TT][Fwd<L>::CB];                    // delta x
+    float y[Fwd<L>::TT][Fwd<L>::CB];
+    float b[Fwd<L>::TT][Fwd<L>::NP][2];
+    float c[Fwd<L>::TT][Fwd<L>::NP][2];
+    int first[Fwd<L>::TT], last[Fwd<L>::TT];
+};
+
+// FULL: the outputs (second pass, or the only one).  Otherwise the first pass over segments.
+template <typename T, int L, bool FULL, bool PACKED>
+__global__ void __launch_bounds__(128) scan_fwd_kernel(const ScanArgs a) {
+    using F = Fwd<L>;
+    constexpr int CB = F::CB, TT = F::TT, NP = F::NP;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    FwdSmem<L> &sm = *reinterpret_cast<FwdSmem<L> *>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int nl = lane % L, cl = lane / L;
+    const int segs = FULL ? a.nseg : a.nseg - 1;        // (the last segment's end state joins nothing)
+    const int nblk = a.gblocks * a.G;
+    const int blk = blockIdx.x % nblk, rest = blockIdx.x / nblk;
+    const int s = rest % segs, b = rest / segs;
+    const Chans<CB> ch(a, blk);
+    const int c0 = warp * (128 / L) + cl * 4, n0 = nl * 4;  // this thread's channels (in the block) and states
+    const int nc = ch.count - c0;
+    const int t0 = s * a.seglen, t1 = min(a.T, t0 + a.seglen);
+    if (PACKED && FULL && blockIdx.x == 0) check_cu(a.cu, a.nseq, a.T, a.err);
+
+    State A2, h;
+    load_rows(a, a.A + (long long)(ch.first + c0) * a.N, nc, n0, A2, LOG2E);
+    const long long segpos = ((long long)b * a.nseg + s) * NP + n0;
+    if (FULL && s > 0)
+        load_padded(a.seg + (segpos - NP) * a.DP + ch.pad + c0, a.DP, h);
+    else if (FULL && !PACKED && a.state_in)
+        load_rows(a, a.state_in + ((long long)b * a.D + ch.first + c0) * a.N, nc, n0, h);
+    else
+        zero(h);
+    f2 sum_lo = 0ull, sum_hi = 0ull;
+    bool cut = false;
+
+    // this thread's vectors of a tile: token vt + k VSTEP, channels vc ..
+    constexpr int VROW = CB / 8, VSTEP = 128 / VROW > 0 ? 128 / VROW : 1;
+    const int vc = (tid % VROW) * 8, vt = tid / VROW;
+    const bool vlive = F::NVEC >= 128 || tid < F::NVEC;
+    const int vn = ch.count - vc;
+    float bias[8], skip[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        bias[i] = (a.bias && i < vn) ? a.bias[ch.first + vc + i] : 0.f;
+        skip[i] = (FULL && a.skip && i < vn) ? a.skip[ch.first + vc + i] : 0.f;
+    }
+    uint4 rx[F::VPT], rd[F::VPT], rz[F::VPT];
+    uint16_t rb[F::BPT], rc[F::BPT];
+    auto fetch = [&](int base) {
+        if (base >= t1) return;
+#pragma unroll
+        for (int k = 0; k < F::VPT; ++k) {
+            const int t = base + vt + k * VSTEP;
+            rx[k] = rd[k] = rz[k] = make_uint4(0, 0, 0, 0);
+            if (vlive && t < t1 && vn > 0) {
+                const long long row = (long long)b * a.T + t;
+                const int c = ch.first + vc;
+                rx[k] = load8(static_cast<const uint16_t *>(a.x) + row * a.x_ld + c, vn, a.vec);
+                rd[k] = load8(static_cast<const uint16_t *>(a.dt) + row * a.dt_ld + c, vn, a.vec);
+                if (FULL && a.z) rz[k] = load8(static_cast<const uint16_t *>(a.z) + row * a.z_ld + c, vn, a.vec);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < F::BPT; ++k) {
+            const int i = tid + k * 128, t = base + i / NP, n = i % NP;
+            rb[k] = rc[k] = 0;
+            if (i < TT * NP && t < t1 && n < a.N) {
+                const long long row = (long long)b * a.T + t;
+                rb[k] = static_cast<const uint16_t *>(a.Bm)[row * a.b_ld + ch.g * a.N + n];
+                if (FULL) rc[k] = static_cast<const uint16_t *>(a.Cm)[row * a.c_ld + ch.g * a.N + n];
+            }
+        }
+    };
+    auto to_f = [](uint16_t v) { return Elt<T>::to_f(*reinterpret_cast<const T *>(&v)); };
+
+    fetch(t0);
+    for (int base = t0; base < t1; base += TT) {
+        // stage the tile
+        uint4 x_now[F::VPT], z_now[F::VPT];
+#pragma unroll
+        for (int k = 0; k < F::VPT; ++k) {
+            x_now[k] = rx[k], z_now[k] = rz[k];
+            if (!vlive) continue;
+            float x[8], d[8], u[8];
+            widen8<T>(rx[k], x);
+            widen8<T>(rd[k], d);
+            const bool in = base + vt + k * VSTEP < t1;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                d[i] += bias[i];
+                if (a.softplus) d[i] = softplus(d[i]);
+                d[i] = in && i < vn ? d[i] : 0.f;  // past the end: a step of zero, which changes nothing
+                u[i] = d[i] * x[i];
+            }
+            put8(&sm.delta[vt + k * VSTEP][vc], d);
+            put8(&sm.u[vt + k * VSTEP][vc], u);
+        }
+#pragma unroll
+        for (int k = 0; k < F::BPT; ++k) {
+            const int i = tid + k * 128;
+            if (i < TT * NP) {
+                const float vb = to_f(rb[k]);
+                *reinterpret_cast<float2 *>(sm.b[i / NP][i % NP]) = make_float2(vb, vb);
+                if (FULL) {
+                    const float v = to_f(rc[k]);
+                    *reinterpret_cast<float2 *>(sm.c[i / NP][i % NP]) = make_float2(v, v);
+                }
+            }
+        }
+        if (PACKED && tid < TT) edges(a, base + tid, t1, sm.first[tid], sm.last[tid]);
+        __syncthreads();
+        fetch(base + TT);
+        if (FULL && a.saved && base % SAVE == 0)
+            store_padded(a.saved + (((long long)b * ((a.T + SAVE - 1) / SAVE) + base / SAVE) * NP + n0) * a.DP + ch.pad + c0,
+                         a.DP, h);
+#pragma unroll 4
+        for (int j = 0; j < TT; ++j) {
+            if (PACKED) {
+                const int n = sm.first[j];
+                if (n >= 0) {
+                    cut = true;
+                    if (a.state_in)
+                        load_rows(a, a.state_in + ((long long)n * a.D + ch.first + c0) * a.N, nc, n0, h);
+                    else
+                        zero(h);
+                }
+            }
+            const F2x2 d = lds_f2x2(&sm.delta[j][c0]), u = lds_f2x2(&sm.u[j][c0]);
+            f2 y_lo = 0ull, y_hi = 0ull;
+#pragma unroll
+            for (int n = 0; n < 4; n += 2) {
+                const F2x2 bb = lds_f2x2(sm.b[j][n0 + n]);
+                const F2x2 cc = FULL ? lds_f2x2(sm.c[j][n0 + n]) : F2x2{0ull, 0ull};
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    const f2 bn = m ? bb.hi : bb.lo, cn = m ? cc.hi : cc.lo;
+                    f2 *hn = h[n + m];
+                    hn[0] = fma2(exp2x2(mul2(A2[n + m][0], d.lo)), hn[0], mul2(u.lo, bn));
+                    hn[1] = fma2(exp2x2(mul2(A2[n + m][1], d.hi)), hn[1], mul2(u.hi, bn));
+                    if (FULL) {
+                        y_lo = fma2(hn[0], cn, y_lo);
+                        y_hi = fma2(hn[1], cn, y_hi);
+                    }
+                }
+            }
+            if (FULL) {
+                float y[LaneSum<L>::R];
+                LaneSum<L>::run(y_lo, y_hi, nl, y);
+                if (LaneSum<L>::keeper(nl))
+#pragma unroll
+                    for (int i = 0; i < LaneSum<L>::R; ++i) sm.y[j][c0 + LaneSum<L>::at(nl) + i] = y[i];
+            } else {
+                sum_lo = add2(sum_lo, d.lo);
+                sum_hi = add2(sum_hi, d.hi);
+            }
+            if (PACKED && FULL) {
+                const int n = sm.last[j];
+                if (n >= 0 && a.state_out)
+                    store_rows(a, a.state_out + ((long long)n * a.D + ch.first + c0) * a.N, nc, n0, h);
+            }
+        }
+        __syncthreads();
+        if (FULL) {
+#pragma unroll
+            for (int k = 0; k < F::VPT; ++k) {
+                const int t = base + vt + k * VSTEP;
+                if (!vlive || t >= t1 || vn <= 0) continue;
+                float y[8], x[8], z[8];
+                get8(&sm.y[vt + k * VSTEP][vc], y);
+                widen8<T>(x_now[k], x);
+                widen8<T>(z_now[k], z);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    y[i] = fmaf(skip[i], x[i], y[i]);
+                    if (a.z) y[i] *= z[i] * sigmoid(z[i]);
+                }
+                store8(static_cast<uint16_t *>(a.y) + ((long long)b * a.T + t) * a.D + ch.first + vc, narrow8<T>(y), vn, a.vec);
+            }
+        }
+    }
+    if (FULL) {
+        if (!PACKED && a.state_out && s == a.nseg - 1)
+            store_rows(a, a.state_out + ((long long)b * a.D + ch.first + c0) * a.N, nc, n0, h);
+        return;
+    }
+    store_padded(a.seg + segpos * a.DP + ch.pad + c0, a.DP, h);
+    if (nl == 0) {
+        ulonglong2 v;
+        v.x = sum_lo, v.y = sum_hi;
+        *reinterpret_cast<ulonglong2 *>(a.segdt + ((long long)b * a.nseg + s) * a.DP + ch.pad + c0) = v;
+    }
+    if (PACKED && blk == 0 && tid == 0) a.cut[s] = cut;
+}
+
+// Joins the segments: seg[s] becomes the state at the end of segment s (forward) or the gradient that leaves segment
+// s at its start (reverse, from the last segment down), for every padded (state, channel) of a row.
+template <int NP>
+__global__ void __launch_bounds__(128) scan_join_kernel(const ScanArgs a, const float *start, bool reverse) {
+    const int pc = blockIdx.x * 128 + threadIdx.x, n = blockIdx.y % NP, b = blockIdx.y / NP;
+    if (pc >= a.DP) return;
+    const int g = pc / a.gpad, in = pc - g * a.gpad;
+    const bool live = in < a.Dg && n < a.N;
+    const int c = g * a.Dg + in;
+    const float A2 = live ? a.A[(long long)c * a.N + n] * LOG2E : 0.f;
+    float h = (live && start) ? start[((long long)b * a.D + c) * a.N + n] : 0.f;
+    for (int i = 0; i < a.nseg - 1; ++i) {
+        const int s = reverse ? a.nseg - 1 - i : i;
+        const long long at = (long long)b * a.nseg + s;
+        float *p = a.seg + (at * NP + n) * a.DP + pc;
+        const float through = (a.cut && a.cut[s]) ? 0.f : ex2(A2 * a.segdt[at * a.DP + pc]);
+        h = fmaf(through, h, *p);
+        *p = h;
+    }
+}
+
+// Sequences without tokens pass their states through.
+__global__ void __launch_bounds__(256) scan_empty_kernel(const int32_t *cu, long long per, const float *src, float *dst) {
+    const long long n = blockIdx.x;
+    if (cu[n] != cu[n + 1]) return;
+    for (long long i = threadIdx.x; i < per; i += 256) dst[n * per + i] = src ? src[n * per + i] : 0.f;
+}
+
+template <typename T, int L, bool FULL, bool PACKED>
+cudaError_t launch_one(const ScanArgs &a, cudaStream_t s) {
+    const int segs = FULL ? a.nseg : a.nseg - 1;
+    const long long blocks = (long long)a.gblocks * a.G * segs * a.B;
+    auto k = scan_fwd_kernel<T, L, FULL, PACKED>;
+    const size_t smem = sizeof(FwdSmem<L>);
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_plain(k, dim3((unsigned)blocks), dim3(128), smem, s, a);
+}
+template <typename T, int L>
+cudaError_t launch_l(const ScanArgs &a, bool full, cudaStream_t s) {
+    if (full) return a.cu ? launch_one<T, L, true, true>(a, s) : launch_one<T, L, true, false>(a, s);
+    return a.cu ? launch_one<T, L, false, true>(a, s) : launch_one<T, L, false, false>(a, s);
+}
+template <typename T>
+cudaError_t launch_t(const ScanArgs &a, int L, bool full, cudaStream_t s) {
+    switch (L) {
+        case 1: return launch_l<T, 1>(a, full, s);
+        case 2: return launch_l<T, 2>(a, full, s);
+        case 4: return launch_l<T, 4>(a, full, s);
+        case 8: return launch_l<T, 8>(a, full, s);
+        default: return launch_l<T, 16>(a, full, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_scan_fwd(const ScanArgs &a, int L, bool bf16, bool full, cudaStream_t s) {
+    return bf16 ? launch_t<__nv_bfloat16>(a, L, full, s) : launch_t<__half>(a, L, full, s);
+}
+
+cudaError_t launch_scan_join(const ScanArgs &a, int L, const float *start, bool reverse, cudaStream_t s) {
+    const dim3 grid((a.DP + 127) / 128, (unsigned)(4 * L * a.B));
+    switch (L) {
+        case 1: return launch_plain(scan_join_kernel<4>, grid, dim3(128), 0, s, a, start, reverse);
+        case 2: return launch_plain(scan_join_kernel<8>, grid, dim3(128), 0, s, a, start, reverse);
+        case 4: return launch_plain(scan_join_kernel<16>, grid, dim3(128), 0, s, a, start, reverse);
+        case 8: return launch_plain(scan_join_kernel<32>, grid, dim3(128), 0, s, a, start, reverse);
+        default: return launch_plain(scan_join_kernel<64>, grid, dim3(128), 0, s, a, start, reverse);
+    }
+}
+
+cudaError_t launch_scan_empty(const ScanArgs &a, const float *src, float *dst, cudaStream_t s) {
+    return launch_plain(scan_empty_kernel, dim3(a.nseq), dim3(256), 0, s, a.cu, (long long)a.D * a.N, src, dst);
+}
+
+}  // namespace scan
+}  // namespace gdr

@@ -84,7 +84,12 @@ typedef enum gdr_status {
     GDR_ERR_INTERNAL = 11
 } gdr_status;
 
-typedef enum gdr_dtype { GDR_BF16 = 0, GDR_FP16 = 1, GDR_FP32 = 2 } gdr_dtype;
+typedef enum gdr_dtype {
+    GDR_BF16 = 0,
+    GDR_FP16 = 1,
+    GDR_FP32 = 2,
+    GDR_E4M3 = 3 /* 8-bit floats (the norm's output only) */
+} gdr_dtype;
 
 /* gdr_problem.flags */
 #define GDR_L2NORM_QK              (1u << 0)  /* use_qk_l2norm_in_kernel */
@@ -272,6 +277,136 @@ gdr_status gdr_fwd_noalloc(const gdr_problem *p, const void *q, const void *k, c
  */
 gdr_status gdr_decode(const gdr_problem *p, const void *q, const void *k, const void *v, const void *g,
                       const void *beta, const float *state_in, float *state_out, void *o, void *stream);
+
+/*
+ * The operators around the recurrence: a root-mean-square norm in front of a layer, the
+ * short causal convolution of its q, k, v (or x) channels, and the selective state space
+ * scan, the diagonal sibling of the delta rule (no counterpart on the pages: additions of
+ * this library).  They differ from the conventions above in two points: the tensors that
+ * a layer slices out of a fused projection may have a row stride (`*_ld`, elements between
+ * the rows of consecutive tokens, batch rows following one another; all other tensors are
+ * contiguous), and every pointer must be aligned to its own elements only
+ * (GDR_ERR_ALIGN otherwise; 16-byte aligned data with sizes and strides in multiples of
+ * 8 elements takes the wide path).
+ */
+
+/*
+ * Root-mean-square norm of rows, with the residual's addition and an 8-bit output.
+ *   h = x + residual;  y = h / sqrt(mean(h^2) + eps) * weight
+ *   in : x [rows, D] (dtype, row stride x_ld); weight [D] (weight_dtype: dtype or fp32);
+ *        residual [rows, D] (residual_dtype: dtype or fp32) or NULL
+ *   out: y [rows, D]: dtype, or e4m3 (y_dtype = GDR_E4M3) as the values y / scale
+ *        residual_out [rows, D] = h in residual_dtype (with a residual; may be `residual`)
+ *        scale (e4m3) [rows] (scale_group = 0) or [rows, ceil(D / 128)] (scale_group = 128):
+ *          max(max |y|, 1e-30) / 448 over the row or over each 128 columns
+ * y is computed from the unrounded sum.  A NaN in a scale's columns makes the scale and
+ * its values NaN.  rows = 0 is valid.  1 <= D <= GDR_NORM_MAX_D.
+ * Backward at h (the stored sum, or x without a residual; type residual_dtype, row stride
+ * x_ld): with r = 1 / sqrt(mean(h^2) + eps),
+ *   dh = r (weight dy - h r^2 mean(weight dy h)) + dresidual,  dweight = sum_rows dy h r
+ *   in : h, weight, dy [rows, D] (dtype), dresidual [rows, D] (residual_dtype) or NULL
+ *   out: dx [rows, D] = dh in dtype; dresidual_in [rows, D] = dh in fp32 (only with an fp32
+ *        residual; nullable); dweight [D] (weight_dtype).  Fixed summation order.
+ */
+#define GDR_NORM_MAX_D 16384
+typedef struct gdr_norm_problem {
+    int64_t rows, x_ld;
+    int D;
+    gdr_dtype dtype;          /* bf16 or fp16: x, dy, dx (and y) */
+    gdr_dtype weight_dtype;   /* dtype or GDR_FP32 */
+    gdr_dtype residual_dtype; /* dtype or GDR_FP32 */
+    gdr_dtype y_dtype;        /* dtype or GDR_E4M3 */
+    int scale_group;          /* 0 or 128 */
+    float eps;
+} gdr_norm_problem;
+gdr_status gdr_norm_fwd(const gdr_norm_problem *p, const void *x, const void *weight, const void *residual, void *y,
+                        void *residual_out, float *scale, void *stream);
+gdr_status gdr_norm_bwd_workspace_size(const gdr_norm_problem *p, size_t *bytes);
+gdr_status gdr_norm_bwd(const gdr_norm_problem *p, const void *h, const void *weight, const void *dy,
+                        const void *dresidual, void *dx, float *dresidual_in, void *dweight, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
+/*
+ * Short causal convolution: every channel with its own W taps (2 <= W <= 4), optionally
+ * through SiLU (GDR_CONV_SILU).
+ *   pre_t = bias + sum_{j<W} weight[:, W-1-j] x_{t-j};  y = pre  or  pre sigmoid(pre)
+ *   in : x [B,T,D] (dtype, row stride x_ld), weight [D,W], bias [D] or NULL (weight_dtype:
+ *        dtype or fp32); state_in [N,W-1,D] (dtype): the inputs before each sequence's
+ *        first token, oldest first, or NULL (zeros)
+ *   out: y [B,T,D]; state_out [N,W-1,D]: the last W-1 inputs of each sequence (reaching
+ *        back into state_in for short ones), or NULL.  Not state_in itself.
+ * Packed batches (cu_seqlens) as in gdr_fwd: B = 1, N = num_seqs.  A malformed cu_seqlens
+ * latches GDR_ERR_CUSEQLENS; the outputs are then unspecified, and nothing outside the
+ * given buffers is touched.  T = 0 passes the states through.
+ * gdr_conv_step: dense rows only; the states are updated in place.  Meant for T = 1 or a
+ * few tokens (one thread walks all tokens of its channels).
+ * Backward: dy [B,T,D], dstate_out [N,W-1,D] or NULL (zeros) -> dx [B,T,D], dweight, dbias
+ * (weight_dtype; dbias nullable, only with a bias), dstate_in [N,W-1,D] (nullable).
+ * Fixed summation order.
+ */
+#define GDR_CONV_SILU (1u << 0)
+typedef struct gdr_conv_problem {
+    int B, T, D, W;
+    int64_t x_ld;
+    gdr_dtype dtype, weight_dtype;
+    const int32_t *cu_seqlens; /* DEVICE int32 [num_seqs+1] or NULL for dense */
+    int num_seqs;
+    unsigned flags;
+} gdr_conv_problem;
+gdr_status gdr_conv_fwd(const gdr_conv_problem *p, const void *x, const void *weight, const void *bias,
+                        const void *state_in, void *y, void *state_out, void *stream);
+gdr_status gdr_conv_step(const gdr_conv_problem *p, const void *x, const void *weight, const void *bias, void *state,
+                         void *y, void *stream);
+gdr_status gdr_conv_bwd_workspace_size(const gdr_conv_problem *p, size_t *bytes);
+gdr_status gdr_conv_bwd(const gdr_conv_problem *p, const void *x, const void *weight, const void *bias, const void *dy,
+                        const void *state_in, const void *dstate_out, void *dx, void *dweight, void *dbias,
+                        void *dstate_in, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Selective state space scan: per channel d with N states (1 <= N <= GDR_SCAN_MAX_N),
+ *   delta_t = dt_t + dt_bias (through softplus with GDR_SCAN_DT_SOFTPLUS)
+ *   h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t        (fp32)
+ *   y_t = (C_t . h_t + D x_t) * z_t sigmoid(z_t)           (D, z: optional)
+ *   in : x, dt, z [B,T,D] (dtype, row strides x_ld, dt_ld, z_ld; z nullable); A [D,N],
+ *        D [D], dt_bias [D] fp32 (the last two nullable); B, C [B,T,G,N] (dtype, row
+ *        strides b_ld, c_ld; channel d reads group d / (D/G)); state_in [num_seqs or B,D,N]
+ *        fp32 or NULL (zeros)
+ *   out: y [B,T,D] (dtype); state_out, as state_in, or NULL (not state_in itself);
+ *        saved: NULL, or a buffer of gdr_scan_saved_bytes bytes (16-byte aligned) that the
+ *        backward reads: the states before every 16 tokens, 4 N / 16 bytes a token and
+ *        channel (N and the channels of a group padded)
+ * Packed batches and malformed cu_seqlens as in gdr_conv_fwd.  T = 0 passes the states
+ * through.  Rows and channels that do not fill the chip are cut along the tokens into
+ * segments whose states are joined (workspace: gdr_scan_workspace_size, 256-byte aligned).
+ * gdr_scan_step: dense rows, the states updated in place; meant for T = 1 or a few tokens.
+ * Backward: dy [B,T,D], dstate_out or NULL (zeros), saved -> dx, ddt, dz [B,T,D], dB, dC
+ * [B,T,G,N] (dtype), dA, dD, ddt_bias, dstate_in (fp32; dstate_in nullable; dD, dz and
+ * ddt_bias exactly when D, z and dt_bias are given).  Fixed summation order.
+ */
+#define GDR_SCAN_MAX_N 64
+#define GDR_SCAN_DT_SOFTPLUS (1u << 0)
+typedef struct gdr_scan_problem {
+    int B, T, D, N, G;
+    int64_t x_ld, dt_ld, z_ld, b_ld, c_ld;
+    gdr_dtype dtype;
+    const int32_t *cu_seqlens; /* DEVICE int32 [num_seqs+1] or NULL for dense */
+    int num_seqs;
+    unsigned flags;
+} gdr_scan_problem;
+gdr_status gdr_scan_saved_bytes(const gdr_scan_problem *p, size_t *bytes);
+gdr_status gdr_scan_workspace_size(const gdr_scan_problem *p, int backward, size_t *bytes);
+gdr_status gdr_scan_fwd(const gdr_scan_problem *p, const void *x, const void *dt, const float *A, const void *B,
+                        const void *C, const float *D, const void *z, const float *dt_bias, const float *state_in,
+                        void *y, float *state_out, void *saved, void *workspace, size_t workspace_bytes,
+                        void *stream);
+gdr_status gdr_scan_step(const gdr_scan_problem *p, const void *x, const void *dt, const float *A, const void *B,
+                         const void *C, const float *D, const void *z, const float *dt_bias, float *state, void *y,
+                         void *stream);
+gdr_status gdr_scan_bwd(const gdr_scan_problem *p, const void *x, const void *dt, const float *A, const void *B,
+                        const void *C, const float *D, const void *z, const float *dt_bias, const void *dy,
+                        const float *state_in, const float *dstate_out, const void *saved, void *dx, void *ddt,
+                        float *dA, void *dB, void *dC, float *dD, void *dz, float *ddt_bias, float *dstate_in,
+                        void *workspace, size_t workspace_bytes, void *stream);
 
 /* Synchronises `stream`, then returns and clears the device error word of the
  * current device (GDR_OK when no kernel latched an error), or GDR_ERR_CUDA when
