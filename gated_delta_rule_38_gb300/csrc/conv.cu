@@ -7,13 +7,14 @@
 // Inputs before a sequence's first token are its W - 1 cached ones (state [N, W-1, D]) or zeros; their gradients
 // come out as if they were tokens of it.
 //
-// A thread walks TT tokens of VEC channels with the last W - 1 inputs (backward: also the W - 1 open sums of dx) in
+// A thread walks TT tokens of 4 channels with the last W - 1 inputs (backward: also the W - 1 open sums of dx) in
 // registers, so every element is read and written once but for W - 1 tokens of overlap between neighbouring walks:
 // the kernels are bound by HBM.  A block is 32 lanes along the channels (one contiguous row segment a warp) by 8
 // walks.  All sums are fp32.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "host.h"
 #include "launch.h"
 #include "seqwalk.cuh"
@@ -22,231 +23,445 @@ namespace gdr {
 namespace {
 
 constexpr int WALKS = 8;  // walks (warps) of a block
+constexpr int NC = 4;     // channels a thread
 
 struct ConvArgs {
     const void *x, *w, *bias, *state_in;
     void *y, *state_out;
     const void *dy, *dstate_out;   // backward: gradients of y and of the final states
     void *dx, *dstate_in;
-    float *dw_part, *db_part;      // backward: [blocks along the tokens][D * W] and [..][D]
+    float *part;                   // backward: [blocks along the tokens][D * W | D]
     const int32_t *cu;
     unsigned *err;
     long long x_ld;
     int B, T, D, N;
     int tt, tiles, cblocks;        // tokens a walk; walks a row; blocks along the channels
-    bool w_f32, silu;
+    uint32_t tiles_m, cblocks_m;   // (divisors as multiply-high, see Geo::div_hq)
+    int tiles_s, cblocks_s;
+    bool w_f32, w_wide, silu;
 };
 
-// N consecutive parameters of type T or fp32 as fp32.
-template <typename T, int N>
-__device__ __forceinline__ void load_params(const void *p, long long at, bool f32, float *o) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = load_gate<T>(p, at + i, f32);
-}
+// A thread's NC channels: NC consecutive ones from one access (WIDE), or, where rows are not aligned for that, every
+// 32nd, so that the lanes of a warp still read and write contiguous elements.
+template <int NC, bool WIDE>
+struct Lane {
+    int c;  // first channel
+    int D;
+    __device__ __forceinline__ int chan(int i) const { return WIDE ? c + i : c + 32 * i; }
+    __device__ __forceinline__ bool has(int i) const { return WIDE || chan(i) < D; }
+};
 
-template <typename T, int VEC>
-__device__ __forceinline__ void load_x(const T *p, float *o) {
-    if constexpr (VEC == 8) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t r[4] = {u.x, u.y, u.z, u.w};
+// The raw elements of one token: NC / 2 words of two channels each, or (narrow) one register an element, so that
+// nothing waits for a load before its use.
+template <int NC, bool WIDE>
+struct Raw {
+    uint32_t w[WIDE ? NC / 2 : NC];
+    __device__ __forceinline__ void load(const uint16_t *p, const Lane<NC, WIDE> &l) {  // p: the token's row
+        if constexpr (WIDE) {
+            if constexpr (NC == 4) {
+                const uint2 u = *reinterpret_cast<const uint2 *>(p + l.c);
+                w[0] = u.x, w[1] = u.y;
+            } else {
+                w[0] = *reinterpret_cast<const uint32_t *>(p + l.c);
+            }
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = Elt<T>::unpack(r[i]);
-            o[2 * i] = f.x, o[2 * i + 1] = f.y;
+            for (int i = 0; i < NC; ++i) w[i] = l.has(i) ? p[l.chan(i)] : 0;
         }
-    } else if constexpr (VEC == 4) {
-        const uint2 u = *reinterpret_cast<const uint2 *>(p);
-        const float2 f = Elt<T>::unpack(u.x), g = Elt<T>::unpack(u.y);
-        o[0] = f.x, o[1] = f.y, o[2] = g.x, o[3] = g.y;
-    } else {
-        o[0] = Elt<T>::to_f(p[0]);
     }
+    template <typename T>
+    __device__ __forceinline__ void widen(f2 *o) const {
+#pragma unroll
+        for (int i = 0; i < NC / 2; ++i) o[i] = widen2<T>(WIDE ? w[i] : w[2 * i % (WIDE ? NC / 2 : NC)] | w[(2 * i + 1) % (WIDE ? NC / 2 : NC)] << 16);
+    }
+};
+template <typename T, int NC, bool WIDE>
+__device__ __forceinline__ void load_x(const void *p, long long row, const Lane<NC, WIDE> &l, f2 *o) {  // contiguous rows
+    Raw<NC, WIDE> r;
+    r.load(static_cast<const uint16_t *>(p) + row * l.D, l);
+    r.template widen<T>(o);
 }
-template <typename T, int VEC>
-__device__ __forceinline__ void store_x(T *p, const float *v) {
-    if constexpr (VEC == 8) {
-        uint4 u;
-        u.x = Elt<T>::pack(v[0], v[1]), u.y = Elt<T>::pack(v[2], v[3]);
-        u.z = Elt<T>::pack(v[4], v[5]), u.w = Elt<T>::pack(v[6], v[7]);
-        *reinterpret_cast<uint4 *>(p) = u;
-    } else if constexpr (VEC == 4) {
-        *reinterpret_cast<uint2 *>(p) = make_uint2(Elt<T>::pack(v[0], v[1]), Elt<T>::pack(v[2], v[3]));
+template <typename T, int NC, bool WIDE>
+__device__ __forceinline__ void store_at(uint16_t *p, const Lane<NC, WIDE> &l, const f2 *v) {  // p: the token's row
+    uint32_t w[NC / 2];
+#pragma unroll
+    for (int i = 0; i < NC / 2; ++i) w[i] = narrow2<T>(v[i]);
+    if constexpr (WIDE) {
+        if constexpr (NC == 4)
+            *reinterpret_cast<uint2 *>(p + l.c) = make_uint2(w[0], w[1]);
+        else
+            *reinterpret_cast<uint32_t *>(p + l.c) = w[0];
     } else {
-        p[0] = Elt<T>::from_f(v[0]);
+#pragma unroll
+        for (int i = 0; i < NC; ++i)
+            if (l.has(i)) p[l.chan(i)] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
     }
 }
 
-__device__ __forceinline__ float sigmoid_fast(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+template <typename T, int NC, bool WIDE>
+__device__ __forceinline__ void store_x(void *base, long long row, const Lane<NC, WIDE> &l, const f2 *v) {
+    store_at<T, NC, WIDE>(static_cast<uint16_t *>(base) + row * l.D, l, v);
+}
+
+// Taps w[j] (of the input j tokens back) and bias.
+template <typename T, int NC, int W, bool WIDE>
+struct Taps {
+    f2 w[W][NC / 2], bias[NC / 2];
+    __device__ __forceinline__ void load(const ConvArgs &a, const Lane<NC, WIDE> &l) {
+        float v[NC * W], b[NC];
+        if (WIDE && !a.w_f32 && a.w_wide) {  // NC W consecutive elements
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(a.w) + (long long)l.c * W);
+            uint32_t u[NC * W / 2];
+#pragma unroll
+            for (int i = 0; i < NC * W / 2; i += 2) {
+                if constexpr (NC == 4) {
+                    const uint2 q = *reinterpret_cast<const uint2 *>(p + i);
+                    u[i] = q.x, u[i + 1] = q.y;
+                } else {
+                    u[i] = p[i];
+                    if (i + 1 < NC * W / 2) u[i + 1] = p[i + 1];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < NC * W / 2; ++i) unpack2(widen2<T>(u[i]), v[2 * i], v[2 * i + 1]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NC * W; ++i)
+                v[i] = l.has(i / W) ? load_gate<T>(a.w, (long long)l.chan(i / W) * W + i % W, a.w_f32) : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < NC; ++i) b[i] = (a.bias && l.has(i)) ? load_gate<T>(a.bias, l.chan(i), a.w_f32) : 0.f;
+#pragma unroll
+        for (int i = 0; i < NC / 2; ++i) {
+#pragma unroll
+            for (int j = 0; j < W; ++j) w[j][i] = pack2(v[2 * i * W + W - 1 - j], v[(2 * i + 1) * W + W - 1 - j]);
+            bias[i] = pack2(b[2 * i], b[2 * i + 1]);
+        }
+    }
+    // pre of pair i at input x with the W - 1 inputs before it in xs (nearest first)
+    __device__ __forceinline__ f2 pre(int i, f2 x, const f2 (*xs)[NC / 2]) const {
+        f2 p = fma2(w[0][i], x, bias[i]);
+#pragma unroll
+        for (int j = 1; j < W; ++j) p = fma2(w[j][i], xs[j - 1][i], p);
+        return p;
+    }
+};
+
+template <int NC, int W>
+__device__ __forceinline__ void push(f2 (*xs)[NC / 2], const f2 *x) {
+#pragma unroll
+    for (int j = W - 1; j > 1; --j)
+#pragma unroll
+        for (int i = 0; i < NC / 2; ++i) xs[j - 1][i] = xs[j - 2][i];
+#pragma unroll
+    for (int i = 0; i < NC / 2; ++i) xs[0][i] = x[i];
+}
 
 // The cached inputs of sequence n (zeros without them): xs[j-1] = input j tokens before its first.
-template <typename T, int VEC, int W>
-__device__ __forceinline__ void cached_inputs(const ConvArgs &a, long long n, int c, float (*xs)[VEC]) {
+template <typename T, int NC, int W, bool WIDE>
+__device__ __forceinline__ void cached_inputs(const ConvArgs &a, long long n, const Lane<NC, WIDE> &l, f2 (*xs)[NC / 2]) {
 #pragma unroll
     for (int j = 1; j < W; ++j) {
         if (a.state_in) {
-            load_x<T, VEC>(static_cast<const T *>(a.state_in) + (n * (W - 1) + (W - 1 - j)) * a.D + c, xs[j - 1]);
+            load_x<T, NC, WIDE>(a.state_in, n * (W - 1) + (W - 1 - j), l, xs[j - 1]);
         } else {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) xs[j - 1][i] = 0.f;
+            for (int i = 0; i < NC / 2; ++i) xs[j - 1][i] = 0ull;
         }
     }
 }
 
-// The W - 1 inputs before token t0 of a sequence that starts at `start` (both tokens of the row at `row`).
-template <typename T, int VEC, int W>
-__device__ __forceinline__ void inputs_before(const ConvArgs &a, const T *row, int t0, int start, long long n, int c,
-                                              float (*xs)[VEC]) {
-    if (t0 - start < W - 1) cached_inputs<T, VEC, W>(a, n, c, xs);
-    float past[W - 1][VEC];
-#pragma unroll
-    for (int j = 1; j < W; ++j)
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) past[j - 1][i] = xs[j - 1][i];
+// The W - 1 inputs before token t0 of a sequence that starts at token `start` of the row: tokens of it, or cached.
+template <typename T, int NC, int W, bool WIDE>
+__device__ __forceinline__ void inputs_before(const ConvArgs &a, const uint16_t *row, int t0, int start, long long n,
+                                              const Lane<NC, WIDE> &l, f2 (*xs)[NC / 2]) {
 #pragma unroll
     for (int j = 1; j < W; ++j) {
-        if (t0 - j >= start) {
-            load_x<T, VEC>(row + (long long)(t0 - j) * a.x_ld + c, xs[j - 1]);
+        const int back = j - (t0 - start);  // > 0: that many tokens before the sequence's first
+        if (back <= 0) {
+            Raw<NC, WIDE> r;
+            r.load(row + (long long)(t0 - j) * a.x_ld, l);
+            r.template widen<T>(xs[j - 1]);
+        } else if (a.state_in && back < W) {
+            load_x<T, NC, WIDE>(a.state_in, n * (W - 1) + (W - 1 - back), l, xs[j - 1]);
         } else {
-            // j - (t0 - start) tokens before the start: one of the cached inputs
 #pragma unroll
-            for (int k = 1; k < W; ++k)
-                if (k == j - (t0 - start))
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) xs[j - 1][i] = past[k - 1][i];
+            for (int i = 0; i < NC / 2; ++i) xs[j - 1][i] = 0ull;
         }
     }
 }
 
-// Block -> channel of this lane and (row, first token) of this warp's walk; false past either end.
-template <int VEC>
-__device__ __forceinline__ bool my_walk(const ConvArgs &a, int &c, int &b, int &t0, long long &tblock) {
-    tblock = blockIdx.x / (unsigned)a.cblocks;
-    c = ((int)(blockIdx.x - tblock * a.cblocks) * 32 + (int)threadIdx.x) * VEC;
-    const long long walk = tblock * WALKS + threadIdx.y;
-    b = (int)(walk / a.tiles);
-    t0 = (int)(walk - (long long)b * a.tiles) * a.tt;
-    return c < a.D && b < a.B;
+// Block -> channels of this lane and (row, first token) of this warp's walk; false past either end.
+template <int NC, bool WIDE>
+__device__ __forceinline__ bool my_walk(const ConvArgs &a, Lane<NC, WIDE> &l, int &b, int &t0, long long &tblock) {
+    const unsigned tb = (__umulhi(blockIdx.x, a.cblocks_m) + blockIdx.x) >> a.cblocks_s;
+    tblock = tb;
+    const int c0 = (int)(blockIdx.x - tb * a.cblocks) * 32 * NC;
+    l.c = WIDE ? c0 + (int)threadIdx.x * NC : c0 + (int)threadIdx.x;
+    l.D = a.D;
+    const unsigned walk = tb * WALKS + threadIdx.y;
+    b = (int)((__umulhi(walk, a.tiles_m) + walk) >> a.tiles_s);
+    t0 = (int)(walk - b * a.tiles) * a.tt;
+    return (!WIDE || l.c < a.D) && b < a.B;  // (all lanes of a warp share in the copies of the ragged form)
 }
 
-template <typename T, int VEC, int W, bool PACKED>
-__global__ void __launch_bounds__(32 * WALKS) conv_fwd_kernel(const ConvArgs a) {
-    constexpr int U = 8;  // tokens in flight
+// One tensor's tokens of a warp on their way from memory, as asynchronous copies into a ring of kAhead tokens in shared
+// memory: reads in flight cost no registers.  WIDE: every lane copies its own 8 bytes.  Otherwise rows start at any
+// element: the lanes copy the aligned 16-byte pieces that hold the warp's 128 channels (17 at most, cut off at the
+// tensor's ends) and read their channels from there.
+constexpr int kAhead = 16;
+template <bool WIDE>
+struct RingRow {
+    static constexpr int bytes = WIDE ? 32 * 8 : 18 * 16;  // of one token of a warp
+};
+template <bool WIDE>
+struct Pipe {
+    const uint16_t *next;   // token to copy next: this lane's channels (WIDE) or the warp's first
+    const uint16_t *cur;    // token to take next (its misalignment)
+    const char *lo, *hi;    // the tensor
+    long long ld;
+    uint32_t ring;          // this lane's or the warp's part of slot 0
+    int lane, need;         // bytes of a row that the warp needs
+    __device__ __forceinline__ void init(unsigned char *smem, const void *base, long long rows, long long ld_, long long row,
+                                         const Lane<NC, WIDE> &l) {
+        lane = threadIdx.x;
+        ld = ld_;
+        const int c0 = WIDE ? l.c : l.c - lane;
+        next = cur = static_cast<const uint16_t *>(base) + row * ld + c0;
+        ring = smem_u32(smem) + threadIdx.y * (kAhead * RingRow<WIDE>::bytes) + (WIDE ? lane * 8 : 0);
+        lo = static_cast<const char *>(base);
+        hi = reinterpret_cast<const char *>(static_cast<const uint16_t *>(base) + (rows - 1) * ld + l.D);
+        need = 2 * min(32 * NC, l.D - c0);
+    }
+    __device__ __forceinline__ void issue(int slot, bool in) {
+        if (in) {
+            const uint32_t to = ring + slot * RingRow<WIDE>::bytes;
+            if constexpr (WIDE) {
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(to), "l"(next) : "memory");
+            } else {
+                const uintptr_t at = reinterpret_cast<uintptr_t>(next);
+                const int skew = (int)(at & 15);
+                if (lane * 16 < skew + need) {
+                    const char *src = reinterpret_cast<const char *>(at - skew) + lane * 16;
+                    if (src >= lo) {
+                        const long long left = hi - src;
+                        const int n = left < 16 ? (int)left : 16;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(to + lane * 16), "l"(src), "r"(n)
+                                     : "memory");
+                    } else {  // the piece begins before the tensor
+                        for (int i = skew; i < 16 && i - skew < need; i += 2)
+                            sts16(to + i, *reinterpret_cast<const uint16_t *>(src + i));
+                    }
+                }
+            }
+        }
+        next += ld;
+    }
+    template <typename T>
+    __device__ __forceinline__ void take(int slot, f2 *o) {
+        const uint32_t from = ring + slot * RingRow<WIDE>::bytes;
+        if constexpr (WIDE) {
+            uint32_t a, b;
+            asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];\n" : "=r"(a), "=r"(b) : "r"(from) : "memory");
+            o[0] = widen2<T>(a), o[1] = widen2<T>(b);
+        } else {
+            // (channels past the row's end hold what follows it, or nothing: they are never stored or summed)
+            const uint32_t p = from + (uint32_t)(reinterpret_cast<uintptr_t>(cur) & 15) + lane * 2;
+            o[0] = widen2<T>((uint32_t)lds16v(p) | (uint32_t)lds16v(p + 64) << 16);
+            o[1] = widen2<T>((uint32_t)lds16v(p + 128) | (uint32_t)lds16v(p + 192) << 16);
+            cur += ld;
+        }
+    }
+    // One group of copies at most GROUPS - 1 behind the newest is complete for the whole warp.
+    template <int LEFT>
+    static __device__ __forceinline__ void arrive() {
+        cp_async_wait<LEFT>();
+        if (!WIDE) __syncwarp();
+    }
+    static __device__ __forceinline__ uint16_t lds16v(uint32_t at) {
+        uint16_t v;
+        asm volatile("ld.shared.b16 %0, [%1];\n" : "=h"(v) : "r"(at) : "memory");
+        return v;
+    }
+};
+
+template <bool V>
+struct Flag {
+    static constexpr bool value = V;
+};
+
+template <typename T, int W, bool WIDE, bool PACKED>
+__global__ void __launch_bounds__(32 * WALKS, WIDE ? 4 : 3) conv_fwd_kernel(const ConvArgs a) {
+    constexpr int U = 4, GROUPS = kAhead / U;   // tokens a group of copies; groups
+    extern __shared__ __align__(16) unsigned char ring[];
     if (PACKED && blockIdx.x == 0 && threadIdx.y == 0) check_cu(a.cu, a.N, a.T, a.err);
-    int c, b, t0;
+    Lane<NC, WIDE> l;
+    int b, t0;
     long long tblock;
-    if (!my_walk<VEC>(a, c, b, t0, tblock)) return;
+    if (!my_walk(a, l, b, t0, tblock)) return;
     const int t1 = min(a.T, t0 + a.tt);
-    const T *row = static_cast<const T *>(a.x) + (long long)b * a.T * a.x_ld;
-    T *out = static_cast<T *>(a.y) + (long long)b * a.T * a.D + c;
+    const uint16_t *row = static_cast<const uint16_t *>(a.x) + (long long)b * a.T * a.x_ld;
+    const long long row0 = (long long)b * a.T;
 
-    float wp[VEC * W], bias[VEC], xs[W - 1][VEC];
-    load_params<T, VEC * W>(a.w, (long long)c * W, a.w_f32, wp);
+    Pipe<WIDE> px;
+    px.init(ring, a.x, (long long)a.B * a.T, a.x_ld, row0 + t0, l);
+    auto fetch = [&](int t, int g) {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) bias[i] = 0.f;
-    if (a.bias) load_params<T, VEC>(a.bias, c, a.w_f32, bias);
-
+        for (int u = 0; u < U; ++u) px.issue(g * U + u, t + u < t1);
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) fetch(t0 + g * U, g);
+    uint16_t *out = static_cast<uint16_t *>(a.y) + (row0 + t0) * a.D;
+    Taps<T, NC, W, WIDE> taps;
+    taps.load(a, l);
     SeqWalk sw;
     if (PACKED) sw.find(a.cu, a.N, t0);
     long long seq = PACKED ? sw.cur() : b;
-    if (!PACKED) {
-        inputs_before<T, VEC, W>(a, row, t0, 0, seq, c, xs);
-    } else if (sw.bound != t0) {
-        inputs_before<T, VEC, W>(a, row, t0, max(0, a.cu[seq]), seq, c, xs);
-    } else {
-        cached_inputs<T, VEC, W>(a, seq, c, xs);  // (replaced at the first token)
-    }
-    auto write_state = [&](long long n, const float(*s)[VEC]) {
+    f2 xs[W - 1][NC / 2];
+    if (PACKED && sw.bound == t0)
+        cached_inputs<T, NC, W, WIDE>(a, seq, l, xs);  // (replaced at the first token)
+    else
+        inputs_before<T, NC, W, WIDE>(a, row, t0, PACKED ? max(0, a.cu[seq]) : 0, seq, l, xs);
+    auto write_state = [&](long long n, const f2(*s)[NC / 2]) {
         if (!a.state_out) return;
 #pragma unroll
-        for (int j = 1; j < W; ++j)
-            store_x<T, VEC>(static_cast<T *>(a.state_out) + (n * (W - 1) + (W - 1 - j)) * a.D + c, s[j - 1]);
+        for (int j = 1; j < W; ++j) store_x<T, NC, WIDE>(a.state_out, n * (W - 1) + (W - 1 - j), l, s[j - 1]);
     };
     auto empty = [&](long long n) {
-        float e[W - 1][VEC];
-        cached_inputs<T, VEC, W>(a, n, c, e);
+        f2 e[W - 1][NC / 2];
+        cached_inputs<T, NC, W, WIDE>(a, n, l, e);
         write_state(n, e);
     };
-
-    for (int t = t0; t < t1; t += U) {
-        float x[U][VEC];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (t + u < t1) load_x<T, VEC>(row + (long long)(t + u) * a.x_ld + c, x[u]);
+    // U tokens from t; CHECKED: some of them may lie past t1, or a sequence may start or end among them
+    auto tokens = [&](int t, int g, auto checked) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (t + u >= t1) break;
-            if (PACKED && t + u == sw.bound) {
-                if (sw.step(t + u, empty)) {
-                    seq = sw.cur();
-                    cached_inputs<T, VEC, W>(a, seq, c, xs);
-                }
+            if (checked.value && t + u >= t1) break;
+            if (PACKED && checked.value && t + u == sw.bound && sw.step(t + u, empty)) {
+                seq = sw.cur();
+                cached_inputs<T, NC, W, WIDE>(a, seq, l, xs);
             }
-            float y[VEC];
+            f2 x[NC / 2], y[NC / 2];
+            px.template take<T>(g * U + u, x);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                float pre = fmaf(wp[i * W + W - 1], x[u][i], bias[i]);
-#pragma unroll
-                for (int j = 1; j < W; ++j) pre = fmaf(wp[i * W + W - 1 - j], xs[j - 1][i], pre);
-                y[i] = a.silu ? pre * sigmoid_fast(pre) : pre;
+            for (int i = 0; i < NC / 2; ++i) {
+                y[i] = taps.pre(i, x[i], xs);
+                if (a.silu) y[i] = mul2(y[i], sigmoid2(y[i]));
             }
-            store_x<T, VEC>(out + (long long)(t + u) * a.D, y);
-#pragma unroll
-            for (int j = W - 1; j > 1; --j)
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) xs[j - 1][i] = xs[j - 2][i];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) xs[0][i] = x[u][i];
-            if (PACKED && t + u + 1 == sw.bound) write_state(seq, xs);
+            store_at<T, NC, WIDE>(out, l, y);
+            out += a.D;
+            push<NC, W>(xs, x);
+            if (PACKED && checked.value && t + u + 1 == sw.bound) write_state(seq, xs);
         }
+    };
+    int g = 0;
+    for (int t = t0; t < t1; t += U) {
+        Pipe<WIDE>::template arrive<GROUPS - 1>();
+        if (t + U <= t1 && !(PACKED && sw.bound >= t && sw.bound <= t + U))
+            tokens(t, g, Flag<false>());
+        else
+            tokens(t, g, Flag<true>());
+        if (!WIDE) __syncwarp();  // (all lanes have read the slots)
+        fetch(t + GROUPS * U, g);
+        g = g + 1 == GROUPS ? 0 : g + 1;
     }
+    cp_async_wait<0>();
     if (!PACKED && t1 == a.T) write_state(seq, xs);
     if (PACKED && t1 == a.T && sw.bound == a.T) sw.step(a.T, empty);
 }
 
-template <typename T, int VEC, int W, bool PACKED>
-__global__ void __launch_bounds__(32 * WALKS) conv_bwd_kernel(const ConvArgs a) {
-    constexpr int U = 4;
-    constexpr int NP = VEC * (W + 1);
-    __shared__ float s_part[WALKS][NP][32];
-    if (PACKED && blockIdx.x == 0 && threadIdx.y == 0) check_cu(a.cu, a.N, a.T, a.err);
-    int c, b, t0;
+// One row and NC channels a thread for its few tokens: the thread that reads a channel's cached inputs is the one that
+// replaces them.  Few registers, so that a launch with one token keeps the memory busy by its number of threads.
+template <typename T, int W, bool WIDE>
+__global__ void __launch_bounds__(32 * WALKS, 5) conv_step_kernel(const ConvArgs a) {
+    Lane<NC, WIDE> l;
+    int b, t0;
     long long tblock;
-    const bool live = my_walk<VEC>(a, c, b, t0, tblock);
-    float wp[VEC * W], dw[VEC * W], db[VEC];
+    if (!my_walk(a, l, b, t0, tblock)) return;
+    const uint16_t *row = static_cast<const uint16_t *>(a.x) + (long long)b * a.T * a.x_ld;
+    Raw<NC, WIDE> raw;
+    raw.load(row, l);
+    f2 xs[W - 1][NC / 2];
+    cached_inputs<T, NC, W, WIDE>(a, b, l, xs);
+    Taps<T, NC, W, WIDE> taps;
+    taps.load(a, l);
+    for (int t = 0; t < a.T; ++t) {
+        f2 x[NC / 2], y[NC / 2];
+        raw.template widen<T>(x);
+        if (t + 1 < a.T) raw.load(row + (long long)(t + 1) * a.x_ld, l);
 #pragma unroll
-    for (int i = 0; i < VEC * W; ++i) dw[i] = 0.f;
+        for (int i = 0; i < NC / 2; ++i) {
+            y[i] = taps.pre(i, x[i], xs);
+            if (a.silu) y[i] = mul2(y[i], sigmoid2(y[i]));
+        }
+        store_x<T, NC, WIDE>(a.y, (long long)b * a.T + t, l, y);
+        push<NC, W>(xs, x);
+    }
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) db[i] = 0.f;
+    for (int j = 1; j < W; ++j) store_x<T, NC, WIDE>(a.state_out, (long long)b * (W - 1) + (W - 1 - j), l, xs[j - 1]);
+}
+
+template <typename T, int W, bool WIDE, bool PACKED>
+__global__ void __launch_bounds__(32 * WALKS, 2) conv_bwd_kernel(const ConvArgs a) {
+    constexpr int U = 4, GROUPS = kAhead / U;
+    constexpr int NP = NC * (W + 1);
+    extern __shared__ __align__(16) unsigned char ring[];  // two rings, then the walks' sums in their place
+    float(*s_part)[NP][32] = reinterpret_cast<float(*)[NP][32]>(ring);
+    if (PACKED && blockIdx.x == 0 && threadIdx.y == 0) check_cu(a.cu, a.N, a.T, a.err);
+    Lane<NC, WIDE> l;
+    int b, t0;
+    long long tblock;
+    const bool live = my_walk(a, l, b, t0, tblock);
+    f2 dw[W][NC / 2], db[NC / 2];
+#pragma unroll
+    for (int i = 0; i < NC / 2; ++i) {
+        db[i] = 0ull;
+#pragma unroll
+        for (int j = 0; j < W; ++j) dw[j][i] = 0ull;
+    }
     if (live) {
         const int t1 = min(a.T, t0 + a.tt);
-        const T *row = static_cast<const T *>(a.x) + (long long)b * a.T * a.x_ld;
-        const T *dy = static_cast<const T *>(a.dy) + (long long)b * a.T * a.D + c;
-        T *dx = static_cast<T *>(a.dx) + (long long)b * a.T * a.D + c;
-        float bias[VEC], xs[W - 1][VEC], acc[W - 1][VEC];  // acc[j-1]: the open sum of dx, j tokens back
-        load_params<T, VEC * W>(a.w, (long long)c * W, a.w_f32, wp);
+        const int tend = min(a.T, t1 + W - 1);  // the sums of the last W - 1 inputs close past the walk's end
+        const uint16_t *row = static_cast<const uint16_t *>(a.x) + (long long)b * a.T * a.x_ld;
+        const long long row0 = (long long)b * a.T;
+        Pipe<WIDE> px, pg;
+        px.init(ring, a.x, (long long)a.B * a.T, a.x_ld, row0 + t0, l);
+        pg.init(ring + WALKS * kAhead * RingRow<WIDE>::bytes, a.dy, (long long)a.B * a.T, a.D, row0 + t0, l);
+        auto fetch = [&](int t, int g) {
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) bias[i] = 0.f;
-        if (a.bias) load_params<T, VEC>(a.bias, c, a.w_f32, bias);
+            for (int u = 0; u < U; ++u) {
+                px.issue(g * U + u, t + u < tend);
+                pg.issue(g * U + u, t + u < tend);
+            }
+            cp_async_commit();
+        };
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) fetch(t0 + g * U, g);
+        uint16_t *out = static_cast<uint16_t *>(a.dx) + (row0 + t0 - (W - 1)) * a.D;  // (stored to from token t0 on)
+        Taps<T, NC, W, WIDE> taps;
+        taps.load(a, l);
+        f2 xs[W - 1][NC / 2], acc[W - 1][NC / 2];  // acc[j-1]: the open sum of dx, j tokens back
 #pragma unroll
         for (int j = 1; j < W; ++j)
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) acc[j - 1][i] = 0.f;
+            for (int i = 0; i < NC / 2; ++i) acc[j - 1][i] = 0ull;
 
         SeqWalk sw;
         if (PACKED) sw.find(a.cu, a.N, t0);
         long long seq = PACKED ? sw.cur() : b;
         int start = 0;
         if (PACKED && sw.bound != t0) start = max(0, a.cu[seq]);
-        if (!PACKED || sw.bound != t0)
-            inputs_before<T, VEC, W>(a, row, t0, start, seq, c, xs);
+        if (PACKED && sw.bound == t0)
+            cached_inputs<T, NC, W, WIDE>(a, seq, l, xs);  // (replaced at the first token)
         else
-            cached_inputs<T, VEC, W>(a, seq, c, xs);  // (replaced at the first token)
+            inputs_before<T, NC, W, WIDE>(a, row, t0, start, seq, l, xs);
         // A finished sum: of an input of this walk, or of a cached input of a sequence that starts in it.
-        auto emit = [&](int s, const float *v) {
+        auto emit = [&](int s, const f2 *v) {
             if (s >= start) {
-                if (s >= t0 && s < t1) store_x<T, VEC>(dx + (long long)s * a.D, v);
+                if (s >= t0 && s < t1) store_x<T, NC, WIDE>(a.dx, row0 + s, l, v);
             } else if (start >= t0 && a.dstate_in && W - 1 + s - start >= 0) {
-                store_x<T, VEC>(static_cast<T *>(a.dstate_in) + (seq * (W - 1) + (W - 1 + s - start)) * a.D + c, v);
+                store_x<T, NC, WIDE>(a.dstate_in, seq * (W - 1) + (W - 1 + s - start), l, v);
             }
         };
         // The last W - 1 sums of a sequence that ends at token e: also the final state's gradient.
@@ -254,42 +469,34 @@ __global__ void __launch_bounds__(32 * WALKS) conv_bwd_kernel(const ConvArgs a) 
 #pragma unroll
             for (int j = W - 1; j >= 1; --j) {
                 if (a.dstate_out) {
-                    float d[VEC];
-                    load_x<T, VEC>(static_cast<const T *>(a.dstate_out) + (seq * (W - 1) + (W - 1 - j)) * a.D + c, d);
+                    f2 d[NC / 2];
+                    load_x<T, NC, WIDE>(a.dstate_out, seq * (W - 1) + (W - 1 - j), l, d);
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) acc[j - 1][i] += d[i];
+                    for (int i = 0; i < NC / 2; ++i) acc[j - 1][i] = add2(acc[j - 1][i], d[i]);
                 }
                 emit(e - j, acc[j - 1]);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) acc[j - 1][i] = 0.f;
+                for (int i = 0; i < NC / 2; ++i) acc[j - 1][i] = 0ull;
             }
         };
         auto empty = [&](long long n) {
             if (!a.dstate_in) return;
 #pragma unroll
             for (int j = 0; j < W - 1; ++j) {
-                float d[VEC];
+                f2 d[NC / 2];
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) d[i] = 0.f;
-                if (a.dstate_out) load_x<T, VEC>(static_cast<const T *>(a.dstate_out) + (n * (W - 1) + j) * a.D + c, d);
-                store_x<T, VEC>(static_cast<T *>(a.dstate_in) + (n * (W - 1) + j) * a.D + c, d);
+                for (int i = 0; i < NC / 2; ++i) d[i] = 0ull;
+                if (a.dstate_out) load_x<T, NC, WIDE>(a.dstate_out, n * (W - 1) + j, l, d);
+                store_x<T, NC, WIDE>(a.dstate_in, n * (W - 1) + j, l, d);
             }
         };
-
-        const int tend = min(a.T, t1 + W - 1);  // the sums of the last W - 1 inputs close past the walk's end
-        bool open = true;                       // a sequence of this walk is still to be flushed
-        for (int t = t0; open && t < tend; t += U) {
-            float x[U][VEC], g[U][VEC];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (t + u < tend) {
-                    load_x<T, VEC>(row + (long long)(t + u) * a.x_ld + c, x[u]);
-                    load_x<T, VEC>(dy + (long long)(t + u) * a.D, g[u]);
-                }
+        bool open = true;  // the walk's last sequence is still to be flushed
+        // U tokens from t; CHECKED: not all of them are the walk's own, well inside one sequence
+        auto tokens = [&](int t, int g, auto checked) {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (!open || t + u >= tend) break;
-                if (PACKED && t + u == sw.bound) {
+                if (checked.value && (!open || t + u >= tend)) break;
+                if (PACKED && checked.value && t + u == sw.bound) {
                     if (t + u > t0) flush(t + u);
                     if (t + u >= t1) {
                         open = false;
@@ -298,80 +505,102 @@ __global__ void __launch_bounds__(32 * WALKS) conv_bwd_kernel(const ConvArgs a) 
                     if (sw.step(t + u, empty)) {
                         seq = sw.cur();
                         start = t + u;
-                        cached_inputs<T, VEC, W>(a, seq, c, xs);
+                        cached_inputs<T, NC, W, WIDE>(a, seq, l, xs);
                     }
                 }
-                const bool mine = t + u < t1;
-                float done[VEC];
+                const bool mine = !checked.value || t + u < t1;
+                f2 x[NC / 2], d[NC / 2], done[NC / 2];
+                px.template take<T>(g * U + u, x);
+                pg.template take<T>(g * U + u, d);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    float d = g[u][i];
+                for (int i = 0; i < NC / 2; ++i) {
                     if (a.silu) {
-                        float pre = fmaf(wp[i * W + W - 1], x[u][i], bias[i]);
-#pragma unroll
-                        for (int j = 1; j < W; ++j) pre = fmaf(wp[i * W + W - 1 - j], xs[j - 1][i], pre);
-                        const float s = sigmoid_fast(pre);
-                        d *= fmaf(pre * s, 1.f - s, s);
+                        const f2 pre = taps.pre(i, x[i], xs), s = sigmoid2(pre);
+                        // sig + pre sig (1 - sig)
+                        d[i] = mul2(d[i], fma2(mul2(pre, s), fma2(s, both(-1.f), both(1.f)), s));
                     }
-                    done[i] = fmaf(wp[i * W], d, acc[W - 2][i]);
+                    done[i] = fma2(taps.w[W - 1][i], d[i], acc[W - 2][i]);
 #pragma unroll
-                    for (int j = W - 2; j >= 1; --j) acc[j][i] = fmaf(wp[i * W + W - 1 - j], d, acc[j - 1][i]);
-                    acc[0][i] = wp[i * W + W - 1] * d;
-                    const float dm = mine ? d : 0.f;
-                    dw[i * W + W - 1] = fmaf(dm, x[u][i], dw[i * W + W - 1]);
+                    for (int j = W - 2; j >= 1; --j) acc[j][i] = fma2(taps.w[j][i], d[i], acc[j - 1][i]);
+                    acc[0][i] = mul2(taps.w[0][i], d[i]);
+                    if (mine) {
+                        dw[0][i] = fma2(d[i], x[i], dw[0][i]);
 #pragma unroll
-                    for (int j = 1; j < W; ++j)
-                        dw[i * W + W - 1 - j] = fmaf(dm, xs[j - 1][i], dw[i * W + W - 1 - j]);
-                    db[i] += dm;
-#pragma unroll
-                    for (int j = W - 1; j > 1; --j) xs[j - 1][i] = xs[j - 2][i];
-                    xs[0][i] = x[u][i];
+                        for (int j = 1; j < W; ++j) dw[j][i] = fma2(d[i], xs[j - 1][i], dw[j][i]);
+                        db[i] = add2(db[i], d[i]);
+                    }
                 }
-                emit(t + u - (W - 1), done);
+                push<NC, W>(xs, x);
+                if (checked.value)
+                    emit(t + u - (W - 1), done);
+                else
+                    store_at<T, NC, WIDE>(out, l, done);
+                out += a.D;
             }
+        };
+        int g = 0;
+        for (int t = t0; open && t < tend; t += U) {
+            Pipe<WIDE>::template arrive<GROUPS - 1>();
+            if (t + U <= t1 && t - (W - 1) >= max(t0, start) && !(PACKED && sw.bound >= t && sw.bound < t + U))
+                tokens(t, g, Flag<false>());
+            else
+                tokens(t, g, Flag<true>());
+            if (!WIDE) __syncwarp();  // (all lanes have read the slots)
+        fetch(t + GROUPS * U, g);
+            g = g + 1 == GROUPS ? 0 : g + 1;
         }
+        cp_async_wait<0>();
         if (open && tend == a.T && (!PACKED || sw.bound == a.T)) flush(a.T);
         if (PACKED && t1 == a.T && sw.bound == a.T) sw.step(a.T, empty);
     }
     // the block's share of dw and db: its walks added in order
+    __syncthreads();  // (the rings are read no more)
 #pragma unroll
-    for (int i = 0; i < VEC * W; ++i) s_part[threadIdx.y][i][threadIdx.x] = dw[i];
+    for (int i = 0; i < NC / 2; ++i) {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) s_part[threadIdx.y][VEC * W + i][threadIdx.x] = db[i];
+        for (int j = 0; j < W; ++j)
+            unpack2(dw[j][i], s_part[threadIdx.y][2 * i * W + W - 1 - j][threadIdx.x],
+                    s_part[threadIdx.y][(2 * i + 1) * W + W - 1 - j][threadIdx.x]);
+        unpack2(db[i], s_part[threadIdx.y][NC * W + 2 * i][threadIdx.x], s_part[threadIdx.y][NC * W + 2 * i + 1][threadIdx.x]);
+    }
     __syncthreads();
-    if (c >= a.D) return;
     for (int i = threadIdx.y; i < NP; i += WALKS) {
         float s = 0.f;
 #pragma unroll
         for (int k = 0; k < WALKS; ++k) s += s_part[k][i][threadIdx.x];
-        if (i < VEC * W)
-            a.dw_part[tblock * a.D * W + (long long)c * W + i] = s;
-        else if (a.db_part)
-            a.db_part[tblock * a.D + c + i - VEC * W] = s;
+        const bool weight = i < NC * W;
+        const int e = weight ? i / W : i - NC * W;  // the thread's channel
+        if (l.c >= a.D || !l.has(e)) continue;
+        float *part = a.part + tblock * (W + 1) * a.D;
+        part[weight ? (long long)l.chan(e) * W + i % W : (long long)a.D * W + l.chan(e)] = s;
     }
 }
 
-// Tokens a walk: long walks repeat fewer overlapping reads, short ones fill the chip; the longest of 64, 32, 16 and
-// 8 that still gives two blocks an SM.
-int conv_tt(const gdr_conv_problem *p, int vec) {
-    const long long cb = (p->D + 32 * vec - 1) / (32 * vec);
-    int tt = 64;
-    for (; tt > 8; tt /= 2) {
+// Tokens a walk.  Long walks repeat fewer overlapping reads and start-ups (worth about 16 tokens a walk), short ones
+// fill the chip; the length that minimises rounds of resident blocks times the tokens of one.  (At 2 x 4096 x 12288
+// the backward takes 5.05 rounds of two blocks an SM with 64 tokens and 2.8 with 120: 147 and 131 us.)
+int conv_tt(const gdr_conv_problem *p, bool bwd) {
+    const long long cb = (p->D + 32 * NC - 1) / (32 * NC), slots = (long long)kSMs * (bwd ? 2 : 4);
+    long long best = 0;
+    int best_tt = 8;
+    for (int tt = 8; tt <= 128; tt += 8) {
         const long long walks = (long long)p->B * ((p->T + tt - 1) / tt);
-        if ((walks + WALKS - 1) / WALKS * cb >= 2 * kSMs) break;
+        const long long rounds = ((walks + WALKS - 1) / WALKS * cb + slots - 1) / slots;
+        const long long cost = rounds * (tt + 16);
+        if (best == 0 || cost < best) best = cost, best_tt = tt;
     }
-    return tt;
+    return best_tt;
 }
 
 struct ConvGrid {
     int tt, tiles, cblocks;
     long long tblocks;
 };
-ConvGrid conv_grid(const gdr_conv_problem *p, int vec, int tt) {
+ConvGrid conv_grid(const gdr_conv_problem *p, int tt) {
     ConvGrid g;
     g.tt = tt;
     g.tiles = (p->T + g.tt - 1) / g.tt;
-    g.cblocks = (p->D + 32 * vec - 1) / (32 * vec);
+    g.cblocks = (p->D + 32 * NC - 1) / (32 * NC);
     g.tblocks = ((long long)p->B * g.tiles + WALKS - 1) / WALKS;
     return g;
 }
@@ -386,35 +615,53 @@ gdr_status check_conv(const gdr_conv_problem *p) {
     return GDR_OK;
 }
 
-// Blocks of a launch fit the grid's x dimension.
-bool grid_fits(const ConvGrid &g) { return g.tblocks * g.cblocks <= 0x7fffffffLL; }
+// Blocks fit the grid's x dimension, and walks an int.
+bool grid_fits(const ConvGrid &g) { return g.tblocks * g.cblocks <= 0x7fffffffLL && g.tblocks * WALKS <= 0x7fffffffLL; }
 
-template <typename T, int VEC, bool PACKED>
-cudaError_t conv_fwd_w(const ConvArgs &a, int W, const ConvGrid &g, cudaStream_t s) {
+template <typename K>
+cudaError_t launch_ring(K k, dim3 grid, size_t smem, cudaStream_t s, const ConvArgs &a) {
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_plain(k, grid, dim3(32, WALKS), smem, s, a);
+}
+template <typename T, int W, bool WIDE, bool PACKED>
+cudaError_t conv_one(const ConvArgs &a, bool bwd, dim3 grid, cudaStream_t s) {
+    constexpr size_t one = (size_t)WALKS * kAhead * RingRow<WIDE>::bytes, sums = (size_t)WALKS * NC * (W + 1) * 32 * sizeof(float);
+    if (bwd) return launch_ring(conv_bwd_kernel<T, W, WIDE, PACKED>, grid, 2 * one > sums ? 2 * one : sums, s, a);
+    return launch_ring(conv_fwd_kernel<T, W, WIDE, PACKED>, grid, one, s, a);
+}
+template <typename T, bool WIDE, bool PACKED>
+cudaError_t conv_w(const ConvArgs &a, int W, bool bwd, const ConvGrid &g, cudaStream_t s) {
+    const dim3 grid((unsigned)(g.tblocks * g.cblocks));
+    if (W == 2) return conv_one<T, 2, WIDE, PACKED>(a, bwd, grid, s);
+    if (W == 3) return conv_one<T, 3, WIDE, PACKED>(a, bwd, grid, s);
+    return conv_one<T, 4, WIDE, PACKED>(a, bwd, grid, s);
+}
+template <typename T, bool WIDE>
+cudaError_t conv_step_w(const ConvArgs &a, int W, const ConvGrid &g, cudaStream_t s) {
     const dim3 grid((unsigned)(g.tblocks * g.cblocks)), block(32, WALKS);
-    if (W == 2) return launch_plain(conv_fwd_kernel<T, VEC, 2, PACKED>, grid, block, 0, s, a);
-    if (W == 3) return launch_plain(conv_fwd_kernel<T, VEC, 3, PACKED>, grid, block, 0, s, a);
-    return launch_plain(conv_fwd_kernel<T, VEC, 4, PACKED>, grid, block, 0, s, a);
+    if (W == 2) return launch_plain(conv_step_kernel<T, 2, WIDE>, grid, block, 0, s, a);
+    if (W == 3) return launch_plain(conv_step_kernel<T, 3, WIDE>, grid, block, 0, s, a);
+    return launch_plain(conv_step_kernel<T, 4, WIDE>, grid, block, 0, s, a);
 }
-template <typename T>
-cudaError_t conv_fwd_t(const ConvArgs &a, int W, bool vec, const ConvGrid &g, cudaStream_t s) {
-    if (vec) return a.cu ? conv_fwd_w<T, 8, true>(a, W, g, s) : conv_fwd_w<T, 8, false>(a, W, g, s);
-    return a.cu ? conv_fwd_w<T, 1, true>(a, W, g, s) : conv_fwd_w<T, 1, false>(a, W, g, s);
-}
-template <typename T, int VEC, bool PACKED>
-cudaError_t conv_bwd_w(const ConvArgs &a, int W, const ConvGrid &g, cudaStream_t s) {
-    const dim3 grid((unsigned)(g.tblocks * g.cblocks)), block(32, WALKS);
-    if (W == 2) return launch_plain(conv_bwd_kernel<T, VEC, 2, PACKED>, grid, block, 0, s, a);
-    if (W == 3) return launch_plain(conv_bwd_kernel<T, VEC, 3, PACKED>, grid, block, 0, s, a);
-    return launch_plain(conv_bwd_kernel<T, VEC, 4, PACKED>, grid, block, 0, s, a);
-}
-template <typename T>
-cudaError_t conv_bwd_t(const ConvArgs &a, int W, bool vec, const ConvGrid &g, cudaStream_t s) {
-    if (vec) return a.cu ? conv_bwd_w<T, 4, true>(a, W, g, s) : conv_bwd_w<T, 4, false>(a, W, g, s);
-    return a.cu ? conv_bwd_w<T, 1, true>(a, W, g, s) : conv_bwd_w<T, 1, false>(a, W, g, s);
+cudaError_t launch_conv_step(const gdr_conv_problem *p, const ConvArgs &a, bool wide, const ConvGrid &g, cudaStream_t s) {
+    if (p->dtype == GDR_BF16)
+        return wide ? conv_step_w<__nv_bfloat16, true>(a, p->W, g, s) : conv_step_w<__nv_bfloat16, false>(a, p->W, g, s);
+    return wide ? conv_step_w<__half, true>(a, p->W, g, s) : conv_step_w<__half, false>(a, p->W, g, s);
 }
 
-ConvArgs conv_args(const gdr_conv_problem *p, const ConvGrid &g, unsigned *err) {
+template <typename T>
+cudaError_t conv_t(const ConvArgs &a, int W, bool wide, bool bwd, const ConvGrid &g, cudaStream_t s) {
+    if (wide) return a.cu ? conv_w<T, true, true>(a, W, bwd, g, s) : conv_w<T, true, false>(a, W, bwd, g, s);
+    return a.cu ? conv_w<T, false, true>(a, W, bwd, g, s) : conv_w<T, false, false>(a, W, bwd, g, s);
+}
+cudaError_t launch_conv(const gdr_conv_problem *p, const ConvArgs &a, bool wide, bool bwd, const ConvGrid &g, cudaStream_t s) {
+    return p->dtype == GDR_BF16 ? conv_t<__nv_bfloat16>(a, p->W, wide, bwd, g, s) : conv_t<__half>(a, p->W, wide, bwd, g, s);
+}
+
+ConvArgs conv_args(const gdr_conv_problem *p, const ConvGrid &g, bool w_wide, unsigned *err) {
     ConvArgs a = {};
     a.cu = p->cu_seqlens;
     a.err = err;
@@ -422,7 +669,10 @@ ConvArgs conv_args(const gdr_conv_problem *p, const ConvGrid &g, unsigned *err) 
     a.B = p->B, a.T = p->T, a.D = p->D;
     a.N = p->cu_seqlens ? p->num_seqs : p->B;
     a.tt = g.tt, a.tiles = g.tiles, a.cblocks = g.cblocks;
+    div_magic(g.tiles, a.tiles_m, a.tiles_s);
+    div_magic(g.cblocks, a.cblocks_m, a.cblocks_s);
     a.w_f32 = p->weight_dtype == GDR_FP32;
+    a.w_wide = w_wide;
     a.silu = (p->flags & GDR_CONV_SILU) != 0;
     return a;
 }
@@ -439,25 +689,25 @@ gdr_status conv_no_tokens(const gdr_conv_problem *p, const void *src, void *dst,
 }
 
 gdr_status conv_fwd_core(const gdr_conv_problem *p, const void *x, const void *weight, const void *bias,
-                         const void *state_in, void *y, void *state_out, int tt, void *stream) {
+                         const void *state_in, void *y, void *state_out, bool step, void *stream) {
     if (!weight || (p->T > 0 && (!x || !y))) return GDR_ERR_NULL;
     const size_t ws = esize(p->weight_dtype);
     for (const void *q : {x, state_in, (const void *)y, (const void *)state_out})
         if (!aligned_to(q, 2)) return GDR_ERR_ALIGN;
     if (!aligned_to(weight, ws) || !aligned_to(bias, ws)) return GDR_ERR_ALIGN;
-    const bool vec = p->D % 8 == 0 && p->x_ld % 8 == 0 && aligned16(x) && aligned16(y) && aligned16(state_in) &&
-                     aligned16(state_out);
-    const ConvGrid g = conv_grid(p, vec ? 8 : 1, tt ? tt : conv_tt(p, vec ? 8 : 1));
+    bool wide = p->D % 4 == 0 && p->x_ld % 4 == 0;
+    for (const void *q : {x, state_in, (const void *)y, (const void *)state_out}) wide = wide && aligned_to(q, 8);
+    const ConvGrid g = conv_grid(p, !step ? conv_tt(p, false) : p->T > 0 ? p->T : 1);
     if (!grid_fits(g)) return GDR_ERR_SHAPE;
     unsigned *err = nullptr;
     gdr_status st = device_state(&err);
     if (st != GDR_OK) return st;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     if (p->T == 0) return conv_no_tokens(p, state_in, state_out, cs);
-    ConvArgs a = conv_args(p, g, err);
+    ConvArgs a = conv_args(p, g, aligned_to(weight, 8), err);
     a.x = x, a.w = weight, a.bias = bias, a.state_in = state_in, a.y = y, a.state_out = state_out;
     return timed(K_CONV_FWD, cs, [&] {
-        return p->dtype == GDR_BF16 ? conv_fwd_t<__nv_bfloat16>(a, p->W, vec, g, cs) : conv_fwd_t<__half>(a, p->W, vec, g, cs);
+        return step ? launch_conv_step(p, a, wide, g, cs) : launch_conv(p, a, wide, false, g, cs);
     });
 }
 
@@ -474,7 +724,7 @@ gdr_status gdr_conv_fwd(const gdr_conv_problem *p, const void *x, const void *we
     if (st != GDR_OK) return st;
     // (a sequence's first and last tokens belong to different threads)
     if (state_out && state_out == state_in) return GDR_ERR_UNSUPPORTED;
-    return conv_fwd_core(p, x, weight, bias, state_in, y, state_out, 0, stream);
+    return conv_fwd_core(p, x, weight, bias, state_in, y, state_out, false, stream);
 }
 
 gdr_status gdr_conv_step(const gdr_conv_problem *p, const void *x, const void *weight, const void *bias, void *state,
@@ -483,24 +733,17 @@ gdr_status gdr_conv_step(const gdr_conv_problem *p, const void *x, const void *w
     if (st != GDR_OK) return st;
     if (p->cu_seqlens) return GDR_ERR_UNSUPPORTED;
     if (!state) return GDR_ERR_NULL;
-    // one walk a row: the thread that reads a channel's cached inputs is the one that replaces them
-    return conv_fwd_core(p, x, weight, bias, state, y, state, p->T > 0 ? p->T : 1, stream);
+    return conv_fwd_core(p, x, weight, bias, state, y, state, true, stream);
 }
 
 gdr_status gdr_conv_bwd_workspace_size(const gdr_conv_problem *p, size_t *bytes) {
     gdr_status st = check_conv(p);
     if (st != GDR_OK) return st;
     if (!bytes) return GDR_ERR_NULL;
-    // (covers the wide and the narrow path, whose walks differ)
-    size_t most = 0;
-    if (p->T > 0)
-        for (int vec : {1, 4}) {
-            const ConvGrid g = conv_grid(p, vec, conv_tt(p, vec));
-            const size_t n = round_up((size_t)g.tblocks * p->D * p->W * sizeof(float), 256) +
-                             round_up((size_t)g.tblocks * p->D * sizeof(float), 256);
-            most = n > most ? n : most;
-        }
-    *bytes = most;
+    *bytes = 0;
+    if (p->T == 0) return GDR_OK;
+    const ConvGrid g = conv_grid(p, conv_tt(p, true));
+    *bytes = round_up((size_t)g.tblocks * p->D * (p->W + 1) * sizeof(float), 256);
     return GDR_OK;
 }
 
@@ -518,10 +761,10 @@ gdr_status gdr_conv_bwd(const gdr_conv_problem *p, const void *x, const void *we
         if (!aligned_to(q, ws)) return GDR_ERR_ALIGN;
     if (need && (!workspace || workspace_bytes < need)) return GDR_ERR_WORKSPACE;
     if (need && !aligned_to(workspace, 256)) return GDR_ERR_ALIGN;
-    bool vec = p->D % 4 == 0 && p->x_ld % 4 == 0;
+    bool wide = p->D % 4 == 0 && p->x_ld % 4 == 0;
     for (const void *q : {x, dy, state_in, dstate_out, (const void *)dx, (const void *)dstate_in})
-        vec = vec && aligned_to(q, 8);
-    const ConvGrid g = conv_grid(p, vec ? 4 : 1, conv_tt(p, vec ? 4 : 1));
+        wide = wide && aligned_to(q, 8);
+    const ConvGrid g = conv_grid(p, conv_tt(p, true));
     if (!grid_fits(g)) return GDR_ERR_SHAPE;
     unsigned *err = nullptr;
     if ((st = device_state(&err)) != GDR_OK) return st;
@@ -532,23 +775,17 @@ gdr_status gdr_conv_bwd(const gdr_conv_problem *p, const void *x, const void *we
         if (e != cudaSuccess) return cuda_status(e);
         return conv_no_tokens(p, dstate_out, dstate_in, cs);
     }
-    ConvArgs a = conv_args(p, g, err);
+    ConvArgs a = conv_args(p, g, aligned_to(weight, 8), err);
     a.x = x, a.w = weight, a.bias = bias, a.state_in = state_in, a.dy = dy, a.dstate_out = dstate_out;
     a.dx = dx, a.dstate_in = dstate_in;
-    a.dw_part = static_cast<float *>(workspace);
-    if (dbias)
-        a.db_part = reinterpret_cast<float *>(static_cast<char *>(workspace) +
-                                              round_up((size_t)g.tblocks * p->D * p->W * sizeof(float), 256));
+    a.part = static_cast<float *>(workspace);
     const bool bf = p->dtype == GDR_BF16;
-    st = timed(K_CONV_BWD, cs, [&] {
-        return bf ? conv_bwd_t<__nv_bfloat16>(a, p->W, vec, g, cs) : conv_bwd_t<__half>(a, p->W, vec, g, cs);
-    });
+    st = timed(K_CONV_BWD, cs, [&] { return launch_conv(p, a, wide, true, g, cs); });
     if (st != GDR_OK) return st;
-    st = timed(K_REDUCE, cs, [&] {
-        return launch_reduce_rows(a.dw_part, g.tblocks, (long long)p->D * p->W, p->D * p->W, dweight, bf, a.w_f32, cs);
+    return timed(K_REDUCE, cs, [&] {
+        const RowSums out[2] = {{dweight, p->D * p->W}, {dbias, p->D}};
+        return launch_reduce_rows(a.part, g.tblocks, (long long)p->D * (p->W + 1), out, dbias ? 2 : 1, bf, a.w_f32, cs);
     });
-    if (st != GDR_OK || !dbias) return st;
-    return timed(K_REDUCE, cs, [&] { return launch_reduce_rows(a.db_part, g.tblocks, p->D, p->D, dbias, bf, a.w_f32, cs); });
 }
 
 }  // extern "C"

@@ -170,8 +170,13 @@ cudaError_t launch_bwd_chunk_tc(const Args &a, const void *q, const void *k, con
                                 const void *delta, const void *ddelta, void *dq, void *dk, void *dv, void *dg,
                                 void *dbeta, cudaStream_t s);
 
-// out[c] = sum over r < parts of part[r stride + c], c < cols, in a fixed order; out in bf16 / fp16 or fp32.
-cudaError_t launch_reduce_rows(const float *part, long long parts, long long stride, int cols, void *out, bool bf16,
-                               bool out_f32, cudaStream_t s);
+// Column sums of part [parts, stride], in a fixed order: the first out[0].cols columns to out[0].to, the next
+// out[1].cols to out[1].to, and so on (1 to 3 outputs, bf16 / fp16 or fp32).
+struct RowSums {
+    void *to;
+    int cols;
+};
+cudaError_t launch_reduce_rows(const float *part, long long parts, long long stride, const RowSums *out, int outs,
+                               bool bf16, bool out_f32, cudaStream_t s);
 
 }  // namespace gdr

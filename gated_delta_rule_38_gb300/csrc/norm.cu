@@ -13,13 +13,12 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "host.h"
 #include "launch.h"
 
 namespace gdr {
 namespace {
-
-constexpr int kNormThreads = 512;  // largest block: 128 registers a thread
 
 enum { RES_NONE = 0, RES_HALF = 1, RES_F32 = 2 };
 
@@ -31,59 +30,10 @@ struct NormArgs {
     void *dx, *dres;           // backward: dres only for an fp32 residual stream
     float *dw_part;            // backward: [blocks * rows per block][D]
     long long rows, x_ld;
-    int D, tpr, res_kind, group, nscale;  // group: 0 = one scale a row
+    int D, tpr, group, nscale;  // group: 0 = one scale a row
     bool w_f32;
     float eps;
 };
-
-// VEC consecutive elements of T at p as fp32 (one 16-byte load for VEC = 8).
-template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T *p, float *o) {
-    if (VEC == 8) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t r[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = Elt<T>::unpack(r[i]);
-            o[2 * i] = f.x, o[2 * i + 1] = f.y;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) o[i] = Elt<T>::to_f(p[i]);
-    }
-}
-template <typename T, int VEC>
-__device__ __forceinline__ void store_vec(T *p, const float *v) {
-    if (VEC == 8) {
-        uint4 u;
-        u.x = Elt<T>::pack(v[0], v[1]), u.y = Elt<T>::pack(v[2], v[3]);
-        u.z = Elt<T>::pack(v[4], v[5]), u.w = Elt<T>::pack(v[6], v[7]);
-        *reinterpret_cast<uint4 *>(p) = u;
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) p[i] = Elt<T>::from_f(v[i]);
-    }
-}
-template <int VEC>
-__device__ __forceinline__ void load_vec_f32(const float *p, float *o) {
-    if (VEC == 8) {
-        const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-        o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) o[i] = p[i];
-    }
-}
-template <int VEC>
-__device__ __forceinline__ void store_vec_f32(float *p, const float *v) {
-    if (VEC == 8) {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) p[i] = v[i];
-    }
-}
 
 // Where a thread's elements lie in its row.  VEC = 8: vector v of thread t at column 8 (v TPR + t).  VEC = 1
 // (TPR >= 32): a warp takes 128 consecutive columns in four steps of its lanes, so that every load is contiguous
@@ -98,118 +48,201 @@ struct Cols {
     }
 };
 
+// A thread's elements of one row as they lie in memory (16-bit or fp32), so that the next row can be on its way
+// while this one is worked on; zeros past the row's end.
+template <int VEC, int NV, bool F32>
+struct RawRow {
+    static constexpr int W = F32 ? VEC * NV : VEC * NV / 2;  // words
+    uint32_t w[W];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void load(const void *base, long long at, const Cols<VEC> &col, int D) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = col(v);
+            if constexpr (VEC == 8) {
+                constexpr int Q = F32 ? 2 : 1;
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    uint4 u = make_uint4(0, 0, 0, 0);
+                    if (c < D) {
+                        const uint4 *p = F32 ? reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + at + c)
+                                             : reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + at + c);
+                        u = p[q];
+                    }
+                    uint32_t *o = w + (v * Q + q) * 4;
+                    o[0] = u.x, o[1] = u.y, o[2] = u.z, o[3] = u.w;
+                }
+            } else if constexpr (F32) {
+                w[v] = c < D ? static_cast<const uint32_t *>(base)[at + c] : 0;
+            } else {
+                const uint32_t e = c < D ? static_cast<const uint16_t *>(base)[at + c] : 0;
+                if (v & 1) w[v / 2] |= e << 16; else w[v / 2] = e;
+            }
+        }
+    }
+    // pairs of consecutive elements
+    template <typename T>
+    __device__ __forceinline__ f2 pair(int i) const {
+        if constexpr (F32) return pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+        else return widen2<T>(w[i]);
+    }
+};
+
+// The same elements back to memory.
+template <typename T, int VEC, int NV, bool F32>
+__device__ __forceinline__ void store_row(void *base, long long at, const Cols<VEC> &col, int D, const f2 *h) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        const int c = col(v);
+        if (c >= D) continue;
+        if constexpr (VEC == 8) {
+            const f2 *e = h + v * 4;
+            if constexpr (F32) {
+                ulonglong2 *p = reinterpret_cast<ulonglong2 *>(static_cast<float *>(base) + at + c);
+                p[0] = make_ulonglong2(e[0], e[1]);
+                p[1] = make_ulonglong2(e[2], e[3]);
+            } else {
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + at + c) =
+                    make_uint4(narrow2<T>(e[0]), narrow2<T>(e[1]), narrow2<T>(e[2]), narrow2<T>(e[3]));
+            }
+        } else {
+            float lo, hi;
+            unpack2(h[v / 2], lo, hi);
+            const float x = v & 1 ? hi : lo;
+            if constexpr (F32) static_cast<float *>(base)[at + c] = x;
+            else static_cast<T *>(base)[at + c] = Elt<T>::from_f(x);
+        }
+    }
+}
+
+// The thread's weights as fp32 pairs (zeros past the row's end).
+template <typename T, int VEC, int NV>
+__device__ __forceinline__ void load_weight(const NormArgs &a, const Cols<VEC> &col, f2 *w) {
+    if (a.w_f32) {
+        RawRow<VEC, NV, true> r;
+        r.load(a.w, 0, col, a.D);
+#pragma unroll
+        for (int i = 0; i < VEC * NV / 2; ++i) w[i] = r.template pair<T>(i);
+    } else {
+        RawRow<VEC, NV, false> r;
+        r.load(a.w, 0, col, a.D);
+#pragma unroll
+        for (int i = 0; i < VEC * NV / 2; ++i) w[i] = r.template pair<T>(i);
+    }
+}
+
 __device__ __forceinline__ float lanes_sum(float x, int lanes) {
     for (int o = lanes >> 1; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
-// Maximum of non-negative floats (and NaN, which wins) by their bits.
-__device__ __forceinline__ uint32_t lanes_max(uint32_t x, int lanes) {
-    for (int o = lanes >> 1; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
-    return x;
+// Maximum of magnitudes; a NaN wins.  (Over lanes by the bits, which order non-negative floats, NaN last.)
+__device__ __forceinline__ float max_abs(float m, float x) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(x)));
+    return r;
 }
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+__device__ __forceinline__ float lanes_max(float m, int lanes) {
+    uint32_t x = __float_as_uint(m);
+    for (int o = lanes >> 1; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return __uint_as_float(x);
+}
 
-template <typename T, int VEC, int NV, bool QUANT>
-__global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(const NormArgs a) {
-    constexpr int EPT = VEC * NV;
-    __shared__ float s_sum[2][32];
-    __shared__ uint32_t s_max[2][32];
+// Registers: 16 elements a thread leave room for three blocks of 256 an SM (two in the backward) with the weights and
+// the next row's loads held in registers.  Rows over 8,192 take 32 elements a thread and hold neither.
+template <int EPT, int BT>
+struct Bounds {
+    static constexpr bool hold = EPT <= 16;
+    static constexpr int fwd = BT == 256 ? 3 : 1, bwd = BT == 256 ? 2 : 1;
+};
+
+template <typename T, int VEC, int NV, int BT, bool QUANT, int RES>
+__global__ void __launch_bounds__(BT, Bounds<VEC * NV, BT>::fwd) norm_fwd_kernel(const NormArgs a) {
+    constexpr int P = VEC * NV / 2;  // pairs a thread
+    constexpr bool HOLD = Bounds<VEC * NV, BT>::hold;
+    __shared__ float s_sum[2][16];
+    __shared__ float s_max[2][16];
     const int tpr = a.tpr, slot = threadIdx.x / tpr, t = threadIdx.x & (tpr - 1);
     const int rpb = blockDim.x / tpr, lanes = min(tpr, 32), wpr = tpr >> 5;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Cols<VEC> col(tpr, t);
     const float inv_d = 1.0f / (float)a.D;
+    const long long step = (long long)gridDim.x * rpb;
+    RawRow<VEC, NV, false> rx;
+    RawRow<VEC, NV, RES == RES_F32> rr;
+    auto fetch = [&](long long row) {
+        if (row < a.rows) {
+            rx.load(a.x, row * a.x_ld, col, a.D);
+            if (RES != RES_NONE) rr.load(a.res, row * a.D, col, a.D);
+        } else {
+            rx.zero();
+            rr.zero();
+        }
+    };
+    long long row = (long long)blockIdx.x * rpb + slot;
+    f2 w[P];
+    if (HOLD) {
+        fetch(row);
+        load_weight<T, VEC, NV>(a, col, w);
+    }
     int parity = 0;
-    for (long long r0 = (long long)blockIdx.x * rpb; r0 < a.rows; r0 += (long long)gridDim.x * rpb, parity ^= 1) {
-        const long long row = r0 + slot;
+    // (all threads of a block run the same number of rounds: its last slot's rows may lie past the end)
+    for (long long r0 = (long long)blockIdx.x * rpb; r0 < a.rows; r0 += step, row += step, parity ^= 1) {
         const bool live = row < a.rows;
-        const T *x = static_cast<const T *>(a.x) + row * a.x_ld;
-        float h[EPT];
+        f2 h[P], ss2 = 0ull;
+        if (!HOLD) fetch(row);
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = col(v);
-            if (live && c < a.D) {
-                load_vec<T, VEC>(x + c, h + v * VEC);
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) h[v * VEC + i] = 0.f;
-            }
+        for (int i = 0; i < P; ++i) {
+            h[i] = rx.template pair<T>(i);
+            if (RES != RES_NONE) h[i] = add2(h[i], rr.template pair<T>(i));
+            ss2 = fma2(h[i], h[i], ss2);
         }
-        if (a.res_kind != RES_NONE) {
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int c = col(v);
-                if (!(live && c < a.D)) continue;
-                float e[VEC];
-                if (a.res_kind == RES_F32)
-                    load_vec_f32<VEC>(static_cast<const float *>(a.res) + row * a.D + c, e);
-                else
-                    load_vec<T, VEC>(static_cast<const T *>(a.res) + row * a.D + c, e);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) h[v * VEC + i] += e[i];
-                if (a.res_kind == RES_F32)
-                    store_vec_f32<VEC>(static_cast<float *>(a.res_out) + row * a.D + c, h + v * VEC);
-                else
-                    store_vec<T, VEC>(static_cast<T *>(a.res_out) + row * a.D + c, h + v * VEC);
-            }
-        }
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) ss = fmaf(h[i], h[i], ss);
-        ss = lanes_sum(ss, lanes);
+        if (HOLD) fetch(row + step);
+        if (RES != RES_NONE && live) store_row<T, VEC, NV, RES == RES_F32>(a.res_out, row * a.D, col, a.D, h);
+        float ss = lanes_sum(sum2(ss2), lanes);
         if (tpr > 32) {
             if (lane == 0) s_sum[parity][warp] = ss;
             __syncthreads();
             ss = 0.f;
             for (int i = 0; i < wpr; ++i) ss += s_sum[parity][slot * wpr + i];
         }
-        const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
+        const f2 r = both(rsqrtf(fmaf(ss, inv_d, a.eps)));
+        if (!HOLD) load_weight<T, VEC, NV>(a, col, w);
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = col(v);
-            if (c >= a.D) continue;
-            float w[VEC];
-            if (a.w_f32)
-                load_vec_f32<VEC>(static_cast<const float *>(a.w) + c, w);
-            else
-                load_vec<T, VEC>(static_cast<const T *>(a.w) + c, w);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) h[v * VEC + i] *= r * w[i];
-        }
+        for (int i = 0; i < P; ++i) h[i] = mul2(mul2(h[i], r), w[i]);
         if constexpr (!QUANT) {
-#pragma unroll
-            for (int v = 0; v < NV; ++v) {
-                const int c = col(v);
-                if (live && c < a.D) store_vec<T, VEC>(static_cast<T *>(a.y) + row * a.D + c, h + v * VEC);
-            }
+            if (live) store_row<T, VEC, NV, false>(a.y, row * a.D, col, a.D, h);
         } else {
-            // largest magnitude of each vector, then of its scale's columns
-            uint32_t m[NV];
+            float y[2 * P], m[NV];  // largest magnitude of each vector, then of its scale's columns
+#pragma unroll
+            for (int i = 0; i < P; ++i) unpack2(h[i], y[2 * i], y[2 * i + 1]);
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
-                m[v] = 0;
+                m[v] = 0.f;
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) m[v] = max(m[v], abs_bits(h[v * VEC + i]));
+                for (int i = 0; i < VEC; ++i) m[v] = max_abs(m[v], y[v * VEC + i]);
             }
             if (a.group == 0) {
-                uint32_t mm = 0;
+                float mm = 0.f;
 #pragma unroll
-                for (int v = 0; v < NV; ++v) mm = max(mm, m[v]);
+                for (int v = 0; v < NV; ++v) mm = max_abs(mm, m[v]);
                 mm = lanes_max(mm, lanes);
                 if (tpr > 32) {
                     if (lane == 0) s_max[parity][warp] = mm;
                     __syncthreads();
-                    mm = 0;
-                    for (int i = 0; i < wpr; ++i) mm = max(mm, s_max[parity][slot * wpr + i]);
+                    mm = 0.f;
+                    for (int i = 0; i < wpr; ++i) mm = max_abs(mm, s_max[parity][slot * wpr + i]);
                 }
 #pragma unroll
                 for (int v = 0; v < NV; ++v) m[v] = mm;
             } else if (VEC == 8) {
                 // 16 lanes of 8 columns are a group; a row of 8 lanes has at most 128 columns, all one group
                 if (tpr < 16) {
-                    uint32_t mm = 0;
+                    float mm = 0.f;
 #pragma unroll
-                    for (int v = 0; v < NV; ++v) mm = max(mm, m[v]);
+                    for (int v = 0; v < NV; ++v) mm = max_abs(mm, m[v]);
                     mm = lanes_max(mm, 8);
 #pragma unroll
                     for (int v = 0; v < NV; ++v) m[v] = mm;
@@ -221,7 +254,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(const NormArgs a
                 // four steps of a warp are a group
 #pragma unroll
                 for (int q = 0; q + 3 < NV; q += 4) {
-                    const uint32_t mm = max(max(m[q], m[q + 1]), max(m[q + 2], m[q + 3]));
+                    const float mm = max_abs(max_abs(m[q], m[q + 1]), max_abs(m[q + 2], m[q + 3]));
                     m[q] = m[q + 1] = m[q + 2] = m[q + 3] = lanes_max(mm, 32);
                 }
             }
@@ -229,23 +262,21 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(const NormArgs a
             for (int v = 0; v < NV; ++v) {
                 const int c = col(v);
                 if (!(live && c < a.D)) continue;
-                const float mx = __uint_as_float(m[v]);
-                const float sc = (mx < 1e-30f ? 1e-30f : mx) / 448.0f;  // (a NaN stays)
+                const float sc = (m[v] < 1e-30f ? 1e-30f : m[v]) * (1.0f / 448.0f);  // (a NaN stays)
                 const float is = 1.0f / sc;
+                const float *e = y + v * VEC;
                 unsigned char *q = static_cast<unsigned char *>(a.y) + row * a.D + c;
-                if (VEC == 8) {
+                if constexpr (VEC == 8) {
                     uint32_t u[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float *e = h + v * VEC + 4 * i;
-                        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(e[0] * is, e[1] * is), __NV_SATFINITE, __NV_E4M3);
-                        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(e[2] * is, e[3] * is), __NV_SATFINITE, __NV_E4M3);
+                        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(e[4 * i] * is, e[4 * i + 1] * is), __NV_SATFINITE, __NV_E4M3);
+                        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(e[4 * i + 2] * is, e[4 * i + 3] * is), __NV_SATFINITE, __NV_E4M3);
                         u[i] = lo | (hi << 16);
                     }
                     *reinterpret_cast<uint2 *>(q) = make_uint2(u[0], u[1]);
                 } else {
-#pragma unroll
-                    for (int i = 0; i < VEC; ++i) q[i] = __nv_cvt_float_to_fp8(h[v * VEC + i] * is, __NV_SATFINITE, __NV_E4M3);
+                    q[0] = __nv_cvt_float_to_fp8(e[0] * is, __NV_SATFINITE, __NV_E4M3);
                 }
                 if (a.group == 0 ? c == 0 : (c & 127) == 0) a.scale[row * a.nscale + (a.group ? c >> 7 : 0)] = sc;
             }
@@ -255,56 +286,57 @@ __global__ void __launch_bounds__(kNormThreads) norm_fwd_kernel(const NormArgs a
 
 // Each block walks rows and keeps its threads' share of dw in registers; the per-block sums are added by
 // reduce_rows_kernel in a fixed order.
-template <typename T, int VEC, int NV>
-__global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(const NormArgs a) {
-    constexpr int EPT = VEC * NV;
-    __shared__ float2 s_sum[2][32];
+template <typename T, int VEC, int NV, int BT, bool F32>
+__global__ void __launch_bounds__(BT, Bounds<VEC * NV, BT>::bwd) norm_bwd_kernel(const NormArgs a) {
+    constexpr int P = VEC * NV / 2;
+    constexpr bool HOLD = Bounds<VEC * NV, BT>::hold;
+    __shared__ float2 s_sum[2][16];
     const int tpr = a.tpr, slot = threadIdx.x / tpr, t = threadIdx.x & (tpr - 1);
     const int rpb = blockDim.x / tpr, lanes = min(tpr, 32), wpr = tpr >> 5;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Cols<VEC> col(tpr, t);
     const float inv_d = 1.0f / (float)a.D;
-    float dw[EPT];
+    const long long step = (long long)gridDim.x * rpb;
+    RawRow<VEC, NV, F32> rh, re;  // h; the gradient that reaches the summed stream from later layers
+    RawRow<VEC, NV, false> rg;    // dy
+    auto fetch = [&](long long row) {
+        if (row < a.rows) {
+            rh.load(a.x, row * a.x_ld, col, a.D);
+            rg.load(a.dy, row * a.D, col, a.D);
+            if (HOLD && a.res) re.load(a.res, row * a.D, col, a.D);
+        } else {
+            rh.zero();
+            rg.zero();
+            re.zero();
+        }
+    };
+    long long row = (long long)blockIdx.x * rpb + slot;
+    re.zero();
+    f2 w[P], dw[P];
+    if (HOLD) {
+        fetch(row);
+        load_weight<T, VEC, NV>(a, col, w);
+    }
 #pragma unroll
-    for (int i = 0; i < EPT; ++i) dw[i] = 0.f;
+    for (int i = 0; i < P; ++i) dw[i] = 0ull;
     int parity = 0;
-    for (long long r0 = (long long)blockIdx.x * rpb; r0 < a.rows; r0 += (long long)gridDim.x * rpb, parity ^= 1) {
-        const long long row = r0 + slot;
+    for (long long r0 = (long long)blockIdx.x * rpb; r0 < a.rows; r0 += step, row += step, parity ^= 1) {
         const bool live = row < a.rows;
-        float h[EPT], g[EPT];  // g: dy, then w dy
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = col(v);
-            if (live && c < a.D) {
-                if (a.res_kind == RES_F32)
-                    load_vec_f32<VEC>(static_cast<const float *>(a.x) + row * a.x_ld + c, h + v * VEC);
-                else
-                    load_vec<T, VEC>(static_cast<const T *>(a.x) + row * a.x_ld + c, h + v * VEC);
-                load_vec<T, VEC>(static_cast<const T *>(a.dy) + row * a.D + c, g + v * VEC);
-            } else {
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) h[v * VEC + i] = g[v * VEC + i] = 0.f;
-            }
+        f2 h[P], g[P], e[P], ss2 = 0ull, sd2 = 0ull;
+        if (!HOLD) {
+            fetch(row);
+            load_weight<T, VEC, NV>(a, col, w);
         }
-        float ss = 0.f, sd = 0.f;
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = col(v);
-            if (c >= a.D) continue;
-            float w[VEC];
-            if (a.w_f32)
-                load_vec_f32<VEC>(static_cast<const float *>(a.w) + c, w);
-            else
-                load_vec<T, VEC>(static_cast<const T *>(a.w) + c, w);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const int k = v * VEC + i;
-                ss = fmaf(h[k], h[k], ss);
-                sd = fmaf(g[k] * w[i], h[k], sd);
-            }
+        for (int i = 0; i < P; ++i) {
+            h[i] = rh.template pair<T>(i);
+            g[i] = rg.template pair<T>(i);
+            if (HOLD) e[i] = re.template pair<T>(i);
+            ss2 = fma2(h[i], h[i], ss2);
+            sd2 = fma2(mul2(g[i], w[i]), h[i], sd2);
         }
-        ss = lanes_sum(ss, lanes);
-        sd = lanes_sum(sd, lanes);
+        if (HOLD) fetch(row + step);
+        float ss = lanes_sum(sum2(ss2), lanes), sd = lanes_sum(sum2(sd2), lanes);
         if (tpr > 32) {
             if (lane == 0) s_sum[parity][warp] = make_float2(ss, sd);
             __syncthreads();
@@ -315,72 +347,27 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_kernel(const NormArgs a
             }
         }
         const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
-        const float k2 = r * r * (sd * inv_d);
-        const float one = a.eps * r * r;  // 1 - h^2 r^2 at D = 1, where the two terms below cancel but for it
+        const f2 r2 = both(r), k2 = both(-(r * r * r) * (sd * inv_d));
+        if (!HOLD) {
+            // (the weights again, and the later layers' gradient, now that dy's registers are to be freed)
+            load_weight<T, VEC, NV>(a, col, w);
+            if (a.res && live) re.load(a.res, row * a.D, col, a.D);
+        }
+        // at D = 1 the two terms of dh cancel but for 1 - h^2 r^2 = eps r^2
+        const f2 one = both(a.D == 1 ? a.eps * r * r * r : r);
 #pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = col(v);
-            if (!(live && c < a.D)) continue;
-            float w[VEC], d[VEC], e[VEC];
-            if (a.w_f32)
-                load_vec_f32<VEC>(static_cast<const float *>(a.w) + c, w);
-            else
-                load_vec<T, VEC>(static_cast<const T *>(a.w) + c, w);
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                const int k = v * VEC + i;
-                dw[k] = fmaf(g[k], h[k] * r, dw[k]);
-                d[i] = r * (a.D == 1 ? g[k] * w[i] * one : g[k] * w[i] - h[k] * k2);
-            }
-            if (a.res) {  // the gradient that reaches the summed stream from later layers
-                if (a.res_kind == RES_F32)
-                    load_vec_f32<VEC>(static_cast<const float *>(a.res) + row * a.D + c, e);
-                else
-                    load_vec<T, VEC>(static_cast<const T *>(a.res) + row * a.D + c, e);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) d[i] += e[i];
-            }
-            store_vec<T, VEC>(static_cast<T *>(a.dx) + row * a.D + c, d);
-            if (a.dres) store_vec_f32<VEC>(static_cast<float *>(a.dres) + row * a.D + c, d);
+        for (int i = 0; i < P; ++i) {
+            dw[i] = fma2(g[i], mul2(h[i], r2), dw[i]);
+            const f2 own = mul2(mul2(g[i], w[i]), one);
+            if (!HOLD) e[i] = re.template pair<T>(i);
+            h[i] = add2(e[i], a.D == 1 ? own : fma2(h[i], k2, own));
+        }
+        if (live) {
+            store_row<T, VEC, NV, false>(a.dx, row * a.D, col, a.D, h);
+            if (F32 && a.dres) store_row<T, VEC, NV, true>(a.dres, row * a.D, col, a.D, h);
         }
     }
-    float *part = a.dw_part + ((long long)blockIdx.x * rpb + slot) * a.D;
-#pragma unroll
-    for (int v = 0; v < NV; ++v) {
-        const int c = col(v);
-        if (c < a.D) store_vec_f32<VEC>(part + c, dw + v * VEC);
-    }
-}
-
-// out[c] = sum over `parts` rows of part[.][c]: 32 columns a block, its eight warps take every eighth row.
-template <typename T>
-__global__ void __launch_bounds__(256) reduce_rows_kernel(const float *part, long long parts, long long stride, int cols,
-                                                          void *out, bool out_f32) {
-    __shared__ float s[8][33];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
-    float x = 0.f;
-    if (c < cols) {
-        float p[4] = {0.f, 0.f, 0.f, 0.f};
-        long long i = warp;
-        for (; i + 24 < parts; i += 32) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) p[k] += part[(i + 8 * k) * stride + c];
-        }
-        for (; i < parts; i += 8) p[0] += part[i * stride + c];
-        x = (p[0] + p[1]) + (p[2] + p[3]);
-    }
-    s[warp][lane] = x;
-    __syncthreads();
-    if (warp == 0 && c < cols) {
-        float y = 0.f;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) y += s[k][lane];
-        if (out_f32)
-            static_cast<float *>(out)[c] = y;
-        else
-            static_cast<T *>(out)[c] = Elt<T>::from_f(y);
-    }
+    store_row<T, VEC, NV, true>(a.dw_part, ((long long)blockIdx.x * rpb + slot) * a.D, col, a.D, dw);
 }
 
 // Threads a row: the power of two that covers D with 16 elements a thread (32 for rows over 8,192).
@@ -389,7 +376,7 @@ struct NormShape {
 };
 NormShape norm_shape(int D, bool vec) {
     NormShape s;
-    s.ept = D <= 16 * kNormThreads ? 16 : 32;
+    s.ept = D <= 8192 ? 16 : 32;
     s.tpr = vec ? 8 : 32;
     while (s.tpr * s.ept < D) s.tpr *= 2;
     s.threads = s.tpr < 256 ? 256 : s.tpr;
@@ -397,34 +384,43 @@ NormShape norm_shape(int D, bool vec) {
     return s;
 }
 
-// Blocks of the backward: as many as are resident at once, so that dw is summed over few partial rows.
-int norm_bwd_blocks(long long rows, const NormShape &s) {
+// Blocks: at most as many as are resident at once; each walks rows, with its weights in registers and its next
+// row's loads in flight.
+int norm_blocks(long long rows, const NormShape &s, bool bwd) {
     const long long need = (rows + s.rpb - 1) / s.rpb;
-    const long long most = (long long)kSMs * (1024 / s.threads);
+    const long long most = (long long)kSMs * (s.threads == 256 ? (bwd ? 2 : 3) : 1);
     return (int)(need < most ? need : most);
 }
 
-template <typename T, bool QUANT>
-cudaError_t norm_fwd_t(const NormArgs &a, const NormShape &s, bool vec, cudaStream_t st) {
-    const long long need = (a.rows + s.rpb - 1) / s.rpb;
-    const dim3 grid((unsigned)(need < 0x7fffffff ? need : 0x7fffffff)), block(s.threads);
-    if (vec) {
-        if (s.ept == 16) return launch_plain(norm_fwd_kernel<T, 8, 2, QUANT>, grid, block, 0, st, a);
-        return launch_plain(norm_fwd_kernel<T, 8, 4, QUANT>, grid, block, 0, st, a);
+template <typename T, int VEC, int EPT, int BT>
+cudaError_t norm_fwd_v(const NormArgs &a, bool quant, int res, dim3 grid, cudaStream_t st) {
+    constexpr int NV = EPT / VEC;
+    const dim3 block(BT);
+    if (quant) {
+        if (res == RES_NONE) return launch_plain(norm_fwd_kernel<T, VEC, NV, BT, true, RES_NONE>, grid, block, 0, st, a);
+        if (res == RES_HALF) return launch_plain(norm_fwd_kernel<T, VEC, NV, BT, true, RES_HALF>, grid, block, 0, st, a);
+        return launch_plain(norm_fwd_kernel<T, VEC, NV, BT, true, RES_F32>, grid, block, 0, st, a);
     }
-    if (s.ept == 16) return launch_plain(norm_fwd_kernel<T, 1, 16, QUANT>, grid, block, 0, st, a);
-    return launch_plain(norm_fwd_kernel<T, 1, 32, QUANT>, grid, block, 0, st, a);
+    if (res == RES_NONE) return launch_plain(norm_fwd_kernel<T, VEC, NV, BT, false, RES_NONE>, grid, block, 0, st, a);
+    if (res == RES_HALF) return launch_plain(norm_fwd_kernel<T, VEC, NV, BT, false, RES_HALF>, grid, block, 0, st, a);
+    return launch_plain(norm_fwd_kernel<T, VEC, NV, BT, false, RES_F32>, grid, block, 0, st, a);
 }
-
-template <typename T>
-cudaError_t norm_bwd_t(const NormArgs &a, const NormShape &s, bool vec, int blocks, cudaStream_t st) {
-    const dim3 grid(blocks), block(s.threads);
-    if (vec) {
-        if (s.ept == 16) return launch_plain(norm_bwd_kernel<T, 8, 2>, grid, block, 0, st, a);
-        return launch_plain(norm_bwd_kernel<T, 8, 4>, grid, block, 0, st, a);
-    }
-    if (s.ept == 16) return launch_plain(norm_bwd_kernel<T, 1, 16>, grid, block, 0, st, a);
-    return launch_plain(norm_bwd_kernel<T, 1, 32>, grid, block, 0, st, a);
+template <typename T, int VEC>
+cudaError_t norm_fwd_t(const NormArgs &a, const NormShape &s, bool quant, int res, cudaStream_t st) {
+    const dim3 grid(norm_blocks(a.rows, s, false));
+    if (s.ept == 32) return norm_fwd_v<T, VEC, 32, 512>(a, quant, res, grid, st);
+    return s.threads == 256 ? norm_fwd_v<T, VEC, 16, 256>(a, quant, res, grid, st)
+                            : norm_fwd_v<T, VEC, 16, 512>(a, quant, res, grid, st);
+}
+template <typename T, int VEC, int EPT, int BT>
+cudaError_t norm_bwd_v(const NormArgs &a, bool f32, int blocks, cudaStream_t st) {
+    if (f32) return launch_plain(norm_bwd_kernel<T, VEC, EPT / VEC, BT, true>, dim3(blocks), dim3(BT), 0, st, a);
+    return launch_plain(norm_bwd_kernel<T, VEC, EPT / VEC, BT, false>, dim3(blocks), dim3(BT), 0, st, a);
+}
+template <typename T, int VEC>
+cudaError_t norm_bwd_t(const NormArgs &a, const NormShape &s, bool f32, int blocks, cudaStream_t st) {
+    if (s.ept == 32) return norm_bwd_v<T, VEC, 32, 512>(a, f32, blocks, st);
+    return s.threads == 256 ? norm_bwd_v<T, VEC, 16, 256>(a, f32, blocks, st) : norm_bwd_v<T, VEC, 16, 512>(a, f32, blocks, st);
 }
 
 gdr_status check_norm(const gdr_norm_problem *p) {
@@ -447,15 +443,6 @@ bool norm_ptr(const void *p, size_t elem, size_t vec_bytes, bool *vec) {
 }
 
 }  // namespace
-
-cudaError_t launch_reduce_rows(const float *part, long long parts, long long stride, int cols, void *out, bool bf16,
-                               bool out_f32, cudaStream_t s) {
-    const dim3 grid((unsigned)((cols + 31) / 32));
-    if (bf16)
-        return launch_plain(reduce_rows_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, part, parts, stride, cols, out,
-                            out_f32);
-    return launch_plain(reduce_rows_kernel<__half>, grid, dim3(256), 0, s, part, parts, stride, cols, out, out_f32);
-}
 
 }  // namespace gdr
 
@@ -485,14 +472,14 @@ gdr_status gdr_norm_fwd(const gdr_norm_problem *p, const void *x, const void *we
     a.group = p->scale_group;
     a.nscale = p->scale_group ? (p->D + 127) / 128 : 1;
     a.w_f32 = p->weight_dtype == GDR_FP32;
-    a.res_kind = !residual ? RES_NONE : p->residual_dtype == GDR_FP32 ? RES_F32 : RES_HALF;
+    const int res = !residual ? RES_NONE : p->residual_dtype == GDR_FP32 ? RES_F32 : RES_HALF;
     const NormShape s = norm_shape(p->D, vec);
     a.tpr = s.tpr;
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     return timed(K_NORM_FWD, cs, [&] {
         if (p->dtype == GDR_BF16)
-            return quant ? norm_fwd_t<__nv_bfloat16, true>(a, s, vec, cs) : norm_fwd_t<__nv_bfloat16, false>(a, s, vec, cs);
-        return quant ? norm_fwd_t<__half, true>(a, s, vec, cs) : norm_fwd_t<__half, false>(a, s, vec, cs);
+            return vec ? norm_fwd_t<__nv_bfloat16, 8>(a, s, quant, res, cs) : norm_fwd_t<__nv_bfloat16, 1>(a, s, quant, res, cs);
+        return vec ? norm_fwd_t<__half, 8>(a, s, quant, res, cs) : norm_fwd_t<__half, 1>(a, s, quant, res, cs);
     });
 }
 
@@ -502,7 +489,7 @@ gdr_status gdr_norm_bwd_workspace_size(const gdr_norm_problem *p, size_t *bytes)
     if (!bytes) return GDR_ERR_NULL;
     // (the wide path packs more of a narrow row's partial sums into a block: its size covers both)
     const NormShape s = norm_shape(p->D, true);
-    const int blocks = p->rows ? norm_bwd_blocks(p->rows, s) : 0;
+    const int blocks = p->rows ? norm_blocks(p->rows, s, true) : 0;
     *bytes = round_up((size_t)blocks * s.rpb * p->D * sizeof(float), 256);
     return GDR_OK;
 }
@@ -532,18 +519,18 @@ gdr_status gdr_norm_bwd(const gdr_norm_problem *p, const void *h, const void *we
     a.dw_part = static_cast<float *>(workspace);
     a.rows = p->rows, a.x_ld = p->x_ld, a.D = p->D, a.eps = p->eps;
     a.w_f32 = p->weight_dtype == GDR_FP32;
-    a.res_kind = f32 ? RES_F32 : RES_HALF;
     const NormShape s = norm_shape(p->D, vec);
     a.tpr = s.tpr;
-    const int blocks = norm_bwd_blocks(p->rows, s);
+    const int blocks = norm_blocks(p->rows, s, true);
     st = timed(K_NORM_BWD, cs, [&] {
-        return p->dtype == GDR_BF16 ? norm_bwd_t<__nv_bfloat16>(a, s, vec, blocks, cs)
-                                    : norm_bwd_t<__half>(a, s, vec, blocks, cs);
+        if (p->dtype == GDR_BF16)
+            return vec ? norm_bwd_t<__nv_bfloat16, 8>(a, s, f32, blocks, cs) : norm_bwd_t<__nv_bfloat16, 1>(a, s, f32, blocks, cs);
+        return vec ? norm_bwd_t<__half, 8>(a, s, f32, blocks, cs) : norm_bwd_t<__half, 1>(a, s, f32, blocks, cs);
     });
     if (st != GDR_OK) return st;
     return timed(K_REDUCE, cs, [&] {
-        return launch_reduce_rows(a.dw_part, (long long)blocks * s.rpb, p->D, p->D, dweight, p->dtype == GDR_BF16,
-                                  a.w_f32, cs);
+        const RowSums out = {dweight, p->D};
+        return launch_reduce_rows(a.dw_part, (long long)blocks * s.rpb, p->D, &out, 1, p->dtype == GDR_BF16, a.w_f32, cs);
     });
 }
 

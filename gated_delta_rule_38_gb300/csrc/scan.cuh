@@ -11,6 +11,7 @@
 #include <stdint.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "host.h"
 #include "launch.h"
 #include "seqwalk.cuh"
@@ -19,7 +20,6 @@ namespace gdr {
 namespace scan {
 
 constexpr int SAVE = 16;       // tokens between saved states; segments are multiples of it
-constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 struct ScanArgs {
     const void *x, *dt, *z, *Bm, *Cm;
@@ -32,7 +32,9 @@ struct ScanArgs {
     const void *dy;
     const float *dstate_out;
     void *dx, *ddt, *dz, *dB, *dC;
-    float *dstate_in, *dA_part, *dD_part, *dbias_part, *dbc_part;
+    float *dstate_in, *dbc_part;
+    float *param_part;     // [B nseg][dA | dD | ddt_bias]: rows of param_ld floats, the latter two at dD_at, dbias_at
+    long long param_ld, dD_at, dbias_at;
     const int32_t *cu;
     unsigned *err;
     long long x_ld, dt_ld, z_ld, b_ld, c_ld;
@@ -43,45 +45,6 @@ struct ScanArgs {
     bool softplus, vec, vec_bc, st_vec;
 };
 
-// ---------------------------------------------------------------- two fp32 at a time
-
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pack2(float a, float b) {
-    f2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpack2(f2 v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-    f2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 add2(f2 a, f2 b) {
-    f2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-    f2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ f2 exp2x2(f2 v) {
-    float a, b;
-    unpack2(v, a, b);
-    return pack2(ex2(a), ex2(b));
-}
-__device__ __forceinline__ float sum2(f2 v) {
-    float a, b;
-    unpack2(v, a, b);
-    return a + b;
-}
 struct F2x2 {
     f2 lo, hi;
 };
@@ -90,24 +53,31 @@ __device__ __forceinline__ F2x2 lds_f2x2(const float *p) {
     return F2x2{v.x, v.y};
 }
 
-// ---------------------------------------------------------------- scalar functions
+// ---------------------------------------------------------------- pairs of scalars
 
-// log(1 + e^x) = max(x, 0) + log1p(t) with t = e^-|x|, and log1p(t) = 2 atanh(t / (2 + t)) by atanh's series in
-// s = t / (2 + t) <= 1/3: the terms left out are below 2e-9 of the sum, so small steps keep their relative precision.
-__device__ __forceinline__ float softplus(float x) {
-    const float t = ex2(-fabsf(x) * LOG2E);
-    const float s = __fdividef(t, 2.f + t), q = s * s;
-    float p = 1.f / 15.f;
-    p = fmaf(p, q, 1.f / 13.f);
-    p = fmaf(p, q, 1.f / 11.f);
-    p = fmaf(p, q, 1.f / 9.f);
-    p = fmaf(p, q, 1.f / 7.f);
-    p = fmaf(p, q, 1.f / 5.f);
-    p = fmaf(p, q, 1.f / 3.f);
-    p = fmaf(p, q, 1.f);
-    return fmaf(2.f * s, p, fmaxf(x, 0.f));
+// log(1 + e^x) = max(x, 0) + log1p(t), t = e^-|x| in (0, 1], with log1p(t) = t P(t).  P is the polynomial of degree 8
+// that minimises the largest relative error on [0, 1] (3.0e-8; found by the exchange algorithm of Remez), so small
+// steps keep their relative precision, which a logarithm of 1 + t would lose.
+__device__ __forceinline__ f2 softplus2(f2 x) {
+    float a, b;
+    unpack2(x, a, b);
+    const f2 t = ex2x2(mul2(pack2(-fabsf(a), -fabsf(b)), both(LOG2E)));
+    f2 p = both(0.0052326941f);
+    p = fma2(p, t, both(-0.0295052398f));
+    p = fma2(p, t, both(0.0782259554f));
+    p = fma2(p, t, both(-0.1366324574f));
+    p = fma2(p, t, both(0.1910600662f));
+    p = fma2(p, t, both(-0.2484298199f));
+    p = fma2(p, t, both(0.3331909776f));
+    p = fma2(p, t, both(-0.4999949336f));
+    p = fma2(p, t, both(0.9999999404f));
+    return fma2(p, t, pack2(fmaxf(a, 0.f), fmaxf(b, 0.f)));
 }
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + ex2(-x * LOG2E)); }
+__device__ __forceinline__ float softplus(float x) {
+    float a, b;
+    unpack2(softplus2(pack2(x, x)), a, b);
+    return a;
+}
 
 // ---------------------------------------------------------------- geometry
 
@@ -145,26 +115,42 @@ __device__ __forceinline__ void store8(uint16_t *p, uint4 u, int n, bool vec) {
     for (int i = 0; i < 8; ++i)
         if (i < n) p[i] = (uint16_t)(r[i >> 1] >> (16 * (i & 1)));
 }
+// Eight 16-bit elements as four fp32 pairs, and back.
 template <typename T>
-__device__ __forceinline__ void widen8(uint4 u, float *o) {
-    const uint32_t r[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = Elt<T>::unpack(r[i]);
-        o[2 * i] = f.x, o[2 * i + 1] = f.y;
-    }
+__device__ __forceinline__ void widen8(uint4 u, f2 *o) {
+    o[0] = widen2<T>(u.x), o[1] = widen2<T>(u.y), o[2] = widen2<T>(u.z), o[3] = widen2<T>(u.w);
 }
 template <typename T>
-__device__ __forceinline__ uint4 narrow8(const float *v) {
-    return make_uint4(Elt<T>::pack(v[0], v[1]), Elt<T>::pack(v[2], v[3]), Elt<T>::pack(v[4], v[5]), Elt<T>::pack(v[6], v[7]));
+__device__ __forceinline__ uint4 narrow8(const f2 *v) {
+    return make_uint4(narrow2<T>(v[0]), narrow2<T>(v[1]), narrow2<T>(v[2]), narrow2<T>(v[3]));
 }
-__device__ __forceinline__ void put8(float *p, const float *v) {
-    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void put8(float *p, const f2 *v) {
+    reinterpret_cast<ulonglong2 *>(p)[0] = make_ulonglong2(v[0], v[1]);
+    reinterpret_cast<ulonglong2 *>(p)[1] = make_ulonglong2(v[2], v[3]);
 }
-__device__ __forceinline__ void get8(const float *p, float *v) {
-    const float4 a = reinterpret_cast<const float4 *>(p)[0], b = reinterpret_cast<const float4 *>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+__device__ __forceinline__ void get8(const float *p, f2 *v) {
+    const ulonglong2 a = reinterpret_cast<const ulonglong2 *>(p)[0], b = reinterpret_cast<const ulonglong2 *>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+}
+
+// Asynchronous 16-byte copies, in groups (common.cuh's, as barriers for the compiler too: the copied places are read and
+// written by plain accesses around them).
+__device__ __forceinline__ void copy16(void *to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(LEFT) : "memory");
+}
+
+// Eight elements of a token row into this thread's own place in shared memory: an asynchronous copy where the row
+// allows 16-byte accesses and all eight exist, else plain loads.  `n` of them exist; the others become zeros.
+__device__ __forceinline__ void copy8(uint16_t *to, const uint16_t *from, int n, bool vec) {
+    if (vec && n >= 8)
+        copy16(to, from);
+    else
+        *reinterpret_cast<uint4 *>(to) = load8(from, n, false);
 }
 
 // Packed batches: the sequence that token t starts (first) and the one that it ends (last), -1 for neither.

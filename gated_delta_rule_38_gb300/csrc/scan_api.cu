@@ -49,21 +49,29 @@ Cover cover_of(const gdr_scan_problem *p, bool bwd) {
     c.gpad = (Dg + pad - 1) / pad * pad;
     c.gblocks = (Dg + CB - 1) / CB;
     c.DP = c.gpad * p->G;
-    // Segments: splitting costs a second, state-only pass, so the token axis is cut only when one block a channel
-    // block would leave most of the chip idle, and then into as many segments as fill it once.
-    const long long blocks = (long long)c.gblocks * p->G * p->B, slots = (long long)kSMs * (bwd ? 2 : 3);
-    long long want = blocks * 2 > slots ? 1 : slots / blocks;
-    const long long most = p->T / 64;                      // a segment is worth its start-up from 64 tokens on
-    want = want < most ? want : most;
-    if (want < 2) want = 1;
+    // Segments.  Splitting costs a state-only first pass (about 0.7 of a full one), so the token axis is cut only when
+    // one block a channel block would leave the chip idle, and into the number of segments with the least estimated
+    // time: blocks on the fullest SM (at least the few that it takes to hide their latencies) times the tokens of one,
+    // with 24 tokens' worth of start-up.
+    const long long blocks = (long long)c.gblocks * p->G * p->B, knee = bwd ? 2 : 4;
+    long long want = 1, best = 0;
+    for (long long n = 1; n == 1 || (n <= 64 && n * 64 <= p->T); ++n) {
+        long long q = (blocks * n + kSMs - 1) / kSMs;
+        q = q > knee ? (bwd ? (q + knee - 1) / knee * knee : q) : knee;
+        const long long cost = q * ((p->T + n - 1) / n + 24) * (n > 1 ? 17 : 10);
+        if (best == 0 || cost < best) best = cost, want = n;
+    }
     c.seglen = (int)(((p->T + want - 1) / want + SAVE - 1) / SAVE * SAVE);
     if (c.seglen < SAVE) c.seglen = SAVE;
     c.nseg = p->T > 0 ? (p->T + c.seglen - 1) / c.seglen : 1;
     return c;
 }
 
+// Floats of one partial row of the parameters' gradients (16-byte rows).
+size_t param_ld(const gdr_scan_problem *p) { return ((size_t)p->D * (p->N + 2) + 3) / 4 * 4; }
+
 struct Layout {
-    size_t seg = 0, segdt = 0, cut = 0, dA = 0, dD = 0, dbias = 0, dbc = 0, bytes = 0;
+    size_t seg = 0, segdt = 0, cut = 0, param = 0, dbc = 0, bytes = 0;
 };
 Layout layout_of(const gdr_scan_problem *p, bool bwd) {
     Layout l;
@@ -80,9 +88,7 @@ Layout layout_of(const gdr_scan_problem *p, bool bwd) {
         take(l.cut, c.nseg);
     }
     if (bwd) {
-        take(l.dA, parts * p->D * p->N);
-        take(l.dD, parts * p->D);
-        take(l.dbias, parts * p->D);
+        take(l.param, parts * param_ld(p));
         take(l.dbc, (size_t)c.gblocks * p->B * p->T * p->G * 2 * c.NP);
     }
     l.bytes = at;
@@ -120,6 +126,11 @@ struct Ptrs {
 
 bool token_strides(const gdr_scan_problem *p) {
     return (p->D / p->G) % 8 == 0 && p->x_ld % 8 == 0 && p->dt_ld % 8 == 0 && p->z_ld % 8 == 0;
+}
+
+// 16-byte pieces of B and C.
+bool bc_wide(const gdr_scan_problem *p, const void *B, const void *C) {
+    return p->N % 8 == 0 && p->b_ld % 8 == 0 && p->c_ld % 8 == 0 && aligned16(B) && aligned16(C);
 }
 
 gdr_status pass_states(const gdr_scan_problem *p, const float *src, float *dst, cudaStream_t s) {
@@ -185,6 +196,7 @@ gdr_status gdr_scan_fwd(const gdr_scan_problem *p, const void *x, const void *dt
     a.x = x, a.dt = dt, a.z = z, a.Bm = B, a.Cm = C, a.A = A, a.skip = D, a.bias = dt_bias, a.state_in = state_in;
     a.y = y, a.state_out = state_out, a.saved = static_cast<float *>(saved);
     a.vec = tok.wide && token_strides(p);
+    a.vec_bc = bc_wide(p, B, C);
     a.st_vec = states.wide && p->N % 4 == 0;
     const bool bf = p->dtype == GDR_BF16;
     if (c.nseg > 1) {
@@ -262,11 +274,13 @@ gdr_status gdr_scan_bwd(const gdr_scan_problem *p, const void *x, const void *dt
     a.x = x, a.dt = dt, a.z = z, a.Bm = B, a.Cm = C, a.A = A, a.skip = D, a.bias = dt_bias, a.state_in = state_in;
     a.dy = dy, a.dstate_out = dstate_out, a.saved = static_cast<float *>(const_cast<void *>(saved));
     a.dx = dx, a.ddt = ddt, a.dz = dz, a.dB = dB, a.dC = dC, a.dstate_in = dstate_in;
-    a.dA_part = at<float>(workspace, l.dA);
-    a.dD_part = D ? at<float>(workspace, l.dD) : nullptr;
-    a.dbias_part = dt_bias ? at<float>(workspace, l.dbias) : nullptr;
+    a.param_part = at<float>(workspace, l.param);
+    a.param_ld = param_ld(p);
+    a.dD_at = D ? (int64_t)p->D * p->N : -1;
+    a.dbias_at = dt_bias ? (int64_t)p->D * (p->N + (D ? 1 : 0)) : -1;
     a.dbc_part = at<float>(workspace, l.dbc);
     a.vec = tok.wide && token_strides(p);
+    a.vec_bc = bc_wide(p, B, C);
     a.st_vec = states.wide && p->N % 4 == 0;
     const bool bf = p->dtype == GDR_BF16;
     if (c.nseg > 1) {
@@ -281,13 +295,14 @@ gdr_status gdr_scan_bwd(const gdr_scan_problem *p, const void *x, const void *dt
     if (st != GDR_OK) return st;
     st = timed(K_REDUCE, cs, [&] { return launch_scan_dbc(a, c.L, bf, cs); });
     if (st != GDR_OK) return st;
-    const long long parts = (long long)p->B * c.nseg;
-    const int dn = p->D * p->N;
-    st = timed(K_REDUCE, cs, [&] { return launch_reduce_rows(a.dA_part, parts, dn, dn, dA, bf, true, cs); });
-    if (st == GDR_OK && D)
-        st = timed(K_REDUCE, cs, [&] { return launch_reduce_rows(a.dD_part, parts, p->D, p->D, dD, bf, true, cs); });
-    if (st == GDR_OK && dt_bias)
-        st = timed(K_REDUCE, cs, [&] { return launch_reduce_rows(a.dbias_part, parts, p->D, p->D, ddt_bias, bf, true, cs); });
+    // the parameters' gradients: partial rows of [D N | D | D] a segment
+    st = timed(K_REDUCE, cs, [&] {
+        RowSums out[3] = {{dA, p->D * p->N}};
+        int n = 1;
+        if (D) out[n++] = {dD, p->D};
+        if (dt_bias) out[n++] = {ddt_bias, p->D};
+        return launch_reduce_rows(a.param_part, (long long)p->B * c.nseg, a.param_ld, out, n, bf, true, cs);
+    });
     if (st != GDR_OK || !p->cu_seqlens || !dstate_in) return st;
     return timed(K_SCAN_JOIN, cs, [&] { return launch_scan_empty(a, dstate_out, dstate_in, cs); });
 }

@@ -32,80 +32,138 @@ struct Bwd {
     static constexpr int CL = 32 / L;                    // channel lanes of a warp
     static constexpr int NVEC = TT * CB / 8;
     static constexpr int VPT = NVEC > NT ? NVEC / NT : 1;
+    static constexpr int VROW = CB / 8, VSTEP = NT / VROW;
+    static constexpr int BW = NP >= 8 ? 8 : 4;           // states of a vector of B or C
+    static constexpr int BROW = NP / BW, BSTEP = NT / BROW;
+    static constexpr int BPT = TT > BSTEP ? TT / BSTEP : 1;
 };
 
-template <int L>
+// The raw tiles (two of each: the next one is on its way while one is worked on) are private to the threads that copy
+// them, the states before the groups to the threads that own the states.
+template <int L, bool LOCAL>
 struct BwdSmem {
-    float delta[TT][Bwd<L>::CB];                         // then the gradient of delta
-    float x[TT][Bwd<L>::CB];                             // then dx
-    float gy[TT][Bwd<L>::CB];                            // then yp
-    float b[TT][Bwd<L>::NP][2];
-    float c[TT][Bwd<L>::NP][2];
-    float start[TT / SB][4][Bwd<L>::NT][4];              // the state before every group: thread-private
-    float red[Bwd<L>::NW][SB][Bwd<L>::CL][2 * Bwd<L>::NP];
-    float bc[Bwd<L>::NW][TT][2 * Bwd<L>::NP];            // a warp's sums of dB | dC
-    int first[TT], last[TT];
+    using W = Bwd<L>;
+    uint16_t raw[2][LOCAL ? 3 : 4][TT][W::CB];           // dt, dy, z, x
+    uint16_t raw_bc[2][LOCAL ? 1 : 2][TT][W::NP];        // C, B
+    float delta[TT][W::CB];                              // then the gradient of delta
+    float gy[TT][W::CB];                                 // then yp
+    float c[TT][W::NP][2];
+    float bias[W::CB];
+    int first[2][TT], last[2][TT];
+};
+template <int L>
+struct BwdFull : BwdSmem<L, false> {
+    using W = Bwd<L>;
+    float x[TT][W::CB];                                  // then dx
+    float b[TT][W::NP][2];
+    float start[TT / SB][4][W::NT][4];                   // the state before every group: thread-private
+    float red[W::NW][2][W::CL][2 * W::NP];               // two tokens' dB | dC of a warp's channel lanes
+    float bc[W::NW][TT][2 * W::NP];                      // a warp's sums of dB | dC
 };
 
-// Stages x, delta and gy of the tile at `base` (LOCAL: without x, and C without B).
-template <typename T, int L, bool LOCAL>
-__device__ __forceinline__ void stage(const ScanArgs &a, BwdSmem<L> &sm, const Chans<Bwd<L>::CB> &ch, int b, int base, int t1,
-                                      int vc, int vt, int vn, bool vlive, const float *bias) {
+// The copies of the tile at `base` into buffer `buf`.
+template <int L, bool LOCAL, bool PACKED>
+__device__ __forceinline__ void fetch(const ScanArgs &a, BwdSmem<L, LOCAL> &sm, const Chans<Bwd<L>::CB> &ch, int b, int base,
+                                      int t0, int t1, int buf) {
     using W = Bwd<L>;
-    constexpr int VSTEP = W::NT / (W::CB / 8);
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, vc = (tid % W::VROW) * 8, vt = tid / W::VROW, vn = ch.count - vc;
+    const int bn = (tid % W::BROW) * 8, bt = tid / W::BROW;
+    if (base >= t0) {
+#pragma unroll
+        for (int k = 0; k < W::VPT; ++k) {
+            const int j = vt + k * W::VSTEP, t = base + j;
+            if (j < TT && t < t1 && vn > 0) {
+                const long long row = (long long)b * a.T + t;
+                const int c = ch.first + vc;
+                copy8(&sm.raw[buf][0][j][vc], static_cast<const uint16_t *>(a.dt) + row * a.dt_ld + c, vn, a.vec);
+                copy8(&sm.raw[buf][1][j][vc], static_cast<const uint16_t *>(a.dy) + row * a.D + c, vn, a.vec);
+                if (a.z) copy8(&sm.raw[buf][2][j][vc], static_cast<const uint16_t *>(a.z) + row * a.z_ld + c, vn, a.vec);
+                if (!LOCAL) copy8(&sm.raw[buf][LOCAL ? 0 : 3][j][vc], static_cast<const uint16_t *>(a.x) + row * a.x_ld + c, vn, a.vec);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < W::BPT; ++k) {
+            const int j = bt + k * W::BSTEP, t = base + j;
+            if (j < TT && t < t1) {
+                const long long row = (long long)b * a.T + t;
+                const uint16_t *pc = static_cast<const uint16_t *>(a.Cm) + row * a.c_ld + ch.g * a.N + bn;
+                const uint16_t *pb = static_cast<const uint16_t *>(a.Bm) + row * a.b_ld + ch.g * a.N + bn;
+                if constexpr (W::BW == 8) {
+                    copy8(&sm.raw_bc[buf][0][j][bn], pc, a.N - bn, a.vec_bc);
+                    if (!LOCAL) copy8(&sm.raw_bc[buf][LOCAL ? 0 : 1][j][bn], pb, a.N - bn, a.vec_bc);
+                } else {
+                    for (int n = 0; n < W::BW; ++n) {
+                        sm.raw_bc[buf][0][j][n] = n < a.N ? pc[n] : (uint16_t)0;
+                        if (!LOCAL) sm.raw_bc[buf][LOCAL ? 0 : 1][j][n] = n < a.N ? pb[n] : (uint16_t)0;
+                    }
+                }
+            }
+        }
+        if (PACKED)
+            for (int j = tid; j < TT; j += W::NT) edges(a, base + j, t1, sm.first[buf][j], sm.last[buf][j]);
+    }
+    copies_commit();
+}
+
+// One raw row of B or C as duplicated fp32.
+template <typename T, int BW>
+__device__ __forceinline__ void spread(const uint16_t *r, bool in, float *o) {
+#pragma unroll
+    for (int n = 0; n < BW; n += 2) {
+        float v0, v1;
+        unpack2(widen2<T>(in ? *reinterpret_cast<const uint32_t *>(r + n) : 0u), v0, v1);
+        *reinterpret_cast<float4 *>(o + 2 * n) = make_float4(v0, v0, v1, v1);
+    }
+}
+
+// delta, gy and C of the tile that has arrived in `buf` (and through `xb` what the full pass adds).
+template <typename T, int L, bool LOCAL, typename F>
+__device__ __forceinline__ void stage(const ScanArgs &a, BwdSmem<L, LOCAL> &sm, const Chans<Bwd<L>::CB> &ch, int base, int t1,
+                                      int buf, F &&xb) {
+    using W = Bwd<L>;
+    const int tid = threadIdx.x, vc = (tid % W::VROW) * 8, vt = tid / W::VROW, vn = ch.count - vc;
+    const int bn = (tid % W::BROW) * 8, bt = tid / W::BROW;
 #pragma unroll
     for (int k = 0; k < W::VPT; ++k) {
-        const int j = vt + k * VSTEP, t = base + j;
-        if (!vlive) break;
-        const bool in = t < t1 && vn > 0;
-        const long long row = (long long)b * a.T + t;
-        const int c = ch.first + vc;
-        uint4 rx = make_uint4(0, 0, 0, 0), rd = rx, rz = rx, rg = rx;
+        const int j = vt + k * W::VSTEP;
+        if (j >= TT) break;
+        f2 d[4], g[4], v[4];
+        const bool in = base + j < t1 && vn > 0;
         if (in) {
-            rd = load8(static_cast<const uint16_t *>(a.dt) + row * a.dt_ld + c, vn, a.vec);
-            rg = load8(static_cast<const uint16_t *>(a.dy) + row * a.D + c, vn, a.vec);
-            if (!LOCAL) rx = load8(static_cast<const uint16_t *>(a.x) + row * a.x_ld + c, vn, a.vec);
-            if (a.z) rz = load8(static_cast<const uint16_t *>(a.z) + row * a.z_ld + c, vn, a.vec);
-        }
-        float d[8], g[8], v[8];
-        widen8<T>(rd, d);
-        widen8<T>(rg, g);
-        widen8<T>(rz, v);
+            widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][0][j][vc]), d);
+            widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][1][j][vc]), g);
+            get8(&sm.bias[vc], v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            d[i] += bias[i];
-            if (a.softplus) d[i] = softplus(d[i]);
-            d[i] = in && i < vn ? d[i] : 0.f;
-            if (a.z) g[i] *= v[i] * sigmoid(v[i]);
-            g[i] = in && i < vn ? g[i] : 0.f;
+            for (int i = 0; i < 4; ++i) {
+                d[i] = add2(d[i], v[i]);
+                if (a.softplus) d[i] = softplus2(d[i]);
+            }
+            if (a.z) {
+                widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][2][j][vc]), v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) g[i] = mul2(g[i], mul2(v[i], sigmoid2(v[i])));
+            }
+        } else {  // past the end: a step of zero and no gradient
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[i] = g[i] = 0ull;
         }
         put8(&sm.delta[j][vc], d);
         put8(&sm.gy[j][vc], g);
-        if (!LOCAL) {
-            widen8<T>(rx, v);
-            put8(&sm.x[j][vc], v);
-        }
+        xb(j, vc, in);
     }
-    for (int i = tid; i < TT * W::NP; i += W::NT) {
-        const int j = i / W::NP, n = i % W::NP, t = base + j;
-        float vb = 0.f, vcx = 0.f;
-        if (t < t1 && n < a.N) {
-            const long long row = (long long)b * a.T + t;
-            if (!LOCAL) vb = Elt<T>::to_f(static_cast<const T *>(a.Bm)[row * a.b_ld + ch.g * a.N + n]);
-            vcx = Elt<T>::to_f(static_cast<const T *>(a.Cm)[row * a.c_ld + ch.g * a.N + n]);
-        }
-        if (!LOCAL) *reinterpret_cast<float2 *>(sm.b[j][n]) = make_float2(vb, vb);
-        *reinterpret_cast<float2 *>(sm.c[j][n]) = make_float2(vcx, vcx);
+#pragma unroll
+    for (int k = 0; k < W::BPT; ++k) {
+        const int j = bt + k * W::BSTEP;
+        if (j < TT) spread<T, W::BW>(sm.raw_bc[buf][0][j] + bn, base + j < t1, sm.c[j][bn]);
     }
 }
 
 // First pass: the gradient that segment s sends back past its start when none reaches it from later segments.
 template <typename T, int L, bool PACKED>
-__global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_local_kernel(const ScanArgs a) {
+__global__ void __launch_bounds__(Bwd<L>::NT, L >= 4 ? 5 : 2) scan_bwd_local_kernel(const ScanArgs a) {
     using W = Bwd<L>;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    BwdSmem<L> &sm = *reinterpret_cast<BwdSmem<L> *>(smem_raw);
+    BwdSmem<L, true> &sm = *reinterpret_cast<BwdSmem<L, true> *>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nl = lane % L, cl = lane / L;
     const int nblk = a.gblocks * a.G, segs = a.nseg - 1;
@@ -114,12 +172,9 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_local_kernel(const ScanAr
     const Chans<W::CB> ch(a, blk);
     const int c0 = warp * (W::CL * 4) + cl * 4, n0 = nl * 4, nc = ch.count - c0;
     const int t0 = s * a.seglen, t1 = min(a.T, t0 + a.seglen);
-    constexpr int VROW = W::CB / 8;
-    const int vc = (tid % VROW) * 8, vt = tid / VROW, vn = ch.count - vc;
-    const bool vlive = W::NVEC >= W::NT || tid < W::NVEC;
-    float bias[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) bias[i] = (a.bias && i < vn) ? a.bias[ch.first + vc + i] : 0.f;
+    const int top = t0 + (t1 - 1 - t0) / TT * TT;
+    fetch<L, true, PACKED>(a, sm, ch, b, top, t0, t1, 0);
+    for (int i = tid; i < W::CB; i += W::NT) sm.bias[i] = (a.bias && i < ch.count) ? a.bias[ch.first + i] : 0.f;
     State A2, back;
     load_rows(a, a.A + (long long)(ch.first + c0) * a.N, nc, n0, A2, LOG2E);
     if (!PACKED && s == a.nseg - 1 && a.dstate_out)
@@ -128,15 +183,17 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_local_kernel(const ScanAr
         zero(back);
     f2 sum_lo = 0ull, sum_hi = 0ull;
     bool cut = false;
-    for (int base = t0 + (t1 - 1 - t0) / TT * TT; base >= t0; base -= TT) {
-        stage<T, L, true>(a, sm, ch, b, base, t1, vc, vt, vn, vlive, bias);
-        if (PACKED)
-            for (int j = tid; j < TT; j += W::NT) edges(a, base + j, t1, sm.first[j], sm.last[j]);
+    __syncthreads();
+    int buf = 0;
+    for (int base = top; base >= t0; base -= TT, buf ^= 1) {
+        fetch<L, true, PACKED>(a, sm, ch, b, base - TT, t0, t1, buf ^ 1);
+        copies_wait<1>();
+        stage<T, L, true>(a, sm, ch, base, t1, buf, [](int, int, bool) {});
         __syncthreads();
 #pragma unroll 4
         for (int j = TT - 1; j >= 0; --j) {
             if (PACKED) {
-                const int n = sm.last[j];
+                const int n = sm.last[buf][j];
                 if (n >= 0) {
                     cut = true;
                     if (a.dstate_out)
@@ -151,10 +208,10 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_local_kernel(const ScanAr
                 const F2x2 cc = lds_f2x2(sm.c[j][n0 + n]);
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    const f2 cn = m ? cc.hi : cc.lo;
+                    const f2 cm = m ? cc.hi : cc.lo;
                     f2 *k = back[n + m];
-                    k[0] = mul2(exp2x2(mul2(A2[n + m][0], d.lo)), fma2(gy.lo, cn, k[0]));
-                    k[1] = mul2(exp2x2(mul2(A2[n + m][1], d.hi)), fma2(gy.hi, cn, k[1]));
+                    k[0] = mul2(ex2x2(mul2(A2[n + m][0], d.lo)), fma2(gy.lo, cm, k[0]));
+                    k[1] = mul2(ex2x2(mul2(A2[n + m][1], d.hi)), fma2(gy.hi, cm, k[1]));
                 }
             }
             sum_lo = add2(sum_lo, d.lo);
@@ -162,6 +219,7 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_local_kernel(const ScanAr
         }
         __syncthreads();
     }
+    copies_wait<0>();
     const long long at = (long long)b * a.nseg + s;
     store_padded(a.seg + (at * W::NP + n0) * a.DP + ch.pad + c0, a.DP, back);
     if (nl == 0) {
@@ -172,13 +230,12 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_local_kernel(const ScanAr
     if (PACKED && blk == 0 && tid == 0) a.cut[s] = cut;
 }
 
-// A thread's gradients of its states of one token: h, a and the state before, 16 elements each.
 template <typename T, int L, bool PACKED>
 __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) {
     using W = Bwd<L>;
-    constexpr int NP = W::NP, NT = W::NT, VROW = W::CB / 8, VSTEP = NT / VROW;
+    constexpr int NP = W::NP, NT = W::NT;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    BwdSmem<L> &sm = *reinterpret_cast<BwdSmem<L> *>(smem_raw);
+    BwdFull<L> &sm = *reinterpret_cast<BwdFull<L> *>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nl = lane % L, cl = lane / L;
     const int nblk = a.gblocks * a.G;
@@ -187,16 +244,25 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
     const Chans<W::CB> ch(a, blk);
     const int c0 = warp * (W::CL * 4) + cl * 4, n0 = nl * 4, nc = ch.count - c0;
     const int t0 = s * a.seglen, t1 = min(a.T, t0 + a.seglen);
-    const int vc = (tid % VROW) * 8, vt = tid / VROW, vn = ch.count - vc;
-    const bool vlive = W::NVEC >= NT || tid < W::NVEC;
+    const int top = t0 + (t1 - 1 - t0) / TT * TT;
+    const int vc = (tid % W::VROW) * 8, vt = tid / W::VROW, vn = ch.count - vc;
+    const int bn = (tid % W::BROW) * 8, bt = tid / W::BROW;
     if (PACKED && blockIdx.x == 0) check_cu(a.cu, a.nseq, a.T, a.err);
 
-    float bias[8], dbias[8];
+    // the saved state before the tile at `base`, into the last group's slot (free once that group is done)
+    const float *saved = a.saved + ((long long)b * ((a.T + SAVE - 1) / SAVE) * NP + n0) * a.DP + ch.pad + c0;
+    auto fetch_state = [&](int base) {
+        if (base >= t0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        bias[i] = (a.bias && i < vn) ? a.bias[ch.first + vc + i] : 0.f;
-        dbias[i] = 0.f;
-    }
+            for (int n = 0; n < 4; ++n)
+                copy16(sm.start[TT / SB - 1][n][tid], saved + ((long long)(base / SAVE) * NP + n) * a.DP);
+        }
+    };
+    fetch_state(top);
+    fetch<L, false, PACKED>(a, sm, ch, b, top, t0, t1, 0);
+    for (int i = tid; i < W::CB; i += NT) sm.bias[i] = (a.bias && i < ch.count) ? a.bias[ch.first + i] : 0.f;
+
+    f2 dbias[4] = {0ull, 0ull, 0ull, 0ull};
     State A2, back, dA;
     load_rows(a, a.A + (long long)(ch.first + c0) * a.N, nc, n0, A2, LOG2E);
     zero(dA);
@@ -214,34 +280,46 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
         skip[i] = (a.skip && own + i < ch.count) ? a.skip[ch.first + own + i] : 0.f;
         dskip[i] = 0.f;
     }
-    const long long chunks = (a.T + SAVE - 1) / SAVE;
+    auto initial = [&](int n, State h) {  // the state that sequence n starts from
+        if (a.state_in)
+            load_rows(a, a.state_in + ((long long)n * a.D + ch.first + c0) * a.N, nc, n0, h);
+        else
+            zero(h);
+    };
+    __syncthreads();
 
-    for (int base = t0 + (t1 - 1 - t0) / TT * TT; base >= t0; base -= TT) {
-        stage<T, L, false>(a, sm, ch, b, base, t1, vc, vt, vn, vlive, bias);
-        if (PACKED)
-            for (int j = tid; j < TT; j += NT) edges(a, base + j, t1, sm.first[j], sm.last[j]);
+    int buf = 0;
+    for (int base = top; base >= t0; base -= TT, buf ^= 1) {
+        copies_wait<0>();
+        stage<T, L, false>(a, sm, ch, base, t1, buf, [&](int j, int c, bool in) {
+            f2 x[4] = {0ull, 0ull, 0ull, 0ull};
+            if (in) widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][3][j][c]), x);
+            put8(&sm.x[j][c], x);
+        });
+#pragma unroll
+        for (int k = 0; k < W::BPT; ++k) {
+            const int j = bt + k * W::BSTEP;
+            if (j < TT) spread<T, W::BW>(sm.raw_bc[buf][1][j] + bn, base + j < t1, sm.b[j][bn]);
+        }
+        fetch<L, false, PACKED>(a, sm, ch, b, base - TT, t0, t1, buf ^ 1);
         __syncthreads();
         // forward over the tile: the state before every group of SB tokens
         {
             State h;
-            load_padded(a.saved + (((long long)b * chunks + base / SAVE) * NP + n0) * a.DP + ch.pad + c0, a.DP, h);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const F2x2 v = lds_f2x2(sm.start[TT / SB - 1][n][tid]);
+                h[n][0] = v.lo, h[n][1] = v.hi;
+            }
             for (int grp = 0; grp < TT / SB; ++grp) {
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    ulonglong2 v;
-                    v.x = h[n][0], v.y = h[n][1];
-                    *reinterpret_cast<ulonglong2 *>(sm.start[grp][n][tid]) = v;
-                }
+                for (int n = 0; n < 4; ++n)
+                    *reinterpret_cast<ulonglong2 *>(sm.start[grp][n][tid]) = make_ulonglong2(h[n][0], h[n][1]);
                 if (grp == TT / SB - 1) break;
 #pragma unroll
                 for (int i = 0; i < SB; ++i) {
                     const int j = grp * SB + i;
-                    if (PACKED && sm.first[j] >= 0) {
-                        if (a.state_in)
-                            load_rows(a, a.state_in + ((long long)sm.first[j] * a.D + ch.first + c0) * a.N, nc, n0, h);
-                        else
-                            zero(h);
-                    }
+                    if (PACKED && sm.first[buf][j] >= 0) initial(sm.first[buf][j], h);
                     const F2x2 d = lds_f2x2(&sm.delta[j][c0]), x = lds_f2x2(&sm.x[j][c0]);
                     const f2 u_lo = mul2(d.lo, x.lo), u_hi = mul2(d.hi, x.hi);
 #pragma unroll
@@ -249,10 +327,10 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
                         const F2x2 bb = lds_f2x2(sm.b[j][n0 + n]);
 #pragma unroll
                         for (int m = 0; m < 2; ++m) {
-                            const f2 bn = m ? bb.hi : bb.lo;
+                            const f2 bm = m ? bb.hi : bb.lo;
                             f2 *hn = h[n + m];
-                            hn[0] = fma2(exp2x2(mul2(A2[n + m][0], d.lo)), hn[0], mul2(u_lo, bn));
-                            hn[1] = fma2(exp2x2(mul2(A2[n + m][1], d.hi)), hn[1], mul2(u_hi, bn));
+                            hn[0] = fma2(ex2x2(mul2(A2[n + m][0], d.lo)), hn[0], mul2(u_lo, bm));
+                            hn[1] = fma2(ex2x2(mul2(A2[n + m][1], d.hi)), hn[1], mul2(u_hi, bm));
                         }
                     }
                 }
@@ -275,12 +353,7 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
                     from[n][0] = i ? hs[i ? i - 1 : 0][n][0] : h0[n][0];
                     from[n][1] = i ? hs[i ? i - 1 : 0][n][1] : h0[n][1];
                 }
-                if (PACKED && sm.first[j] >= 0) {
-                    if (a.state_in)
-                        load_rows(a, a.state_in + ((long long)sm.first[j] * a.D + ch.first + c0) * a.N, nc, n0, from);
-                    else
-                        zero(from);
-                }
+                if (PACKED && sm.first[buf][j] >= 0) initial(sm.first[buf][j], from);
                 const F2x2 d = lds_f2x2(&sm.delta[j][c0]), x = lds_f2x2(&sm.x[j][c0]);
                 const f2 u_lo = mul2(d.lo, x.lo), u_hi = mul2(d.hi, x.hi);
                 f2 y_lo = 0ull, y_hi = 0ull;
@@ -289,16 +362,20 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
                     const F2x2 bb = lds_f2x2(sm.b[j][n0 + n]), cc = lds_f2x2(sm.c[j][n0 + n]);
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
-                        const f2 bn = m ? bb.hi : bb.lo, cn = m ? cc.hi : cc.lo;
-                        dec[i][n + m][0] = exp2x2(mul2(A2[n + m][0], d.lo));
-                        dec[i][n + m][1] = exp2x2(mul2(A2[n + m][1], d.hi));
-                        hs[i][n + m][0] = fma2(dec[i][n + m][0], from[n + m][0], mul2(u_lo, bn));
-                        hs[i][n + m][1] = fma2(dec[i][n + m][1], from[n + m][1], mul2(u_hi, bn));
-                        y_lo = fma2(hs[i][n + m][0], cn, y_lo);
-                        y_hi = fma2(hs[i][n + m][1], cn, y_hi);
+                        const f2 bm = m ? bb.hi : bb.lo, cm = m ? cc.hi : cc.lo;
+                        dec[i][n + m][0] = ex2x2(mul2(A2[n + m][0], d.lo));
+                        dec[i][n + m][1] = ex2x2(mul2(A2[n + m][1], d.hi));
+                        hs[i][n + m][0] = fma2(dec[i][n + m][0], from[n + m][0], mul2(u_lo, bm));
+                        hs[i][n + m][1] = fma2(dec[i][n + m][1], from[n + m][1], mul2(u_hi, bm));
+                        y_lo = fma2(hs[i][n + m][0], cm, y_lo);
+                        y_hi = fma2(hs[i][n + m][1], cm, y_hi);
                     }
                 }
                 if (a.dz) LaneSum<L>::run(y_lo, y_hi, nl, yp[i]);
+            }
+            if (grp == TT / SB - 1) {  // (its slot has been read)
+                fetch_state(base - TT);
+                copies_commit();
             }
 #pragma unroll
             for (int i = SB - 1; i >= 0; --i) {
@@ -310,15 +387,11 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
                     from[n][1] = i ? hs[i ? i - 1 : 0][n][1] : h0[n][1];
                 }
                 if (PACKED) {
-                    if (sm.first[j] >= 0) {
-                        if (a.state_in)
-                            load_rows(a, a.state_in + ((long long)sm.first[j] * a.D + ch.first + c0) * a.N, nc, n0, from);
-                        else
-                            zero(from);
-                    }
-                    if (sm.last[j] >= 0) {
+                    if (sm.first[buf][j] >= 0) initial(sm.first[buf][j], from);
+                    const int n = sm.last[buf][j];
+                    if (n >= 0) {
                         if (a.dstate_out)
-                            load_rows(a, a.dstate_out + ((long long)sm.last[j] * a.D + ch.first + c0) * a.N, nc, n0, back);
+                            load_rows(a, a.dstate_out + ((long long)n * a.D + ch.first + c0) * a.N, nc, n0, back);
                         else
                             zero(back);
                     }
@@ -333,12 +406,12 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
                         const int k = n + m;
-                        const f2 bn = m ? bb.hi : bb.lo, cn = m ? cc.hi : cc.lo;
-                        const f2 g_lo = fma2(gy.lo, cn, back[k][0]), g_hi = fma2(gy.hi, cn, back[k][1]);
+                        const f2 bm = m ? bb.hi : bb.lo, cm = m ? cc.hi : cc.lo;
+                        const f2 g_lo = fma2(gy.lo, cm, back[k][0]), g_hi = fma2(gy.hi, cm, back[k][1]);
                         dc[k] = sum2(fma2(gy.hi, hs[i][k][1], mul2(gy.lo, hs[i][k][0])));
                         db[k] = sum2(fma2(g_hi, u_hi, mul2(g_lo, u_lo)));
-                        s_lo = fma2(g_lo, bn, s_lo);
-                        s_hi = fma2(g_hi, bn, s_hi);
+                        s_lo = fma2(g_lo, bm, s_lo);
+                        s_hi = fma2(g_hi, bm, s_hi);
                         back[k][0] = mul2(g_lo, dec[i][k][0]);
                         back[k][1] = mul2(g_hi, dec[i][k][1]);
                         const f2 p_lo = mul2(back[k][0], from[k][0]), p_hi = mul2(back[k][1], from[k][1]);
@@ -349,7 +422,7 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
                     }
                 }
                 // (odd channel lanes swap the two halves of their row, so that neighbouring rows use other banks)
-                float *r = sm.red[warp][i][cl];
+                float *r = sm.red[warp][i & 1][cl];
                 *reinterpret_cast<float4 *>(r + ((cl & 1) ? NP : 0) + n0) = make_float4(db[0], db[1], db[2], db[3]);
                 *reinterpret_cast<float4 *>(r + ((cl & 1) ? 0 : NP) + n0) = make_float4(dc[0], dc[1], dc[2], dc[3]);
                 float sv[R], qv[R];
@@ -366,85 +439,91 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
                         dskip[e] = fmaf(gv, xv, dskip[e]);
                     }
                 }
-                if (PACKED && sm.first[j] >= 0 && a.dstate_in)
-                    store_rows(a, a.dstate_in + ((long long)sm.first[j] * a.D + ch.first + c0) * a.N, nc, n0, back);
-            }
-            __syncwarp();
-            // the warp's sums of dB and dC over its channel lanes: 4 columns of one token a lane
+                if (PACKED && sm.first[buf][j] >= 0 && a.dstate_in)
+                    store_rows(a, a.dstate_in + ((long long)sm.first[buf][j] * a.D + ch.first + c0) * a.N, nc, n0, back);
+                if (i & 1) continue;
+                // the warp's sums of dB and dC over its channel lanes, two tokens at a time: 4 columns of one a lane
+                __syncwarp();
 #pragma unroll
-            for (int o = lane; o < SB * 2 * NP / 4; o += 32) {
-                const int i = o / (2 * NP / 4), col = (o % (2 * NP / 4)) * 4;
-                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int o = lane; o < 2 * 2 * NP / 4; o += 32) {
+                    const int e = o / (2 * NP / 4), col = (o % (2 * NP / 4)) * 4;
+                    f2 v_lo = 0ull, v_hi = 0ull;
 #pragma unroll
-                for (int k = 0; k < W::CL; ++k) {
-                    const float4 e = *reinterpret_cast<const float4 *>(&sm.red[warp][i][k][(k & 1) ? (col + NP) % (2 * NP) : col]);
-                    v.x += e.x, v.y += e.y, v.z += e.z, v.w += e.w;
+                    for (int k = 0; k < W::CL; ++k) {
+                        const F2x2 v = lds_f2x2(&sm.red[warp][e][k][(k & 1) ? (col + NP) % (2 * NP) : col]);
+                        v_lo = add2(v_lo, v.lo), v_hi = add2(v_hi, v.hi);
+                    }
+                    *reinterpret_cast<ulonglong2 *>(&sm.bc[warp][j + e][col]) = make_ulonglong2(v_lo, v_hi);
                 }
-                *reinterpret_cast<float4 *>(&sm.bc[warp][grp * SB + i][col]) = v;
+                __syncwarp();
             }
-            __syncwarp();
         }
         __syncthreads();
         // the tile's outputs
 #pragma unroll
         for (int k = 0; k < W::VPT; ++k) {
-            const int j = vt + k * VSTEP, t = base + j;
-            if (!vlive || t >= t1 || vn <= 0) continue;
-            const long long row = (long long)b * a.T + t;
-            const int c = ch.first + vc;
-            const long long at = row * a.D + c;
-            float v[8], r[8], o[8];
+            const int j = vt + k * W::VSTEP, t = base + j;
+            if (j >= TT || t >= t1 || vn <= 0) continue;
+            const long long at = ((long long)b * a.T + t) * a.D + ch.first + vc;
+            f2 v[4], r[4], o[4];
             get8(&sm.x[j][vc], v);
             store8(static_cast<uint16_t *>(a.dx) + at, narrow8<T>(v), vn, a.vec);
             get8(&sm.delta[j][vc], v);
             if (a.softplus) {
-                widen8<T>(load8(static_cast<const uint16_t *>(a.dt) + row * a.dt_ld + c, vn, a.vec), r);
+                widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][0][j][vc]), r);
+                get8(&sm.bias[vc], o);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] *= sigmoid(r[i] + bias[i]);
+                for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], sigmoid2(add2(r[i], o[i])));
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dbias[i] += v[i];
+            for (int i = 0; i < 4; ++i) dbias[i] = add2(dbias[i], v[i]);
             store8(static_cast<uint16_t *>(a.ddt) + at, narrow8<T>(v), vn, a.vec);
             if (a.dz) {
                 get8(&sm.gy[j][vc], v);
-                widen8<T>(load8(static_cast<const uint16_t *>(a.z) + row * a.z_ld + c, vn, a.vec), r);
-                widen8<T>(load8(static_cast<const uint16_t *>(a.dy) + at, vn, a.vec), o);
+                widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][1][j][vc]), o);
+                widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][2][j][vc]), r);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float sg = sigmoid(r[i]);
-                    v[i] = o[i] * v[i] * sg * fmaf(r[i], 1.f - sg, 1.f);
+                for (int i = 0; i < 4; ++i) {
+                    const f2 sg = sigmoid2(r[i]);  // yp dy sig (1 + z (1 - sig))
+                    v[i] = mul2(mul2(v[i], o[i]), mul2(sg, fma2(r[i], fma2(sg, both(-1.f), both(1.f)), both(1.f))));
                 }
                 store8(static_cast<uint16_t *>(a.dz) + at, narrow8<T>(v), vn, a.vec);
             }
         }
-        for (int i = tid; i < TT * 2 * NP; i += NT) {
-            const int j = i / (2 * NP), col = i % (2 * NP), t = base + j;
+        for (int i = tid; i < TT * 2 * NP / 4; i += NT) {
+            const int j = i / (2 * NP / 4), col = (i % (2 * NP / 4)) * 4, t = base + j;
             if (t >= t1) continue;
-            float v = 0.f;
+            f2 v_lo = 0ull, v_hi = 0ull;
 #pragma unroll
-            for (int w = 0; w < W::NW; ++w) v += sm.bc[w][j][col];
+            for (int w = 0; w < W::NW; ++w) {
+                const F2x2 v = lds_f2x2(&sm.bc[w][j][col]);
+                v_lo = add2(v_lo, v.lo), v_hi = add2(v_hi, v.hi);
+            }
             const int cb = blk - ch.g * a.gblocks;
-            a.dbc_part[(((long long)cb * a.B * a.T + (long long)b * a.T + t) * a.G + ch.g) * (2 * NP) + col] = v;
+            *reinterpret_cast<ulonglong2 *>(
+                a.dbc_part + (((long long)cb * a.B * a.T + (long long)b * a.T + t) * a.G + ch.g) * (2 * NP) + col) = make_ulonglong2(v_lo, v_hi);
         }
-        __syncthreads();
+        // (what is staged next is each thread's own, or was last read before the barrier above, but for bc)
     }
     const long long part = (long long)b * a.nseg + s;
     if (!PACKED && s == 0 && a.dstate_in)
         store_rows(a, a.dstate_in + ((long long)b * a.D + ch.first + c0) * a.N, nc, n0, back);
-    store_rows(a, a.dA_part + (part * a.D + ch.first + c0) * a.N, nc, n0, dA);
-    if (a.dD_part && LaneSum<L>::keeper(nl))
+    float *param = a.param_part + part * a.param_ld;
+    store_rows(a, param + (long long)(ch.first + c0) * a.N, nc, n0, dA);
+    if (a.dD_at >= 0 && LaneSum<L>::keeper(nl))
 #pragma unroll
         for (int e = 0; e < R; ++e)
-            if (own + e < ch.count) a.dD_part[part * a.D + ch.first + own + e] = dskip[e];
-    if (a.dbias_part) {
+            if (own + e < ch.count) param[a.dD_at + ch.first + own + e] = dskip[e];
+    if (a.dbias_at >= 0) {
         // threads of one vector column, added in order
-        float *buf = &sm.delta[0][0];                    // NT x 8 floats: NT <= TT CB / 8
-        if (vlive) put8(buf + tid * 8, dbias);
+        __syncthreads();
+        float *buf8 = &sm.delta[0][0];                   // 8 floats of each thread that holds vectors
+        if (vt < TT) put8(buf8 + tid * 8, dbias);
         __syncthreads();
         for (int c = tid; c < W::CB; c += NT) {
             float v = 0.f;
-            for (int k = c / 8; k < (W::NVEC < NT ? W::NVEC : NT); k += VROW) v += buf[k * 8 + c % 8];
-            if (c < ch.count) a.dbias_part[part * a.D + ch.first + c] = v;
+            for (int k = c / 8; k < (W::NVEC < NT ? W::NVEC : NT); k += W::VROW) v += buf8[k * 8 + c % 8];
+            if (c < ch.count) param[a.dbias_at + ch.first + c] = v;
         }
     }
 }
@@ -480,10 +559,10 @@ cudaError_t launch_smem(K k, long long blocks, int threads, size_t smem, cudaStr
 template <typename T, int L>
 cudaError_t launch_l(const ScanArgs &a, bool full, cudaStream_t s) {
     const long long blocks = (long long)a.gblocks * a.G * (full ? a.nseg : a.nseg - 1) * a.B;
-    const size_t smem = sizeof(BwdSmem<L>);
     if (full)
-        return a.cu ? launch_smem(scan_bwd_kernel<T, L, true>, blocks, Bwd<L>::NT, smem, s, a)
-                    : launch_smem(scan_bwd_kernel<T, L, false>, blocks, Bwd<L>::NT, smem, s, a);
+        return a.cu ? launch_smem(scan_bwd_kernel<T, L, true>, blocks, Bwd<L>::NT, sizeof(BwdFull<L>), s, a)
+                    : launch_smem(scan_bwd_kernel<T, L, false>, blocks, Bwd<L>::NT, sizeof(BwdFull<L>), s, a);
+    const size_t smem = sizeof(BwdSmem<L, true>);
     return a.cu ? launch_smem(scan_bwd_local_kernel<T, L, true>, blocks, Bwd<L>::NT, smem, s, a)
                 : launch_smem(scan_bwd_local_kernel<T, L, false>, blocks, Bwd<L>::NT, smem, s, a);
 }

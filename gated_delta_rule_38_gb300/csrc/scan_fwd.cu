@@ -25,26 +25,32 @@ struct Fwd {
     static constexpr int TT = L >= 4 ? 16 : 4 * L;      // tokens a tile
     static constexpr int NVEC = TT * CB / 8;            // 8-channel vectors of a tile
     static constexpr int VPT = NVEC > 128 ? NVEC / 128 : 1;
-    static constexpr int BPT = TT * NP > 128 ? TT * NP / 128 : 1;
+    static constexpr int BVEC = TT * NP / 8;            // 8-state vectors of a tile's B
+    static constexpr int BPT = BVEC > 128 ? BVEC / 128 : 1;
 };
 
-template <int L>
+// The raw tiles (two of each: the next one is on its way while one is worked on) are private to the threads that copy
+// them; so are, but for the recurrence in between, the staged elements of a vector.
+template <int L, bool FULL>
 struct FwdSmem {
-    float delta[Fwd<L>::TT][Fwd<L>::CB];
-    float u[Fwd<L>::TT][Fwd<L>::CB];                    // delta x
-    float y[Fwd<L>::TT][Fwd<L>::CB];
-    float b[Fwd<L>::TT][Fwd<L>::NP][2];
-    float c[Fwd<L>::TT][Fwd<L>::NP][2];
-    int first[Fwd<L>::TT], last[Fwd<L>::TT];
+    using F = Fwd<L>;
+    uint16_t raw[2][FULL ? 3 : 2][F::TT][F::CB];        // dt, x, z
+    uint16_t raw_bc[2][FULL ? 2 : 1][F::TT][F::NP];
+    float delta[F::TT][F::CB];
+    float u[F::TT][F::CB];                              // delta x; then the output of the recurrence
+    float b[F::TT][F::NP][2];
+    float c[FULL ? F::TT : 1][F::NP][2];
+    float bias[F::CB], skip[F::CB];
+    int first[2][F::TT], last[2][F::TT];
 };
 
 // FULL: the outputs (second pass, or the only one).  Otherwise the first pass over segments.
 template <typename T, int L, bool FULL, bool PACKED>
-__global__ void __launch_bounds__(128) scan_fwd_kernel(const ScanArgs a) {
+__global__ void __launch_bounds__(128, FULL ? 4 : 5) scan_fwd_kernel(const ScanArgs a) {
     using F = Fwd<L>;
     constexpr int CB = F::CB, TT = F::TT, NP = F::NP;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    FwdSmem<L> &sm = *reinterpret_cast<FwdSmem<L> *>(smem_raw);
+    FwdSmem<L, FULL> &sm = *reinterpret_cast<FwdSmem<L, FULL> *>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nl = lane % L, cl = lane / L;
     const int segs = FULL ? a.nseg : a.nseg - 1;        // (the last segment's end state joins nothing)
@@ -57,6 +63,56 @@ __global__ void __launch_bounds__(128) scan_fwd_kernel(const ScanArgs a) {
     const int t0 = s * a.seglen, t1 = min(a.T, t0 + a.seglen);
     if (PACKED && FULL && blockIdx.x == 0) check_cu(a.cu, a.nseq, a.T, a.err);
 
+    // this thread's vectors of a tile: token vt + k VSTEP, channels vc ..; and of B and C: token bt + k BSTEP, states bn ..
+    constexpr int VROW = CB / 8, VSTEP = 128 / VROW, BROW = NP >= 8 ? NP / 8 : 1, BSTEP = 128 / BROW;
+    constexpr int BW = NP >= 8 ? 8 : 4;                 // states of such a vector
+    const int vc = (tid % VROW) * 8, vt = tid / VROW, vn = ch.count - vc;
+    const int bn = (tid % BROW) * 8, bt = tid / BROW;
+    const bool vlive = F::NVEC >= 128 || tid < F::NVEC;
+    const long long row0 = (long long)b * a.T;
+    for (int i = tid; i < CB; i += 128) {
+        sm.bias[i] = (a.bias && i < ch.count) ? a.bias[ch.first + i] : 0.f;
+        sm.skip[i] = (a.skip && i < ch.count) ? a.skip[ch.first + i] : 0.f;
+    }
+    auto fetch = [&](int base, int buf) {
+        if (base < t1) {
+#pragma unroll
+            for (int k = 0; k < F::VPT; ++k) {
+                const int j = vt + k * VSTEP, t = base + j;
+                if (vlive && t < t1 && vn > 0) {
+                    const long long row = row0 + t;
+                    const int c = ch.first + vc;
+                    copy8(&sm.raw[buf][0][j][vc], static_cast<const uint16_t *>(a.dt) + row * a.dt_ld + c, vn, a.vec);
+                    copy8(&sm.raw[buf][1][j][vc], static_cast<const uint16_t *>(a.x) + row * a.x_ld + c, vn, a.vec);
+                    if (FULL && a.z)
+                        copy8(&sm.raw[buf][FULL ? 2 : 0][j][vc], static_cast<const uint16_t *>(a.z) + row * a.z_ld + c, vn, a.vec);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < F::BPT; ++k) {
+                const int j = bt + k * BSTEP, t = base + j;
+                if (j < TT && t < t1) {
+                    const long long row = row0 + t;
+                    const int at = ch.g * a.N + bn;
+                    const uint16_t *pb = static_cast<const uint16_t *>(a.Bm) + row * a.b_ld + at;
+                    const uint16_t *pc = static_cast<const uint16_t *>(a.Cm) + row * a.c_ld + at;
+                    if constexpr (BW == 8) {
+                        copy8(&sm.raw_bc[buf][0][j][bn], pb, a.N - bn, a.vec_bc);
+                        if (FULL) copy8(&sm.raw_bc[buf][FULL ? 1 : 0][j][bn], pc, a.N - bn, a.vec_bc);
+                    } else {
+                        for (int n = 0; n < BW; ++n) {
+                            sm.raw_bc[buf][0][j][n] = n < a.N ? pb[n] : (uint16_t)0;
+                            if (FULL) sm.raw_bc[buf][FULL ? 1 : 0][j][n] = n < a.N ? pc[n] : (uint16_t)0;
+                        }
+                    }
+                }
+            }
+            if (PACKED && tid < TT) edges(a, base + tid, t1, sm.first[buf][tid], sm.last[buf][tid]);
+        }
+        copies_commit();
+    };
+    fetch(t0, 0);
+
     State A2, h;
     load_rows(a, a.A + (long long)(ch.first + c0) * a.N, nc, n0, A2, LOG2E);
     const long long segpos = ((long long)b * a.nseg + s) * NP + n0;
@@ -68,91 +124,61 @@ __global__ void __launch_bounds__(128) scan_fwd_kernel(const ScanArgs a) {
         zero(h);
     f2 sum_lo = 0ull, sum_hi = 0ull;
     bool cut = false;
+    __syncthreads();
 
-    // this thread's vectors of a tile: token vt + k VSTEP, channels vc ..
-    constexpr int VROW = CB / 8, VSTEP = 128 / VROW > 0 ? 128 / VROW : 1;
-    const int vc = (tid % VROW) * 8, vt = tid / VROW;
-    const bool vlive = F::NVEC >= 128 || tid < F::NVEC;
-    const int vn = ch.count - vc;
-    float bias[8], skip[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        bias[i] = (a.bias && i < vn) ? a.bias[ch.first + vc + i] : 0.f;
-        skip[i] = (FULL && a.skip && i < vn) ? a.skip[ch.first + vc + i] : 0.f;
-    }
-    uint4 rx[F::VPT], rd[F::VPT], rz[F::VPT];
-    uint16_t rb[F::BPT], rc[F::BPT];
-    auto fetch = [&](int base) {
-        if (base >= t1) return;
-#pragma unroll
-        for (int k = 0; k < F::VPT; ++k) {
-            const int t = base + vt + k * VSTEP;
-            rx[k] = rd[k] = rz[k] = make_uint4(0, 0, 0, 0);
-            if (vlive && t < t1 && vn > 0) {
-                const long long row = (long long)b * a.T + t;
-                const int c = ch.first + vc;
-                rx[k] = load8(static_cast<const uint16_t *>(a.x) + row * a.x_ld + c, vn, a.vec);
-                rd[k] = load8(static_cast<const uint16_t *>(a.dt) + row * a.dt_ld + c, vn, a.vec);
-                if (FULL && a.z) rz[k] = load8(static_cast<const uint16_t *>(a.z) + row * a.z_ld + c, vn, a.vec);
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < F::BPT; ++k) {
-            const int i = tid + k * 128, t = base + i / NP, n = i % NP;
-            rb[k] = rc[k] = 0;
-            if (i < TT * NP && t < t1 && n < a.N) {
-                const long long row = (long long)b * a.T + t;
-                rb[k] = static_cast<const uint16_t *>(a.Bm)[row * a.b_ld + ch.g * a.N + n];
-                if (FULL) rc[k] = static_cast<const uint16_t *>(a.Cm)[row * a.c_ld + ch.g * a.N + n];
-            }
-        }
-    };
-    auto to_f = [](uint16_t v) { return Elt<T>::to_f(*reinterpret_cast<const T *>(&v)); };
-
-    fetch(t0);
-    for (int base = t0; base < t1; base += TT) {
+    int buf = 0;
+    for (int base = t0; base < t1; base += TT, buf ^= 1) {
+        fetch(base + TT, buf ^ 1);
+        copies_wait<1>();
         // stage the tile
-        uint4 x_now[F::VPT], z_now[F::VPT];
 #pragma unroll
         for (int k = 0; k < F::VPT; ++k) {
-            x_now[k] = rx[k], z_now[k] = rz[k];
             if (!vlive) continue;
-            float x[8], d[8], u[8];
-            widen8<T>(rx[k], x);
-            widen8<T>(rd[k], d);
-            const bool in = base + vt + k * VSTEP < t1;
+            const int j = vt + k * VSTEP;
+            f2 x[4], d[4], bias[4];
+            if (base + j < t1 && vn > 0) {
+                widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][0][j][vc]), d);
+                widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][1][j][vc]), x);
+                get8(&sm.bias[vc], bias);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                d[i] += bias[i];
-                if (a.softplus) d[i] = softplus(d[i]);
-                d[i] = in && i < vn ? d[i] : 0.f;  // past the end: a step of zero, which changes nothing
-                u[i] = d[i] * x[i];
+                for (int i = 0; i < 4; ++i) {
+                    d[i] = add2(d[i], bias[i]);
+                    if (a.softplus) d[i] = softplus2(d[i]);
+                    x[i] = mul2(d[i], x[i]);
+                }
+            } else {  // past the end: a step of zero, which changes nothing
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[i] = x[i] = 0ull;
             }
-            put8(&sm.delta[vt + k * VSTEP][vc], d);
-            put8(&sm.u[vt + k * VSTEP][vc], u);
+            put8(&sm.delta[j][vc], d);
+            put8(&sm.u[j][vc], x);
         }
 #pragma unroll
         for (int k = 0; k < F::BPT; ++k) {
-            const int i = tid + k * 128;
-            if (i < TT * NP) {
-                const float vb = to_f(rb[k]);
-                *reinterpret_cast<float2 *>(sm.b[i / NP][i % NP]) = make_float2(vb, vb);
-                if (FULL) {
-                    const float v = to_f(rc[k]);
-                    *reinterpret_cast<float2 *>(sm.c[i / NP][i % NP]) = make_float2(v, v);
+            const int j = bt + k * BSTEP;
+            if (j < TT) {
+                const bool in = base + j < t1;
+#pragma unroll
+                for (int m = 0; m < (FULL ? 2 : 1); ++m) {
+                    const uint16_t *r = sm.raw_bc[buf][m][j] + bn;
+                    float *o = m ? sm.c[FULL ? j : 0][bn] : sm.b[j][bn];
+#pragma unroll
+                    for (int n = 0; n < BW; n += 2) {
+                        float v0, v1;
+                        unpack2(widen2<T>(in ? *reinterpret_cast<const uint32_t *>(r + n) : 0u), v0, v1);
+                        *reinterpret_cast<float4 *>(o + 2 * n) = make_float4(v0, v0, v1, v1);
+                    }
                 }
             }
         }
-        if (PACKED && tid < TT) edges(a, base + tid, t1, sm.first[tid], sm.last[tid]);
         __syncthreads();
-        fetch(base + TT);
         if (FULL && a.saved && base % SAVE == 0)
             store_padded(a.saved + (((long long)b * ((a.T + SAVE - 1) / SAVE) + base / SAVE) * NP + n0) * a.DP + ch.pad + c0,
                          a.DP, h);
 #pragma unroll 4
         for (int j = 0; j < TT; ++j) {
             if (PACKED) {
-                const int n = sm.first[j];
+                const int n = sm.first[buf][j];
                 if (n >= 0) {
                     cut = true;
                     if (a.state_in)
@@ -166,31 +192,32 @@ __global__ void __launch_bounds__(128) scan_fwd_kernel(const ScanArgs a) {
 #pragma unroll
             for (int n = 0; n < 4; n += 2) {
                 const F2x2 bb = lds_f2x2(sm.b[j][n0 + n]);
-                const F2x2 cc = FULL ? lds_f2x2(sm.c[j][n0 + n]) : F2x2{0ull, 0ull};
+                const F2x2 cc = FULL ? lds_f2x2(sm.c[FULL ? j : 0][n0 + n]) : F2x2{0ull, 0ull};
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    const f2 bn = m ? bb.hi : bb.lo, cn = m ? cc.hi : cc.lo;
+                    const f2 bm = m ? bb.hi : bb.lo, cm = m ? cc.hi : cc.lo;
                     f2 *hn = h[n + m];
-                    hn[0] = fma2(exp2x2(mul2(A2[n + m][0], d.lo)), hn[0], mul2(u.lo, bn));
-                    hn[1] = fma2(exp2x2(mul2(A2[n + m][1], d.hi)), hn[1], mul2(u.hi, bn));
+                    hn[0] = fma2(ex2x2(mul2(A2[n + m][0], d.lo)), hn[0], mul2(u.lo, bm));
+                    hn[1] = fma2(ex2x2(mul2(A2[n + m][1], d.hi)), hn[1], mul2(u.hi, bm));
                     if (FULL) {
-                        y_lo = fma2(hn[0], cn, y_lo);
-                        y_hi = fma2(hn[1], cn, y_hi);
+                        y_lo = fma2(hn[0], cm, y_lo);
+                        y_hi = fma2(hn[1], cm, y_hi);
                     }
                 }
             }
             if (FULL) {
                 float y[LaneSum<L>::R];
                 LaneSum<L>::run(y_lo, y_hi, nl, y);
+                __syncwarp();  // (u of this token has been read by all lanes of its channels)
                 if (LaneSum<L>::keeper(nl))
 #pragma unroll
-                    for (int i = 0; i < LaneSum<L>::R; ++i) sm.y[j][c0 + LaneSum<L>::at(nl) + i] = y[i];
+                    for (int i = 0; i < LaneSum<L>::R; ++i) sm.u[j][c0 + LaneSum<L>::at(nl) + i] = y[i];
             } else {
                 sum_lo = add2(sum_lo, d.lo);
                 sum_hi = add2(sum_hi, d.hi);
             }
             if (PACKED && FULL) {
-                const int n = sm.last[j];
+                const int n = sm.last[buf][j];
                 if (n >= 0 && a.state_out)
                     store_rows(a, a.state_out + ((long long)n * a.D + ch.first + c0) * a.N, nc, n0, h);
             }
@@ -199,21 +226,24 @@ __global__ void __launch_bounds__(128) scan_fwd_kernel(const ScanArgs a) {
         if (FULL) {
 #pragma unroll
             for (int k = 0; k < F::VPT; ++k) {
-                const int t = base + vt + k * VSTEP;
+                const int j = vt + k * VSTEP, t = base + j;
                 if (!vlive || t >= t1 || vn <= 0) continue;
-                float y[8], x[8], z[8];
-                get8(&sm.y[vt + k * VSTEP][vc], y);
-                widen8<T>(x_now[k], x);
-                widen8<T>(z_now[k], z);
+                f2 y[4], x[4], z[4], skip[4];
+                get8(&sm.u[j][vc], y);
+                widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][1][j][vc]), x);
+                get8(&sm.skip[vc], skip);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    y[i] = fmaf(skip[i], x[i], y[i]);
-                    if (a.z) y[i] *= z[i] * sigmoid(z[i]);
+                for (int i = 0; i < 4; ++i) y[i] = fma2(skip[i], x[i], y[i]);
+                if (a.z) {
+                    widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][FULL ? 2 : 0][j][vc]), z);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], mul2(z[i], sigmoid2(z[i])));
                 }
-                store8(static_cast<uint16_t *>(a.y) + ((long long)b * a.T + t) * a.D + ch.first + vc, narrow8<T>(y), vn, a.vec);
+                store8(static_cast<uint16_t *>(a.y) + (row0 + t) * a.D + ch.first + vc, narrow8<T>(y), vn, a.vec);
             }
         }
     }
+    copies_wait<0>();
     if (FULL) {
         if (!PACKED && a.state_out && s == a.nseg - 1)
             store_rows(a, a.state_out + ((long long)b * a.D + ch.first + c0) * a.N, nc, n0, h);
@@ -261,7 +291,7 @@ cudaError_t launch_one(const ScanArgs &a, cudaStream_t s) {
     const int segs = FULL ? a.nseg : a.nseg - 1;
     const long long blocks = (long long)a.gblocks * a.G * segs * a.B;
     auto k = scan_fwd_kernel<T, L, FULL, PACKED>;
-    const size_t smem = sizeof(FwdSmem<L>);
+    const size_t smem = sizeof(FwdSmem<L, FULL>);
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
