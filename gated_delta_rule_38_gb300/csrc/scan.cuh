@@ -3,8 +3,10 @@
 //
 // Lane layout.  Every thread owns 4 channels x 4 states (in registers, fp32), L lanes side by side hold one channel's
 // N <= 4 L states (padded with states whose B and C are zero), and the 32 / L lane groups of a warp take consecutive
-// channels.  Pairs of channels go through the two-element instructions: a channel's step delta and input are then
-// natural pairs, and B and C are staged twice (B_n, B_n) so that they are pairs too.
+// channels.  Pairs of channels go through the two-element instructions.  Shared memory gives 128 bytes a clock to the lanes
+// together, however many of them read the same address, so what a lane reads a token is kept small: 16 bytes of delta
+// and of the input, and 8 bytes of B and of C in their own 16-bit type (with B and C staged as duplicated fp32 pairs
+// the forward's 41 wavefronts a warp and token took 72 % of its time).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -51,6 +53,17 @@ struct F2x2 {
 __device__ __forceinline__ F2x2 lds_f2x2(const float *p) {
     const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(p);
     return F2x2{v.x, v.y};
+}
+
+// Four 16-bit elements (a thread's states of B or C), each as the pair (v, v).
+template <typename T>
+__device__ __forceinline__ void lds_dup4(const uint16_t *p, f2 *o) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    float v[4];
+    unpack2(widen2<T>(u.x), v[0], v[1]);
+    unpack2(widen2<T>(u.y), v[2], v[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = pack2(v[i], v[i]);
 }
 
 // ---------------------------------------------------------------- pairs of scalars

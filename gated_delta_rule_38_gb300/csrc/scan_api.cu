@@ -49,16 +49,17 @@ Cover cover_of(const gdr_scan_problem *p, bool bwd) {
     c.gpad = (Dg + pad - 1) / pad * pad;
     c.gblocks = (Dg + CB - 1) / CB;
     c.DP = c.gpad * p->G;
-    // Segments.  Splitting costs a state-only first pass (about 0.7 of a full one), so the token axis is cut only when
-    // one block a channel block would leave the chip idle, and into the number of segments with the least estimated
-    // time: blocks on the fullest SM (at least the few that it takes to hide their latencies) times the tokens of one,
-    // with 24 tokens' worth of start-up.
-    const long long blocks = (long long)c.gblocks * p->G * p->B, knee = bwd ? 2 : 4;
-    long long want = 1, best = 0;
-    for (long long n = 1; n == 1 || (n <= 64 && n * 64 <= p->T); ++n) {
-        long long q = (blocks * n + kSMs - 1) / kSMs;
-        q = q > knee ? (bwd ? (q + knee - 1) / knee * knee : q) : knee;
-        const long long cost = q * ((p->T + n - 1) / n + 24) * (n > 1 ? 17 : 10);
+    // Segments.  Splitting costs a state-only first pass (about 0.7 of a full one) and a join, so the token axis is cut
+    // only when one block a channel block would leave the chip idle, and into the number of segments with the least
+    // estimated time: rounds of resident blocks (half a round lost at the end) times the tokens of one, 16 tokens'
+    // worth of start-up each, and 0.4 tokens' worth of join a segment.  (2 x 4096 x 4096, 64 blocks: both passes take
+    // 522 us with 3 segments, 317 with 9, 284 with 28 and 276 with 64, and the join 8, 8, 14 and 26.)
+    const double blocks = (double)c.gblocks * p->G * p->B, slots = (double)kSMs * (bwd ? 2 : 5);
+    long long want = 1;
+    double best = 0;
+    for (long long n = 1; n == 1 || (n <= 256 && n * 64 <= p->T); ++n) {
+        const double rounds = blocks * n / slots + (n > 1 ? 0.5 : 0.0);
+        const double cost = (rounds > 1 ? rounds : 1.0) * ((double)p->T / n + 16) * (n > 1 ? 1.7 : 1.0) + 0.4 * (double)(n - 1);
         if (best == 0 || cost < best) best = cost, want = n;
     }
     c.seglen = (int)(((p->T + want - 1) / want + SAVE - 1) / SAVE * SAVE);

@@ -47,7 +47,6 @@ struct BwdSmem {
     uint16_t raw_bc[2][LOCAL ? 1 : 2][TT][W::NP];        // C, B
     float delta[TT][W::CB];                              // then the gradient of delta
     float gy[TT][W::CB];                                 // then yp
-    float c[TT][W::NP][2];
     float bias[W::CB];
     int first[2][TT], last[2][TT];
 };
@@ -55,7 +54,6 @@ template <int L>
 struct BwdFull : BwdSmem<L, false> {
     using W = Bwd<L>;
     float x[TT][W::CB];                                  // then dx
-    float b[TT][W::NP][2];
     float start[TT / SB][4][W::NT][4];                   // the state before every group: thread-private
     float red[W::NW][2][W::CL][2 * W::NP];               // two tokens' dB | dC of a warp's channel lanes
     float bc[W::NW][TT][2 * W::NP];                      // a warp's sums of dB | dC
@@ -84,7 +82,8 @@ __device__ __forceinline__ void fetch(const ScanArgs &a, BwdSmem<L, LOCAL> &sm, 
 #pragma unroll
         for (int k = 0; k < W::BPT; ++k) {
             const int j = bt + k * W::BSTEP, t = base + j;
-            if (j < TT && t < t1) {
+            if (j >= TT) break;
+            if (t < t1) {
                 const long long row = (long long)b * a.T + t;
                 const uint16_t *pc = static_cast<const uint16_t *>(a.Cm) + row * a.c_ld + ch.g * a.N + bn;
                 const uint16_t *pb = static_cast<const uint16_t *>(a.Bm) + row * a.b_ld + ch.g * a.N + bn;
@@ -97,6 +96,11 @@ __device__ __forceinline__ void fetch(const ScanArgs &a, BwdSmem<L, LOCAL> &sm, 
                         if (!LOCAL) sm.raw_bc[buf][LOCAL ? 0 : 1][j][n] = n < a.N ? pb[n] : (uint16_t)0;
                     }
                 }
+            } else {  // past the end: zeros
+                for (int n = 0; n < W::BW; n += 4) {
+                    *reinterpret_cast<uint2 *>(&sm.raw_bc[buf][0][j][bn + n]) = make_uint2(0, 0);
+                    if (!LOCAL) *reinterpret_cast<uint2 *>(&sm.raw_bc[buf][LOCAL ? 0 : 1][j][bn + n]) = make_uint2(0, 0);
+                }
             }
         }
         if (PACKED)
@@ -105,24 +109,12 @@ __device__ __forceinline__ void fetch(const ScanArgs &a, BwdSmem<L, LOCAL> &sm, 
     copies_commit();
 }
 
-// One raw row of B or C as duplicated fp32.
-template <typename T, int BW>
-__device__ __forceinline__ void spread(const uint16_t *r, bool in, float *o) {
-#pragma unroll
-    for (int n = 0; n < BW; n += 2) {
-        float v0, v1;
-        unpack2(widen2<T>(in ? *reinterpret_cast<const uint32_t *>(r + n) : 0u), v0, v1);
-        *reinterpret_cast<float4 *>(o + 2 * n) = make_float4(v0, v0, v1, v1);
-    }
-}
-
-// delta, gy and C of the tile that has arrived in `buf` (and through `xb` what the full pass adds).
+// delta and gy of the tile that has arrived in `buf` (and through `xb` what the full pass adds).
 template <typename T, int L, bool LOCAL, typename F>
 __device__ __forceinline__ void stage(const ScanArgs &a, BwdSmem<L, LOCAL> &sm, const Chans<Bwd<L>::CB> &ch, int base, int t1,
                                       int buf, F &&xb) {
     using W = Bwd<L>;
     const int tid = threadIdx.x, vc = (tid % W::VROW) * 8, vt = tid / W::VROW, vn = ch.count - vc;
-    const int bn = (tid % W::BROW) * 8, bt = tid / W::BROW;
 #pragma unroll
     for (int k = 0; k < W::VPT; ++k) {
         const int j = vt + k * W::VSTEP;
@@ -150,11 +142,6 @@ __device__ __forceinline__ void stage(const ScanArgs &a, BwdSmem<L, LOCAL> &sm, 
         put8(&sm.delta[j][vc], d);
         put8(&sm.gy[j][vc], g);
         xb(j, vc, in);
-    }
-#pragma unroll
-    for (int k = 0; k < W::BPT; ++k) {
-        const int j = bt + k * W::BSTEP;
-        if (j < TT) spread<T, W::BW>(sm.raw_bc[buf][0][j] + bn, base + j < t1, sm.c[j][bn]);
     }
 }
 
@@ -203,16 +190,12 @@ __global__ void __launch_bounds__(Bwd<L>::NT, L >= 4 ? 5 : 2) scan_bwd_local_ker
                 }
             }
             const F2x2 d = lds_f2x2(&sm.delta[j][c0]), gy = lds_f2x2(&sm.gy[j][c0]);
+            f2 cc[4];
+            lds_dup4<T>(&sm.raw_bc[buf][0][j][n0], cc);
 #pragma unroll
-            for (int n = 0; n < 4; n += 2) {
-                const F2x2 cc = lds_f2x2(sm.c[j][n0 + n]);
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const f2 cm = m ? cc.hi : cc.lo;
-                    f2 *k = back[n + m];
-                    k[0] = mul2(ex2x2(mul2(A2[n + m][0], d.lo)), fma2(gy.lo, cm, k[0]));
-                    k[1] = mul2(ex2x2(mul2(A2[n + m][1], d.hi)), fma2(gy.hi, cm, k[1]));
-                }
+            for (int n = 0; n < 4; ++n) {
+                back[n][0] = mul2(ex2x2(mul2(A2[n][0], d.lo)), fma2(gy.lo, cc[n], back[n][0]));
+                back[n][1] = mul2(ex2x2(mul2(A2[n][1], d.hi)), fma2(gy.hi, cc[n], back[n][1]));
             }
             sum_lo = add2(sum_lo, d.lo);
             sum_hi = add2(sum_hi, d.hi);
@@ -246,7 +229,6 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
     const int t0 = s * a.seglen, t1 = min(a.T, t0 + a.seglen);
     const int top = t0 + (t1 - 1 - t0) / TT * TT;
     const int vc = (tid % W::VROW) * 8, vt = tid / W::VROW, vn = ch.count - vc;
-    const int bn = (tid % W::BROW) * 8, bt = tid / W::BROW;
     if (PACKED && blockIdx.x == 0) check_cu(a.cu, a.nseq, a.T, a.err);
 
     // the saved state before the tile at `base`, into the last group's slot (free once that group is done)
@@ -296,11 +278,6 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
             if (in) widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][3][j][c]), x);
             put8(&sm.x[j][c], x);
         });
-#pragma unroll
-        for (int k = 0; k < W::BPT; ++k) {
-            const int j = bt + k * W::BSTEP;
-            if (j < TT) spread<T, W::BW>(sm.raw_bc[buf][1][j] + bn, base + j < t1, sm.b[j][bn]);
-        }
         fetch<L, false, PACKED>(a, sm, ch, b, base - TT, t0, t1, buf ^ 1);
         __syncthreads();
         // forward over the tile: the state before every group of SB tokens
@@ -322,16 +299,12 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
                     if (PACKED && sm.first[buf][j] >= 0) initial(sm.first[buf][j], h);
                     const F2x2 d = lds_f2x2(&sm.delta[j][c0]), x = lds_f2x2(&sm.x[j][c0]);
                     const f2 u_lo = mul2(d.lo, x.lo), u_hi = mul2(d.hi, x.hi);
+                    f2 bb[4];
+                    lds_dup4<T>(&sm.raw_bc[buf][1][j][n0], bb);
 #pragma unroll
-                    for (int n = 0; n < 4; n += 2) {
-                        const F2x2 bb = lds_f2x2(sm.b[j][n0 + n]);
-#pragma unroll
-                        for (int m = 0; m < 2; ++m) {
-                            const f2 bm = m ? bb.hi : bb.lo;
-                            f2 *hn = h[n + m];
-                            hn[0] = fma2(ex2x2(mul2(A2[n + m][0], d.lo)), hn[0], mul2(u_lo, bm));
-                            hn[1] = fma2(ex2x2(mul2(A2[n + m][1], d.hi)), hn[1], mul2(u_hi, bm));
-                        }
+                    for (int n = 0; n < 4; ++n) {
+                        h[n][0] = fma2(ex2x2(mul2(A2[n][0], d.lo)), h[n][0], mul2(u_lo, bb[n]));
+                        h[n][1] = fma2(ex2x2(mul2(A2[n][1], d.hi)), h[n][1], mul2(u_hi, bb[n]));
                     }
                 }
             }
@@ -357,19 +330,17 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
                 const F2x2 d = lds_f2x2(&sm.delta[j][c0]), x = lds_f2x2(&sm.x[j][c0]);
                 const f2 u_lo = mul2(d.lo, x.lo), u_hi = mul2(d.hi, x.hi);
                 f2 y_lo = 0ull, y_hi = 0ull;
+                f2 bb[4], cc[4];
+                lds_dup4<T>(&sm.raw_bc[buf][1][j][n0], bb);
+                lds_dup4<T>(&sm.raw_bc[buf][0][j][n0], cc);
 #pragma unroll
-                for (int n = 0; n < 4; n += 2) {
-                    const F2x2 bb = lds_f2x2(sm.b[j][n0 + n]), cc = lds_f2x2(sm.c[j][n0 + n]);
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        const f2 bm = m ? bb.hi : bb.lo, cm = m ? cc.hi : cc.lo;
-                        dec[i][n + m][0] = ex2x2(mul2(A2[n + m][0], d.lo));
-                        dec[i][n + m][1] = ex2x2(mul2(A2[n + m][1], d.hi));
-                        hs[i][n + m][0] = fma2(dec[i][n + m][0], from[n + m][0], mul2(u_lo, bm));
-                        hs[i][n + m][1] = fma2(dec[i][n + m][1], from[n + m][1], mul2(u_hi, bm));
-                        y_lo = fma2(hs[i][n + m][0], cm, y_lo);
-                        y_hi = fma2(hs[i][n + m][1], cm, y_hi);
-                    }
+                for (int n = 0; n < 4; ++n) {
+                    dec[i][n][0] = ex2x2(mul2(A2[n][0], d.lo));
+                    dec[i][n][1] = ex2x2(mul2(A2[n][1], d.hi));
+                    hs[i][n][0] = fma2(dec[i][n][0], from[n][0], mul2(u_lo, bb[n]));
+                    hs[i][n][1] = fma2(dec[i][n][1], from[n][1], mul2(u_hi, bb[n]));
+                    y_lo = fma2(hs[i][n][0], cc[n], y_lo);
+                    y_hi = fma2(hs[i][n][1], cc[n], y_hi);
                 }
                 if (a.dz) LaneSum<L>::run(y_lo, y_hi, nl, yp[i]);
             }
@@ -400,26 +371,23 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
                 const f2 u_lo = mul2(d.lo, x.lo), u_hi = mul2(d.hi, x.hi);
                 f2 s_lo = 0ull, s_hi = 0ull, q_lo = 0ull, q_hi = 0ull;
                 float db[4], dc[4];
+                f2 bb[4], cc[4];
+                lds_dup4<T>(&sm.raw_bc[buf][1][j][n0], bb);
+                lds_dup4<T>(&sm.raw_bc[buf][0][j][n0], cc);
 #pragma unroll
-                for (int n = 0; n < 4; n += 2) {
-                    const F2x2 bb = lds_f2x2(sm.b[j][n0 + n]), cc = lds_f2x2(sm.c[j][n0 + n]);
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        const int k = n + m;
-                        const f2 bm = m ? bb.hi : bb.lo, cm = m ? cc.hi : cc.lo;
-                        const f2 g_lo = fma2(gy.lo, cm, back[k][0]), g_hi = fma2(gy.hi, cm, back[k][1]);
-                        dc[k] = sum2(fma2(gy.hi, hs[i][k][1], mul2(gy.lo, hs[i][k][0])));
-                        db[k] = sum2(fma2(g_hi, u_hi, mul2(g_lo, u_lo)));
-                        s_lo = fma2(g_lo, bm, s_lo);
-                        s_hi = fma2(g_hi, bm, s_hi);
-                        back[k][0] = mul2(g_lo, dec[i][k][0]);
-                        back[k][1] = mul2(g_hi, dec[i][k][1]);
-                        const f2 p_lo = mul2(back[k][0], from[k][0]), p_hi = mul2(back[k][1], from[k][1]);
-                        dA[k][0] = fma2(d.lo, p_lo, dA[k][0]);
-                        dA[k][1] = fma2(d.hi, p_hi, dA[k][1]);
-                        q_lo = fma2(A2[k][0], p_lo, q_lo);
-                        q_hi = fma2(A2[k][1], p_hi, q_hi);
-                    }
+                for (int k = 0; k < 4; ++k) {
+                    const f2 g_lo = fma2(gy.lo, cc[k], back[k][0]), g_hi = fma2(gy.hi, cc[k], back[k][1]);
+                    dc[k] = sum2(fma2(gy.hi, hs[i][k][1], mul2(gy.lo, hs[i][k][0])));
+                    db[k] = sum2(fma2(g_hi, u_hi, mul2(g_lo, u_lo)));
+                    s_lo = fma2(g_lo, bb[k], s_lo);
+                    s_hi = fma2(g_hi, bb[k], s_hi);
+                    back[k][0] = mul2(g_lo, dec[i][k][0]);
+                    back[k][1] = mul2(g_hi, dec[i][k][1]);
+                    const f2 p_lo = mul2(back[k][0], from[k][0]), p_hi = mul2(back[k][1], from[k][1]);
+                    dA[k][0] = fma2(d.lo, p_lo, dA[k][0]);
+                    dA[k][1] = fma2(d.hi, p_hi, dA[k][1]);
+                    q_lo = fma2(A2[k][0], p_lo, q_lo);
+                    q_hi = fma2(A2[k][1], p_hi, q_hi);
                 }
                 // (odd channel lanes swap the two halves of their row, so that neighbouring rows use other banks)
                 float *r = sm.red[warp][i & 1][cl];

@@ -30,7 +30,7 @@ struct Fwd {
 };
 
 // The raw tiles (two of each: the next one is on its way while one is worked on) are private to the threads that copy
-// them; so are, but for the recurrence in between, the staged elements of a vector.
+// them, but for B and C; so are, but for the recurrence in between, the staged elements of a vector.
 template <int L, bool FULL>
 struct FwdSmem {
     using F = Fwd<L>;
@@ -38,15 +38,13 @@ struct FwdSmem {
     uint16_t raw_bc[2][FULL ? 2 : 1][F::TT][F::NP];
     float delta[F::TT][F::CB];
     float u[F::TT][F::CB];                              // delta x; then the output of the recurrence
-    float b[F::TT][F::NP][2];
-    float c[FULL ? F::TT : 1][F::NP][2];
     float bias[F::CB], skip[F::CB];
     int first[2][F::TT], last[2][F::TT];
 };
 
 // FULL: the outputs (second pass, or the only one).  Otherwise the first pass over segments.
 template <typename T, int L, bool FULL, bool PACKED>
-__global__ void __launch_bounds__(128, FULL ? 4 : 5) scan_fwd_kernel(const ScanArgs a) {
+__global__ void __launch_bounds__(128, FULL ? 5 : 6) scan_fwd_kernel(const ScanArgs a) {
     using F = Fwd<L>;
     constexpr int CB = F::CB, TT = F::TT, NP = F::NP;
     extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -91,7 +89,8 @@ __global__ void __launch_bounds__(128, FULL ? 4 : 5) scan_fwd_kernel(const ScanA
 #pragma unroll
             for (int k = 0; k < F::BPT; ++k) {
                 const int j = bt + k * BSTEP, t = base + j;
-                if (j < TT && t < t1) {
+                if (j >= TT) break;
+                if (t < t1) {
                     const long long row = row0 + t;
                     const int at = ch.g * a.N + bn;
                     const uint16_t *pb = static_cast<const uint16_t *>(a.Bm) + row * a.b_ld + at;
@@ -104,6 +103,11 @@ __global__ void __launch_bounds__(128, FULL ? 4 : 5) scan_fwd_kernel(const ScanA
                             sm.raw_bc[buf][0][j][n] = n < a.N ? pb[n] : (uint16_t)0;
                             if (FULL) sm.raw_bc[buf][FULL ? 1 : 0][j][n] = n < a.N ? pc[n] : (uint16_t)0;
                         }
+                    }
+                } else {  // past the end: zeros
+                    for (int n = 0; n < BW; n += 4) {
+                        *reinterpret_cast<uint2 *>(&sm.raw_bc[buf][0][j][bn + n]) = make_uint2(0, 0);
+                        if (FULL) *reinterpret_cast<uint2 *>(&sm.raw_bc[buf][FULL ? 1 : 0][j][bn + n]) = make_uint2(0, 0);
                     }
                 }
             }
@@ -153,24 +157,6 @@ __global__ void __launch_bounds__(128, FULL ? 4 : 5) scan_fwd_kernel(const ScanA
             put8(&sm.delta[j][vc], d);
             put8(&sm.u[j][vc], x);
         }
-#pragma unroll
-        for (int k = 0; k < F::BPT; ++k) {
-            const int j = bt + k * BSTEP;
-            if (j < TT) {
-                const bool in = base + j < t1;
-#pragma unroll
-                for (int m = 0; m < (FULL ? 2 : 1); ++m) {
-                    const uint16_t *r = sm.raw_bc[buf][m][j] + bn;
-                    float *o = m ? sm.c[FULL ? j : 0][bn] : sm.b[j][bn];
-#pragma unroll
-                    for (int n = 0; n < BW; n += 2) {
-                        float v0, v1;
-                        unpack2(widen2<T>(in ? *reinterpret_cast<const uint32_t *>(r + n) : 0u), v0, v1);
-                        *reinterpret_cast<float4 *>(o + 2 * n) = make_float4(v0, v0, v1, v1);
-                    }
-                }
-            }
-        }
         __syncthreads();
         if (FULL && a.saved && base % SAVE == 0)
             store_padded(a.saved + (((long long)b * ((a.T + SAVE - 1) / SAVE) + base / SAVE) * NP + n0) * a.DP + ch.pad + c0,
@@ -188,21 +174,16 @@ __global__ void __launch_bounds__(128, FULL ? 4 : 5) scan_fwd_kernel(const ScanA
                 }
             }
             const F2x2 d = lds_f2x2(&sm.delta[j][c0]), u = lds_f2x2(&sm.u[j][c0]);
-            f2 y_lo = 0ull, y_hi = 0ull;
+            f2 y_lo = 0ull, y_hi = 0ull, bb[4], cc[4];
+            lds_dup4<T>(&sm.raw_bc[buf][0][j][n0], bb);
+            if (FULL) lds_dup4<T>(&sm.raw_bc[buf][FULL ? 1 : 0][j][n0], cc);
 #pragma unroll
-            for (int n = 0; n < 4; n += 2) {
-                const F2x2 bb = lds_f2x2(sm.b[j][n0 + n]);
-                const F2x2 cc = FULL ? lds_f2x2(sm.c[FULL ? j : 0][n0 + n]) : F2x2{0ull, 0ull};
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const f2 bm = m ? bb.hi : bb.lo, cm = m ? cc.hi : cc.lo;
-                    f2 *hn = h[n + m];
-                    hn[0] = fma2(ex2x2(mul2(A2[n + m][0], d.lo)), hn[0], mul2(u.lo, bm));
-                    hn[1] = fma2(ex2x2(mul2(A2[n + m][1], d.hi)), hn[1], mul2(u.hi, bm));
-                    if (FULL) {
-                        y_lo = fma2(hn[0], cm, y_lo);
-                        y_hi = fma2(hn[1], cm, y_hi);
-                    }
+            for (int n = 0; n < 4; ++n) {
+                h[n][0] = fma2(ex2x2(mul2(A2[n][0], d.lo)), h[n][0], mul2(u.lo, bb[n]));
+                h[n][1] = fma2(ex2x2(mul2(A2[n][1], d.hi)), h[n][1], mul2(u.hi, bb[n]));
+                if (FULL) {
+                    y_lo = fma2(h[n][0], cc[n], y_lo);
+                    y_hi = fma2(h[n][1], cc[n], y_hi);
                 }
             }
             if (FULL) {
@@ -269,13 +250,33 @@ __global__ void __launch_bounds__(128) scan_join_kernel(const ScanArgs a, const 
     const int c = g * a.Dg + in;
     const float A2 = live ? a.A[(long long)c * a.N + n] * LOG2E : 0.f;
     float h = (live && start) ? start[((long long)b * a.D + c) * a.N + n] : 0.f;
-    for (int i = 0; i < a.nseg - 1; ++i) {
-        const int s = reverse ? a.nseg - 1 - i : i;
-        const long long at = (long long)b * a.nseg + s;
-        float *p = a.seg + (at * NP + n) * a.DP + pc;
-        const float through = (a.cut && a.cut[s]) ? 0.f : ex2(A2 * a.segdt[at * a.DP + pc]);
-        h = fmaf(through, h, *p);
-        *p = h;
+    constexpr int U = 8;  // segments a batch; the next batch's loads are in flight while one is joined
+    const long long b0 = (long long)b * a.nseg;
+    const int steps = a.nseg - 1;
+    float own[U], dt[U];
+    int cut[U];
+    auto fetch = [&](int i) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = reverse ? steps - i - u : i + u;
+            const bool in = i + u < steps;
+            own[u] = in ? a.seg[((b0 + s) * NP + n) * a.DP + pc] : 0.f;
+            dt[u] = in ? a.segdt[(b0 + s) * a.DP + pc] : 0.f;
+            cut[u] = in && a.cut ? a.cut[s] : 0;
+        }
+    };
+    fetch(0);
+    for (int i = 0; i < steps; i += U) {
+        float now[U], through[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) now[u] = own[u], through[u] = cut[u] ? 0.f : ex2(A2 * dt[u]);
+        fetch(i + U);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = reverse ? steps - i - u : i + u;
+            h = fmaf(through[u], h, now[u]);
+            if (i + u < steps) a.seg[((b0 + s) * NP + n) * a.DP + pc] = h;
+        }
     }
 }
 

@@ -25,7 +25,7 @@ def _p(t):
 
 
 def _s(t):
-    return torch.cuda.current_stream(t.device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _dt(t, name, allowed):
