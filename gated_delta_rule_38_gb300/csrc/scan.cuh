@@ -45,6 +45,7 @@ struct ScanArgs {
     int gpad, DP;          // padded channels a group, and of all groups
     int nseg, seglen;
     bool softplus, vec, vec_bc, st_vec;
+    // vec, vec_bc: the token tensors, B and C, take the 16-byte accesses; otherwise their rows are copied as pieces
 };
 
 struct F2x2 {
@@ -118,16 +119,6 @@ __device__ __forceinline__ uint4 load8(const uint16_t *p, int n, bool vec) {
         if (i < n) r[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
-__device__ __forceinline__ void store8(uint16_t *p, uint4 u, int n, bool vec) {
-    if (vec && n >= 8) {
-        *reinterpret_cast<uint4 *>(p) = u;
-        return;
-    }
-    const uint32_t r[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n) p[i] = (uint16_t)(r[i >> 1] >> (16 * (i & 1)));
-}
 // Eight 16-bit elements as four fp32 pairs, and back.
 template <typename T>
 __device__ __forceinline__ void widen8(uint4 u, f2 *o) {
@@ -157,13 +148,44 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;\n" ::"n"(LEFT) : "memory");
 }
 
-// Eight elements of a token row into this thread's own place in shared memory: an asynchronous copy where the row
-// allows 16-byte accesses and all eight exist, else plain loads.  `n` of them exist; the others become zeros.
+// Eight elements into this thread's own place in shared memory: an asynchronous copy where all of them exist, else
+// plain loads.  `n` of them exist; the others become zeros.
 __device__ __forceinline__ void copy8(uint16_t *to, const uint16_t *from, int n, bool vec) {
     if (vec && n >= 8)
         copy16(to, from);
     else
         *reinterpret_cast<uint4 *>(to) = load8(from, n, false);
+}
+
+// Rows of a tensor that allows no 16-byte accesses (odd widths or strides, views at any element).  Threads copy the
+// aligned 16-byte pieces that hold `width` elements of each row, cut off at the tensor's ends, so that the copies are
+// asynchronous all the same; element e of row j then lies at to[j rs + skew + e], rs >= width + 7.
+struct Rows {
+    const uint16_t *base;
+    long long ld, first, rows;   // row stride; first element of interest in a row; rows of the tensor
+    int cols;                    // elements of a row
+    __device__ __forceinline__ const uint16_t *at(long long row) const { return base + row * ld + first; }
+    __device__ __forceinline__ int skew(long long row) const { return (int)((reinterpret_cast<uintptr_t>(at(row)) & 15) >> 1); }
+};
+template <int NT, int PIECES>
+__device__ __forceinline__ void copy_rows(uint16_t *to, int rs, const Rows &r, long long row, int rows, int width) {
+    const char *lo = reinterpret_cast<const char *>(r.base);
+    const char *hi = reinterpret_cast<const char *>(r.base + (r.rows - 1) * r.ld + r.cols);
+    for (int i = threadIdx.x; i < rows * PIECES; i += NT) {
+        const int j = i / PIECES, k = i % PIECES;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(r.at(row + j));
+        const int skew = (int)(at & 15);
+        if (k * 16 >= skew + 2 * width) continue;
+        const char *src = reinterpret_cast<const char *>(at - skew) + k * 16;
+        uint16_t *dst = to + j * rs + k * 8;
+        if (src >= lo) {
+            const long long left = hi - src;
+            const int n = left < 16 ? (int)left : 16;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(dst)), "l"(src), "r"(n) : "memory");
+        } else {  // the piece begins before the tensor
+            for (int e = skew / 2; e < 8 && e - skew / 2 < width; ++e) dst[e] = reinterpret_cast<const uint16_t *>(src)[e];
+        }
+    }
 }
 
 // Packed batches: the sequence that token t starts (first) and the one that it ends (last), -1 for neither.
@@ -178,6 +200,21 @@ __device__ __forceinline__ void edges(const ScanArgs &a, int t, int t_end, int &
     if (a.cu[lo] == t) first = lo;
     if (a.cu[lo + 1] == t + 1) last = lo;
 }
+
+// For every token of a tile at once (the first lanes of a block's first warp): first[], last[], and whether any is set.
+template <int TOKENS>
+__device__ __forceinline__ void tile_edges(const ScanArgs &a, int base, int t_end, int *first, int *last, int *any) {
+    if (threadIdx.x >= TOKENS) return;
+    edges(a, base + threadIdx.x, t_end, first[threadIdx.x], last[threadIdx.x]);
+    const int some = __any_sync(0xffffffffu >> (32 - TOKENS), first[threadIdx.x] >= 0 || last[threadIdx.x] >= 0);
+    if (threadIdx.x == 0) *any = some;
+}
+
+// A compile-time flag to pass to a generic lambda: tiles that no sequence starts or ends in run without the tests.
+template <bool V>
+struct Flag {
+    static constexpr bool value = V;
+};
 
 // ---------------------------------------------------------------- a thread's 4 channels x 4 states
 

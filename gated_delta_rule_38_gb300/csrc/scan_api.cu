@@ -8,8 +8,10 @@ cudaError_t launch_scan_fwd(const ScanArgs &a, int L, bool bf16, bool full, cuda
 cudaError_t launch_scan_join(const ScanArgs &a, int L, const float *start, bool reverse, cudaStream_t s);
 cudaError_t launch_scan_empty(const ScanArgs &a, const float *src, float *dst, cudaStream_t s);
 cudaError_t launch_scan_step(const ScanArgs &a, int L, bool bf16, cudaStream_t s);
-cudaError_t launch_scan_bwd(const ScanArgs &a, int L, bool bf16, bool full, cudaStream_t s);
-cudaError_t launch_scan_dbc(const ScanArgs &a, int L, bool bf16, cudaStream_t s);
+cudaError_t launch_scan_bwd_bf16(const ScanArgs &a, int L, bool full, cudaStream_t s);
+cudaError_t launch_scan_bwd_fp16(const ScanArgs &a, int L, bool full, cudaStream_t s);
+cudaError_t launch_scan_dbc_bf16(const ScanArgs &a, int L, cudaStream_t s);
+cudaError_t launch_scan_dbc_fp16(const ScanArgs &a, int L, cudaStream_t s);
 
 namespace {
 
@@ -287,14 +289,14 @@ gdr_status gdr_scan_bwd(const gdr_scan_problem *p, const void *x, const void *dt
     if (c.nseg > 1) {
         a.seg = at<float>(workspace, l.seg), a.segdt = at<float>(workspace, l.segdt);
         if (p->cu_seqlens) a.cut = at<int32_t>(workspace, l.cut);
-        st = timed(K_SCAN_LOCAL, cs, [&] { return launch_scan_bwd(a, c.L, bf, false, cs); });
+        st = timed(K_SCAN_LOCAL, cs, [&] { return bf ? launch_scan_bwd_bf16(a, c.L, false, cs) : launch_scan_bwd_fp16(a, c.L, false, cs); });
         if (st != GDR_OK) return st;
         st = timed(K_SCAN_JOIN, cs, [&] { return launch_scan_join(a, c.L, nullptr, true, cs); });
         if (st != GDR_OK) return st;
     }
-    st = timed(K_SCAN_BWD, cs, [&] { return launch_scan_bwd(a, c.L, bf, true, cs); });
+    st = timed(K_SCAN_BWD, cs, [&] { return bf ? launch_scan_bwd_bf16(a, c.L, true, cs) : launch_scan_bwd_fp16(a, c.L, true, cs); });
     if (st != GDR_OK) return st;
-    st = timed(K_REDUCE, cs, [&] { return launch_scan_dbc(a, c.L, bf, cs); });
+    st = timed(K_REDUCE, cs, [&] { return bf ? launch_scan_dbc_bf16(a, c.L, cs) : launch_scan_dbc_fp16(a, c.L, cs); });
     if (st != GDR_OK) return st;
     // the parameters' gradients: partial rows of [D N | D | D] a segment
     st = timed(K_REDUCE, cs, [&] {

@@ -14,6 +14,8 @@
 // the warp's and the block's through shared memory, and over the blocks by a second kernel, all in a fixed order.
 // As in the forward, segments give parallelism along the token axis: a first pass leaves the gradient that each
 // segment alone sends back past its start, and the scan joins them.
+#pragma once
+
 #include "scan.cuh"
 
 namespace gdr {
@@ -36,121 +38,205 @@ struct Bwd {
     static constexpr int BW = NP >= 8 ? 8 : 4;           // states of a vector of B or C
     static constexpr int BROW = NP / BW, BSTEP = NT / BROW;
     static constexpr int BPT = TT > BSTEP ? TT / BSTEP : 1;
+    // The ragged rows' elements are taken as pairs of tokens of a channel: task i is the pair (2 (i / COLS), + 1) of 32
+    // channels, warp w takes w, w + NW, ..  A lane sums over tokens in GROUP sums that take the tokens in the order of
+    // the whole vectors' threads (token modulo CLS), so that both forms give the same bits.
+    static constexpr int COLS = CB / 32, TASKS = TT / 2 * COLS / NW;
+    static constexpr int CLS = VSTEP < TT ? VSTEP : TT;
+    static constexpr int NCOL = COLS > NW ? COLS / NW : 1;
+    static constexpr int PL = CLS / 2 / (NW > COLS ? NW / COLS : 1);
+    static constexpr int GROUP = NCOL * PL;
+    static_assert(GROUP <= 4 && TASKS % GROUP == 0, "sums of a lane");
 };
 
-// The raw tiles (two of each: the next one is on its way while one is worked on) are private to the threads that copy
-// them, the states before the groups to the threads that own the states.
+// As in the forward: the staged tile and, behind it in dynamic shared memory, the raw ones (dt, dy, z, x; C, B as pieces).
 template <int L, bool LOCAL>
-struct BwdSmem {
+struct BwdStage {
     using W = Bwd<L>;
-    uint16_t raw[2][LOCAL ? 3 : 4][TT][W::CB];           // dt, dy, z, x
-    uint16_t raw_bc[2][LOCAL ? 1 : 2][TT][W::NP];        // C, B
+    static constexpr int M = LOCAL ? 3 : 4, MB = LOCAL ? 1 : 2, RB = W::NP < 8 ? 16 : W::NP + 8;
+    uint16_t raw_bc[2][MB][TT][W::NP];                   // C, B
     float delta[TT][W::CB];                              // then the gradient of delta
     float gy[TT][W::CB];                                 // then yp
     float bias[W::CB];
-    int first[2][TT], last[2][TT];
+    int first[2][TT], last[2][TT], any[4];
+    static __host__ __device__ constexpr int row(bool vec) { return vec ? W::CB : W::CB + 8; }
 };
 template <int L>
-struct BwdFull : BwdSmem<L, false> {
+struct BwdFull : BwdStage<L, false> {
     using W = Bwd<L>;
     float x[TT][W::CB];                                  // then dx
     float start[TT / SB][4][W::NT][4];                   // the state before every group: thread-private
     float red[W::NW][2][W::CL][2 * W::NP];               // two tokens' dB | dC of a warp's channel lanes
     float bc[W::NW][TT][2 * W::NP];                      // a warp's sums of dB | dC
 };
+template <int L, bool LOCAL>
+size_t raw_bytes(bool vec, bool vec_bc) {
+    using S = BwdStage<L, LOCAL>;
+    return sizeof(uint16_t) * (2 * S::M * TT * S::row(vec) + (vec_bc ? 0 : 2 * S::MB * TT * S::RB));
+}
 
-// The copies of the tile at `base` into buffer `buf`.
-template <int L, bool LOCAL, bool PACKED>
-__device__ __forceinline__ void fetch(const ScanArgs &a, BwdSmem<L, LOCAL> &sm, const Chans<Bwd<L>::CB> &ch, int b, int base,
-                                      int t0, int t1, int buf) {
+// A block's view of its tiles: the copies, and the tensors' rows.
+template <typename T, int L, bool LOCAL, bool PACKED>
+struct Tiles {
     using W = Bwd<L>;
-    const int tid = threadIdx.x, vc = (tid % W::VROW) * 8, vt = tid / W::VROW, vn = ch.count - vc;
-    const int bn = (tid % W::BROW) * 8, bt = tid / W::BROW;
-    if (base >= t0) {
+    using S = BwdStage<L, LOCAL>;
+    const ScanArgs &a;
+    S &sm;
+    uint16_t *raws;
+    const Chans<W::CB> &ch;
+    long long row0;
+    int t0, t1, tid, vc, vt, vn, bn, bt;
+    bool vec, vec_bc;
+    __device__ __forceinline__ Tiles(const ScanArgs &a_, S &s_, void *raws_, const Chans<W::CB> &c_, int b, int t0_, int t1_)
+        : a(a_), sm(s_), raws(static_cast<uint16_t *>(raws_)), ch(c_), row0((long long)b * a_.T), t0(t0_), t1(t1_), vec(a_.vec),
+          vec_bc(a_.vec_bc) {
+        tid = threadIdx.x;
+        vc = (tid % W::VROW) * 8, vt = tid / W::VROW, vn = ch.count - vc;
+        bn = (tid % W::BROW) * 8, bt = tid / W::BROW;
+    }
+    __device__ __forceinline__ uint16_t *raw(int buf, int m, int j, bool v) const {
+        return raws + ((buf * S::M + m) * TT + j) * S::row(v);
+    }
+    __device__ __forceinline__ uint16_t *rag_bc(int buf, int m, int j) const {
+        return raw(2, 0, 0, vec) + ((buf * S::MB + m) * TT + j) * S::RB;
+    }
+    // dt, dy, z, x
+    __device__ __forceinline__ Rows src(int m) const {
+        const void *p = m == 0 ? a.dt : m == 1 ? a.dy : m == 2 ? a.z : a.x;
+        const long long ld = m == 0 ? a.dt_ld : m == 1 ? a.D : m == 2 ? a.z_ld : a.x_ld;
+        return Rows{static_cast<const uint16_t *>(p), ld, ch.first, (long long)a.B * a.T, a.D};
+    }
+    __device__ __forceinline__ Rows src_bc(int m) const {
+        return Rows{static_cast<const uint16_t *>(m ? a.Bm : a.Cm), m ? a.b_ld : a.c_ld, ch.g * a.N, (long long)a.B * a.T, a.G * a.N};
+    }
+    // The copies of the tile at `base` into buffer `buf`.
+    __device__ __forceinline__ void fetch(int base, int buf) const {
+        if (base >= t0) {
+            const int rows = min(TT, t1 - base);
 #pragma unroll
-        for (int k = 0; k < W::VPT; ++k) {
-            const int j = vt + k * W::VSTEP, t = base + j;
-            if (j < TT && t < t1 && vn > 0) {
-                const long long row = (long long)b * a.T + t;
-                const int c = ch.first + vc;
-                copy8(&sm.raw[buf][0][j][vc], static_cast<const uint16_t *>(a.dt) + row * a.dt_ld + c, vn, a.vec);
-                copy8(&sm.raw[buf][1][j][vc], static_cast<const uint16_t *>(a.dy) + row * a.D + c, vn, a.vec);
-                if (a.z) copy8(&sm.raw[buf][2][j][vc], static_cast<const uint16_t *>(a.z) + row * a.z_ld + c, vn, a.vec);
-                if (!LOCAL) copy8(&sm.raw[buf][LOCAL ? 0 : 3][j][vc], static_cast<const uint16_t *>(a.x) + row * a.x_ld + c, vn, a.vec);
-            }
-        }
+            for (int m = 0; m < S::M; ++m) {
+                if (m == 2 && !a.z) continue;
+                if (vec) {
 #pragma unroll
-        for (int k = 0; k < W::BPT; ++k) {
-            const int j = bt + k * W::BSTEP, t = base + j;
-            if (j >= TT) break;
-            if (t < t1) {
-                const long long row = (long long)b * a.T + t;
-                const uint16_t *pc = static_cast<const uint16_t *>(a.Cm) + row * a.c_ld + ch.g * a.N + bn;
-                const uint16_t *pb = static_cast<const uint16_t *>(a.Bm) + row * a.b_ld + ch.g * a.N + bn;
-                if constexpr (W::BW == 8) {
-                    copy8(&sm.raw_bc[buf][0][j][bn], pc, a.N - bn, a.vec_bc);
-                    if (!LOCAL) copy8(&sm.raw_bc[buf][LOCAL ? 0 : 1][j][bn], pb, a.N - bn, a.vec_bc);
+                    for (int k = 0; k < W::VPT; ++k) {
+                        const int j = vt + k * W::VSTEP;
+                        if (j < rows && vn > 0) copy8(raw(buf, m, j, true) + vc, src(m).at(row0 + base + j) + vc, vn, true);
+                    }
                 } else {
-                    for (int n = 0; n < W::BW; ++n) {
-                        sm.raw_bc[buf][0][j][n] = n < a.N ? pc[n] : (uint16_t)0;
-                        if (!LOCAL) sm.raw_bc[buf][LOCAL ? 0 : 1][j][n] = n < a.N ? pb[n] : (uint16_t)0;
+                    copy_rows<W::NT, W::CB / 8 + 1>(raw(buf, m, 0, false), S::row(false), src(m), row0 + base, rows, ch.count);
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < S::MB; ++m) {
+                if (!vec_bc) {
+                    copy_rows<W::NT, W::NP / 8 + 2>(rag_bc(buf, m, 0), S::RB, src_bc(m), row0 + base, rows, a.N);
+                } else if constexpr (W::BW == 8) {
+#pragma unroll
+                    for (int k = 0; k < W::BPT; ++k) {
+                        const int j = bt + k * W::BSTEP;
+                        if (j < rows)
+                            copy8(&sm.raw_bc[buf][m][j][bn], src_bc(m).at(row0 + base + j) + bn, a.N - bn, true);
+                        else if (j < TT)  // past the end: zeros
+                            *reinterpret_cast<uint4 *>(&sm.raw_bc[buf][m][j][bn]) = make_uint4(0, 0, 0, 0);
                     }
                 }
-            } else {  // past the end: zeros
-                for (int n = 0; n < W::BW; n += 4) {
-                    *reinterpret_cast<uint2 *>(&sm.raw_bc[buf][0][j][bn + n]) = make_uint2(0, 0);
-                    if (!LOCAL) *reinterpret_cast<uint2 *>(&sm.raw_bc[buf][LOCAL ? 0 : 1][j][bn + n]) = make_uint2(0, 0);
+            }
+            if (PACKED) tile_edges<TT>(a, base, t1, sm.first[buf], sm.last[buf], &sm.any[buf]);
+        }
+        copies_commit();
+    }
+    // Pairs of tokens of one channel, for the ragged rows: consecutive lanes take consecutive channels.
+    template <typename F>
+    __device__ __forceinline__ void each_pair(F &&f) const {
+        for (int rep = 0; rep < W::TASKS / W::GROUP; ++rep)
+#pragma unroll
+            for (int k = 0; k < W::GROUP; ++k) {
+                const int i = (tid >> 5) + W::NW * (rep * W::GROUP + k);
+                f(i / W::COLS * 2, i % W::COLS * 32 + (tid & 31), k);
+            }
+    }
+    __device__ __forceinline__ f2 pair_of(int buf, int m, int base, int j, int c) const {
+        const Rows r = src(m);
+        const uint16_t lo = raw(buf, m, j, false)[r.skew(row0 + base + j) + c];
+        const uint16_t hi = raw(buf, m, j + 1, false)[r.skew(row0 + base + j + 1) + c];
+        return widen2<T>((uint32_t)lo | (uint32_t)hi << 16);
+    }
+    __device__ __forceinline__ f2 delta_of(f2 raw_dt, f2 bias) const {
+        const f2 d = add2(raw_dt, bias);
+        return a.softplus ? softplus2(d) : d;
+    }
+    // delta and gy (and x) of the tile that has arrived in `buf`; a step of zero and no gradient past the ends.
+    __device__ __forceinline__ void stage(int base, int buf, float (*xs)[W::CB]) const {
+        if (!(vec && vec_bc)) __syncthreads();
+        if (vec) {
+#pragma unroll
+            for (int k = 0; k < W::VPT; ++k) {
+                const int j = vt + k * W::VSTEP;
+                if (j >= TT) break;
+                f2 d[4], g[4], v[4];
+                const bool in = base + j < t1 && vn > 0;
+                if (in) {
+                    widen8<T>(*reinterpret_cast<const uint4 *>(raw(buf, 0, j, true) + vc), d);
+                    widen8<T>(*reinterpret_cast<const uint4 *>(raw(buf, 1, j, true) + vc), g);
+                    get8(&sm.bias[vc], v);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) d[i] = delta_of(d[i], v[i]);
+                    if (a.z) {
+                        widen8<T>(*reinterpret_cast<const uint4 *>(raw(buf, 2, j, true) + vc), v);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) g[i] = mul2(g[i], mul2(v[i], sigmoid2(v[i])));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) d[i] = g[i] = 0ull;
+                }
+                put8(&sm.delta[j][vc], d);
+                put8(&sm.gy[j][vc], g);
+                if (!LOCAL) {
+                    f2 x[4] = {0ull, 0ull, 0ull, 0ull};
+                    if (in) widen8<T>(*reinterpret_cast<const uint4 *>(raw(buf, LOCAL ? 0 : 3, j, true) + vc), x);
+                    put8(&xs[j][vc], x);
+                }
+            }
+        } else {
+            each_pair([&](int j, int c, int) {
+                const f2 d = delta_of(pair_of(buf, 0, base, j, c), both(sm.bias[c]));
+                f2 g = pair_of(buf, 1, base, j, c);
+                if (a.z) {
+                    const f2 z = pair_of(buf, 2, base, j, c);
+                    g = mul2(g, mul2(z, sigmoid2(z)));
+                }
+                const bool in0 = c < ch.count && base + j < t1, in1 = c < ch.count && base + j + 1 < t1;
+                float v0, v1;
+                unpack2(d, v0, v1);
+                sm.delta[j][c] = in0 ? v0 : 0.f, sm.delta[j + 1][c] = in1 ? v1 : 0.f;
+                unpack2(g, v0, v1);
+                sm.gy[j][c] = in0 ? v0 : 0.f, sm.gy[j + 1][c] = in1 ? v1 : 0.f;
+                if (!LOCAL) {
+                    unpack2(pair_of(buf, LOCAL ? 0 : 3, base, j, c), v0, v1);
+                    xs[j][c] = in0 ? v0 : 0.f, xs[j + 1][c] = in1 ? v1 : 0.f;
+                }
+            });
+        }
+        if (!vec_bc) {
+#pragma unroll
+            for (int m = 0; m < S::MB; ++m) {
+                const Rows r = src_bc(m);
+                for (int i = tid; i < TT * W::NP; i += W::NT) {
+                    const int j = i / W::NP, n = i % W::NP;
+                    sm.raw_bc[buf][m][j][n] = base + j < t1 && n < a.N ? rag_bc(buf, m, j)[r.skew(row0 + base + j) + n] : (uint16_t)0;
                 }
             }
         }
-        if (PACKED)
-            for (int j = tid; j < TT; j += W::NT) edges(a, base + j, t1, sm.first[buf][j], sm.last[buf][j]);
     }
-    copies_commit();
-}
-
-// delta and gy of the tile that has arrived in `buf` (and through `xb` what the full pass adds).
-template <typename T, int L, bool LOCAL, typename F>
-__device__ __forceinline__ void stage(const ScanArgs &a, BwdSmem<L, LOCAL> &sm, const Chans<Bwd<L>::CB> &ch, int base, int t1,
-                                      int buf, F &&xb) {
-    using W = Bwd<L>;
-    const int tid = threadIdx.x, vc = (tid % W::VROW) * 8, vt = tid / W::VROW, vn = ch.count - vc;
-#pragma unroll
-    for (int k = 0; k < W::VPT; ++k) {
-        const int j = vt + k * W::VSTEP;
-        if (j >= TT) break;
-        f2 d[4], g[4], v[4];
-        const bool in = base + j < t1 && vn > 0;
-        if (in) {
-            widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][0][j][vc]), d);
-            widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][1][j][vc]), g);
-            get8(&sm.bias[vc], v);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                d[i] = add2(d[i], v[i]);
-                if (a.softplus) d[i] = softplus2(d[i]);
-            }
-            if (a.z) {
-                widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][2][j][vc]), v);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) g[i] = mul2(g[i], mul2(v[i], sigmoid2(v[i])));
-            }
-        } else {  // past the end: a step of zero and no gradient
-#pragma unroll
-            for (int i = 0; i < 4; ++i) d[i] = g[i] = 0ull;
-        }
-        put8(&sm.delta[j][vc], d);
-        put8(&sm.gy[j][vc], g);
-        xb(j, vc, in);
-    }
-}
+};
 
 // First pass: the gradient that segment s sends back past its start when none reaches it from later segments.
 template <typename T, int L, bool PACKED>
 __global__ void __launch_bounds__(Bwd<L>::NT, L >= 4 ? 5 : 2) scan_bwd_local_kernel(const ScanArgs a) {
     using W = Bwd<L>;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    BwdSmem<L, true> &sm = *reinterpret_cast<BwdSmem<L, true> *>(smem_raw);
+    BwdStage<L, true> &sm = *reinterpret_cast<BwdStage<L, true> *>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int nl = lane % L, cl = lane / L;
     const int nblk = a.gblocks * a.G, segs = a.nseg - 1;
@@ -160,7 +246,8 @@ __global__ void __launch_bounds__(Bwd<L>::NT, L >= 4 ? 5 : 2) scan_bwd_local_ker
     const int c0 = warp * (W::CL * 4) + cl * 4, n0 = nl * 4, nc = ch.count - c0;
     const int t0 = s * a.seglen, t1 = min(a.T, t0 + a.seglen);
     const int top = t0 + (t1 - 1 - t0) / TT * TT;
-    fetch<L, true, PACKED>(a, sm, ch, b, top, t0, t1, 0);
+    const Tiles<T, L, true, PACKED> tiles(a, sm, &sm + 1, ch, b, t0, t1);
+    tiles.fetch(top, 0);
     for (int i = tid; i < W::CB; i += W::NT) sm.bias[i] = (a.bias && i < ch.count) ? a.bias[ch.first + i] : 0.f;
     State A2, back;
     load_rows(a, a.A + (long long)(ch.first + c0) * a.N, nc, n0, A2, LOG2E);
@@ -173,13 +260,14 @@ __global__ void __launch_bounds__(Bwd<L>::NT, L >= 4 ? 5 : 2) scan_bwd_local_ker
     __syncthreads();
     int buf = 0;
     for (int base = top; base >= t0; base -= TT, buf ^= 1) {
-        fetch<L, true, PACKED>(a, sm, ch, b, base - TT, t0, t1, buf ^ 1);
+        tiles.fetch(base - TT, buf ^ 1);
         copies_wait<1>();
-        stage<T, L, true>(a, sm, ch, base, t1, buf, [](int, int, bool) {});
+        tiles.stage(base, buf, nullptr);
         __syncthreads();
+        auto tokens = [&](auto edged) {
 #pragma unroll 4
         for (int j = TT - 1; j >= 0; --j) {
-            if (PACKED) {
+            if (edged.value) {
                 const int n = sm.last[buf][j];
                 if (n >= 0) {
                     cut = true;
@@ -200,6 +288,11 @@ __global__ void __launch_bounds__(Bwd<L>::NT, L >= 4 ? 5 : 2) scan_bwd_local_ker
             sum_lo = add2(sum_lo, d.lo);
             sum_hi = add2(sum_hi, d.hi);
         }
+        };
+        if (PACKED && sm.any[buf])
+            tokens(Flag<PACKED>());
+        else
+            tokens(Flag<false>());
         __syncthreads();
     }
     copies_wait<0>();
@@ -228,7 +321,8 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
     const int c0 = warp * (W::CL * 4) + cl * 4, n0 = nl * 4, nc = ch.count - c0;
     const int t0 = s * a.seglen, t1 = min(a.T, t0 + a.seglen);
     const int top = t0 + (t1 - 1 - t0) / TT * TT;
-    const int vc = (tid % W::VROW) * 8, vt = tid / W::VROW, vn = ch.count - vc;
+    const Tiles<T, L, false, PACKED> tiles(a, sm, &sm + 1, ch, b, t0, t1);
+    const int vc = tiles.vc, vt = tiles.vt, vn = tiles.vn;
     if (PACKED && blockIdx.x == 0) check_cu(a.cu, a.nseq, a.T, a.err);
 
     // the saved state before the tile at `base`, into the last group's slot (free once that group is done)
@@ -241,7 +335,7 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
         }
     };
     fetch_state(top);
-    fetch<L, false, PACKED>(a, sm, ch, b, top, t0, t1, 0);
+    tiles.fetch(top, 0);
     for (int i = tid; i < W::CB; i += NT) sm.bias[i] = (a.bias && i < ch.count) ? a.bias[ch.first + i] : 0.f;
 
     f2 dbias[4] = {0ull, 0ull, 0ull, 0ull};
@@ -273,13 +367,10 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
     int buf = 0;
     for (int base = top; base >= t0; base -= TT, buf ^= 1) {
         copies_wait<0>();
-        stage<T, L, false>(a, sm, ch, base, t1, buf, [&](int j, int c, bool in) {
-            f2 x[4] = {0ull, 0ull, 0ull, 0ull};
-            if (in) widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][3][j][c]), x);
-            put8(&sm.x[j][c], x);
-        });
-        fetch<L, false, PACKED>(a, sm, ch, b, base - TT, t0, t1, buf ^ 1);
+        tiles.stage(base, buf, sm.x);
+        tiles.fetch(base - TT, buf ^ 1);
         __syncthreads();
+        auto tile = [&](auto edged) {
         // forward over the tile: the state before every group of SB tokens
         {
             State h;
@@ -296,7 +387,7 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
 #pragma unroll
                 for (int i = 0; i < SB; ++i) {
                     const int j = grp * SB + i;
-                    if (PACKED && sm.first[buf][j] >= 0) initial(sm.first[buf][j], h);
+                    if (edged.value && sm.first[buf][j] >= 0) initial(sm.first[buf][j], h);
                     const F2x2 d = lds_f2x2(&sm.delta[j][c0]), x = lds_f2x2(&sm.x[j][c0]);
                     const f2 u_lo = mul2(d.lo, x.lo), u_hi = mul2(d.hi, x.hi);
                     f2 bb[4];
@@ -326,7 +417,7 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
                     from[n][0] = i ? hs[i ? i - 1 : 0][n][0] : h0[n][0];
                     from[n][1] = i ? hs[i ? i - 1 : 0][n][1] : h0[n][1];
                 }
-                if (PACKED && sm.first[buf][j] >= 0) initial(sm.first[buf][j], from);
+                if (edged.value && sm.first[buf][j] >= 0) initial(sm.first[buf][j], from);
                 const F2x2 d = lds_f2x2(&sm.delta[j][c0]), x = lds_f2x2(&sm.x[j][c0]);
                 const f2 u_lo = mul2(d.lo, x.lo), u_hi = mul2(d.hi, x.hi);
                 f2 y_lo = 0ull, y_hi = 0ull;
@@ -357,7 +448,7 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
                     from[n][0] = i ? hs[i ? i - 1 : 0][n][0] : h0[n][0];
                     from[n][1] = i ? hs[i ? i - 1 : 0][n][1] : h0[n][1];
                 }
-                if (PACKED) {
+                if (edged.value) {
                     if (sm.first[buf][j] >= 0) initial(sm.first[buf][j], from);
                     const int n = sm.last[buf][j];
                     if (n >= 0) {
@@ -407,7 +498,7 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
                         dskip[e] = fmaf(gv, xv, dskip[e]);
                     }
                 }
-                if (PACKED && sm.first[buf][j] >= 0 && a.dstate_in)
+                if (edged.value && sm.first[buf][j] >= 0 && a.dstate_in)
                     store_rows(a, a.dstate_in + ((long long)sm.first[buf][j] * a.D + ch.first + c0) * a.N, nc, n0, back);
                 if (i & 1) continue;
                 // the warp's sums of dB and dC over its channel lanes, two tokens at a time: 4 columns of one a lane
@@ -426,37 +517,65 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
                 __syncwarp();
             }
         }
+        };
+        if (PACKED && sm.any[buf])
+            tile(Flag<PACKED>());
+        else
+            tile(Flag<false>());
         __syncthreads();
         // the tile's outputs
+        auto through_softplus = [&](f2 v, f2 raw_dt, f2 bias) { return a.softplus ? mul2(v, sigmoid2(add2(raw_dt, bias))) : v; };
+        auto through_gate = [&](f2 yp, f2 dy, f2 z) {  // yp dy sig (1 + z (1 - sig))
+            const f2 sg = sigmoid2(z);
+            return mul2(mul2(yp, dy), mul2(sg, fma2(z, fma2(sg, both(-1.f), both(1.f)), both(1.f))));
+        };
+        if (tiles.vec) {
 #pragma unroll
-        for (int k = 0; k < W::VPT; ++k) {
-            const int j = vt + k * W::VSTEP, t = base + j;
-            if (j >= TT || t >= t1 || vn <= 0) continue;
-            const long long at = ((long long)b * a.T + t) * a.D + ch.first + vc;
-            f2 v[4], r[4], o[4];
-            get8(&sm.x[j][vc], v);
-            store8(static_cast<uint16_t *>(a.dx) + at, narrow8<T>(v), vn, a.vec);
-            get8(&sm.delta[j][vc], v);
-            if (a.softplus) {
-                widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][0][j][vc]), r);
+            for (int k = 0; k < W::VPT; ++k) {
+                const int j = vt + k * W::VSTEP, t = base + j;
+                if (j >= TT || t >= t1 || vn <= 0) continue;
+                const long long at = ((long long)b * a.T + t) * a.D + ch.first + vc;
+                f2 v[4], r[4], o[4];
+                get8(&sm.x[j][vc], v);
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dx) + at) = narrow8<T>(v);
+                get8(&sm.delta[j][vc], v);
+                widen8<T>(*reinterpret_cast<const uint4 *>(tiles.raw(buf, 0, j, true) + vc), r);
                 get8(&sm.bias[vc], o);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], sigmoid2(add2(r[i], o[i])));
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dbias[i] = add2(dbias[i], v[i]);
-            store8(static_cast<uint16_t *>(a.ddt) + at, narrow8<T>(v), vn, a.vec);
-            if (a.dz) {
-                get8(&sm.gy[j][vc], v);
-                widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][1][j][vc]), o);
-                widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][2][j][vc]), r);
-#pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const f2 sg = sigmoid2(r[i]);  // yp dy sig (1 + z (1 - sig))
-                    v[i] = mul2(mul2(v[i], o[i]), mul2(sg, fma2(r[i], fma2(sg, both(-1.f), both(1.f)), both(1.f))));
+                    v[i] = through_softplus(v[i], r[i], o[i]);
+                    dbias[i] = add2(dbias[i], v[i]);
                 }
-                store8(static_cast<uint16_t *>(a.dz) + at, narrow8<T>(v), vn, a.vec);
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.ddt) + at) = narrow8<T>(v);
+                if (a.dz) {
+                    get8(&sm.gy[j][vc], v);
+                    widen8<T>(*reinterpret_cast<const uint4 *>(tiles.raw(buf, 1, j, true) + vc), o);
+                    widen8<T>(*reinterpret_cast<const uint4 *>(tiles.raw(buf, 2, j, true) + vc), r);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = through_gate(v[i], o[i], r[i]);
+                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.dz) + at) = narrow8<T>(v);
+                }
             }
+        } else {
+            const long long at0 = ((long long)b * a.T + base) * a.D + ch.first;
+            tiles.each_pair([&](int j, int c, int k) {
+                const bool in0 = c < ch.count && base + j < t1, in1 = c < ch.count && base + j + 1 < t1;
+                const long long p0 = at0 + (long long)j * a.D + c, p1 = p0 + a.D;
+                auto put = [&](void *to, f2 v) {
+                    const uint32_t w = narrow2<T>(v);
+                    if (in0) static_cast<uint16_t *>(to)[p0] = (uint16_t)w;
+                    if (in1) static_cast<uint16_t *>(to)[p1] = (uint16_t)(w >> 16);
+                };
+                put(a.dx, pack2(sm.x[j][c], sm.x[j + 1][c]));
+                f2 v = through_softplus(pack2(sm.delta[j][c], sm.delta[j + 1][c]), tiles.pair_of(buf, 0, base, j, c), both(sm.bias[c]));
+                put(a.ddt, v);
+                float v0, v1;
+                unpack2(v, v0, v1);
+                dbias[k % W::NCOL * W::PL + k / W::NCOL] =
+                    add2(dbias[k % W::NCOL * W::PL + k / W::NCOL], pack2(in0 ? v0 : 0.f, in1 ? v1 : 0.f));
+                if (a.dz)
+                    put(a.dz, through_gate(pack2(sm.gy[j][c], sm.gy[j + 1][c]), tiles.pair_of(buf, 1, base, j, c), tiles.pair_of(buf, 2, base, j, c)));
+            });
         }
         for (int i = tid; i < TT * 2 * NP / 4; i += NT) {
             const int j = i / (2 * NP / 4), col = (i % (2 * NP / 4)) * 4, t = base + j;
@@ -483,14 +602,22 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
         for (int e = 0; e < R; ++e)
             if (own + e < ch.count) param[a.dD_at + ch.first + own + e] = dskip[e];
     if (a.dbias_at >= 0) {
-        // threads of one vector column, added in order
+        // the threads that share a channel, added in order
         __syncthreads();
-        float *buf8 = &sm.delta[0][0];                   // 8 floats of each thread that holds vectors
-        if (vt < TT) put8(buf8 + tid * 8, dbias);
+        float *part8 = &sm.delta[0][0];
+        if (tiles.vec) {
+            if (vt < TT) put8(part8 + vt * W::CB + vc, dbias);
+        } else {
+#pragma unroll
+            for (int k = 0; k < W::GROUP; ++k) {
+                const int i = warp + W::NW * k, j = i / W::COLS * 2, c = i % W::COLS * 32 + lane;
+                unpack2(dbias[k % W::NCOL * W::PL + k / W::NCOL], part8[j * W::CB + c], part8[(j + 1) * W::CB + c]);
+            }
+        }
         __syncthreads();
         for (int c = tid; c < W::CB; c += NT) {
             float v = 0.f;
-            for (int k = c / 8; k < (W::NVEC < NT ? W::NVEC : NT); k += W::VROW) v += buf8[k * 8 + c % 8];
+            for (int k = 0; k < W::CLS; ++k) v += part8[k * W::CB + c];
             if (c < ch.count) param[a.dbias_at + ch.first + c] = v;
         }
     }
@@ -527,10 +654,11 @@ cudaError_t launch_smem(K k, long long blocks, int threads, size_t smem, cudaStr
 template <typename T, int L>
 cudaError_t launch_l(const ScanArgs &a, bool full, cudaStream_t s) {
     const long long blocks = (long long)a.gblocks * a.G * (full ? a.nseg : a.nseg - 1) * a.B;
+    const size_t full_smem = sizeof(BwdFull<L>) + raw_bytes<L, false>(a.vec, a.vec_bc);
     if (full)
-        return a.cu ? launch_smem(scan_bwd_kernel<T, L, true>, blocks, Bwd<L>::NT, sizeof(BwdFull<L>), s, a)
-                    : launch_smem(scan_bwd_kernel<T, L, false>, blocks, Bwd<L>::NT, sizeof(BwdFull<L>), s, a);
-    const size_t smem = sizeof(BwdSmem<L, true>);
+        return a.cu ? launch_smem(scan_bwd_kernel<T, L, true>, blocks, Bwd<L>::NT, full_smem, s, a)
+                    : launch_smem(scan_bwd_kernel<T, L, false>, blocks, Bwd<L>::NT, full_smem, s, a);
+    const size_t smem = sizeof(BwdStage<L, true>) + raw_bytes<L, true>(a.vec, a.vec_bc);
     return a.cu ? launch_smem(scan_bwd_local_kernel<T, L, true>, blocks, Bwd<L>::NT, smem, s, a)
                 : launch_smem(scan_bwd_local_kernel<T, L, false>, blocks, Bwd<L>::NT, smem, s, a);
 }
@@ -546,16 +674,5 @@ cudaError_t launch_t(const ScanArgs &a, int L, bool full, cudaStream_t s) {
 }
 
 }  // namespace
-
-cudaError_t launch_scan_bwd(const ScanArgs &a, int L, bool bf16, bool full, cudaStream_t s) {
-    return bf16 ? launch_t<__nv_bfloat16>(a, L, full, s) : launch_t<__half>(a, L, full, s);
-}
-
-cudaError_t launch_scan_dbc(const ScanArgs &a, int L, bool bf16, cudaStream_t s) {
-    const long long blocks = ((long long)a.B * a.T * a.G * 8 * L + 255) / 256;
-    if (bf16) return launch_plain(scan_dbc_kernel<__nv_bfloat16>, dim3((unsigned)blocks), dim3(256), 0, s, a, 4 * L);
-    return launch_plain(scan_dbc_kernel<__half>, dim3((unsigned)blocks), dim3(256), 0, s, a, 4 * L);
-}
-
 }  // namespace scan
 }  // namespace gdr

@@ -29,17 +29,29 @@ struct Fwd {
     static constexpr int BPT = BVEC > 128 ? BVEC / 128 : 1;
 };
 
-// The raw tiles (two of each: the next one is on its way while one is worked on) are private to the threads that copy
-// them, but for B and C; so are, but for the recurrence in between, the staged elements of a vector.
+// The staged tile, and behind it in dynamic shared memory the raw ones (two of each: the next one is on its way while
+// one is worked on): dt, x, z as [TT][row] with rows of CB elements, or CB + 8 where they are copied as pieces, and in
+// that case B and C once more as pieces.  Where rows allow whole vectors a thread copies, stages and stores the same
+// elements, and no other thread touches its part of the raw tiles, but for B and C.
 template <int L, bool FULL>
 struct FwdSmem {
     using F = Fwd<L>;
-    uint16_t raw[2][FULL ? 3 : 2][F::TT][F::CB];        // dt, x, z
-    uint16_t raw_bc[2][FULL ? 2 : 1][F::TT][F::NP];
+    static constexpr int M = FULL ? 3 : 2, MB = FULL ? 2 : 1, RB = F::NP < 8 ? 16 : F::NP + 8;
+    uint16_t raw_bc[2][MB][F::TT][F::NP];
     float delta[F::TT][F::CB];
     float u[F::TT][F::CB];                              // delta x; then the output of the recurrence
     float bias[F::CB], skip[F::CB];
-    int first[2][F::TT], last[2][F::TT];
+    int first[2][F::TT], last[2][F::TT], any[4];
+    static __host__ __device__ constexpr int row(bool vec) { return vec ? F::CB : F::CB + 8; }
+    __device__ __forceinline__ uint16_t *raw(int buf, int m, int j, bool vec) {
+        return reinterpret_cast<uint16_t *>(this + 1) + ((buf * M + m) * F::TT + j) * row(vec);
+    }
+    __device__ __forceinline__ uint16_t *rag_bc(int buf, int m, int j, bool vec) {
+        return raw(2, 0, 0, vec) + ((buf * MB + m) * F::TT + j) * RB;
+    }
+    static size_t bytes(bool vec, bool vec_bc) {
+        return sizeof(FwdSmem) + sizeof(uint16_t) * (2 * M * F::TT * row(vec) + (vec_bc ? 0 : 2 * MB * F::TT * RB));
+    }
 };
 
 // FULL: the outputs (second pass, or the only one).  Otherwise the first pass over segments.
@@ -67,53 +79,64 @@ __global__ void __launch_bounds__(128, FULL ? 5 : 6) scan_fwd_kernel(const ScanA
     const int vc = (tid % VROW) * 8, vt = tid / VROW, vn = ch.count - vc;
     const int bn = (tid % BROW) * 8, bt = tid / BROW;
     const bool vlive = F::NVEC >= 128 || tid < F::NVEC;
+    const bool vec = a.vec, vec_bc = a.vec_bc;
     const long long row0 = (long long)b * a.T;
     for (int i = tid; i < CB; i += 128) {
         sm.bias[i] = (a.bias && i < ch.count) ? a.bias[ch.first + i] : 0.f;
         sm.skip[i] = (a.skip && i < ch.count) ? a.skip[ch.first + i] : 0.f;
     }
+    const Rows src[3] = {{static_cast<const uint16_t *>(a.dt), a.dt_ld, ch.first, (long long)a.B * a.T, a.D},
+                         {static_cast<const uint16_t *>(a.x), a.x_ld, ch.first, (long long)a.B * a.T, a.D},
+                         {static_cast<const uint16_t *>(a.z), a.z_ld, ch.first, (long long)a.B * a.T, a.D}};
+    const Rows src_bc[2] = {{static_cast<const uint16_t *>(a.Bm), a.b_ld, ch.g * a.N, (long long)a.B * a.T, a.G * a.N},
+                            {static_cast<const uint16_t *>(a.Cm), a.c_ld, ch.g * a.N, (long long)a.B * a.T, a.G * a.N}};
+    const int tensors = FULL && a.z ? 3 : 2;
     auto fetch = [&](int base, int buf) {
         if (base < t1) {
+            const int rows = min(TT, t1 - base);
+            if (vec) {
 #pragma unroll
-            for (int k = 0; k < F::VPT; ++k) {
-                const int j = vt + k * VSTEP, t = base + j;
-                if (vlive && t < t1 && vn > 0) {
-                    const long long row = row0 + t;
-                    const int c = ch.first + vc;
-                    copy8(&sm.raw[buf][0][j][vc], static_cast<const uint16_t *>(a.dt) + row * a.dt_ld + c, vn, a.vec);
-                    copy8(&sm.raw[buf][1][j][vc], static_cast<const uint16_t *>(a.x) + row * a.x_ld + c, vn, a.vec);
-                    if (FULL && a.z)
-                        copy8(&sm.raw[buf][FULL ? 2 : 0][j][vc], static_cast<const uint16_t *>(a.z) + row * a.z_ld + c, vn, a.vec);
+                for (int k = 0; k < F::VPT; ++k) {
+                    const int j = vt + k * VSTEP;
+                    if (vlive && j < rows && vn > 0)
+#pragma unroll
+                        for (int m = 0; m < (FULL ? 3 : 2); ++m)
+                            if (m < tensors) copy8(sm.raw(buf, m, j, true) + vc, src[m].at(row0 + base + j) + vc, vn, true);
                 }
+            } else {
+#pragma unroll
+                for (int m = 0; m < (FULL ? 3 : 2); ++m)
+                    if (m < tensors)
+                        copy_rows<128, CB / 8 + 1>(sm.raw(buf, m, 0, false), sm.row(false), src[m], row0 + base, rows, ch.count);
             }
 #pragma unroll
-            for (int k = 0; k < F::BPT; ++k) {
-                const int j = bt + k * BSTEP, t = base + j;
-                if (j >= TT) break;
-                if (t < t1) {
-                    const long long row = row0 + t;
-                    const int at = ch.g * a.N + bn;
-                    const uint16_t *pb = static_cast<const uint16_t *>(a.Bm) + row * a.b_ld + at;
-                    const uint16_t *pc = static_cast<const uint16_t *>(a.Cm) + row * a.c_ld + at;
-                    if constexpr (BW == 8) {
-                        copy8(&sm.raw_bc[buf][0][j][bn], pb, a.N - bn, a.vec_bc);
-                        if (FULL) copy8(&sm.raw_bc[buf][FULL ? 1 : 0][j][bn], pc, a.N - bn, a.vec_bc);
-                    } else {
-                        for (int n = 0; n < BW; ++n) {
-                            sm.raw_bc[buf][0][j][n] = n < a.N ? pb[n] : (uint16_t)0;
-                            if (FULL) sm.raw_bc[buf][FULL ? 1 : 0][j][n] = n < a.N ? pc[n] : (uint16_t)0;
-                        }
-                    }
-                } else {  // past the end: zeros
-                    for (int n = 0; n < BW; n += 4) {
-                        *reinterpret_cast<uint2 *>(&sm.raw_bc[buf][0][j][bn + n]) = make_uint2(0, 0);
-                        if (FULL) *reinterpret_cast<uint2 *>(&sm.raw_bc[buf][FULL ? 1 : 0][j][bn + n]) = make_uint2(0, 0);
+            for (int m = 0; m < (FULL ? 2 : 1); ++m) {
+                if (!vec_bc) {
+                    copy_rows<128, NP / 8 + 2>(sm.rag_bc(buf, m, 0, vec), sm.RB, src_bc[m], row0 + base, rows, a.N);
+                } else if constexpr (BW == 8) {
+#pragma unroll
+                    for (int k = 0; k < F::BPT; ++k) {
+                        const int j = bt + k * BSTEP;
+                        if (j < rows)
+                            copy8(&sm.raw_bc[buf][m][j][bn], src_bc[m].at(row0 + base + j) + bn, a.N - bn, true);
+                        else if (j < TT)  // past the end: zeros
+                            *reinterpret_cast<uint4 *>(&sm.raw_bc[buf][m][j][bn]) = make_uint4(0, 0, 0, 0);
                     }
                 }
             }
-            if (PACKED && tid < TT) edges(a, base + tid, t1, sm.first[buf][tid], sm.last[buf][tid]);
+            if (PACKED) tile_edges<TT>(a, base, t1, sm.first[buf], sm.last[buf], &sm.any[buf]);
         }
         copies_commit();
+    };
+    // Pairs of tokens of one channel, for the ragged rows: consecutive lanes take consecutive channels.
+    auto each_pair = [&](auto &&f) {
+        constexpr int COLS = CB / 32;
+        for (int i = warp; i < TT / 2 * COLS; i += 4) f(i / COLS * 2, i % COLS * 32 + lane);
+    };
+    auto pair_of = [&](int buf, int m, int base, int j, int c) {
+        const uint16_t lo = sm.raw(buf, m, j, false)[src[m].skew(row0 + base + j) + c];
+        const uint16_t hi = sm.raw(buf, m, j + 1, false)[src[m].skew(row0 + base + j + 1) + c];
+        return widen2<T>((uint32_t)lo | (uint32_t)hi << 16);
     };
     fetch(t0, 0);
 
@@ -134,36 +157,60 @@ __global__ void __launch_bounds__(128, FULL ? 5 : 6) scan_fwd_kernel(const ScanA
     for (int base = t0; base < t1; base += TT, buf ^= 1) {
         fetch(base + TT, buf ^ 1);
         copies_wait<1>();
+        if (!(vec && vec_bc)) __syncthreads();
         // stage the tile
+        if (vec) {
 #pragma unroll
-        for (int k = 0; k < F::VPT; ++k) {
-            if (!vlive) continue;
-            const int j = vt + k * VSTEP;
-            f2 x[4], d[4], bias[4];
-            if (base + j < t1 && vn > 0) {
-                widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][0][j][vc]), d);
-                widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][1][j][vc]), x);
-                get8(&sm.bias[vc], bias);
+            for (int k = 0; k < F::VPT; ++k) {
+                if (!vlive) continue;
+                const int j = vt + k * VSTEP;
+                f2 x[4], d[4], bias[4];
+                if (base + j < t1 && vn > 0) {
+                    widen8<T>(*reinterpret_cast<const uint4 *>(sm.raw(buf, 0, j, true) + vc), d);
+                    widen8<T>(*reinterpret_cast<const uint4 *>(sm.raw(buf, 1, j, true) + vc), x);
+                    get8(&sm.bias[vc], bias);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    d[i] = add2(d[i], bias[i]);
-                    if (a.softplus) d[i] = softplus2(d[i]);
-                    x[i] = mul2(d[i], x[i]);
+                    for (int i = 0; i < 4; ++i) {
+                        d[i] = add2(d[i], bias[i]);
+                        if (a.softplus) d[i] = softplus2(d[i]);
+                        x[i] = mul2(d[i], x[i]);
+                    }
+                } else {  // past the end: a step of zero, which changes nothing
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) d[i] = x[i] = 0ull;
                 }
-            } else {  // past the end: a step of zero, which changes nothing
-#pragma unroll
-                for (int i = 0; i < 4; ++i) d[i] = x[i] = 0ull;
+                put8(&sm.delta[j][vc], d);
+                put8(&sm.u[j][vc], x);
             }
-            put8(&sm.delta[j][vc], d);
-            put8(&sm.u[j][vc], x);
+        } else {
+            each_pair([&](int j, int c) {
+                f2 d = add2(pair_of(buf, 0, base, j, c), both(sm.bias[c]));
+                if (a.softplus) d = softplus2(d);
+                const f2 u = mul2(d, pair_of(buf, 1, base, j, c));
+                float d0, d1, u0, u1;
+                unpack2(d, d0, d1);
+                unpack2(u, u0, u1);
+                const bool in0 = c < ch.count && base + j < t1, in1 = c < ch.count && base + j + 1 < t1;
+                sm.delta[j][c] = in0 ? d0 : 0.f, sm.delta[j + 1][c] = in1 ? d1 : 0.f;
+                sm.u[j][c] = in0 ? u0 : 0.f, sm.u[j + 1][c] = in1 ? u1 : 0.f;
+            });
+        }
+        if (!vec_bc) {
+#pragma unroll
+            for (int m = 0; m < (FULL ? 2 : 1); ++m)
+                for (int i = tid; i < TT * NP; i += 128) {
+                    const int j = i / NP, n = i % NP;
+                    sm.raw_bc[buf][m][j][n] = base + j < t1 && n < a.N ? sm.rag_bc(buf, m, j, vec)[src_bc[m].skew(row0 + base + j) + n] : (uint16_t)0;
+                }
         }
         __syncthreads();
         if (FULL && a.saved && base % SAVE == 0)
             store_padded(a.saved + (((long long)b * ((a.T + SAVE - 1) / SAVE) + base / SAVE) * NP + n0) * a.DP + ch.pad + c0,
                          a.DP, h);
+        auto tokens = [&](auto edged) {
 #pragma unroll 4
         for (int j = 0; j < TT; ++j) {
-            if (PACKED) {
+            if (edged.value) {
                 const int n = sm.first[buf][j];
                 if (n >= 0) {
                     cut = true;
@@ -197,32 +244,50 @@ __global__ void __launch_bounds__(128, FULL ? 5 : 6) scan_fwd_kernel(const ScanA
                 sum_lo = add2(sum_lo, d.lo);
                 sum_hi = add2(sum_hi, d.hi);
             }
-            if (PACKED && FULL) {
+            if (edged.value && FULL) {
                 const int n = sm.last[buf][j];
                 if (n >= 0 && a.state_out)
                     store_rows(a, a.state_out + ((long long)n * a.D + ch.first + c0) * a.N, nc, n0, h);
             }
         }
+        };
+        if (PACKED && sm.any[buf])
+            tokens(Flag<PACKED>());
+        else
+            tokens(Flag<false>());
         __syncthreads();
-        if (FULL) {
+        if (FULL && vec) {
 #pragma unroll
             for (int k = 0; k < F::VPT; ++k) {
                 const int j = vt + k * VSTEP, t = base + j;
                 if (!vlive || t >= t1 || vn <= 0) continue;
                 f2 y[4], x[4], z[4], skip[4];
                 get8(&sm.u[j][vc], y);
-                widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][1][j][vc]), x);
+                widen8<T>(*reinterpret_cast<const uint4 *>(sm.raw(buf, 1, j, true) + vc), x);
                 get8(&sm.skip[vc], skip);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) y[i] = fma2(skip[i], x[i], y[i]);
                 if (a.z) {
-                    widen8<T>(*reinterpret_cast<const uint4 *>(&sm.raw[buf][FULL ? 2 : 0][j][vc]), z);
+                    widen8<T>(*reinterpret_cast<const uint4 *>(sm.raw(buf, FULL ? 2 : 0, j, true) + vc), z);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) y[i] = mul2(y[i], mul2(z[i], sigmoid2(z[i])));
                 }
-                store8(static_cast<uint16_t *>(a.y) + (row0 + t) * a.D + ch.first + vc, narrow8<T>(y), vn, a.vec);
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.y) + (row0 + t) * a.D + ch.first + vc) = narrow8<T>(y);
             }
+        } else if (FULL) {
+            uint16_t *out = static_cast<uint16_t *>(a.y) + (row0 + base) * a.D + ch.first;
+            each_pair([&](int j, int c) {
+                f2 y = fma2(both(sm.skip[c]), pair_of(buf, 1, base, j, c), pack2(sm.u[j][c], sm.u[j + 1][c]));
+                if (a.z) {
+                    const f2 z = pair_of(buf, FULL ? 2 : 0, base, j, c);
+                    y = mul2(y, mul2(z, sigmoid2(z)));
+                }
+                const uint32_t w = narrow2<T>(y);
+                if (c < ch.count && base + j < t1) out[(long long)j * a.D + c] = (uint16_t)w;
+                if (c < ch.count && base + j + 1 < t1) out[(long long)(j + 1) * a.D + c] = (uint16_t)(w >> 16);
+            });
         }
+        if (!vec) __syncthreads();  // (the next copies go where other threads have read)
     }
     copies_wait<0>();
     if (FULL) {
@@ -292,7 +357,7 @@ cudaError_t launch_one(const ScanArgs &a, cudaStream_t s) {
     const int segs = FULL ? a.nseg : a.nseg - 1;
     const long long blocks = (long long)a.gblocks * a.G * segs * a.B;
     auto k = scan_fwd_kernel<T, L, FULL, PACKED>;
-    const size_t smem = sizeof(FwdSmem<L, FULL>);
+    const size_t smem = FwdSmem<L, FULL>::bytes(a.vec, a.vec_bc);
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
