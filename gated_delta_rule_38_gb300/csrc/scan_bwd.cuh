@@ -379,6 +379,7 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
                 const F2x2 v = lds_f2x2(sm.start[TT / SB - 1][n][tid]);
                 h[n][0] = v.lo, h[n][1] = v.hi;
             }
+#pragma unroll 1  // (the tile's code is to stay in the instruction cache)
             for (int grp = 0; grp < TT / SB; ++grp) {
 #pragma unroll
                 for (int n = 0; n < 4; ++n)
@@ -400,6 +401,7 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
                 }
             }
         }
+#pragma unroll 1
         for (int grp = TT / SB - 1; grp >= 0; --grp) {
             State h0, dec[SB], hs[SB];                   // state before the group; a_t and h_t of its tokens
             float yp[SB][R];
