@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(256, 2) scan_step_kernel(const ScanArgs a, int
         float h[RB][4];
 #pragma unroll
         for (int r = 0; r < RB; ++r) {
-            const float4 f = ring[slot][r][tid];
+            const float4 f = mine ? ring[slot][r][tid] : make_float4(0.f, 0.f, 0.f, 0.f);  // (padded states stay zero)
             h[r][0] = f.x, h[r][1] = f.y, h[r][2] = f.z, h[r][3] = f.w;
         }
         copy_group(b + AHEAD * RB, slot);
