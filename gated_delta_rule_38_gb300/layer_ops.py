@@ -68,6 +68,8 @@ def rms_norm_fwd(x, weight, residual=None, eps=1e-6, quant=None, scale_group=0, 
     if scale_group not in (0, 128):
         raise ValueError(f"scale_group is {scale_group}, expected 0 or 128")
     x, ld = _rows(x)
+    if D % 8 == 0 and (ld % 8 or x.data_ptr() % 16):  # a copy takes the whole-vector form, whose bits are those of any
+        x, ld = x.contiguous(), D                     # other view's
     yt = torch.float8_e4m3fn if quant else x.dtype
     _check(out, "out", x.shape, yt, x, optional=True)
     y = out if out is not None else torch.empty(x.shape, dtype=yt, device=x.device)

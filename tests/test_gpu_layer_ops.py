@@ -44,7 +44,7 @@ def test_error_word_clear():
 
 # ---------------------------------------------------------------- RMS norm
 
-NORM_D = [1, 7, 8, 100, 128, 136, 333, 1024, 1031, 4096, 8192, 8200, 12289, 16384]
+NORM_D = [1, 7, 8, 100, 128, 136, 333, 1024, 1031, 4096, 8185, 8186, 8192, 8200, 12289, 16377, 16378, 16383, 16384]
 
 
 @DT
