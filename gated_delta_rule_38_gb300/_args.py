@@ -39,6 +39,17 @@ def _check(t, name, shape=None, dtype=None, like=None, optional=False, contiguou
         raise ValueError(f"{name} must be contiguous")
 
 
+def _need(t, name, shape, dtype, like, contiguous=True):
+    """_check of a required tensor with everything given: one quick test, and _check for the message when it fails."""
+    try:
+        ok = t.shape == shape and t.dtype == dtype and t.get_device() == like.get_device() and (
+            not contiguous or t.is_contiguous())
+    except AttributeError:
+        ok = False
+    if not ok:
+        _check(t, name, shape, dtype, like, contiguous=contiguous)
+
+
 def _check_cu(cu, q):
     if cu is not None:
         _check(cu, "cu_seqlens", (cu.numel(),), torch.int32, q)
@@ -57,11 +68,11 @@ def _cu(cu_seqlens):
 def _rows(t, inner=1):
     """(t, row stride): a tensor whose last ``inner`` dimensions are contiguous and whose rows follow one another at
     one stride (a slice of a fused projection is one); any other view is copied."""
+    if t.is_contiguous():
+        return t, t.shape[-1] if inner == 1 else t.shape[-1] * t.shape[-2]
     n = 1
     for d in t.shape[t.dim() - inner:]:
         n *= d
-    if t.is_contiguous():
-        return t, n
     lead = t.dim() - inner
     want, ok = 1, True
     for i in range(t.dim() - 1, lead - 1, -1):

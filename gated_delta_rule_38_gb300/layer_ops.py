@@ -14,7 +14,7 @@ from ctypes import byref, c_size_t
 import torch
 
 from . import _lib
-from ._args import _DT, _check, _check_cu, _cu, _rows
+from ._args import _DT, _check, _check_cu, _cu, _need, _rows
 
 __all__ = ["rms_norm", "rms_norm_fwd", "rms_norm_bwd", "short_conv", "short_conv_fwd", "short_conv_bwd",
            "short_conv_step", "selective_scan", "selective_scan_fwd", "selective_scan_bwd", "selective_scan_step"]
@@ -29,14 +29,21 @@ def _s(t):
 
 
 def _dt(t, name, allowed):
+    if not isinstance(t, torch.Tensor):
+        _check(t, name)
     if t.dtype not in allowed:
         raise ValueError(f"{name} has dtype {t.dtype}, expected one of {', '.join(str(d) for d in allowed)}")
     return _DT[t.dtype]
 
 
+_HALF = (torch.bfloat16, torch.float16)
+
+
 def _tokens(x, name):
-    _check(x, name, contiguous=False)
-    return _dt(x, name, (torch.bfloat16, torch.float16))
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype in _HALF):
+        _check(x, name, contiguous=False)
+        _dt(x, name, _HALF)
+    return _DT[x.dtype]
 
 
 def _workspace(fn, p, like):
@@ -57,12 +64,12 @@ def rms_norm_fwd(x, weight, residual=None, eps=1e-6, quant=None, scale_group=0, 
     """
     xd = _tokens(x, "x")
     D = x.shape[-1]
-    _check(weight, "weight", (D,), None, x)
     wd = _dt(weight, "weight", (x.dtype, torch.float32))
+    _need(weight, "weight", (D,), weight.dtype, x)
     rd = xd
     if residual is not None:
-        _check(residual, "residual", x.shape, None, x)
         rd = _dt(residual, "residual", (x.dtype, torch.float32))
+        _need(residual, "residual", x.shape, residual.dtype, x)
     if quant not in (None, "e4m3"):
         raise ValueError(f"quant is {quant!r}, expected None or 'e4m3'")
     if scale_group not in (0, 128):
@@ -71,7 +78,8 @@ def rms_norm_fwd(x, weight, residual=None, eps=1e-6, quant=None, scale_group=0, 
     if D % 8 == 0 and (ld % 8 or x.data_ptr() % 16):  # a copy takes the whole-vector form, whose bits are those of any
         x, ld = x.contiguous(), D                     # other view's
     yt = torch.float8_e4m3fn if quant else x.dtype
-    _check(out, "out", x.shape, yt, x, optional=True)
+    if out is not None:
+        _need(out, "out", x.shape, yt, x)
     y = out if out is not None else torch.empty(x.shape, dtype=yt, device=x.device)
     res_out = None if residual is None else torch.empty_like(residual)
     scale = None
@@ -92,14 +100,15 @@ def rms_norm_bwd(h, weight, dy, dresidual=None, eps=1e-6, dtype=None):
     h has that type too, and its fp32 form when h is fp32.
     """
     yd = _tokens(dy, "dy")
-    _check(h, "h", dy.shape, None, dy, contiguous=False)
     hd = _dt(h, "h", (dy.dtype, torch.float32))
+    _need(h, "h", dy.shape, h.dtype, dy, contiguous=False)
     if dtype is not None and dtype != dy.dtype:
         raise ValueError(f"dtype is {dtype}, dy has {dy.dtype}")
     D = h.shape[-1]
-    _check(weight, "weight", (D,), None, h)
     wd = _dt(weight, "weight", (dy.dtype, torch.float32))
-    _check(dresidual, "dresidual", h.shape, h.dtype, h, optional=True)
+    _need(weight, "weight", (D,), weight.dtype, h)
+    if dresidual is not None:
+        _need(dresidual, "dresidual", h.shape, h.dtype, h)
     h, ld = _rows(h)
     dy = dy.contiguous()
     dx = torch.empty_like(dy)
@@ -145,11 +154,12 @@ def _conv_problem(x, weight, bias, activation, cu):
     if x.dim() != 3:
         raise ValueError("x must be [B, T, D]")
     B, T, D = x.shape
-    _check(weight, "weight", None, None, x)
+    wd = _dt(weight, "weight", (x.dtype, torch.float32))
     if weight.dim() != 2 or weight.shape[0] != D or not 2 <= weight.shape[1] <= 4:
         raise ValueError(f"weight has shape {tuple(weight.shape)}, expected ({D}, W) with W from 2 to 4")
-    wd = _dt(weight, "weight", (x.dtype, torch.float32))
-    _check(bias, "bias", (D,), weight.dtype, x, optional=True)
+    _need(weight, "weight", weight.shape, weight.dtype, x)
+    if bias is not None:
+        _need(bias, "bias", (D,), weight.dtype, x)
     if activation not in (None, "silu"):
         raise ValueError(f"activation is {activation!r}, expected None or 'silu'")
     _check_cu(cu, x)
@@ -170,8 +180,10 @@ def short_conv_fwd(x, weight, bias=None, activation=None, initial_state=None, ou
     """
     cu = _cu(cu_seqlens)
     p, x, sshape = _conv_problem(x, weight, bias, activation, cu)
-    _check(initial_state, "initial_state", sshape, x.dtype, x, optional=True)
-    _check(out, "out", x.shape, x.dtype, x, optional=True)
+    if initial_state is not None:
+        _need(initial_state, "initial_state", sshape, x.dtype, x)
+    if out is not None:
+        _need(out, "out", x.shape, x.dtype, x)
     y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
     fin = torch.empty(sshape, dtype=x.dtype, device=x.device) if output_final_state else None
     _lib.check(_lib.load().gdr_conv_fwd(byref(p), _p(x), _p(weight), _p(bias), _p(initial_state), _p(y), _p(fin), _s(x)),
@@ -183,8 +195,9 @@ def short_conv_step(x, state, weight, bias=None, activation=None, out=None):
     """y for one new token (or a few) of every row, x [B,T,D]; the cached inputs ``state`` [B,W-1,D] are updated in
     place.  Equals short_conv_fwd over the same tokens."""
     p, x, sshape = _conv_problem(x, weight, bias, activation, None)
-    _check(state, "state", sshape, x.dtype, x)
-    _check(out, "out", x.shape, x.dtype, x, optional=True)
+    _need(state, "state", sshape, x.dtype, x)
+    if out is not None:
+        _need(out, "out", x.shape, x.dtype, x)
     y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
     _lib.check(_lib.load().gdr_conv_step(byref(p), _p(x), _p(weight), _p(bias), _p(state), _p(y), _s(x)), "gdr_conv_step")
     return y
@@ -194,9 +207,11 @@ def short_conv_bwd(x, weight, dy, bias=None, activation=None, initial_state=None
     """(dx, dweight, dbias, dinitial_state); dbias is None without a bias, dinitial_state without an initial state."""
     cu = _cu(cu_seqlens)
     p, x, sshape = _conv_problem(x, weight, bias, activation, cu)
-    _check(dy, "dy", x.shape, x.dtype, x)
-    _check(initial_state, "initial_state", sshape, x.dtype, x, optional=True)
-    _check(dfinal_state, "dfinal_state", sshape, x.dtype, x, optional=True)
+    _need(dy, "dy", x.shape, x.dtype, x)
+    if initial_state is not None:
+        _need(initial_state, "initial_state", sshape, x.dtype, x)
+    if dfinal_state is not None:
+        _need(dfinal_state, "dfinal_state", sshape, x.dtype, x)
     dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     dw = torch.empty_like(weight)
     db = None if bias is None else torch.empty_like(bias)
@@ -238,18 +253,24 @@ def _scan_problem(x, dt, A, B, C, D, z, dt_bias, dt_softplus, cu):
     if x.dim() != 3:
         raise ValueError("x must be [B, T, D]")
     nb, T, width = x.shape
-    _check(dt, "dt", x.shape, x.dtype, x, contiguous=False)
-    _check(z, "z", x.shape, x.dtype, x, optional=True, contiguous=False)
-    _check(A, "A", None, torch.float32, x)
+    for name, t in (("A", A), ("B", B), ("C", C)):
+        if not isinstance(t, torch.Tensor):
+            _check(t, name)
+    _need(dt, "dt", x.shape, x.dtype, x, False)
+    if z is not None:
+        _need(z, "z", x.shape, x.dtype, x, False)
     if A.dim() != 2 or A.shape[0] != width:
         raise ValueError(f"A has shape {tuple(A.shape)}, expected ({width}, N)")
     N = A.shape[1]
-    _check(B, "B", None, x.dtype, x, contiguous=False)
-    if B.dim() != 4 or tuple(B.shape[:2]) != (nb, T) or B.shape[3] != N:
+    _need(A, "A", (width, N), torch.float32, x)
+    if B.dim() != 4:
         raise ValueError(f"B has shape {tuple(B.shape)}, expected ({nb}, {T}, G, {N})")
-    _check(C, "C", B.shape, x.dtype, x, contiguous=False)
-    _check(D, "D", (width,), torch.float32, x, optional=True)
-    _check(dt_bias, "dt_bias", (width,), torch.float32, x, optional=True)
+    _need(B, "B", (nb, T, B.shape[2], N), x.dtype, x, False)
+    _need(C, "C", B.shape, x.dtype, x, False)
+    if D is not None:
+        _need(D, "D", (width,), torch.float32, x)
+    if dt_bias is not None:
+        _need(dt_bias, "dt_bias", (width,), torch.float32, x)
     _check_cu(cu, x)
     x, x_ld = _rows(x)
     dt, dt_ld = _rows(dt)
@@ -275,8 +296,10 @@ def selective_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, dt_softplus
     """
     cu = _cu(cu_seqlens)
     p, x, dt, B, C, z, sshape = _scan_problem(x, dt, A, B, C, D, z, dt_bias, dt_softplus, cu)
-    _check(initial_state, "initial_state", sshape, torch.float32, x, optional=True)
-    _check(out, "out", x.shape, x.dtype, x, optional=True)
+    if initial_state is not None:
+        _need(initial_state, "initial_state", sshape, torch.float32, x)
+    if out is not None:
+        _need(out, "out", x.shape, x.dtype, x)
     lib = _lib.load()
     y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
     fin = torch.empty(sshape, dtype=torch.float32, device=x.device) if output_final_state else None
@@ -293,8 +316,9 @@ def selective_scan_step(x, dt, A, B, C, state, D=None, z=None, dt_bias=None, dt_
     """y for one new token (or a few) of every row; ``state`` [B,D,N] fp32 is updated in place.  Equals
     selective_scan_fwd over the same tokens."""
     p, x, dt, B, C, z, sshape = _scan_problem(x, dt, A, B, C, D, z, dt_bias, dt_softplus, None)
-    _check(state, "state", sshape, torch.float32, x)
-    _check(out, "out", x.shape, x.dtype, x, optional=True)
+    _need(state, "state", sshape, torch.float32, x)
+    if out is not None:
+        _need(out, "out", x.shape, x.dtype, x)
     y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
     _lib.check(_lib.load().gdr_scan_step(byref(p), _p(x), _p(dt), _p(A), _p(B), _p(C), _p(D), _p(z), _p(dt_bias),
                                          _p(state), _p(y), _s(x)), "gdr_scan_step")
@@ -309,9 +333,11 @@ def selective_scan_bwd(x, dt, A, B, C, dy, saved, D=None, z=None, dt_bias=None, 
     others fp32."""
     cu = _cu(cu_seqlens)
     p, x, dt, B, C, z, sshape = _scan_problem(x, dt, A, B, C, D, z, dt_bias, dt_softplus, cu)
-    _check(dy, "dy", x.shape, x.dtype, x)
-    _check(initial_state, "initial_state", sshape, torch.float32, x, optional=True)
-    _check(dfinal_state, "dfinal_state", sshape, torch.float32, x, optional=True)
+    _need(dy, "dy", x.shape, x.dtype, x)
+    if initial_state is not None:
+        _need(initial_state, "initial_state", sshape, torch.float32, x)
+    if dfinal_state is not None:
+        _need(dfinal_state, "dfinal_state", sshape, torch.float32, x)
     _check(saved, "saved", None, torch.uint8, x)
     lib = _lib.load()
     n = c_size_t(0)

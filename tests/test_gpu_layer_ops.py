@@ -510,3 +510,49 @@ def test_profiler_names():
     got = gdr._lib.profile_read()
     gdr._lib.profile_enable(False)
     assert {"norm_fwd", "norm_bwd", "conv_fwd", "conv_bwd", "scan_fwd", "scan_bwd", "reduce"} <= set(got)
+
+
+def test_refusals():
+    """Tensors that do not fit are refused by name before anything is launched."""
+    randn = gen(0)
+    x, w = randn(2, 6, 32, dtype=BF), randn(32, 4, dtype=BF)
+    f = _raises
+    nw = randn(32)
+    f(gdr.rms_norm_fwd, "x", x.float(), nw)
+    f(gdr.rms_norm_fwd, "weight", x, nw[:31])
+    f(gdr.rms_norm_fwd, "weight", x, nw.half())
+    f(gdr.rms_norm_fwd, "residual", x, nw, residual=x[:1])
+    f(gdr.rms_norm_fwd, "quant", x, nw, quant="int8")
+    f(gdr.rms_norm_fwd, "scale_group", x, nw, quant="e4m3", scale_group=64)
+    f(gdr.rms_norm_fwd, "out", x, nw, out=x.float())
+    f(gdr.rms_norm_bwd, "h", x, nw, x[:1])
+    f(gdr.rms_norm_bwd, "dtype", x, nw, x, dtype=FH)
+    f(gdr.short_conv_fwd, "weight", x, w[:31])
+    f(gdr.short_conv_fwd, "weight", x, randn(32, 5, dtype=BF))
+    f(gdr.short_conv_fwd, "bias", x, w, randn(32))
+    f(gdr.short_conv_fwd, "activation", x, w, activation="relu")
+    f(gdr.short_conv_fwd, "initial_state", x, w, initial_state=randn(2, 2, 32, dtype=BF))
+    f(gdr.short_conv_fwd, "B = 1", x, w, cu_seqlens=cu_of((3, 3)))
+    f(gdr.short_conv_step, "state", x, randn(2, 3, 32), w)
+    f(gdr.short_conv_bwd, "dy", x, w, x.transpose(1, 2))
+    s, _, _ = scan_inputs((2, 6, 32, 16, 2, None, True, True, True), BF)
+    a = (s["x"], s["dt"], s["A"], s["B"], s["C"])
+    for i, name in enumerate("x dt A B C".split()):
+        bad = list(a)
+        bad[i] = bad[i].double()
+        f(gdr.selective_scan_fwd, name, *bad)
+        bad[i] = None
+        f(gdr.selective_scan_fwd, name, *bad)
+    f(gdr.selective_scan_fwd, "B", s["x"], s["dt"], s["A"], s["B"][..., :8], s["C"])
+    f(gdr.selective_scan_fwd, "initial_state", *a, initial_state=s["h0"].transpose(1, 2))
+    f(gdr.selective_scan_step, "state", *a, s["h0"].half())
+    f(gdr.selective_scan_bwd, "saved", *a, s["x"], torch.empty(4, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(gdr.GdrError):
+        gdr.selective_scan_fwd(s["x"], s["dt"], randn(32, 80), randn(2, 6, 1, 80, dtype=BF), randn(2, 6, 1, 80, dtype=BF))
+    with pytest.raises(gdr.GdrError):
+        gdr.rms_norm_fwd(randn(2, 16392, dtype=BF), randn(16392))
+
+
+def _raises(fn, match, *a, **k):
+    with pytest.raises(ValueError, match=match):
+        fn(*a, **k)
