@@ -36,8 +36,8 @@ struct Bwd {
     static constexpr int VPT = NVEC > NT ? NVEC / NT : 1;
     static constexpr int VROW = CB / 8, VSTEP = NT / VROW;
     static constexpr int BW = NP >= 8 ? 8 : 4;           // states of a vector of B or C
-    static constexpr int BROW = NP / BW, BSTEP = NT / BROW;
-    static constexpr int BPT = TT > BSTEP ? TT / BSTEP : 1;
+    static constexpr int BROW = NP / BW;
+    static_assert(TT * BROW <= NT, "one vector of B a thread");
     // The ragged rows' elements are taken as pairs of tokens of a channel: task i is the pair (2 (i / COLS), + 1) of 32
     // channels, warp w takes w, w + NW, ..  A lane sums over tokens in GROUP sums that take the tokens in the order of
     // the whole vectors' threads (token modulo CLS), so that both forms give the same bits.
@@ -131,14 +131,10 @@ struct Tiles {
                 if (!vec_bc) {
                     copy_rows<W::NT, W::NP / 8 + 2>(rag_bc(buf, m, 0), S::RB, src_bc(m), row0 + base, rows, a.N);
                 } else if constexpr (W::BW == 8) {
-#pragma unroll
-                    for (int k = 0; k < W::BPT; ++k) {
-                        const int j = bt + k * W::BSTEP;
-                        if (j < rows)
-                            copy8(&sm.raw_bc[buf][m][j][bn], src_bc(m).at(row0 + base + j) + bn, a.N - bn, true);
-                        else if (j < TT)  // past the end: zeros
-                            *reinterpret_cast<uint4 *>(&sm.raw_bc[buf][m][j][bn]) = make_uint4(0, 0, 0, 0);
-                    }
+                    if (bt < rows)
+                        copy8(&sm.raw_bc[buf][m][bt][bn], src_bc(m).at(row0 + base + bt) + bn, a.N - bn, true);
+                    else if (bt < TT)  // past the end: zeros
+                        *reinterpret_cast<uint4 *>(&sm.raw_bc[buf][m][bt][bn]) = make_uint4(0, 0, 0, 0);
                 }
             }
             if (PACKED) tile_edges<TT>(a, base, t1, sm.first[buf], sm.last[buf], &sm.any[buf]);

@@ -25,8 +25,6 @@ struct Fwd {
     static constexpr int TT = L >= 4 ? 16 : 4 * L;      // tokens a tile
     static constexpr int NVEC = TT * CB / 8;            // 8-channel vectors of a tile
     static constexpr int VPT = NVEC > 128 ? NVEC / 128 : 1;
-    static constexpr int BVEC = TT * NP / 8;            // 8-state vectors of a tile's B
-    static constexpr int BPT = BVEC > 128 ? BVEC / 128 : 1;
 };
 
 // The staged tile, and behind it in dynamic shared memory the raw ones (two of each: the next one is on its way while
@@ -73,8 +71,9 @@ __global__ void __launch_bounds__(128, FULL ? 5 : 6) scan_fwd_kernel(const ScanA
     const int t0 = s * a.seglen, t1 = min(a.T, t0 + a.seglen);
     if (PACKED && FULL && blockIdx.x == 0) check_cu(a.cu, a.nseq, a.T, a.err);
 
-    // this thread's vectors of a tile: token vt + k VSTEP, channels vc ..; and of B and C: token bt + k BSTEP, states bn ..
-    constexpr int VROW = CB / 8, VSTEP = 128 / VROW, BROW = NP >= 8 ? NP / 8 : 1, BSTEP = 128 / BROW;
+    // this thread's vectors of a tile: token vt + k VSTEP, channels vc ..; and of B and C: token bt, states bn ..
+    constexpr int VROW = CB / 8, VSTEP = 128 / VROW, BROW = NP >= 8 ? NP / 8 : 1;
+    static_assert(TT * BROW <= 128, "one vector of B a thread");
     constexpr int BW = NP >= 8 ? 8 : 4;                 // states of such a vector
     const int vc = (tid % VROW) * 8, vt = tid / VROW, vn = ch.count - vc;
     const int bn = (tid % BROW) * 8, bt = tid / BROW;
@@ -114,14 +113,10 @@ __global__ void __launch_bounds__(128, FULL ? 5 : 6) scan_fwd_kernel(const ScanA
                 if (!vec_bc) {
                     copy_rows<128, NP / 8 + 2>(sm.rag_bc(buf, m, 0, vec), sm.RB, src_bc[m], row0 + base, rows, a.N);
                 } else if constexpr (BW == 8) {
-#pragma unroll
-                    for (int k = 0; k < F::BPT; ++k) {
-                        const int j = bt + k * BSTEP;
-                        if (j < rows)
-                            copy8(&sm.raw_bc[buf][m][j][bn], src_bc[m].at(row0 + base + j) + bn, a.N - bn, true);
-                        else if (j < TT)  // past the end: zeros
-                            *reinterpret_cast<uint4 *>(&sm.raw_bc[buf][m][j][bn]) = make_uint4(0, 0, 0, 0);
-                    }
+                    if (bt < rows)
+                        copy8(&sm.raw_bc[buf][m][bt][bn], src_bc[m].at(row0 + base + bt) + bn, a.N - bn, true);
+                    else if (bt < TT)  // past the end: zeros
+                        *reinterpret_cast<uint4 *>(&sm.raw_bc[buf][m][bt][bn]) = make_uint4(0, 0, 0, 0);
                 }
             }
             if (PACKED) tile_edges<TT>(a, base, t1, sm.first[buf], sm.last[buf], &sm.any[buf]);
