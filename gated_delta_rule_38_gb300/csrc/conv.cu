@@ -290,6 +290,9 @@ struct Flag {
     static constexpr bool value = V;
 };
 
+// Bound by HBM with the fp32 work of the SiLU close behind (58 % of the issue slots): 2 x 4096 x 12288 bf16 takes 76 us for
+// 403 MB, 5.3 TB/s.  Ragged rows cost three times the instructions an element (2-byte accesses to shared memory and
+// out): 5311 x 4099 fp16 takes 39 us for 87 MB, 2.3 TB/s.
 template <typename T, int W, bool WIDE, bool PACKED>
 __global__ void __launch_bounds__(32 * WALKS, WIDE ? 4 : 3) conv_fwd_kernel(const ConvArgs a) {
     constexpr int U = 4, GROUPS = kAhead / U;   // tokens a group of copies; groups
@@ -372,7 +375,8 @@ __global__ void __launch_bounds__(32 * WALKS, WIDE ? 4 : 3) conv_fwd_kernel(cons
 }
 
 // One row and NC channels a thread for its few tokens: the thread that reads a channel's cached inputs is the one that
-// replaces them.  Few registers, so that a launch with one token keeps the memory busy by its number of threads.
+// replaces them.  Few registers, so that a launch with one token keeps the memory busy by its number of threads.  Bound by
+// the latency of one round of loads a block: 256 x 12288 takes 12.3 us for 50 MB, 4.1 TB/s.
 template <typename T, int W, bool WIDE>
 __global__ void __launch_bounds__(32 * WALKS, 5) conv_step_kernel(const ConvArgs a) {
     Lane<NC, WIDE> l;
@@ -402,6 +406,9 @@ __global__ void __launch_bounds__(32 * WALKS, 5) conv_step_kernel(const ConvArgs
     for (int j = 1; j < W; ++j) store_x<T, NC, WIDE>(a.state_out, (long long)b * (W - 1) + (W - 1 - j), l, xs[j - 1]);
 }
 
+// The sums of dw, db and dx of 4 channels stay in registers (126 a thread): two blocks an SM, which the latency of the
+// SiLU's exponential and reciprocal bounds before HBM does (50 % of the issue slots; three blocks spill 350 bytes a
+// thread).  2 x 4096 x 12288 bf16: 140 us for 604 MB, 4.3 TB/s.
 template <typename T, int W, bool WIDE, bool PACKED>
 __global__ void __launch_bounds__(32 * WALKS, 2) conv_bwd_kernel(const ConvArgs a) {
     constexpr int U = 4, GROUPS = kAhead / U;
@@ -577,8 +584,8 @@ __global__ void __launch_bounds__(32 * WALKS, 2) conv_bwd_kernel(const ConvArgs 
 }
 
 // Tokens a walk.  Long walks repeat fewer overlapping reads and start-ups (worth about 16 tokens a walk), short ones
-// fill the chip; the length that minimises rounds of resident blocks times the tokens of one.  (At 2 x 4096 x 12288
-// the backward takes 5.05 rounds of two blocks an SM with 64 tokens and 2.8 with 120: 147 and 131 us.)
+// fill the chip; the length that minimises rounds of resident blocks times the tokens of one.  (2 x 4096 x 12288:
+// the backward's 120 tokens a walk make 2.8 rounds of two blocks an SM, 64 make 5.05 and cost an eighth more.)
 int conv_tt(const gdr_conv_problem *p, bool bwd) {
     const long long cb = (p->D + 32 * NC - 1) / (32 * NC), slots = (long long)kSMs * (bwd ? 2 : 4);
     long long best = 0;

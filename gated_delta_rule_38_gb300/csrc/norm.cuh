@@ -13,7 +13,7 @@
 // Two forms.  Where every row starts on a 16-byte boundary a thread owns whole vectors of 8 columns.  Otherwise
 // (ragged) a block brings rows into shared memory as the aligned 16-byte pieces that hold them, asynchronously and a
 // row ahead, and a thread owns every TPR-th column, so that lanes side by side read and write side by side.  (7203 x 4381:
-// 150 us with vectors cut at the multiples of 8 elements and weights in shared memory, 167 with single elements.)
+// 82 us; 150 with vectors cut at the multiples of 8 elements and weights in shared memory, 167 with single elements.)
 #pragma once
 
 #include <cuda_fp8.h>
@@ -128,6 +128,8 @@ struct Bounds {
     static constexpr int fwd = BT == 256 ? 3 : 1, bwd = BT == 256 ? 2 : 1;
 };
 
+// 8192 x 4096 bf16: 46 us with a bf16 residual (268 MB, 5.8 TB/s, 86 % of a copy's rate); with an fp32 residual and e4m3
+// output 62 us (369 MB, 5.9 TB/s).
 template <typename T, int NV, int BT, bool QUANT, int RES>
 __global__ void __launch_bounds__(BT, Bounds<NV, BT>::fwd) norm_fwd_kernel(const NormArgs a) {
     constexpr int P = 4 * NV;  // pairs a thread
@@ -248,7 +250,8 @@ __device__ __forceinline__ void sum_slots(const NormArgs &a, const float *slots,
 }
 
 // Each block walks rows and keeps its threads' share of dw in registers; the per-block sums are added by
-// reduce_rows_kernel in a fixed order.
+// reduce_rows_kernel in a fixed order.  8192 x 4096 bf16: 53 us for 201 MB, 3.8 TB/s: two blocks an SM (dw and the held
+// next row take the registers) leave the two sums of a row, each across the block, partly uncovered.
 template <typename T, int NV, int BT, bool F32>
 __global__ void __launch_bounds__(BT, Bounds<NV, BT>::bwd) norm_bwd_kernel(const NormArgs a) {
     constexpr int P = 4 * NV;

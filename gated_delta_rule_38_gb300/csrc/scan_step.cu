@@ -17,7 +17,8 @@ namespace {
 constexpr int RB = 4;      // rows a group
 constexpr int AHEAD = 2;   // groups of states in flight
 
-// ONE: one token a row.
+// ONE: one token a row.  256 x 4096, N = 16, bf16: 32 us for 143 MB, 4.4 TB/s (65 % of a copy's rate), with 57 % of the issue
+// slots taken by the states' arithmetic.  One row of 2048 channels: the launch's latency.
 template <typename T, int NL, bool ONE>
 __global__ void __launch_bounds__(256, 2) scan_step_kernel(const ScanArgs a, int chunk) {
     constexpr int OWN = RB > NL ? RB / NL : 1;  // rows whose scalars a lane computes (lanes past RB repeat them)
