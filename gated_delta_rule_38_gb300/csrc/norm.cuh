@@ -120,12 +120,12 @@ __device__ __forceinline__ float inv_scale(float m, float &scale) {
     return 1.0f / scale;
 }
 
-// Registers: 16 elements a thread leave room for three blocks of 256 an SM (two in the backward) with the weights and
-// the next row's loads held in registers.  Rows over 8,192 take 32 elements a thread and hold neither.
+// Registers: 16 elements a thread leave room for three blocks of 256 an SM with the weights and the next row's loads held
+// in registers.  Rows over 8,192 take 32 elements a thread and hold neither.
 template <int NV, int BT>
 struct Bounds {
     static constexpr bool hold = NV <= 2;
-    static constexpr int fwd = BT == 256 ? 3 : 1, bwd = BT == 256 ? 2 : 1;
+    static constexpr int fwd = BT == 256 ? 3 : 1;
 };
 
 // 8192 x 4096 bf16: 46 us with a bf16 residual (268 MB, 5.8 TB/s, 86 % of a copy's rate); with an fp32 residual and e4m3
@@ -249,59 +249,97 @@ __device__ __forceinline__ void sum_slots(const NormArgs &a, const float *slots,
     }
 }
 
+// A thread's elements of one row of h, of dy and of the gradient that reaches the summed stream from later layers, in
+// places of shared memory that only it uses: vector k of a stage lies at [stage][k][thread].
+template <int NV, int BT, bool F32>
+struct BwdRows {
+    static constexpr int VH = F32 ? 2 : 1;                       // 16-byte vectors of 8 elements of h
+    static constexpr int H = 0, G = NV * VH, E = G + NV;         // where each begins
+    static constexpr int stages = NV <= 2 || !F32 ? 2 : 1;
+    uint4 *mine;
+    int per;                                                     // vectors a stage
+    __device__ __forceinline__ BwdRows(void *smem, bool later) : mine(static_cast<uint4 *>(smem) + threadIdx.x), per(later ? E + NV * VH : E) {}
+    static size_t bytes(bool later) { return (size_t)stages * (later ? E + NV * VH : E) * BT * sizeof(uint4); }
+    __device__ __forceinline__ uint4 *at(int stage, int k) const { return mine + (stage * per + k) * BT; }
+    // `in`: the row exists; else zeros, as past the row's end.
+    template <int V>
+    __device__ __forceinline__ void copy(int stage, int k0, const void *base, long long row_at, int tpr, int t, int D, bool in) const {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (v * tpr + t) * 8;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                uint4 *to = at(stage, k0 + v * V + k);
+                const char *from = static_cast<const char *>(base) + (row_at + c) * (2 * V) + 16 * k;
+                if (in && c < D)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(to)), "l"(from) : "memory");
+                else
+                    *to = make_uint4(0, 0, 0, 0);
+            }
+        }
+    }
+    // the four pairs of vector v
+    template <typename T, int V>
+    __device__ __forceinline__ void get(int stage, int k0, int v, f2 *o) const {
+        const uint4 u = *at(stage, k0 + v * V);
+        if constexpr (V == 1) {
+            o[0] = widen2<T>(u.x), o[1] = widen2<T>(u.y), o[2] = widen2<T>(u.z), o[3] = widen2<T>(u.w);
+        } else {
+            const uint4 x = *at(stage, k0 + v * V + 1);
+            o[0] = pack2(__uint_as_float(u.x), __uint_as_float(u.y)), o[1] = pack2(__uint_as_float(u.z), __uint_as_float(u.w));
+            o[2] = pack2(__uint_as_float(x.x), __uint_as_float(x.y)), o[3] = pack2(__uint_as_float(x.z), __uint_as_float(x.w));
+        }
+    }
+};
+
 // Each block walks rows and keeps its threads' share of dw in registers; the per-block sums are added by
-// reduce_rows_kernel in a fixed order.  8192 x 4096 bf16: 53 us for 201 MB, 3.8 TB/s: two blocks an SM (dw and the held
-// next row take the registers) leave the two sums of a row, each across the block, partly uncovered.
+// reduce_rows_kernel in a fixed order.  The next row comes by asynchronous copies while this one is worked on, and both
+// passes over a row read it from shared memory, so that no registers hold rows.  8192 x 4096 bf16: 52 us for 201 MB, 3.9 TB/s,
+// at two blocks an SM (three, at 80 registers: 56); 2048 x 16384 with a later gradient: 58 us with the reduction for 268 MB
+// (103 with rows in registers, loaded twice).
 template <typename T, int NV, int BT, bool F32>
-__global__ void __launch_bounds__(BT, Bounds<NV, BT>::bwd) norm_bwd_kernel(const NormArgs a) {
-    constexpr int P = 4 * NV;
-    constexpr bool HOLD = Bounds<NV, BT>::hold;
+__global__ void __launch_bounds__(BT, BT > 256 ? 1 : 2) norm_bwd_kernel(const NormArgs a) {
+    using R = BwdRows<NV, BT, F32>;
+    constexpr int P = 4 * NV, VH = R::VH, AHEAD = R::stages - 1;
     __shared__ float2 s_sum[2][16];
-    extern __shared__ __align__(16) float s_slots[];  // with several rows a block: their shares of dw
+    extern __shared__ __align__(16) float s_dyn[];   // the rows; then, with several rows a block, their shares of dw
     const int tpr = a.tpr, slot = threadIdx.x / tpr, t = threadIdx.x & (tpr - 1), D = a.D;
     const int rpb = blockDim.x / tpr, lanes = min(tpr, 32), wpr = tpr >> 5;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float inv_d = 1.0f / (float)D;
     const long long step = (long long)gridDim.x * rpb;
-    RawRow<NV, F32> rh, re;  // h; the gradient that reaches the summed stream from later layers
-    RawRow<NV, false> rg;    // dy
-    auto fetch = [&](long long row) {
-        if (row < a.rows) {
-            rh.load(a.x, row * a.x_ld, tpr, t, D);
-            rg.load(a.dy, row * D, tpr, t, D);
-            if (HOLD && a.res) re.load(a.res, row * D, tpr, t, D);
-        } else {
-            rh.zero();
-            rg.zero();
-            re.zero();
-        }
+    const R rows(s_dyn, a.res != nullptr);
+    auto fetch = [&](long long row, int stage) {
+        const bool in = row < a.rows;
+        rows.template copy<VH>(stage, R::H, a.x, row * a.x_ld, tpr, t, D, in);
+        rows.template copy<1>(stage, R::G, a.dy, row * D, tpr, t, D, in);
+        if (a.res) rows.template copy<VH>(stage, R::E, a.res, row * D, tpr, t, D, in);
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
     };
     long long row = (long long)blockIdx.x * rpb + slot;
-    re.zero();
+    fetch(row, 0);
     f2 w[P], dw[P];
-    if (HOLD) {
-        fetch(row);
-        load_weight<T, NV>(a, t, w);
-    }
+    load_weight<T, NV>(a, t, w);
 #pragma unroll
     for (int i = 0; i < P; ++i) dw[i] = 0ull;
     int parity = 0;
     for (long long r0 = (long long)blockIdx.x * rpb; r0 < a.rows; r0 += step, row += step, parity ^= 1) {
         const bool live = row < a.rows;
-        f2 h[P], g[P], e[P], ss2 = 0ull, sd2 = 0ull;
-        if (!HOLD) {
-            fetch(row);
-            load_weight<T, NV>(a, t, w);
-        }
+        const int stage = AHEAD ? parity : 0;
+        if (AHEAD) fetch(row + step, stage ^ 1);
+        asm volatile("cp.async.wait_group %0;\n" ::"n"(AHEAD) : "memory");
+        f2 ss2 = 0ull, sd2 = 0ull;
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            h[i] = rh.template pair<T>(i);
-            g[i] = rg.template pair<T>(i);
-            if (HOLD) e[i] = re.template pair<T>(i);
-            ss2 = fma2(h[i], h[i], ss2);
-            sd2 = fma2(mul2(g[i], w[i]), h[i], sd2);
+        for (int v = 0; v < NV; ++v) {
+            f2 h[4], g[4];
+            rows.template get<T, VH>(stage, R::H, v, h);
+            rows.template get<T, 1>(stage, R::G, v, g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                ss2 = fma2(h[i], h[i], ss2);
+                sd2 = fma2(mul2(g[i], w[v * 4 + i]), h[i], sd2);
+            }
         }
-        if (HOLD) fetch(row + step);
         float ss = lanes_sum(sum2(ss2), lanes), sd = lanes_sum(sum2(sd2), lanes);
         if (tpr > 32) {
             if (lane == 0) s_sum[parity][warp] = make_float2(ss, sd);
@@ -314,28 +352,33 @@ __global__ void __launch_bounds__(BT, Bounds<NV, BT>::bwd) norm_bwd_kernel(const
         }
         const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
         const f2 r2 = both(r), k2 = both(-(r * r * r) * (sd * inv_d)), one = both(D == 1 ? a.eps * r * r * r : r);
-        if (!HOLD) {
-            // (the weights again, and the later layers' gradient, now that dy's registers are to be freed)
-            load_weight<T, NV>(a, t, w);
-            if (a.res && live) re.load(a.res, row * D, tpr, t, D);
-        }
+        f2 out[P];
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            dw[i] = fma2(g[i], mul2(h[i], r2), dw[i]);
-            if (!HOLD) e[i] = re.template pair<T>(i);
-            h[i] = add2(e[i], dh_pair(g[i], w[i], h[i], one, k2, D == 1));
+        for (int v = 0; v < NV; ++v) {
+            f2 h[4], g[4], e[4] = {0ull, 0ull, 0ull, 0ull};
+            rows.template get<T, VH>(stage, R::H, v, h);
+            rows.template get<T, 1>(stage, R::G, v, g);
+            if (a.res) rows.template get<T, VH>(stage, R::E, v, e);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                dw[v * 4 + i] = fma2(g[i], mul2(h[i], r2), dw[v * 4 + i]);
+                out[v * 4 + i] = add2(e[i], dh_pair(g[i], w[v * 4 + i], h[i], one, k2, D == 1));
+            }
         }
+        if (!AHEAD) fetch(row + step, 0);
         if (live) {
-            store_row<T, NV, false>(a.dx, row * D, tpr, t, D, h);
-            if (F32 && a.dres) store_row<T, NV, true>(a.dres, row * D, tpr, t, D, h);
+            store_row<T, NV, false>(a.dx, row * D, tpr, t, D, out);
+            if (F32 && a.dres) store_row<T, NV, true>(a.dres, row * D, tpr, t, D, out);
         }
     }
+    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
     if (rpb == 1) {
         store_row<T, NV, true>(a.dw_part, (long long)blockIdx.x * D, tpr, t, D, dw);
     } else {
-        store_row<T, NV, true>(s_slots, slot * D, tpr, t, D, dw);
+        __syncthreads();  // (the rows are read no more)
+        store_row<T, NV, true>(s_dyn, slot * D, tpr, t, D, dw);
         __syncthreads();
-        sum_slots(a, s_slots, rpb);
+        sum_slots(a, s_dyn, rpb);
     }
 }
 
@@ -643,12 +686,19 @@ cudaError_t norm_fwd_t(const NormArgs &a, const NormShape &s, bool vec, bool qua
     if (s.nv == 4) return norm_fwd_r<T, 32, 512>(a, s, n, quant, res, st);
     return s.threads <= 288 ? norm_fwd_r<T, 16, 288>(a, s, n, quant, res, st) : norm_fwd_r<T, 16, 512>(a, s, n, quant, res, st);
 }
+template <typename K>
+cudaError_t launch_wide(K k, int blocks, int threads, size_t smem, const NormArgs &a, cudaStream_t st) {
+    if (smem > 47 * 1024) {  // (the kernel's own shared memory counts too)
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_plain(k, dim3(blocks), dim3(threads), smem, st, a);
+}
 template <typename T, int NV, int BT>
 cudaError_t norm_bwd_v(const NormArgs &a, int blocks, bool f32, cudaStream_t st) {
-    const int rpb = BT / a.tpr;
-    const size_t smem = rpb > 1 ? (size_t)rpb * a.D * sizeof(float) : 0;  // (at most 16 KB: a thread has 16 columns)
-    if (f32) return launch_plain(norm_bwd_kernel<T, NV, BT, true>, dim3(blocks), dim3(BT), smem, st, a);
-    return launch_plain(norm_bwd_kernel<T, NV, BT, false>, dim3(blocks), dim3(BT), smem, st, a);
+    // (the shares of dw, at most 4 bytes a column of a thread, fit in the rows' place)
+    if (f32) return launch_wide(norm_bwd_kernel<T, NV, BT, true>, blocks, BT, BwdRows<NV, BT, true>::bytes(a.res), a, st);
+    return launch_wide(norm_bwd_kernel<T, NV, BT, false>, blocks, BT, BwdRows<NV, BT, false>::bytes(a.res), a, st);
 }
 template <typename T, int EPT, int BT>
 cudaError_t norm_bwd_r(const NormArgs &a, const NormShape &s, int n, bool f32, cudaStream_t st) {
