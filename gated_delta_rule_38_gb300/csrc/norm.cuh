@@ -114,11 +114,8 @@ __device__ __forceinline__ float lanes_max(float m, int lanes) {
     for (int o = lanes >> 1; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
     return __uint_as_float(x);
 }
-// 1 / scale of columns whose largest magnitude is m, and the scale.  (A NaN stays.)
-__device__ __forceinline__ float inv_scale(float m, float &scale) {
-    scale = (m < 1e-30f ? 1e-30f : m) * (1.0f / 448.0f);
-    return 1.0f / scale;
-}
+// The scale of columns whose largest magnitude is m.  (A NaN stays.)
+__device__ __forceinline__ float scale_of(float m) { return (m < 1e-30f ? 1e-30f : m) / 448.0f; }
 
 // Registers: 16 elements a thread leave room for three blocks of 256 an SM with the weights and the next row's loads held
 // in registers.  Rows over 8,192 take 32 elements a thread and hold neither.
@@ -216,14 +213,13 @@ __global__ void __launch_bounds__(BT, Bounds<NV, BT>::fwd) norm_fwd_kernel(const
             for (int v = 0; v < NV; ++v) {
                 const int c = (v * tpr + t) * 8;
                 if (!(live && c < D)) continue;
-                float scale;
-                const float is = inv_scale(m[v], scale);
+                const float scale = scale_of(m[v]);
                 const float *e = y + v * 8;
                 uint32_t u[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(e[4 * i] * is, e[4 * i + 1] * is), __NV_SATFINITE, __NV_E4M3);
-                    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(e[4 * i + 2] * is, e[4 * i + 3] * is), __NV_SATFINITE, __NV_E4M3);
+                    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(e[4 * i] / scale, e[4 * i + 1] / scale), __NV_SATFINITE, __NV_E4M3);
+                    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(e[4 * i + 2] / scale, e[4 * i + 3] / scale), __NV_SATFINITE, __NV_E4M3);
                     u[i] = lo | (hi << 16);
                 }
                 *reinterpret_cast<uint2 *>(static_cast<unsigned char *>(a.y) + row * D + c) = make_uint2(u[0], u[1]);
@@ -510,35 +506,35 @@ __global__ void __launch_bounds__(BT, RagBounds<EPT, BT>::blocks) norm_fwd_ragge
                 if (lane == 0) s_chunk[j * wpr + (t >> 5)] = __uint_as_float(m);
             }
             __syncthreads();
-            // one thread a scale: the largest of its columns' maxima, which the reciprocal of the scale then replaces
-            const int used = (D + 31) / 32, each = a.group ? 4 : used;
-            float is[2] = {0.f, 0.f};
+            // one thread a scale: the largest of its columns' maxima, which the scale then replaces
+            const int used = (D + 31) / 32;
+            float own[2] = {0.f, 0.f};
             if (a.group) {
                 for (int i = 0, q = t; q < a.nscale; ++i, q += tpr) {
-                    float m = s_chunk[4 * q], scale;
+                    float m = s_chunk[4 * q];
 #pragma unroll
                     for (int k = 1; k < 4; ++k)
                         if (4 * q + k < used) m = max_abs(m, s_chunk[4 * q + k]);
-                    is[i & 1] = inv_scale(m, scale);
-                    if (live) a.scale[row * a.nscale + q] = scale;
+                    own[i & 1] = scale_of(m);
+                    if (live) a.scale[row * a.nscale + q] = own[i & 1];
                 }
             } else {
-                float m = 0.f, scale;
+                float m = 0.f;
                 for (int i = lane; i < used; i += 32) m = max_abs(m, s_chunk[i]);
-                is[0] = inv_scale(lanes_max(m, 32), scale);
-                if (live && t == 0) a.scale[row] = scale;
+                own[0] = scale_of(lanes_max(m, 32));
+                if (live && t == 0) a.scale[row] = own[0];
             }
             if (a.group) {
                 __syncthreads();
-                for (int i = 0, q = t; q < a.nscale; ++i, q += tpr) s_chunk[4 * q] = is[i & 1];
+                for (int i = 0, q = t; q < a.nscale; ++i, q += tpr) s_chunk[4 * q] = own[i & 1];
                 __syncthreads();
             }
 #pragma unroll
             for (int j = 0; j < EPT; ++j) {
                 const int c = t + j * tpr;
                 if (!(live && c < D)) continue;
-                const float inv = a.group ? s_chunk[(c >> 7) * each] : is[0];
-                static_cast<unsigned char *>(a.y)[row * D + c] = __nv_cvt_float_to_fp8(h[j] * inv, __NV_SATFINITE, __NV_E4M3);
+                const float scale = a.group ? s_chunk[(c >> 7) * 4] : own[0];
+                static_cast<unsigned char *>(a.y)[row * D + c] = __nv_cvt_float_to_fp8(h[j] / scale, __NV_SATFINITE, __NV_E4M3);
             }
             __syncthreads();  // (the maxima have been read)
         }
