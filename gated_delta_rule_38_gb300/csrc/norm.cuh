@@ -652,7 +652,7 @@ cudaError_t launch_ragged(K k, const NormArgs &a, const NormShape &s, int blocks
     const size_t one = (size_t)s.rpb * place;
     const int stages = 2 * one + extra <= 100 * 1024 ? 2 : 1;
     const size_t smem = stages * one + extra;
-    if (smem > 48 * 1024) {
+    if (smem > 47 * 1024) {  // (the kernel's own shared memory counts too)
         const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
     }
