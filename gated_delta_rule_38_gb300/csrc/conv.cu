@@ -627,10 +627,8 @@ bool grid_fits(const ConvGrid &g) { return g.tblocks * g.cblocks <= 0x7fffffffLL
 
 template <typename K>
 cudaError_t launch_ring(K k, dim3 grid, size_t smem, cudaStream_t s, const ConvArgs &a) {
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_smem(k, smem);
+    if (e != cudaSuccess) return e;
     return launch_plain(k, grid, dim3(32, WALKS), smem, s, a);
 }
 template <typename T, int W, bool WIDE, bool PACKED>

@@ -36,6 +36,17 @@ gdr_status timed(int id, cudaStream_t s, F &&f) {
     return prof_end(id, s, a, b, f());
 }
 
+// Lets kernel k have `smem` bytes of dynamic shared memory.  Past 48 KB, which a kernel's static part (here 256 bytes at
+// most) shares, that has to be allowed first.  The limit is state of the kernel, not of the launch, and common to all host
+// threads: it is only ever set to one value, the most that a block can have, so that no thread lowers it between another
+// one's call of this and its launch.
+constexpr size_t kSmemFree = 47 * 1024, kSmemMost = 226 * 1024;
+template <typename K>
+cudaError_t allow_smem(K k, size_t smem) {
+    if (smem <= kSmemFree) return cudaSuccess;
+    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemMost);
+}
+
 inline bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline bool aligned16(const void *p) { return aligned_to(p, 16); }
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }

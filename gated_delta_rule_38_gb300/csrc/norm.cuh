@@ -652,10 +652,8 @@ cudaError_t launch_ragged(K k, const NormArgs &a, const NormShape &s, int blocks
     const size_t one = (size_t)s.rpb * place;
     const int stages = 2 * one + extra <= 100 * 1024 ? 2 : 1;
     const size_t smem = stages * one + extra;
-    if (smem > 47 * 1024) {  // (the kernel's own shared memory counts too)
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_smem(k, smem);
+    if (e != cudaSuccess) return e;
     return launch_plain(k, dim3(blocks), dim3(s.threads), smem, st, a, s.rpb, stages);
 }
 template <typename T, int EPT, int BT>
@@ -684,10 +682,8 @@ cudaError_t norm_fwd_t(const NormArgs &a, const NormShape &s, bool vec, bool qua
 }
 template <typename K>
 cudaError_t launch_wide(K k, int blocks, int threads, size_t smem, const NormArgs &a, cudaStream_t st) {
-    if (smem > 47 * 1024) {  // (the kernel's own shared memory counts too)
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_smem(k, smem);
+    if (e != cudaSuccess) return e;
     return launch_plain(k, dim3(blocks), dim3(threads), smem, st, a);
 }
 template <typename T, int NV, int BT>

@@ -647,10 +647,8 @@ __global__ void __launch_bounds__(256) scan_dbc_kernel(const ScanArgs a, int NP)
 
 template <typename K>
 cudaError_t launch_smem(K k, long long blocks, int threads, size_t smem, cudaStream_t s, const ScanArgs &a) {
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_smem(k, smem);
+    if (e != cudaSuccess) return e;
     return launch_plain(k, dim3((unsigned)blocks), dim3(threads), smem, s, a);
 }
 template <typename T, int L>

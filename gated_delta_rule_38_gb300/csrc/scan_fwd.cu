@@ -356,10 +356,8 @@ cudaError_t launch_one(const ScanArgs &a, cudaStream_t s) {
     const long long blocks = (long long)a.gblocks * a.G * segs * a.B;
     auto k = scan_fwd_kernel<T, L, FULL, PACKED>;
     const size_t smem = FwdSmem<L, FULL>::bytes(a.vec, a.vec_bc);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
-    }
+    const cudaError_t e = allow_smem(k, smem);
+    if (e != cudaSuccess) return e;
     return launch_plain(k, dim3((unsigned)blocks), dim3(128), smem, s, a);
 }
 template <typename T, int L>

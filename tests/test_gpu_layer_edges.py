@@ -1,15 +1,18 @@
-"""The layer operators at their edges: ties of the 8-bit rounding, widths at the limit of shared memory."""
+"""The layer operators at their edges: ties of the 8-bit rounding, widths at the limit of shared memory, calls
+from two host threads."""
 
+import ctypes
 import os
 import subprocess
 import sys
+import threading
 
 import numpy as np
 import pytest
 import torch
 
 import gated_delta_rule_38_gb300 as gdr
-from test_gpu_layer_ops import BF
+from test_gpu_layer_ops import BF, gen, scan_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +85,73 @@ def test_norm_rows_that_just_fill_48_kb(calls):
     r = subprocess.run([sys.executable, "-c", EDGE % (os.path.dirname(tests), tests, calls.replace("; ", "\n"))],
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "done", r.stderr[-2000:]
+
+
+# ---------------------------------------------------------------- two host threads
+
+def _in_threads(*calls, rounds=20000):
+    """Every C call over and over in a host thread of its own; the statuses that each returned."""
+    seen, gate = [set() for _ in calls], threading.Barrier(len(calls))
+
+    def work(call, statuses):
+        gate.wait()
+        for _ in range(rounds):
+            statuses.add(call())
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=a) for a in zip(calls, seen)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return seen
+
+
+def _c(fn, p, *tensors):
+    """The C call with these buffers, workspace last, on a stream of its own."""
+    stream = torch.cuda.Stream()
+    ptrs = [None if t is None else t.data_ptr() for t in tensors]
+
+    def call(keep=(stream, p, tensors)):
+        return fn(ctypes.byref(p), *ptrs, tensors[-1].numel(), stream.cuda_stream)
+
+    return call
+
+
+@pytest.mark.parametrize("D", [4096, 4099], ids=["vectors", "ragged"])
+def test_norm_backward_of_two_sizes_in_two_threads(D):
+    """One kernel at two sizes of shared memory (with and without a later gradient), called by two host threads at once:
+    the limit that one sets is not lowered under the other's launch."""
+    lib, randn = gdr._lib.load(), gen(2)
+    h, w, dy = randn(4, D), randn(D), randn(4, D, dtype=BF)
+    want, calls, outs = [], [], []
+    for later in (h, None):
+        want.append(gdr.rms_norm_bwd(h, w, dy, dresidual=later))
+        p = gdr._lib.NormProblem(4, D, D, 0, 2, 2, 0, 0, 1e-6)
+        outs.append([torch.empty_like(t) for t in want[-1]])
+        calls.append(_c(lib.gdr_norm_bwd, p, h, w, dy, later, *outs[-1], torch.empty(1 << 22, dtype=torch.uint8, device="cuda")))
+    assert _in_threads(*calls) == [{0}, {0}]
+    for got, expected in zip(outs, want):
+        for a, b in zip(got, expected):
+            assert torch.equal(a, b)
+
+
+def test_scan_backward_of_two_sizes_in_two_threads():
+    """The same of the scan's backward, by whole vectors and by ragged rows."""
+    lib = gdr._lib.load()
+    want, calls, outs = [], [], []
+    for D in (128, 131):
+        s, randn, _ = scan_inputs((1, 16, D, 16, 1, None, True, True, True), BF)
+        dy = randn(1, 16, D, dtype=BF)
+        a, o = (s["x"], s["dt"], s["A"], s["B"], s["C"]), (s["D"], s["z"], s["bias"], True, s["h0"])
+        saved = gdr.selective_scan_fwd(*a, *o, save_for_backward=True)[2]
+        want.append(gdr.selective_scan_bwd(*a, dy, saved, *o))
+        p = gdr._lib.ScanProblem(1, 16, D, 16, 1, D, D, D, 16, 16, 0, None, 0, 1)
+        outs.append([torch.empty_like(t) for t in want[-1]])
+        calls.append(_c(lib.gdr_scan_bwd, p, *a, s["D"], s["z"], s["bias"], dy, s["h0"], None, saved, *outs[-1],
+                        torch.empty(1 << 22, dtype=torch.uint8, device="cuda")))
+    assert _in_threads(*calls, rounds=6000) == [{0}, {0}]
+    for got, expected in zip(outs, want):
+        for a, b in zip(got, expected):
+            assert torch.equal(a, b)
