@@ -331,13 +331,15 @@ __global__ void __launch_bounds__(128) scan_join_kernel(const ScanArgs a, const 
     fetch(0);
     for (int i = 0; i < steps; i += U) {
         float now[U], through[U];
+        bool edge[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) now[u] = own[u], through[u] = cut[u] ? 0.f : ex2(A2 * dt[u]);
+        for (int u = 0; u < U; ++u) now[u] = own[u], edge[u] = cut[u] != 0, through[u] = ex2(A2 * dt[u]);
         fetch(i + U);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int s = reverse ? steps - i - u : i + u;
-            h = fmaf(through[u], h, now[u]);
+            // (at an edge nothing of h goes on, not even what is not finite: another sequence's)
+            h = edge[u] ? now[u] : fmaf(through[u], h, now[u]);
             if (i + u < steps) a.seg[((b0 + s) * NP + n) * a.DP + pc] = h;
         }
     }

@@ -1,5 +1,5 @@
 """The layer operators at their edges: ties of the 8-bit rounding, widths at the limit of shared memory, calls
-from two host threads."""
+from two host threads, values that must not cross from one sequence to another."""
 
 import ctypes
 import os
@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import gated_delta_rule_38_gb300 as gdr
-from test_gpu_layer_ops import BF, gen, scan_inputs
+from test_gpu_layer_ops import BF, cu_of, gen, scan_inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -85,6 +85,35 @@ def test_norm_rows_that_just_fill_48_kb(calls):
     r = subprocess.run([sys.executable, "-c", EDGE % (os.path.dirname(tests), tests, calls.replace("; ", "\n"))],
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "done", r.stderr[-2000:]
+
+
+# ---------------------------------------------------------------- selective scan
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("T", [64, 3000], ids=["one segment", "segments"])
+def test_scan_sequences_are_kept_apart(T, value):
+    """What is not finite in one sequence of a packed batch stays out of the others, whether or not the token axis is cut
+    into segments, forward (a state from before the edge) and backward (a gradient from behind it)."""
+    lens = (T // 4, T // 2, 0, T // 4)
+    s, randn, _ = scan_inputs((1, T, 40, 16, 1, lens, True, True, True), BF)
+    cu, dy, ds = cu_of(lens), randn(1, T, 40, dtype=BF), randn(4, 40, 16)
+
+    def call(x, dy):
+        a, o = (x, s["dt"], s["A"], s["B"], s["C"]), (s["D"], s["z"], s["bias"], True, s["h0"])
+        y, fin, saved = gdr.selective_scan_fwd(*a, *o, True, cu, save_for_backward=True)
+        dx, ddt, _, dB, dC, _, dz, _, dh = gdr.selective_scan_bwd(*a, dy, saved, *o, ds, cu)
+        return (y, dx, ddt, dB, dC, dz), (fin, dh)
+
+    want = call(s["x"], dy)
+    first, last = T // 4, T // 4 + T // 2  # the middle sequence
+    for tensor, at in (("x", first + 3), ("dy", last - 5)):
+        bad = {"x": s["x"].clone(), "dy": dy.clone()}
+        bad[tensor][0, at] = value
+        tokens, states = call(bad["x"], bad["dy"])
+        for got, expected in zip(tokens, want[0]):
+            assert torch.equal(got[:, :first], expected[:, :first]) and torch.equal(got[:, last:], expected[:, last:])
+        for got, expected in zip(states, want[1]):
+            assert torch.equal(got[[0, 2, 3]], expected[[0, 2, 3]])
 
 
 # ---------------------------------------------------------------- two host threads
