@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(BT, BT > 256 ? 1 : 2) norm_bwd_kernel(const No
                 ss += f.x, sd += f.y;
             }
         }
-        const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
+        const float r = live ? rsqrtf(fmaf(ss, inv_d, a.eps)) : 0.f;  // (no row: with eps = 0 the factor would be infinite)
         const f2 r2 = both(r), k2 = both(-(r * r * r) * (sd * inv_d)), one = both(D == 1 ? a.eps * r * r * r : r);
         f2 out[P];
 #pragma unroll

@@ -1,5 +1,6 @@
 """The layer operators at their edges: ties of the 8-bit rounding, widths at the limit of shared memory, calls
-from two host threads, values that must not cross from one sequence to another."""
+from two host threads, values that must not cross from one sequence to another,
+extremes of the argument ranges."""
 
 import ctypes
 import os
@@ -12,6 +13,7 @@ import pytest
 import torch
 
 import gated_delta_rule_38_gb300 as gdr
+import layer_ref as ref
 from test_gpu_layer_ops import BF, cu_of, gen, scan_inputs
 
 pytestmark = pytest.mark.gpu
@@ -85,6 +87,18 @@ def test_norm_rows_that_just_fill_48_kb(calls):
     r = subprocess.run([sys.executable, "-c", EDGE % (os.path.dirname(tests), tests, calls.replace("; ", "\n"))],
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "done", r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("R", [1, 37])
+def test_norm_backward_without_eps(R):
+    """Blocks take several rows at a time; with eps = 0 the places past the last row add nothing to dweight."""
+    randn = gen(R)
+    h, w, dy = randn(R, 256, dtype=BF), randn(256), randn(R, 256, dtype=BF)
+    dx, _, dw = gdr.rms_norm_bwd(h, w, dy, eps=0.0)
+    h64, w64 = ref.f64(h), ref.f64(w)
+    (ref.norm(h64, w64, None, 0.0)[0] * ref.f64(dy, False)).sum().backward()
+    ref.check(dx, h64.grad, "dx")
+    ref.check(dw, w64.grad, "dweight")
 
 
 # ---------------------------------------------------------------- selective scan
