@@ -229,7 +229,8 @@ __global__ void __launch_bounds__(BT, Bounds<NV, BT>::fwd) norm_fwd_kernel(const
     }
 }
 
-// dh of a pair: r w g + h k2 (k2 = -r^3 mean(w g h)), where at D = 1 the two terms cancel but for
+// dh of a pair: r w g + h k2 (k2 = -r^3 mean(w g h), taken from the mean's side: r^3 alone leaves fp32's range at rows of
+// 1e13 or, with a small eps, 1e-13), where at D = 1 the two terms cancel but for
 // 1 - h^2 r^2 = eps r^2 (`one` is then eps r^3 and k2 unused).
 __device__ __forceinline__ f2 dh_pair(f2 g, f2 w, f2 h, f2 one, f2 k2, bool d1) {
     const f2 own = mul2(mul2(g, w), one);
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(BT, BT > 256 ? 1 : 2) norm_bwd_kernel(const No
             }
         }
         const float r = live ? rsqrtf(fmaf(ss, inv_d, a.eps)) : 0.f;  // (no row: with eps = 0 the factor would be infinite)
-        const f2 r2 = both(r), k2 = both(-(r * r * r) * (sd * inv_d)), one = both(D == 1 ? a.eps * r * r * r : r);
+        const f2 r2 = both(r), k2 = both(-(r * (sd * inv_d)) * r * r), one = both(D == 1 ? a.eps * r * r * r : r);
         f2 out[P];
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
@@ -608,7 +609,7 @@ __global__ void __launch_bounds__(BT, RagBounds<EPT, BT>::blocks) norm_bwd_ragge
             }
         }
         const float r = rsqrtf(fmaf(ss, inv_d, a.eps));
-        const float k2 = -(r * r * r) * (sd * inv_d), one = D == 1 ? a.eps * r * r * r : r;
+        const float k2 = -(r * (sd * inv_d)) * r * r, one = D == 1 ? a.eps * r * r * r : r;
 #pragma unroll
         for (int j = 0; j < EPT; ++j) {
             const int c = t + j * tpr;

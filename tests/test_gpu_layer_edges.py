@@ -101,6 +101,19 @@ def test_norm_backward_without_eps(R):
     ref.check(dw, w64.grad, "dweight")
 
 
+@pytest.mark.parametrize("D", [256, 259], ids=["vectors", "ragged"])
+@pytest.mark.parametrize("size,eps", [(1e15, 1e-6), (1e-15, 0.0)])
+def test_norm_backward_of_very_large_and_small_rows(size, eps, D):
+    """The gradient does not depend on the cube of the norm's factor staying in range."""
+    randn = gen(D)
+    h, w, dy = randn(5, D, scale=size), randn(D), randn(5, D, dtype=BF)
+    _, dres, dw = gdr.rms_norm_bwd(h, w, dy, eps=eps)
+    h64, w64 = ref.f64(h), ref.f64(w)
+    (ref.norm(h64, w64, None, eps)[0] * ref.f64(dy, False)).sum().backward()
+    ref.check(dres, h64.grad, "dresidual")
+    ref.check(dw, w64.grad, "dweight")
+
+
 # ---------------------------------------------------------------- selective scan
 
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
