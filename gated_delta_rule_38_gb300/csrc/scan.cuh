@@ -225,8 +225,15 @@ __device__ __forceinline__ void zero(State h) {
 #pragma unroll
     for (int n = 0; n < 4; ++n) h[n][0] = h[n][1] = 0ull;
 }
+// A as the exponent of 2 that a unit step takes.  Held finite: A = -inf, or one whose product overflows, forgets at every
+// step, but a step of zero (a tile's places past the last token are such) changes nothing.
+__device__ __forceinline__ float rate2(float A) {
+    const float v = A * LOG2E;
+    return v < -3.4e38f ? -3.4e38f : v;  // (a NaN stays)
+}
+
 // From or to a [.., D, N] fp32 array at channel `ch` (of `nc` that exist from there) and state `n0`.
-__device__ __forceinline__ void load_rows(const ScanArgs &a, const float *p, int nc, int n0, State h, float mul = 1.f) {
+__device__ __forceinline__ void load_rows(const ScanArgs &a, const float *p, int nc, int n0, State h) {
     float v[4][4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -241,9 +248,20 @@ __device__ __forceinline__ void load_rows(const ScanArgs &a, const float *p, int
     }
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-        h[n][0] = pack2(v[0][n] * mul, v[1][n] * mul);
-        h[n][1] = pack2(v[2][n] * mul, v[3][n] * mul);
+        h[n][0] = pack2(v[0][n], v[1][n]);
+        h[n][1] = pack2(v[2][n], v[3][n]);
     }
+}
+__device__ __forceinline__ void load_rates(const ScanArgs &a, int c, int nc, int n0, State r) {  // of the channels from c
+    load_rows(a, a.A + (long long)c * a.N, nc, n0, r);
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            float lo, hi;
+            unpack2(r[n][p], lo, hi);
+            r[n][p] = pack2(rate2(lo), rate2(hi));
+        }
 }
 __device__ __forceinline__ void store_rows(const ScanArgs &a, float *p, int nc, int n0, const State h) {
     float v[4][4];

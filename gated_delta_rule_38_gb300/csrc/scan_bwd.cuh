@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(Bwd<L>::NT, L >= 4 ? 5 : 2) scan_bwd_local_ker
     tiles.fetch(top, 0);
     for (int i = tid; i < W::CB; i += W::NT) sm.bias[i] = (a.bias && i < ch.count) ? a.bias[ch.first + i] : 0.f;
     State A2, back;
-    load_rows(a, a.A + (long long)(ch.first + c0) * a.N, nc, n0, A2, LOG2E);
+    load_rates(a, ch.first + c0, nc, n0, A2);
     if (!PACKED && s == a.nseg - 1 && a.dstate_out)
         load_rows(a, a.dstate_out + ((long long)b * a.D + ch.first + c0) * a.N, nc, n0, back);
     else
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(Bwd<L>::NT) scan_bwd_kernel(const ScanArgs a) 
 
     f2 dbias[4] = {0ull, 0ull, 0ull, 0ull};
     State A2, back, dA;
-    load_rows(a, a.A + (long long)(ch.first + c0) * a.N, nc, n0, A2, LOG2E);
+    load_rates(a, ch.first + c0, nc, n0, A2);
     zero(dA);
     if (s < a.nseg - 1)
         load_padded(a.seg + (((long long)b * a.nseg + s + 1) * NP + n0) * a.DP + ch.pad + c0, a.DP, back);

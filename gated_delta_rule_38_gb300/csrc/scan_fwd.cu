@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(128, FULL ? 5 : 6) scan_fwd_kernel(const ScanA
     fetch(t0, 0);
 
     State A2, h;
-    load_rows(a, a.A + (long long)(ch.first + c0) * a.N, nc, n0, A2, LOG2E);
+    load_rates(a, ch.first + c0, nc, n0, A2);
     const long long segpos = ((long long)b * a.nseg + s) * NP + n0;
     if (FULL && s > 0)
         load_padded(a.seg + (segpos - NP) * a.DP + ch.pad + c0, a.DP, h);
@@ -311,7 +311,7 @@ __global__ void __launch_bounds__(128) scan_join_kernel(const ScanArgs a, const 
     const int g = pc / a.gpad, in = pc - g * a.gpad;
     const bool live = in < a.Dg && n < a.N;
     const int c = g * a.Dg + in;
-    const float A2 = live ? a.A[(long long)c * a.N + n] * LOG2E : 0.f;
+    const float A2 = live ? rate2(a.A[(long long)c * a.N + n]) : 0.f;
     float h = (live && start) ? start[((long long)b * a.D + c) * a.N + n] : 0.f;
     constexpr int U = 8;  // segments a batch; the next batch's loads are in flight while one is joined
     const long long b0 = (long long)b * a.nseg;

@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(256, 2) scan_step_kernel(const ScanArgs a, int
     const bool wide = a.st_vec && a.vec_bc, mine = n0 < a.N;
     float A2[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) A2[i] = n0 + i < a.N ? a.A[(long long)d * a.N + n0 + i] * LOG2E : 0.f;
+    for (int i = 0; i < 4; ++i) A2[i] = n0 + i < a.N ? rate2(a.A[(long long)d * a.N + n0 + i]) : 0.f;
     const float bias = a.bias ? a.bias[d] : 0.f, skip = a.skip ? a.skip[d] : 0.f;
     // this lane's rows of a group, and the places of the token to load next (of the first of the rows)
     const int own = RB >= NL ? nl * OWN : nl % RB, T_ = ONE ? 1 : a.T;

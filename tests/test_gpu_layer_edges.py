@@ -143,6 +143,31 @@ def test_scan_sequences_are_kept_apart(T, value):
             assert torch.equal(got[[0, 2, 3]], expected[[0, 2, 3]])
 
 
+@pytest.mark.parametrize("value", [float("-inf"), -3e38])
+@pytest.mark.parametrize("T", [21, 1500], ids=["one segment", "segments"])
+def test_scan_states_that_forget_at_once(T, value):
+    """A = -inf, or so low that A log2(e) overflows: every step forgets the state before it, and the places past the last
+    token of a tile change nothing.  (The gradients' definition multiplies an infinite A by zero; a finite one's hold.)"""
+    s, randn, _ = scan_inputs((1, T, 40, 16, 1, None, True, True, True), BF)
+    s["A"][:, 3] = value
+    dy, ds = randn(1, T, 40, dtype=BF), randn(1, 40, 16)
+    a, o = (s["x"], s["dt"], s["A"], s["B"], s["C"]), (s["D"], s["z"], s["bias"], True, s["h0"])
+    y, fin, saved = gdr.selective_scan_fwd(*a, *o, save_for_backward=True)
+    order = ("x", "dt", "A", "B", "C", "D", "z", "bias", "h0")
+    leaves = [ref.f64(s[k]) for k in order]
+    yw, fw = ref.scan(*leaves[:8], True, leaves[8], None)
+    ref.check(y, yw, "y")
+    ref.check(fin, fw, "final_state")
+    if value > float("-inf"):
+        ((yw * ref.f64(dy, False)).sum() + (fw * ref.f64(ds, False)).sum()).backward()
+        for got, leaf, name in zip(gdr.selective_scan_bwd(*a, dy, saved, *o, ds), leaves, order):
+            ref.check(got, leaf.grad, "d" + name)
+    step = s["h0"].clone()
+    one = gdr.selective_scan_step(*(t[:, :1].contiguous() if t.dim() > 2 else t for t in a), step, s["D"], s["z"][:, :1].contiguous(),
+                                  s["bias"], True)
+    ref.check(one, yw[:, :1], "y of a step")
+
+
 # ---------------------------------------------------------------- two host threads
 
 def _in_threads(*calls, rounds=20000):
