@@ -35,13 +35,13 @@ __global__ void __launch_bounds__(256, 2) scan_step_kernel(const ScanArgs a, int
     const float bias = a.bias ? a.bias[d] : 0.f, skip = a.skip ? a.skip[d] : 0.f;
     // this lane's rows of a group, and the places of the token to load next (of the first of the rows)
     const int own = RB >= NL ? nl * OWN : nl % RB, T_ = ONE ? 1 : a.T;
-    const long long row0 = (long long)b0 * T_, orow = row0 + own * T_;
+    const long long row0 = (long long)b0 * T_, orow = row0 + (long long)own * T_;
     const uint16_t *px = static_cast<const uint16_t *>(a.x) + orow * a.x_ld + d, *pd = static_cast<const uint16_t *>(a.dt) + orow * a.dt_ld + d;
     const uint16_t *pz = a.z ? static_cast<const uint16_t *>(a.z) + orow * a.z_ld + d : nullptr;
     const uint16_t *pb = static_cast<const uint16_t *>(a.Bm) + row0 * a.b_ld + (long long)g * a.N + n0;
     const uint16_t *pc = static_cast<const uint16_t *>(a.Cm) + row0 * a.c_ld + (long long)g * a.N + n0;
     T *py = static_cast<T *>(a.y) + orow * a.D + d;
-    const long long sx = T_ * a.x_ld, sd = T_ * a.dt_ld, sz = T_ * a.z_ld, sb = T_ * a.b_ld, sc = T_ * a.c_ld, sy = T_ * a.D;
+    const long long sx = T_ * a.x_ld, sd = T_ * a.dt_ld, sz = T_ * a.z_ld, sb = T_ * a.b_ld, sc = T_ * a.c_ld, sy = (long long)T_ * a.D;
     // from a group's last token to the next group's first
     const long long gx = RB * sx - (T_ - 1) * a.x_ld, gd = RB * sd - (T_ - 1) * a.dt_ld, gz = RB * sz - (T_ - 1) * a.z_ld;
     const long long gb = RB * sb - (T_ - 1) * a.b_ld, gc = RB * sc - (T_ - 1) * a.c_ld, gy = RB * sy - (long long)(T_ - 1) * a.D;

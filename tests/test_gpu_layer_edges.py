@@ -168,6 +168,26 @@ def test_scan_states_that_forget_at_once(T, value):
     ref.check(one, yw[:, :1], "y of a step")
 
 
+def test_scan_step_of_rows_beyond_2_to_31_elements():
+    """A row's tokens times its channels pass 31 bits; a full group of rows and a partial one."""
+    if torch.cuda.mem_get_info()[0] < 80e9:
+        pytest.skip("needs about 70 GB of free device memory")
+    B, T, D, N = 6, 129, 1 << 24, 4
+    x = torch.empty(B, T, D, dtype=BF, device="cuda").normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    A = -torch.rand(D, N, device="cuda") - 0.2
+    bc = torch.randn(2, B, T, 1, N, device="cuda").to(BF)
+    state = torch.randn(B, D, N, device="cuda")
+    ends = (slice(0, 24), slice(D - 24, D))
+    before = [state[:, c].clone() for c in ends]
+    y = gdr.selective_scan_step(x, x, A, bc[0], bc[1], state, dt_softplus=True)  # (the inputs are their own steps)
+    for c, h in zip(ends, before):
+        xc = ref.f64(x[..., c], False)
+        want, fin = ref.scan(xc, xc, ref.f64(A[c], False), ref.f64(bc[0], False), ref.f64(bc[1], False), None, None, None, True,
+                             ref.f64(h, False), None)
+        ref.check(y[..., c], want, "y")
+        ref.check(state[:, c], fin, "state")
+
+
 # ---------------------------------------------------------------- two host threads
 
 def _in_threads(*calls, rounds=20000):
