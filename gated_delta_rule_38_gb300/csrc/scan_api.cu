@@ -15,9 +15,22 @@ cudaError_t launch_scan_dbc_fp16(const ScanArgs &a, int L, cudaStream_t s);
 
 namespace {
 
+// Lanes a channel: four states each.
+int lanes_of(int N) {
+    int L = 1;
+    while (4 * L < N) L *= 2;
+    return L;
+}
+
+// Channels of a group, padded to the forward's blocks (of 512 / L) in both directions.
+int64_t padded_group(const gdr_scan_problem *p) {
+    const int Dg = p->D / p->G, pad = 512 / lanes_of(p->N);
+    return (int64_t)((Dg + pad - 1) / pad) * pad;
+}
+
 gdr_status check_scan(const gdr_scan_problem *p) {
     if (!p) return GDR_ERR_NULL;
-    if (p->B < 1 || p->T < 0 || p->T > (1 << 30) || p->D < 1 || p->D > (1 << 24) || p->N < 1 || p->N > GDR_SCAN_MAX_N ||
+    if (p->B < 1 || p->B > (1 << 30) || p->T < 0 || p->T > (1 << 30) || p->D < 1 || p->D > (1 << 24) || p->N < 1 || p->N > GDR_SCAN_MAX_N ||
         p->G < 1 || p->D % p->G)
         return GDR_ERR_SHAPE;
     if (p->x_ld < p->D || p->dt_ld < p->D || p->z_ld < p->D || p->b_ld < (int64_t)p->G * p->N ||
@@ -26,16 +39,11 @@ gdr_status check_scan(const gdr_scan_problem *p) {
     if (p->cu_seqlens && (p->B != 1 || p->num_seqs < 1)) return GDR_ERR_SHAPE;
     // every launch's blocks fit the grid
     if (((int64_t)p->D / 32 + p->G) * p->B > 0x7fffffff || (int64_t)p->B * p->T > ((int64_t)1 << 31) / p->G) return GDR_ERR_SHAPE;
+    // padded channels are counted in an int
+    if (padded_group(p) * p->G > 0x7fffffff) return GDR_ERR_SHAPE;
     if (!is_half(p->dtype)) return GDR_ERR_DTYPE;
     if (p->flags & ~(unsigned)GDR_SCAN_DT_SOFTPLUS) return GDR_ERR_UNSUPPORTED;
     return GDR_OK;
-}
-
-// Lanes a channel: four states each.
-int lanes_of(int N) {
-    int L = 1;
-    while (4 * L < N) L *= 2;
-    return L;
 }
 
 // How a direction's blocks cover the problem: channels a block, blocks a group, segments of the token axis.
@@ -46,10 +54,9 @@ Cover cover_of(const gdr_scan_problem *p, bool bwd) {
     Cover c;
     c.L = lanes_of(p->N);
     c.NP = 4 * c.L;
-    const int Dg = p->D / p->G, pad = 512 / c.L;           // padded to the forward's blocks in both directions
     const int CB = bwd && c.L < 4 ? 128 : 512 / c.L;
-    c.gpad = (Dg + pad - 1) / pad * pad;
-    c.gblocks = (Dg + CB - 1) / CB;
+    c.gpad = (int)padded_group(p);
+    c.gblocks = (p->D / p->G + CB - 1) / CB;
     c.DP = c.gpad * p->G;
     // Segments.  Splitting costs a state-only first pass (about 0.7 of a full one) and a join, so the token axis is cut
     // only when one block a channel block would leave the chip idle, and into the number of segments with the least
