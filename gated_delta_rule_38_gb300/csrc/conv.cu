@@ -686,6 +686,15 @@ size_t conv_state_bytes(const gdr_conv_problem *p) {
     return (size_t)(p->cu_seqlens ? p->num_seqs : p->B) * (p->W - 1) * p->D * 2;
 }
 
+size_t tokens_bytes(const gdr_conv_problem *p) { return (size_t)p->B * p->T * p->D * 2; }
+
+// Whether an output of `n` bytes touches the tokens or the states that other threads may still read: each walk reads the
+// W - 1 tokens before its own (the backward also those behind).
+bool conv_touches(const gdr_conv_problem *p, const void *out, size_t n, const void *tokens, int64_t ld, const void *states) {
+    return p->T > 0 && (touches(out, n, tokens, (size_t)p->B * p->T, (size_t)p->D * 2, (size_t)ld * 2) ||
+                        touches(out, n, states, 1, conv_state_bytes(p), conv_state_bytes(p)));
+}
+
 // Without tokens the states pass through: dst = src, or zeros.
 gdr_status conv_no_tokens(const gdr_conv_problem *p, const void *src, void *dst, cudaStream_t s) {
     if (!dst || dst == src) return GDR_OK;
@@ -700,6 +709,9 @@ gdr_status conv_fwd_core(const gdr_conv_problem *p, const void *x, const void *w
     for (const void *q : {x, state_in, (const void *)y, (const void *)state_out})
         if (!aligned_to(q, 2)) return GDR_ERR_ALIGN;
     if (!aligned_to(weight, ws) || !aligned_to(bias, ws)) return GDR_ERR_ALIGN;
+    if (!step && (conv_touches(p, y, tokens_bytes(p), x, p->x_ld, state_in) ||
+                  conv_touches(p, state_out, conv_state_bytes(p), x, p->x_ld, state_in)))
+        return GDR_ERR_UNSUPPORTED;
     bool wide = p->D % 4 == 0 && p->x_ld % 4 == 0;
     for (const void *q : {x, state_in, (const void *)y, (const void *)state_out}) wide = wide && aligned_to(q, 8);
     const ConvGrid g = conv_grid(p, !step ? conv_tt(p, false) : p->T > 0 ? p->T : 1);
@@ -727,8 +739,6 @@ gdr_status gdr_conv_fwd(const gdr_conv_problem *p, const void *x, const void *we
                         const void *state_in, void *y, void *state_out, void *stream) {
     gdr_status st = check_conv(p);
     if (st != GDR_OK) return st;
-    // (a sequence's first and last tokens belong to different threads)
-    if (state_out && state_out == state_in) return GDR_ERR_UNSUPPORTED;
     return conv_fwd_core(p, x, weight, bias, state_in, y, state_out, false, stream);
 }
 
@@ -766,6 +776,12 @@ gdr_status gdr_conv_bwd(const gdr_conv_problem *p, const void *x, const void *we
         if (!aligned_to(q, ws)) return GDR_ERR_ALIGN;
     if (need && (!workspace || workspace_bytes < need)) return GDR_ERR_WORKSPACE;
     if (need && !aligned_to(workspace, 256)) return GDR_ERR_ALIGN;
+    for (bool states : {false, true}) {
+        const void *out = states ? dstate_in : dx;
+        const size_t n = states ? conv_state_bytes(p) : tokens_bytes(p);
+        if (conv_touches(p, out, n, x, p->x_ld, state_in) || conv_touches(p, out, n, dy, p->D, dstate_out))
+            return GDR_ERR_UNSUPPORTED;
+    }
     bool wide = p->D % 4 == 0 && p->x_ld % 4 == 0;
     for (const void *q : {x, dy, state_in, dstate_out, (const void *)dx, (const void *)dstate_in})
         wide = wide && aligned_to(q, 8);

@@ -49,6 +49,15 @@ cudaError_t allow_smem(K k, size_t smem) {
 
 inline bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 inline bool aligned16(const void *p) { return aligned_to(p, 16); }
+// Whether `n` bytes from p touch any of `rows` rows of `width` bytes, `ld` bytes apart, from q.  (False without either.)
+inline bool touches(const void *p, size_t n, const void *q, size_t rows, size_t width, size_t ld) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    if (!p || !q || n == 0 || rows == 0 || a + n <= b) return false;
+    if (a < b) return true;
+    const size_t row = (a - b) / ld;
+    if (row >= rows) return false;
+    return (a - b) % ld < width || (row + 1 < rows && a + n > b + (row + 1) * ld);
+}
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline size_t esize(gdr_dtype d) { return d == GDR_FP32 ? 4 : 2; }
 inline bool is_half(gdr_dtype d) { return d == GDR_BF16 || d == GDR_FP16; }

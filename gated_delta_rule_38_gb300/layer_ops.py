@@ -176,7 +176,7 @@ def short_conv_fwd(x, weight, bias=None, activation=None, initial_state=None, ou
 
     weight and bias [D] in x's type or fp32, 2 <= W <= 4.  ``initial_state`` [N,W-1,D] (x's type, oldest first) holds
     the inputs before each row's (packed: sequence's) first token, None for zeros; final_state, in the same layout,
-    the last W-1 inputs (None unless ``output_final_state``).
+    the last W-1 inputs (None unless ``output_final_state``).  ``out`` must not overlap x or ``initial_state``.
     """
     cu = _cu(cu_seqlens)
     p, x, sshape = _conv_problem(x, weight, bias, activation, cu)

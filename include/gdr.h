@@ -334,15 +334,18 @@ gdr_status gdr_norm_bwd(const gdr_norm_problem *p, const void *h, const void *we
  *        dtype or fp32); state_in [N,W-1,D] (dtype): the inputs before each sequence's
  *        first token, oldest first, or NULL (zeros)
  *   out: y [B,T,D]; state_out [N,W-1,D]: the last W-1 inputs of each sequence (reaching
- *        back into state_in for short ones), or NULL.  Not state_in itself.
+ *        back into state_in for short ones), or NULL
+ * The outputs overlap neither x nor state_in (GDR_ERR_UNSUPPORTED): neighbouring walks share
+ * tokens.  gdr_conv_step may write y over a contiguous x.
  * Packed batches (cu_seqlens) as in gdr_fwd: B = 1, N = num_seqs.  A malformed cu_seqlens
  * latches GDR_ERR_CUSEQLENS; the outputs are then unspecified, and nothing outside the
  * given buffers is touched.  T = 0 passes the states through.
  * gdr_conv_step: dense rows only; the states are updated in place.  Meant for T = 1 or a
  * few tokens (one thread walks all tokens of its channels).
  * Backward: dy [B,T,D], dstate_out [N,W-1,D] or NULL (zeros) -> dx [B,T,D], dweight, dbias
- * (weight_dtype; dbias nullable, only with a bias), dstate_in [N,W-1,D] (nullable).
- * Fixed summation order.
+ * (weight_dtype; dbias nullable, only with a bias), dstate_in [N,W-1,D] (nullable).  dx and
+ * dstate_in overlap none of x, dy, state_in, dstate_out (GDR_ERR_UNSUPPORTED).  Fixed
+ * summation order.
  */
 #define GDR_CONV_SILU (1u << 0)
 typedef struct gdr_conv_problem {

@@ -114,6 +114,21 @@ def test_norm_backward_of_very_large_and_small_rows(size, eps, D):
     ref.check(dw, w64.grad, "dweight")
 
 
+# ---------------------------------------------------------------- short convolution
+
+def test_conv_in_place_is_refused():
+    """Walks share the tokens between them: an output over the input is refused, strided or not; a step may have it."""
+    randn = gen(4)
+    x, w = randn(2, 40, 64, dtype=BF), randn(64, 4, dtype=BF)
+    before = x.clone()
+    with pytest.raises(gdr.GdrError, match="UNSUPPORTED"):
+        gdr.short_conv_fwd(x, w, out=x)
+    assert torch.equal(x, before)
+    one, state = x[:, :1].contiguous(), randn(2, 3, 64, dtype=BF)
+    want = gdr.short_conv_step(one, state.clone(), w)
+    assert torch.equal(gdr.short_conv_step(one, state, w, out=one), want)
+
+
 # ---------------------------------------------------------------- selective scan
 
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
