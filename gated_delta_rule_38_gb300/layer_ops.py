@@ -3,13 +3,14 @@ scales), the short causal convolution, and the selective state space scan.
 
 Python surface of ``gdr_norm_*``, ``gdr_conv_*`` and ``gdr_scan_*`` in ``include/gdr.h``.  As for the delta rule, the
 ``*_fwd`` / ``*_bwd`` / ``*_step`` functions map onto one library call each and ``rms_norm``, ``short_conv`` and
-``selective_scan`` are differentiable.  Token tensors may be row-strided views (slices of a fused projection are read
-in place); any other view is copied.
+``selective_scan`` are differentiable (once: second derivatives are refused).  Token tensors may be row-strided views
+(slices of a fused projection are read in place); any other view is copied.
 """
 
 from __future__ import annotations
 
 from ctypes import byref, c_size_t
+from functools import wraps
 
 import torch
 
@@ -50,6 +51,35 @@ def _workspace(fn, p, like):
     n = c_size_t(0)
     _lib.check(fn(byref(p), byref(n)), fn.__name__)
     return torch.empty(n.value, dtype=torch.uint8, device=like.device), n.value
+
+
+class _Once(torch.autograd.Function):
+    """Hands on the gradients that a backward pass computed, as depending on all that it read: who differentiates them is
+    told, where torch's once_differentiable lets autograd.grad take the other terms of a loss alone."""
+
+    @staticmethod
+    def forward(ctx, name, grads, *read):
+        ctx.name = name
+        return tuple(None if g is None else g.detach() for g in grads)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"{ctx.name} has no second derivatives")
+
+
+def _once(backward):
+    """A Function's backward that is not differentiable itself."""
+    name = backward.__qualname__.split(".")[0].lstrip("_")
+
+    @wraps(backward)
+    def run(ctx, *grads):
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        if not torch.is_grad_enabled():  # (no graph of the backward pass was asked for)
+            return out
+        return _Once.apply(name, out, *ctx.saved_tensors, *grads)
+
+    return run
 
 
 # ---------------------------------------------------------------- RMS norm
@@ -132,6 +162,7 @@ class _RmsNorm(torch.autograd.Function):
         return y, h
 
     @staticmethod
+    @_once
     def backward(ctx, dy, dh):
         h, weight = ctx.saved_tensors
         if dy is None and dh is None:
@@ -233,6 +264,7 @@ class _ShortConv(torch.autograd.Function):
         return y, fin
 
     @staticmethod
+    @_once
     def backward(ctx, dy, dfin):
         x, weight, bias, h0, cu = ctx.saved_tensors
         dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.contiguous()
@@ -368,6 +400,7 @@ class _SelectiveScan(torch.autograd.Function):
         return y, fin
 
     @staticmethod
+    @_once
     def backward(ctx, dy, dfin):
         x, dt, A, B, C, D, z, dt_bias, h0, cu, saved = ctx.saved_tensors
         dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device) if dy is None else dy.contiguous()

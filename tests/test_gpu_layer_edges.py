@@ -203,6 +203,29 @@ def test_scan_step_of_rows_beyond_2_to_31_elements():
         ref.check(state[:, c], fin, "state")
 
 
+# ---------------------------------------------------------------- autograd
+
+def test_second_derivatives_are_refused():
+    """The backward passes are not differentiable themselves: asked for second derivatives they say so."""
+    randn = gen(9)
+    x, w, cw = randn(1, 6, 32, dtype=BF), randn(32), randn(32, 4, dtype=BF)
+    s, _, _ = scan_inputs((1, 6, 32, 16, 1, None, False, True, True), BF)
+    for f in (lambda t: gdr.rms_norm(t, w)[0], lambda t: gdr.short_conv(t, cw, None, "silu")[0],
+              lambda t: gdr.selective_scan(t, s["dt"], s["A"], s["B"], s["C"], s["D"], s["z"], s["bias"], True)[0]):
+        t = x.clone().requires_grad_()
+        # (with a term of its own that has second derivatives, which alone would come back without a word)
+        loss = f(t).float().square().sum() + t.float().pow(3).sum()
+        (d,) = torch.autograd.grad(loss, t, create_graph=True)
+        with pytest.raises(RuntimeError, match="no second derivatives"):
+            torch.autograd.grad(d.float().sum(), t, retain_graph=True)
+        with pytest.raises(RuntimeError, match="no second derivatives"):
+            d.float().sum().backward()
+        # the first ones are those of a pass without a graph
+        t2 = x.clone().requires_grad_()
+        (f(t2).float().square().sum() + t2.float().pow(3).sum()).backward()
+        assert torch.equal(t2.grad, d)
+
+
 # ---------------------------------------------------------------- two host threads
 
 def _in_threads(*calls, rounds=20000):
