@@ -29,8 +29,8 @@ constexpr int kNormThreads = 512;
 struct NormShape {
     int tpr, nv, threads, rpb;
 };
-inline NormShape norm_shape(int D, bool rag) {
-    NormShape s;
+constexpr NormShape norm_shape(int D, bool rag) {
+    NormShape s = {};
     s.nv = D <= 16 * kNormThreads ? 2 : 4;
     if (rag) {
         s.tpr = (D + s.nv * 8 * 32 - 1) / (s.nv * 8 * 32) * 32;
@@ -44,6 +44,16 @@ inline NormShape norm_shape(int D, bool rag) {
     }
     return s;
 }
+
+// Every width's threads cover it, fit a block and have a row: a shape without one would walk no rows and never end.
+constexpr bool norm_shapes_hold(int from, int to, bool rag) {
+    for (int D = from; D <= to; ++D) {
+        const NormShape s = norm_shape(D, rag);
+        if (s.rpb < 1 || s.threads != s.tpr * s.rpb || s.threads > kNormThreads || s.tpr * s.nv * 8 < D || (rag && s.tpr % 32)) return false;
+    }
+    return true;
+}
+static_assert(norm_shapes_hold(1, GDR_NORM_MAX_D, false) && norm_shapes_hold(1, GDR_NORM_MAX_D, true), "norm shapes");
 
 // Blocks: at most as many as are resident at once; each walks rows, with its weights at hand and its next row's loads
 // in flight.
