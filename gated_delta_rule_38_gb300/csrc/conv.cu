@@ -43,7 +43,7 @@ struct ConvArgs {
 
 // A thread's NC channels: NC consecutive ones from one access (WIDE), or, where rows are not aligned for that, every
 // 32nd, so that the lanes of a warp still read and write contiguous elements.
-template <int NC, bool WIDE>
+template <bool WIDE>
 struct Lane {
     int c;  // first channel
     int D;
@@ -53,17 +53,13 @@ struct Lane {
 
 // The raw elements of one token: NC / 2 words of two channels each, or (narrow) one register an element, so that
 // nothing waits for a load before its use.
-template <int NC, bool WIDE>
+template <bool WIDE>
 struct Raw {
     uint32_t w[WIDE ? NC / 2 : NC];
-    __device__ __forceinline__ void load(const uint16_t *p, const Lane<NC, WIDE> &l) {  // p: the token's row
+    __device__ __forceinline__ void load(const uint16_t *p, const Lane<WIDE> &l) {  // p: the token's row
         if constexpr (WIDE) {
-            if constexpr (NC == 4) {
-                const uint2 u = *reinterpret_cast<const uint2 *>(p + l.c);
-                w[0] = u.x, w[1] = u.y;
-            } else {
-                w[0] = *reinterpret_cast<const uint32_t *>(p + l.c);
-            }
+            const uint2 u = *reinterpret_cast<const uint2 *>(p + l.c);
+            w[0] = u.x, w[1] = u.y;
         } else {
 #pragma unroll
             for (int i = 0; i < NC; ++i) w[i] = l.has(i) ? p[l.chan(i)] : 0;
@@ -75,22 +71,19 @@ struct Raw {
         for (int i = 0; i < NC / 2; ++i) o[i] = widen2<T>(WIDE ? w[i] : w[2 * i % (WIDE ? NC / 2 : NC)] | w[(2 * i + 1) % (WIDE ? NC / 2 : NC)] << 16);
     }
 };
-template <typename T, int NC, bool WIDE>
-__device__ __forceinline__ void load_x(const void *p, long long row, const Lane<NC, WIDE> &l, f2 *o) {  // contiguous rows
-    Raw<NC, WIDE> r;
+template <typename T, bool WIDE>
+__device__ __forceinline__ void load_x(const void *p, long long row, const Lane<WIDE> &l, f2 *o) {  // contiguous rows
+    Raw<WIDE> r;
     r.load(static_cast<const uint16_t *>(p) + row * l.D, l);
     r.template widen<T>(o);
 }
-template <typename T, int NC, bool WIDE>
-__device__ __forceinline__ void store_at(uint16_t *p, const Lane<NC, WIDE> &l, const f2 *v) {  // p: the token's row
+template <typename T, bool WIDE>
+__device__ __forceinline__ void store_at(uint16_t *p, const Lane<WIDE> &l, const f2 *v) {  // p: the token's row
     uint32_t w[NC / 2];
 #pragma unroll
     for (int i = 0; i < NC / 2; ++i) w[i] = narrow2<T>(v[i]);
     if constexpr (WIDE) {
-        if constexpr (NC == 4)
-            *reinterpret_cast<uint2 *>(p + l.c) = make_uint2(w[0], w[1]);
-        else
-            *reinterpret_cast<uint32_t *>(p + l.c) = w[0];
+        *reinterpret_cast<uint2 *>(p + l.c) = make_uint2(w[0], w[1]);
     } else {
 #pragma unroll
         for (int i = 0; i < NC; ++i)
@@ -98,29 +91,24 @@ __device__ __forceinline__ void store_at(uint16_t *p, const Lane<NC, WIDE> &l, c
     }
 }
 
-template <typename T, int NC, bool WIDE>
-__device__ __forceinline__ void store_x(void *base, long long row, const Lane<NC, WIDE> &l, const f2 *v) {
-    store_at<T, NC, WIDE>(static_cast<uint16_t *>(base) + row * l.D, l, v);
+template <typename T, bool WIDE>
+__device__ __forceinline__ void store_x(void *base, long long row, const Lane<WIDE> &l, const f2 *v) {
+    store_at<T, WIDE>(static_cast<uint16_t *>(base) + row * l.D, l, v);
 }
 
 // Taps w[j] (of the input j tokens back) and bias.
-template <typename T, int NC, int W, bool WIDE>
+template <typename T, int W, bool WIDE>
 struct Taps {
     f2 w[W][NC / 2], bias[NC / 2];
-    __device__ __forceinline__ void load(const ConvArgs &a, const Lane<NC, WIDE> &l) {
+    __device__ __forceinline__ void load(const ConvArgs &a, const Lane<WIDE> &l) {
         float v[NC * W], b[NC];
         if (WIDE && !a.w_f32 && a.w_wide) {  // NC W consecutive elements
             const uint32_t *p = reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(a.w) + (long long)l.c * W);
             uint32_t u[NC * W / 2];
 #pragma unroll
             for (int i = 0; i < NC * W / 2; i += 2) {
-                if constexpr (NC == 4) {
-                    const uint2 q = *reinterpret_cast<const uint2 *>(p + i);
-                    u[i] = q.x, u[i + 1] = q.y;
-                } else {
-                    u[i] = p[i];
-                    if (i + 1 < NC * W / 2) u[i + 1] = p[i + 1];
-                }
+                const uint2 q = *reinterpret_cast<const uint2 *>(p + i);
+                u[i] = q.x, u[i + 1] = q.y;
             }
 #pragma unroll
             for (int i = 0; i < NC * W / 2; ++i) unpack2(widen2<T>(u[i]), v[2 * i], v[2 * i + 1]);
@@ -147,7 +135,7 @@ struct Taps {
     }
 };
 
-template <int NC, int W>
+template <int W>
 __device__ __forceinline__ void push(f2 (*xs)[NC / 2], const f2 *x) {
 #pragma unroll
     for (int j = W - 1; j > 1; --j)
@@ -158,12 +146,12 @@ __device__ __forceinline__ void push(f2 (*xs)[NC / 2], const f2 *x) {
 }
 
 // The cached inputs of sequence n (zeros without them): xs[j-1] = input j tokens before its first.
-template <typename T, int NC, int W, bool WIDE>
-__device__ __forceinline__ void cached_inputs(const ConvArgs &a, long long n, const Lane<NC, WIDE> &l, f2 (*xs)[NC / 2]) {
+template <typename T, int W, bool WIDE>
+__device__ __forceinline__ void cached_inputs(const ConvArgs &a, long long n, const Lane<WIDE> &l, f2 (*xs)[NC / 2]) {
 #pragma unroll
     for (int j = 1; j < W; ++j) {
         if (a.state_in) {
-            load_x<T, NC, WIDE>(a.state_in, n * (W - 1) + (W - 1 - j), l, xs[j - 1]);
+            load_x<T, WIDE>(a.state_in, n * (W - 1) + (W - 1 - j), l, xs[j - 1]);
         } else {
 #pragma unroll
             for (int i = 0; i < NC / 2; ++i) xs[j - 1][i] = 0ull;
@@ -172,18 +160,18 @@ __device__ __forceinline__ void cached_inputs(const ConvArgs &a, long long n, co
 }
 
 // The W - 1 inputs before token t0 of a sequence that starts at token `start` of the row: tokens of it, or cached.
-template <typename T, int NC, int W, bool WIDE>
+template <typename T, int W, bool WIDE>
 __device__ __forceinline__ void inputs_before(const ConvArgs &a, const uint16_t *row, int t0, int start, long long n,
-                                              const Lane<NC, WIDE> &l, f2 (*xs)[NC / 2]) {
+                                              const Lane<WIDE> &l, f2 (*xs)[NC / 2]) {
 #pragma unroll
     for (int j = 1; j < W; ++j) {
         const int back = j - (t0 - start);  // > 0: that many tokens before the sequence's first
         if (back <= 0) {
-            Raw<NC, WIDE> r;
+            Raw<WIDE> r;
             r.load(row + (long long)(t0 - j) * a.x_ld, l);
             r.template widen<T>(xs[j - 1]);
         } else if (a.state_in && back < W) {
-            load_x<T, NC, WIDE>(a.state_in, n * (W - 1) + (W - 1 - back), l, xs[j - 1]);
+            load_x<T, WIDE>(a.state_in, n * (W - 1) + (W - 1 - back), l, xs[j - 1]);
         } else {
 #pragma unroll
             for (int i = 0; i < NC / 2; ++i) xs[j - 1][i] = 0ull;
@@ -192,8 +180,8 @@ __device__ __forceinline__ void inputs_before(const ConvArgs &a, const uint16_t 
 }
 
 // Block -> channels of this lane and (row, first token) of this warp's walk; false past either end.
-template <int NC, bool WIDE>
-__device__ __forceinline__ bool my_walk(const ConvArgs &a, Lane<NC, WIDE> &l, int &b, int &t0, long long &tblock) {
+template <bool WIDE>
+__device__ __forceinline__ bool my_walk(const ConvArgs &a, Lane<WIDE> &l, int &b, int &t0, long long &tblock) {
     const unsigned tb = (__umulhi(blockIdx.x, a.cblocks_m) + blockIdx.x) >> a.cblocks_s;
     tblock = tb;
     const int c0 = (int)(blockIdx.x - tb * a.cblocks) * 32 * NC;
@@ -223,7 +211,7 @@ struct Pipe {
     uint32_t ring;          // this lane's or the warp's part of slot 0
     int lane, need;         // bytes of a row that the warp needs
     __device__ __forceinline__ void init(unsigned char *smem, const void *base, long long rows, long long ld_, long long row,
-                                         const Lane<NC, WIDE> &l) {
+                                         const Lane<WIDE> &l) {
         lane = threadIdx.x;
         ld = ld_;
         const int c0 = WIDE ? l.c : l.c - lane;
@@ -298,7 +286,7 @@ __global__ void __launch_bounds__(32 * WALKS, WIDE ? 4 : 3) conv_fwd_kernel(cons
     constexpr int U = 4, GROUPS = kAhead / U;   // tokens a group of copies; groups
     extern __shared__ __align__(16) unsigned char ring[];
     if (PACKED && blockIdx.x == 0 && threadIdx.y == 0) check_cu(a.cu, a.N, a.T, a.err);
-    Lane<NC, WIDE> l;
+    Lane<WIDE> l;
     int b, t0;
     long long tblock;
     if (!my_walk(a, l, b, t0, tblock)) return;
@@ -316,24 +304,24 @@ __global__ void __launch_bounds__(32 * WALKS, WIDE ? 4 : 3) conv_fwd_kernel(cons
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) fetch(t0 + g * U, g);
     uint16_t *out = static_cast<uint16_t *>(a.y) + (row0 + t0) * a.D;
-    Taps<T, NC, W, WIDE> taps;
+    Taps<T, W, WIDE> taps;
     taps.load(a, l);
     SeqWalk sw;
     if (PACKED) sw.find(a.cu, a.N, t0);
     long long seq = PACKED ? sw.cur() : b;
     f2 xs[W - 1][NC / 2];
     if (PACKED && sw.bound == t0)
-        cached_inputs<T, NC, W, WIDE>(a, seq, l, xs);  // (replaced at the first token)
+        cached_inputs<T, W, WIDE>(a, seq, l, xs);  // (replaced at the first token)
     else
-        inputs_before<T, NC, W, WIDE>(a, row, t0, PACKED ? max(0, a.cu[seq]) : 0, seq, l, xs);
+        inputs_before<T, W, WIDE>(a, row, t0, PACKED ? max(0, a.cu[seq]) : 0, seq, l, xs);
     auto write_state = [&](long long n, const f2(*s)[NC / 2]) {
         if (!a.state_out) return;
 #pragma unroll
-        for (int j = 1; j < W; ++j) store_x<T, NC, WIDE>(a.state_out, n * (W - 1) + (W - 1 - j), l, s[j - 1]);
+        for (int j = 1; j < W; ++j) store_x<T, WIDE>(a.state_out, n * (W - 1) + (W - 1 - j), l, s[j - 1]);
     };
     auto empty = [&](long long n) {
         f2 e[W - 1][NC / 2];
-        cached_inputs<T, NC, W, WIDE>(a, n, l, e);
+        cached_inputs<T, W, WIDE>(a, n, l, e);
         write_state(n, e);
     };
     // U tokens from t; CHECKED: some of them may lie past t1, or a sequence may start or end among them
@@ -343,7 +331,7 @@ __global__ void __launch_bounds__(32 * WALKS, WIDE ? 4 : 3) conv_fwd_kernel(cons
             if (checked.value && t + u >= t1) break;
             if (PACKED && checked.value && t + u == sw.bound && sw.step(t + u, empty)) {
                 seq = sw.cur();
-                cached_inputs<T, NC, W, WIDE>(a, seq, l, xs);
+                cached_inputs<T, W, WIDE>(a, seq, l, xs);
             }
             f2 x[NC / 2], y[NC / 2];
             px.template take<T>(g * U + u, x);
@@ -352,9 +340,9 @@ __global__ void __launch_bounds__(32 * WALKS, WIDE ? 4 : 3) conv_fwd_kernel(cons
                 y[i] = taps.pre(i, x[i], xs);
                 if (a.silu) y[i] = mul2(y[i], sigmoid2(y[i]));
             }
-            store_at<T, NC, WIDE>(out, l, y);
+            store_at<T, WIDE>(out, l, y);
             out += a.D;
-            push<NC, W>(xs, x);
+            push<W>(xs, x);
             if (PACKED && checked.value && t + u + 1 == sw.bound) write_state(seq, xs);
         }
     };
@@ -379,16 +367,16 @@ __global__ void __launch_bounds__(32 * WALKS, WIDE ? 4 : 3) conv_fwd_kernel(cons
 // the latency of one round of loads a block: 256 x 12288 takes 12.3 us for 50 MB, 4.1 TB/s.
 template <typename T, int W, bool WIDE>
 __global__ void __launch_bounds__(32 * WALKS, 5) conv_step_kernel(const ConvArgs a) {
-    Lane<NC, WIDE> l;
+    Lane<WIDE> l;
     int b, t0;
     long long tblock;
     if (!my_walk(a, l, b, t0, tblock)) return;
     const uint16_t *row = static_cast<const uint16_t *>(a.x) + (long long)b * a.T * a.x_ld;
-    Raw<NC, WIDE> raw;
+    Raw<WIDE> raw;
     raw.load(row, l);
     f2 xs[W - 1][NC / 2];
-    cached_inputs<T, NC, W, WIDE>(a, b, l, xs);
-    Taps<T, NC, W, WIDE> taps;
+    cached_inputs<T, W, WIDE>(a, b, l, xs);
+    Taps<T, W, WIDE> taps;
     taps.load(a, l);
     for (int t = 0; t < a.T; ++t) {
         f2 x[NC / 2], y[NC / 2];
@@ -399,11 +387,11 @@ __global__ void __launch_bounds__(32 * WALKS, 5) conv_step_kernel(const ConvArgs
             y[i] = taps.pre(i, x[i], xs);
             if (a.silu) y[i] = mul2(y[i], sigmoid2(y[i]));
         }
-        store_x<T, NC, WIDE>(a.y, (long long)b * a.T + t, l, y);
-        push<NC, W>(xs, x);
+        store_x<T, WIDE>(a.y, (long long)b * a.T + t, l, y);
+        push<W>(xs, x);
     }
 #pragma unroll
-    for (int j = 1; j < W; ++j) store_x<T, NC, WIDE>(a.state_out, (long long)b * (W - 1) + (W - 1 - j), l, xs[j - 1]);
+    for (int j = 1; j < W; ++j) store_x<T, WIDE>(a.state_out, (long long)b * (W - 1) + (W - 1 - j), l, xs[j - 1]);
 }
 
 // The sums of dw, db and dx of 4 channels stay in registers (126 a thread): two blocks an SM, which the latency of the
@@ -416,7 +404,7 @@ __global__ void __launch_bounds__(32 * WALKS, 2) conv_bwd_kernel(const ConvArgs 
     extern __shared__ __align__(16) unsigned char ring[];  // two rings, then the walks' sums in their place
     float(*s_part)[NP][32] = reinterpret_cast<float(*)[NP][32]>(ring);
     if (PACKED && blockIdx.x == 0 && threadIdx.y == 0) check_cu(a.cu, a.N, a.T, a.err);
-    Lane<NC, WIDE> l;
+    Lane<WIDE> l;
     int b, t0;
     long long tblock;
     const bool live = my_walk(a, l, b, t0, tblock);
@@ -446,7 +434,7 @@ __global__ void __launch_bounds__(32 * WALKS, 2) conv_bwd_kernel(const ConvArgs 
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) fetch(t0 + g * U, g);
         uint16_t *out = static_cast<uint16_t *>(a.dx) + (row0 + t0 - (W - 1)) * a.D;  // (stored to from token t0 on)
-        Taps<T, NC, W, WIDE> taps;
+        Taps<T, W, WIDE> taps;
         taps.load(a, l);
         f2 xs[W - 1][NC / 2], acc[W - 1][NC / 2];  // acc[j-1]: the open sum of dx, j tokens back
 #pragma unroll
@@ -460,15 +448,15 @@ __global__ void __launch_bounds__(32 * WALKS, 2) conv_bwd_kernel(const ConvArgs 
         int start = 0;
         if (PACKED && sw.bound != t0) start = max(0, a.cu[seq]);
         if (PACKED && sw.bound == t0)
-            cached_inputs<T, NC, W, WIDE>(a, seq, l, xs);  // (replaced at the first token)
+            cached_inputs<T, W, WIDE>(a, seq, l, xs);  // (replaced at the first token)
         else
-            inputs_before<T, NC, W, WIDE>(a, row, t0, start, seq, l, xs);
+            inputs_before<T, W, WIDE>(a, row, t0, start, seq, l, xs);
         // A finished sum: of an input of this walk, or of a cached input of a sequence that starts in it.
         auto emit = [&](int s, const f2 *v) {
             if (s >= start) {
-                if (s >= t0 && s < t1) store_x<T, NC, WIDE>(a.dx, row0 + s, l, v);
+                if (s >= t0 && s < t1) store_x<T, WIDE>(a.dx, row0 + s, l, v);
             } else if (start >= t0 && a.dstate_in && W - 1 + s - start >= 0) {
-                store_x<T, NC, WIDE>(a.dstate_in, seq * (W - 1) + (W - 1 + s - start), l, v);
+                store_x<T, WIDE>(a.dstate_in, seq * (W - 1) + (W - 1 + s - start), l, v);
             }
         };
         // The last W - 1 sums of a sequence that ends at token e: also the final state's gradient.
@@ -477,7 +465,7 @@ __global__ void __launch_bounds__(32 * WALKS, 2) conv_bwd_kernel(const ConvArgs 
             for (int j = W - 1; j >= 1; --j) {
                 if (a.dstate_out) {
                     f2 d[NC / 2];
-                    load_x<T, NC, WIDE>(a.dstate_out, seq * (W - 1) + (W - 1 - j), l, d);
+                    load_x<T, WIDE>(a.dstate_out, seq * (W - 1) + (W - 1 - j), l, d);
 #pragma unroll
                     for (int i = 0; i < NC / 2; ++i) acc[j - 1][i] = add2(acc[j - 1][i], d[i]);
                 }
@@ -493,8 +481,8 @@ __global__ void __launch_bounds__(32 * WALKS, 2) conv_bwd_kernel(const ConvArgs 
                 f2 d[NC / 2];
 #pragma unroll
                 for (int i = 0; i < NC / 2; ++i) d[i] = 0ull;
-                if (a.dstate_out) load_x<T, NC, WIDE>(a.dstate_out, n * (W - 1) + j, l, d);
-                store_x<T, NC, WIDE>(a.dstate_in, n * (W - 1) + j, l, d);
+                if (a.dstate_out) load_x<T, WIDE>(a.dstate_out, n * (W - 1) + j, l, d);
+                store_x<T, WIDE>(a.dstate_in, n * (W - 1) + j, l, d);
             }
         };
         bool open = true;  // the walk's last sequence is still to be flushed
@@ -512,7 +500,7 @@ __global__ void __launch_bounds__(32 * WALKS, 2) conv_bwd_kernel(const ConvArgs 
                     if (sw.step(t + u, empty)) {
                         seq = sw.cur();
                         start = t + u;
-                        cached_inputs<T, NC, W, WIDE>(a, seq, l, xs);
+                        cached_inputs<T, W, WIDE>(a, seq, l, xs);
                     }
                 }
                 const bool mine = !checked.value || t + u < t1;
@@ -537,11 +525,11 @@ __global__ void __launch_bounds__(32 * WALKS, 2) conv_bwd_kernel(const ConvArgs 
                         db[i] = add2(db[i], d[i]);
                     }
                 }
-                push<NC, W>(xs, x);
+                push<W>(xs, x);
                 if (checked.value)
                     emit(t + u - (W - 1), done);
                 else
-                    store_at<T, NC, WIDE>(out, l, done);
+                    store_at<T, WIDE>(out, l, done);
                 out += a.D;
             }
         };
@@ -553,7 +541,7 @@ __global__ void __launch_bounds__(32 * WALKS, 2) conv_bwd_kernel(const ConvArgs 
             else
                 tokens(t, g, Flag<true>());
             if (!WIDE) __syncwarp();  // (all lanes have read the slots)
-        fetch(t + GROUPS * U, g);
+            fetch(t + GROUPS * U, g);
             g = g + 1 == GROUPS ? 0 : g + 1;
         }
         cp_async_wait<0>();

@@ -110,15 +110,6 @@ struct Chans {
 
 // ---------------------------------------------------------------- tiles
 
-// Eight 16-bit elements from p; `n` of them exist.
-__device__ __forceinline__ uint4 load8(const uint16_t *p, int n, bool vec) {
-    if (vec && n >= 8) return *reinterpret_cast<const uint4 *>(p);
-    uint32_t r[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (i < n) r[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
-    return make_uint4(r[0], r[1], r[2], r[3]);
-}
 // Eight 16-bit elements as four fp32 pairs, and back.
 template <typename T>
 __device__ __forceinline__ void widen8(uint4 u, f2 *o) {
@@ -148,13 +139,12 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;\n" ::"n"(LEFT) : "memory");
 }
 
-// Eight elements into this thread's own place in shared memory: an asynchronous copy where all of them exist, else
-// plain loads.  `n` of them exist; the others become zeros.
-__device__ __forceinline__ void copy8(uint16_t *to, const uint16_t *from, int n, bool vec) {
-    if (vec && n >= 8)
+// Eight elements into shared memory: an asynchronous copy, or zeros where they do not exist.
+__device__ __forceinline__ void copy8(uint16_t *to, const uint16_t *from, bool exist) {
+    if (exist)
         copy16(to, from);
     else
-        *reinterpret_cast<uint4 *>(to) = load8(from, n, false);
+        *reinterpret_cast<uint4 *>(to) = make_uint4(0, 0, 0, 0);
 }
 
 // Rows of a tensor that allows no 16-byte accesses (odd widths or strides, views at any element).  Threads copy the

@@ -120,7 +120,7 @@ struct Tiles {
 #pragma unroll
                     for (int k = 0; k < W::VPT; ++k) {
                         const int j = vt + k * W::VSTEP;
-                        if (j < rows && vn > 0) copy8(raw(buf, m, j, true) + vc, src(m).at(row0 + base + j) + vc, vn, true);
+                        if (j < rows && vn > 0) copy16(raw(buf, m, j, true) + vc, src(m).at(row0 + base + j) + vc);
                     }
                 } else {
                     copy_rows<W::NT, W::CB / 8 + 1>(raw(buf, m, 0, false), S::row(false), src(m), row0 + base, rows, ch.count);
@@ -132,7 +132,7 @@ struct Tiles {
                     copy_rows<W::NT, W::NP / 8 + 2>(rag_bc(buf, m, 0), S::RB, src_bc(m), row0 + base, rows, a.N);
                 } else if constexpr (W::BW == 8) {
                     if (bt < rows)
-                        copy8(&sm.raw_bc[buf][m][bt][bn], src_bc(m).at(row0 + base + bt) + bn, a.N - bn, true);
+                        copy8(&sm.raw_bc[buf][m][bt][bn], src_bc(m).at(row0 + base + bt) + bn, bn < a.N);
                     else if (bt < TT)  // past the end: zeros
                         *reinterpret_cast<uint4 *>(&sm.raw_bc[buf][m][bt][bn]) = make_uint4(0, 0, 0, 0);
                 }

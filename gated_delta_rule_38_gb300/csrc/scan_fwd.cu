@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(128, FULL ? 5 : 6) scan_fwd_kernel(const ScanA
                     if (vlive && j < rows && vn > 0)
 #pragma unroll
                         for (int m = 0; m < (FULL ? 3 : 2); ++m)
-                            if (m < tensors) copy8(sm.raw(buf, m, j, true) + vc, src[m].at(row0 + base + j) + vc, vn, true);
+                            if (m < tensors) copy16(sm.raw(buf, m, j, true) + vc, src[m].at(row0 + base + j) + vc);
                 }
             } else {
 #pragma unroll
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(128, FULL ? 5 : 6) scan_fwd_kernel(const ScanA
                     copy_rows<128, NP / 8 + 2>(sm.rag_bc(buf, m, 0, vec), sm.RB, src_bc[m], row0 + base, rows, a.N);
                 } else if constexpr (BW == 8) {
                     if (bt < rows)
-                        copy8(&sm.raw_bc[buf][m][bt][bn], src_bc[m].at(row0 + base + bt) + bn, a.N - bn, true);
+                        copy8(&sm.raw_bc[buf][m][bt][bn], src_bc[m].at(row0 + base + bt) + bn, bn < a.N);
                     else if (bt < TT)  // past the end: zeros
                         *reinterpret_cast<uint4 *>(&sm.raw_bc[buf][m][bt][bn]) = make_uint4(0, 0, 0, 0);
                 }
