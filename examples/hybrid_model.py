@@ -34,7 +34,8 @@ class Conv(nn.Module):
             return y
         if x.shape[1] == 1 and "conv" in state:
             return gdr.short_conv_step(x, state["conv"], self.weight, activation="silu")
-        y, state["conv"] = gdr.short_conv_fwd(x, self.weight, activation="silu", output_final_state=True, cu_seqlens=cu)
+        y, state["conv"] = gdr.short_conv_fwd(x, self.weight, activation="silu", initial_state=state.get("conv"),
+                                              output_final_state=True, cu_seqlens=cu)
         return y
 
 
@@ -62,7 +63,8 @@ class DeltaMixer(nn.Module):
             o, _ = gdr.recurrent_gated_delta_rule(*(t.contiguous() for t in (q, k, v, g + 2, beta)),
                                                   initial_state=state["delta"], inplace=True, **act)
         else:
-            o, state["delta"] = gdr.chunk_gated_delta_rule(q, k, v, g + 2, beta, cu_seqlens=cu, output_final_state=True, **act)
+            o, state["delta"] = gdr.chunk_gated_delta_rule(q, k, v, g + 2, beta, initial_state=state.get("delta"), cu_seqlens=cu,
+                                                           output_final_state=True, **act)
         return self.out(o.reshape(B, T, self.inner))
 
 
@@ -90,7 +92,7 @@ class ScanMixer(nn.Module):
         elif x.shape[1] == 1 and "scan" in state:
             y = gdr.selective_scan_step(*args, state["scan"], **opt)
         else:
-            y, state["scan"], _ = gdr.selective_scan_fwd(*args, cu_seqlens=cu, **opt)
+            y, state["scan"], _ = gdr.selective_scan_fwd(*args, initial_state=state.get("scan"), cu_seqlens=cu, **opt)
         return self.out(y)
 
 
@@ -103,7 +105,8 @@ class Model(nn.Module):
         self.head = linear(width, vocab)
 
     def forward(self, tokens, cu=None, states=None):
-        """Logits; ``states`` (a list of one dict a block) is filled by a prompt and advanced by single tokens."""
+        """Logits; ``states`` (a list of one dict a block) is filled by a prompt and advanced by single tokens or by more
+        of the prompts."""
         h = self.embed(tokens).float()  # the residual stream is fp32
         y = torch.zeros_like(h, dtype=BF)
         for i, mixer in enumerate(self.mixers):
