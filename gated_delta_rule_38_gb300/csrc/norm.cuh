@@ -117,6 +117,36 @@ __device__ __forceinline__ float lanes_max(float m, int lanes) {
 // The scale of columns whose largest magnitude is m.  (A NaN stays.)
 __device__ __forceinline__ float scale_of(float m) { return (m < 1e-30f ? 1e-30f : m) / 448.0f; }
 
+// y / scale to the nearest fp32 number from one reciprocal a scale: the quotient's estimate y (1 / scale) is off by an ulp or
+// two, its remainder is exact in one fused operation, and the remainder times the reciprocal corrects it (Markstein, IBM
+// Journal of Research and Development 34, 1990).  Small rows are taken 2^64 times as large, so that no remainder
+// underflows; an infinite scale has no remainder and makes what is finite 0.  (Equal to the division in 6e10 pairs tried, most
+// of them beside ties of the 8-bit type, where the estimate alone falls on the other side.  8192 x 4096 from an fp32 stream:
+// 66 us as with the estimate, 70 with a division an element; ragged 7203 x 4381: 126 us, 117 and 138.)
+struct Quotient {
+    float up, rs, neg;
+    __device__ __forceinline__ Quotient() {}
+    __device__ __forceinline__ explicit Quotient(float scale) {
+        up = scale < 1e-25f ? 0x1p64f : 1.f;
+        const float s = scale * up;
+        rs = 1.0f / s;
+        neg = s < __int_as_float(0x7f800000) ? -s : 0.f;
+    }
+    __device__ __forceinline__ float of(float y) const {
+        y *= up;
+        const float q = y * rs;
+        return fmaf(fmaf(q, neg, y), rs, q);
+    }
+    __device__ __forceinline__ float2 of(f2 y) const {
+        y = mul2(y, both(up));
+        f2 q = mul2(y, both(rs));
+        q = fma2(fma2(q, both(neg), y), both(rs), q);
+        float2 r;
+        unpack2(q, r.x, r.y);
+        return r;
+    }
+};
+
 // Registers: 16 elements a thread leave room for three blocks of 256 an SM with the weights and the next row's loads held
 // in registers.  Rows over 8,192 take 32 elements a thread and hold neither.
 template <int NV, int BT>
@@ -214,12 +244,13 @@ __global__ void __launch_bounds__(BT, Bounds<NV, BT>::fwd) norm_fwd_kernel(const
                 const int c = (v * tpr + t) * 8;
                 if (!(live && c < D)) continue;
                 const float scale = scale_of(m[v]);
-                const float *e = y + v * 8;
+                const Quotient quot(scale);
+                const f2 *e = h + v * 4;
                 uint32_t u[2];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(e[4 * i] / scale, e[4 * i + 1] / scale), __NV_SATFINITE, __NV_E4M3);
-                    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(e[4 * i + 2] / scale, e[4 * i + 3] / scale), __NV_SATFINITE, __NV_E4M3);
+                    const uint32_t lo = __nv_cvt_float2_to_fp8x2(quot.of(e[2 * i]), __NV_SATFINITE, __NV_E4M3);
+                    const uint32_t hi = __nv_cvt_float2_to_fp8x2(quot.of(e[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
                     u[i] = lo | (hi << 16);
                 }
                 *reinterpret_cast<uint2 *>(static_cast<unsigned char *>(a.y) + row * D + c) = make_uint2(u[0], u[1]);
@@ -507,35 +538,37 @@ __global__ void __launch_bounds__(BT, RagBounds<EPT, BT>::blocks) norm_fwd_ragge
                 if (lane == 0) s_chunk[j * wpr + (t >> 5)] = __uint_as_float(m);
             }
             __syncthreads();
-            // one thread a scale: the largest of its columns' maxima, which the scale then replaces
+            // one thread a scale: the largest of its columns' maxima, which the scale's quotient then replaces
             const int used = (D + 31) / 32;
-            float own[2] = {0.f, 0.f};
+            Quotient own[2];
             if (a.group) {
                 for (int i = 0, q = t; q < a.nscale; ++i, q += tpr) {
                     float m = s_chunk[4 * q];
 #pragma unroll
                     for (int k = 1; k < 4; ++k)
                         if (4 * q + k < used) m = max_abs(m, s_chunk[4 * q + k]);
-                    own[i & 1] = scale_of(m);
-                    if (live) a.scale[row * a.nscale + q] = own[i & 1];
+                    const float scale = scale_of(m);
+                    own[i & 1] = Quotient(scale);
+                    if (live) a.scale[row * a.nscale + q] = scale;
                 }
             } else {
                 float m = 0.f;
                 for (int i = lane; i < used; i += 32) m = max_abs(m, s_chunk[i]);
-                own[0] = scale_of(lanes_max(m, 32));
-                if (live && t == 0) a.scale[row] = own[0];
+                const float scale = scale_of(lanes_max(m, 32));
+                own[0] = Quotient(scale);
+                if (live && t == 0) a.scale[row] = scale;
             }
             if (a.group) {
                 __syncthreads();
-                for (int i = 0, q = t; q < a.nscale; ++i, q += tpr) s_chunk[4 * q] = own[i & 1];
+                for (int i = 0, q = t; q < a.nscale; ++i, q += tpr) *reinterpret_cast<Quotient *>(s_chunk + 4 * q) = own[i & 1];
                 __syncthreads();
             }
 #pragma unroll
             for (int j = 0; j < EPT; ++j) {
                 const int c = t + j * tpr;
                 if (!(live && c < D)) continue;
-                const float scale = a.group ? s_chunk[(c >> 7) * 4] : own[0];
-                static_cast<unsigned char *>(a.y)[row * D + c] = __nv_cvt_float_to_fp8(h[j] / scale, __NV_SATFINITE, __NV_E4M3);
+                const float q = a.group ? reinterpret_cast<const Quotient *>(s_chunk + (c >> 7) * 4)->of(h[j]) : own[0].of(h[j]);
+                static_cast<unsigned char *>(a.y)[row * D + c] = __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
             }
             __syncthreads();  // (the maxima have been read)
         }

@@ -44,6 +44,29 @@ def test_e4m3_rounds_the_quotient(group, shift):
     assert torch.equal(q.float().cpu(), want.float().expand(R, -1))
 
 
+@pytest.mark.parametrize("top", [1e-31, 3e-29, 1e-25, 1e-20, 1e30, 3e38])
+@pytest.mark.parametrize("shift", [0, 1], ids=["vectors", "ragged"])
+def test_e4m3_of_very_small_and_large_rows(shift, top):
+    """The quotient holds at both ends of the scales: the least one (of rows below 1e-30), and an infinite one, by which
+    what is finite becomes 0.  A quarter of each row is 2, the rest 0, so that the norm's factor is 1 and y twice the
+    weight."""
+    D = 1024
+    rng = np.random.default_rng(3)
+    w = (np.exp2(rng.uniform(-11, 0, D)) * top * np.where(rng.random(D) < 0.5, -1, 1)).astype(np.float32)
+    w[0] = top
+    x = np.zeros(D, dtype=np.float32)
+    x[::4] = 2
+    with np.errstate(over="ignore", invalid="ignore"):
+        y = x * w
+        m = np.float32(max(np.abs(y).max(), np.float32(1e-30)))
+        scale = np.float32(np.float64(m) / 448) if np.isfinite(m) else m
+        want = torch.from_numpy(y / scale).to(torch.float8_e4m3fn).float()
+    out = torch.empty(D + 1, dtype=torch.float8_e4m3fn, device="cuda")[shift:shift + D].view(1, D)
+    q, _, got = gdr.rms_norm_fwd(torch.from_numpy(x).cuda().to(BF)[None], torch.from_numpy(w).cuda(), eps=0.0, quant="e4m3", out=out)
+    assert got.item() == float(scale)
+    assert torch.equal(q.float().cpu()[0].nan_to_num(1e4), want.nan_to_num(1e4))
+
+
 EDGE = '''
 import sys
 sys.path[:0] = [%r, %r]
