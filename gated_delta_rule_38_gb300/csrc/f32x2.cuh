@@ -37,6 +37,10 @@ __device__ __forceinline__ float sum2(f2 v) {
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
+// Exponentials and reciprocals are the hardware's approximations (relative error 2^-22 and 2^-23 at most, results below
+// 2^-126 flushed): one instruction each, where expf and a division take several.  What that costs was measured against 64 bits: the scan's states after 8,192 and 16,384 tokens at a memory of 2,000 and 20,000
+// are off by 9e-7 and 2e-6, its dA by 1.4e-6 and 3.2e-6 (a plain fp32 recurrence with expf: 2e-5 and 9e-5, 4e-5 and 1e-4).
+
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));

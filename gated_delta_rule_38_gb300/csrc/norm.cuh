@@ -6,14 +6,14 @@
 //   backward at the stored h:  dh_c = r (w_c dy_c - h_c r^2 mean_c(w_c dy_c h_c)) + dresidual_c,
 //                              dw_c = sum over rows of dy_c h_c r
 //
-// Each element is read and written once: a row lives in the registers of its threads (fp32) between the two
-// passes over it that the formulas need, so the kernels are bound by HBM.  A row is spread over TPR threads
+// Each element is read and written once: between the two passes over a row that the formulas need it lives in the
+// registers of its threads (forward, fp32) or in shared memory (backward), so the kernels are bound by HBM.  A row is spread over TPR threads
 // (a power of two, 8 to 512) of EPT elements each; rows narrower than a block share it.  All sums are fp32.
 //
 // Two forms.  Where every row starts on a 16-byte boundary a thread owns whole vectors of 8 columns.  Otherwise
 // (ragged) a block brings rows into shared memory as the aligned 16-byte pieces that hold them, asynchronously and a
-// row ahead, and a thread owns every TPR-th column, so that lanes side by side read and write side by side.  (7203 x 4381:
-// 82 us; 150 with vectors cut at the multiples of 8 elements and weights in shared memory, 167 with single elements.)
+// row ahead, and a thread owns every TPR-th column, so that lanes side by side read and write side by side.  (7203 x 4381 with
+// a residual: 82 us; 150 with vectors cut at the multiples of 8 elements and weights in shared memory, 167 with single elements.)
 #pragma once
 
 #include <cuda_fp8.h>
@@ -155,8 +155,8 @@ struct Bounds {
     static constexpr int fwd = BT == 256 ? 3 : 1;
 };
 
-// 8192 x 4096 bf16: 46 us with a bf16 residual (268 MB, 5.8 TB/s, 86 % of a copy's rate); with an fp32 residual and e4m3
-// output 62 us (369 MB, 5.9 TB/s).
+// 8192 x 4096 bf16, cold caches: 48 us with a bf16 residual (268 MB, 5.6 TB/s, 83 % of a copy's rate); with an fp32 residual
+// and e4m3 output 66 us (369 MB, 5.6 TB/s).
 template <typename T, int NV, int BT, bool QUANT, int RES>
 __global__ void __launch_bounds__(BT, Bounds<NV, BT>::fwd) norm_fwd_kernel(const NormArgs a) {
     constexpr int P = 4 * NV;  // pairs a thread
@@ -322,9 +322,9 @@ struct BwdRows {
 
 // Each block walks rows and keeps its threads' share of dw in registers; the per-block sums are added by
 // reduce_rows_kernel in a fixed order.  The next row comes by asynchronous copies while this one is worked on, and both
-// passes over a row read it from shared memory, so that no registers hold rows.  8192 x 4096 bf16: 52 us for 201 MB, 3.9 TB/s,
-// at two blocks an SM (three, at 80 registers: 56); 2048 x 16384 with a later gradient: 58 us with the reduction for 268 MB
-// (103 with rows in registers, loaded twice).
+// passes over a row read it from shared memory, so that no registers hold rows.  With a later gradient, bf16, cold caches:
+// 8192 x 4096 46 us for 268 MB, 5.8 TB/s, at two blocks an SM (three, at 80 registers, take 4 us more), and 8 us of reduction;
+// 2048 x 16384 58 us with the reduction for 268 MB (103 with rows in registers, loaded twice).
 template <typename T, int NV, int BT, bool F32>
 __global__ void __launch_bounds__(BT, BT > 256 ? 1 : 2) norm_bwd_kernel(const NormArgs a) {
     using R = BwdRows<NV, BT, F32>;

@@ -16,7 +16,7 @@ struct NormArgs {
     float *scale;
     const void *dy;            // backward
     void *dx, *dres;           // backward: dres only for an fp32 residual stream
-    float *dw_part;            // backward: [blocks * rows per block][D]
+    float *dw_part;            // backward: [blocks][D]
     long long rows, x_ld;
     int D, tpr, group, nscale;  // group: 0 = one scale a row
     bool w_f32;

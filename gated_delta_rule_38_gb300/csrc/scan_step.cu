@@ -194,7 +194,8 @@ template <typename T>
 cudaError_t launch_t(const ScanArgs &a, int L, cudaStream_t s) {
     const bool one = a.T == 1;
     const int per = 256 / L, xb = (a.D + per - 1) / per;
-    // Rows a block: as many as leave four blocks an SM, so that a thread's fixed work is shared by them.
+    // Rows a block: as many as leave four blocks an SM, of which two are resident at a time, so that a thread's fixed work is
+    // shared by the rows.
     const long long most = (long long)a.B * xb / (4 * kSMs);
     int chunk = (int)(most / RB * RB);
     chunk = chunk < RB ? RB : chunk > 64 ? 64 : chunk;
