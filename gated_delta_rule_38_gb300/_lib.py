@@ -33,7 +33,8 @@ EXPORTS = ["gdr_max_chunks", "gdr_prepare_chunks", "gdr_fwd_workspace_size", "gd
            "gdr_bwd_ex", "gdr_decode", "gdr_debug_set_wait_polls", "gdr_last_cuda_error",
            "gdr_norm_fwd", "gdr_norm_bwd_workspace_size", "gdr_norm_bwd",
            "gdr_conv_fwd", "gdr_conv_step", "gdr_conv_bwd_workspace_size", "gdr_conv_bwd",
-           "gdr_scan_saved_bytes", "gdr_scan_workspace_size", "gdr_scan_fwd", "gdr_scan_step", "gdr_scan_bwd"]
+           "gdr_scan_saved_bytes", "gdr_scan_workspace_size", "gdr_scan_fwd", "gdr_scan_step", "gdr_scan_bwd",
+           "gdr_lin_workspace_size", "gdr_lin_fwd", "gdr_lin_step", "gdr_lin_bwd"]
 
 
 class Problem(ctypes.Structure):
@@ -67,6 +68,14 @@ class ScanProblem(ctypes.Structure):
         ("x_ld", ctypes.c_int64), ("dt_ld", ctypes.c_int64), ("z_ld", ctypes.c_int64), ("b_ld", ctypes.c_int64),
         ("c_ld", ctypes.c_int64), ("dtype", ctypes.c_int), ("cu_seqlens", ctypes.c_void_p),
         ("num_seqs", ctypes.c_int), ("flags", ctypes.c_uint),
+    ]
+
+
+class LinProblem(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int), ("T", ctypes.c_int), ("Hk", ctypes.c_int), ("H", ctypes.c_int), ("K", ctypes.c_int),
+        ("V", ctypes.c_int), ("q_ld", ctypes.c_int64), ("k_ld", ctypes.c_int64), ("v_ld", ctypes.c_int64),
+        ("dtype", ctypes.c_int), ("scale", ctypes.c_float), ("cu_seqlens", ctypes.c_void_p), ("num_seqs", ctypes.c_int),
     ]
 
 
@@ -136,7 +145,7 @@ def load() -> ctypes.CDLL:
         lib.gdr_debug_set_wait_polls.argtypes = [ctypes.c_longlong]
         lib.gdr_debug_set_wait_polls.restype = i32
         size_p = ctypes.POINTER(ctypes.c_size_t)
-        norm, conv, scan = (ctypes.POINTER(s) for s in (NormProblem, ConvProblem, ScanProblem))
+        norm, conv, scan, lin = (ctypes.POINTER(s) for s in (NormProblem, ConvProblem, ScanProblem, LinProblem))
         for name, args in (
                 ("gdr_norm_fwd", [norm] + [P] * 7), ("gdr_norm_bwd_workspace_size", [norm, size_p]),
                 ("gdr_norm_bwd", [norm] + [P] * 8 + [ctypes.c_size_t, P]),
@@ -145,7 +154,10 @@ def load() -> ctypes.CDLL:
                 ("gdr_conv_bwd", [conv] + [P] * 11 + [ctypes.c_size_t, P]),
                 ("gdr_scan_saved_bytes", [scan, size_p]), ("gdr_scan_workspace_size", [scan, i32, size_p]),
                 ("gdr_scan_fwd", [scan] + [P] * 13 + [ctypes.c_size_t, P]), ("gdr_scan_step", [scan] + [P] * 11),
-                ("gdr_scan_bwd", [scan] + [P] * 22 + [ctypes.c_size_t, P])):
+                ("gdr_scan_bwd", [scan] + [P] * 22 + [ctypes.c_size_t, P]),
+                ("gdr_lin_workspace_size", [lin, i32, size_p]),
+                ("gdr_lin_fwd", [lin] + [P] * 8 + [ctypes.c_size_t, P]), ("gdr_lin_step", [lin] + [P] * 7),
+                ("gdr_lin_bwd", [lin] + [P] * 12 + [ctypes.c_size_t, P])):
             fn = getattr(lib, name)
             fn.argtypes, fn.restype = args, i32
         lib.gdr_version.argtypes = []

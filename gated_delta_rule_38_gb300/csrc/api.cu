@@ -465,7 +465,8 @@ const char *const kKernelNames[K_COUNT] = {"prep_chunks", "wy_fwd",     "chain_f
                                            "chain_rev",   "gate_act",   "pad",       "onechunk_dg",
                                            "norm_fwd",    "norm_bwd",   "conv_fwd",  "conv_bwd",
                                            "scan_local",  "scan_join",  "scan_fwd",  "scan_step",
-                                           "scan_bwd",    "reduce"};
+                                           "scan_bwd",    "reduce",     "lin_states", "lin_fwd",
+                                           "lin_step",    "lin_bwd"};
 struct Pending {
     int id;
     cudaEvent_t a, b;

@@ -1,0 +1,666 @@
+// Linear attention with one decay lambda = exp(decay) a head, in chunks of 128 tokens on tcgen05:
+//
+//   S_t = lambda S_{t-1} + k_t v_t^T,  o_t = scale S_t^T q_t
+//   a chunk of L tokens r, s from the state S before it:
+//     P_rs = lambda^(r-s) q_r . k_s  (s <= r);   o = scale (P V + diag(lambda^(r+1)) Q S)
+//     S <- lambda^L S + (diag(lambda^(L-1-s)) K)^T V
+//
+// The gradients are walks of the same form: dq = scale x the walk (do, v, k) from the transposed states, and backwards in
+// time, where position r sees s >= r, dk = the walk (v, do, scale q) and dv = the walk (k, scale q, do) from the
+// gradient of the final state, which has decayed by lambda^(L-1-r) at row r and by lambda^L at the chunk's start; the
+// keys then enter the state with lambda^(s+1).  So one kernel runs the forward and, three walks side by side, the
+// backward.
+//
+// One CTA of 18 warps walks one segment of a sequence for one head; all tiles are 128 wide (narrower heads load zeros).
+//   warps 0..7    the state: row 32 (w mod 4) + lane, 64 of the 128 columns.  fp32 in registers, a copy rounded to 16
+//                 bits in shared memory as the operand of Q S; between two updates they take the output rows
+//   warps 8..15   P from Q K^T (tensor memory to tensor memory, where it is the left operand of P V), and the decayed
+//                 keys, a 16-bit number and the remainder's 16-bit number each: two products whose sum is as good as
+//                 keys of 16 bits of mantissa, because the states are handed on in fp32 (rounded once they would be
+//                 off by 1e-3; so they are by 4e-6)
+//   warp 16       tile loads (TMA) into a ring of five 32 KB tiles
+//   warp 17       the MMAs
+// The accumulators of one chunk's state update start from zero and are added to the state in fp32 registers, rounded to
+// nearest: in the tensor core's own accumulator the additions of a long walk would lose in one direction.
+// lambda^128 is kept as two fp32 numbers, so that a memory of any length is not off by what rounding it once would add up to.
+//
+// Segments.  Where sequences x heads leave SMs idle the token axis is cut; a first launch (`states_only`) leaves every
+// window's own end state, and a segment begins with the decayed sum of the windows before it, in a fixed order.
+#include "common.cuh"
+#include "f32x2.cuh"
+#include "lin.h"
+#include "seqwalk.cuh"
+#include "umma.cuh"
+
+namespace gdr {
+namespace lin {
+namespace {
+
+constexpr int NT = 576;
+constexpr uint32_t TILE = 32768, BLK = 16384;     // a tile: two blocks of 64 columns, 128 rows each
+constexpr int RING = 5;
+constexpr uint32_t S_LO = RING * TILE;            // the keys' remainders
+constexpr uint32_t S_ST = S_LO + TILE;            // the state's copy (state pass: the remainders of odd chunks)
+constexpr uint32_t S_BAR = S_ST + TILE;
+constexpr uint32_t B_FULL = S_BAR, B_EMPTY = S_BAR + 8 * RING, B_QK = B_EMPTY + 8 * RING, B_S = B_QK + 8, B_P = B_S + 16,
+                   B_K = B_P + 8, B_PV = B_K + 16, B_DS = B_PV + 8, B_DONE = B_DS + 16, S_SLOT = B_DONE + 8, S_FLAG = S_SLOT + 4;
+constexpr uint32_t S_LAM = S_FLAG + 8;            // lambda^128 as two fp32 numbers
+constexpr uint32_t S_BYTES = S_LAM + 8 + 1024;
+static_assert(S_BYTES <= kSmemMost, "shared memory");
+// tensor memory columns: Q K^T and, in its place, P (columns s < 64 at T_P0, the others at T_P1); Q S; P V; the update
+constexpr uint32_t T_QK = 0, T_P0 = 0, T_P1 = 64, T_QS = 128, T_PV = 256, T_DS = 384;
+
+template <typename T> struct IsBf16 { static constexpr bool value = false; };
+template <> struct IsBf16<__nv_bfloat16> { static constexpr bool value = true; };
+
+// ---------------------------------------------------------------- waits
+
+__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+constexpr long kPolls = 8000000L;
+// Waits for a barrier's phase; gives up when another role raised the block's flag, or after a bound (then it raises it).
+__device__ __noinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *flag, unsigned *err) {
+    for (long it = 0; it < kPolls; ++it) {
+        uint32_t done;
+        asm volatile(
+            "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(done)
+            : "r"(bar), "r"(parity), "r"(500u)  // (ns: each try suspends at most about that long)
+            : "memory");
+        if (done) return true;
+        if ((it & 63) == 63 && *flag) return false;
+    }
+    raise_error(err, GDR_ERR_TIMEOUT);
+    *flag = 1;
+    return false;
+}
+// Every lane polls and the warp agrees on the outcome.
+__device__ __forceinline__ bool wwait(uint32_t bar, uint32_t parity, volatile int *flag, unsigned *err) {
+    return __all_sync(0xffffffffu, wait_phase(bar, parity, flag, err));
+}
+
+// ---------------------------------------------------------------- tensor memory
+
+// 32 lanes x 32 or 16 columns; the wait names the registers, so that nothing that uses them moves above it.
+__device__ __forceinline__ void tld32(uint32_t a, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(a));
+}
+__device__ __forceinline__ void tld16(uint32_t a, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(a));
+}
+__device__ __forceinline__ void twait16(uint32_t *r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+__device__ __forceinline__ void twait32(uint32_t *r) {
+    twait16(r);
+    twait16(r + 16);
+}
+__device__ __forceinline__ void tst16(uint32_t a, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(a),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tst_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+// D (+)= A B with A in tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool accumulate) {
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"((uint32_t)accumulate));
+}
+__device__ __forceinline__ f2 f2_of(uint32_t lo, uint32_t hi) {
+    return pack2(__uint_as_float(lo), __uint_as_float(hi));
+}
+
+// ---------------------------------------------------------------- segments
+
+struct Seg {
+    int n;           // sequence, -1: none
+    int t0, t1;      // its tokens, of all rows
+    int seq0, seq1;  // the sequence's
+};
+// Cuts of one length over the sequences.
+struct Cuts {
+    const LinArgs &a;
+    int len;
+    __device__ __forceinline__ Cuts(const LinArgs &a_, int len_) : a(a_), len(len_) {}
+    __device__ __forceinline__ int per() const { return a.T > 0 ? (int)((a.T + (long long)len - 1) / len) : 1; }
+    __device__ __forceinline__ int cu(int n) const { return min(max(a.cu[n], 0), a.T); }
+    // The segment at a place.  Packed: sequence starts and multiples of len in one sorted order (of equal ones the
+    // starts first); the piece from one to the next.  In range whatever cu holds.
+    __device__ Seg at(int slot) const {
+        Seg s;
+        if (!a.cu) {
+            const int w = per();
+            s.n = slot / w;
+            const int i = slot - s.n * w;
+            s.seq0 = s.n * a.T;
+            s.seq1 = s.seq0 + a.T;
+            s.t0 = s.seq0 + (int)min((long long)i * len, (long long)a.T);
+            s.t1 = s.seq0 + (int)min((i + 1ll) * len, (long long)a.T);
+            return s;
+        }
+        // the first `slot` of the sorted order hold p starts: the smallest p with start p behind multiple slot - 1 - p
+        int lo = max(0, slot - (a.T > 0 ? per() : 0)), hi = min(slot, a.N);
+        while (lo < hi) {
+            const int p = (lo + hi) >> 1;
+            if ((long long)cu(p) > (long long)(slot - 1 - p) * len) hi = p;
+            else lo = p + 1;
+        }
+        int p = lo, q = slot - lo;
+        const int W = a.T > 0 ? per() : 0;
+        const bool start = p < a.N && (q >= W || (long long)cu(p) <= (long long)q * len);
+        s.t0 = start ? cu(p) : (int)min((long long)q * len, (long long)a.T);
+        if (start) ++p; else ++q;
+        s.n = p - 1;
+        s.seq0 = s.seq1 = 0;
+        s.t1 = s.t0;
+        if (s.n < 0) return s;
+        s.seq0 = cu(s.n);
+        s.seq1 = max(cu(s.n + 1), s.seq0);
+        s.t1 = min(s.seq1, q < W ? (int)min((long long)q * len, (long long)a.T) : a.T);
+        if (s.t1 < s.t0 || s.t0 < s.seq0) s.t1 = s.t0;
+        // (an empty piece belongs to its sequence only if that is empty: then it hands the state through)
+        if (s.t1 == s.t0 && !(start && s.seq1 == s.seq0)) s.n = -1;
+        return s;
+    }
+    // Within a sequence: the next cut behind t, the last one at or before it, and the place of the piece that begins at t.
+    __device__ __forceinline__ int base(const Seg &s) const { return a.cu ? 0 : s.seq0; }
+    __device__ __forceinline__ int next(const Seg &s, int t) const {
+        const long long c = base(s) + ((long long)(t - base(s)) / len + 1) * len;
+        return (int)min(c, (long long)s.seq1);
+    }
+    __device__ __forceinline__ int last(const Seg &s, int t) const { return base(s) + (t - base(s)) / len * len; }
+    __device__ __forceinline__ long long place(const Seg &s, int t) const {
+        if (!a.cu) return (long long)s.n * per() + (t - s.seq0) / len;
+        return t % len ? (long long)s.n + (s.seq0 + (long long)len - 1) / len : (long long)s.n + 1 + t / len;
+    }
+};
+
+// ---------------------------------------------------------------- the kernel
+
+template <typename T, bool STATES>
+__global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__ LinParams p) {
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem =
+        reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sb = smem_u32(smem);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const LinArgs &a = p.a;
+    const unsigned item = blockIdx.x;
+    const int wi = (int)(item % (unsigned)a.nwalk);
+    const unsigned rest = item / (unsigned)a.nwalk;
+    const int j = (int)(rest % (unsigned)a.H), slot = (int)(rest / (unsigned)a.H);
+    const Walk &w = p.w[wi];
+    const bool rev = w.rev;
+    const int kd = w.kd, vd = w.vd;
+    if (blockIdx.x == 0 && a.cu) check_cu(a.cu, a.N, a.T, a.err);
+
+    const Cuts cuts(a, STATES ? a.win_len : a.main_len);
+    const Seg seg = cuts.at(slot);
+    if (seg.n < 0) return;
+    bool at_start = rev ? seg.t1 == seg.seq1 : seg.t0 == seg.seq0;  // the walk begins (ends) with this segment
+    bool at_end = rev ? seg.t0 == seg.seq0 : seg.t1 == seg.seq1;
+    if (STATES) {
+        // a window's state is wanted where a segment begins behind it
+        const Cuts mc(a, a.main_len);
+        if (rev ? mc.last(seg, seg.t0) <= seg.seq0 : mc.next(seg, seg.t0) >= seg.seq1) return;
+    }
+    const int nc = (seg.t1 - seg.t0 + LC - 1) / LC;
+    if (nc == 0 && !(w.end != nullptr)) return;
+    const bool has_start = !STATES && (w.start != nullptr || !at_start);
+    const bool want_end = STATES || (w.end != nullptr && at_end);
+    volatile int *flag = reinterpret_cast<volatile int *>(smem + S_FLAG);
+    volatile float *lam = reinterpret_cast<volatile float *>(smem + S_LAM);
+    const float g = a.decay[j] < -120.f ? -120.f : a.decay[j];  // (e^-120 is 0 in fp32; 0 x -inf would be NaN)
+    const float lg = g * LOG2E;
+
+    if (tid == 0) {
+        for (int i = 0; i < RING; ++i) {
+            umma::mbar_init(sb + B_FULL + 8 * i, 1);
+            umma::mbar_init(sb + B_EMPTY + 8 * i, 1);
+        }
+        umma::mbar_init(sb + B_QK, 1);
+        umma::mbar_init(sb + B_P, 8);
+        umma::mbar_init(sb + B_PV, 1);
+        for (int i = 0; i < 2; ++i) {
+            umma::mbar_init(sb + B_S + 8 * i, 8);
+            umma::mbar_init(sb + B_K + 8 * i, 8);
+            umma::mbar_init(sb + B_DS + 8 * i, 1);
+        }
+        umma::mbar_init(sb + B_DONE, 1);
+        umma::fence_mbar_init();
+        *flag = 0;
+    }
+    if (tid == 32) {
+        const double l = exp((double)g * LC);
+        lam[0] = (float)l;
+        lam[1] = (float)(l - (double)(float)l);
+    }
+    if (warp == 17) umma::alloc(sb + S_SLOT, 512);
+    umma::fence_before();
+    __syncthreads();
+    umma::fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + S_SLOT);
+
+    // chunk c of the walk: its first token and length
+    auto chunk = [&](int c, int &t, int &L) {
+        t = seg.t0 + (rev ? nc - 1 - c : c) * LC;
+        L = min(LC, seg.t1 - t);
+    };
+    constexpr int PER = STATES ? 2 : 3;  // tiles a chunk: (q,) k, v
+    auto slot_of = [&](int c, int which) { return (PER * c + which) % RING; };
+    auto phase_of = [&](int c, int which) { return (uint32_t)(((PER * c + which) / RING) & 1); };
+    constexpr int KI = STATES ? 0 : 1, VI = KI + 1;
+    // The state pass' hand-offs run up to two chunks ahead of one another, so each parity of chunks has its own barriers.
+    auto bar_of = [&](uint32_t bar, int c) { return sb + bar + (STATES && (c & 1) ? 8u : 0u); };
+    auto par_of = [&](int c) { return (uint32_t)((STATES ? c >> 1 : c) & 1); };
+    const int ksteps = (kd + 15) / 16, kblk = kd > 64 ? 2 : 1, vblk = vd > 64 ? 2 : 1;
+    const int NV = (vd + 15) / 16 * 16;
+
+    if (warp == 16) {
+        // ------------------------------------------------------------ tile loads
+        const int hq = j / w.q_div, hk = j / w.k_div, hv = j / w.v_div;
+        int issued = 0;
+        bool ok = true;
+        for (int c = 0; c < nc && ok; ++c) {
+            int t, L;
+            chunk(c, t, L);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int x = PER * c + i, sl = x % RING;
+                if (x >= RING) ok = ok && wwait(sb + B_EMPTY + 8 * sl, ((x / RING) - 1) & 1, flag, a.err);
+                if (!ok) break;
+                if (lane == 0) {
+                    const uint32_t dst = sb + sl * TILE, bar = sb + B_FULL + 8 * sl;
+                    const CUtensorMap *m = i == VI ? &w.tv : i == KI ? &w.tk : &w.tq;
+                    const int h = i == VI ? hv : i == KI ? hk : hq, nb = i == VI ? vblk : kblk;
+                    tma::expect_tx(bar, nb * BLK);
+                    for (int b = 0; b < nb; ++b) tma::load3d(dst + b * BLK, m, 64 * b, h, t, bar);
+                }
+                ++issued;
+                __syncwarp();
+            }
+        }
+        if (!ok) {  // after an error: let the loads in flight land (bounded)
+            for (int x = max(0, issued - RING); x < issued; ++x)
+                umma::mbar_spin(sb + B_FULL + 8 * (x % RING), (x / RING) & 1, 4000000L);
+        }
+    } else if (warp == 17) {
+        // ------------------------------------------------------------ MMAs
+        constexpr bool bf = IsBf16<T>::value;
+        const uint32_t i_qk = umma::idesc(128, 128, bf, false, false), i_qs = umma::idesc(128, NV, bf, false, true),
+                       i_ds = umma::idesc(128, NV, bf, true, true);
+        bool ok = true;
+        for (int c = 0; c < nc; ++c) {
+            int t, L;
+            chunk(c, t, L);
+            const int ts = (L + 15) / 16;
+            const uint32_t kt = sb + slot_of(c, KI) * TILE, vt = sb + slot_of(c, VI) * TILE;
+            const bool upd = want_end || c + 1 < nc, use_s = c > 0 || has_start;
+            if (!STATES) {
+                const uint32_t qt = sb + slot_of(c, 0) * TILE;
+                ok = ok && wwait(sb + B_FULL + 8 * slot_of(c, 0), phase_of(c, 0), flag, a.err);
+                ok = ok && wwait(sb + B_FULL + 8 * slot_of(c, KI), phase_of(c, KI), flag, a.err);
+                // (P of the chunk before has been read: Q K^T takes its place)
+                if (c > 0) ok = ok && wwait(sb + B_PV, (c - 1) & 1, flag, a.err);
+                if (!ok) break;
+                umma::fence_after();
+                if (lane == 0) {
+                    for (int ks = 0; ks < ksteps; ++ks) {
+                        const uint32_t o = (uint32_t)(ks >> 2) * BLK + (uint32_t)(ks & 3) * 32u;
+                        umma::mma(tmem + T_QK, umma::desc(qt + o, 16, 1024), umma::desc(kt + o, 16, 1024), i_qk, ks > 0);
+                    }
+                    umma::commit(sb + B_QK);
+                }
+                __syncwarp();
+                // the state's copy is there, and the accumulators of the chunk before have been read
+                ok = ok && wwait(sb + B_S, c & 1, flag, a.err);
+                if (!ok) break;
+                umma::fence_after();
+                if (lane == 0) {
+                    if (use_s) {
+                        for (int ks = 0; ks < ksteps; ++ks) {
+                            const uint32_t o = (uint32_t)(ks >> 2) * BLK + (uint32_t)(ks & 3) * 32u;
+                            umma::mma(tmem + T_QS, umma::desc(qt + o, 16, 1024),
+                                      umma::desc(sb + S_ST + (uint32_t)ks * 2048u, BLK, 1024), i_qs, ks > 0);
+                        }
+                    }
+                    umma::commit(sb + B_EMPTY + 8 * slot_of(c, 0));
+                }
+                __syncwarp();
+                ok = ok && wwait(sb + B_P, c & 1, flag, a.err);
+                ok = ok && wwait(sb + B_FULL + 8 * slot_of(c, VI), phase_of(c, VI), flag, a.err);
+                if (!ok) break;
+                umma::fence_after();
+                if (lane == 0) {
+                    for (int ks = 0; ks < ts; ++ks)
+                        mma_ts(tmem + T_PV, tmem + (ks < 4 ? T_P0 + 8 * ks : T_P1 + 8 * (ks - 4)),
+                               umma::desc(vt + (uint32_t)ks * 2048u, BLK, 1024), i_qs, ks > 0);
+                    umma::commit(sb + B_PV);
+                }
+                __syncwarp();
+            } else {
+                ok = ok && wwait(sb + B_FULL + 8 * slot_of(c, VI), phase_of(c, VI), flag, a.err);
+            }
+            if (upd) {
+                ok = ok && wwait(bar_of(B_K, c), par_of(c), flag, a.err);
+                // (state pass: the accumulator of two chunks before has been read)
+                if (STATES && c >= 2) ok = ok && wwait(bar_of(B_S, c), par_of(c - 2), flag, a.err);
+                if (!ok) break;
+                umma::fence_after();
+                if (lane == 0) {
+                    const uint32_t lo = sb + (STATES && (c & 1) ? S_ST : S_LO), d = tmem + T_DS - (STATES && (c & 1) ? 128 : 0);
+                    for (int half = 0; half < 2; ++half)
+                        for (int ks = 0; ks < ts; ++ks)
+                            umma::mma(d, umma::desc((half ? lo : kt) + (uint32_t)ks * 2048u, BLK, 1024),
+                                      umma::desc(vt + (uint32_t)ks * 2048u, BLK, 1024), i_ds, half || ks > 0);
+                    umma::commit(bar_of(B_DS, c));
+                }
+                __syncwarp();
+            }
+            if (!ok) break;
+            if (lane == 0) {
+                umma::commit(sb + B_EMPTY + 8 * slot_of(c, KI));
+                umma::commit(sb + B_EMPTY + 8 * slot_of(c, VI));
+            }
+            __syncwarp();
+        }
+        // every MMA, and every arrival that waits for one, has happened before shared memory goes away
+        if (lane == 0) {
+            umma::commit(sb + B_DONE);
+            umma::mbar_spin(sb + B_DONE, 0, 4000000L);
+        }
+        __syncwarp();
+    } else if (warp >= 8) {
+        // ------------------------------------------------------------ P, and the decayed keys
+        const int grp = (warp - 8) >> 2, q4 = warp & 3, r = q4 * 32 + lane;
+        const uint32_t quad = (uint32_t)(q4 * 32) << 16;
+        const float s_kv = w.s_kv;
+        bool ok = true;
+        for (int c = 0; c < nc; ++c) {
+            int t, L;
+            chunk(c, t, L);
+            const uint32_t kt = sb + slot_of(c, KI) * TILE, vt = sb + slot_of(c, VI) * TILE;
+            const bool upd = want_end || c + 1 < nc;
+            if (!STATES) {
+                ok = wwait(sb + B_QK, c & 1, flag, a.err);
+                if (!ok) break;
+                umma::fence_after();
+#pragma unroll
+                for (int hb = 0; hb < 2; ++hb) {
+                    const int sblk = grp * 2 + hb;  // columns s = 32 sblk ..
+                    const uint32_t col = T_QK + 32 * sblk, dst = tmem + quad + (grp ? T_P1 : T_P0) + 16 * hb;
+                    uint32_t o[16];
+                    const int dist = rev ? sblk - q4 : q4 - sblk;  // blocks of 32 between the keys and the row
+                    if (dist < 0) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = 0;
+                    } else {
+                        uint32_t x[32];
+                        tld32(tmem + quad + col, x);
+                        twait32(x);
+                        // lambda^|r-s|: on the diagonal one exponential each; beyond it a row's factor (distance to the
+                        // block's near edge) times a column's (from there), both at most 1
+                        const float rowf = s_kv * ex2((float)(32 * dist + (rev ? -lane : lane - 31)) * lg);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float f[2], v[2] = {__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])};
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int cc = 2 * i + e, d = rev ? cc - lane : lane - cc;
+                                bool in = true;
+                                if (dist == 0) {
+                                    in = d >= 0;
+                                    f[e] = s_kv * ex2((float)d * lg);
+                                } else {
+                                    f[e] = rowf * ex2((float)(rev ? cc : 31 - cc) * lg);
+                                }
+                                if (rev) in = in && 32 * sblk + cc < L;
+                                v[e] = in ? v[e] * f[e] : 0.f;
+                            }
+                            o[i] = Elt<T>::pack(v[0], v[1]);
+                        }
+                    }
+                    tst16(dst, o);
+                }
+                tst_wait();
+                umma::fence_before();
+            }
+            if (L < LC || STATES || upd) {
+                ok = wwait(sb + B_FULL + 8 * slot_of(c, VI), phase_of(c, VI), flag, a.err);
+                ok = ok && wwait(sb + B_FULL + 8 * slot_of(c, KI), phase_of(c, KI), flag, a.err);
+                if (!ok) break;
+            }
+            if (L < LC) {
+                // the rows behind a short chunk are another sequence's: what they hold must not meet even a zero
+                if (r >= L && r < (L + 15) / 16 * 16 && grp < vblk)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) umma::st_shared_v4(vt + grp * BLK + r * 128 + i * 16, 0, 0, 0, 0);
+                umma::fence_async_smem();
+            }
+            if (!STATES) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sb + B_P);
+            }
+            if (upd) {
+                // (the remainders' place: read by the update of one chunk before, or two)
+                if (STATES && c >= 2) {
+                    ok = wwait(bar_of(B_DS, c), par_of(c - 2), flag, a.err);
+                    if (!ok) break;
+                }
+                const uint32_t lo = sb + (STATES && (c & 1) ? S_ST : S_LO);
+                const float f = s_kv * ex2((float)(rev ? r + 1 : L - 1 - r) * lg);
+                const bool in = r < L;
+                if (grp < kblk) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t off = grp * BLK + r * 128 + i * 16;
+                        const uint4 u = umma::ld_shared_v4(kt + off);
+                        const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+                        uint32_t h[4], l[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const f2 v = mul2(widen2<T>(x[e]), both(f));
+                            h[e] = narrow2<T>(v);
+                            l[e] = narrow2<T>(fma2(widen2<T>(h[e]), both(-1.f), v));
+                            if (!in) h[e] = l[e] = 0;
+                        }
+                        umma::st_shared_v4(kt + off, h[0], h[1], h[2], h[3]);
+                        umma::st_shared_v4(lo + off, l[0], l[1], l[2], l[3]);
+                    }
+                }
+                umma::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_of(B_K, c));
+            }
+        }
+    } else {
+        // ------------------------------------------------------------ the state and the output rows
+        const int cg = warp >> 2, q4 = warp & 3, row = q4 * 32 + lane;
+        const uint32_t quad = (uint32_t)(q4 * 32) << 16;
+        const bool live = row < kd;
+        f2 st[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) st[i] = 0ull;
+        if (!STATES) {
+            if (w.start) {
+                const float *s0 = w.start + ((long long)seg.n * a.H + j) * kd * vd + (long long)row * w.rs;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int col = cg * 64 + 2 * i;
+                    if (live && col < vd) st[i] = pack2(s0[(long long)col * w.cs], s0[(long long)(col + 1) * w.cs]);
+                }
+            }
+            if (!at_start) {
+                // the windows before this segment, in the walk's order
+                const Cuts wc(a, a.win_len);
+                int pos = rev ? seg.seq1 : seg.seq0;
+                const int stop = rev ? seg.t1 : seg.t0;
+                while (pos != stop) {
+                    int from, to;
+                    if (rev) {
+                        to = pos;
+                        from = max(wc.last(seg, pos - 1), seg.seq0);
+                        pos = from;
+                    } else {
+                        from = pos;
+                        to = wc.next(seg, pos);
+                        pos = to;
+                    }
+                    const float *e = w.ext + (wc.place(seg, from) * a.H + j) * kStateFloats + (long long)row * w.ers;
+                    const f2 d = both(ex2((float)(to - from) * lg));
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int col = cg * 64 + 2 * i;
+                        if (live && col < vd) st[i] = fma2(d, st[i], pack2(e[(long long)col * w.ecs], e[(long long)(col + 1) * w.ecs]));
+                    }
+                }
+            }
+        }
+        auto put_state = [&]() {
+            if (cg * 64 < NV) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    umma::st_shared_v4(sb + S_ST + cg * BLK + row * 128 + (((uint32_t)i ^ (row & 7)) << 4), narrow2<T>(st[4 * i]),
+                                       narrow2<T>(st[4 * i + 1]), narrow2<T>(st[4 * i + 2]), narrow2<T>(st[4 * i + 3]));
+            }
+            umma::fence_async_smem();
+        };
+        if (!STATES) {
+            put_state();
+            umma::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sb + B_S);
+        }
+        bool ok = true;
+        for (int c = 0; c < nc; ++c) {
+            int t, L;
+            chunk(c, t, L);
+            const bool upd = want_end || c + 1 < nc, use_s = c > 0 || has_start;
+            if (!STATES) {
+                ok = wwait(sb + B_PV, c & 1, flag, a.err);
+                if (!ok) break;
+                umma::fence_after();
+                const float rf = use_s ? w.s_out * ex2((float)(rev ? L - 1 - row : row + 1) * lg) : 0.f;
+                const long long at = (((long long)t + row) * a.H + j) * vd;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int col = cg * 64 + i * 16;
+                    if (col >= vd) break;
+                    uint32_t x[16], y[16];
+                    tld16(tmem + quad + T_PV + col, x);
+                    if (use_s) tld16(tmem + quad + T_QS + col, y);
+                    twait16(x);
+                    if (use_s) twait16(y);
+                    f2 v[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        v[e] = mul2(f2_of(x[2 * e], x[2 * e + 1]), both(w.s_out));
+                        if (use_s) v[e] = fma2(f2_of(y[2 * e], y[2 * e + 1]), both(rf), v[e]);
+                    }
+                    if (row < L) {
+                        if (w.out_f32) {
+                            float *o = static_cast<float *>(w.out) + at + col;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (col + 4 * e < vd) *reinterpret_cast<ulonglong2 *>(o + 4 * e) = make_ulonglong2(v[2 * e], v[2 * e + 1]);
+                        } else {
+                            T *o = static_cast<T *>(w.out) + at + col;
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (col + 8 * e < vd)
+                                    *reinterpret_cast<uint4 *>(o + 8 * e) = make_uint4(narrow2<T>(v[4 * e]), narrow2<T>(v[4 * e + 1]),
+                                                                                      narrow2<T>(v[4 * e + 2]), narrow2<T>(v[4 * e + 3]));
+                        }
+                    }
+                }
+                umma::fence_before();
+            }
+            if (upd) {
+                ok = wwait(bar_of(B_DS, c), par_of(c), flag, a.err);
+                if (!ok) break;
+                umma::fence_after();
+                const uint32_t d = tmem + quad + T_DS - (STATES && (c & 1) ? 128 : 0);
+                const f2 l1 = L == LC ? both(lam[0]) : both(ex2((float)L * lg)), l2 = L == LC ? both(lam[1]) : 0ull;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int col = cg * 64 + i * 16;
+                    if (col >= NV) break;
+                    uint32_t x[16];
+                    tld16(d + col, x);
+                    twait16(x);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        f2 &s = st[8 * i + e];
+                        s = fma2(l1, s, fma2(l2, s, f2_of(x[2 * e], x[2 * e + 1])));
+                    }
+                }
+                if (!STATES && c + 1 < nc) put_state();
+                umma::fence_before();
+            }
+            if (STATES || c + 1 < nc) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_of(B_S, c));
+            }
+        }
+        if (ok && want_end && live) {
+            if (STATES) {
+                float *e = w.states + ((long long)slot * a.H + j) * kStateFloats + row;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int col = cg * 64 + 2 * i;
+                    if (col < vd) unpack2(st[i], e[col * LD], e[(col + 1) * LD]);
+                }
+            } else {
+                float *e = w.end + ((long long)seg.n * a.H + j) * kd * vd + (long long)row * w.rs;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int col = cg * 64 + 2 * i;
+                    if (col < vd) unpack2(st[i], e[(long long)col * w.cs], e[(long long)(col + 1) * w.cs]);
+                }
+            }
+        }
+    }
+    umma::fence_before();
+    __syncthreads();
+    if (warp == 17) umma::dealloc(tmem, 512);
+}
+
+template <typename T, bool STATES>
+cudaError_t launch_t(const LinParams &p, cudaStream_t s) {
+    const long long n = lin_slots(p.a, STATES ? p.a.win_len : p.a.main_len) * p.a.H * p.a.nwalk;
+    if (n == 0) return cudaSuccess;
+    auto k = lin_walk_kernel<T, STATES>;
+    const cudaError_t e = allow_smem(k, S_BYTES);
+    if (e != cudaSuccess) return e;
+    return launch_plain(k, dim3((unsigned)n), dim3(NT), S_BYTES, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_lin_walks(const LinParams &p, bool bf16, cudaStream_t s) {
+    return bf16 ? launch_t<__nv_bfloat16, false>(p, s) : launch_t<__half, false>(p, s);
+}
+cudaError_t launch_lin_states(const LinParams &p, bool bf16, cudaStream_t s) {
+    return bf16 ? launch_t<__nv_bfloat16, true>(p, s) : launch_t<__half, true>(p, s);
+}
+
+}  // namespace lin
+}  // namespace gdr

@@ -411,6 +411,44 @@ gdr_status gdr_scan_bwd(const gdr_scan_problem *p, const void *x, const void *dt
                         float *dA, void *dB, void *dC, float *dD, void *dz, float *ddt_bias, float *dstate_in,
                         void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * Linear attention with one decay a head, lambda = exp(decay) (decay <= 0 a log factor a token,
+ * a constant of the head: no gradient), the delta rule's sibling without its correction:
+ *   S_t = lambda S_{t-1} + k_t v_t^T   (fp32),   o_t = scale S_t^T q_t
+ *   in : q, k [B,T,Hk,K], v [B,T,H,V] (dtype, row strides q_ld, k_ld, v_ld; head j reads
+ *        q/k head j / (H/Hk)); decay [H] fp32 (below -120: taken as -120, which is lambda = 0);
+ *        state_in [num_seqs or B,H,K,V] fp32 or NULL (zeros)
+ *   out: o [B,T,H,V] (dtype); state_out, as state_in, or NULL
+ * K and V from 8 to 128 in steps of 8.  Token tensors and states are 16-byte aligned, their
+ * row strides multiples of 8 (GDR_ERR_ALIGN).  state_out overlaps no state_in and o none of
+ * q, k, v (GDR_ERR_UNSUPPORTED).  Packed batches and malformed cu_seqlens as in gdr_conv_fwd.
+ * T = 0 passes the states through.  A value that is not finite reaches the outputs of its own
+ * sequence and head only, from its chunk of 128 tokens on.  Where sequences and heads do not
+ * fill the chip the token axis is cut (workspace: gdr_lin_workspace_size, 256-byte aligned).
+ * gdr_lin_step: dense rows, the states updated in place; meant for T = 1 or a few tokens; its
+ * token tensors are aligned to their elements only.
+ * Backward: dout [B,T,H,V] (contiguous), dstate_out or NULL (zeros) -> dq, dk [B,T,Hk,K],
+ * dv [B,T,H,V] (dtype), dstate_in (fp32, nullable).  The outputs overlap no input
+ * (GDR_ERR_UNSUPPORTED).  Fixed summation order.
+ */
+typedef struct gdr_lin_problem {
+    int B, T, Hk, H, K, V;
+    int64_t q_ld, k_ld, v_ld;
+    gdr_dtype dtype;
+    float scale;
+    const int32_t *cu_seqlens; /* DEVICE int32 [num_seqs+1] or NULL for dense */
+    int num_seqs;
+} gdr_lin_problem;
+gdr_status gdr_lin_workspace_size(const gdr_lin_problem *p, int backward, size_t *bytes);
+gdr_status gdr_lin_fwd(const gdr_lin_problem *p, const void *q, const void *k, const void *v, const float *decay,
+                       const float *state_in, void *o, float *state_out, void *workspace, size_t workspace_bytes,
+                       void *stream);
+gdr_status gdr_lin_step(const gdr_lin_problem *p, const void *q, const void *k, const void *v, const float *decay,
+                        float *state, void *o, void *stream);
+gdr_status gdr_lin_bwd(const gdr_lin_problem *p, const void *q, const void *k, const void *v, const float *decay,
+                       const void *dout, const float *state_in, const float *dstate_out, void *dq, void *dk, void *dv,
+                       float *dstate_in, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Synchronises `stream`, then returns and clears the device error word of the
  * current device (GDR_OK when no kernel latched an error), or GDR_ERR_CUDA when
  * the stream reports a CUDA error. */
