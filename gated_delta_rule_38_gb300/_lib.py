@@ -19,6 +19,7 @@ GDR_INTER_CARD_CP = 1 << 11
 GDR_CHUNK = 64
 GDR_CONV_SILU = 1 << 0
 GDR_SCAN_DT_SOFTPLUS = 1 << 0
+GDR_GATE_RAW, GDR_GATE_SIGMOID, GDR_GATE_SILU = 0, 1, 2
 
 STATUS_NAMES = {
     0: "GDR_OK", 1: "GDR_ERR_NULL", 2: "GDR_ERR_SHAPE", 3: "GDR_ERR_DTYPE", 4: "GDR_ERR_UNSUPPORTED",
@@ -34,7 +35,9 @@ EXPORTS = ["gdr_max_chunks", "gdr_prepare_chunks", "gdr_fwd_workspace_size", "gd
            "gdr_norm_fwd", "gdr_norm_bwd_workspace_size", "gdr_norm_bwd",
            "gdr_conv_fwd", "gdr_conv_step", "gdr_conv_bwd_workspace_size", "gdr_conv_bwd",
            "gdr_scan_saved_bytes", "gdr_scan_workspace_size", "gdr_scan_fwd", "gdr_scan_step", "gdr_scan_bwd",
-           "gdr_lin_workspace_size", "gdr_lin_fwd", "gdr_lin_step", "gdr_lin_bwd"]
+           "gdr_lin_workspace_size", "gdr_lin_fwd", "gdr_lin_step", "gdr_lin_bwd",
+           "gdr_gated_norm_fwd", "gdr_gated_norm_bwd_workspace_size", "gdr_gated_norm_bwd",
+           "gdr_block_norm_fwd", "gdr_block_norm_bwd_workspace_size", "gdr_block_norm_bwd"]
 
 
 class Problem(ctypes.Structure):
@@ -76,6 +79,22 @@ class LinProblem(ctypes.Structure):
         ("B", ctypes.c_int), ("T", ctypes.c_int), ("Hk", ctypes.c_int), ("H", ctypes.c_int), ("K", ctypes.c_int),
         ("V", ctypes.c_int), ("q_ld", ctypes.c_int64), ("k_ld", ctypes.c_int64), ("v_ld", ctypes.c_int64),
         ("dtype", ctypes.c_int), ("scale", ctypes.c_float), ("cu_seqlens", ctypes.c_void_p), ("num_seqs", ctypes.c_int),
+    ]
+
+
+class GatedNormProblem(ctypes.Structure):
+    _fields_ = [
+        ("tokens", ctypes.c_int64), ("x_ld", ctypes.c_int64), ("gate_ld", ctypes.c_int64), ("heads", ctypes.c_int),
+        ("D", ctypes.c_int), ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int), ("gate_act", ctypes.c_uint),
+        ("eps", ctypes.c_float),
+    ]
+
+
+class BlockNormProblem(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("x_ld", ctypes.c_int64), ("gate_ld", ctypes.c_int64), ("D", ctypes.c_int),
+        ("dtype", ctypes.c_int), ("weight_dtype", ctypes.c_int), ("residual_dtype", ctypes.c_int),
+        ("gate_act", ctypes.c_uint), ("residual_scale", ctypes.c_float), ("eps", ctypes.c_float),
     ]
 
 
@@ -145,7 +164,8 @@ def load() -> ctypes.CDLL:
         lib.gdr_debug_set_wait_polls.argtypes = [ctypes.c_longlong]
         lib.gdr_debug_set_wait_polls.restype = i32
         size_p = ctypes.POINTER(ctypes.c_size_t)
-        norm, conv, scan, lin = (ctypes.POINTER(s) for s in (NormProblem, ConvProblem, ScanProblem, LinProblem))
+        norm, conv, scan, lin, gated, block = (ctypes.POINTER(s) for s in (
+            NormProblem, ConvProblem, ScanProblem, LinProblem, GatedNormProblem, BlockNormProblem))
         for name, args in (
                 ("gdr_norm_fwd", [norm] + [P] * 7), ("gdr_norm_bwd_workspace_size", [norm, size_p]),
                 ("gdr_norm_bwd", [norm] + [P] * 8 + [ctypes.c_size_t, P]),
@@ -157,7 +177,11 @@ def load() -> ctypes.CDLL:
                 ("gdr_scan_bwd", [scan] + [P] * 22 + [ctypes.c_size_t, P]),
                 ("gdr_lin_workspace_size", [lin, i32, size_p]),
                 ("gdr_lin_fwd", [lin] + [P] * 8 + [ctypes.c_size_t, P]), ("gdr_lin_step", [lin] + [P] * 7),
-                ("gdr_lin_bwd", [lin] + [P] * 12 + [ctypes.c_size_t, P])):
+                ("gdr_lin_bwd", [lin] + [P] * 12 + [ctypes.c_size_t, P]),
+                ("gdr_gated_norm_fwd", [gated] + [P] * 5), ("gdr_gated_norm_bwd_workspace_size", [gated, size_p]),
+                ("gdr_gated_norm_bwd", [gated] + [P] * 8 + [ctypes.c_size_t, P]),
+                ("gdr_block_norm_fwd", [block] + [P] * 8), ("gdr_block_norm_bwd_workspace_size", [block, size_p]),
+                ("gdr_block_norm_bwd", [block] + [P] * 13 + [ctypes.c_size_t, P])):
             fn = getattr(lib, name)
             fn.argtypes, fn.restype = args, i32
         lib.gdr_version.argtypes = []

@@ -466,7 +466,8 @@ const char *const kKernelNames[K_COUNT] = {"prep_chunks", "wy_fwd",     "chain_f
                                            "norm_fwd",    "norm_bwd",   "conv_fwd",  "conv_bwd",
                                            "scan_local",  "scan_join",  "scan_fwd",  "scan_step",
                                            "scan_bwd",    "reduce",     "lin_states", "lin_fwd",
-                                           "lin_step",    "lin_bwd"};
+                                           "lin_step",    "lin_bwd",    "gated_norm_fwd", "gated_norm_bwd",
+                                           "block_norm_fwd", "block_norm_bwd"};
 struct Pending {
     int id;
     cudaEvent_t a, b;

@@ -21,7 +21,8 @@ gdr_status cuda_status(cudaError_t e);
 enum KernelId {
     K_PREP = 0, K_WY_FWD, K_CHAIN_FWD, K_CHAIN_FWD_RECOMPUTE, K_CHAIN_BWD, K_CHAIN_PAIR, K_BWD_CHUNK, K_CHUNK_P,
     K_CHAIN_REV, K_GATE_ACT, K_PAD, K_ONECHUNK, K_NORM_FWD, K_NORM_BWD, K_CONV_FWD, K_CONV_BWD, K_SCAN_LOCAL,
-    K_SCAN_JOIN, K_SCAN_FWD, K_SCAN_STEP, K_SCAN_BWD, K_REDUCE, K_LIN_STATES, K_LIN_FWD, K_LIN_STEP, K_LIN_BWD, K_COUNT
+    K_SCAN_JOIN, K_SCAN_FWD, K_SCAN_STEP, K_SCAN_BWD, K_REDUCE, K_LIN_STATES, K_LIN_FWD, K_LIN_STEP, K_LIN_BWD,
+    K_GATED_FWD, K_GATED_BWD, K_BLOCK_FWD, K_BLOCK_BWD, K_COUNT
 };
 
 // Around one launch: an event pair while the profiler is on, and the launch's status.

@@ -1,0 +1,569 @@
+// The norm of a mixer's output with its gate, and the norms behind and before a block fused with its gate and residual
+// scale:
+//
+//   gated:  y = x r w act(g),  r = 1 / sqrt(mean x^2 + eps)
+//     dn = dy w act(g);  dx = r dn - x r^3 mean(dn x);  dg = dy x r w act'(g);  dw = sum over rows of dy x r act(g)
+//   block:  n = x r1 (or x);  b = n pw;  h = res + s b act(g);  y = h r2 w
+//     dh = r2 w dy - h r2^3 mean(w dy h) + dres;  db = s dh act(g);  dg = s dh b act'(g);  dn = db pw
+//     dx = r1 dn - x r1^3 mean(dn x);  dpw = sum of db n;  dw = sum of dy h r2
+//   at the stored h; act is the number itself, its sigmoid or g sigmoid(g), or 1 without a gate.
+//
+// Every element is read and written once, so all four are bound by HBM.  A block walks rows; a row is spread over TPR
+// threads of 8 NG elements each, and the next row's elements come into shared memory by asynchronous copies while this
+// one is worked on (all passes over a row read it there).  All sums are fp32; sums over rows leave one partial row a
+// block, which a second kernel adds in a fixed order.
+//
+// Two forms, told apart by RAG: where every row of every tensor starts on a 16-byte boundary, a thread owns vectors of 8
+// columns and copies what it reads itself; otherwise a row's threads bring the aligned 16-byte pieces that hold it and a
+// thread owns every TPR-th column.
+#pragma once
+
+#include "norm.cuh"
+#include "rownorm.h"
+
+namespace gdr {
+namespace rownorm {
+namespace {
+
+using namespace norm;
+
+// Access to the rows of up to five tensors.  Elements come in groups of 8: group k of thread t holds columns 8 (k TPR + t)
+// and on, or, ragged, t + (8 k + e) TPR.
+template <typename T, int NG, int BT, bool RAG>
+struct Rows {
+    const RowArgs &a;
+    char *smem;
+    int t, slot, per;  // thread of the row, row slot of the block; bytes a stage (vec) or a slot's row (ragged)
+    __device__ __forceinline__ Rows(const RowArgs &a_, void *s) : a(a_), smem(static_cast<char *>(s)) {
+        slot = threadIdx.x / a.tpr;
+        t = threadIdx.x - slot * a.tpr;
+        per = 0;
+#pragma unroll
+        for (int i = 0; i < kMaxIn; ++i) per += size(i);
+    }
+    // an input's bytes in a stage, and where it begins
+    __device__ __forceinline__ int size(int i) const {
+        if (!a.in[i].elem) return 0;
+        return RAG ? rag_place(a.D, a.in[i].elem) : NG * BT * 8 * a.in[i].elem;
+    }
+    __device__ __forceinline__ int off(int i) const {
+        int o = 0;
+#pragma unroll
+        for (int k = 0; k < kMaxIn; ++k)
+            if (k < i) o += size(k);
+        return o;
+    }
+    __device__ __forceinline__ const char *at(int i, long long row) const {
+        const RowIn &in = a.in[i];
+        long long e = row * in.ld;
+        if (in.heads > 1) {
+            const long long token = a.rows <= 0x7fffffff ? (long long)((unsigned)row / (unsigned)in.heads) : row / in.heads;
+            e = token * in.ld + (row - token * in.heads) * a.D;
+        }
+        return static_cast<const char *>(in.p) + e * in.elem;
+    }
+    __device__ __forceinline__ char *place(int stage, int i) const {
+        return smem + (RAG ? (size_t)(stage * a.rpb + slot) * per : (size_t)stage * per) + off(i);
+    }
+    __device__ __forceinline__ void fetch(long long row, int stage) const {
+        const bool in = row < a.rows;
+#pragma unroll
+        for (int i = 0; i < kMaxIn; ++i) {
+            const int elem = a.in[i].elem;
+            if (!elem) continue;
+            char *to = place(stage, i);
+            if constexpr (RAG) {
+                if (!in) continue;
+                const char *base = static_cast<const char *>(a.in[i].p), *src0 = at(i, row), *hi = at(i, a.rows - 1) + a.D * elem;
+                const int sk = (int)(reinterpret_cast<uintptr_t>(src0) & 15), bytes = a.D * elem, pieces = (sk + bytes + 15) / 16;
+                for (int k = t; k < pieces; k += a.tpr) {
+                    const char *src = src0 - sk + k * 16;
+                    if (src >= base) {
+                        const long long left = hi - src;
+                        const int n = left < 16 ? (int)left : 16;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(to + k * 16)), "l"(src), "r"(n) : "memory");
+                    } else {  // the piece begins before the tensor
+                        for (int b = sk; b < 16 && b - sk < bytes; b += 2)
+                            *reinterpret_cast<uint16_t *>(to + b) = *reinterpret_cast<const uint16_t *>(src + b);
+                    }
+                }
+            } else {
+                const char *src = at(i, in ? row : 0);
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const int c = (g * a.tpr + t) * 8;
+                    for (int h = 0; h < elem / 2; ++h) {  // halves of an fp32 group lie BT places apart
+                        char *d = to + ((g * (elem / 2) + h) * BT + threadIdx.x) * 16;
+                        if (in && c < a.D)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(d)), "l"(src + c * elem + h * 16) : "memory");
+                        else
+                            *reinterpret_cast<uint4 *>(d) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;\n" ::: "memory");
+    }
+    template <bool F32>
+    __device__ __forceinline__ void get(int stage, int i, long long row, int g, f2 *o) const {
+        const char *s = place(stage, i);
+        if constexpr (RAG) {
+            s += reinterpret_cast<uintptr_t>(at(i, row)) & 15;
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int c = t + (8 * g + e) * a.tpr;
+                v[e] = row < a.rows && c < a.D ? rag_get<T, F32>(s, c) : 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = pack2(v[2 * e], v[2 * e + 1]);
+        } else {
+            const uint4 *q = reinterpret_cast<const uint4 *>(s) + (g * (F32 ? 2 : 1)) * BT + threadIdx.x;
+            const uint4 u = q[0];
+            if constexpr (F32) {
+                const uint4 x = q[BT];
+                o[0] = pack2(__uint_as_float(u.x), __uint_as_float(u.y)), o[1] = pack2(__uint_as_float(u.z), __uint_as_float(u.w));
+                o[2] = pack2(__uint_as_float(x.x), __uint_as_float(x.y)), o[3] = pack2(__uint_as_float(x.z), __uint_as_float(x.w));
+            } else {
+                o[0] = widen2<T>(u.x), o[1] = widen2<T>(u.y), o[2] = widen2<T>(u.z), o[3] = widen2<T>(u.w);
+            }
+        }
+    }
+    // a group of an output [rows, D]
+    template <bool F32>
+    __device__ __forceinline__ void put(void *to, long long row, int g, const f2 *v) const {
+        if (row >= a.rows) return;
+        if constexpr (RAG) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) unpack2(v[e], x[2 * e], x[2 * e + 1]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int c = t + (8 * g + e) * a.tpr;
+                if (c < a.D) rag_put<T, F32>(to, row * a.D + c, x[e]);
+            }
+        } else {
+            const int c = (g * a.tpr + t) * 8;
+            if (c >= a.D) return;
+            if constexpr (F32) {
+                ulonglong2 *q = reinterpret_cast<ulonglong2 *>(static_cast<float *>(to) + row * a.D + c);
+                q[0] = make_ulonglong2(v[0], v[1]);
+                q[1] = make_ulonglong2(v[2], v[3]);
+            } else {
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(to) + row * a.D + c) =
+                    make_uint4(narrow2<T>(v[0]), narrow2<T>(v[1]), narrow2<T>(v[2]), narrow2<T>(v[3]));
+            }
+        }
+    }
+    // a group of a weight
+    __device__ __forceinline__ void weight(const void *w, int g, f2 *o) const {
+        float x[8];
+        if constexpr (!RAG) {
+            const int c = (g * a.tpr + t) * 8;
+            if (c < a.D && a.w_f32) {
+                const ulonglong2 *q = reinterpret_cast<const ulonglong2 *>(static_cast<const float *>(w) + c);
+                const ulonglong2 u = q[0], v = q[1];
+                o[0] = u.x, o[1] = u.y, o[2] = v.x, o[3] = v.y;
+                return;
+            }
+            if (c < a.D) {
+                const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(w) + c);
+                o[0] = widen2<T>(u.x), o[1] = widen2<T>(u.y), o[2] = widen2<T>(u.z), o[3] = widen2<T>(u.w);
+                return;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = 0ull;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int c = t + (8 * g + e) * a.tpr;
+                x[e] = c < a.D ? load_gate<T>(w, c, a.w_f32) : 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = pack2(x[2 * e], x[2 * e + 1]);
+        }
+    }
+    // this thread's sums over its rows, added up over the block's row slots, as `which` of the block's partial rows
+    __device__ __forceinline__ void put_sums(const f2 *v, int which, int count) const {
+        float *out = a.part + ((long long)blockIdx.x * count + which) * a.D;
+        float *slots = reinterpret_cast<float *>(smem);
+        __syncthreads();  // (the rows, or the sums before these, are read no more)
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) unpack2(v[4 * g + e], x[2 * e], x[2 * e + 1]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int c = RAG ? t + (8 * g + e) * a.tpr : (g * a.tpr + t) * 8 + e;
+                if (c < a.D) {
+                    if (a.rpb == 1) out[c] = x[e];
+                    else slots[slot * a.D + c] = x[e];
+                }
+            }
+        }
+        if (a.rpb == 1) return;
+        __syncthreads();
+        for (int c = threadIdx.x; c < a.D; c += blockDim.x) {
+            float s = 0.f;
+            for (int i = 0; i < a.rpb; ++i) s += slots[i * a.D + c];
+            out[c] = s;
+        }
+    }
+};
+
+// Sums over a row's threads of N numbers each.  `red`: [2][16][N] floats that only this sum uses, by parity of the row.
+template <int N>
+__device__ __forceinline__ void row_sums(float *v, float *red, int parity, int tpr, int slot) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = lanes_sum(v[i], min(tpr, 32));
+    if (tpr <= 32) return;
+    float *r = red + parity * 16 * N;
+    if (lane == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) r[warp * N + i] = v[i];
+    __syncthreads();
+    const int wpr = tpr >> 5;
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = 0.f;
+    for (int k = 0; k < wpr; ++k)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += r[(slot * wpr + k) * N + i];
+}
+
+// The gate's factors of four pairs and, where asked for, their derivatives.
+template <bool GRAD>
+__device__ __forceinline__ void gate_of_pairs(int act, const f2 *g, f2 *f, f2 *df) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (act == ACT_RAW) {
+            f[e] = g[e];
+            if (GRAD) df[e] = both(1.f);
+            continue;
+        }
+        // sigmoid(g) and 1 - sigmoid(g), each without cancellation
+        float x[2], s[2], c[2];
+        unpack2(g[e], x[0], x[1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const float z = ex2(-fabsf(x[k]) * LOG2E), q = rcp(1.f + z), p = z * q;
+            s[k] = x[k] < 0.f ? p : q;
+            c[k] = x[k] < 0.f ? q : p;
+        }
+        const f2 sg = pack2(s[0], s[1]), cg = pack2(c[0], c[1]);
+        if (act == ACT_SIGMOID) {
+            f[e] = sg;
+            if (GRAD) df[e] = mul2(sg, cg);
+        } else {
+            // (far below, where the sigmoid has underflowed, an infinite g times it would be NaN where the limit is 0)
+            f[e] = mul2(pack2(fmaxf(x[0], -1e30f), fmaxf(x[1], -1e30f)), sg);
+            if (GRAD) df[e] = add2(mul2(f[e], cg), sg);
+        }
+    }
+}
+
+// Waits for this row's copies; ragged rows were brought by all threads of the row.
+template <bool RAG>
+__device__ __forceinline__ void arrive(bool ahead) {
+    if (ahead) asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+    if (RAG) __syncthreads();
+}
+
+// Loops over the block's rows: body(row, stage, parity) with the row's elements at hand.
+template <bool RAG, typename R, typename F>
+__device__ __forceinline__ void walk(const R &rows, const RowArgs &a, F &&body) {
+    const long long step = (long long)gridDim.x * a.rpb;
+    long long row = (long long)blockIdx.x * a.rpb + rows.slot;
+    const bool two = a.stages == 2;
+    if (two) rows.fetch(row, 0);
+    int parity = 0;
+    for (long long r0 = (long long)blockIdx.x * a.rpb; r0 < a.rows; r0 += step, row += step, parity ^= 1) {
+        const int stage = two ? parity : 0;
+        if (RAG) __syncthreads();  // (the place that is filled now has been read)
+        rows.fetch(two ? row + step : row, two ? stage ^ 1 : 0);
+        arrive<RAG>(two);
+        body(row, stage, parity);
+    }
+    asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+}
+
+// ---------------------------------------------------------------- gated norm
+
+template <typename T, int NG, int BT, bool RAG>
+__global__ void __launch_bounds__(BT, BT > 288 ? 1 : 3) gated_fwd_kernel(const RowArgs a) {
+    extern __shared__ __align__(16) char s_rows[];
+    __shared__ float red[2 * 16];
+    const Rows<T, NG, BT, RAG> rows(a, s_rows);
+    f2 w[4 * NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) rows.weight(a.w, g, w + 4 * g);
+    const float inv_d = 1.0f / (float)a.D;
+    walk<RAG>(rows, a, [&](long long row, int stage, int parity) {
+        f2 x[4 * NG], ss = 0ull;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            rows.template get<false>(stage, IN_X, row, g, x + 4 * g);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ss = fma2(x[4 * g + e], x[4 * g + e], ss);
+        }
+        float s[1] = {sum2(ss)};
+        row_sums<1>(s, red, parity, a.tpr, rows.slot);
+        const f2 r = both(rsqrtf(fmaf(s[0], inv_d, a.eps)));
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            f2 z[4], f[4];
+            rows.template get<false>(stage, IN_GATE, row, g, z);
+            gate_of_pairs<false>(a.act, z, f, nullptr);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = mul2(mul2(mul2(x[4 * g + e], r), w[4 * g + e]), f[e]);
+            rows.template put<false>(a.y, row, g, f);
+        }
+    });
+}
+
+template <typename T, int NG, int BT, bool RAG>
+__global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) gated_bwd_kernel(const RowArgs a) {
+    extern __shared__ __align__(16) char s_rows[];
+    __shared__ float red[2 * 16 * 2];
+    const Rows<T, NG, BT, RAG> rows(a, s_rows);
+    f2 w[4 * NG], dw[4 * NG];
+#pragma unroll
+    for (int g = 0; g < NG; ++g) rows.weight(a.w, g, w + 4 * g);
+#pragma unroll
+    for (int i = 0; i < 4 * NG; ++i) dw[i] = 0ull;
+    const float inv_d = 1.0f / (float)a.D;
+    walk<RAG>(rows, a, [&](long long row, int stage, int parity) {
+        f2 dn[4 * NG], ss = 0ull, sd = 0ull;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            f2 x[4], z[4], f[4], d[4];
+            rows.template get<false>(stage, IN_X, row, g, x);
+            rows.template get<false>(stage, IN_GATE, row, g, z);
+            rows.template get<false>(stage, IN_DY, row, g, d);
+            gate_of_pairs<false>(a.act, z, f, nullptr);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                dn[4 * g + e] = mul2(mul2(d[e], w[4 * g + e]), f[e]);
+                ss = fma2(x[e], x[e], ss);
+                sd = fma2(dn[4 * g + e], x[e], sd);
+            }
+        }
+        float s[2] = {sum2(ss), sum2(sd)};
+        row_sums<2>(s, red, parity, a.tpr, rows.slot);
+        // (a place past the last row: with eps = 0 its factor would be infinite)
+        const float r = row < a.rows ? rsqrtf(fmaf(s[0], inv_d, a.eps)) : 0.f;
+        const f2 r2 = both(r), k2 = both(-(r * (s[1] * inv_d)) * r * r), one = both(a.D == 1 ? a.eps * r * r * r : r);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            f2 x[4], z[4], f[4], df[4], d[4], dx[4], dg[4];
+            rows.template get<false>(stage, IN_X, row, g, x);
+            rows.template get<false>(stage, IN_GATE, row, g, z);
+            rows.template get<false>(stage, IN_DY, row, g, d);
+            gate_of_pairs<true>(a.act, z, f, df);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const f2 n = mul2(mul2(x[e], r2), d[e]);  // dy x r
+                dw[4 * g + e] = fma2(n, f[e], dw[4 * g + e]);
+                dg[e] = mul2(mul2(n, w[4 * g + e]), df[e]);
+                const f2 own = mul2(dn[4 * g + e], one);
+                dx[e] = a.D == 1 ? own : fma2(x[e], k2, own);
+            }
+            rows.template put<false>(a.dx, row, g, dx);
+            rows.template put<false>(a.dgate, row, g, dg);
+        }
+    });
+    rows.put_sums(dw, 0, 1);
+}
+
+// ---------------------------------------------------------------- block norm
+
+template <typename T, int NG, int BT, bool RAG, bool F32>
+__global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) block_fwd_kernel(const RowArgs a) {
+    constexpr bool HOLD = NG <= 2;  // weights in registers
+    extern __shared__ __align__(16) char s_rows[];
+    __shared__ float red1[2 * 16], red2[2 * 16];
+    const Rows<T, NG, BT, RAG> rows(a, s_rows);
+    f2 w[HOLD ? 4 * NG : 4], pw[HOLD ? 4 * NG : 4];
+    if (HOLD) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            rows.weight(a.w, g, w + 4 * g);
+            if (a.pw) rows.weight(a.pw, g, pw + 4 * g);
+        }
+    }
+    const float inv_d = 1.0f / (float)a.D;
+    walk<RAG>(rows, a, [&](long long row, int stage, int parity) {
+        f2 h[4 * NG];
+        f2 scale = both(a.rscale);
+#pragma unroll
+        for (int g = 0; g < NG; ++g) rows.template get<false>(stage, IN_X, row, g, h + 4 * g);
+        if (a.pw) {
+            f2 ss = 0ull;
+#pragma unroll
+            for (int i = 0; i < 4 * NG; ++i) ss = fma2(h[i], h[i], ss);
+            float s[1] = {sum2(ss)};
+            row_sums<1>(s, red1, parity, a.tpr, rows.slot);
+            const f2 r = both(rsqrtf(fmaf(s[0], inv_d, a.eps)));
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                if (!HOLD) rows.weight(a.pw, g, pw);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) h[4 * g + e] = mul2(mul2(h[4 * g + e], r), pw[HOLD ? 4 * g + e : e]);
+            }
+        }
+        f2 ss = 0ull;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            f2 z[4], f[4], res[4];
+            rows.template get<F32>(stage, IN_RES, row, g, res);
+            if (a.act != ACT_NONE) {
+                rows.template get<false>(stage, IN_GATE, row, g, z);
+                gate_of_pairs<false>(a.act, z, f, nullptr);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) h[4 * g + e] = mul2(h[4 * g + e], f[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                h[4 * g + e] = fma2(h[4 * g + e], scale, res[e]);
+                ss = fma2(h[4 * g + e], h[4 * g + e], ss);
+            }
+            rows.template put<F32>(a.res_out, row, g, h + 4 * g);
+        }
+        float s[1] = {sum2(ss)};
+        row_sums<1>(s, red2, parity, a.tpr, rows.slot);
+        const f2 r = both(rsqrtf(fmaf(s[0], inv_d, a.eps)));
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            if (!HOLD) rows.weight(a.w, g, w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) h[4 * g + e] = mul2(mul2(h[4 * g + e], r), w[HOLD ? 4 * g + e : e]);
+            rows.template put<false>(a.y, row, g, h + 4 * g);
+        }
+    });
+}
+
+template <typename T, int NG, int BT, bool RAG, bool F32>
+__global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) block_bwd_kernel(const RowArgs a) {
+    constexpr bool HOLD = NG <= 2;
+    extern __shared__ __align__(16) char s_rows[];
+    __shared__ float red1[2 * 16 * 3], red2[2 * 16];
+    const Rows<T, NG, BT, RAG> rows(a, s_rows);
+    f2 w[HOLD ? 4 * NG : 4], pw[HOLD ? 4 * NG : 4], dw[4 * NG], dpw[4 * NG];
+    if (HOLD) {
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            rows.weight(a.w, g, w + 4 * g);
+            if (a.pw) rows.weight(a.pw, g, pw + 4 * g);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4 * NG; ++i) dw[i] = dpw[i] = 0ull;
+    const float inv_d = 1.0f / (float)a.D;
+    walk<RAG>(rows, a, [&](long long row, int stage, int parity) {
+        f2 sx = 0ull, sh = 0ull, sd = 0ull;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            f2 x[4], h[4], d[4];
+            rows.template get<false>(stage, IN_X, row, g, x);
+            rows.template get<F32>(stage, IN_H, row, g, h);
+            rows.template get<false>(stage, IN_DY, row, g, d);
+            if (!HOLD) rows.weight(a.w, g, w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                sx = fma2(x[e], x[e], sx);
+                sh = fma2(h[e], h[e], sh);
+                sd = fma2(mul2(d[e], w[HOLD ? 4 * g + e : e]), h[e], sd);
+            }
+        }
+        float s[3] = {sum2(sx), sum2(sh), sum2(sd)};
+        row_sums<3>(s, red1, parity, a.tpr, rows.slot);
+        const bool live = row < a.rows;
+        const float r1 = !a.pw ? 1.f : live ? rsqrtf(fmaf(s[0], inv_d, a.eps)) : 0.f;
+        const float r2 = live ? rsqrtf(fmaf(s[1], inv_d, a.eps)) : 0.f;
+        const f2 k2 = both(-(r2 * (s[2] * inv_d)) * r2 * r2), one = both(a.D == 1 ? a.eps * r2 * r2 * r2 : r2);
+        f2 dn[4 * NG], sn = 0ull;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            f2 x[4], h[4], d[4], dh[4], f[4], df[4];
+            rows.template get<false>(stage, IN_X, row, g, x);
+            rows.template get<F32>(stage, IN_H, row, g, h);
+            rows.template get<false>(stage, IN_DY, row, g, d);
+            if (a.in[IN_DRES].elem) rows.template get<F32>(stage, IN_DRES, row, g, dh);
+            else dh[0] = dh[1] = dh[2] = dh[3] = 0ull;
+            if (!HOLD) {
+                rows.weight(a.w, g, w);
+                if (a.pw) rows.weight(a.pw, g, pw);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const f2 wd = mul2(mul2(d[e], w[HOLD ? 4 * g + e : e]), one);
+                dh[e] = add2(dh[e], a.D == 1 ? wd : fma2(h[e], k2, wd));
+                dw[4 * g + e] = fma2(mul2(h[e], both(r2)), d[e], dw[4 * g + e]);
+            }
+            rows.template put<F32>(a.dres, row, g, dh);
+            if (a.act != ACT_NONE) {
+                f2 z[4];
+                rows.template get<false>(stage, IN_GATE, row, g, z);
+                gate_of_pairs<true>(a.act, z, f, df);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const f2 p = a.pw ? pw[HOLD ? 4 * g + e : e] : both(1.f);
+                const f2 db = mul2(dh[e], both(a.rscale)), n = mul2(x[e], both(r1));
+                if (a.act != ACT_NONE) df[e] = mul2(mul2(db, mul2(n, p)), df[e]);
+                const f2 dg = a.act != ACT_NONE ? mul2(db, f[e]) : db;
+                dpw[4 * g + e] = fma2(dg, n, dpw[4 * g + e]);
+                dn[4 * g + e] = mul2(dg, p);
+                sn = fma2(dn[4 * g + e], x[e], sn);
+            }
+            if (a.act != ACT_NONE) rows.template put<false>(a.dgate, row, g, df);
+        }
+        f2 k1 = 0ull, one1 = both(1.f);
+        if (a.pw) {
+            float q[1] = {sum2(sn)};
+            row_sums<1>(q, red2, parity, a.tpr, rows.slot);
+            k1 = both(-(r1 * (q[0] * inv_d)) * r1 * r1);
+            one1 = both(a.D == 1 ? a.eps * r1 * r1 * r1 : r1);
+        }
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            f2 x[4];
+            rows.template get<false>(stage, IN_X, row, g, x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const f2 own = mul2(dn[4 * g + e], one1);
+                dn[4 * g + e] = !a.pw || a.D == 1 ? own : fma2(x[e], k1, own);
+            }
+            rows.template put<false>(a.dx, row, g, dn + 4 * g);
+        }
+    });
+    rows.put_sums(dw, 0, a.pw ? 2 : 1);
+    if (a.pw) rows.put_sums(dpw, 1, 2);
+}
+
+// ---------------------------------------------------------------- launches
+
+template <typename K>
+cudaError_t launch_rows(K k, const RowArgs &a, const RowForm &f, cudaStream_t st) {
+    const cudaError_t e = allow_smem(k, f.smem);
+    if (e != cudaSuccess) return e;
+    return launch_plain(k, dim3(f.blocks), dim3(f.s.threads), f.smem, st, a);
+}
+// (ragged blocks take any multiple of 32 up to the bound; vec blocks are the bound itself)
+#define GDR_ROW_FORMS(KERNEL, ...)                                                                                      \
+    do {                                                                                                                \
+        if (f.vec) {                                                                                                    \
+            if (f.s.nv == 4) return launch_rows(KERNEL<T, 4, 512, false __VA_ARGS__>, a, f, st);                        \
+            return f.s.threads == 256 ? launch_rows(KERNEL<T, 2, 256, false __VA_ARGS__>, a, f, st)                     \
+                                      : launch_rows(KERNEL<T, 2, 512, false __VA_ARGS__>, a, f, st);                    \
+        }                                                                                                               \
+        if (f.s.nv == 4) return launch_rows(KERNEL<T, 4, 512, true __VA_ARGS__>, a, f, st);                             \
+        return f.s.threads <= 288 ? launch_rows(KERNEL<T, 2, 288, true __VA_ARGS__>, a, f, st)                          \
+                                  : launch_rows(KERNEL<T, 2, 512, true __VA_ARGS__>, a, f, st);                         \
+    } while (0)
+
+}  // namespace
+}  // namespace rownorm
+}  // namespace gdr

@@ -1,0 +1,245 @@
+// Entry points of the gated norm and the block norm: checks, the choice of form and workspaces.
+#include "rownorm.h"
+
+namespace gdr {
+namespace rownorm {
+namespace {
+
+// A pointer that is given is aligned to its elements; `vec` is cleared unless all allow 16-byte accesses.
+bool ptr_ok(const void *p, size_t elem, bool *vec) {
+    if (!p) return true;
+    if (!aligned_to(p, elem)) return false;
+    if (!aligned16(p)) *vec = false;
+    return true;
+}
+
+// How the rows are spread, staged and walked.  A block keeps two rows' places (one on its way while the other is worked
+// on) where that leaves room for another block beside it, or its rows do not fit twice anyway; the grid is what is
+// resident at once.  (8192 x 4096, block norm's backward with an fp32 stream, 57 KB a row.)
+RowForm form_of(const RowArgs &a, long long rows, bool vec, bool bwd) {
+    RowForm f = {};
+    f.vec = vec;
+    f.s = norm::norm_shape(a.D, !vec);
+    size_t place = 0;
+    for (const RowIn &in : a.in)
+        if (in.elem) place += vec ? (size_t)f.s.nv * f.s.threads * 8 * in.elem : (size_t)f.s.rpb * ((a.D * in.elem + 14 + 15) / 16 * 16);
+    const size_t all = 227 * 1024;
+    const int most = f.s.threads > 288 ? 1 : bwd ? 2 : 3;  // (by registers, see the kernels' bounds)
+    auto resident = [&](size_t smem) {
+        const int n = (int)(all / (smem + 2048));
+        return n < most ? n : most;
+    };
+    const int stages = resident(2 * place) >= 1 ? 2 : 1;
+    f.smem = stages * place;
+    const long long need = (rows + f.s.rpb - 1) / f.s.rpb, at_once = (long long)kSMs * resident(f.smem);
+    f.blocks = (int)(need < at_once ? need : at_once);
+    return f;
+}
+void apply(RowArgs *a, const RowForm &f) {
+    a->tpr = f.s.tpr, a->rpb = f.s.rpb;
+    size_t place = 0;
+    for (const RowIn &in : a->in)
+        if (in.elem) place += f.vec ? (size_t)f.s.nv * f.s.threads * 8 * in.elem : (size_t)f.s.rpb * ((a->D * in.elem + 14 + 15) / 16 * 16);
+    a->stages = f.smem >= 2 * place ? 2 : 1;
+}
+
+// Partial rows of the parameters' gradients: whichever form a call takes has at most this many blocks.
+size_t parts_bytes(long long rows, int D, int outs) {
+    size_t most = 0;
+    for (bool rag : {false, true}) {
+        const norm::NormShape s = norm::norm_shape(D, rag);
+        const long long need = (rows + s.rpb - 1) / s.rpb, at_once = (long long)kSMs * (s.threads > 288 ? 1 : 2);
+        const size_t n = (size_t)(need < at_once ? need : at_once);
+        most = n > most ? n : most;
+    }
+    return round_up(most * outs * D * sizeof(float), 256);
+}
+
+gdr_status check_gated(const gdr_gated_norm_problem *p) {
+    if (!p) return GDR_ERR_NULL;
+    if (p->tokens < 0 || p->heads < 1 || p->D < 1 || p->D > GDR_NORM_MAX_D || p->tokens > ((int64_t)1 << 40) / p->heads) return GDR_ERR_SHAPE;
+    const int64_t wide = (int64_t)p->heads * p->D;
+    if (p->x_ld < wide || p->gate_ld < wide) return GDR_ERR_SHAPE;
+    if (!is_half(p->dtype) || (p->weight_dtype != p->dtype && p->weight_dtype != GDR_FP32)) return GDR_ERR_DTYPE;
+    if (p->gate_act != GDR_GATE_SIGMOID && p->gate_act != GDR_GATE_SILU) return GDR_ERR_UNSUPPORTED;
+    return GDR_OK;
+}
+gdr_status check_block(const gdr_block_norm_problem *p) {
+    if (!p) return GDR_ERR_NULL;
+    if (p->rows < 0 || p->rows > ((int64_t)1 << 40) || p->D < 1 || p->D > GDR_NORM_MAX_D || p->x_ld < p->D || p->gate_ld < p->D) return GDR_ERR_SHAPE;
+    if (!is_half(p->dtype) || (p->weight_dtype != p->dtype && p->weight_dtype != GDR_FP32) ||
+        (p->residual_dtype != p->dtype && p->residual_dtype != GDR_FP32))
+        return GDR_ERR_DTYPE;
+    if (p->gate_act != GDR_GATE_RAW && p->gate_act != GDR_GATE_SIGMOID && p->gate_act != GDR_GATE_SILU) return GDR_ERR_UNSUPPORTED;
+    return GDR_OK;
+}
+int act_of(unsigned gate_act) { return gate_act == GDR_GATE_SIGMOID ? ACT_SIGMOID : gate_act == GDR_GATE_SILU ? ACT_SILU : ACT_RAW; }
+// Rows of all heads at one stride where the tokens follow one another.
+RowIn heads_in(const void *p, int64_t ld, int heads, int D) {
+    if (ld == (int64_t)heads * D) return {p, D, 1, 2};
+    return {p, ld, heads, 2};
+}
+// An output over rows that other threads still read.
+bool over(const void *out, size_t rows, size_t width, const void *in, size_t in_ld) { return touches(out, rows * width, in, rows, width, in_ld); }
+
+}  // namespace
+}  // namespace rownorm
+}  // namespace gdr
+
+using namespace gdr;
+using namespace gdr::rownorm;
+
+extern "C" {
+
+gdr_status gdr_gated_norm_fwd(const gdr_gated_norm_problem *p, const void *x, const void *gate, const void *weight, void *y, void *stream) {
+    gdr_status st = check_gated(p);
+    if (st != GDR_OK) return st;
+    if (p->tokens == 0) return GDR_OK;
+    if (!x || !gate || !weight || !y) return GDR_ERR_NULL;
+    bool vec = p->D % 8 == 0 && p->x_ld % 8 == 0 && p->gate_ld % 8 == 0;
+    if (!ptr_ok(x, 2, &vec) || !ptr_ok(gate, 2, &vec) || !ptr_ok(y, 2, &vec) || !ptr_ok(weight, esize(p->weight_dtype), &vec)) return GDR_ERR_ALIGN;
+    const size_t wide = (size_t)p->heads * p->D * 2;
+    if (over(y, p->tokens, wide, x, p->x_ld * 2) || over(y, p->tokens, wide, gate, p->gate_ld * 2)) return GDR_ERR_UNSUPPORTED;
+    unsigned *err = nullptr;
+    if ((st = device_state(&err)) != GDR_OK) return st;
+    RowArgs a = {};
+    a.in[IN_X] = heads_in(x, p->x_ld, p->heads, p->D), a.in[IN_GATE] = heads_in(gate, p->gate_ld, p->heads, p->D);
+    a.w = weight, a.y = y, a.rows = p->tokens * p->heads, a.D = p->D, a.eps = p->eps;
+    a.w_f32 = p->weight_dtype == GDR_FP32, a.act = act_of(p->gate_act);
+    const RowForm f = form_of(a, a.rows, vec, false);
+    apply(&a, f);
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    return timed(K_GATED_FWD, cs, [&] { return p->dtype == GDR_BF16 ? gated_fwd_bf16(a, f, cs) : gated_fwd_fp16(a, f, cs); });
+}
+
+gdr_status gdr_gated_norm_bwd_workspace_size(const gdr_gated_norm_problem *p, size_t *bytes) {
+    const gdr_status st = check_gated(p);
+    if (st != GDR_OK) return st;
+    if (!bytes) return GDR_ERR_NULL;
+    *bytes = parts_bytes(p->tokens * p->heads, p->D, 1);
+    return GDR_OK;
+}
+
+gdr_status gdr_gated_norm_bwd(const gdr_gated_norm_problem *p, const void *x, const void *gate, const void *weight, const void *dy,
+                              void *dx, void *dgate, void *dweight, void *workspace, size_t workspace_bytes, void *stream) {
+    size_t need = 0;
+    gdr_status st = gdr_gated_norm_bwd_workspace_size(p, &need);
+    if (st != GDR_OK) return st;
+    if (!weight || !dweight || (p->tokens && (!x || !gate || !dy || !dx || !dgate))) return GDR_ERR_NULL;
+    bool vec = p->D % 8 == 0 && p->x_ld % 8 == 0 && p->gate_ld % 8 == 0, any = true;
+    if (!ptr_ok(x, 2, &vec) || !ptr_ok(gate, 2, &vec) || !ptr_ok(dy, 2, &vec) || !ptr_ok(dx, 2, &vec) || !ptr_ok(dgate, 2, &vec) ||
+        !ptr_ok(weight, esize(p->weight_dtype), &vec) || !ptr_ok(dweight, esize(p->weight_dtype), &any))
+        return GDR_ERR_ALIGN;
+    const size_t wide = (size_t)p->heads * p->D * 2;
+    for (const void *o : {dx, dgate})
+        if (over(o, p->tokens, wide, x, p->x_ld * 2) || over(o, p->tokens, wide, gate, p->gate_ld * 2) || over(o, p->tokens, wide, dy, wide))
+            return GDR_ERR_UNSUPPORTED;
+    if (need && (!workspace || workspace_bytes < need)) return GDR_ERR_WORKSPACE;
+    if (need && !aligned_to(workspace, 256)) return GDR_ERR_ALIGN;
+    unsigned *err = nullptr;
+    if ((st = device_state(&err)) != GDR_OK) return st;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (p->tokens == 0) return cuda_status(cudaMemsetAsync(dweight, 0, (size_t)p->D * esize(p->weight_dtype), cs));
+    RowArgs a = {};
+    a.in[IN_X] = heads_in(x, p->x_ld, p->heads, p->D), a.in[IN_GATE] = heads_in(gate, p->gate_ld, p->heads, p->D), a.in[IN_DY] = {dy, p->D, 1, 2};
+    a.w = weight, a.dx = dx, a.dgate = dgate, a.rows = p->tokens * p->heads, a.D = p->D, a.eps = p->eps;
+    a.part = static_cast<float *>(workspace);
+    a.w_f32 = p->weight_dtype == GDR_FP32, a.act = act_of(p->gate_act);
+    const RowForm f = form_of(a, a.rows, vec, true);
+    apply(&a, f);
+    st = timed(K_GATED_BWD, cs, [&] { return p->dtype == GDR_BF16 ? gated_bwd_bf16(a, f, cs) : gated_bwd_fp16(a, f, cs); });
+    if (st != GDR_OK) return st;
+    return timed(K_REDUCE, cs, [&] {
+        const RowSums out = {dweight, p->D};
+        return launch_reduce_rows(a.part, f.blocks, p->D, &out, 1, p->dtype == GDR_BF16, a.w_f32, cs);
+    });
+}
+
+gdr_status gdr_block_norm_fwd(const gdr_block_norm_problem *p, const void *x, const void *residual, const void *weight,
+                              const void *post_weight, const void *gate, void *y, void *residual_out, void *stream) {
+    gdr_status st = check_block(p);
+    if (st != GDR_OK) return st;
+    if (p->rows == 0) return GDR_OK;
+    if (!x || !residual || !weight || !y || !residual_out) return GDR_ERR_NULL;
+    const size_t rs = esize(p->residual_dtype), ws = esize(p->weight_dtype), n = (size_t)p->rows, D = p->D;
+    bool vec = p->D % 8 == 0 && p->x_ld % 8 == 0 && p->gate_ld % 8 == 0;
+    if (!ptr_ok(x, 2, &vec) || !ptr_ok(residual, rs, &vec) || !ptr_ok(weight, ws, &vec) || !ptr_ok(post_weight, ws, &vec) ||
+        !ptr_ok(gate, 2, &vec) || !ptr_ok(y, 2, &vec) || !ptr_ok(residual_out, rs, &vec))
+        return GDR_ERR_ALIGN;
+    // (residual_out may be the residual itself: a thread writes what only it has read; not another overlap of the two)
+    if (over(y, n, 2 * D, x, p->x_ld * 2) || over(y, n, 2 * D, gate, p->gate_ld * 2) || touches(y, n * 2 * D, residual, 1, n * rs * D, n * rs * D) ||
+        touches(y, n * 2 * D, residual_out, 1, n * rs * D, n * rs * D) || over(residual_out, n, rs * D, x, p->x_ld * 2) ||
+        over(residual_out, n, rs * D, gate, p->gate_ld * 2) ||
+        (residual_out != residual && touches(residual_out, n * rs * D, residual, 1, n * rs * D, n * rs * D)))
+        return GDR_ERR_UNSUPPORTED;
+    unsigned *err = nullptr;
+    if ((st = device_state(&err)) != GDR_OK) return st;
+    RowArgs a = {};
+    a.in[IN_X] = {x, p->x_ld, 1, 2}, a.in[IN_RES] = {residual, p->D, 1, (int)rs};
+    if (gate) a.in[IN_GATE] = {gate, p->gate_ld, 1, 2};
+    a.w = weight, a.pw = post_weight, a.y = y, a.res_out = residual_out, a.rows = p->rows, a.D = p->D;
+    a.eps = p->eps, a.rscale = p->residual_scale, a.w_f32 = p->weight_dtype == GDR_FP32, a.act = gate ? act_of(p->gate_act) : ACT_NONE;
+    RowForm f = form_of(a, a.rows, vec, false);
+    f.f32 = p->residual_dtype == GDR_FP32;
+    apply(&a, f);
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    return timed(K_BLOCK_FWD, cs, [&] { return p->dtype == GDR_BF16 ? block_fwd_bf16(a, f, cs) : block_fwd_fp16(a, f, cs); });
+}
+
+gdr_status gdr_block_norm_bwd_workspace_size(const gdr_block_norm_problem *p, size_t *bytes) {
+    const gdr_status st = check_block(p);
+    if (st != GDR_OK) return st;
+    if (!bytes) return GDR_ERR_NULL;
+    *bytes = parts_bytes(p->rows, p->D, 2);
+    return GDR_OK;
+}
+
+gdr_status gdr_block_norm_bwd(const gdr_block_norm_problem *p, const void *x, const void *h, const void *weight, const void *post_weight,
+                              const void *gate, const void *dy, const void *dresidual, void *dx, void *dresidual_in, void *dweight,
+                              void *dpost_weight, void *dgate, void *workspace, size_t workspace_bytes, void *stream) {
+    size_t need = 0;
+    gdr_status st = gdr_block_norm_bwd_workspace_size(p, &need);
+    if (st != GDR_OK) return st;
+    if (!weight || !dweight || ((post_weight != nullptr) != (dpost_weight != nullptr))) return GDR_ERR_NULL;
+    if (p->rows && (!x || !h || !dy || !dx || !dresidual_in || ((gate != nullptr) != (dgate != nullptr)))) return GDR_ERR_NULL;
+    const size_t rs = esize(p->residual_dtype), ws = esize(p->weight_dtype), n = (size_t)p->rows, D = p->D;
+    bool vec = p->D % 8 == 0 && p->x_ld % 8 == 0 && p->gate_ld % 8 == 0, any = true;
+    if (!ptr_ok(x, 2, &vec) || !ptr_ok(h, rs, &vec) || !ptr_ok(weight, ws, &vec) || !ptr_ok(post_weight, ws, &vec) || !ptr_ok(gate, 2, &vec) ||
+        !ptr_ok(dy, 2, &vec) || !ptr_ok(dresidual, rs, &vec) || !ptr_ok(dx, 2, &vec) || !ptr_ok(dresidual_in, rs, &vec) ||
+        !ptr_ok(dgate, 2, &vec) || !ptr_ok(dweight, ws, &any) || !ptr_ok(dpost_weight, ws, &any))
+        return GDR_ERR_ALIGN;
+    for (const void *o : {(const void *)dx, (const void *)dresidual_in, (const void *)dgate}) {
+        const size_t w = (o == dresidual_in ? rs : 2) * D;
+        if (over(o, n, w, x, p->x_ld * 2) || over(o, n, w, gate, p->gate_ld * 2) || touches(o, n * w, h, 1, n * rs * D, n * rs * D) ||
+            touches(o, n * w, dy, 1, n * 2 * D, n * 2 * D) || touches(o, n * w, dresidual, 1, n * rs * D, n * rs * D))
+            return GDR_ERR_UNSUPPORTED;
+    }
+    if (need && (!workspace || workspace_bytes < need)) return GDR_ERR_WORKSPACE;
+    if (need && !aligned_to(workspace, 256)) return GDR_ERR_ALIGN;
+    unsigned *err = nullptr;
+    if ((st = device_state(&err)) != GDR_OK) return st;
+    const cudaStream_t cs = static_cast<cudaStream_t>(stream);
+    if (p->rows == 0) {
+        st = cuda_status(cudaMemsetAsync(dweight, 0, D * ws, cs));
+        return st == GDR_OK && dpost_weight ? cuda_status(cudaMemsetAsync(dpost_weight, 0, D * ws, cs)) : st;
+    }
+    RowArgs a = {};
+    a.in[IN_X] = {x, p->x_ld, 1, 2}, a.in[IN_H] = {h, p->D, 1, (int)rs}, a.in[IN_DY] = {dy, p->D, 1, 2};
+    if (gate) a.in[IN_GATE] = {gate, p->gate_ld, 1, 2};
+    if (dresidual) a.in[IN_DRES] = {dresidual, p->D, 1, (int)rs};
+    a.w = weight, a.pw = post_weight, a.dx = dx, a.dres = dresidual_in, a.dgate = dgate, a.rows = p->rows, a.D = p->D;
+    a.part = static_cast<float *>(workspace);
+    a.eps = p->eps, a.rscale = p->residual_scale, a.w_f32 = p->weight_dtype == GDR_FP32, a.act = gate ? act_of(p->gate_act) : ACT_NONE;
+    RowForm f = form_of(a, a.rows, vec, true);
+    f.f32 = p->residual_dtype == GDR_FP32;
+    apply(&a, f);
+    st = timed(K_BLOCK_BWD, cs, [&] { return p->dtype == GDR_BF16 ? block_bwd_bf16(a, f, cs) : block_bwd_fp16(a, f, cs); });
+    if (st != GDR_OK) return st;
+    return timed(K_REDUCE, cs, [&] {
+        const RowSums out[2] = {{dweight, p->D}, {dpost_weight, p->D}};
+        const int outs = post_weight ? 2 : 1;
+        return launch_reduce_rows(a.part, f.blocks, (long long)outs * p->D, out, outs, p->dtype == GDR_BF16, a.w_f32, cs);
+    });
+}
+
+}  // extern "C"

@@ -1,0 +1,19 @@
+// The block norm's kernels in bf16.
+#include "rownorm.cuh"
+
+namespace gdr {
+namespace rownorm {
+namespace {
+using T = __nv_bfloat16;
+}
+cudaError_t block_fwd_bf16(const RowArgs &a, const RowForm &f, cudaStream_t st) {
+    if (f.f32) GDR_ROW_FORMS(block_fwd_kernel, , true);
+    GDR_ROW_FORMS(block_fwd_kernel, , false);
+}
+cudaError_t block_bwd_bf16(const RowArgs &a, const RowForm &f, cudaStream_t st) {
+    if (f.f32) GDR_ROW_FORMS(block_bwd_kernel, , true);
+    GDR_ROW_FORMS(block_bwd_kernel, , false);
+}
+
+}  // namespace rownorm
+}  // namespace gdr

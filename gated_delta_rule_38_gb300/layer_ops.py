@@ -18,7 +18,8 @@ from . import _lib
 from ._args import _DT, _check, _check_cu, _cu, _need, _rows
 
 __all__ = ["rms_norm", "rms_norm_fwd", "rms_norm_bwd", "short_conv", "short_conv_fwd", "short_conv_bwd",
-           "short_conv_step", "selective_scan", "selective_scan_fwd", "selective_scan_bwd", "selective_scan_step"]
+           "short_conv_step", "selective_scan", "selective_scan_fwd", "selective_scan_bwd", "selective_scan_step",
+           "gated_rms_norm", "gated_rms_norm_fwd", "gated_rms_norm_bwd", "block_norm", "block_norm_fwd", "block_norm_bwd"]
 
 
 def _p(t):
@@ -176,6 +177,171 @@ class _RmsNorm(torch.autograd.Function):
 def rms_norm(x, weight, residual=None, eps=1e-6):
     """Differentiable: (y, residual_out or None).  See rms_norm_fwd."""
     return _RmsNorm.apply(x, weight, None if residual is None else residual.contiguous(), eps)
+
+
+# ---------------------------------------------------------------- norm of a mixer's output with its gate
+
+_ACT = {None: _lib.GDR_GATE_RAW, "sigmoid": _lib.GDR_GATE_SIGMOID, "silu": _lib.GDR_GATE_SILU}
+
+
+def _gated_problem(x, gate, weight, eps, activation):
+    xd = _tokens(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must be [..., D]")
+    D = x.shape[-1]
+    _need(gate, "gate", x.shape, x.dtype, x, False)
+    wd = _dt(weight, "weight", (x.dtype, torch.float32))
+    _need(weight, "weight", (D,), weight.dtype, x)
+    if activation not in ("silu", "sigmoid"):
+        raise ValueError(f"activation is {activation!r}, expected 'silu' or 'sigmoid'")
+    # heads of a token lie side by side, tokens at a stride
+    heads = x.shape[-2] if x.dim() > 2 else 1
+    inner = 2 if heads > 1 else 1
+    (x, x_ld), (gate, g_ld) = _rows(x, inner), _rows(gate, inner)
+    p = _lib.GatedNormProblem(x.numel() // (heads * D) if heads * D else 0, x_ld, g_ld, heads, D, xd, wd, _ACT[activation], eps)
+    return p, x, gate
+
+
+def gated_rms_norm_fwd(x, gate, weight, eps=1e-6, activation="silu", out=None):
+    """y = x / sqrt(mean(x^2) + eps) * weight * act(gate) over the last dimension: a mixer's output norm and its gate.
+
+    x, gate [..., D] bf16 or fp16 (typically [B,T,H,D], a norm a head; slices of a projection are read in place); weight
+    [D] of x's type or fp32; ``activation`` "silu" or "sigmoid".  ``out`` must not overlap x or gate.
+    """
+    p, x, gate = _gated_problem(x, gate, weight, eps, activation)
+    if out is not None:
+        _need(out, "out", x.shape, x.dtype, x)
+    y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _lib.check(_lib.load().gdr_gated_norm_fwd(byref(p), _p(x), _p(gate), _p(weight), _p(y), _s(x)), "gdr_gated_norm_fwd")
+    return y
+
+
+def gated_rms_norm_bwd(x, gate, weight, dy, eps=1e-6, activation="silu"):
+    """(dx, dgate, dweight); dweight in weight's type."""
+    p, x, gate = _gated_problem(x, gate, weight, eps, activation)
+    _need(dy, "dy", x.shape, x.dtype, x, False)
+    dy = dy.contiguous()
+    dx, dg = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for _ in range(2))
+    dw = torch.empty_like(weight)
+    lib = _lib.load()
+    ws, n = _workspace(lib.gdr_gated_norm_bwd_workspace_size, p, x)
+    _lib.check(lib.gdr_gated_norm_bwd(byref(p), _p(x), _p(gate), _p(weight), _p(dy), _p(dx), _p(dg), _p(dw), _p(ws), n, _s(x)),
+               "gdr_gated_norm_bwd")
+    return dx, dg, dw
+
+
+class _GatedRmsNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, gate, weight, eps, activation):
+        ctx.save_for_backward(x, gate, weight)
+        ctx.opt = eps, activation
+        return gated_rms_norm_fwd(x, gate, weight, eps, activation)
+
+    @staticmethod
+    @_once
+    def backward(ctx, dy):
+        dx, dg, dw = gated_rms_norm_bwd(*ctx.saved_tensors, dy, *ctx.opt)
+        return dx, dg, dw, None, None
+
+
+def gated_rms_norm(x, gate, weight, eps=1e-6, activation="silu"):
+    """Differentiable: y.  See gated_rms_norm_fwd."""
+    return _GatedRmsNorm.apply(x, gate, weight, eps, activation)
+
+
+# ---------------------------------------------------------------- norms behind and before a block
+
+def _block_problem(x, h, name, weight, post_weight, gate, gate_activation, residual_scale, eps):
+    xd = _tokens(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must be [..., D]")
+    D = x.shape[-1]
+    hd = _dt(h, name, (x.dtype, torch.float32))
+    _need(h, name, x.shape, h.dtype, x)
+    wd = _dt(weight, "weight", (x.dtype, torch.float32))
+    _need(weight, "weight", (D,), weight.dtype, x)
+    if post_weight is not None:
+        _need(post_weight, "post_weight", (D,), weight.dtype, x)
+    if gate_activation not in _ACT:
+        raise ValueError(f"gate_activation is {gate_activation!r}, expected None, 'sigmoid' or 'silu'")
+    x, x_ld = _rows(x)
+    g_ld = D
+    if gate is not None:
+        _need(gate, "gate", x.shape, x.dtype, x, False)
+        gate, g_ld = _rows(gate)
+    elif gate_activation is not None:
+        raise ValueError("gate_activation without a gate")
+    p = _lib.BlockNormProblem(x.numel() // D if D else 0, x_ld, g_ld, D, xd, wd, hd, _ACT[gate_activation], residual_scale, eps)
+    return p, x, gate
+
+
+def block_norm_fwd(x, residual, weight, post_weight=None, gate=None, gate_activation=None, residual_scale=1.0, eps=1e-6,
+                   out=None):
+    """(y, residual_out) between a block whose output is x and the next one, which reads y:
+
+        b = x / sqrt(mean(x^2) + eps) * post_weight      (x itself without a post_weight)
+        residual_out = residual + residual_scale * b * act(gate)
+        y = residual_out / sqrt(mean(residual_out^2) + eps) * weight
+
+    x [..., D] bf16 or fp16; residual [..., D] of x's type or fp32, as residual_out; weight and post_weight [D] of x's type
+    or fp32 (both the same); gate [..., D] of x's type through ``gate_activation`` (None: as it is, "sigmoid", "silu").
+    ``out`` (for y) must not overlap the inputs.
+    """
+    p, x, gate = _block_problem(x, residual, "residual", weight, post_weight, gate, gate_activation, residual_scale, eps)
+    if out is not None:
+        _need(out, "out", x.shape, x.dtype, x)
+    y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    h = torch.empty(residual.shape, dtype=residual.dtype, device=x.device)
+    _lib.check(_lib.load().gdr_block_norm_fwd(byref(p), _p(x), _p(residual), _p(weight), _p(post_weight), _p(gate), _p(y), _p(h),
+                                              _s(x)), "gdr_block_norm_fwd")
+    return y, h
+
+
+def block_norm_bwd(x, h, weight, dy, dresidual=None, post_weight=None, gate=None, gate_activation=None, residual_scale=1.0,
+                   eps=1e-6):
+    """(dx, dresidual_in, dweight, dpost_weight, dgate) at h, the forward's residual_out; ``dresidual`` (h's type) is the
+    gradient that reaches it from later layers.  The gradients of what was not given are None."""
+    p, x, gate = _block_problem(x, h, "h", weight, post_weight, gate, gate_activation, residual_scale, eps)
+    _need(dy, "dy", x.shape, x.dtype, x, False)
+    dy = dy.contiguous()
+    if dresidual is not None:
+        _need(dresidual, "dresidual", h.shape, h.dtype, x)
+    dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dres = torch.empty(h.shape, dtype=h.dtype, device=x.device)
+    dg = None if gate is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    dw = torch.empty_like(weight)
+    dp = None if post_weight is None else torch.empty_like(post_weight)
+    lib = _lib.load()
+    ws, n = _workspace(lib.gdr_block_norm_bwd_workspace_size, p, x)
+    _lib.check(lib.gdr_block_norm_bwd(byref(p), _p(x), _p(h), _p(weight), _p(post_weight), _p(gate), _p(dy), _p(dresidual),
+                                      _p(dx), _p(dres), _p(dw), _p(dp), _p(dg), _p(ws), n, _s(x)), "gdr_block_norm_bwd")
+    return dx, dres, dw, dp, dg
+
+
+class _BlockNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, residual, weight, post_weight, gate, gate_activation, residual_scale, eps):
+        y, h = block_norm_fwd(x, residual, weight, post_weight, gate, gate_activation, residual_scale, eps)
+        ctx.save_for_backward(x, h, weight, post_weight, gate)
+        ctx.opt = gate_activation, residual_scale, eps
+        ctx.set_materialize_grads(False)
+        return y, h
+
+    @staticmethod
+    @_once
+    def backward(ctx, dy, dh):
+        x, h, weight, post_weight, gate = ctx.saved_tensors
+        if dy is None and dh is None:
+            return (None,) * 8
+        if dy is None:
+            dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
+        dx, dr, dw, dp, dg = block_norm_bwd(x, h, weight, dy, None if dh is None else dh.contiguous(), post_weight, gate, *ctx.opt)
+        return dx, dr, dw, dp, dg, None, None, None
+
+
+def block_norm(x, residual, weight, post_weight=None, gate=None, gate_activation=None, residual_scale=1.0, eps=1e-6):
+    """Differentiable: (y, residual_out).  See block_norm_fwd."""
+    return _BlockNorm.apply(x, residual.contiguous(), weight, post_weight, gate, gate_activation, residual_scale, eps)
 
 
 # ---------------------------------------------------------------- short causal convolution

@@ -449,6 +449,65 @@ gdr_status gdr_lin_bwd(const gdr_lin_problem *p, const void *q, const void *k, c
                        const void *dout, const float *state_in, const float *dstate_out, void *dq, void *dk, void *dv,
                        float *dstate_in, void *workspace, size_t workspace_bytes, void *stream);
 
+/* What a gate's numbers g become: g itself, its sigmoid, or g sigmoid(g). */
+#define GDR_GATE_RAW 0u
+#define GDR_GATE_SIGMOID 1u
+#define GDR_GATE_SILU 2u
+
+/*
+ * A mixer's output norm and gate: over each D columns (a head, or the whole width),
+ *   y = x / sqrt(mean(x^2) + eps) * weight * act(gate)      (act: GDR_GATE_SIGMOID or GDR_GATE_SILU)
+ *   in : x, gate [tokens, heads, D] (dtype, x_ld and gate_ld elements between tokens, heads of a
+ *        token side by side); weight [D] (weight_dtype: dtype or fp32), one for all heads
+ *   out: y [tokens, heads, D] (dtype), contiguous
+ * tokens = 0 is valid.  1 <= D <= GDR_NORM_MAX_D.
+ * Backward: dy [tokens, heads, D] -> dx, dgate (dtype, contiguous), dweight [D] (weight_dtype).
+ * Fixed summation order.  Outputs overlap no input (GDR_ERR_UNSUPPORTED).
+ */
+typedef struct gdr_gated_norm_problem {
+    int64_t tokens, x_ld, gate_ld;
+    int heads, D;
+    gdr_dtype dtype, weight_dtype;
+    unsigned gate_act;
+    float eps;
+} gdr_gated_norm_problem;
+gdr_status gdr_gated_norm_fwd(const gdr_gated_norm_problem *p, const void *x, const void *gate, const void *weight,
+                              void *y, void *stream);
+gdr_status gdr_gated_norm_bwd_workspace_size(const gdr_gated_norm_problem *p, size_t *bytes);
+gdr_status gdr_gated_norm_bwd(const gdr_gated_norm_problem *p, const void *x, const void *gate, const void *weight,
+                              const void *dy, void *dx, void *dgate, void *dweight, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
+/*
+ * The norms behind a block and before the next one, with the block's gate and residual scale:
+ *   b = x / sqrt(mean(x^2) + eps) * post_weight   (x itself without a post_weight)
+ *   h = residual + residual_scale * b * act(gate) (no gate: 1)
+ *   y = h / sqrt(mean(h^2) + eps) * weight
+ *   in : x [rows, D], gate [rows, D] or NULL (dtype, row strides x_ld, gate_ld); residual [rows, D]
+ *        (residual_dtype: dtype or fp32); weight [D], post_weight [D] or NULL (weight_dtype: dtype or fp32)
+ *   out: y [rows, D] (dtype); residual_out [rows, D] = h in residual_dtype (may be `residual`)
+ * y is computed from the unrounded sum.  rows = 0 is valid.  1 <= D <= GDR_NORM_MAX_D.
+ * Backward at the stored h (residual_out): dy [rows, D] (dtype), dresidual [rows, D] (residual_dtype), the
+ * gradient that reaches h from later layers, or NULL
+ *   out: dx [rows, D] (dtype), dresidual_in [rows, D] (residual_dtype), dweight, dpost_weight [D] (weight_dtype;
+ *        the latter exactly with post_weight), dgate [rows, D] (dtype; exactly with gate)
+ * Fixed summation order.  Other overlaps of outputs with inputs: GDR_ERR_UNSUPPORTED.
+ */
+typedef struct gdr_block_norm_problem {
+    int64_t rows, x_ld, gate_ld;
+    int D;
+    gdr_dtype dtype, weight_dtype, residual_dtype;
+    unsigned gate_act; /* read with a gate */
+    float residual_scale, eps;
+} gdr_block_norm_problem;
+gdr_status gdr_block_norm_fwd(const gdr_block_norm_problem *p, const void *x, const void *residual, const void *weight,
+                              const void *post_weight, const void *gate, void *y, void *residual_out, void *stream);
+gdr_status gdr_block_norm_bwd_workspace_size(const gdr_block_norm_problem *p, size_t *bytes);
+gdr_status gdr_block_norm_bwd(const gdr_block_norm_problem *p, const void *x, const void *h, const void *weight,
+                              const void *post_weight, const void *gate, const void *dy, const void *dresidual, void *dx,
+                              void *dresidual_in, void *dweight, void *dpost_weight, void *dgate, void *workspace,
+                              size_t workspace_bytes, void *stream);
+
 /* Synchronises `stream`, then returns and clears the device error word of the
  * current device (GDR_OK when no kernel latched an error), or GDR_ERR_CUDA when
  * the stream reports a CUDA error. */
