@@ -120,7 +120,7 @@ gdr_status gdr_lin_fwd(const gdr_lin_problem *p, const void *q, const void *k, c
     if (tokens == 0 && !state_out) return GDR_OK;
     Walk &w = lp.w[0];
     if (tokens && (!token_map(&w.tq, p, q, p->q_ld, p->Hk, p->K) || !token_map(&w.tk, p, k, p->k_ld, p->Hk, p->K) ||
-                   !token_map(&w.tv, p, v, p->v_ld, p->H, p->V)))
+                   !token_map(&w.tv, p, v, p->v_ld, p->H, p->V) || !token_map(&w.to, p, o, (int64_t)p->H * p->V, p->H, p->V)))
         return cuda_status(cudaErrorInvalidValue);
     w.kd = p->K, w.vd = p->V;
     w.q_div = w.k_div = p->H / p->Hk, w.v_div = 1;
@@ -190,6 +190,10 @@ gdr_status gdr_lin_bwd(const gdr_lin_problem *p, const void *q, const void *k, c
                    !token_map(&mv, p, v, p->v_ld, p->H, p->V) || !token_map(&md, p, dout, (int64_t)p->H * p->V, p->H, p->V)))
         return cuda_status(cudaErrorInvalidValue);
     const int grp = p->H / p->Hk;
+    if (tokens && (!token_map(&lp.w[1].to, p, dv, (int64_t)p->H * p->V, p->H, p->V) ||
+                   (grp == 1 && (!token_map(&lp.w[2].to, p, dk, (int64_t)p->H * p->K, p->H, p->K) ||
+                                 !token_map(&lp.w[0].to, p, dq, (int64_t)p->H * p->K, p->H, p->K)))))
+        return cuda_status(cudaErrorInvalidValue);
     char *ws = static_cast<char *>(workspace);
     float *fw = reinterpret_cast<float *>(ws), *bw = reinterpret_cast<float *>(ws + l.one);
     float *pq = grp > 1 ? reinterpret_cast<float *>(ws + l.dq) : nullptr, *pk = grp > 1 ? reinterpret_cast<float *>(ws + l.dk) : nullptr;

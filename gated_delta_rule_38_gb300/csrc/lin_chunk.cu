@@ -11,15 +11,17 @@
 // keys then enter the state with lambda^(s+1).  So one kernel runs the forward and, three walks side by side, the
 // backward.
 //
-// One CTA of 18 warps walks one segment of a sequence for one head; all tiles are 128 wide (narrower heads load zeros).
-//   warps 0..7    the state: row 32 (w mod 4) + lane, 64 of the 128 columns.  fp32 in registers, a copy rounded to 16
-//                 bits in shared memory as the operand of Q S; between two updates they take the output rows
-//   warps 8..15   P from Q K^T (tensor memory to tensor memory, where it is the left operand of P V), and the decayed
-//                 keys, a 16-bit number and the remainder's 16-bit number each: two products whose sum is as good as
-//                 keys of 16 bits of mantissa, because the states are handed on in fp32 (rounded once they would be
-//                 off by 1e-3; so they are by 4e-6)
-//   warp 16       tile loads (TMA) into a ring of five 32 KB tiles
+// One CTA walks one segment of a sequence for one head; all tiles are 128 wide (narrower heads load zeros).
+//   warps 0..15   lanes 32 (w mod 4) .., columns 32 (w / 4) ..: the block of P from Q K^T (tensor memory to tensor memory,
+//                 where it is the left operand of P V), the decayed keys, the output rows, and the state, fp32 in
+//                 registers with a copy rounded to 16 bits in shared memory as the operand of Q S
+//   warp 16       tile loads (TMA) into a ring of five 32 KB tiles, and the output tiles' stores
 //   warp 17       the MMAs
+// The sixteen warps pass through these steps together: four roles of four warps each needed more registers than a thread
+// can have beside them, and what they spilled went to L2 (B = 1, T = 2048, 152 heads: 156 us, STEPS us so).
+// A decayed key is two 16-bit numbers, the rounded one and the remainder's, each with a product of its own: their sum is
+// as good as keys of 16 bits of mantissa, because the states are handed on in fp32 (rounded once they would be off by
+// 1e-3; so they are by 3e-6).
 // The accumulators of one chunk's state update start from zero and are added to the state in fp32 registers, rounded to
 // nearest: in the tensor core's own accumulator the additions of a long walk would lose in one direction.
 // lambda^128 is kept as two fp32 numbers, so that a memory of any length is not off by what rounding it once would add up to.
@@ -36,19 +38,22 @@ namespace gdr {
 namespace lin {
 namespace {
 
-constexpr int NT = 576;
+constexpr int NW = 16, NT = 32 * (NW + 2);        // working warps; threads
 constexpr uint32_t TILE = 32768, BLK = 16384;     // a tile: two blocks of 64 columns, 128 rows each
 constexpr int RING = 5;
 constexpr uint32_t S_LO = RING * TILE;            // the keys' remainders
 constexpr uint32_t S_ST = S_LO + TILE;            // the state's copy (state pass: the remainders of odd chunks)
 constexpr uint32_t S_BAR = S_ST + TILE;
-constexpr uint32_t B_FULL = S_BAR, B_EMPTY = S_BAR + 8 * RING, B_QK = B_EMPTY + 8 * RING, B_S = B_QK + 8, B_P = B_S + 16,
-                   B_K = B_P + 8, B_PV = B_K + 16, B_DS = B_PV + 8, B_DONE = B_DS + 16, S_SLOT = B_DONE + 8, S_FLAG = S_SLOT + 4;
+constexpr uint32_t B_FULL = S_BAR, B_EMPTY = S_BAR + 8 * RING, B_QK = B_EMPTY + 8 * RING, B_S = B_QK + 8, B_P = B_S + 8,
+                   B_O = B_P + 8, B_PV = B_O + 8, B_K = B_PV + 8, B_DS = B_K + 16, B_DONE = B_DS + 16, S_SLOT = B_DONE + 8, S_FLAG = S_SLOT + 4;
 constexpr uint32_t S_LAM = S_FLAG + 8;            // lambda^128 as two fp32 numbers
-constexpr uint32_t S_BYTES = S_LAM + 8 + 1024;
+// decays of up to 31 tokens: COL[c] = lambda^(31-c) (rev: lambda^c); DIAG[31 + row - key] = lambda^|row - key| where the row
+// sees the key, else 0
+constexpr uint32_t S_COL = (S_LAM + 8 + 15) / 16 * 16, S_DIAG = S_COL + 128;
+constexpr uint32_t S_BYTES = S_DIAG + 256 + 1024;
 static_assert(S_BYTES <= kSmemMost, "shared memory");
-// tensor memory columns: Q K^T and, in its place, P (columns s < 64 at T_P0, the others at T_P1); Q S; P V; the update
-constexpr uint32_t T_QK = 0, T_P0 = 0, T_P1 = 64, T_QS = 128, T_PV = 256, T_DS = 384;
+// tensor memory columns: Q K^T and, in its place, P (each 32 columns in the lower half of their own); Q S; P V; the update
+constexpr uint32_t T_QK = 0, T_QS = 128, T_PV = 256, T_DS = 384;
 
 template <typename T> struct IsBf16 { static constexpr bool value = false; };
 template <> struct IsBf16<__nv_bfloat16> { static constexpr bool value = true; };
@@ -58,41 +63,50 @@ template <> struct IsBf16<__nv_bfloat16> { static constexpr bool value = true; }
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
-constexpr long kPolls = 8000000L;
-// Waits for a barrier's phase; gives up when another role raised the block's flag, or after a bound (then it raises it).
-__device__ __noinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *flag, unsigned *err) {
-    for (long it = 0; it < kPolls; ++it) {
-        uint32_t done;
-        asm volatile(
-            "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\nselp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(done)
-            : "r"(bar), "r"(parity), "r"(500u)  // (ns: each try suspends at most about that long)
-            : "memory");
-        if (done) return true;
-        if ((it & 63) == 63 && *flag) return false;
+__device__ __forceinline__ uint32_t lds32_now(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float lds_f(uint32_t addr) { return __uint_as_float(lds32(addr)); }
+constexpr unsigned long long kWaitNs = 2000000000ull;
+__device__ __forceinline__ unsigned long long now_ns() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %globaltimer;\n" : "=l"(t));
+    return t;
+}
+__device__ __forceinline__ bool try_phase(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+// Waits for a barrier's phase; gives up when another role raised the block's flag, or after two seconds (then it raises it).
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, uint32_t flag, unsigned *err) {
+    if (try_phase(bar, parity)) return true;
+    const unsigned long long from = now_ns();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i)
+            if (try_phase(bar, parity)) return true;
+        if (lds32_now(flag)) return false;
+        if (now_ns() - from > kWaitNs) break;
     }
     raise_error(err, GDR_ERR_TIMEOUT);
-    *flag = 1;
+    sts32(flag, 1);
     return false;
 }
 // Every lane polls and the warp agrees on the outcome.
-__device__ __forceinline__ bool wwait(uint32_t bar, uint32_t parity, volatile int *flag, unsigned *err) {
+__device__ __forceinline__ bool wwait(uint32_t bar, uint32_t parity, uint32_t flag, unsigned *err) {
     return __all_sync(0xffffffffu, wait_phase(bar, parity, flag, err));
 }
 
 // ---------------------------------------------------------------- tensor memory
 
-// 32 lanes x 32 or 16 columns; the wait names the registers, so that nothing that uses them moves above it.
-__device__ __forceinline__ void tld32(uint32_t a, uint32_t *r) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(a));
-}
+// 32 lanes x 16 columns; the wait names the registers, so that nothing that uses them moves above it.
 __device__ __forceinline__ void tld16(uint32_t a, uint32_t *r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
@@ -105,24 +119,38 @@ __device__ __forceinline__ void twait16(uint32_t *r) {
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
                    "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
-__device__ __forceinline__ void twait32(uint32_t *r) {
-    twait16(r);
-    twait16(r + 16);
-}
-__device__ __forceinline__ void tst16(uint32_t a, const uint32_t *r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(a),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
+__device__ __forceinline__ void tst8(uint32_t a, const uint32_t *r) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(a), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 __device__ __forceinline__ void tst_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-// D (+)= A B with A in tensor memory.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool accumulate) {
+// D (+)= A B, issued by the lane that has `on`; the whole warp computes the operands, which so stay uniform.  (In a branch
+// of one lane every MMA took 100 cycles to issue, half as long again as it runs.)
+__device__ __forceinline__ void mma_ss(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t id, bool accumulate) {
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-        "r"(a), "l"(b), "r"(id), "r"((uint32_t)accumulate));
+        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"((uint32_t)accumulate), "r"(on));
+}
+// ... with A in tensor memory.
+__device__ __forceinline__ void mma_ts(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool accumulate) {
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(id), "r"((uint32_t)accumulate), "r"(on));
+}
+__device__ __forceinline__ void commit_on(uint32_t on, uint32_t bar) {
+    asm volatile(
+        "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar), "r"(on));
+}
+// A descriptor's words: the upper one is the same for every step of an operand, the lower one moves on by 16 bytes each.
+__device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) {
+    const uint32_t lo = (uint32_t)d + (bytes >> 4), hi = (uint32_t)(d >> 32);
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
 }
 __device__ __forceinline__ f2 f2_of(uint32_t lo, uint32_t hi) {
     return pack2(__uint_as_float(lo), __uint_as_float(hi));
@@ -201,7 +229,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sb = smem_u32(smem);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const LinArgs &a = p.a;
     const unsigned item = blockIdx.x;
     const int wi = (int)(item % (unsigned)a.nwalk);
@@ -226,8 +254,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
     if (nc == 0 && !(w.end != nullptr)) return;
     const bool has_start = !STATES && (w.start != nullptr || !at_start);
     const bool want_end = STATES || (w.end != nullptr && at_end);
-    volatile int *flag = reinterpret_cast<volatile int *>(smem + S_FLAG);
-    volatile float *lam = reinterpret_cast<volatile float *>(smem + S_LAM);
+    const uint32_t flag = sb + S_FLAG;
     const float g = a.decay[j] < -120.f ? -120.f : a.decay[j];  // (e^-120 is 0 in fp32; 0 x -inf would be NaN)
     const float lg = g * LOG2E;
 
@@ -237,23 +264,29 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
             umma::mbar_init(sb + B_EMPTY + 8 * i, 1);
         }
         umma::mbar_init(sb + B_QK, 1);
-        umma::mbar_init(sb + B_P, 8);
         umma::mbar_init(sb + B_PV, 1);
+        umma::mbar_init(sb + B_S, NW);
+        umma::mbar_init(sb + B_P, NW);
+        umma::mbar_init(sb + B_O, NW);
         for (int i = 0; i < 2; ++i) {
-            umma::mbar_init(sb + B_S + 8 * i, 8);
-            umma::mbar_init(sb + B_K + 8 * i, 8);
+            umma::mbar_init(sb + B_K + 8 * i, NW);
             umma::mbar_init(sb + B_DS + 8 * i, 1);
         }
         umma::mbar_init(sb + B_DONE, 1);
         umma::fence_mbar_init();
-        *flag = 0;
+        sts32(flag, 0);
     }
     if (tid == 32) {
         const double l = exp((double)g * LC);
-        lam[0] = (float)l;
-        lam[1] = (float)(l - (double)(float)l);
+        sts32(sb + S_LAM, __float_as_uint((float)l));
+        sts32(sb + S_LAM + 4, __float_as_uint((float)(l - (double)(float)l)));
     }
-    if (warp == 17) umma::alloc(sb + S_SLOT, 512);
+    if (tid >= 64 && tid < 96) reinterpret_cast<float *>(smem + S_COL)[lane] = ex2((float)(rev ? lane : 31 - lane) * lg);
+    if (tid >= 96 && tid < 160) {
+        const int d = rev ? 31 - (tid - 96) : tid - 96 - 31;
+        reinterpret_cast<float *>(smem + S_DIAG)[tid - 96] = d >= 0 ? ex2((float)d * lg) : 0.f;
+    }
+    if (warp == NW + 1) umma::alloc(sb + S_SLOT, 512);
     umma::fence_before();
     __syncthreads();
     umma::fence_after();
@@ -274,23 +307,41 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
     const int ksteps = (kd + 15) / 16, kblk = kd > 64 ? 2 : 1, vblk = vd > 64 ? 2 : 1;
     const int NV = (vd + 15) / 16 * 16;
 
-    if (warp == 16) {
-        // ------------------------------------------------------------ tile loads
+    // full chunks' 16-bit output rows leave through the q tile as a TMA store
+    const bool staged = !STATES && !w.out_f32;
+    if (warp == NW) {
+        // ------------------------------------------------------------ tile loads, output stores
         const int hq = j / w.q_div, hk = j / w.k_div, hv = j / w.v_div;
         int issued = 0;
         bool ok = true;
+        auto store = [&](int c) {  // the output rows of chunk c, once they are in its q tile
+            ok = ok && wwait(sb + B_O, c & 1, flag, a.err);
+            int t, L;
+            chunk(c, t, L);
+            if (ok && staged && L == LC && lane == 0) {
+                for (int b = 0; b < vblk; ++b) tma::store3d(&w.to, 64 * b, j, t, sb + slot_of(c, 0) * TILE + b * BLK);
+                tma::commit_group();
+                tma::wait_read();
+            }
+            __syncwarp();
+        };
         for (int c = 0; c < nc && ok; ++c) {
             int t, L;
             chunk(c, t, L);
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
                 const int x = PER * c + i, sl = x % RING;
-                if (x >= RING) ok = ok && wwait(sb + B_EMPTY + 8 * sl, ((x / RING) - 1) & 1, flag, a.err);
+                const CUtensorMap *m = i == VI ? &w.tv : i == KI ? &w.tk : &w.tq;
+                const int h = i == VI ? hv : i == KI ? hk : hq, nb = i == VI ? vblk : kblk;
+                if (x >= RING) {
+                    if (lane == 0)
+                        for (int b = 0; b < nb; ++b) tma::prefetch3d(m, 64 * b, h, t);
+                    if (!STATES && (x - RING) % PER == 0) store((x - RING) / PER);
+                    else ok = ok && wwait(sb + B_EMPTY + 8 * sl, ((x / RING) - 1) & 1, flag, a.err);
+                }
                 if (!ok) break;
                 if (lane == 0) {
                     const uint32_t dst = sb + sl * TILE, bar = sb + B_FULL + 8 * sl;
-                    const CUtensorMap *m = i == VI ? &w.tv : i == KI ? &w.tk : &w.tq;
-                    const int h = i == VI ? hv : i == KI ? hk : hq, nb = i == VI ? vblk : kblk;
                     tma::expect_tx(bar, nb * BLK);
                     for (int b = 0; b < nb; ++b) tma::load3d(dst + b * BLK, m, 64 * b, h, t, bar);
                 }
@@ -298,15 +349,19 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                 __syncwarp();
             }
         }
+        if (!STATES && ok)  // the q tiles that nothing was loaded into since
+            for (int c = max(0, (PER * nc - RING + PER - 1) / PER); c < nc; ++c) store(c);
+        if (lane == 0) tma::wait_all();
         if (!ok) {  // after an error: let the loads in flight land (bounded)
             for (int x = max(0, issued - RING); x < issued; ++x)
                 umma::mbar_spin(sb + B_FULL + 8 * (x % RING), (x / RING) & 1, 4000000L);
         }
-    } else if (warp == 17) {
+    } else if (warp == NW + 1) {
         // ------------------------------------------------------------ MMAs
         constexpr bool bf = IsBf16<T>::value;
         const uint32_t i_qk = umma::idesc(128, 128, bf, false, false), i_qs = umma::idesc(128, NV, bf, false, true),
                        i_ds = umma::idesc(128, NV, bf, true, true);
+        const uint32_t on = lane == 0;
         bool ok = true;
         for (int c = 0; c < nc; ++c) {
             int t, L;
@@ -322,189 +377,84 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                 if (c > 0) ok = ok && wwait(sb + B_PV, (c - 1) & 1, flag, a.err);
                 if (!ok) break;
                 umma::fence_after();
-                if (lane == 0) {
-                    for (int ks = 0; ks < ksteps; ++ks) {
+                const uint64_t dq = umma::desc(qt, 16, 1024), dk = umma::desc(kt, 16, 1024);
+                {
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) {
                         const uint32_t o = (uint32_t)(ks >> 2) * BLK + (uint32_t)(ks & 3) * 32u;
-                        umma::mma(tmem + T_QK, umma::desc(qt + o, 16, 1024), umma::desc(kt + o, 16, 1024), i_qk, ks > 0);
+                        if (ks < ksteps) mma_ss(on, tmem + T_QK, desc_at(dq, o), desc_at(dk, o), i_qk, ks > 0);
                     }
-                    umma::commit(sb + B_QK);
+                    commit_on(on, sb + B_QK);
                 }
-                __syncwarp();
                 // the state's copy is there, and the accumulators of the chunk before have been read
                 ok = ok && wwait(sb + B_S, c & 1, flag, a.err);
                 if (!ok) break;
                 umma::fence_after();
-                if (lane == 0) {
-                    if (use_s) {
-                        for (int ks = 0; ks < ksteps; ++ks) {
-                            const uint32_t o = (uint32_t)(ks >> 2) * BLK + (uint32_t)(ks & 3) * 32u;
-                            umma::mma(tmem + T_QS, umma::desc(qt + o, 16, 1024),
-                                      umma::desc(sb + S_ST + (uint32_t)ks * 2048u, BLK, 1024), i_qs, ks > 0);
-                        }
+                if (use_s) {
+                    const uint64_t ds = umma::desc(sb + S_ST, BLK, 1024);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks) {
+                        const uint32_t o = (uint32_t)(ks >> 2) * BLK + (uint32_t)(ks & 3) * 32u;
+                        if (ks < ksteps) mma_ss(on, tmem + T_QS, desc_at(dq, o), desc_at(ds, ks * 2048u), i_qs, ks > 0);
                     }
-                    umma::commit(sb + B_EMPTY + 8 * slot_of(c, 0));
                 }
-                __syncwarp();
                 ok = ok && wwait(sb + B_P, c & 1, flag, a.err);
                 ok = ok && wwait(sb + B_FULL + 8 * slot_of(c, VI), phase_of(c, VI), flag, a.err);
                 if (!ok) break;
                 umma::fence_after();
-                if (lane == 0) {
-                    for (int ks = 0; ks < ts; ++ks)
-                        mma_ts(tmem + T_PV, tmem + (ks < 4 ? T_P0 + 8 * ks : T_P1 + 8 * (ks - 4)),
-                               umma::desc(vt + (uint32_t)ks * 2048u, BLK, 1024), i_qs, ks > 0);
-                    umma::commit(sb + B_PV);
+                {
+                    const uint64_t dv = umma::desc(vt, BLK, 1024);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        if (ks < ts) mma_ts(on, tmem + T_PV, tmem + T_QK + 32 * (ks >> 1) + 8 * (ks & 1), desc_at(dv, ks * 2048u), i_qs, ks > 0);
+                    commit_on(on, sb + B_PV);
                 }
-                __syncwarp();
             } else {
                 ok = ok && wwait(sb + B_FULL + 8 * slot_of(c, VI), phase_of(c, VI), flag, a.err);
             }
             if (upd) {
+                // (state pass: the keys of chunk c come after the state has taken the accumulator of chunk c - 2)
                 ok = ok && wwait(bar_of(B_K, c), par_of(c), flag, a.err);
-                // (state pass: the accumulator of two chunks before has been read)
-                if (STATES && c >= 2) ok = ok && wwait(bar_of(B_S, c), par_of(c - 2), flag, a.err);
                 if (!ok) break;
                 umma::fence_after();
-                if (lane == 0) {
+                {
                     const uint32_t lo = sb + (STATES && (c & 1) ? S_ST : S_LO), d = tmem + T_DS - (STATES && (c & 1) ? 128 : 0);
-                    for (int half = 0; half < 2; ++half)
-                        for (int ks = 0; ks < ts; ++ks)
-                            umma::mma(d, umma::desc((half ? lo : kt) + (uint32_t)ks * 2048u, BLK, 1024),
-                                      umma::desc(vt + (uint32_t)ks * 2048u, BLK, 1024), i_ds, half || ks > 0);
-                    umma::commit(bar_of(B_DS, c));
+                    const uint64_t dv = umma::desc(vt, BLK, 1024), dh = umma::desc(kt, BLK, 1024), dl = umma::desc(lo, BLK, 1024);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        if (ks < ts) mma_ss(on, d, desc_at(dh, ks * 2048u), desc_at(dv, ks * 2048u), i_ds, ks > 0);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        if (ks < ts) mma_ss(on, d, desc_at(dl, ks * 2048u), desc_at(dv, ks * 2048u), i_ds, true);
+                    commit_on(on, bar_of(B_DS, c));
                 }
-                __syncwarp();
             }
             if (!ok) break;
-            if (lane == 0) {
-                umma::commit(sb + B_EMPTY + 8 * slot_of(c, KI));
-                umma::commit(sb + B_EMPTY + 8 * slot_of(c, VI));
+            {  // (a q tile's too, so that every use of a place is one phase: the output's store waits longer)
+#pragma unroll
+                for (int i = 0; i < PER; ++i) commit_on(on, sb + B_EMPTY + 8 * slot_of(c, i));
             }
-            __syncwarp();
         }
         // every MMA, and every arrival that waits for one, has happened before shared memory goes away
-        if (lane == 0) {
-            umma::commit(sb + B_DONE);
-            umma::mbar_spin(sb + B_DONE, 0, 4000000L);
-        }
-        __syncwarp();
-    } else if (warp >= 8) {
-        // ------------------------------------------------------------ P, and the decayed keys
-        const int grp = (warp - 8) >> 2, q4 = warp & 3, r = q4 * 32 + lane;
-        const uint32_t quad = (uint32_t)(q4 * 32) << 16;
-        const float s_kv = w.s_kv;
-        bool ok = true;
-        for (int c = 0; c < nc; ++c) {
-            int t, L;
-            chunk(c, t, L);
-            const uint32_t kt = sb + slot_of(c, KI) * TILE, vt = sb + slot_of(c, VI) * TILE;
-            const bool upd = want_end || c + 1 < nc;
-            if (!STATES) {
-                ok = wwait(sb + B_QK, c & 1, flag, a.err);
-                if (!ok) break;
-                umma::fence_after();
-#pragma unroll
-                for (int hb = 0; hb < 2; ++hb) {
-                    const int sblk = grp * 2 + hb;  // columns s = 32 sblk ..
-                    const uint32_t col = T_QK + 32 * sblk, dst = tmem + quad + (grp ? T_P1 : T_P0) + 16 * hb;
-                    uint32_t o[16];
-                    const int dist = rev ? sblk - q4 : q4 - sblk;  // blocks of 32 between the keys and the row
-                    if (dist < 0) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) o[i] = 0;
-                    } else {
-                        uint32_t x[32];
-                        tld32(tmem + quad + col, x);
-                        twait32(x);
-                        // lambda^|r-s|: on the diagonal one exponential each; beyond it a row's factor (distance to the
-                        // block's near edge) times a column's (from there), both at most 1
-                        const float rowf = s_kv * ex2((float)(32 * dist + (rev ? -lane : lane - 31)) * lg);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            float f[2], v[2] = {__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])};
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int cc = 2 * i + e, d = rev ? cc - lane : lane - cc;
-                                bool in = true;
-                                if (dist == 0) {
-                                    in = d >= 0;
-                                    f[e] = s_kv * ex2((float)d * lg);
-                                } else {
-                                    f[e] = rowf * ex2((float)(rev ? cc : 31 - cc) * lg);
-                                }
-                                if (rev) in = in && 32 * sblk + cc < L;
-                                v[e] = in ? v[e] * f[e] : 0.f;
-                            }
-                            o[i] = Elt<T>::pack(v[0], v[1]);
-                        }
-                    }
-                    tst16(dst, o);
-                }
-                tst_wait();
-                umma::fence_before();
-            }
-            if (L < LC || STATES || upd) {
-                ok = wwait(sb + B_FULL + 8 * slot_of(c, VI), phase_of(c, VI), flag, a.err);
-                ok = ok && wwait(sb + B_FULL + 8 * slot_of(c, KI), phase_of(c, KI), flag, a.err);
-                if (!ok) break;
-            }
-            if (L < LC) {
-                // the rows behind a short chunk are another sequence's: what they hold must not meet even a zero
-                if (r >= L && r < (L + 15) / 16 * 16 && grp < vblk)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) umma::st_shared_v4(vt + grp * BLK + r * 128 + i * 16, 0, 0, 0, 0);
-                umma::fence_async_smem();
-            }
-            if (!STATES) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sb + B_P);
-            }
-            if (upd) {
-                // (the remainders' place: read by the update of one chunk before, or two)
-                if (STATES && c >= 2) {
-                    ok = wwait(bar_of(B_DS, c), par_of(c - 2), flag, a.err);
-                    if (!ok) break;
-                }
-                const uint32_t lo = sb + (STATES && (c & 1) ? S_ST : S_LO);
-                const float f = s_kv * ex2((float)(rev ? r + 1 : L - 1 - r) * lg);
-                const bool in = r < L;
-                if (grp < kblk) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t off = grp * BLK + r * 128 + i * 16;
-                        const uint4 u = umma::ld_shared_v4(kt + off);
-                        const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-                        uint32_t h[4], l[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const f2 v = mul2(widen2<T>(x[e]), both(f));
-                            h[e] = narrow2<T>(v);
-                            l[e] = narrow2<T>(fma2(widen2<T>(h[e]), both(-1.f), v));
-                            if (!in) h[e] = l[e] = 0;
-                        }
-                        umma::st_shared_v4(kt + off, h[0], h[1], h[2], h[3]);
-                        umma::st_shared_v4(lo + off, l[0], l[1], l[2], l[3]);
-                    }
-                }
-                umma::fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_of(B_K, c));
-            }
-        }
+        commit_on(on, sb + B_DONE);
+        umma::mbar_spin(sb + B_DONE, 0, 4000000L);
     } else {
-        // ------------------------------------------------------------ the state and the output rows
-        const int cg = warp >> 2, q4 = warp & 3, row = q4 * 32 + lane;
-        const uint32_t quad = (uint32_t)(q4 * 32) << 16;
+        // ------------------------------------------------------------ P, keys, output rows, state
+        const int q4 = warp & 3, g4 = warp >> 2, row = q4 * 32 + lane, c0 = g4 * 32;
+        const uint32_t quad = tmem + ((uint32_t)(q4 * 32) << 16);
+        const float s_kv = w.s_kv;
+        const uint32_t tile_row = (uint32_t)(c0 >> 6) * BLK + row * 128;  // this thread's 32 columns of a tile: four places
+        auto place = [&](int i) { return tile_row + ((((uint32_t)(c0 & 63) / 8 + i) ^ (row & 7)) << 4); };
         const bool live = row < kd;
-        f2 st[32];
+        f2 st[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) st[i] = 0ull;
-        if (!STATES) {
+        for (int i = 0; i < 16; ++i) st[i] = 0ull;
+        if (!STATES && has_start) {
             if (w.start) {
                 const float *s0 = w.start + ((long long)seg.n * a.H + j) * kd * vd + (long long)row * w.rs;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int col = cg * 64 + 2 * i;
+                for (int i = 0; i < 16; ++i) {
+                    const int col = c0 + 2 * i;
                     if (live && col < vd) st[i] = pack2(s0[(long long)col * w.cs], s0[(long long)(col + 1) * w.cs]);
                 }
             }
@@ -514,133 +464,222 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                 int pos = rev ? seg.seq1 : seg.seq0;
                 const int stop = rev ? seg.t1 : seg.t0;
                 while (pos != stop) {
-                    int from, to;
-                    if (rev) {
-                        to = pos;
-                        from = max(wc.last(seg, pos - 1), seg.seq0);
-                        pos = from;
-                    } else {
-                        from = pos;
-                        to = wc.next(seg, pos);
-                        pos = to;
-                    }
+                    const int at = pos;
+                    const int from = rev ? max(wc.last(seg, pos - 1), seg.seq0) : pos;
+                    pos = rev ? from : wc.next(seg, pos);
                     const float *e = w.ext + (wc.place(seg, from) * a.H + j) * kStateFloats + (long long)row * w.ers;
-                    const f2 d = both(ex2((float)(to - from) * lg));
+                    const f2 d = both(ex2((float)(rev ? at - from : pos - at) * lg));
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int col = cg * 64 + 2 * i;
+                    for (int i = 0; i < 16; ++i) {
+                        const int col = c0 + 2 * i;
                         if (live && col < vd) st[i] = fma2(d, st[i], pack2(e[(long long)col * w.ecs], e[(long long)(col + 1) * w.ecs]));
                     }
                 }
             }
         }
         auto put_state = [&]() {
-            if (cg * 64 < NV) {
+            if (c0 < NV) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    umma::st_shared_v4(sb + S_ST + cg * BLK + row * 128 + (((uint32_t)i ^ (row & 7)) << 4), narrow2<T>(st[4 * i]),
-                                       narrow2<T>(st[4 * i + 1]), narrow2<T>(st[4 * i + 2]), narrow2<T>(st[4 * i + 3]));
+                for (int i = 0; i < 4; ++i)
+                    umma::st_shared_v4(sb + S_ST + place(i), narrow2<T>(st[4 * i]), narrow2<T>(st[4 * i + 1]),
+                                       narrow2<T>(st[4 * i + 2]), narrow2<T>(st[4 * i + 3]));
             }
             umma::fence_async_smem();
         };
+        // the state after chunk c
+        auto update = [&](int c, int L) {
+            if (c0 >= NV) return;
+            umma::fence_after();
+            const f2 l1 = both(L == LC ? lds_f(sb + S_LAM) : ex2((float)L * lg)), l2 = both(L == LC ? lds_f(sb + S_LAM + 4) : 0.f);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t x[16];
+                tld16(quad + T_DS - (STATES && (c & 1) ? 128 : 0) + c0 + 16 * h, x);
+                twait16(x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) st[8 * h + i] = fma2(l1, st[8 * h + i], fma2(l2, st[8 * h + i], f2_of(x[2 * i], x[2 * i + 1])));
+            }
+            umma::fence_before();
+        };
         if (!STATES) {
             put_state();
-            umma::fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(sb + B_S);
         }
         bool ok = true;
+        int before = 0;  // (state pass) the length of the chunk before
         for (int c = 0; c < nc; ++c) {
             int t, L;
             chunk(c, t, L);
+            const uint32_t kt = sb + slot_of(c, KI) * TILE, vt = sb + slot_of(c, VI) * TILE;
             const bool upd = want_end || c + 1 < nc, use_s = c > 0 || has_start;
+            if (!STATES) {
+                ok = wwait(sb + B_QK, c & 1, flag, a.err);
+                if (!ok) break;
+                umma::fence_after();
+                const int dist = rev ? g4 - q4 : q4 - g4;  // blocks of 32 between this block's keys and its rows
+                // lambda^|r-s|: beyond the diagonal block a row's factor (distance to the block's near edge) times a column's
+                // (from there), both at most 1; in it the power of the distance
+                const float rowf = s_kv * ex2((float)(32 * dist + (rev ? -lane : lane - 31)) * lg);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t o[8];
+                    if (dist < 0) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) o[i] = 0;
+                    } else {
+                        uint32_t x[16];
+                        tld16(quad + T_QK + c0 + 16 * h, x);
+                        twait16(x);
+                        if (dist > 0) {
+                            const f2 rf = both(rowf);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint4 cf = umma::ld_shared_v4(sb + S_COL + 64 * h + 16 * i);
+                                o[2 * i] = narrow2<T>(mul2(mul2(f2_of(x[4 * i], x[4 * i + 1]), rf), f2_of(cf.x, cf.y)));
+                                o[2 * i + 1] = narrow2<T>(mul2(mul2(f2_of(x[4 * i + 2], x[4 * i + 3]), rf), f2_of(cf.z, cf.w)));
+                            }
+                        } else {
+                            const uint32_t dg = sb + S_DIAG + 4 * lane - 64 * h;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float f0 = lds_f(dg + 4 * (31 - 2 * i)), f1 = lds_f(dg + 4 * (30 - 2 * i));
+                                o[i] = Elt<T>::pack(f0 != 0.f ? __uint_as_float(x[2 * i]) * (s_kv * f0) : 0.f,
+                                                    f1 != 0.f ? __uint_as_float(x[2 * i + 1]) * (s_kv * f1) : 0.f);
+                            }
+                        }
+                        if (rev && L < LC) {  // (a short chunk's rows see no keys behind it)
+                            const int most = L - c0 - 16 * h;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o[i] = 2 * i + 1 < most ? o[i] : 2 * i < most ? o[i] & 0xffffu : 0u;
+                        }
+                    }
+                    // (columns of this block that it has read: the lower 16 of its 32)
+                    tst8(quad + T_QK + c0 + 8 * h, o);
+                }
+                tst_wait();
+                umma::fence_before();
+            }
+            if (L < LC || upd) {
+                ok = wwait(sb + B_FULL + 8 * slot_of(c, VI), phase_of(c, VI), flag, a.err) &&
+                     wwait(sb + B_FULL + 8 * slot_of(c, KI), phase_of(c, KI), flag, a.err);
+                if (!ok) break;
+            }
+            if (L < LC) {
+                // the rows behind a short chunk are another sequence's: what they hold must not meet even a zero
+                if (row >= L && row < (L + 15) / 16 * 16 && c0 < 64 * vblk)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) umma::st_shared_v4(vt + place(i), 0, 0, 0, 0);
+                umma::fence_async_smem();
+            }
+            if (!STATES) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sb + B_P);
+            }
+            if (upd) {
+                const uint32_t lo = sb + (STATES && (c & 1) ? S_ST : S_LO);
+                const float f = s_kv * ex2((float)(rev ? row + 1 : L - 1 - row) * lg);
+                const bool in = row < L;
+                if (c0 < 64 * kblk) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 u = umma::ld_shared_v4(kt + place(i));
+                        const uint32_t x[4] = {u.x, u.y, u.z, u.w};
+                        uint32_t h[4], l[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const f2 v = mul2(widen2<T>(x[e]), both(f));
+                            h[e] = narrow2<T>(v);
+                            l[e] = narrow2<T>(fma2(widen2<T>(h[e]), both(-1.f), v));
+                            if (!in) h[e] = l[e] = 0;
+                        }
+                        umma::st_shared_v4(kt + place(i), h[0], h[1], h[2], h[3]);
+                        umma::st_shared_v4(lo + place(i), l[0], l[1], l[2], l[3]);
+                    }
+                }
+                umma::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_of(B_K, c));
+            }
             if (!STATES) {
                 ok = wwait(sb + B_PV, c & 1, flag, a.err);
                 if (!ok) break;
-                umma::fence_after();
-                const float rf = use_s ? w.s_out * ex2((float)(rev ? L - 1 - row : row + 1) * lg) : 0.f;
-                const long long at = (((long long)t + row) * a.H + j) * vd;
+                if (c0 < vd) {
+                    umma::fence_after();
+                    const float rf = use_s ? w.s_out * ex2((float)(rev ? L - 1 - row : row + 1) * lg) : 0.f;
+                    const long long at = (((long long)t + row) * a.H + j) * vd + c0;
+                    const uint32_t qt = sb + slot_of(c, 0) * TILE;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int col = cg * 64 + i * 16;
-                    if (col >= vd) break;
-                    uint32_t x[16], y[16];
-                    tld16(tmem + quad + T_PV + col, x);
-                    if (use_s) tld16(tmem + quad + T_QS + col, y);
-                    twait16(x);
-                    if (use_s) twait16(y);
-                    f2 v[8];
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t x[16], y[16];
+                        tld16(quad + T_PV + c0 + 16 * h, x);
+                        if (use_s) tld16(quad + T_QS + c0 + 16 * h, y);
+                        twait16(x);
+                        if (use_s) twait16(y);
+                        f2 v[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        v[e] = mul2(f2_of(x[2 * e], x[2 * e + 1]), both(w.s_out));
-                        if (use_s) v[e] = fma2(f2_of(y[2 * e], y[2 * e + 1]), both(rf), v[e]);
-                    }
-                    if (row < L) {
+                        for (int e = 0; e < 8; ++e) {
+                            v[e] = mul2(f2_of(x[2 * e], x[2 * e + 1]), both(w.s_out));
+                            if (use_s) v[e] = fma2(f2_of(y[2 * e], y[2 * e + 1]), both(rf), v[e]);
+                        }
                         if (w.out_f32) {
-                            float *o = static_cast<float *>(w.out) + at + col;
+                            float *o = static_cast<float *>(w.out) + at + 16 * h;
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                if (col + 4 * e < vd) *reinterpret_cast<ulonglong2 *>(o + 4 * e) = make_ulonglong2(v[2 * e], v[2 * e + 1]);
+                                if (row < L && c0 + 16 * h + 4 * e < vd) *reinterpret_cast<ulonglong2 *>(o + 4 * e) = make_ulonglong2(v[2 * e], v[2 * e + 1]);
                         } else {
-                            T *o = static_cast<T *>(w.out) + at + col;
 #pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                if (col + 8 * e < vd)
-                                    *reinterpret_cast<uint4 *>(o + 8 * e) = make_uint4(narrow2<T>(v[4 * e]), narrow2<T>(v[4 * e + 1]),
-                                                                                      narrow2<T>(v[4 * e + 2]), narrow2<T>(v[4 * e + 3]));
+                            for (int e = 0; e < 2; ++e) {
+                                const uint32_t n[4] = {narrow2<T>(v[4 * e]), narrow2<T>(v[4 * e + 1]), narrow2<T>(v[4 * e + 2]), narrow2<T>(v[4 * e + 3])};
+                                if (L == LC)
+                                    umma::st_shared_v4(qt + place(2 * h + e), n[0], n[1], n[2], n[3]);
+                                else if (row < L && c0 + 16 * h + 8 * e < vd)
+                                    *reinterpret_cast<uint4 *>(static_cast<T *>(w.out) + at + 16 * h + 8 * e) = make_uint4(n[0], n[1], n[2], n[3]);
+                            }
                         }
                     }
+                    umma::fence_before();
+                    umma::fence_async_smem();
                 }
-                umma::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sb + B_O);
             }
-            if (upd) {
+            if (STATES) {
+                if (c > 0) {
+                    ok = wwait(bar_of(B_DS, c - 1), par_of(c - 1), flag, a.err);
+                    if (!ok) break;
+                    update(c - 1, before);
+                }
+                before = L;
+            } else if (upd) {
                 ok = wwait(bar_of(B_DS, c), par_of(c), flag, a.err);
                 if (!ok) break;
-                umma::fence_after();
-                const uint32_t d = tmem + quad + T_DS - (STATES && (c & 1) ? 128 : 0);
-                const f2 l1 = L == LC ? both(lam[0]) : both(ex2((float)L * lg)), l2 = L == LC ? both(lam[1]) : 0ull;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int col = cg * 64 + i * 16;
-                    if (col >= NV) break;
-                    uint32_t x[16];
-                    tld16(d + col, x);
-                    twait16(x);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        f2 &s = st[8 * i + e];
-                        s = fma2(l1, s, fma2(l2, s, f2_of(x[2 * e], x[2 * e + 1])));
-                    }
-                }
-                if (!STATES && c + 1 < nc) put_state();
-                umma::fence_before();
+                update(c, L);
+                if (c + 1 < nc) put_state();
             }
-            if (STATES || c + 1 < nc) {
+            if (!STATES && c + 1 < nc) {
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar_of(B_S, c));
+                if (lane == 0) mbar_arrive(sb + B_S);
             }
         }
+        if (STATES && ok && nc > 0) {
+            ok = wwait(bar_of(B_DS, nc - 1), par_of(nc - 1), flag, a.err);
+            if (ok) update(nc - 1, before);
+        }
         if (ok && want_end && live) {
-            if (STATES) {
-                float *e = w.states + ((long long)slot * a.H + j) * kStateFloats + row;
+            const long long n = STATES ? (long long)slot : (long long)seg.n;
+            float *e = STATES ? w.states + (n * a.H + j) * kStateFloats + row : w.end + (n * a.H + j) * kd * vd + (long long)row * w.rs;
+            const long long step = STATES ? LD : w.cs;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int col = cg * 64 + 2 * i;
-                    if (col < vd) unpack2(st[i], e[col * LD], e[(col + 1) * LD]);
-                }
-            } else {
-                float *e = w.end + ((long long)seg.n * a.H + j) * kd * vd + (long long)row * w.rs;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int col = cg * 64 + 2 * i;
-                    if (col < vd) unpack2(st[i], e[(long long)col * w.cs], e[(long long)(col + 1) * w.cs]);
-                }
+            for (int i = 0; i < 16; ++i) {
+                const int col = c0 + 2 * i;
+                if (col < vd) unpack2(st[i], e[col * step], e[(col + 1) * step]);
             }
         }
     }
     umma::fence_before();
     __syncthreads();
-    if (warp == 17) umma::dealloc(tmem, 512);
+    if (warp == NW + 1) umma::dealloc(tmem, 512);
 }
 
 template <typename T, bool STATES>
