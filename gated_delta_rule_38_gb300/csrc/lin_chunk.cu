@@ -12,13 +12,18 @@
 // backward.
 //
 // One CTA walks one segment of a sequence for one head; all tiles are 128 wide (narrower heads load zeros).
-//   warps 0..15   lanes 32 (w mod 4) .., columns 32 (w / 4) ..: the block of P from Q K^T (tensor memory to tensor memory,
-//                 where it is the left operand of P V), the decayed keys, the output rows, and the state, fp32 in
-//                 registers with a copy rounded to 16 bits in shared memory as the operand of Q S
-//   warp 16       tile loads (TMA) into a ring of five 32 KB tiles, and the output tiles' stores
-//   warp 17       the MMAs
-// The sixteen warps pass through these steps together: four roles of four warps each needed more registers than a thread
-// can have beside them, and what they spilled went to L2 (B = 1, T = 2048, 152 heads: 156 us, STEPS us so).
+//   warps 0..7    the state: lanes 32 (w mod 4) .., 64 of the 128 columns; fp32 in registers, with a copy rounded to 16 bits
+//                 in shared memory as the operand of Q S; and the output rows
+//   warps 8..11   lanes 32 (w mod 4) ..
+//   all twelve    P from Q K^T (tensor memory to tensor memory, where it is the left operand of P V), in blocks of 32 x 32:
+//                 warps 8..11 those on the diagonal, the others those beyond it; then the decayed keys
+//   warp 12       tile loads (TMA) into a ring of five 32 KB tiles, and the output tiles' stores
+//   warp 13       the MMAs:  Q S, P V, the state's update, Q K^T of the next chunk
+// The chain of a chunk: the update, the state's copy and the next Q S on one side, the next Q K^T and P on the other, then
+// P V, and the next update; output rows and keys are made beside it.
+// Fourteen warps leave a thread 128 registers; with eighteen and 96 the state's threads spilled, and what they spilled went
+// to L2.  Loops that can stay loops do: unrolled, a chunk's code no longer fitted the instruction caches next to the
+// schedulers.  (B = 1, T = 2048, 152 heads: 156 us with spills, 72 with sixteen warps through all steps together, @US@ so.)
 // A decayed key is two 16-bit numbers, the rounded one and the remainder's, each with a product of its own: their sum is
 // as good as keys of 16 bits of mantissa, because the states are handed on in fp32 (rounded once they would be off by
 // 1e-3; so they are by 3e-6).
@@ -38,7 +43,8 @@ namespace gdr {
 namespace lin {
 namespace {
 
-constexpr int NW = 16, NT = 32 * (NW + 2);        // working warps; threads
+constexpr int NS = 8, NK = 4, NT = 32 * (NS + NK + 2);  // warps of the state and of the keys; threads
+constexpr int CW = LD / (NS / 4);                       // columns of a state warp
 constexpr uint32_t TILE = 32768, BLK = 16384;     // a tile: two blocks of 64 columns, 128 rows each
 constexpr int RING = 5;
 constexpr uint32_t S_LO = RING * TILE;            // the keys' remainders
@@ -47,8 +53,8 @@ constexpr uint32_t S_BAR = S_ST + TILE;
 constexpr uint32_t B_FULL = S_BAR, B_EMPTY = S_BAR + 8 * RING, B_QK = B_EMPTY + 8 * RING, B_S = B_QK + 8, B_P = B_S + 8,
                    B_O = B_P + 8, B_PV = B_O + 8, B_K = B_PV + 8, B_DS = B_K + 16, B_DONE = B_DS + 16, S_SLOT = B_DONE + 8, S_FLAG = S_SLOT + 4;
 constexpr uint32_t S_LAM = S_FLAG + 8;            // lambda^128 as two fp32 numbers
-// decays of up to 31 tokens: COL[c] = lambda^(31-c) (rev: lambda^c); DIAG[31 + row - key] = lambda^|row - key| where the row
-// sees the key, else 0
+// decays of up to 31 tokens: COL[c] = lambda^(31-c) (rev: lambda^c); DIAG[31 + row - key] = s_kv lambda^|row - key| where
+// the row sees the key, else 0
 constexpr uint32_t S_COL = (S_LAM + 8 + 15) / 16 * 16, S_DIAG = S_COL + 128;
 constexpr uint32_t S_BYTES = S_DIAG + 256 + 1024;
 static_assert(S_BYTES <= kSmemMost, "shared memory");
@@ -106,7 +112,26 @@ __device__ __forceinline__ bool wwait(uint32_t bar, uint32_t parity, uint32_t fl
 
 // ---------------------------------------------------------------- tensor memory
 
-// 32 lanes x 16 columns; the wait names the registers, so that nothing that uses them moves above it.
+// 32 lanes x 32 columns; the wait names the registers, so that nothing that uses them moves above it.
+__device__ __forceinline__ void tld32(uint32_t a, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(a));
+}
+__device__ __forceinline__ void twait16(uint32_t *r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+__device__ __forceinline__ void twait32(uint32_t *r) {
+    twait16(r);
+    twait16(r + 16);
+}
 __device__ __forceinline__ void tld16(uint32_t a, uint32_t *r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
@@ -114,15 +139,17 @@ __device__ __forceinline__ void tld16(uint32_t a, uint32_t *r) {
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(a));
 }
-__device__ __forceinline__ void twait16(uint32_t *r) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
-}
 __device__ __forceinline__ void tst8(uint32_t a, const uint32_t *r) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(a), "r"(r[0]), "r"(r[1]),
                  "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
+}
+__device__ __forceinline__ void tst16(uint32_t a, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(a),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
 }
 __device__ __forceinline__ void tst_wait() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 // D (+)= A B, issued by the lane that has `on`; the whole warp computes the operands, which so stay uniform.  (In a branch
@@ -263,13 +290,13 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
             umma::mbar_init(sb + B_FULL + 8 * i, 1);
             umma::mbar_init(sb + B_EMPTY + 8 * i, 1);
         }
-        umma::mbar_init(sb + B_QK, 1);
+        umma::mbar_init(sb + B_QK, 2);
         umma::mbar_init(sb + B_PV, 1);
-        umma::mbar_init(sb + B_S, NW);
-        umma::mbar_init(sb + B_P, NW);
-        umma::mbar_init(sb + B_O, NW);
+        umma::mbar_init(sb + B_P, NS + NK);
+        umma::mbar_init(sb + B_O, NS);
+        umma::mbar_init(sb + B_S, NS);
         for (int i = 0; i < 2; ++i) {
-            umma::mbar_init(sb + B_K + 8 * i, NW);
+            umma::mbar_init(sb + B_K + 8 * i, NS + NK);
             umma::mbar_init(sb + B_DS + 8 * i, 1);
         }
         umma::mbar_init(sb + B_DONE, 1);
@@ -284,9 +311,9 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
     if (tid >= 64 && tid < 96) reinterpret_cast<float *>(smem + S_COL)[lane] = ex2((float)(rev ? lane : 31 - lane) * lg);
     if (tid >= 96 && tid < 160) {
         const int d = rev ? 31 - (tid - 96) : tid - 96 - 31;
-        reinterpret_cast<float *>(smem + S_DIAG)[tid - 96] = d >= 0 ? ex2((float)d * lg) : 0.f;
+        reinterpret_cast<float *>(smem + S_DIAG)[tid - 96] = d >= 0 ? w.s_kv * ex2((float)d * lg) : 0.f;
     }
-    if (warp == NW + 1) umma::alloc(sb + S_SLOT, 512);
+    if (warp == NS + NK + 1) umma::alloc(sb + S_SLOT, 512);
     umma::fence_before();
     __syncthreads();
     umma::fence_after();
@@ -307,9 +334,44 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
     const int ksteps = (kd + 15) / 16, kblk = kd > 64 ? 2 : 1, vblk = vd > 64 ? 2 : 1;
     const int NV = (vd + 15) / 16 * 16;
 
+    // The decayed keys of chunk c, eights i0 .. i1 of the columns of row 32 (warp mod 4) + lane; the rounded ones in place of k.
+    auto make_keys = [&](int c, int L, int i0, int i1) {
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t kt = sb + slot_of(c, KI) * TILE, lo = sb + (STATES && (c & 1) ? S_ST : S_LO);
+        const float f = w.s_kv * ex2((float)(rev ? row + 1 : L - 1 - row) * lg);
+        const bool in = row < L;
+#pragma unroll 1
+        for (int i = i0; i < i1; i += 2) {
+            uint4 u[2];
+            uint32_t at[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                at[k] = (uint32_t)(i >> 3) * BLK + row * 128 + (((uint32_t)((i & 7) + k) ^ (row & 7)) << 4);
+                u[k] = umma::ld_shared_v4(kt + at[k]);
+                if (!in) u[k] = make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t x[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+                uint32_t h[4], l[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const f2 v = mul2(widen2<T>(x[e]), both(f));
+                    h[e] = narrow2<T>(v);
+                    l[e] = narrow2<T>(fma2(widen2<T>(h[e]), both(-1.f), v));
+                }
+                umma::st_shared_v4(kt + at[k], h[0], h[1], h[2], h[3]);
+                umma::st_shared_v4(lo + at[k], l[0], l[1], l[2], l[3]);
+            }
+        }
+        umma::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_of(B_K, c));
+    };
+
     // full chunks' 16-bit output rows leave through the q tile as a TMA store
     const bool staged = !STATES && !w.out_f32;
-    if (warp == NW) {
+    if (warp == NS + NK) {
         // ------------------------------------------------------------ tile loads, output stores
         const int hq = j / w.q_div, hk = j / w.k_div, hv = j / w.v_div;
         int issued = 0;
@@ -325,28 +387,31 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
             }
             __syncwarp();
         };
-        for (int c = 0; c < nc && ok; ++c) {
+        // a chunk's tile into its place of the ring
+        auto tile = [&](int c, int i) {
             int t, L;
             chunk(c, t, L);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int x = PER * c + i, sl = x % RING;
-                const CUtensorMap *m = i == VI ? &w.tv : i == KI ? &w.tk : &w.tq;
-                const int h = i == VI ? hv : i == KI ? hk : hq, nb = i == VI ? vblk : kblk;
+            const CUtensorMap *m = i == VI ? &w.tv : i == KI ? &w.tk : &w.tq;
+            const int h = i == VI ? hv : i == KI ? hk : hq, nb = i == VI ? vblk : kblk;
+            if (lane == 0) {
+                const uint32_t dst = sb + slot_of(c, i) * TILE, bar = sb + B_FULL + 8 * slot_of(c, i);
+                tma::expect_tx(bar, nb * BLK);
+#pragma unroll 1
+                for (int b = 0; b < nb; ++b) tma::load3d(dst + b * BLK, m, 64 * b, h, t, bar);
+            }
+            __syncwarp();
+        };
+        for (int c = 0; c < nc && ok; ++c) {
+#pragma unroll 1
+            for (int i = 0; i < PER && ok; ++i) {
+                const int x = PER * c + i;
                 if (x >= RING) {
-                    if (lane == 0)
-                        for (int b = 0; b < nb; ++b) tma::prefetch3d(m, 64 * b, h, t);
+                    ok = ok && wwait(sb + B_EMPTY + 8 * (x % RING), ((x / RING) - 1) & 1, flag, a.err);
                     if (!STATES && (x - RING) % PER == 0) store((x - RING) / PER);
-                    else ok = ok && wwait(sb + B_EMPTY + 8 * sl, ((x / RING) - 1) & 1, flag, a.err);
                 }
                 if (!ok) break;
-                if (lane == 0) {
-                    const uint32_t dst = sb + sl * TILE, bar = sb + B_FULL + 8 * sl;
-                    tma::expect_tx(bar, nb * BLK);
-                    for (int b = 0; b < nb; ++b) tma::load3d(dst + b * BLK, m, 64 * b, h, t, bar);
-                }
+                tile(c, i);
                 ++issued;
-                __syncwarp();
             }
         }
         if (!STATES && ok)  // the q tiles that nothing was loaded into since
@@ -356,104 +421,180 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
             for (int x = max(0, issued - RING); x < issued; ++x)
                 umma::mbar_spin(sb + B_FULL + 8 * (x % RING), (x / RING) & 1, 4000000L);
         }
-    } else if (warp == NW + 1) {
+    } else if (warp == NS + NK + 1) {
         // ------------------------------------------------------------ MMAs
         constexpr bool bf = IsBf16<T>::value;
         const uint32_t i_qk = umma::idesc(128, 128, bf, false, false), i_qs = umma::idesc(128, NV, bf, false, true),
                        i_ds = umma::idesc(128, NV, bf, true, true);
         const uint32_t on = lane == 0;
         bool ok = true;
-        for (int c = 0; c < nc; ++c) {
+        auto full = [&](int c, int which) { return wwait(sb + B_FULL + 8 * slot_of(c, which), phase_of(c, which), flag, a.err); };
+        auto wait_qk = [&](int c) {
+            ok = ok && full(c, 0) && full(c, KI);
+            // (P of the chunk before has been read: Q K^T takes its place)
+            if (c > 0) ok = ok && wwait(sb + B_PV, (c - 1) & 1, flag, a.err);
+            umma::fence_after();
+        };
+        auto issue_qk = [&](int c) {
+            const uint64_t dq = umma::desc(sb + slot_of(c, 0) * TILE, 16, 1024), dk = umma::desc(sb + slot_of(c, KI) * TILE, 16, 1024);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+                const uint32_t o = (uint32_t)(ks >> 2) * BLK + (uint32_t)(ks & 3) * 32u;
+                if (ks < ksteps) mma_ss(on, tmem + T_QK, desc_at(dq, o), desc_at(dk, o), i_qk, ks > 0);
+            }
+            commit_on(on, sb + B_QK);
+            if (lane == 0) mbar_arrive(sb + B_QK);  // (hands on that q and k have landed)
+        };
+        // one of the two products of chunk c's state update: with the keys or with their remainders
+        auto issue_ds = [&](int c, uint32_t keys, int ts, bool more) {
+            const uint32_t d = tmem + T_DS - (STATES && (c & 1) ? 128 : 0);
+            const uint64_t dv = umma::desc(sb + slot_of(c, VI) * TILE, BLK, 1024), dk = umma::desc(keys, BLK, 1024);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+                if (ks < ts) mma_ss(on, d, desc_at(dk, ks * 2048u), desc_at(dv, ks * 2048u), i_ds, more || ks > 0);
+        };
+        if (!STATES && nc > 0) {
+            wait_qk(0);
+            if (ok) issue_qk(0);
+        }
+        for (int c = 0; c < nc && ok; ++c) {
             int t, L;
             chunk(c, t, L);
             const int ts = (L + 15) / 16;
-            const uint32_t kt = sb + slot_of(c, KI) * TILE, vt = sb + slot_of(c, VI) * TILE;
+            const uint32_t kt = sb + slot_of(c, KI) * TILE, lo = sb + (STATES && (c & 1) ? S_ST : S_LO);
             const bool upd = want_end || c + 1 < nc, use_s = c > 0 || has_start;
             if (!STATES) {
-                const uint32_t qt = sb + slot_of(c, 0) * TILE;
-                ok = ok && wwait(sb + B_FULL + 8 * slot_of(c, 0), phase_of(c, 0), flag, a.err);
-                ok = ok && wwait(sb + B_FULL + 8 * slot_of(c, KI), phase_of(c, KI), flag, a.err);
-                // (P of the chunk before has been read: Q K^T takes its place)
-                if (c > 0) ok = ok && wwait(sb + B_PV, (c - 1) & 1, flag, a.err);
-                if (!ok) break;
-                umma::fence_after();
-                const uint64_t dq = umma::desc(qt, 16, 1024), dk = umma::desc(kt, 16, 1024);
-                {
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks) {
-                        const uint32_t o = (uint32_t)(ks >> 2) * BLK + (uint32_t)(ks & 3) * 32u;
-                        if (ks < ksteps) mma_ss(on, tmem + T_QK, desc_at(dq, o), desc_at(dk, o), i_qk, ks > 0);
-                    }
-                    commit_on(on, sb + B_QK);
-                }
                 // the state's copy is there, and the accumulators of the chunk before have been read
                 ok = ok && wwait(sb + B_S, c & 1, flag, a.err);
                 if (!ok) break;
                 umma::fence_after();
                 if (use_s) {
-                    const uint64_t ds = umma::desc(sb + S_ST, BLK, 1024);
+                    const uint64_t dq = umma::desc(sb + slot_of(c, 0) * TILE, 16, 1024), ds = umma::desc(sb + S_ST, BLK, 1024);
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks) {
                         const uint32_t o = (uint32_t)(ks >> 2) * BLK + (uint32_t)(ks & 3) * 32u;
                         if (ks < ksteps) mma_ss(on, tmem + T_QS, desc_at(dq, o), desc_at(ds, ks * 2048u), i_qs, ks > 0);
                     }
                 }
-                ok = ok && wwait(sb + B_P, c & 1, flag, a.err);
-                ok = ok && wwait(sb + B_FULL + 8 * slot_of(c, VI), phase_of(c, VI), flag, a.err);
+                ok = ok && wwait(sb + B_P, c & 1, flag, a.err) && full(c, VI);
                 if (!ok) break;
                 umma::fence_after();
-                {
-                    const uint64_t dv = umma::desc(vt, BLK, 1024);
+                const uint64_t dv = umma::desc(sb + slot_of(c, VI) * TILE, BLK, 1024);
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        if (ks < ts) mma_ts(on, tmem + T_PV, tmem + T_QK + 32 * (ks >> 1) + 8 * (ks & 1), desc_at(dv, ks * 2048u), i_qs, ks > 0);
-                    commit_on(on, sb + B_PV);
-                }
+                for (int ks = 0; ks < 8; ++ks)
+                    if (ks < ts) mma_ts(on, tmem + T_PV, tmem + T_QK + 32 * (ks >> 1) + 8 * (ks & 1), desc_at(dv, ks * 2048u), i_qs, ks > 0);
+                commit_on(on, sb + B_PV);
+                // (q has been read; every use of a place is one phase of its barrier, though the output's store waits longer)
+                commit_on(on, sb + B_EMPTY + 8 * slot_of(c, 0));
             } else {
-                ok = ok && wwait(sb + B_FULL + 8 * slot_of(c, VI), phase_of(c, VI), flag, a.err);
+                ok = ok && full(c, VI);
             }
             if (upd) {
-                // (state pass: the keys of chunk c come after the state has taken the accumulator of chunk c - 2)
                 ok = ok && wwait(bar_of(B_K, c), par_of(c), flag, a.err);
+                // (state pass: its accumulator was read, two chunks before, ahead of these keys)
                 if (!ok) break;
                 umma::fence_after();
-                {
-                    const uint32_t lo = sb + (STATES && (c & 1) ? S_ST : S_LO), d = tmem + T_DS - (STATES && (c & 1) ? 128 : 0);
-                    const uint64_t dv = umma::desc(vt, BLK, 1024), dh = umma::desc(kt, BLK, 1024), dl = umma::desc(lo, BLK, 1024);
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        if (ks < ts) mma_ss(on, d, desc_at(dh, ks * 2048u), desc_at(dv, ks * 2048u), i_ds, ks > 0);
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        if (ks < ts) mma_ss(on, d, desc_at(dl, ks * 2048u), desc_at(dv, ks * 2048u), i_ds, true);
-                    commit_on(on, bar_of(B_DS, c));
-                }
+                issue_ds(c, kt, ts, false);
+                if (!STATES && c + 1 < nc) wait_qk(c + 1);
+                if (!ok) break;
+                issue_ds(c, lo, ts, true);
+                commit_on(on, bar_of(B_DS, c));
             }
             if (!ok) break;
-            {  // (a q tile's too, so that every use of a place is one phase: the output's store waits longer)
-#pragma unroll
-                for (int i = 0; i < PER; ++i) commit_on(on, sb + B_EMPTY + 8 * slot_of(c, i));
-            }
+            commit_on(on, sb + B_EMPTY + 8 * slot_of(c, KI));
+            commit_on(on, sb + B_EMPTY + 8 * slot_of(c, VI));
+            // (runs while the state is updated)
+            if (!STATES && c + 1 < nc) issue_qk(c + 1);
         }
         // every MMA, and every arrival that waits for one, has happened before shared memory goes away
         commit_on(on, sb + B_DONE);
         umma::mbar_spin(sb + B_DONE, 0, 4000000L);
-    } else {
-        // ------------------------------------------------------------ P, keys, output rows, state
-        const int q4 = warp & 3, g4 = warp >> 2, row = q4 * 32 + lane, c0 = g4 * 32;
-        const uint32_t quad = tmem + ((uint32_t)(q4 * 32) << 16);
-        const float s_kv = w.s_kv;
-        const uint32_t tile_row = (uint32_t)(c0 >> 6) * BLK + row * 128;  // this thread's 32 columns of a tile: four places
-        auto place = [&](int i) { return tile_row + ((((uint32_t)(c0 & 63) / 8 + i) ^ (row & 7)) << 4); };
-        const bool live = row < kd;
-        f2 st[16];
+    } else if (warp >= NS) {
+        // ------------------------------------------------------------ P, and the decayed keys
+        const int q4 = warp & 3, row = q4 * 32 + lane;
+        const uint32_t quad = tmem + ((uint32_t)(q4 * 32) << 16), swz = row & 7;
+        // the i-th eight columns of this thread's row in a tile
+        auto place = [&](int i) { return (uint32_t)(i >> 3) * BLK + row * 128 + (((uint32_t)(i & 7) ^ swz) << 4); };
+        // zeros behind the last row of chunk c's v, as far as the MMAs read
+        auto clear_v = [&](int c, int L) {
+            if (!wwait(sb + B_FULL + 8 * slot_of(c, VI), phase_of(c, VI), flag, a.err)) return false;
+            if (row >= L && row < (L + 15) / 16 * 16)
+#pragma unroll 1
+                for (int i = 0; i < 8 * vblk; ++i) umma::st_shared_v4(sb + slot_of(c, VI) * TILE + place(i), 0, 0, 0, 0);
+            __syncwarp();
+            return true;
+        };
+        // The blocks of P on the diagonal and those that see nothing.
+        auto make_p = [&](int c, int L) {
+            if (!wwait(sb + B_QK, c & 1, flag, a.err)) return false;
+            umma::fence_after();
+            uint32_t o[16], x[32];
+            float f[32];
+            tld32(quad + T_QK + 32 * q4, x);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) st[i] = 0ull;
+            for (int i = 0; i < 32; ++i) f[i] = reinterpret_cast<const float *>(smem + S_DIAG)[31 + lane - i];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = 0;
+#pragma unroll 1
+            for (int blk = rev ? 0 : q4 + 1; blk < (rev ? q4 : 4); ++blk) tst16(quad + T_QK + 32 * blk, o);
+            twait32(x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                o[i] = Elt<T>::pack(f[2 * i] != 0.f ? __uint_as_float(x[2 * i]) * f[2 * i] : 0.f,
+                                    f[2 * i + 1] != 0.f ? __uint_as_float(x[2 * i + 1]) * f[2 * i + 1] : 0.f);
+            if (rev && L < LC) {  // (a short chunk's rows see no keys behind it)
+                const int most = L - 32 * q4;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = 2 * i + 1 < most ? o[i] : 2 * i < most ? o[i] & 0xffffu : 0u;
+            }
+            tst16(quad + T_QK + 32 * q4, o);
+            if (L < LC) {
+                // the rows behind a short chunk are another sequence's: what they hold must not meet even a zero
+                if (!clear_v(c, L)) return false;
+                umma::fence_async_smem();
+            }
+            tst_wait();
+            umma::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sb + B_P);
+            return true;
+        };
+        bool ok = true;
+        for (int c = 0; c < nc && ok; ++c) {
+            int t, L;
+            chunk(c, t, L);
+            if (!STATES) {
+                ok = make_p(c, L);
+                // (the remainders' place: read by the update of the chunk before)
+                if (want_end || c + 1 < nc) {
+                    if (c > 0) ok = ok && wwait(sb + B_DS, (c - 1) & 1, flag, a.err);
+                    if (ok) make_keys(c, L, 12, min(16, 8 * kblk));
+                }
+                continue;
+            }
+            // (half of the keys' columns, the state warps the others; the remainders' place was read two chunks before)
+            ok = wwait(sb + B_FULL + 8 * slot_of(c, VI), phase_of(c, VI), flag, a.err) &&
+                 wwait(sb + B_FULL + 8 * slot_of(c, KI), phase_of(c, KI), flag, a.err);
+            if (ok && L < LC) clear_v(c, L);
+            if (c >= 2) ok = ok && wwait(bar_of(B_DS, c), par_of(c - 2), flag, a.err);
+            if (ok) make_keys(c, L, 0, 8);
+        }
+    } else {
+        // ------------------------------------------------------------ the state and the output rows
+        const int q4 = warp & 3, row = q4 * 32 + lane, c0 = (warp >> 2) * CW;
+        const uint32_t quad = tmem + ((uint32_t)(q4 * 32) << 16);
+        const uint32_t tile_row = (uint32_t)(c0 >> 6) * BLK + row * 128, swz = row & 7;
+        // the i-th eight of this thread's columns in a tile
+        auto place = [&](int i) { return tile_row + (((uint32_t)((c0 & 63) / 8 + i) ^ swz) << 4); };
+        const bool live = row < kd;
+        f2 st[CW / 2];
+#pragma unroll
+        for (int i = 0; i < CW / 2; ++i) st[i] = 0ull;
         if (!STATES && has_start) {
             if (w.start) {
                 const float *s0 = w.start + ((long long)seg.n * a.H + j) * kd * vd + (long long)row * w.rs;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                for (int i = 0; i < CW / 2; ++i) {
                     const int col = c0 + 2 * i;
                     if (live && col < vd) st[i] = pack2(s0[(long long)col * w.cs], s0[(long long)(col + 1) * w.cs]);
                 }
@@ -470,7 +611,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                     const float *e = w.ext + (wc.place(seg, from) * a.H + j) * kStateFloats + (long long)row * w.ers;
                     const f2 d = both(ex2((float)(rev ? at - from : pos - at) * lg));
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < CW / 2; ++i) {
                         const int col = c0 + 2 * i;
                         if (live && col < vd) st[i] = fma2(d, st[i], pack2(e[(long long)col * w.ecs], e[(long long)(col + 1) * w.ecs]));
                     }
@@ -480,128 +621,98 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
         auto put_state = [&]() {
             if (c0 < NV) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < CW / 8; ++i)
                     umma::st_shared_v4(sb + S_ST + place(i), narrow2<T>(st[4 * i]), narrow2<T>(st[4 * i + 1]),
                                        narrow2<T>(st[4 * i + 2]), narrow2<T>(st[4 * i + 3]));
             }
-            umma::fence_async_smem();
         };
         // the state after chunk c
         auto update = [&](int c, int L) {
             if (c0 >= NV) return;
             umma::fence_after();
             const f2 l1 = both(L == LC ? lds_f(sb + S_LAM) : ex2((float)L * lg)), l2 = both(L == LC ? lds_f(sb + S_LAM + 4) : 0.f);
+            const uint32_t at = quad + T_DS - (STATES && (c & 1) ? 128 : 0) + c0;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t x[16];
-                tld16(quad + T_DS - (STATES && (c & 1) ? 128 : 0) + c0 + 16 * h, x);
-                twait16(x);
+            for (int h = 0; h < CW / 32; ++h) {
+                uint32_t x[32];
+                tld32(at + 32 * h, x);
+                twait32(x);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) st[8 * h + i] = fma2(l1, st[8 * h + i], fma2(l2, st[8 * h + i], f2_of(x[2 * i], x[2 * i + 1])));
+                for (int i = 0; i < 16; ++i) {
+                    f2 &v = st[16 * h + i];
+                    v = fma2(l1, v, fma2(l2, v, f2_of(x[2 * i], x[2 * i + 1])));
+                }
             }
             umma::fence_before();
         };
+        // The blocks of P beyond the diagonal, each lambda^|r-s| as a row's factor (distance to the block's near edge) times a
+        // column's (from there), both at most 1: warps 4..7 the nearest, 0..3 the others.
+        auto make_p = [&](int c, int L) {
+            if (!wwait(sb + B_QK, c & 1, flag, a.err)) return false;
+            umma::fence_after();
+            const int d0 = c0 ? 1 : 2, d1 = c0 ? 1 : 3;
+#pragma unroll 1
+            for (int h = 0; h < 2 * (d1 - d0 + 1); ++h) {
+                const int dist = d0 + (h >> 1), blk = rev ? q4 + dist : q4 - dist;
+                if (blk < 0 || blk > 3) break;
+                const uint32_t at = quad + T_QK + 32 * blk;
+                const f2 rf = both(w.s_kv * ex2((float)(32 * dist + (rev ? -lane : lane - 31)) * lg));
+                uint32_t x[16], o[8];
+                float4 f[4];
+                tld16(at + 16 * (h & 1), x);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f[i] = reinterpret_cast<const float4 *>(smem + S_COL)[4 * (h & 1) + i];
+                twait16(x);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    o[2 * i] = narrow2<T>(mul2(mul2(f2_of(x[4 * i], x[4 * i + 1]), rf), pack2(f[i].x, f[i].y)));
+                    o[2 * i + 1] = narrow2<T>(mul2(mul2(f2_of(x[4 * i + 2], x[4 * i + 3]), rf), pack2(f[i].z, f[i].w)));
+                }
+                if (rev && L < LC) {
+                    const int most = L - 32 * blk - 16 * (h & 1);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] = 2 * i + 1 < most ? o[i] : 2 * i < most ? o[i] & 0xffffu : 0u;
+                }
+                // (columns of this block that it has read: the lower 16 of its 32)
+                tst8(at + 8 * (h & 1), o);
+            }
+            tst_wait();
+            umma::fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sb + B_P);
+            return true;
+        };
+        // this warp's share of the keys: a quarter of the columns (state pass), or three eighths
+        const int k0 = STATES ? 8 + c0 / 16 : c0 / 64 * 6, k1 = min(k0 + (STATES ? 4 : 6), 8 * kblk);
+        bool ok = true;
         if (!STATES) {
             put_state();
+            umma::fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(sb + B_S);
+            if (nc > 0) {
+                int t, L;
+                chunk(0, t, L);
+                ok = make_p(0, L);
+                if (ok && (want_end || nc > 1)) make_keys(0, L, k0, k1);
+            }
         }
-        bool ok = true;
         int before = 0;  // (state pass) the length of the chunk before
-        for (int c = 0; c < nc; ++c) {
+        for (int c = 0; c < nc && ok; ++c) {
             int t, L;
             chunk(c, t, L);
-            const uint32_t kt = sb + slot_of(c, KI) * TILE, vt = sb + slot_of(c, VI) * TILE;
             const bool upd = want_end || c + 1 < nc, use_s = c > 0 || has_start;
-            if (!STATES) {
-                ok = wwait(sb + B_QK, c & 1, flag, a.err);
+            if (STATES) {
+                ok = wwait(sb + B_FULL + 8 * slot_of(c, KI), phase_of(c, KI), flag, a.err);
                 if (!ok) break;
-                umma::fence_after();
-                const int dist = rev ? g4 - q4 : q4 - g4;  // blocks of 32 between this block's keys and its rows
-                // lambda^|r-s|: beyond the diagonal block a row's factor (distance to the block's near edge) times a column's
-                // (from there), both at most 1; in it the power of the distance
-                const float rowf = s_kv * ex2((float)(32 * dist + (rev ? -lane : lane - 31)) * lg);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t o[8];
-                    if (dist < 0) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) o[i] = 0;
-                    } else {
-                        uint32_t x[16];
-                        tld16(quad + T_QK + c0 + 16 * h, x);
-                        twait16(x);
-                        if (dist > 0) {
-                            const f2 rf = both(rowf);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint4 cf = umma::ld_shared_v4(sb + S_COL + 64 * h + 16 * i);
-                                o[2 * i] = narrow2<T>(mul2(mul2(f2_of(x[4 * i], x[4 * i + 1]), rf), f2_of(cf.x, cf.y)));
-                                o[2 * i + 1] = narrow2<T>(mul2(mul2(f2_of(x[4 * i + 2], x[4 * i + 3]), rf), f2_of(cf.z, cf.w)));
-                            }
-                        } else {
-                            const uint32_t dg = sb + S_DIAG + 4 * lane - 64 * h;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float f0 = lds_f(dg + 4 * (31 - 2 * i)), f1 = lds_f(dg + 4 * (30 - 2 * i));
-                                o[i] = Elt<T>::pack(f0 != 0.f ? __uint_as_float(x[2 * i]) * (s_kv * f0) : 0.f,
-                                                    f1 != 0.f ? __uint_as_float(x[2 * i + 1]) * (s_kv * f1) : 0.f);
-                            }
-                        }
-                        if (rev && L < LC) {  // (a short chunk's rows see no keys behind it)
-                            const int most = L - c0 - 16 * h;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) o[i] = 2 * i + 1 < most ? o[i] : 2 * i < most ? o[i] & 0xffffu : 0u;
-                        }
-                    }
-                    // (columns of this block that it has read: the lower 16 of its 32)
-                    tst8(quad + T_QK + c0 + 8 * h, o);
+                make_keys(c, L, k0, k1);
+                if (c > 0) {
+                    ok = wwait(bar_of(B_DS, c - 1), par_of(c - 1), flag, a.err);
+                    if (!ok) break;
+                    update(c - 1, before);
                 }
-                tst_wait();
-                umma::fence_before();
-            }
-            if (L < LC || upd) {
-                ok = wwait(sb + B_FULL + 8 * slot_of(c, VI), phase_of(c, VI), flag, a.err) &&
-                     wwait(sb + B_FULL + 8 * slot_of(c, KI), phase_of(c, KI), flag, a.err);
-                if (!ok) break;
-            }
-            if (L < LC) {
-                // the rows behind a short chunk are another sequence's: what they hold must not meet even a zero
-                if (row >= L && row < (L + 15) / 16 * 16 && c0 < 64 * vblk)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) umma::st_shared_v4(vt + place(i), 0, 0, 0, 0);
-                umma::fence_async_smem();
-            }
-            if (!STATES) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sb + B_P);
-            }
-            if (upd) {
-                const uint32_t lo = sb + (STATES && (c & 1) ? S_ST : S_LO);
-                const float f = s_kv * ex2((float)(rev ? row + 1 : L - 1 - row) * lg);
-                const bool in = row < L;
-                if (c0 < 64 * kblk) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint4 u = umma::ld_shared_v4(kt + place(i));
-                        const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-                        uint32_t h[4], l[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const f2 v = mul2(widen2<T>(x[e]), both(f));
-                            h[e] = narrow2<T>(v);
-                            l[e] = narrow2<T>(fma2(widen2<T>(h[e]), both(-1.f), v));
-                            if (!in) h[e] = l[e] = 0;
-                        }
-                        umma::st_shared_v4(kt + place(i), h[0], h[1], h[2], h[3]);
-                        umma::st_shared_v4(lo + place(i), l[0], l[1], l[2], l[3]);
-                    }
-                }
-                umma::fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_of(B_K, c));
-            }
-            if (!STATES) {
+                before = L;
+            } else {
                 ok = wwait(sb + B_PV, c & 1, flag, a.err);
                 if (!ok) break;
                 if (c0 < vd) {
@@ -609,32 +720,32 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                     const float rf = use_s ? w.s_out * ex2((float)(rev ? L - 1 - row : row + 1) * lg) : 0.f;
                     const long long at = (((long long)t + row) * a.H + j) * vd + c0;
                     const uint32_t qt = sb + slot_of(c, 0) * TILE;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+#pragma unroll 1
+                    for (int h = 0; h < CW / 16; ++h) {
                         uint32_t x[16], y[16];
                         tld16(quad + T_PV + c0 + 16 * h, x);
                         if (use_s) tld16(quad + T_QS + c0 + 16 * h, y);
                         twait16(x);
-                        if (use_s) twait16(y);
                         f2 v[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            v[e] = mul2(f2_of(x[2 * e], x[2 * e + 1]), both(w.s_out));
-                            if (use_s) v[e] = fma2(f2_of(y[2 * e], y[2 * e + 1]), both(rf), v[e]);
+                        for (int e = 0; e < 8; ++e) v[e] = mul2(f2_of(x[2 * e], x[2 * e + 1]), both(w.s_out));
+                        if (use_s) {
+                            twait16(y);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) v[e] = fma2(f2_of(y[2 * e], y[2 * e + 1]), both(rf), v[e]);
                         }
-                        if (w.out_f32) {
-                            float *o = static_cast<float *>(w.out) + at + 16 * h;
+                        if (staged && L == LC) {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (row < L && c0 + 16 * h + 4 * e < vd) *reinterpret_cast<ulonglong2 *>(o + 4 * e) = make_ulonglong2(v[2 * e], v[2 * e + 1]);
-                        } else {
+                            for (int e = 0; e < 2; ++e)
+                                umma::st_shared_v4(qt + place(2 * h + e), narrow2<T>(v[4 * e]), narrow2<T>(v[4 * e + 1]), narrow2<T>(v[4 * e + 2]), narrow2<T>(v[4 * e + 3]));
+                        } else if (row < L) {
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const uint32_t n[4] = {narrow2<T>(v[4 * e]), narrow2<T>(v[4 * e + 1]), narrow2<T>(v[4 * e + 2]), narrow2<T>(v[4 * e + 3])};
-                                if (L == LC)
-                                    umma::st_shared_v4(qt + place(2 * h + e), n[0], n[1], n[2], n[3]);
-                                else if (row < L && c0 + 16 * h + 8 * e < vd)
-                                    *reinterpret_cast<uint4 *>(static_cast<T *>(w.out) + at + 16 * h + 8 * e) = make_uint4(n[0], n[1], n[2], n[3]);
+                            for (int e = 0; e < 4; ++e) {
+                                if (c0 + 16 * h + 4 * e >= vd) break;
+                                if (w.out_f32)
+                                    *reinterpret_cast<ulonglong2 *>(static_cast<float *>(w.out) + at + 16 * h + 4 * e) = make_ulonglong2(v[2 * e], v[2 * e + 1]);
+                                else
+                                    *reinterpret_cast<uint2 *>(static_cast<T *>(w.out) + at + 16 * h + 4 * e) = make_uint2(narrow2<T>(v[2 * e]), narrow2<T>(v[2 * e + 1]));
                             }
                         }
                     }
@@ -643,23 +754,21 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sb + B_O);
-            }
-            if (STATES) {
-                if (c > 0) {
-                    ok = wwait(bar_of(B_DS, c - 1), par_of(c - 1), flag, a.err);
+                if (upd) {
+                    ok = wwait(sb + B_DS, c & 1, flag, a.err);
                     if (!ok) break;
-                    update(c - 1, before);
+                    update(c, L);
                 }
-                before = L;
-            } else if (upd) {
-                ok = wwait(bar_of(B_DS, c), par_of(c), flag, a.err);
-                if (!ok) break;
-                update(c, L);
-                if (c + 1 < nc) put_state();
-            }
-            if (!STATES && c + 1 < nc) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sb + B_S);
+                if (c + 1 < nc) {
+                    put_state();
+                    umma::fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sb + B_S);
+                    int tn, Ln;
+                    chunk(c + 1, tn, Ln);
+                    ok = make_p(c + 1, Ln);
+                    if (ok && (want_end || c + 2 < nc)) make_keys(c + 1, Ln, k0, k1);
+                }
             }
         }
         if (STATES && ok && nc > 0) {
@@ -671,7 +780,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
             float *e = STATES ? w.states + (n * a.H + j) * kStateFloats + row : w.end + (n * a.H + j) * kd * vd + (long long)row * w.rs;
             const long long step = STATES ? LD : w.cs;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < CW / 2; ++i) {
                 const int col = c0 + 2 * i;
                 if (col < vd) unpack2(st[i], e[col * step], e[(col + 1) * step]);
             }
@@ -679,7 +788,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
     }
     umma::fence_before();
     __syncthreads();
-    if (warp == NW + 1) umma::dealloc(tmem, 512);
+    if (warp == NS + NK + 1) umma::dealloc(tmem, 512);
 }
 
 template <typename T, bool STATES>
