@@ -18,7 +18,6 @@ constexpr int kStateFloats = LD * LD; // one state of the segments' exchange, pa
 // (v, do, q) -> dk and (k, q, do) -> dv.
 struct Walk {
     CUtensorMap tq, tk, tv;  // [tokens][heads][cols], boxes 64 x 1 x 128; tq, tk have kd columns, tv vd
-    CUtensorMap to;          // out, where it is 16-bit
     int kd, vd;
     int q_div, k_div, v_div; // head of the tensor = walk's head / div
     bool rev;

@@ -21,8 +21,9 @@ gdr_status check_lin(const gdr_lin_problem *p) {
     return GDR_OK;
 }
 
-// The cut: tokens of a segment and of a window, with the least estimated time.  In units of a chunk's time in the walk: a
-// chunk of the state pass takes half of one, a block's start and end 1.5, the state pass' launch 2.
+// The cut: tokens of a segment and of a window, with the least estimated time.  In microseconds, as measured: a chunk takes 4
+// in a walk and 2.2 in the state pass, a block's start and end 6 in both, each window before a segment 1 where its state is
+// summed up, a second launch 2.  (2 x 4096 tokens, 32 heads: 88 us with 2 segments; 1 x 65536, 16 heads: 311 with 9, 396 with 19.)
 void cut(const gdr_lin_problem *p, int walks, LinArgs *a) {
     const long long nc = (p->T + LC - 1) / LC, heads = (long long)p->H * walks;
     const long long rows = p->cu_seqlens ? 1 : p->B, more = p->cu_seqlens ? p->num_seqs : 0;
@@ -31,10 +32,10 @@ void cut(const gdr_lin_problem *p, int walks, LinArgs *a) {
     a->main_len = a->win_len = (int)((nc > 0 ? nc : 1) * LC);
     for (long long n = 1; n <= nc && n <= 512; ++n) {
         const long long len = (nc + n - 1) / n;
-        const double walk = rounds(rows * n * heads + more) * ((double)len + 1.5);
         for (long long d = 1; d <= (n == 1 ? 1 : 4); d *= 2) {
             const long long win = (len + d - 1) / d;
-            const double states = n == 1 ? 0 : rounds(rows * (n - 1) * d * (walks > 1 ? 2 : 1) * p->H + more) * (0.5 * win + 1) + 2;
+            const double walk = rounds(rows * n * heads + more) * (4.0 * (double)(win * d) + 6 + 0.5 * (double)((n - 1) * d));
+            const double states = n == 1 ? 0 : rounds(rows * (n - 1) * d * (walks > 1 ? 2 : 1) * p->H + more) * (2.2 * (double)win + 6) + 2;
             if (best < 0 || walk + states < best) best = walk + states, a->main_len = (int)(win * d * LC), a->win_len = (int)(win * LC);
         }
     }
@@ -120,7 +121,7 @@ gdr_status gdr_lin_fwd(const gdr_lin_problem *p, const void *q, const void *k, c
     if (tokens == 0 && !state_out) return GDR_OK;
     Walk &w = lp.w[0];
     if (tokens && (!token_map(&w.tq, p, q, p->q_ld, p->Hk, p->K) || !token_map(&w.tk, p, k, p->k_ld, p->Hk, p->K) ||
-                   !token_map(&w.tv, p, v, p->v_ld, p->H, p->V) || !token_map(&w.to, p, o, (int64_t)p->H * p->V, p->H, p->V)))
+                   !token_map(&w.tv, p, v, p->v_ld, p->H, p->V)))
         return cuda_status(cudaErrorInvalidValue);
     w.kd = p->K, w.vd = p->V;
     w.q_div = w.k_div = p->H / p->Hk, w.v_div = 1;
@@ -190,10 +191,6 @@ gdr_status gdr_lin_bwd(const gdr_lin_problem *p, const void *q, const void *k, c
                    !token_map(&mv, p, v, p->v_ld, p->H, p->V) || !token_map(&md, p, dout, (int64_t)p->H * p->V, p->H, p->V)))
         return cuda_status(cudaErrorInvalidValue);
     const int grp = p->H / p->Hk;
-    if (tokens && (!token_map(&lp.w[1].to, p, dv, (int64_t)p->H * p->V, p->H, p->V) ||
-                   (grp == 1 && (!token_map(&lp.w[2].to, p, dk, (int64_t)p->H * p->K, p->H, p->K) ||
-                                 !token_map(&lp.w[0].to, p, dq, (int64_t)p->H * p->K, p->H, p->K)))))
-        return cuda_status(cudaErrorInvalidValue);
     char *ws = static_cast<char *>(workspace);
     float *fw = reinterpret_cast<float *>(ws), *bw = reinterpret_cast<float *>(ws + l.one);
     float *pq = grp > 1 ? reinterpret_cast<float *>(ws + l.dq) : nullptr, *pk = grp > 1 ? reinterpret_cast<float *>(ws + l.dk) : nullptr;

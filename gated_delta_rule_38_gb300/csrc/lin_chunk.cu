@@ -16,14 +16,15 @@
 //                 in shared memory as the operand of Q S; and the output rows
 //   warps 8..11   lanes 32 (w mod 4) ..
 //   all twelve    P from Q K^T (tensor memory to tensor memory, where it is the left operand of P V), in blocks of 32 x 32:
-//                 warps 8..11 those on the diagonal, the others those beyond it; then the decayed keys
-//   warp 12       tile loads (TMA) into a ring of five 32 KB tiles, and the output tiles' stores
+//                 warps 8..11 those on the diagonal and next to it, the others those beyond; then the decayed keys
+//   warp 12       tile loads (TMA) into a ring of five 32 KB tiles
 //   warp 13       the MMAs:  Q S, P V, the state's update, Q K^T of the next chunk
 // The chain of a chunk: the update, the state's copy and the next Q S on one side, the next Q K^T and P on the other, then
 // P V, and the next update; output rows and keys are made beside it.
 // Fourteen warps leave a thread 128 registers; with eighteen and 96 the state's threads spilled, and what they spilled went
 // to L2.  Loops that can stay loops do: unrolled, a chunk's code no longer fitted the instruction caches next to the
-// schedulers.  (B = 1, T = 2048, 152 heads: 156 us with spills, 72 with sixteen warps through all steps together, @US@ so.)
+// schedulers.  (B = 1, T = 2048, 152 heads, 318 MB: 156 us with spills, 72 with sixteen
+// warps through all steps together, 63 so, which is 5.0 TB/s.)
 // A decayed key is two 16-bit numbers, the rounded one and the remainder's, each with a product of its own: their sum is
 // as good as keys of 16 bits of mantissa, because the states are handed on in fp32 (rounded once they would be off by
 // 1e-3; so they are by 3e-6).
@@ -51,7 +52,7 @@ constexpr uint32_t S_LO = RING * TILE;            // the keys' remainders
 constexpr uint32_t S_ST = S_LO + TILE;            // the state's copy (state pass: the remainders of odd chunks)
 constexpr uint32_t S_BAR = S_ST + TILE;
 constexpr uint32_t B_FULL = S_BAR, B_EMPTY = S_BAR + 8 * RING, B_QK = B_EMPTY + 8 * RING, B_S = B_QK + 8, B_P = B_S + 8,
-                   B_O = B_P + 8, B_PV = B_O + 8, B_K = B_PV + 8, B_DS = B_K + 16, B_DONE = B_DS + 16, S_SLOT = B_DONE + 8, S_FLAG = S_SLOT + 4;
+                   B_PV = B_P + 8, B_K = B_PV + 8, B_DS = B_K + 16, B_DONE = B_DS + 16, S_SLOT = B_DONE + 8, S_FLAG = S_SLOT + 4;
 constexpr uint32_t S_LAM = S_FLAG + 8;            // lambda^128 as two fp32 numbers
 // decays of up to 31 tokens: COL[c] = lambda^(31-c) (rev: lambda^c); DIAG[31 + row - key] = s_kv lambda^|row - key| where
 // the row sees the key, else 0
@@ -104,6 +105,11 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, uint32
     raise_error(err, GDR_ERR_TIMEOUT);
     sts32(flag, 1);
     return false;
+}
+// Two or three at once: their tests overlap.
+__device__ __forceinline__ bool wait_phases(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, uint32_t b2, uint32_t p2, uint32_t flag, unsigned *err) {
+    const bool r0 = try_phase(b0, p0), r1 = try_phase(b1, p1), r2 = try_phase(b2, p2);
+    return (r0 || wait_phase(b0, p0, flag, err)) && (r1 || wait_phase(b1, p1, flag, err)) && (r2 || wait_phase(b2, p2, flag, err));
 }
 // Every lane polls and the warp agrees on the outcome.
 __device__ __forceinline__ bool wwait(uint32_t bar, uint32_t parity, uint32_t flag, unsigned *err) {
@@ -178,6 +184,10 @@ __device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) {
     uint64_t r;
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
     return r;
+}
+// 32 bytes of one row, from a 32-byte boundary.
+__device__ __forceinline__ void store32(void *p, f2 a, f2 b, f2 c, f2 d) {
+    asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};\n" ::"l"(p), "l"(a), "l"(b), "l"(c), "l"(d) : "memory");
 }
 __device__ __forceinline__ f2 f2_of(uint32_t lo, uint32_t hi) {
     return pack2(__uint_as_float(lo), __uint_as_float(hi));
@@ -285,23 +295,52 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
     const float g = a.decay[j] < -120.f ? -120.f : a.decay[j];  // (e^-120 is 0 in fp32; 0 x -inf would be NaN)
     const float lg = g * LOG2E;
 
-    if (tid == 0) {
-        for (int i = 0; i < RING; ++i) {
-            umma::mbar_init(sb + B_FULL + 8 * i, 1);
-            umma::mbar_init(sb + B_EMPTY + 8 * i, 1);
+    // chunk c of the walk: its first token and length
+    auto chunk = [&](int c, int &t, int &L) {
+        t = seg.t0 + (rev ? nc - 1 - c : c) * LC;
+        L = min(LC, seg.t1 - t);
+    };
+    constexpr int PER = STATES ? 2 : 3;  // tiles a chunk: (q,) k, v
+    auto slot_of = [&](int c, int which) { return (PER * c + which) % RING; };
+    auto phase_of = [&](int c, int which) { return (uint32_t)(((PER * c + which) / RING) & 1); };
+    constexpr int KI = STATES ? 0 : 1, VI = KI + 1;
+    const int kblk = kd > 64 ? 2 : 1, vblk = vd > 64 ? 2 : 1;
+    // a chunk's tile into its place of the ring
+    auto tile = [&](int c, int i) {
+        int t, L;
+        chunk(c, t, L);
+        const CUtensorMap *m = i == VI ? &w.tv : i == KI ? &w.tk : &w.tq;
+        const int h = j / (i == VI ? w.v_div : i == KI ? w.k_div : w.q_div), nb = i == VI ? vblk : kblk;
+        if (lane == 0) {
+            const uint32_t dst = sb + slot_of(c, i) * TILE, bar = sb + B_FULL + 8 * slot_of(c, i);
+            tma::expect_tx(bar, nb * BLK);
+#pragma unroll 1
+            for (int b = 0; b < nb; ++b) tma::load3d(dst + b * BLK, m, 64 * b, h, t, bar);
         }
-        umma::mbar_init(sb + B_QK, 2);
-        umma::mbar_init(sb + B_PV, 1);
-        umma::mbar_init(sb + B_P, NS + NK);
-        umma::mbar_init(sb + B_O, NS);
-        umma::mbar_init(sb + B_S, NS);
-        for (int i = 0; i < 2; ++i) {
-            umma::mbar_init(sb + B_K + 8 * i, NS + NK);
-            umma::mbar_init(sb + B_DS + 8 * i, 1);
+        __syncwarp();
+    };
+    // The loading warp prepares the barriers and begins with the first chunk while the others prepare the rest.
+    if (warp == NS + NK) {
+        if (lane == 0) {
+            for (int i = 0; i < RING; ++i) {
+                umma::mbar_init(sb + B_FULL + 8 * i, 1);
+                umma::mbar_init(sb + B_EMPTY + 8 * i, 1);
+            }
+            umma::mbar_init(sb + B_QK, 2);
+            umma::mbar_init(sb + B_PV, 1);
+            umma::mbar_init(sb + B_P, NS + NK);
+            umma::mbar_init(sb + B_S, NS);
+            for (int i = 0; i < 2; ++i) {
+                umma::mbar_init(sb + B_K + 8 * i, NS + NK);
+                umma::mbar_init(sb + B_DS + 8 * i, 1);
+            }
+            umma::mbar_init(sb + B_DONE, 1);
+            umma::fence_mbar_init();
+            sts32(flag, 0);
         }
-        umma::mbar_init(sb + B_DONE, 1);
-        umma::fence_mbar_init();
-        sts32(flag, 0);
+        __syncwarp();
+#pragma unroll 1
+        for (int i = 0; i < PER && nc > 0; ++i) tile(0, i);
     }
     if (tid == 32) {
         const double l = exp((double)g * LC);
@@ -319,19 +358,10 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
     umma::fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + S_SLOT);
 
-    // chunk c of the walk: its first token and length
-    auto chunk = [&](int c, int &t, int &L) {
-        t = seg.t0 + (rev ? nc - 1 - c : c) * LC;
-        L = min(LC, seg.t1 - t);
-    };
-    constexpr int PER = STATES ? 2 : 3;  // tiles a chunk: (q,) k, v
-    auto slot_of = [&](int c, int which) { return (PER * c + which) % RING; };
-    auto phase_of = [&](int c, int which) { return (uint32_t)(((PER * c + which) / RING) & 1); };
-    constexpr int KI = STATES ? 0 : 1, VI = KI + 1;
     // The state pass' hand-offs run up to two chunks ahead of one another, so each parity of chunks has its own barriers.
     auto bar_of = [&](uint32_t bar, int c) { return sb + bar + (STATES && (c & 1) ? 8u : 0u); };
     auto par_of = [&](int c) { return (uint32_t)((STATES ? c >> 1 : c) & 1); };
-    const int ksteps = (kd + 15) / 16, kblk = kd > 64 ? 2 : 1, vblk = vd > 64 ? 2 : 1;
+    const int ksteps = (kd + 15) / 16;
     const int NV = (vd + 15) / 16 * 16;
 
     // The decayed keys of chunk c, eights i0 .. i1 of the columns of row 32 (warp mod 4) + lane; the rounded ones in place of k.
@@ -369,54 +399,96 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
         if (lane == 0) mbar_arrive(bar_of(B_K, c));
     };
 
-    // full chunks' 16-bit output rows leave through the q tile as a TMA store
-    const bool staged = !STATES && !w.out_f32;
-    if (warp == NS + NK) {
-        // ------------------------------------------------------------ tile loads, output stores
-        const int hq = j / w.q_div, hk = j / w.k_div, hv = j / w.v_div;
-        int issued = 0;
-        bool ok = true;
-        auto store = [&](int c) {  // the output rows of chunk c, once they are in its q tile
-            ok = ok && wwait(sb + B_O, c & 1, flag, a.err);
-            int t, L;
-            chunk(c, t, L);
-            if (ok && staged && L == LC && lane == 0) {
-                for (int b = 0; b < vblk; ++b) tma::store3d(&w.to, 64 * b, j, t, sb + slot_of(c, 0) * TILE + b * BLK);
-                tma::commit_group();
-                tma::wait_read();
-            }
-            __syncwarp();
-        };
-        // a chunk's tile into its place of the ring
-        auto tile = [&](int c, int i) {
-            int t, L;
-            chunk(c, t, L);
-            const CUtensorMap *m = i == VI ? &w.tv : i == KI ? &w.tk : &w.tq;
-            const int h = i == VI ? hv : i == KI ? hk : hq, nb = i == VI ? vblk : kblk;
-            if (lane == 0) {
-                const uint32_t dst = sb + slot_of(c, i) * TILE, bar = sb + B_FULL + 8 * slot_of(c, i);
-                tma::expect_tx(bar, nb * BLK);
+    // The block of P `dist` blocks of 32 from the diagonal in this warp's rows, if there is one: lambda^|r-s| as a row's factor
+    // (distance to the block's near edge) times a column's (from there), both at most 1.
+    auto p_beyond = [&](int dist, int L) {
+        const int q4 = warp & 3, blk = rev ? q4 + dist : q4 - dist;
+        if (blk < 0 || blk > 3) return;
+        const uint32_t at = tmem + ((uint32_t)(q4 * 32) << 16) + T_QK + 32 * blk;
+        const f2 rf = both(w.s_kv * ex2((float)(32 * dist + (rev ? -lane : lane - 31)) * lg));
 #pragma unroll 1
-                for (int b = 0; b < nb; ++b) tma::load3d(dst + b * BLK, m, 64 * b, h, t, bar);
+        for (int h = 0; h < 2; ++h) {
+            uint32_t x[16], o[8];
+            float4 f[4];
+            tld16(at + 16 * h, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = reinterpret_cast<const float4 *>(smem + S_COL)[4 * h + i];
+            twait16(x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                o[2 * i] = narrow2<T>(mul2(mul2(f2_of(x[4 * i], x[4 * i + 1]), rf), pack2(f[i].x, f[i].y)));
+                o[2 * i + 1] = narrow2<T>(mul2(mul2(f2_of(x[4 * i + 2], x[4 * i + 3]), rf), pack2(f[i].z, f[i].w)));
             }
-            __syncwarp();
-        };
-        for (int c = 0; c < nc && ok; ++c) {
+            if (rev && L < LC) {  // (a short chunk's rows see no keys behind it)
+                const int most = L - 32 * blk - 16 * h;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] = 2 * i + 1 < most ? o[i] : 2 * i < most ? o[i] & 0xffffu : 0u;
+            }
+            // (columns of this block that it has read: the lower 16 of its 32)
+            tst8(at + 8 * h, o);
+        }
+    };
+
+    // The output rows of chunk c, columns c0 .. c1 (multiples of 16) of row 32 (warp mod 4) + lane.  Rows of 16 columns are whole
+    // 32-byte sectors where they begin on one.  (A lane has a row of its own.  A tile staged for a TMA store kept its place from
+    // the loads, and the next chunk's v came late.)
+    auto out_rows = [&](int c, int t, int L, int c0, int c1) {
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t quad = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const bool use_s = c > 0 || has_start;
+        umma::fence_after();
+        const float rf = use_s ? w.s_out * ex2((float)(rev ? L - 1 - row : row + 1) * lg) : 0.f;
+        const long long at = (((long long)t + row) * a.H + j) * vd;
+        const bool wide = row < L && vd % 16 == 0 && reinterpret_cast<uintptr_t>(w.out) % 32 == 0;
 #pragma unroll 1
-            for (int i = 0; i < PER && ok; ++i) {
-                const int x = PER * c + i;
-                if (x >= RING) {
-                    ok = ok && wwait(sb + B_EMPTY + 8 * (x % RING), ((x / RING) - 1) & 1, flag, a.err);
-                    if (!STATES && (x - RING) % PER == 0) store((x - RING) / PER);
+        for (int col = c0; col < c1 && col < vd; col += 16) {
+            uint32_t x[16], y[16];
+            tld16(quad + T_PV + col, x);
+            if (use_s) tld16(quad + T_QS + col, y);
+            twait16(x);
+            f2 v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = mul2(f2_of(x[2 * e], x[2 * e + 1]), both(w.s_out));
+            if (use_s) {
+                twait16(y);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = fma2(f2_of(y[2 * e], y[2 * e + 1]), both(rf), v[e]);
+            }
+            if (w.out_f32) {
+                float *o = static_cast<float *>(w.out) + at + col;
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (row < L && col + 8 * e < vd) store32(o + 8 * e, v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            } else {
+                T *o = static_cast<T *>(w.out) + at + col;
+                uint32_t u[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] = narrow2<T>(v[e]);
+                if (wide) {
+                    store32(o, (f2)u[1] << 32 | u[0], (f2)u[3] << 32 | u[2], (f2)u[5] << 32 | u[4], (f2)u[7] << 32 | u[6]);
+                } else if (row < L) {
+                    *reinterpret_cast<uint4 *>(o) = make_uint4(u[0], u[1], u[2], u[3]);
+                    if (col + 8 < vd) *reinterpret_cast<uint4 *>(o + 8) = make_uint4(u[4], u[5], u[6], u[7]);
                 }
+            }
+        }
+        umma::fence_before();
+    };
+
+    if (warp == NS + NK) {
+        // ------------------------------------------------------------ tile loads
+        int issued = PER;
+        bool ok = true;
+        for (int c = 1; c < nc && ok; ++c) {
+#pragma unroll 1
+            for (int i = 0; i < PER; ++i) {
+                const int x = PER * c + i;
+                if (x >= RING) ok = ok && wwait(sb + B_EMPTY + 8 * (x % RING), ((x / RING) - 1) & 1, flag, a.err);
                 if (!ok) break;
                 tile(c, i);
                 ++issued;
             }
         }
-        if (!STATES && ok)  // the q tiles that nothing was loaded into since
-            for (int c = max(0, (PER * nc - RING + PER - 1) / PER); c < nc; ++c) store(c);
-        if (lane == 0) tma::wait_all();
         if (!ok) {  // after an error: let the loads in flight land (bounded)
             for (int x = max(0, issued - RING); x < issued; ++x)
                 umma::mbar_spin(sb + B_FULL + 8 * (x % RING), (x / RING) & 1, 4000000L);
@@ -430,9 +502,10 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
         bool ok = true;
         auto full = [&](int c, int which) { return wwait(sb + B_FULL + 8 * slot_of(c, which), phase_of(c, which), flag, a.err); };
         auto wait_qk = [&](int c) {
-            ok = ok && full(c, 0) && full(c, KI);
-            // (P of the chunk before has been read: Q K^T takes its place)
-            if (c > 0) ok = ok && wwait(sb + B_PV, (c - 1) & 1, flag, a.err);
+            // (and P of the chunk before has been read: Q K^T takes its place)
+            const uint32_t b = sb + B_FULL + 8 * slot_of(c, 0), f = phase_of(c, 0);
+            ok = ok && __all_sync(0xffffffffu, wait_phases(b, f, sb + B_FULL + 8 * slot_of(c, KI), phase_of(c, KI), c > 0 ? sb + B_PV : b,
+                                                           c > 0 ? (c - 1) & 1 : f, flag, a.err));
             umma::fence_after();
         };
         auto issue_qk = [&](int c) {
@@ -476,7 +549,9 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                         if (ks < ksteps) mma_ss(on, tmem + T_QS, desc_at(dq, o), desc_at(ds, ks * 2048u), i_qs, ks > 0);
                     }
                 }
-                ok = ok && wwait(sb + B_P, c & 1, flag, a.err) && full(c, VI);
+                commit_on(on, sb + B_EMPTY + 8 * slot_of(c, 0));
+                const uint32_t b = sb + B_FULL + 8 * slot_of(c, VI), f = phase_of(c, VI);
+                ok = ok && __all_sync(0xffffffffu, wait_phases(sb + B_P, c & 1, b, f, b, f, flag, a.err));
                 if (!ok) break;
                 umma::fence_after();
                 const uint64_t dv = umma::desc(sb + slot_of(c, VI) * TILE, BLK, 1024);
@@ -484,8 +559,6 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                 for (int ks = 0; ks < 8; ++ks)
                     if (ks < ts) mma_ts(on, tmem + T_PV, tmem + T_QK + 32 * (ks >> 1) + 8 * (ks & 1), desc_at(dv, ks * 2048u), i_qs, ks > 0);
                 commit_on(on, sb + B_PV);
-                // (q has been read; every use of a place is one phase of its barrier, though the output's store waits longer)
-                commit_on(on, sb + B_EMPTY + 8 * slot_of(c, 0));
             } else {
                 ok = ok && full(c, VI);
             }
@@ -524,7 +597,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
             __syncwarp();
             return true;
         };
-        // The blocks of P on the diagonal and those that see nothing.
+        // The blocks of P on the diagonal, next to it, and those that see nothing.
         auto make_p = [&](int c, int L) {
             if (!wwait(sb + B_QK, c & 1, flag, a.err)) return false;
             umma::fence_after();
@@ -548,6 +621,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                 for (int i = 0; i < 16; ++i) o[i] = 2 * i + 1 < most ? o[i] : 2 * i < most ? o[i] & 0xffffu : 0u;
             }
             tst16(quad + T_QK + 32 * q4, o);
+            p_beyond(1, L);
             if (L < LC) {
                 // the rows behind a short chunk are another sequence's: what they hold must not meet even a zero
                 if (!clear_v(c, L)) return false;
@@ -568,7 +642,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                 // (the remainders' place: read by the update of the chunk before)
                 if (want_end || c + 1 < nc) {
                     if (c > 0) ok = ok && wwait(sb + B_DS, (c - 1) & 1, flag, a.err);
-                    if (ok) make_keys(c, L, 12, min(16, 8 * kblk));
+                    if (ok) make_keys(c, L, 10, min(16, 8 * kblk));
                 }
                 continue;
             }
@@ -594,9 +668,16 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
             if (w.start) {
                 const float *s0 = w.start + ((long long)seg.n * a.H + j) * kd * vd + (long long)row * w.rs;
 #pragma unroll
-                for (int i = 0; i < CW / 2; ++i) {
-                    const int col = c0 + 2 * i;
-                    if (live && col < vd) st[i] = pack2(s0[(long long)col * w.cs], s0[(long long)(col + 1) * w.cs]);
+                for (int i = 0; i < CW / 4; ++i) {
+                    const int col = c0 + 4 * i;
+                    if (!live || col >= vd) continue;
+                    if (w.cs == 1) {
+                        const ulonglong2 u = *reinterpret_cast<const ulonglong2 *>(s0 + col);
+                        st[2 * i] = u.x, st[2 * i + 1] = u.y;
+                    } else {
+                        const long long cs = w.cs;
+                        st[2 * i] = pack2(s0[col * cs], s0[(col + 1) * cs]), st[2 * i + 1] = pack2(s0[(col + 2) * cs], s0[(col + 3) * cs]);
+                    }
                 }
             }
             if (!at_start) {
@@ -645,45 +726,19 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
             }
             umma::fence_before();
         };
-        // The blocks of P beyond the diagonal, each lambda^|r-s| as a row's factor (distance to the block's near edge) times a
-        // column's (from there), both at most 1: warps 4..7 the nearest, 0..3 the others.
+        // The blocks of P two or three from the diagonal.
         auto make_p = [&](int c, int L) {
             if (!wwait(sb + B_QK, c & 1, flag, a.err)) return false;
             umma::fence_after();
-            const int d0 = c0 ? 1 : 2, d1 = c0 ? 1 : 3;
-#pragma unroll 1
-            for (int h = 0; h < 2 * (d1 - d0 + 1); ++h) {
-                const int dist = d0 + (h >> 1), blk = rev ? q4 + dist : q4 - dist;
-                if (blk < 0 || blk > 3) break;
-                const uint32_t at = quad + T_QK + 32 * blk;
-                const f2 rf = both(w.s_kv * ex2((float)(32 * dist + (rev ? -lane : lane - 31)) * lg));
-                uint32_t x[16], o[8];
-                float4 f[4];
-                tld16(at + 16 * (h & 1), x);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) f[i] = reinterpret_cast<const float4 *>(smem + S_COL)[4 * (h & 1) + i];
-                twait16(x);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    o[2 * i] = narrow2<T>(mul2(mul2(f2_of(x[4 * i], x[4 * i + 1]), rf), pack2(f[i].x, f[i].y)));
-                    o[2 * i + 1] = narrow2<T>(mul2(mul2(f2_of(x[4 * i + 2], x[4 * i + 3]), rf), pack2(f[i].z, f[i].w)));
-                }
-                if (rev && L < LC) {
-                    const int most = L - 32 * blk - 16 * (h & 1);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) o[i] = 2 * i + 1 < most ? o[i] : 2 * i < most ? o[i] & 0xffffu : 0u;
-                }
-                // (columns of this block that it has read: the lower 16 of its 32)
-                tst8(at + 8 * (h & 1), o);
-            }
+            p_beyond(c0 ? 2 : 3, L);
             tst_wait();
             umma::fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(sb + B_P);
             return true;
         };
-        // this warp's share of the keys: a quarter of the columns (state pass), or three eighths
-        const int k0 = STATES ? 8 + c0 / 16 : c0 / 64 * 6, k1 = min(k0 + (STATES ? 4 : 6), 8 * kblk);
+        // this warp's share of the keys: a quarter of the columns (state pass), or six and four eights of sixteen
+        const int k0 = STATES ? 8 + c0 / 16 : c0 ? 6 : 0, k1 = min(STATES ? k0 + 4 : c0 ? 10 : 6, 8 * kblk);
         bool ok = true;
         if (!STATES) {
             put_state();
@@ -701,7 +756,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
         for (int c = 0; c < nc && ok; ++c) {
             int t, L;
             chunk(c, t, L);
-            const bool upd = want_end || c + 1 < nc, use_s = c > 0 || has_start;
+            const bool upd = want_end || c + 1 < nc;
             if (STATES) {
                 ok = wwait(sb + B_FULL + 8 * slot_of(c, KI), phase_of(c, KI), flag, a.err);
                 if (!ok) break;
@@ -715,45 +770,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
             } else {
                 ok = wwait(sb + B_PV, c & 1, flag, a.err);
                 if (!ok) break;
-                if (c0 < vd) {
-                    umma::fence_after();
-                    const float rf = use_s ? w.s_out * ex2((float)(rev ? L - 1 - row : row + 1) * lg) : 0.f;
-                    const long long at = (((long long)t + row) * a.H + j) * vd + c0;
-                    const uint32_t qt = sb + slot_of(c, 0) * TILE;
-#pragma unroll 1
-                    for (int h = 0; h < CW / 16; ++h) {
-                        uint32_t x[16], y[16];
-                        tld16(quad + T_PV + c0 + 16 * h, x);
-                        if (use_s) tld16(quad + T_QS + c0 + 16 * h, y);
-                        twait16(x);
-                        f2 v[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = mul2(f2_of(x[2 * e], x[2 * e + 1]), both(w.s_out));
-                        if (use_s) {
-                            twait16(y);
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) v[e] = fma2(f2_of(y[2 * e], y[2 * e + 1]), both(rf), v[e]);
-                        }
-                        if (staged && L == LC) {
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                umma::st_shared_v4(qt + place(2 * h + e), narrow2<T>(v[4 * e]), narrow2<T>(v[4 * e + 1]), narrow2<T>(v[4 * e + 2]), narrow2<T>(v[4 * e + 3]));
-                        } else if (row < L) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if (c0 + 16 * h + 4 * e >= vd) break;
-                                if (w.out_f32)
-                                    *reinterpret_cast<ulonglong2 *>(static_cast<float *>(w.out) + at + 16 * h + 4 * e) = make_ulonglong2(v[2 * e], v[2 * e + 1]);
-                                else
-                                    *reinterpret_cast<uint2 *>(static_cast<T *>(w.out) + at + 16 * h + 4 * e) = make_uint2(narrow2<T>(v[2 * e]), narrow2<T>(v[2 * e + 1]));
-                            }
-                        }
-                    }
-                    umma::fence_before();
-                    umma::fence_async_smem();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(sb + B_O);
+                out_rows(c, t, L, c0, c0 + 64);
                 if (upd) {
                     ok = wwait(sb + B_DS, c & 1, flag, a.err);
                     if (!ok) break;
@@ -778,11 +795,17 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
         if (ok && want_end && live) {
             const long long n = STATES ? (long long)slot : (long long)seg.n;
             float *e = STATES ? w.states + (n * a.H + j) * kStateFloats + row : w.end + (n * a.H + j) * kd * vd + (long long)row * w.rs;
-            const long long step = STATES ? LD : w.cs;
+            const long long cs = STATES ? LD : w.cs;
 #pragma unroll
-            for (int i = 0; i < CW / 2; ++i) {
-                const int col = c0 + 2 * i;
-                if (col < vd) unpack2(st[i], e[col * step], e[(col + 1) * step]);
+            for (int i = 0; i < CW / 4; ++i) {
+                const int col = c0 + 4 * i;
+                if (col >= vd) continue;
+                if (!STATES && cs == 1) {
+                    *reinterpret_cast<ulonglong2 *>(e + col) = make_ulonglong2(st[2 * i], st[2 * i + 1]);
+                } else {
+                    unpack2(st[2 * i], e[col * cs], e[(col + 1) * cs]);
+                    unpack2(st[2 * i + 1], e[(col + 2) * cs], e[(col + 3) * cs]);
+                }
             }
         }
     }
