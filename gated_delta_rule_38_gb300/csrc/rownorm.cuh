@@ -27,31 +27,38 @@ namespace {
 
 using namespace norm;
 
-// Access to the rows of up to five tensors.  Elements come in groups of 8: group k of thread t holds columns 8 (k TPR + t)
-// and on, or, ragged, t + (8 k + e) TPR.
-template <typename T, int NG, int BT, bool RAG>
+// Access to the rows of the tensors in MASK (bits of IN_*; the gradient from later layers, last, may be missing at run
+// time).  Elements come in groups of 8: group k of thread t holds columns 8 (k TPR + t) and on, or, ragged,
+// t + (8 k + e) TPR.  Everything about places that can be known when compiling is: worked out at run time it took more
+// instructions than the arithmetic (block norm's backward, 8192 x 4096: 188 us then, @BB@ so).
+template <typename T, int NG, int BT, bool RAG, bool F32, unsigned MASK>
 struct Rows {
+    static constexpr int elem(int i) { return (i == IN_H || i == IN_DRES) && F32 ? 4 : 2; }
+    static constexpr bool has(int i) { return MASK >> i & 1; }
     const RowArgs &a;
     char *smem;
-    int t, slot, per;  // thread of the row, row slot of the block; bytes a stage (vec) or a slot's row (ragged)
+    int t, slot;            // thread of the row, row slot of the block
+    uint32_t own;           // vec: the groups of this thread that lie in the row, a bit each
     __device__ __forceinline__ Rows(const RowArgs &a_, void *s) : a(a_), smem(static_cast<char *>(s)) {
         slot = threadIdx.x / a.tpr;
         t = threadIdx.x - slot * a.tpr;
-        per = 0;
+        own = 0;
 #pragma unroll
-        for (int i = 0; i < kMaxIn; ++i) per += size(i);
+        for (int g = 0; g < NG; ++g) own |= (uint32_t)((g * a.tpr + t) * 8 < a.D) << g;
     }
-    // an input's bytes in a stage, and where it begins
-    __device__ __forceinline__ int size(int i) const {
-        if (!a.in[i].elem) return 0;
-        return RAG ? rag_place(a.D, a.in[i].elem) : NG * BT * 8 * a.in[i].elem;
-    }
-    __device__ __forceinline__ int off(int i) const {
+    // where an input's rows begin in a stage (vec: NG groups of all threads, the halves of an fp32 group apart)
+    static constexpr int vec_off(int i) {
         int o = 0;
+        for (int k = 0; k < i; ++k)
+            if (has(k)) o += NG * BT * 8 * elem(k);
+        return o;
+    }
+    __device__ __forceinline__ int rag_off(int i) const {
+        int n2 = 0, n4 = 0;
 #pragma unroll
         for (int k = 0; k < kMaxIn; ++k)
-            if (k < i) o += size(k);
-        return o;
+            if (k < i && has(k)) (elem(k) == 4 ? n4 : n2) += 1;
+        return n2 * rag_place(a.D, 2) + n4 * rag_place(a.D, 4);
     }
     __device__ __forceinline__ const char *at(int i, long long row) const {
         const RowIn &in = a.in[i];
@@ -60,22 +67,23 @@ struct Rows {
             const long long token = a.rows <= 0x7fffffff ? (long long)((unsigned)row / (unsigned)in.heads) : row / in.heads;
             e = token * in.ld + (row - token * in.heads) * a.D;
         }
-        return static_cast<const char *>(in.p) + e * in.elem;
+        return static_cast<const char *>(in.p) + e * elem(i);
     }
-    __device__ __forceinline__ char *place(int stage, int i) const {
-        return smem + (RAG ? (size_t)(stage * a.rpb + slot) * per : (size_t)stage * per) + off(i);
+    template <int I>
+    __device__ __forceinline__ char *place(int stage) const {
+        if constexpr (RAG) return smem + (size_t)(stage * a.rpb + slot) * a.place + rag_off(I);
+        else return smem + stage * a.place + vec_off(I) + threadIdx.x * 16;
     }
-    __device__ __forceinline__ void fetch(long long row, int stage) const {
-        const bool in = row < a.rows;
-#pragma unroll
-        for (int i = 0; i < kMaxIn; ++i) {
-            const int elem = a.in[i].elem;
-            if (!elem) continue;
-            char *to = place(stage, i);
+    template <int I>
+    __device__ __forceinline__ void fetch_one(long long row, int stage) const {
+        if constexpr (has(I)) {
+            const bool in = row < a.rows;
+            if (I == IN_DRES && !a.in[I].p) return;
+            char *to = place<I>(stage);
             if constexpr (RAG) {
-                if (!in) continue;
-                const char *base = static_cast<const char *>(a.in[i].p), *src0 = at(i, row), *hi = at(i, a.rows - 1) + a.D * elem;
-                const int sk = (int)(reinterpret_cast<uintptr_t>(src0) & 15), bytes = a.D * elem, pieces = (sk + bytes + 15) / 16;
+                if (!in) return;
+                const char *base = static_cast<const char *>(a.in[I].p), *src0 = at(I, row), *hi = at(I, a.rows - 1) + a.D * elem(I);
+                const int sk = (int)(reinterpret_cast<uintptr_t>(src0) & 15), bytes = a.D * elem(I), pieces = (sk + bytes + 15) / 16;
                 for (int k = t; k < pieces; k += a.tpr) {
                     const char *src = src0 - sk + k * 16;
                     if (src >= base) {
@@ -88,40 +96,48 @@ struct Rows {
                     }
                 }
             } else {
-                const char *src = at(i, in ? row : 0);
+                const char *src = at(I, in ? row : 0) + t * 8 * elem(I);
+                const uint32_t d = smem_u32(to);
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
-                    const int c = (g * a.tpr + t) * 8;
-                    for (int h = 0; h < elem / 2; ++h) {  // halves of an fp32 group lie BT places apart
-                        char *d = to + ((g * (elem / 2) + h) * BT + threadIdx.x) * 16;
-                        if (in && c < a.D)
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(d)), "l"(src + c * elem + h * 16) : "memory");
-                        else
-                            *reinterpret_cast<uint4 *>(d) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int h = 0; h < elem(I) / 2; ++h) {
+                        const int o = (g * (elem(I) / 2) + h) * BT * 16;
+                        // (no bytes, zeros: for what lies behind the row's end or the last row)
+                        const int n = in && (own >> g & 1) ? 16 : 0;
+                        const char *from = n ? src + g * a.tpr * 8 * elem(I) + h * 16 : src;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(d + o), "l"(from), "r"(n) : "memory");
                     }
                 }
             }
         }
+    }
+    __device__ __forceinline__ void fetch(long long row, int stage) const {
+        fetch_one<0>(row, stage);
+        fetch_one<1>(row, stage);
+        fetch_one<2>(row, stage);
+        fetch_one<3>(row, stage);
+        fetch_one<4>(row, stage);
         asm volatile("cp.async.commit_group;\n" ::: "memory");
     }
-    template <bool F32>
-    __device__ __forceinline__ void get(int stage, int i, long long row, int g, f2 *o) const {
-        const char *s = place(stage, i);
+    template <int I>
+    __device__ __forceinline__ void get(int stage, long long row, int g, f2 *o) const {
+        constexpr bool W = elem(I) == 4;
+        const char *s = place<I>(stage);
         if constexpr (RAG) {
-            s += reinterpret_cast<uintptr_t>(at(i, row)) & 15;
+            s += reinterpret_cast<uintptr_t>(at(I, row)) & 15;
             float v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int c = t + (8 * g + e) * a.tpr;
-                v[e] = row < a.rows && c < a.D ? rag_get<T, F32>(s, c) : 0.f;
+                v[e] = row < a.rows && c < a.D ? rag_get<T, W>(s, c) : 0.f;
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[e] = pack2(v[2 * e], v[2 * e + 1]);
         } else {
-            const uint4 *q = reinterpret_cast<const uint4 *>(s) + (g * (F32 ? 2 : 1)) * BT + threadIdx.x;
-            const uint4 u = q[0];
-            if constexpr (F32) {
-                const uint4 x = q[BT];
+            const uint4 u = *reinterpret_cast<const uint4 *>(s + g * (W ? 2 : 1) * BT * 16);
+            if constexpr (W) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(s + (2 * g + 1) * BT * 16);
                 o[0] = pack2(__uint_as_float(u.x), __uint_as_float(u.y)), o[1] = pack2(__uint_as_float(u.z), __uint_as_float(u.w));
                 o[2] = pack2(__uint_as_float(x.x), __uint_as_float(x.y)), o[3] = pack2(__uint_as_float(x.z), __uint_as_float(x.w));
             } else {
@@ -130,7 +146,7 @@ struct Rows {
         }
     }
     // a group of an output [rows, D]
-    template <bool F32>
+    template <bool W>
     __device__ __forceinline__ void put(void *to, long long row, int g, const f2 *v) const {
         if (row >= a.rows) return;
         if constexpr (RAG) {
@@ -140,12 +156,12 @@ struct Rows {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int c = t + (8 * g + e) * a.tpr;
-                if (c < a.D) rag_put<T, F32>(to, row * a.D + c, x[e]);
+                if (c < a.D) rag_put<T, W>(to, row * a.D + c, x[e]);
             }
         } else {
             const int c = (g * a.tpr + t) * 8;
-            if (c >= a.D) return;
-            if constexpr (F32) {
+            if (!(own >> g & 1)) return;
+            if constexpr (W) {
                 ulonglong2 *q = reinterpret_cast<ulonglong2 *>(static_cast<float *>(to) + row * a.D + c);
                 q[0] = make_ulonglong2(v[0], v[1]);
                 q[1] = make_ulonglong2(v[2], v[3]);
@@ -232,33 +248,30 @@ __device__ __forceinline__ void row_sums(float *v, float *red, int parity, int t
         for (int i = 0; i < N; ++i) v[i] += r[(slot * wpr + k) * N + i];
 }
 
-// The gate's factors of four pairs and, where asked for, their derivatives.
+// The gate's factors of four pairs and, where asked for, their derivatives.  sigmoid(g) = 1 / (1 + e), e = exp(-g), and
+// 1 - sigmoid(g) = e sigmoid(g): neither cancels.  g is taken at -80 at least, where e is finite and the factor 1e-35.
 template <bool GRAD>
 __device__ __forceinline__ void gate_of_pairs(int act, const f2 *g, f2 *f, f2 *df) {
+    if (act == ACT_RAW) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        if (act == ACT_RAW) {
+        for (int e = 0; e < 4; ++e) {
             f[e] = g[e];
             if (GRAD) df[e] = both(1.f);
-            continue;
         }
-        // sigmoid(g) and 1 - sigmoid(g), each without cancellation
-        float x[2], s[2], c[2];
+        return;
+    }
+    const bool silu = act == ACT_SILU;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        float x[2];
         unpack2(g[e], x[0], x[1]);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float z = ex2(-fabsf(x[k]) * LOG2E), q = rcp(1.f + z), p = z * q;
-            s[k] = x[k] < 0.f ? p : q;
-            c[k] = x[k] < 0.f ? q : p;
-        }
-        const f2 sg = pack2(s[0], s[1]), cg = pack2(c[0], c[1]);
-        if (act == ACT_SIGMOID) {
-            f[e] = sg;
-            if (GRAD) df[e] = mul2(sg, cg);
-        } else {
-            // (far below, where the sigmoid has underflowed, an infinite g times it would be NaN where the limit is 0)
-            f[e] = mul2(pack2(fmaxf(x[0], -1e30f), fmaxf(x[1], -1e30f)), sg);
-            if (GRAD) df[e] = add2(mul2(f[e], cg), sg);
+        for (int k = 0; k < 2; ++k) asm("max.NaN.f32 %0, %1, %2;" : "=f"(x[k]) : "f"(x[k]), "f"(-80.f));
+        const f2 y = pack2(x[0], x[1]), z = ex2x2(mul2(y, both(-LOG2E))), sg = rcpx2(add2(z, both(1.f)));
+        f[e] = silu ? mul2(y, sg) : sg;
+        if (GRAD) {
+            const f2 c = mul2(z, sg);
+            df[e] = silu ? fma2(f[e], c, sg) : mul2(sg, c);
         }
     }
 }
@@ -292,10 +305,10 @@ __device__ __forceinline__ void walk(const R &rows, const RowArgs &a, F &&body) 
 // ---------------------------------------------------------------- gated norm
 
 template <typename T, int NG, int BT, bool RAG>
-__global__ void __launch_bounds__(BT, BT > 288 ? 1 : 3) gated_fwd_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(BT, BT > 288 ? 1 : 3) gated_fwd_kernel(const __grid_constant__ RowArgs a) {
     extern __shared__ __align__(16) char s_rows[];
     __shared__ float red[2 * 16];
-    const Rows<T, NG, BT, RAG> rows(a, s_rows);
+    const Rows<T, NG, BT, RAG, false, 1u << IN_X | 1u << IN_GATE> rows(a, s_rows);
     f2 w[4 * NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) rows.weight(a.w, g, w + 4 * g);
@@ -304,7 +317,7 @@ __global__ void __launch_bounds__(BT, BT > 288 ? 1 : 3) gated_fwd_kernel(const R
         f2 x[4 * NG], ss = 0ull;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            rows.template get<false>(stage, IN_X, row, g, x + 4 * g);
+            rows.template get<IN_X>(stage, row, g, x + 4 * g);
 #pragma unroll
             for (int e = 0; e < 4; ++e) ss = fma2(x[4 * g + e], x[4 * g + e], ss);
         }
@@ -314,7 +327,7 @@ __global__ void __launch_bounds__(BT, BT > 288 ? 1 : 3) gated_fwd_kernel(const R
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             f2 z[4], f[4];
-            rows.template get<false>(stage, IN_GATE, row, g, z);
+            rows.template get<IN_GATE>(stage, row, g, z);
             gate_of_pairs<false>(a.act, z, f, nullptr);
 #pragma unroll
             for (int e = 0; e < 4; ++e) f[e] = mul2(mul2(mul2(x[4 * g + e], r), w[4 * g + e]), f[e]);
@@ -324,10 +337,10 @@ __global__ void __launch_bounds__(BT, BT > 288 ? 1 : 3) gated_fwd_kernel(const R
 }
 
 template <typename T, int NG, int BT, bool RAG>
-__global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) gated_bwd_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) gated_bwd_kernel(const __grid_constant__ RowArgs a) {
     extern __shared__ __align__(16) char s_rows[];
     __shared__ float red[2 * 16 * 2];
-    const Rows<T, NG, BT, RAG> rows(a, s_rows);
+    const Rows<T, NG, BT, RAG, false, 1u << IN_X | 1u << IN_GATE | 1u << IN_DY> rows(a, s_rows);
     f2 w[4 * NG], dw[4 * NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) rows.weight(a.w, g, w + 4 * g);
@@ -339,9 +352,9 @@ __global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) gated_bwd_kernel(const R
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             f2 x[4], z[4], f[4], d[4];
-            rows.template get<false>(stage, IN_X, row, g, x);
-            rows.template get<false>(stage, IN_GATE, row, g, z);
-            rows.template get<false>(stage, IN_DY, row, g, d);
+            rows.template get<IN_X>(stage, row, g, x);
+            rows.template get<IN_GATE>(stage, row, g, z);
+            rows.template get<IN_DY>(stage, row, g, d);
             gate_of_pairs<false>(a.act, z, f, nullptr);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -358,9 +371,9 @@ __global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) gated_bwd_kernel(const R
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             f2 x[4], z[4], f[4], df[4], d[4], dx[4], dg[4];
-            rows.template get<false>(stage, IN_X, row, g, x);
-            rows.template get<false>(stage, IN_GATE, row, g, z);
-            rows.template get<false>(stage, IN_DY, row, g, d);
+            rows.template get<IN_X>(stage, row, g, x);
+            rows.template get<IN_GATE>(stage, row, g, z);
+            rows.template get<IN_DY>(stage, row, g, d);
             gate_of_pairs<true>(a.act, z, f, df);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -379,12 +392,12 @@ __global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) gated_bwd_kernel(const R
 
 // ---------------------------------------------------------------- block norm
 
-template <typename T, int NG, int BT, bool RAG, bool F32>
-__global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) block_fwd_kernel(const RowArgs a) {
+template <typename T, int NG, int BT, bool RAG, bool F32, bool GATE>
+__global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) block_fwd_kernel(const __grid_constant__ RowArgs a) {
     constexpr bool HOLD = NG <= 2;  // weights in registers
     extern __shared__ __align__(16) char s_rows[];
     __shared__ float red1[2 * 16], red2[2 * 16];
-    const Rows<T, NG, BT, RAG> rows(a, s_rows);
+    const Rows<T, NG, BT, RAG, F32, 1u << IN_X | (GATE ? 1u << IN_GATE : 0u) | 1u << IN_RES> rows(a, s_rows);
     f2 w[HOLD ? 4 * NG : 4], pw[HOLD ? 4 * NG : 4];
     if (HOLD) {
 #pragma unroll
@@ -398,7 +411,7 @@ __global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) block_fwd_kernel(const R
         f2 h[4 * NG];
         f2 scale = both(a.rscale);
 #pragma unroll
-        for (int g = 0; g < NG; ++g) rows.template get<false>(stage, IN_X, row, g, h + 4 * g);
+        for (int g = 0; g < NG; ++g) rows.template get<IN_X>(stage, row, g, h + 4 * g);
         if (a.pw) {
             f2 ss = 0ull;
 #pragma unroll
@@ -417,9 +430,9 @@ __global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) block_fwd_kernel(const R
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             f2 z[4], f[4], res[4];
-            rows.template get<F32>(stage, IN_RES, row, g, res);
-            if (a.act != ACT_NONE) {
-                rows.template get<false>(stage, IN_GATE, row, g, z);
+            rows.template get<IN_RES>(stage, row, g, res);
+            if constexpr (GATE) {
+                rows.template get<IN_GATE>(stage, row, g, z);
                 gate_of_pairs<false>(a.act, z, f, nullptr);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) h[4 * g + e] = mul2(h[4 * g + e], f[e]);
@@ -444,12 +457,12 @@ __global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) block_fwd_kernel(const R
     });
 }
 
-template <typename T, int NG, int BT, bool RAG, bool F32>
-__global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) block_bwd_kernel(const RowArgs a) {
+template <typename T, int NG, int BT, bool RAG, bool F32, bool GATE>
+__global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) block_bwd_kernel(const __grid_constant__ RowArgs a) {
     constexpr bool HOLD = NG <= 2;
     extern __shared__ __align__(16) char s_rows[];
     __shared__ float red1[2 * 16 * 3], red2[2 * 16];
-    const Rows<T, NG, BT, RAG> rows(a, s_rows);
+    const Rows<T, NG, BT, RAG, F32, 1u << IN_X | (GATE ? 1u << IN_GATE : 0u) | 1u << IN_DY | 1u << IN_H | 1u << IN_DRES> rows(a, s_rows);
     f2 w[HOLD ? 4 * NG : 4], pw[HOLD ? 4 * NG : 4], dw[4 * NG], dpw[4 * NG];
     if (HOLD) {
 #pragma unroll
@@ -466,9 +479,9 @@ __global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) block_bwd_kernel(const R
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             f2 x[4], h[4], d[4];
-            rows.template get<false>(stage, IN_X, row, g, x);
-            rows.template get<F32>(stage, IN_H, row, g, h);
-            rows.template get<false>(stage, IN_DY, row, g, d);
+            rows.template get<IN_X>(stage, row, g, x);
+            rows.template get<IN_H>(stage, row, g, h);
+            rows.template get<IN_DY>(stage, row, g, d);
             if (!HOLD) rows.weight(a.w, g, w);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -487,10 +500,10 @@ __global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) block_bwd_kernel(const R
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             f2 x[4], h[4], d[4], dh[4], f[4], df[4];
-            rows.template get<false>(stage, IN_X, row, g, x);
-            rows.template get<F32>(stage, IN_H, row, g, h);
-            rows.template get<false>(stage, IN_DY, row, g, d);
-            if (a.in[IN_DRES].elem) rows.template get<F32>(stage, IN_DRES, row, g, dh);
+            rows.template get<IN_X>(stage, row, g, x);
+            rows.template get<IN_H>(stage, row, g, h);
+            rows.template get<IN_DY>(stage, row, g, d);
+            if (a.in[IN_DRES].p) rows.template get<IN_DRES>(stage, row, g, dh);
             else dh[0] = dh[1] = dh[2] = dh[3] = 0ull;
             if (!HOLD) {
                 rows.weight(a.w, g, w);
@@ -503,22 +516,22 @@ __global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) block_bwd_kernel(const R
                 dw[4 * g + e] = fma2(mul2(h[e], both(r2)), d[e], dw[4 * g + e]);
             }
             rows.template put<F32>(a.dres, row, g, dh);
-            if (a.act != ACT_NONE) {
+            if constexpr (GATE) {
                 f2 z[4];
-                rows.template get<false>(stage, IN_GATE, row, g, z);
+                rows.template get<IN_GATE>(stage, row, g, z);
                 gate_of_pairs<true>(a.act, z, f, df);
             }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const f2 p = a.pw ? pw[HOLD ? 4 * g + e : e] : both(1.f);
                 const f2 db = mul2(dh[e], both(a.rscale)), n = mul2(x[e], both(r1));
-                if (a.act != ACT_NONE) df[e] = mul2(mul2(db, mul2(n, p)), df[e]);
-                const f2 dg = a.act != ACT_NONE ? mul2(db, f[e]) : db;
+                if (GATE) df[e] = mul2(mul2(db, mul2(n, p)), df[e]);
+                const f2 dg = GATE ? mul2(db, f[e]) : db;
                 dpw[4 * g + e] = fma2(dg, n, dpw[4 * g + e]);
                 dn[4 * g + e] = mul2(dg, p);
                 sn = fma2(dn[4 * g + e], x[e], sn);
             }
-            if (a.act != ACT_NONE) rows.template put<false>(a.dgate, row, g, df);
+            if (GATE) rows.template put<false>(a.dgate, row, g, df);
         }
         f2 k1 = 0ull, one1 = both(1.f);
         if (a.pw) {
@@ -530,7 +543,7 @@ __global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) block_bwd_kernel(const R
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             f2 x[4];
-            rows.template get<false>(stage, IN_X, row, g, x);
+            rows.template get<IN_X>(stage, row, g, x);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const f2 own = mul2(dn[4 * g + e], one1);

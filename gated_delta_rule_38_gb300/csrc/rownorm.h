@@ -15,7 +15,7 @@ struct RowIn {
     const void *p;
     long long ld;
     int heads;
-    int elem;  // bytes an element, 2 or 4; 0: not given
+    int elem;  // bytes an element, 2 or 4 (p null: not given)
 };
 
 constexpr int kMaxIn = 5;
@@ -27,16 +27,17 @@ struct RowArgs {
     float *part;                  // [blocks][D or 2 D]: dw, then dpw
     long long rows;
     int D, tpr, rpb, stages, act;
+    int place;                    // bytes of a stage (vec), or of a row (ragged)
     bool w_f32;
     float eps, rscale;
 };
 
 // The inputs' places in RowArgs::in.
-enum { IN_X = 0, IN_GATE = 1, IN_DY = 2, IN_H = 3, IN_DRES = 4, IN_RES = 3 };
+enum { IN_X = 0, IN_GATE = 1, IN_DY = 2, IN_H = 3, IN_DRES = 4, IN_RES = IN_H };
 
 struct RowForm {
     norm::NormShape s;
-    bool vec, f32;     // whole vectors; an fp32 residual stream
+    bool vec, f32, gate;  // whole vectors; an fp32 residual stream; a gate
     int blocks;
     size_t smem;
 };

@@ -13,6 +13,14 @@ bool ptr_ok(const void *p, size_t elem, bool *vec) {
     return true;
 }
 
+// Bytes of a stage of whole vectors, or of one ragged row.
+size_t place_of(const RowArgs &a, const norm::NormShape &s, bool vec) {
+    size_t n = 0;
+    for (const RowIn &in : a.in)
+        if (in.p) n += vec ? (size_t)s.nv * s.threads * 8 * in.elem : (size_t)((a.D * in.elem + 14 + 15) / 16 * 16);
+    return n;
+}
+
 // How the rows are spread, staged and walked.  A block keeps two rows' places (one on its way while the other is worked
 // on) where that leaves room for another block beside it, or its rows do not fit twice anyway; the grid is what is
 // resident at once.  (8192 x 4096, block norm's backward with an fp32 stream, 57 KB a row.)
@@ -20,9 +28,7 @@ RowForm form_of(const RowArgs &a, long long rows, bool vec, bool bwd) {
     RowForm f = {};
     f.vec = vec;
     f.s = norm::norm_shape(a.D, !vec);
-    size_t place = 0;
-    for (const RowIn &in : a.in)
-        if (in.elem) place += vec ? (size_t)f.s.nv * f.s.threads * 8 * in.elem : (size_t)f.s.rpb * ((a.D * in.elem + 14 + 15) / 16 * 16);
+    const size_t place = place_of(a, f.s, vec) * (vec ? 1 : f.s.rpb);
     const size_t all = 227 * 1024;
     const int most = f.s.threads > 288 ? 1 : bwd ? 2 : 3;  // (by registers, see the kernels' bounds)
     auto resident = [&](size_t smem) {
@@ -37,10 +43,8 @@ RowForm form_of(const RowArgs &a, long long rows, bool vec, bool bwd) {
 }
 void apply(RowArgs *a, const RowForm &f) {
     a->tpr = f.s.tpr, a->rpb = f.s.rpb;
-    size_t place = 0;
-    for (const RowIn &in : a->in)
-        if (in.elem) place += f.vec ? (size_t)f.s.nv * f.s.threads * 8 * in.elem : (size_t)f.s.rpb * ((a->D * in.elem + 14 + 15) / 16 * 16);
-    a->stages = f.smem >= 2 * place ? 2 : 1;
+    a->place = (int)place_of(*a, f.s, f.vec);
+    a->stages = f.smem >= 2 * (size_t)a->place * (f.vec ? 1 : f.s.rpb) ? 2 : 1;
 }
 
 // Partial rows of the parameters' gradients: whichever form a call takes has at most this many blocks.
@@ -180,7 +184,7 @@ gdr_status gdr_block_norm_fwd(const gdr_block_norm_problem *p, const void *x, co
     a.w = weight, a.pw = post_weight, a.y = y, a.res_out = residual_out, a.rows = p->rows, a.D = p->D;
     a.eps = p->eps, a.rscale = p->residual_scale, a.w_f32 = p->weight_dtype == GDR_FP32, a.act = gate ? act_of(p->gate_act) : ACT_NONE;
     RowForm f = form_of(a, a.rows, vec, false);
-    f.f32 = p->residual_dtype == GDR_FP32;
+    f.f32 = p->residual_dtype == GDR_FP32, f.gate = gate != nullptr;
     apply(&a, f);
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     return timed(K_BLOCK_FWD, cs, [&] { return p->dtype == GDR_BF16 ? block_fwd_bf16(a, f, cs) : block_fwd_fp16(a, f, cs); });
@@ -231,7 +235,7 @@ gdr_status gdr_block_norm_bwd(const gdr_block_norm_problem *p, const void *x, co
     a.part = static_cast<float *>(workspace);
     a.eps = p->eps, a.rscale = p->residual_scale, a.w_f32 = p->weight_dtype == GDR_FP32, a.act = gate ? act_of(p->gate_act) : ACT_NONE;
     RowForm f = form_of(a, a.rows, vec, true);
-    f.f32 = p->residual_dtype == GDR_FP32;
+    f.f32 = p->residual_dtype == GDR_FP32, f.gate = gate != nullptr;
     apply(&a, f);
     st = timed(K_BLOCK_BWD, cs, [&] { return p->dtype == GDR_BF16 ? block_bwd_bf16(a, f, cs) : block_bwd_fp16(a, f, cs); });
     if (st != GDR_OK) return st;
