@@ -13,9 +13,11 @@
 // one is worked on (all passes over a row read it there).  All sums are fp32; sums over rows leave one partial row a
 // block, which a second kernel adds in a fixed order.
 //
-// Two forms, told apart by RAG: where every row of every tensor starts on a 16-byte boundary, a thread owns vectors of 8
-// columns and copies what it reads itself; otherwise a row's threads bring the aligned 16-byte pieces that hold it and a
-// thread owns every TPR-th column.
+// A thread owns vectors of 8 columns, aligned to 16 bytes, and copies what it reads itself (fp32: its warp does).  Where
+// rows do not begin on such a boundary (SHIFT: a width that is no multiple of 8, contiguous tensors) the vectors are those of
+// the tensor, not of the row: row r's first element lies r D mod 8 elements into its first vector.  A block walks rows of one
+// remainder only, so that its threads keep their columns, their weights and their sums; the vectors at a row's ends are
+// masked.  (5311 x 4099, gated norm's backward: 167 us with a column of 2 bytes at a time, @SH@ so.)
 #pragma once
 
 #include "norm.cuh"
@@ -28,41 +30,52 @@ namespace {
 using namespace norm;
 
 // Access to the rows of the tensors in MASK (bits of IN_*; the gradient from later layers, last, may be missing at run
-// time).  Elements come in groups of 8: group k of thread t holds columns 8 (k TPR + t) and on, or, ragged,
-// t + (8 k + e) TPR.  Everything about places that can be known when compiling is: worked out at run time it took more
-// instructions than the arithmetic (block norm's backward, 8192 x 4096: 188 us then, @BB@ so).
-template <typename T, int NG, int BT, bool RAG, bool F32, unsigned MASK>
+// time).  Elements come in groups of 8: group g of thread t holds columns 8 (g TPR + t) - shift and on.  Everything about
+// places that can be known when compiling is: worked out at run time it took more instructions than the arithmetic (block
+// norm's backward, 8192 x 4096: 188 us then, 115 so).
+template <typename T, int NG, int BT, bool SHIFT, bool F32, unsigned MASK>
 struct Rows {
     static constexpr int elem(int i) { return (i == IN_H || i == IN_DRES) && F32 ? 4 : 2; }
     static constexpr bool has(int i) { return MASK >> i & 1; }
     const RowArgs &a;
     char *smem;
-    int t, slot;            // thread of the row, row slot of the block
-    uint32_t own;           // vec: the groups of this thread that lie in the row, a bit each
+    int t, slot, shift;     // thread of the row, row slot of the block, elements before a row in its first vector
+    uint32_t own;           // the columns of this thread that lie in the row, a bit each (whole vectors: a bit a group)
     __device__ __forceinline__ Rows(const RowArgs &a_, void *s) : a(a_), smem(static_cast<char *>(s)) {
         slot = threadIdx.x / a.tpr;
         t = threadIdx.x - slot * a.tpr;
+        shift = SHIFT ? (int)((blockIdx.x % (unsigned)a.period) * (unsigned)a.D & 7u) : 0;
         own = 0;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) own |= (uint32_t)((g * a.tpr + t) * 8 < a.D) << g;
+        for (int g = 0; g < NG; ++g) {
+            if (!SHIFT) own |= (uint32_t)(column(g) < a.D) << g;
+#pragma unroll
+            for (int e = 0; SHIFT && e < 8; ++e) own |= (uint32_t)(column(g) + e >= 0 && column(g) + e < a.D) << (8 * g + e);
+        }
     }
-    // where an input's rows begin in a stage (vec: NG groups of all threads, the halves of an fp32 group apart)
-    static constexpr int vec_off(int i) {
+    __device__ __forceinline__ int column(int g) const { return (g * a.tpr + t) * 8 - (SHIFT ? shift : 0); }
+    __device__ __forceinline__ bool any(int g) const { return SHIFT ? own >> (8 * g) & 0xffu : own >> g & 1; }
+    __device__ __forceinline__ bool whole(int g) const { return !SHIFT || (own >> (8 * g) & 0xffu) == 0xffu; }
+    __device__ __forceinline__ bool has_column(int g, int e) const { return SHIFT ? own >> (8 * g + e) & 1 : own >> g & 1; }
+    // the block's rows: of one remainder modulo the period
+    __device__ __forceinline__ long long first() const {
+        if (!SHIFT) return (long long)blockIdx.x * a.rpb + slot;
+        return (long long)(blockIdx.x / (unsigned)a.period * (unsigned)a.rpb + slot) * a.period + blockIdx.x % (unsigned)a.period;
+    }
+    __device__ __forceinline__ int apart() const { return SHIFT ? a.period : 1; }
+    __device__ __forceinline__ long long step() const { return (long long)gridDim.x * a.rpb; }
+    // where an input's rows begin in a stage: NG groups of all threads
+    static constexpr int bytes_before(int i) {  // of a thread
         int o = 0;
         for (int k = 0; k < i; ++k)
-            if (has(k)) o += NG * BT * 8 * elem(k);
+            if (has(k)) o += NG * 8 * elem(k);
         return o;
     }
-    __device__ __forceinline__ int rag_off(int i) const {
-        int n2 = 0, n4 = 0;
-#pragma unroll
-        for (int k = 0; k < kMaxIn; ++k)
-            if (k < i && has(k)) (elem(k) == 4 ? n4 : n2) += 1;
-        return n2 * rag_place(a.D, 2) + n4 * rag_place(a.D, 4);
-    }
+    __device__ __forceinline__ int threads() const { return (int)blockDim.x; }
+    __device__ __forceinline__ int off(int i) const { return bytes_before(i) * threads(); }
     __device__ __forceinline__ const char *at(int i, long long row) const {
         const RowIn &in = a.in[i];
-        long long e = row * in.ld;
+        long long e = row * in.ld - shift;
         if (in.heads > 1) {
             const long long token = a.rows <= 0x7fffffff ? (long long)((unsigned)row / (unsigned)in.heads) : row / in.heads;
             e = token * in.ld + (row - token * in.heads) * a.D;
@@ -70,44 +83,29 @@ struct Rows {
         return static_cast<const char *>(in.p) + e * elem(i);
     }
     template <int I>
-    __device__ __forceinline__ char *place(int stage) const {
-        if constexpr (RAG) return smem + (size_t)(stage * a.rpb + slot) * a.place + rag_off(I);
-        else return smem + stage * a.place + vec_off(I) + threadIdx.x * 16;
-    }
-    template <int I>
     __device__ __forceinline__ void fetch_one(long long row, int stage) const {
         if constexpr (has(I)) {
-            const bool in = row < a.rows;
             if (I == IN_DRES && !a.in[I].p) return;
-            char *to = place<I>(stage);
-            if constexpr (RAG) {
-                if (!in) return;
-                const char *base = static_cast<const char *>(a.in[I].p), *src0 = at(I, row), *hi = at(I, a.rows - 1) + a.D * elem(I);
-                const int sk = (int)(reinterpret_cast<uintptr_t>(src0) & 15), bytes = a.D * elem(I), pieces = (sk + bytes + 15) / 16;
-                for (int k = t; k < pieces; k += a.tpr) {
-                    const char *src = src0 - sk + k * 16;
-                    if (src >= base) {
-                        const long long left = hi - src;
-                        const int n = left < 16 ? (int)left : 16;
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(to + k * 16)), "l"(src), "r"(n) : "memory");
-                    } else {  // the piece begins before the tensor
-                        for (int b = sk; b < 16 && b - sk < bytes; b += 2)
-                            *reinterpret_cast<uint16_t *>(to + b) = *reinterpret_cast<const uint16_t *>(src + b);
-                    }
-                }
-            } else {
-                const char *src = at(I, in ? row : 0) + t * 8 * elem(I);
-                const uint32_t d = smem_u32(to);
+            constexpr bool W = elem(I) == 4;
+            const bool in = row < a.rows;
+            // fp32: two instructions a group, each over a whole run of the warp's (or, with fewer, the row's) lanes
+            const int lanes = min(a.tpr, 32), l = t & (lanes - 1);
+            const char *src = at(I, row) + (W ? (t - l) * 32 + l * 16 : t * 16);
+            const uint32_t to = smem_u32(smem) + stage * a.place + off(I) + (W ? (threadIdx.x - l) * 32 + l * 16 : threadIdx.x * 16);
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
+            for (int g = 0; g < NG; ++g) {
 #pragma unroll
-                    for (int h = 0; h < elem(I) / 2; ++h) {
-                        const int o = (g * (elem(I) / 2) + h) * BT * 16;
-                        // (no bytes, zeros: for what lies behind the row's end or the last row)
-                        const int n = in && (own >> g & 1) ? 16 : 0;
-                        const char *from = n ? src + g * a.tpr * 8 * elem(I) + h * 16 : src;
-                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(d + o), "l"(from), "r"(n) : "memory");
+                for (int h = 0; h < (W ? 2 : 1); ++h) {
+                    const char *from = src + g * a.tpr * 8 * elem(I) + (W ? h * lanes * 16 : 0);
+                    const uint32_t d = to + g * threads() * 8 * elem(I) + (W ? h * lanes * 16 : 0);
+                    // (no bytes, zeros: for what lies behind the row's end or the last row; nothing behind the tensor's end)
+                    const int c = (g * a.tpr + t - l) * 8 + h * lanes * 4 + l * 4 - shift;
+                    int n = in && (W ? c < a.D && c + 4 > 0 : any(g)) ? 16 : 0;
+                    if (SHIFT && n && row == a.rows - 1) {
+                        const long long left = static_cast<const char *>(a.in[I].p) + a.rows * a.D * elem(I) - from;
+                        n = left < 16 ? (int)(left > 0 ? left : 0) : 16;
                     }
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(d), "l"(from), "r"(n) : "memory");
                 }
             }
         }
@@ -121,82 +119,74 @@ struct Rows {
         asm volatile("cp.async.commit_group;\n" ::: "memory");
     }
     template <int I>
-    __device__ __forceinline__ void get(int stage, long long row, int g, f2 *o) const {
+    __device__ __forceinline__ void get(int stage, long long, int g, f2 *o) const {
         constexpr bool W = elem(I) == 4;
-        const char *s = place<I>(stage);
-        if constexpr (RAG) {
-            s += reinterpret_cast<uintptr_t>(at(I, row)) & 15;
-            float v[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = t + (8 * g + e) * a.tpr;
-                v[e] = row < a.rows && c < a.D ? rag_get<T, W>(s, c) : 0.f;
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = pack2(v[2 * e], v[2 * e + 1]);
+        const char *s = smem + stage * a.place + off(I) + (g * threads() + threadIdx.x) * (W ? 32 : 16);
+        const uint4 u = *reinterpret_cast<const uint4 *>(s);
+        if constexpr (W) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(s + 16);
+            o[0] = pack2(__uint_as_float(u.x), __uint_as_float(u.y)), o[1] = pack2(__uint_as_float(u.z), __uint_as_float(u.w));
+            o[2] = pack2(__uint_as_float(x.x), __uint_as_float(x.y)), o[3] = pack2(__uint_as_float(x.z), __uint_as_float(x.w));
         } else {
-            const uint4 u = *reinterpret_cast<const uint4 *>(s + g * (W ? 2 : 1) * BT * 16);
-            if constexpr (W) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(s + (2 * g + 1) * BT * 16);
-                o[0] = pack2(__uint_as_float(u.x), __uint_as_float(u.y)), o[1] = pack2(__uint_as_float(u.z), __uint_as_float(u.w));
-                o[2] = pack2(__uint_as_float(x.x), __uint_as_float(x.y)), o[3] = pack2(__uint_as_float(x.z), __uint_as_float(x.w));
-            } else {
-                o[0] = widen2<T>(u.x), o[1] = widen2<T>(u.y), o[2] = widen2<T>(u.z), o[3] = widen2<T>(u.w);
+            o[0] = widen2<T>(u.x), o[1] = widen2<T>(u.y), o[2] = widen2<T>(u.z), o[3] = widen2<T>(u.w);
+        }
+        if (!whole(g)) {  // (a neighbouring row's elements)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float v0, v1;
+                unpack2(o[e], v0, v1);
+                o[e] = pack2(has_column(g, 2 * e) ? v0 : 0.f, has_column(g, 2 * e + 1) ? v1 : 0.f);
             }
         }
     }
     // a group of an output [rows, D]
     template <bool W>
     __device__ __forceinline__ void put(void *to, long long row, int g, const f2 *v) const {
-        if (row >= a.rows) return;
-        if constexpr (RAG) {
-            float x[8];
+        if (row >= a.rows || !any(g)) return;
+        const long long i = row * a.D + column(g);
+        if (!whole(g)) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) unpack2(v[e], x[2 * e], x[2 * e + 1]);
+            for (int e = 0; e < 4; ++e) {
+                float x[2];
+                unpack2(v[e], x[0], x[1]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = t + (8 * g + e) * a.tpr;
-                if (c < a.D) rag_put<T, W>(to, row * a.D + c, x[e]);
+                for (int k = 0; k < 2; ++k)
+                    if (has_column(g, 2 * e + k)) {
+                        if (W) static_cast<float *>(to)[i + 2 * e + k] = x[k];
+                        else static_cast<T *>(to)[i + 2 * e + k] = Elt<T>::from_f(x[k]);
+                    }
+            }
+        } else if constexpr (W) {
+            float *q = static_cast<float *>(to) + i;
+            if (a.wide) {  // a whole sector a lane
+                asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};\n" ::"l"(q), "l"(v[0]), "l"(v[1]), "l"(v[2]), "l"(v[3]) : "memory");
+            } else {
+                reinterpret_cast<ulonglong2 *>(q)[0] = make_ulonglong2(v[0], v[1]);
+                reinterpret_cast<ulonglong2 *>(q)[1] = make_ulonglong2(v[2], v[3]);
             }
         } else {
-            const int c = (g * a.tpr + t) * 8;
-            if (!(own >> g & 1)) return;
-            if constexpr (W) {
-                ulonglong2 *q = reinterpret_cast<ulonglong2 *>(static_cast<float *>(to) + row * a.D + c);
-                q[0] = make_ulonglong2(v[0], v[1]);
-                q[1] = make_ulonglong2(v[2], v[3]);
-            } else {
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(to) + row * a.D + c) =
-                    make_uint4(narrow2<T>(v[0]), narrow2<T>(v[1]), narrow2<T>(v[2]), narrow2<T>(v[3]));
-            }
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(to) + i) = make_uint4(narrow2<T>(v[0]), narrow2<T>(v[1]), narrow2<T>(v[2]), narrow2<T>(v[3]));
         }
     }
     // a group of a weight
     __device__ __forceinline__ void weight(const void *w, int g, f2 *o) const {
-        float x[8];
-        if constexpr (!RAG) {
-            const int c = (g * a.tpr + t) * 8;
-            if (c < a.D && a.w_f32) {
-                const ulonglong2 *q = reinterpret_cast<const ulonglong2 *>(static_cast<const float *>(w) + c);
-                const ulonglong2 u = q[0], v = q[1];
-                o[0] = u.x, o[1] = u.y, o[2] = v.x, o[3] = v.y;
-                return;
-            }
-            if (c < a.D) {
-                const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(w) + c);
-                o[0] = widen2<T>(u.x), o[1] = widen2<T>(u.y), o[2] = widen2<T>(u.z), o[3] = widen2<T>(u.w);
-                return;
-            }
+        const int c = column(g);
+        if (SHIFT) {
+            float x[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = 0ull;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = t + (8 * g + e) * a.tpr;
-                x[e] = c < a.D ? load_gate<T>(w, c, a.w_f32) : 0.f;
-            }
+            for (int e = 0; e < 8; ++e) x[e] = has_column(g, e) ? load_gate<T>(w, c + e, a.w_f32) : 0.f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[e] = pack2(x[2 * e], x[2 * e + 1]);
+        } else if (!any(g)) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] = 0ull;
+        } else if (a.w_f32) {
+            const ulonglong2 *q = reinterpret_cast<const ulonglong2 *>(static_cast<const float *>(w) + c);
+            const ulonglong2 u = q[0], v = q[1];
+            o[0] = u.x, o[1] = u.y, o[2] = v.x, o[3] = v.y;
+        } else {
+            const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(w) + c);
+            o[0] = widen2<T>(u.x), o[1] = widen2<T>(u.y), o[2] = widen2<T>(u.z), o[3] = widen2<T>(u.w);
         }
     }
     // this thread's sums over its rows, added up over the block's row slots, as `which` of the block's partial rows
@@ -204,18 +194,16 @@ struct Rows {
         float *out = a.part + ((long long)blockIdx.x * count + which) * a.D;
         float *slots = reinterpret_cast<float *>(smem);
         __syncthreads();  // (the rows, or the sums before these, are read no more)
+        float *to = a.rpb == 1 ? out : slots + slot * a.D;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            float x[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) unpack2(v[4 * g + e], x[2 * e], x[2 * e + 1]);
+            for (int e = 0; e < 4; ++e) {
+                float x[2];
+                unpack2(v[4 * g + e], x[0], x[1]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = RAG ? t + (8 * g + e) * a.tpr : (g * a.tpr + t) * 8 + e;
-                if (c < a.D) {
-                    if (a.rpb == 1) out[c] = x[e];
-                    else slots[slot * a.D + c] = x[e];
-                }
+                for (int k = 0; k < 2; ++k)
+                    if (has_column(g, 2 * e + k)) to[column(g) + 2 * e + k] = x[k];
             }
         }
         if (a.rpb == 1) return;
@@ -276,27 +264,23 @@ __device__ __forceinline__ void gate_of_pairs(int act, const f2 *g, f2 *f, f2 *d
     }
 }
 
-// Waits for this row's copies; ragged rows were brought by all threads of the row.
-template <bool RAG>
-__device__ __forceinline__ void arrive(bool ahead) {
-    if (ahead) asm volatile("cp.async.wait_group 1;\n" ::: "memory");
-    else asm volatile("cp.async.wait_group 0;\n" ::: "memory");
-    if (RAG) __syncthreads();
-}
-
-// Loops over the block's rows: body(row, stage, parity) with the row's elements at hand.
-template <bool RAG, typename R, typename F>
+// Loops over the block's rows: body(row, stage, parity) with the row's elements at hand.  (All threads of a block make the
+// same number of rounds: its last slots' rows may lie past the end.)
+template <typename R, typename F>
 __device__ __forceinline__ void walk(const R &rows, const RowArgs &a, F &&body) {
-    const long long step = (long long)gridDim.x * a.rpb;
-    long long row = (long long)blockIdx.x * a.rpb + rows.slot;
     const bool two = a.stages == 2;
+    long long row = rows.first();
+    const long long step = rows.step();
+    long long lead = row - (long long)rows.slot * rows.apart();  // the first slot's row
     if (two) rows.fetch(row, 0);
     int parity = 0;
-    for (long long r0 = (long long)blockIdx.x * a.rpb; r0 < a.rows; r0 += step, row += step, parity ^= 1) {
+    for (; lead < a.rows; lead += step, row += step, parity ^= 1) {
         const int stage = two ? parity : 0;
-        if (RAG) __syncthreads();  // (the place that is filled now has been read)
+        __syncwarp();  // (the place that is filled now has been read)
         rows.fetch(two ? row + step : row, two ? stage ^ 1 : 0);
-        arrive<RAG>(two);
+        if (two) asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+        else asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+        __syncwarp();  // (what this warp's lanes copied for one another)
         body(row, stage, parity);
     }
     asm volatile("cp.async.wait_group 0;\n" ::: "memory");
@@ -304,16 +288,16 @@ __device__ __forceinline__ void walk(const R &rows, const RowArgs &a, F &&body) 
 
 // ---------------------------------------------------------------- gated norm
 
-template <typename T, int NG, int BT, bool RAG>
-__global__ void __launch_bounds__(BT, BT > 288 ? 1 : 3) gated_fwd_kernel(const __grid_constant__ RowArgs a) {
+template <typename T, int NG, int BT, bool SHIFT>
+__global__ void __launch_bounds__(BT, BT > 320 ? 1 : BT > 256 ? 2 : 3) gated_fwd_kernel(const __grid_constant__ RowArgs a) {
     extern __shared__ __align__(16) char s_rows[];
     __shared__ float red[2 * 16];
-    const Rows<T, NG, BT, RAG, false, 1u << IN_X | 1u << IN_GATE> rows(a, s_rows);
+    const Rows<T, NG, BT, SHIFT, false, 1u << IN_X | 1u << IN_GATE> rows(a, s_rows);
     f2 w[4 * NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) rows.weight(a.w, g, w + 4 * g);
     const float inv_d = 1.0f / (float)a.D;
-    walk<RAG>(rows, a, [&](long long row, int stage, int parity) {
+    walk(rows, a, [&](long long row, int stage, int parity) {
         f2 x[4 * NG], ss = 0ull;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -336,18 +320,18 @@ __global__ void __launch_bounds__(BT, BT > 288 ? 1 : 3) gated_fwd_kernel(const _
     });
 }
 
-template <typename T, int NG, int BT, bool RAG>
-__global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) gated_bwd_kernel(const __grid_constant__ RowArgs a) {
+template <typename T, int NG, int BT, bool SHIFT>
+__global__ void __launch_bounds__(BT, BT > 320 ? 1 : 2) gated_bwd_kernel(const __grid_constant__ RowArgs a) {
     extern __shared__ __align__(16) char s_rows[];
     __shared__ float red[2 * 16 * 2];
-    const Rows<T, NG, BT, RAG, false, 1u << IN_X | 1u << IN_GATE | 1u << IN_DY> rows(a, s_rows);
+    const Rows<T, NG, BT, SHIFT, false, 1u << IN_X | 1u << IN_GATE | 1u << IN_DY> rows(a, s_rows);
     f2 w[4 * NG], dw[4 * NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) rows.weight(a.w, g, w + 4 * g);
 #pragma unroll
     for (int i = 0; i < 4 * NG; ++i) dw[i] = 0ull;
     const float inv_d = 1.0f / (float)a.D;
-    walk<RAG>(rows, a, [&](long long row, int stage, int parity) {
+    walk(rows, a, [&](long long row, int stage, int parity) {
         f2 dn[4 * NG], ss = 0ull, sd = 0ull;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -392,12 +376,14 @@ __global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) gated_bwd_kernel(const _
 
 // ---------------------------------------------------------------- block norm
 
-template <typename T, int NG, int BT, bool RAG, bool F32, bool GATE>
-__global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) block_fwd_kernel(const __grid_constant__ RowArgs a) {
-    constexpr bool HOLD = NG <= 2;  // weights in registers
+template <typename T, int NG, int BT, bool SHIFT, bool F32, bool GATE>
+__global__ void __launch_bounds__(BT, BT > 320 ? 1 : BT > 256 || SHIFT ? 2 : 3) block_fwd_kernel(const __grid_constant__ RowArgs a) {
+    // Weights come from the L1 cache row by row: held in registers they cost the third block an SM (8192 x 4096 bf16: 71 us with,
+    // 64 without).  Shifted rows would read them element by element, and hold them.
+    constexpr bool HOLD = SHIFT && NG <= 2;
     extern __shared__ __align__(16) char s_rows[];
     __shared__ float red1[2 * 16], red2[2 * 16];
-    const Rows<T, NG, BT, RAG, F32, 1u << IN_X | (GATE ? 1u << IN_GATE : 0u) | 1u << IN_RES> rows(a, s_rows);
+    const Rows<T, NG, BT, SHIFT, F32, 1u << IN_X | (GATE ? 1u << IN_GATE : 0u) | 1u << IN_RES> rows(a, s_rows);
     f2 w[HOLD ? 4 * NG : 4], pw[HOLD ? 4 * NG : 4];
     if (HOLD) {
 #pragma unroll
@@ -407,7 +393,7 @@ __global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) block_fwd_kernel(const _
         }
     }
     const float inv_d = 1.0f / (float)a.D;
-    walk<RAG>(rows, a, [&](long long row, int stage, int parity) {
+    walk(rows, a, [&](long long row, int stage, int parity) {
         f2 h[4 * NG];
         f2 scale = both(a.rscale);
 #pragma unroll
@@ -457,12 +443,12 @@ __global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) block_fwd_kernel(const _
     });
 }
 
-template <typename T, int NG, int BT, bool RAG, bool F32, bool GATE>
-__global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) block_bwd_kernel(const __grid_constant__ RowArgs a) {
+template <typename T, int NG, int BT, bool SHIFT, bool F32, bool GATE>
+__global__ void __launch_bounds__(BT, BT > 320 ? 1 : 2) block_bwd_kernel(const __grid_constant__ RowArgs a) {
     constexpr bool HOLD = NG <= 2;
     extern __shared__ __align__(16) char s_rows[];
     __shared__ float red1[2 * 16 * 3], red2[2 * 16];
-    const Rows<T, NG, BT, RAG, F32, 1u << IN_X | (GATE ? 1u << IN_GATE : 0u) | 1u << IN_DY | 1u << IN_H | 1u << IN_DRES> rows(a, s_rows);
+    const Rows<T, NG, BT, SHIFT, F32, 1u << IN_X | (GATE ? 1u << IN_GATE : 0u) | 1u << IN_DY | 1u << IN_H | 1u << IN_DRES> rows(a, s_rows);
     f2 w[HOLD ? 4 * NG : 4], pw[HOLD ? 4 * NG : 4], dw[4 * NG], dpw[4 * NG];
     if (HOLD) {
 #pragma unroll
@@ -474,7 +460,7 @@ __global__ void __launch_bounds__(BT, BT > 288 ? 1 : 2) block_bwd_kernel(const _
 #pragma unroll
     for (int i = 0; i < 4 * NG; ++i) dw[i] = dpw[i] = 0ull;
     const float inv_d = 1.0f / (float)a.D;
-    walk<RAG>(rows, a, [&](long long row, int stage, int parity) {
+    walk(rows, a, [&](long long row, int stage, int parity) {
         f2 sx = 0ull, sh = 0ull, sd = 0ull;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
@@ -564,17 +550,17 @@ cudaError_t launch_rows(K k, const RowArgs &a, const RowForm &f, cudaStream_t st
     if (e != cudaSuccess) return e;
     return launch_plain(k, dim3(f.blocks), dim3(f.s.threads), f.smem, st, a);
 }
-// (ragged blocks take any multiple of 32 up to the bound; vec blocks are the bound itself)
 #define GDR_ROW_FORMS(KERNEL, ...)                                                                                      \
     do {                                                                                                                \
-        if (f.vec) {                                                                                                    \
-            if (f.s.nv == 4) return launch_rows(KERNEL<T, 4, 512, false __VA_ARGS__>, a, f, st);                        \
-            return f.s.threads == 256 ? launch_rows(KERNEL<T, 2, 256, false __VA_ARGS__>, a, f, st)                     \
-                                      : launch_rows(KERNEL<T, 2, 512, false __VA_ARGS__>, a, f, st);                    \
+        if (f.shift) {                                                                                                  \
+            if (f.s.nv == 4) return launch_rows(KERNEL<T, 4, 512, true __VA_ARGS__>, a, f, st);                         \
+            return f.s.threads <= 256   ? launch_rows(KERNEL<T, 2, 256, true __VA_ARGS__>, a, f, st)                    \
+                   : f.s.threads <= 320 ? launch_rows(KERNEL<T, 2, 320, true __VA_ARGS__>, a, f, st)                    \
+                                        : launch_rows(KERNEL<T, 2, 512, true __VA_ARGS__>, a, f, st);                   \
         }                                                                                                               \
-        if (f.s.nv == 4) return launch_rows(KERNEL<T, 4, 512, true __VA_ARGS__>, a, f, st);                             \
-        return f.s.threads <= 288 ? launch_rows(KERNEL<T, 2, 288, true __VA_ARGS__>, a, f, st)                          \
-                                  : launch_rows(KERNEL<T, 2, 512, true __VA_ARGS__>, a, f, st);                         \
+        if (f.s.nv == 4) return launch_rows(KERNEL<T, 4, 512, false __VA_ARGS__>, a, f, st);                            \
+        return f.s.threads <= 256 ? launch_rows(KERNEL<T, 2, 256, false __VA_ARGS__>, a, f, st)                         \
+                                  : launch_rows(KERNEL<T, 2, 512, false __VA_ARGS__>, a, f, st);                        \
     } while (0)
 
 }  // namespace

@@ -27,7 +27,8 @@ struct RowArgs {
     float *part;                  // [blocks][D or 2 D]: dw, then dpw
     long long rows;
     int D, tpr, rpb, stages, act;
-    int place;                    // bytes of a stage (vec), or of a row (ragged)
+    int place, period;            // bytes of a stage; rows after which the first element lies as far into a vector again
+    bool wide;                    // fp32 outputs begin on 32-byte boundaries
     bool w_f32;
     float eps, rscale;
 };
@@ -37,7 +38,7 @@ enum { IN_X = 0, IN_GATE = 1, IN_DY = 2, IN_H = 3, IN_DRES = 4, IN_RES = IN_H };
 
 struct RowForm {
     norm::NormShape s;
-    bool vec, f32, gate;  // whole vectors; an fp32 residual stream; a gate
+    bool shift, f32, gate;  // rows that begin inside a vector; an fp32 residual stream; a gate
     int blocks;
     size_t smem;
 };

@@ -5,63 +5,65 @@ namespace gdr {
 namespace rownorm {
 namespace {
 
-// A pointer that is given is aligned to its elements; `vec` is cleared unless all allow 16-byte accesses.
-bool ptr_ok(const void *p, size_t elem, bool *vec) {
-    if (!p) return true;
-    if (!aligned_to(p, elem)) return false;
-    if (!aligned16(p)) *vec = false;
-    return true;
+// How the rows are spread, staged and walked.  A block keeps two rows' places (one on its way while the other is worked on)
+// where both fit; the grid is what is resident at once.  Shifted rows: the same number of blocks for each remainder.
+// (blocks of 256 threads an SM by registers: two, but three of the gated norm's forward and of whole-vector forwards)
+int period_of(int D) {
+    int p = 8;
+    while (p > 1 && D % 2 == 0) p /= 2, D /= 2;
+    return D % 8 == 0 ? 1 : p;
 }
-
-// Bytes of a stage of whole vectors, or of one ragged row.
-size_t place_of(const RowArgs &a, const norm::NormShape &s, bool vec) {
-    size_t n = 0;
-    for (const RowIn &in : a.in)
-        if (in.p) n += vec ? (size_t)s.nv * s.threads * 8 * in.elem : (size_t)((a.D * in.elem + 14 + 15) / 16 * 16);
-    return n;
+// A row's threads: with 16 columns each (32 for the widest rows) the power of two up to 32 that covers it, or a multiple of 32;
+// short rows share a block of at most 256.
+norm::NormShape shape_of(int D) {
+    norm::NormShape s = {};
+    const int vectors = (D % 8 ? D + 7 : D) / 8 + (D % 8 && (D + 7) % 8 ? 1 : 0);
+    s.nv = vectors <= 1024 ? 2 : 4;
+    const int need = (vectors + s.nv - 1) / s.nv;
+    s.tpr = 8;
+    while (s.tpr < 32 && s.tpr < need) s.tpr *= 2;
+    if (need > 32) s.tpr = (need + 31) / 32 * 32;
+    s.rpb = s.tpr < 256 ? 256 / s.tpr : 1;
+    s.threads = s.tpr * s.rpb;
+    return s;
 }
-
-// How the rows are spread, staged and walked.  A block keeps two rows' places (one on its way while the other is worked
-// on) where that leaves room for another block beside it, or its rows do not fit twice anyway; the grid is what is
-// resident at once.  (8192 x 4096, block norm's backward with an fp32 stream, 57 KB a row.)
-RowForm form_of(const RowArgs &a, long long rows, bool vec, bool bwd) {
+RowForm form_of(RowArgs *a, bool bwd, bool gated) {
     RowForm f = {};
-    f.vec = vec;
-    f.s = norm::norm_shape(a.D, !vec);
-    const size_t place = place_of(a, f.s, vec) * (vec ? 1 : f.s.rpb);
+    f.shift = a->D % 8 != 0;
+    f.s = shape_of(a->D);
+    size_t place = 0;
+    for (const RowIn &in : a->in)
+        if (in.p) place += (size_t)f.s.nv * f.s.threads * 8 * in.elem;
     const size_t all = 227 * 1024;
-    const int most = f.s.threads > 288 ? 1 : bwd ? 2 : 3;  // (by registers, see the kernels' bounds)
+    const int most = f.s.threads > (f.shift ? 320 : 256) ? 1 : f.s.threads > 256 || bwd || (f.shift && !gated) ? 2 : 3;
     auto resident = [&](size_t smem) {
         const int n = (int)(all / (smem + 2048));
         return n < most ? n : most;
     };
-    const int stages = resident(2 * place) >= 1 ? 2 : 1;
-    f.smem = stages * place;
-    const long long need = (rows + f.s.rpb - 1) / f.s.rpb, at_once = (long long)kSMs * resident(f.smem);
+    a->stages = resident(2 * place) >= 1 ? 2 : 1;
+    f.smem = a->stages * place;
+    a->tpr = f.s.tpr, a->rpb = f.s.rpb, a->place = (int)place, a->period = period_of(a->D);
+    const long long each = (a->rows + a->period - 1) / a->period, need = (each + f.s.rpb - 1) / f.s.rpb * a->period;
+    const long long at_once = (long long)kSMs * resident(f.smem) / a->period * a->period;
     f.blocks = (int)(need < at_once ? need : at_once);
     return f;
 }
-void apply(RowArgs *a, const RowForm &f) {
-    a->tpr = f.s.tpr, a->rpb = f.s.rpb;
-    a->place = (int)place_of(*a, f.s, f.vec);
-    a->stages = f.smem >= 2 * (size_t)a->place * (f.vec ? 1 : f.s.rpb) ? 2 : 1;
+
+// Partial rows of the parameters' gradients: at most this many blocks.
+size_t parts_bytes(long long rows, int D, int outs) {
+    const norm::NormShape s = shape_of(D);
+    const int period = period_of(D);
+    const long long each = (rows + period - 1) / period, need = (each + s.rpb - 1) / s.rpb * period, at_once = (long long)kSMs * (s.threads > (D % 8 ? 320 : 256) ? 1 : 2);
+    return round_up((size_t)(need < at_once ? need : at_once) * outs * D * sizeof(float), 256);
 }
 
-// Partial rows of the parameters' gradients: whichever form a call takes has at most this many blocks.
-size_t parts_bytes(long long rows, int D, int outs) {
-    size_t most = 0;
-    for (bool rag : {false, true}) {
-        const norm::NormShape s = norm::norm_shape(D, rag);
-        const long long need = (rows + s.rpb - 1) / s.rpb, at_once = (long long)kSMs * (s.threads > 288 ? 1 : 2);
-        const size_t n = (size_t)(need < at_once ? need : at_once);
-        most = n > most ? n : most;
-    }
-    return round_up(most * outs * D * sizeof(float), 256);
-}
+// Rows of whole vectors, or tensors without gaps.
+bool rows_ok(int D, int64_t ld, int64_t wide) { return D % 8 == 0 ? ld % 8 == 0 : ld == wide; }
+bool width_ok(int D) { return D >= 1 && D <= (D % 8 ? GDR_NORM_MAX_D - 8 : GDR_NORM_MAX_D); }
 
 gdr_status check_gated(const gdr_gated_norm_problem *p) {
     if (!p) return GDR_ERR_NULL;
-    if (p->tokens < 0 || p->heads < 1 || p->D < 1 || p->D > GDR_NORM_MAX_D || p->tokens > ((int64_t)1 << 40) / p->heads) return GDR_ERR_SHAPE;
+    if (p->tokens < 0 || p->heads < 1 || !width_ok(p->D) || p->tokens > ((int64_t)1 << 40) / p->heads) return GDR_ERR_SHAPE;
     const int64_t wide = (int64_t)p->heads * p->D;
     if (p->x_ld < wide || p->gate_ld < wide) return GDR_ERR_SHAPE;
     if (!is_half(p->dtype) || (p->weight_dtype != p->dtype && p->weight_dtype != GDR_FP32)) return GDR_ERR_DTYPE;
@@ -70,7 +72,7 @@ gdr_status check_gated(const gdr_gated_norm_problem *p) {
 }
 gdr_status check_block(const gdr_block_norm_problem *p) {
     if (!p) return GDR_ERR_NULL;
-    if (p->rows < 0 || p->rows > ((int64_t)1 << 40) || p->D < 1 || p->D > GDR_NORM_MAX_D || p->x_ld < p->D || p->gate_ld < p->D) return GDR_ERR_SHAPE;
+    if (p->rows < 0 || p->rows > ((int64_t)1 << 40) || !width_ok(p->D) || p->x_ld < p->D || p->gate_ld < p->D) return GDR_ERR_SHAPE;
     if (!is_half(p->dtype) || (p->weight_dtype != p->dtype && p->weight_dtype != GDR_FP32) ||
         (p->residual_dtype != p->dtype && p->residual_dtype != GDR_FP32))
         return GDR_ERR_DTYPE;
@@ -100,8 +102,9 @@ gdr_status gdr_gated_norm_fwd(const gdr_gated_norm_problem *p, const void *x, co
     if (st != GDR_OK) return st;
     if (p->tokens == 0) return GDR_OK;
     if (!x || !gate || !weight || !y) return GDR_ERR_NULL;
-    bool vec = p->D % 8 == 0 && p->x_ld % 8 == 0 && p->gate_ld % 8 == 0;
-    if (!ptr_ok(x, 2, &vec) || !ptr_ok(gate, 2, &vec) || !ptr_ok(y, 2, &vec) || !ptr_ok(weight, esize(p->weight_dtype), &vec)) return GDR_ERR_ALIGN;
+    const int64_t row = (int64_t)p->heads * p->D;
+    if (!aligned16(x) || !aligned16(gate) || !aligned16(y) || !aligned16(weight) || !rows_ok(p->D, p->x_ld, row) || !rows_ok(p->D, p->gate_ld, row))
+        return GDR_ERR_ALIGN;
     const size_t wide = (size_t)p->heads * p->D * 2;
     if (over(y, p->tokens, wide, x, p->x_ld * 2) || over(y, p->tokens, wide, gate, p->gate_ld * 2)) return GDR_ERR_UNSUPPORTED;
     unsigned *err = nullptr;
@@ -110,8 +113,7 @@ gdr_status gdr_gated_norm_fwd(const gdr_gated_norm_problem *p, const void *x, co
     a.in[IN_X] = heads_in(x, p->x_ld, p->heads, p->D), a.in[IN_GATE] = heads_in(gate, p->gate_ld, p->heads, p->D);
     a.w = weight, a.y = y, a.rows = p->tokens * p->heads, a.D = p->D, a.eps = p->eps;
     a.w_f32 = p->weight_dtype == GDR_FP32, a.act = act_of(p->gate_act);
-    const RowForm f = form_of(a, a.rows, vec, false);
-    apply(&a, f);
+    RowForm f = form_of(&a, false, true);
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     return timed(K_GATED_FWD, cs, [&] { return p->dtype == GDR_BF16 ? gated_fwd_bf16(a, f, cs) : gated_fwd_fp16(a, f, cs); });
 }
@@ -130,9 +132,9 @@ gdr_status gdr_gated_norm_bwd(const gdr_gated_norm_problem *p, const void *x, co
     gdr_status st = gdr_gated_norm_bwd_workspace_size(p, &need);
     if (st != GDR_OK) return st;
     if (!weight || !dweight || (p->tokens && (!x || !gate || !dy || !dx || !dgate))) return GDR_ERR_NULL;
-    bool vec = p->D % 8 == 0 && p->x_ld % 8 == 0 && p->gate_ld % 8 == 0, any = true;
-    if (!ptr_ok(x, 2, &vec) || !ptr_ok(gate, 2, &vec) || !ptr_ok(dy, 2, &vec) || !ptr_ok(dx, 2, &vec) || !ptr_ok(dgate, 2, &vec) ||
-        !ptr_ok(weight, esize(p->weight_dtype), &vec) || !ptr_ok(dweight, esize(p->weight_dtype), &any))
+    const int64_t row = (int64_t)p->heads * p->D;
+    if (!aligned16(x) || !aligned16(gate) || !aligned16(dy) || !aligned16(dx) || !aligned16(dgate) || !aligned16(weight) ||
+        !aligned_to(dweight, esize(p->weight_dtype)) || !rows_ok(p->D, p->x_ld, row) || !rows_ok(p->D, p->gate_ld, row))
         return GDR_ERR_ALIGN;
     const size_t wide = (size_t)p->heads * p->D * 2;
     for (const void *o : {dx, dgate})
@@ -149,8 +151,7 @@ gdr_status gdr_gated_norm_bwd(const gdr_gated_norm_problem *p, const void *x, co
     a.w = weight, a.dx = dx, a.dgate = dgate, a.rows = p->tokens * p->heads, a.D = p->D, a.eps = p->eps;
     a.part = static_cast<float *>(workspace);
     a.w_f32 = p->weight_dtype == GDR_FP32, a.act = act_of(p->gate_act);
-    const RowForm f = form_of(a, a.rows, vec, true);
-    apply(&a, f);
+    RowForm f = form_of(&a, true, true);
     st = timed(K_GATED_BWD, cs, [&] { return p->dtype == GDR_BF16 ? gated_bwd_bf16(a, f, cs) : gated_bwd_fp16(a, f, cs); });
     if (st != GDR_OK) return st;
     return timed(K_REDUCE, cs, [&] {
@@ -165,10 +166,9 @@ gdr_status gdr_block_norm_fwd(const gdr_block_norm_problem *p, const void *x, co
     if (st != GDR_OK) return st;
     if (p->rows == 0) return GDR_OK;
     if (!x || !residual || !weight || !y || !residual_out) return GDR_ERR_NULL;
-    const size_t rs = esize(p->residual_dtype), ws = esize(p->weight_dtype), n = (size_t)p->rows, D = p->D;
-    bool vec = p->D % 8 == 0 && p->x_ld % 8 == 0 && p->gate_ld % 8 == 0;
-    if (!ptr_ok(x, 2, &vec) || !ptr_ok(residual, rs, &vec) || !ptr_ok(weight, ws, &vec) || !ptr_ok(post_weight, ws, &vec) ||
-        !ptr_ok(gate, 2, &vec) || !ptr_ok(y, 2, &vec) || !ptr_ok(residual_out, rs, &vec))
+    const size_t rs = esize(p->residual_dtype), n = (size_t)p->rows, D = p->D;
+    if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(post_weight) || !aligned16(gate) || !aligned16(y) ||
+        !aligned16(residual_out) || !rows_ok(p->D, p->x_ld, p->D) || (gate && !rows_ok(p->D, p->gate_ld, p->D)))
         return GDR_ERR_ALIGN;
     // (residual_out may be the residual itself: a thread writes what only it has read; not another overlap of the two)
     if (over(y, n, 2 * D, x, p->x_ld * 2) || over(y, n, 2 * D, gate, p->gate_ld * 2) || touches(y, n * 2 * D, residual, 1, n * rs * D, n * rs * D) ||
@@ -183,9 +183,9 @@ gdr_status gdr_block_norm_fwd(const gdr_block_norm_problem *p, const void *x, co
     if (gate) a.in[IN_GATE] = {gate, p->gate_ld, 1, 2};
     a.w = weight, a.pw = post_weight, a.y = y, a.res_out = residual_out, a.rows = p->rows, a.D = p->D;
     a.eps = p->eps, a.rscale = p->residual_scale, a.w_f32 = p->weight_dtype == GDR_FP32, a.act = gate ? act_of(p->gate_act) : ACT_NONE;
-    RowForm f = form_of(a, a.rows, vec, false);
+    RowForm f = form_of(&a, false, false);
     f.f32 = p->residual_dtype == GDR_FP32, f.gate = gate != nullptr;
-    apply(&a, f);
+    a.wide = aligned_to(residual_out, 32);
     const cudaStream_t cs = static_cast<cudaStream_t>(stream);
     return timed(K_BLOCK_FWD, cs, [&] { return p->dtype == GDR_BF16 ? block_fwd_bf16(a, f, cs) : block_fwd_fp16(a, f, cs); });
 }
@@ -207,10 +207,9 @@ gdr_status gdr_block_norm_bwd(const gdr_block_norm_problem *p, const void *x, co
     if (!weight || !dweight || ((post_weight != nullptr) != (dpost_weight != nullptr))) return GDR_ERR_NULL;
     if (p->rows && (!x || !h || !dy || !dx || !dresidual_in || ((gate != nullptr) != (dgate != nullptr)))) return GDR_ERR_NULL;
     const size_t rs = esize(p->residual_dtype), ws = esize(p->weight_dtype), n = (size_t)p->rows, D = p->D;
-    bool vec = p->D % 8 == 0 && p->x_ld % 8 == 0 && p->gate_ld % 8 == 0, any = true;
-    if (!ptr_ok(x, 2, &vec) || !ptr_ok(h, rs, &vec) || !ptr_ok(weight, ws, &vec) || !ptr_ok(post_weight, ws, &vec) || !ptr_ok(gate, 2, &vec) ||
-        !ptr_ok(dy, 2, &vec) || !ptr_ok(dresidual, rs, &vec) || !ptr_ok(dx, 2, &vec) || !ptr_ok(dresidual_in, rs, &vec) ||
-        !ptr_ok(dgate, 2, &vec) || !ptr_ok(dweight, ws, &any) || !ptr_ok(dpost_weight, ws, &any))
+    if (!aligned16(x) || !aligned16(h) || !aligned16(weight) || !aligned16(post_weight) || !aligned16(gate) || !aligned16(dy) ||
+        !aligned16(dresidual) || !aligned16(dx) || !aligned16(dresidual_in) || !aligned16(dgate) || !aligned_to(dweight, ws) ||
+        !aligned_to(dpost_weight, ws) || !rows_ok(p->D, p->x_ld, p->D) || (gate && !rows_ok(p->D, p->gate_ld, p->D)))
         return GDR_ERR_ALIGN;
     for (const void *o : {(const void *)dx, (const void *)dresidual_in, (const void *)dgate}) {
         const size_t w = (o == dresidual_in ? rs : 2) * D;
@@ -234,9 +233,9 @@ gdr_status gdr_block_norm_bwd(const gdr_block_norm_problem *p, const void *x, co
     a.w = weight, a.pw = post_weight, a.dx = dx, a.dres = dresidual_in, a.dgate = dgate, a.rows = p->rows, a.D = p->D;
     a.part = static_cast<float *>(workspace);
     a.eps = p->eps, a.rscale = p->residual_scale, a.w_f32 = p->weight_dtype == GDR_FP32, a.act = gate ? act_of(p->gate_act) : ACT_NONE;
-    RowForm f = form_of(a, a.rows, vec, true);
+    RowForm f = form_of(&a, true, false);
     f.f32 = p->residual_dtype == GDR_FP32, f.gate = gate != nullptr;
-    apply(&a, f);
+    a.wide = aligned_to(dresidual_in, 32);
     st = timed(K_BLOCK_BWD, cs, [&] { return p->dtype == GDR_BF16 ? block_bwd_bf16(a, f, cs) : block_bwd_fp16(a, f, cs); });
     if (st != GDR_OK) return st;
     return timed(K_REDUCE, cs, [&] {
