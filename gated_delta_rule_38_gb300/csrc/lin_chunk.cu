@@ -368,8 +368,8 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
     auto make_keys = [&](int c, int L, int i0, int i1) {
         const int row = (warp & 3) * 32 + lane;
         const uint32_t kt = sb + slot_of(c, KI) * TILE, lo = sb + (STATES && (c & 1) ? S_ST : S_LO);
-        const float f = w.s_kv * ex2((float)(rev ? row + 1 : L - 1 - row) * lg);
         const bool in = row < L;
+        const float f = in ? w.s_kv * ex2((float)(rev ? row + 1 : L - 1 - row) * lg) : 0.f;  // (behind the end it could be infinite)
 #pragma unroll 1
         for (int i = i0; i < i1; i += 2) {
             uint4 u[2];
