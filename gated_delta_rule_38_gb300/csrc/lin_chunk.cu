@@ -2,7 +2,7 @@
 //
 //   S_t = lambda S_{t-1} + k_t v_t^T,  o_t = scale S_t^T q_t
 //   a chunk of L tokens r, s from the state S before it:
-//     P_rs = lambda^(r-s) q_r . k_s  (s <= r);   o = scale (P V + diag(lambda^(r+1)) Q S)
+//     P_rs = scale lambda^(r-s) q_r . k_s  (s <= r);   o = P V + diag(scale lambda^(r+1)) Q S
 //     S <- lambda^L S + (diag(lambda^(L-1-s)) K)^T V
 //
 // The gradients are walks of the same form: dq = scale x the walk (do, v, k) from the transposed states, and backwards in
@@ -54,7 +54,7 @@ constexpr uint32_t S_BAR = S_ST + TILE;
 constexpr uint32_t B_FULL = S_BAR, B_EMPTY = S_BAR + 8 * RING, B_QK = B_EMPTY + 8 * RING, B_S = B_QK + 8, B_P = B_S + 8,
                    B_PV = B_P + 8, B_K = B_PV + 8, B_DS = B_K + 16, B_DONE = B_DS + 16, S_SLOT = B_DONE + 8, S_FLAG = S_SLOT + 4;
 constexpr uint32_t S_LAM = S_FLAG + 8;            // lambda^128 as two fp32 numbers
-// decays of up to 31 tokens: COL[c] = lambda^(31-c) (rev: lambda^c); DIAG[31 + row - key] = s_kv lambda^|row - key| where
+// decays of up to 31 tokens: COL[c] = lambda^(31-c) (rev: lambda^c); DIAG[31 + row - key] = s_kv s_out lambda^|row - key| where
 // the row sees the key, else 0
 constexpr uint32_t S_COL = (S_LAM + 8 + 15) / 16 * 16, S_DIAG = S_COL + 128;
 constexpr uint32_t S_BYTES = S_DIAG + 256 + 1024;
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
     if (tid >= 64 && tid < 96) reinterpret_cast<float *>(smem + S_COL)[lane] = ex2((float)(rev ? lane : 31 - lane) * lg);
     if (tid >= 96 && tid < 160) {
         const int d = rev ? 31 - (tid - 96) : tid - 96 - 31;
-        reinterpret_cast<float *>(smem + S_DIAG)[tid - 96] = d >= 0 ? w.s_kv * ex2((float)d * lg) : 0.f;
+        reinterpret_cast<float *>(smem + S_DIAG)[tid - 96] = d >= 0 ? w.s_kv * w.s_out * ex2((float)d * lg) : 0.f;
     }
     if (warp == NS + NK + 1) umma::alloc(sb + S_SLOT, 512);
     umma::fence_before();
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
         const int q4 = warp & 3, blk = rev ? q4 + dist : q4 - dist;
         if (blk < 0 || blk > 3) return;
         const uint32_t at = tmem + ((uint32_t)(q4 * 32) << 16) + T_QK + 32 * blk;
-        const f2 rf = both(w.s_kv * ex2((float)(32 * dist + (rev ? -lane : lane - 31)) * lg));
+        const f2 rf = both(w.s_kv * w.s_out * ex2((float)(32 * dist + (rev ? -lane : lane - 31)) * lg));
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
             uint32_t x[16], o[8];
@@ -446,9 +446,9 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
             tld16(quad + T_PV + col, x);
             if (use_s) tld16(quad + T_QS + col, y);
             twait16(x);
-            f2 v[8];
+            f2 v[8];  // (P has both factors; Q S gets them, and the decay, here)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] = mul2(f2_of(x[2 * e], x[2 * e + 1]), both(w.s_out));
+            for (int e = 0; e < 8; ++e) v[e] = f2_of(x[2 * e], x[2 * e + 1]);
             if (use_s) {
                 twait16(y);
 #pragma unroll

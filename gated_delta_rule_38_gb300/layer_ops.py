@@ -184,9 +184,15 @@ def rms_norm(x, weight, residual=None, eps=1e-6):
 _ACT = {None: _lib.GDR_GATE_RAW, "sigmoid": _lib.GDR_GATE_SIGMOID, "silu": _lib.GDR_GATE_SILU}
 
 
-def _vectors(t, ld, D, wide):
+def _vectors(t, D, wide, inner):
     """(t, row stride) as the gated and the block norm read it: rows on 16-byte boundaries, or no gaps between them."""
-    if t is not None and (t.data_ptr() % 16 or (ld % 8 if D % 8 == 0 else ld != wide)):
+    if t.is_contiguous():
+        if t.data_ptr() % 16 == 0:
+            return t, wide
+        ld = wide
+    else:
+        t, ld = _rows(t, inner)
+    if t.data_ptr() % 16 or (ld % 8 if D % 8 == 0 else ld != wide):
         return t.clone(memory_format=torch.contiguous_format), wide
     return t, ld
 
@@ -204,7 +210,8 @@ def _gated_problem(x, gate, weight, eps, activation):
     # heads of a token lie side by side, tokens at a stride
     heads = x.shape[-2] if x.dim() > 2 else 1
     inner = 2 if heads > 1 else 1
-    (x, x_ld), (gate, g_ld) = (_vectors(*_rows(t, inner), D, heads * D) for t in (x, gate))
+    x, x_ld = _vectors(x, D, heads * D, inner)
+    gate, g_ld = _vectors(gate, D, heads * D, inner)
     p = _lib.GatedNormProblem(x.numel() // (heads * D) if heads * D else 0, x_ld, g_ld, heads, D, xd, wd, _ACT[activation], eps)
     return p, x, gate
 
@@ -271,11 +278,11 @@ def _block_problem(x, h, name, weight, post_weight, gate, gate_activation, resid
         _need(post_weight, "post_weight", (D,), weight.dtype, x)
     if gate_activation not in _ACT:
         raise ValueError(f"gate_activation is {gate_activation!r}, expected None, 'sigmoid' or 'silu'")
-    x, x_ld = _vectors(*_rows(x), D, D)
+    x, x_ld = _vectors(x, D, D, 1)
     g_ld = D
     if gate is not None:
         _need(gate, "gate", x.shape, x.dtype, x, False)
-        gate, g_ld = _vectors(*_rows(gate), D, D)
+        gate, g_ld = _vectors(gate, D, D, 1)
     elif gate_activation is not None:
         raise ValueError("gate_activation without a gate")
     p = _lib.BlockNormProblem(x.numel() // D if D else 0, x_ld, g_ld, D, xd, wd, hd, _ACT[gate_activation], residual_scale, eps)
