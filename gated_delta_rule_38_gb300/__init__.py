@@ -16,8 +16,8 @@ API (shapes follow the FlashQLA skill page, "Core API" / "Low-Level API"):
 ``linear_attention`` (``linear_ops``) is the delta rule's sibling with one fixed decay a head, with ``*_fwd``, ``*_bwd``
 and ``*_step`` for single tokens.
 
-Around the recurrence (``layer_ops``): ``rms_norm``, ``short_conv`` and ``selective_scan``, each with ``*_fwd`` and
-``*_bwd`` and, for the last two, ``*_step`` for single tokens.
+Around the recurrence (``layer_ops``): ``rms_norm``, ``gated_rms_norm``, ``block_norm``, ``short_conv`` and
+``selective_scan``, each with ``*_fwd`` and ``*_bwd`` and, for the last two, ``*_step`` for single tokens.
 """
 
 from __future__ import annotations
@@ -30,8 +30,10 @@ import torch
 from . import _lib
 from ._args import _DT, _check, _check_cu, _cu, _ptr, _stream
 from .linear_ops import linear_attention, linear_attention_bwd, linear_attention_fwd, linear_attention_step
-from .layer_ops import (block_norm, block_norm_bwd, block_norm_fwd, gated_rms_norm, gated_rms_norm_bwd, gated_rms_norm_fwd, rms_norm, rms_norm_bwd, rms_norm_fwd, selective_scan, selective_scan_bwd, selective_scan_fwd,
-                        selective_scan_step, short_conv, short_conv_bwd, short_conv_fwd, short_conv_step)
+from .layer_ops import (block_norm, block_norm_bwd, block_norm_fwd, gated_rms_norm, gated_rms_norm_bwd,
+                        gated_rms_norm_fwd, rms_norm, rms_norm_bwd, rms_norm_fwd, selective_scan, selective_scan_bwd,
+                        selective_scan_fwd, selective_scan_step, short_conv, short_conv_bwd, short_conv_fwd,
+                        short_conv_step)
 
 __all__ = ["chunk_gated_delta_rule", "chunk_gated_delta_rule_fwd", "chunk_gated_delta_rule_bwd", "saved_buffer",
            "recurrent_gated_delta_rule", "prepare_chunks", "GdrError", "problem", "workspace_bytes", "rms_norm",

@@ -22,8 +22,8 @@ gdr_status check_lin(const gdr_lin_problem *p) {
 }
 
 // The cut: tokens of a segment and of a window, with the least estimated time.  In microseconds, as measured: a chunk takes 4
-// in a walk and 2.2 in the state pass, a block's start and end 6 in both, each window before a segment 1 where its state is
-// summed up, a second launch 2.  (2 x 4096 tokens, 32 heads: 88 us with 2 segments; 1 x 65536, 16 heads: 311 with 9, 396 with 19.)
+// in a walk and 2.2 in the state pass, a block's start and end 6 in both, each window before a segment 0.5 where its state is
+// summed up, a second launch 2.  (2 x 4096 tokens, 32 heads: 88 us with 2 segments; 1 x 65536, 16 heads: 309 with 9, 396 with 19.)
 void cut(const gdr_lin_problem *p, int walks, LinArgs *a) {
     const long long nc = (p->T + LC - 1) / LC, heads = (long long)p->H * walks;
     const long long rows = p->cu_seqlens ? 1 : p->B, more = p->cu_seqlens ? p->num_seqs : 0;
@@ -108,7 +108,8 @@ gdr_status gdr_lin_fwd(const gdr_lin_problem *p, const void *q, const void *k, c
     const int N = p->cu_seqlens ? p->num_seqs : p->B;
     const size_t qk = (size_t)p->Hk * p->K * 2, vw = (size_t)p->H * p->V * 2, sb = (size_t)N * p->H * p->K * p->V * 4;
     // segments of a sequence read its start state while another one writes the end state; tiles are read ahead of the output
-    if (touches(state_out, sb, state_in, 1, sb, sb) || touches(o, tokens * vw, q, tokens, qk, (size_t)p->q_ld * 2) ||
+    if (touches(state_out, sb, state_in, 1, sb, sb) || touches(o, tokens * vw, state_in, 1, sb, sb) ||
+        touches(o, tokens * vw, state_out, 1, sb, sb) || touches(o, tokens * vw, q, tokens, qk, (size_t)p->q_ld * 2) ||
         touches(o, tokens * vw, k, tokens, qk, (size_t)p->k_ld * 2) || touches(o, tokens * vw, v, tokens, vw, (size_t)p->v_ld * 2))
         return GDR_ERR_UNSUPPORTED;
     const Layout l = layout_of(p, false);
@@ -146,8 +147,9 @@ gdr_status gdr_lin_step(const gdr_lin_problem *p, const void *q, const void *k, 
     if (!aligned_to(q, 2) || !aligned_to(k, 2) || !aligned_to(v, 2) || !aligned_to(o, 2) || !aligned_to(decay, 4) || !aligned16(state))
         return GDR_ERR_ALIGN;
     const size_t tokens = (size_t)p->B * p->T, qk = (size_t)p->Hk * p->K * 2, vw = (size_t)p->H * p->V * 2;
+    const size_t sb = (size_t)p->B * p->H * p->K * p->V * 4;
     if (touches(o, tokens * vw, q, tokens, qk, (size_t)p->q_ld * 2) || touches(o, tokens * vw, k, tokens, qk, (size_t)p->k_ld * 2) ||
-        touches(o, tokens * vw, v, tokens, vw, (size_t)p->v_ld * 2))
+        touches(o, tokens * vw, v, tokens, vw, (size_t)p->v_ld * 2) || touches(o, tokens * vw, state, 1, sb, sb))
         return GDR_ERR_UNSUPPORTED;
     unsigned *err = nullptr;
     if ((st = device_state(&err)) != GDR_OK) return st;
@@ -171,10 +173,14 @@ gdr_status gdr_lin_bwd(const gdr_lin_problem *p, const void *q, const void *k, c
         return GDR_ERR_ALIGN;
     const int N = p->cu_seqlens ? p->num_seqs : p->B;
     const size_t qk = (size_t)p->Hk * p->K * 2, vw = (size_t)p->H * p->V * 2, sb = (size_t)N * p->H * p->K * p->V * 4;
+    if (touches(dq, tokens * qk, dk, 1, tokens * qk, tokens * qk) || touches(dq, tokens * qk, dv, 1, tokens * vw, tokens * vw) ||
+        touches(dk, tokens * qk, dv, 1, tokens * vw, tokens * vw))
+        return GDR_ERR_UNSUPPORTED;
     for (const void *out : {dq, dk, dv}) {
         const size_t n = tokens * (out == dv ? vw : qk);
         if (touches(out, n, q, tokens, qk, (size_t)p->q_ld * 2) || touches(out, n, k, tokens, qk, (size_t)p->k_ld * 2) ||
-            touches(out, n, v, tokens, vw, (size_t)p->v_ld * 2) || touches(out, n, dout, tokens, vw, vw))
+            touches(out, n, v, tokens, vw, (size_t)p->v_ld * 2) || touches(out, n, dout, tokens, vw, vw) ||
+            touches(out, n, state_in, 1, sb, sb) || touches(out, n, dstate_out, 1, sb, sb) || touches(out, n, dstate_in, 1, sb, sb))
             return GDR_ERR_UNSUPPORTED;
     }
     if (touches(dstate_in, sb, dstate_out, 1, sb, sb) || touches(dstate_in, sb, state_in, 1, sb, sb)) return GDR_ERR_UNSUPPORTED;

@@ -140,6 +140,7 @@ gdr_status gdr_gated_norm_bwd(const gdr_gated_norm_problem *p, const void *x, co
     for (const void *o : {dx, dgate})
         if (over(o, p->tokens, wide, x, p->x_ld * 2) || over(o, p->tokens, wide, gate, p->gate_ld * 2) || over(o, p->tokens, wide, dy, wide))
             return GDR_ERR_UNSUPPORTED;
+    if (over(dx, p->tokens, wide, dgate, wide)) return GDR_ERR_UNSUPPORTED;
     if (need && (!workspace || workspace_bytes < need)) return GDR_ERR_WORKSPACE;
     if (need && !aligned_to(workspace, 256)) return GDR_ERR_ALIGN;
     unsigned *err = nullptr;
@@ -217,6 +218,9 @@ gdr_status gdr_block_norm_bwd(const gdr_block_norm_problem *p, const void *x, co
             touches(o, n * w, dy, 1, n * 2 * D, n * 2 * D) || touches(o, n * w, dresidual, 1, n * rs * D, n * rs * D))
             return GDR_ERR_UNSUPPORTED;
     }
+    if (over(dx, n, 2 * D, dgate, 2 * D) || touches(dresidual_in, n * rs * D, dx, 1, n * 2 * D, n * 2 * D) ||
+        touches(dresidual_in, n * rs * D, dgate, 1, n * 2 * D, n * 2 * D))
+        return GDR_ERR_UNSUPPORTED;
     if (need && (!workspace || workspace_bytes < need)) return GDR_ERR_WORKSPACE;
     if (need && !aligned_to(workspace, 256)) return GDR_ERR_ALIGN;
     unsigned *err = nullptr;

@@ -1,10 +1,12 @@
 """The operators around the recurrence in a layer: RMS norm with the residual's addition (and an 8-bit output with
-scales), the short causal convolution, and the selective state space scan.
+scales), the norm of a mixer's output with its gate, the norms behind and before a block around the residual's addition,
+the short causal convolution, and the selective state space scan.
 
-Python surface of ``gdr_norm_*``, ``gdr_conv_*`` and ``gdr_scan_*`` in ``include/gdr.h``.  As for the delta rule, the
-``*_fwd`` / ``*_bwd`` / ``*_step`` functions map onto one library call each and ``rms_norm``, ``short_conv`` and
-``selective_scan`` are differentiable (once: second derivatives are refused).  Token tensors may be row-strided views
-(slices of a fused projection are read in place); any other view is copied.
+Python surface of ``gdr_norm_*``, ``gdr_gated_norm_*``, ``gdr_block_norm_*``, ``gdr_conv_*`` and ``gdr_scan_*`` in
+``include/gdr.h``.  As for the delta rule, the ``*_fwd`` / ``*_bwd`` / ``*_step`` functions map onto one library call each
+and ``rms_norm``, ``gated_rms_norm``, ``block_norm``, ``short_conv`` and ``selective_scan`` are differentiable (once: second
+derivatives are refused).  Token tensors may be row-strided views (slices of a fused projection are read in place); any
+other view is copied.
 """
 
 from __future__ import annotations

@@ -420,16 +420,19 @@ gdr_status gdr_scan_bwd(const gdr_scan_problem *p, const void *x, const void *dt
  *        state_in [num_seqs or B,H,K,V] fp32 or NULL (zeros)
  *   out: o [B,T,H,V] (dtype); state_out, as state_in, or NULL
  * K and V from 8 to 128 in steps of 8.  Token tensors and states are 16-byte aligned, their
- * row strides multiples of 8 (GDR_ERR_ALIGN).  state_out overlaps no state_in and o none of
- * q, k, v (GDR_ERR_UNSUPPORTED).  Packed batches and malformed cu_seqlens as in gdr_conv_fwd.
+ * row strides multiples of 8 (GDR_ERR_ALIGN).  o and state_out overlap no input and not one
+ * another (GDR_ERR_UNSUPPORTED).  Packed batches and malformed cu_seqlens as in gdr_conv_fwd.
  * T = 0 passes the states through.  A value that is not finite reaches the outputs of its own
- * sequence and head only, from its chunk of 128 tokens on.  Where sequences and heads do not
- * fill the chip the token axis is cut (workspace: gdr_lin_workspace_size, 256-byte aligned).
+ * sequence and head only, from its chunk of 128 tokens on.  The states are fp32; what enters a
+ * product of 16-bit matrices (scale q.k, the decayed keys, the copy of a state that q meets) is in
+ * the tokens' type, so with fp16 those have to stay within its range (65504; below 6e-5 they lose
+ * bits).  Where sequences and heads do not fill the chip the token axis is cut (workspace:
+ * gdr_lin_workspace_size, 256-byte aligned).
  * gdr_lin_step: dense rows, the states updated in place; meant for T = 1 or a few tokens; its
  * token tensors are aligned to their elements only.
  * Backward: dout [B,T,H,V] (contiguous), dstate_out or NULL (zeros) -> dq, dk [B,T,Hk,K],
  * dv [B,T,H,V] (dtype), dstate_in (fp32, nullable).  The outputs overlap no input
- * (GDR_ERR_UNSUPPORTED).  Fixed summation order.
+ * and not one another (GDR_ERR_UNSUPPORTED).  Fixed summation order.
  */
 typedef struct gdr_lin_problem {
     int B, T, Hk, H, K, V;
@@ -460,9 +463,11 @@ gdr_status gdr_lin_bwd(const gdr_lin_problem *p, const void *q, const void *k, c
  *   in : x, gate [tokens, heads, D] (dtype, x_ld and gate_ld elements between tokens, heads of a
  *        token side by side); weight [D] (weight_dtype: dtype or fp32), one for all heads
  *   out: y [tokens, heads, D] (dtype), contiguous
- * tokens = 0 is valid.  1 <= D <= GDR_NORM_MAX_D.
+ * tokens = 0 is valid.  1 <= D <= GDR_NORM_MAX_D (less 8 where D is no multiple of 8).  Here and
+ * below all tensors but the weights' gradients are 16-byte aligned, and row strides multiples of
+ * 8, or, where D is no multiple of 8, without gaps (GDR_ERR_ALIGN).
  * Backward: dy [tokens, heads, D] -> dx, dgate (dtype, contiguous), dweight [D] (weight_dtype).
- * Fixed summation order.  Outputs overlap no input (GDR_ERR_UNSUPPORTED).
+ * Fixed summation order.  Outputs overlap no input and not one another (GDR_ERR_UNSUPPORTED).
  */
 typedef struct gdr_gated_norm_problem {
     int64_t tokens, x_ld, gate_ld;
@@ -486,12 +491,12 @@ gdr_status gdr_gated_norm_bwd(const gdr_gated_norm_problem *p, const void *x, co
  *   in : x [rows, D], gate [rows, D] or NULL (dtype, row strides x_ld, gate_ld); residual [rows, D]
  *        (residual_dtype: dtype or fp32); weight [D], post_weight [D] or NULL (weight_dtype: dtype or fp32)
  *   out: y [rows, D] (dtype); residual_out [rows, D] = h in residual_dtype (may be `residual`)
- * y is computed from the unrounded sum.  rows = 0 is valid.  1 <= D <= GDR_NORM_MAX_D.
+ * y is computed from the unrounded sum.  rows = 0 is valid.  D as above.
  * Backward at the stored h (residual_out): dy [rows, D] (dtype), dresidual [rows, D] (residual_dtype), the
  * gradient that reaches h from later layers, or NULL
  *   out: dx [rows, D] (dtype), dresidual_in [rows, D] (residual_dtype), dweight, dpost_weight [D] (weight_dtype;
  *        the latter exactly with post_weight), dgate [rows, D] (dtype; exactly with gate)
- * Fixed summation order.  Other overlaps of outputs with inputs: GDR_ERR_UNSUPPORTED.
+ * Fixed summation order.  Other overlaps of outputs with inputs or one another: GDR_ERR_UNSUPPORTED.
  */
 typedef struct gdr_block_norm_problem {
     int64_t rows, x_ld, gate_ld;

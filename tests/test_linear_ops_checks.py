@@ -88,6 +88,20 @@ def test_lin_pointers(lib):
     assert step(pp=lin(T=0), q=None) == 0
 
 
+def test_lin_outputs_over_states_and_one_another(lib):
+    p, sb = lin(), 2 * 4 * 64 * 96 * 4
+    a = far(FWD)
+    assert fwd(lib, p, o=a["s"]) == UNSUPPORTED and fwd(lib, p, o=a["f"] + sb - 16) == UNSUPPORTED and fwd(lib, p, f=a["o"] + 16) == UNSUPPORTED
+    a = far(BWD)
+    for n in ("dq", "dk", "dv"):
+        for m in ("s", "df", "ds"):
+            assert bwd(lib, p, **{n: a[m] + sb - 16}) == UNSUPPORTED and bwd(lib, p, **{m: a[n] + 16}) == UNSUPPORTED, (n, m)
+        for m in {"dq", "dk", "dv"} - {n}:
+            assert bwd(lib, p, **{n: a[m] + 16}) == UNSUPPORTED, (n, m)
+    s = P + 4 * FAR
+    assert lib.gdr_lin_step(ctypes.byref(p), P, P + FAR, P + 2 * FAR, P + 3 * FAR, s, s + 32, None) == UNSUPPORTED
+
+
 def test_lin_workspaces(lib):
     n = ctypes.c_size_t()
 
@@ -183,6 +197,16 @@ def test_norm_pointers(lib):
         for i in ("x", "h", "g", "dy", "dr"):
             assert call(g, B_BWD, b, n.value, **{k: a[i]}) == UNSUPPORTED, (k, i)
     assert call(g, B_BWD, b, n.value, ws=None) == WORKSPACE and call(g, B_BWD, b, n.value, ws=P + 16) == ALIGN
+
+
+def test_norm_gradients_over_one_another(lib):
+    a, g = far(G_BWD), lib.gdr_gated_norm_bwd
+    p = gated()
+    assert call(g, G_BWD, p, 1 << 40, dx=a["dg"] + 16) == UNSUPPORTED and call(g, G_BWD, p, 1 << 40, dg=a["dx"] + 16) == UNSUPPORTED
+    a, g = far(B_BWD), lib.gdr_block_norm_bwd
+    for n in ("dx", "dri", "dg"):
+        for m in {"dx", "dri", "dg"} - {n}:
+            assert call(g, B_BWD, block(), 1 << 40, **{n: a[m] + 16}) == UNSUPPORTED, (n, m)
 
 
 def test_python_surface_needs_cuda_tensors():
