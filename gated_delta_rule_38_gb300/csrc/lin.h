@@ -22,6 +22,7 @@ struct Walk {
     int q_div, k_div, v_div; // head of the tensor = walk's head / div
     bool rev;
     float s_kv, s_out;
+    float s_state, s_key;    // s_kv = s_state s_key; the states inside are 1 / s_state, a power of two, of the formula's
     const float *start;      // states before the walk's first token (rev: gradients behind the last), or null
     float *end;              // states behind its last token (rev: gradients before the first), or null
     int rs, cs;              // element (row of kd, column of vd) of start and end: row * rs + column * cs

@@ -1,4 +1,6 @@
 // Entry points of the linear attention: checks, the cut of the token axis, workspaces and the order of launches.
+#include <cmath>
+
 #include "lin.h"
 #include "tmap.h"
 
@@ -23,7 +25,7 @@ gdr_status check_lin(const gdr_lin_problem *p) {
 
 // The cut: tokens of a segment and of a window, with the least estimated time.  In microseconds, as measured: a chunk takes 4
 // in a walk and 2.2 in the state pass, a block's start and end 6 in both, each window before a segment 0.5 where its state is
-// summed up, a second launch 2.  (2 x 4096 tokens, 32 heads: 88 us with 2 segments; 1 x 65536, 16 heads: 309 with 9, 396 with 19.)
+// summed up, a second launch 2.  (2 x 4096 tokens, 32 heads: 94 us with 2 segments; 1 x 65536, 16 heads: 312 with 9, 396 with 19.)
 void cut(const gdr_lin_problem *p, int walks, LinArgs *a) {
     const long long nc = (p->T + LC - 1) / LC, heads = (long long)p->H * walks;
     const long long rows = p->cu_seqlens ? 1 : p->B, more = p->cu_seqlens ? p->num_seqs : 0;
@@ -50,6 +52,12 @@ LinArgs args_of(const gdr_lin_problem *p, const float *decay, int walks) {
     a.nwalk = walks;
     cut(p, walks, &a);
     return a;
+}
+// The scale of a walk's keys, and its power of two (within 2^+-24) apart.
+void set_scale(Walk *w, float s) {
+    int e = 0;
+    if (std::isfinite(s) && s != 0.f) e = std::ilogb(s), e = e > 24 ? 24 : e < -24 ? -24 : e;
+    w->s_kv = s, w->s_state = std::ldexp(1.f, e), w->s_key = s / w->s_state;
 }
 bool split(const LinArgs &a) { return a.main_len < a.T; }
 
@@ -126,7 +134,7 @@ gdr_status gdr_lin_fwd(const gdr_lin_problem *p, const void *q, const void *k, c
         return cuda_status(cudaErrorInvalidValue);
     w.kd = p->K, w.vd = p->V;
     w.q_div = w.k_div = p->H / p->Hk, w.v_div = 1;
-    w.s_kv = 1.f, w.s_out = p->scale;
+    set_scale(&w, 1.f), w.s_out = p->scale;
     w.start = state_in, w.end = state_out, w.rs = p->V, w.cs = 1;
     w.states = static_cast<float *>(workspace);
     w.ext = w.states, w.ers = 1, w.ecs = LD;
@@ -205,7 +213,7 @@ gdr_status gdr_lin_bwd(const gdr_lin_problem *p, const void *q, const void *k, c
     v_.tq = mk, v_.tk = mq, v_.tv = md;
     v_.kd = p->K, v_.vd = p->V;
     v_.q_div = v_.k_div = grp, v_.v_div = 1;
-    v_.rev = true, v_.s_kv = p->scale, v_.s_out = 1.f;
+    v_.rev = true, set_scale(&v_, p->scale), v_.s_out = 1.f;
     v_.start = dstate_out, v_.end = dstate_in, v_.rs = p->V, v_.cs = 1;
     v_.states = bw, v_.ext = bw, v_.ers = 1, v_.ecs = LD;
     v_.out = dv;
@@ -214,7 +222,7 @@ gdr_status gdr_lin_bwd(const gdr_lin_problem *p, const void *q, const void *k, c
     k_.tq = mv, k_.tk = md, k_.tv = mq;
     k_.kd = p->V, k_.vd = p->K;
     k_.q_div = k_.k_div = 1, k_.v_div = grp;
-    k_.rev = true, k_.s_kv = p->scale, k_.s_out = 1.f;
+    k_.rev = true, set_scale(&k_, p->scale), k_.s_out = 1.f;
     k_.start = dstate_out, k_.rs = 1, k_.cs = p->V;
     k_.ext = bw, k_.ers = LD, k_.ecs = 1;
     k_.out = grp > 1 ? static_cast<void *>(pk) : dk, k_.out_f32 = grp > 1;
@@ -223,7 +231,7 @@ gdr_status gdr_lin_bwd(const gdr_lin_problem *p, const void *q, const void *k, c
     q_.tq = md, q_.tk = mv, q_.tv = mk;
     q_.kd = p->V, q_.vd = p->K;
     q_.q_div = q_.k_div = 1, q_.v_div = grp;
-    q_.s_kv = 1.f, q_.s_out = p->scale;
+    set_scale(&q_, 1.f), q_.s_out = p->scale;
     q_.start = state_in, q_.rs = 1, q_.cs = p->V;
     q_.states = fw, q_.ext = fw, q_.ers = 1, q_.ecs = LD;
     q_.out = grp > 1 ? static_cast<void *>(pq) : dq, q_.out_f32 = grp > 1;

@@ -24,17 +24,24 @@
 // Fourteen warps leave a thread 128 registers; with eighteen and 96 the state's threads spilled, and what they spilled went
 // to L2.  Loops that can stay loops do: unrolled, a chunk's code no longer fitted the instruction caches next to the
 // schedulers.  (1 x 2048 tokens, 152 heads, one walk a CTA, 318 MB: 156 us with spills, 72 with sixteen warps through all
-// steps together, 63 so, which is 5.0 TB/s, or 4 us a chunk; the matrix instructions take half of them.)
-// A decayed key is two 16-bit numbers, the rounded one and the remainder's, each with a product of its own: their sum is
-// as good as keys of 16 bits of mantissa, because the states are handed on in fp32 (rounded once they would be off by
-// 1e-3; so they are by 3e-6).
+// steps together, 60 so, which is 5.3 TB/s, or 3.8 us a chunk; the matrix instructions take half of them.)
+// The states inside are without their scale's power of two (of the gradients' walks), which the keys then need not carry:
+// in fp16 their remainders would fall below its range.
+// A decayed key is a sum of 16-bit numbers, the rounded one and what that leaves, each with a product of its own, the
+// smallest first: the accumulator loses at each addition by what it holds.  Two of fp16 make 22 bits and states 2e-7 off
+// (of one number: 1e-3).  Two of bf16 make 17 bits and 2.5e-6, which outputs of 8 bits do not show; states that are handed
+// on get a third where the chunk weighs over an eighth in them (3e-7).  Its place is the state's copy's, free between Q S
+// and the next copy, and warps 8..11 make all the keys of such a chunk: the state's warps have no registers for it.
+// (2 x 4096 tokens, 32 heads of memories of 100 tokens: 88 us with the final states, 79 without; where nothing decays, so
+// that every chunk has three, 110.)  The products' loop stays a loop: with its bodies side by side the training step of
+// 2 x 4096 tokens took 296 us, 287 so.
 // The accumulators of one chunk's state update start from zero and are added to the state in fp32 registers, rounded to
 // nearest: in the tensor core's own accumulator the additions of a long walk would lose in one direction.
 // lambda^128 is kept as two fp32 numbers, so that a memory of any length is not off by what rounding it once would add up to.
 //
 // Segments.  Where sequences x heads leave SMs idle the token axis is cut; a first launch (STATES: no q, P or output rows, up to
 // two chunks on their way) leaves every window's own end state, and a segment begins with the decayed sum of the windows
-// before it, in a fixed order.  (1 x 65536 tokens, 16 heads: 97 us for the states and 215 for the walk, 4.9 TB/s in the first
+// before it, in a fixed order.  (1 x 65536 tokens, 16 heads: 99 us for the states and 215 for the walk, 4.8 TB/s in the first
 // launch, which reads 8/9 of k and v.)
 #include "common.cuh"
 #include "f32x2.cuh"
@@ -51,10 +58,12 @@ constexpr int CW = LD / (NS / 4);                       // columns of a state wa
 constexpr uint32_t TILE = 32768, BLK = 16384;     // a tile: two blocks of 64 columns, 128 rows each
 constexpr int RING = 5;
 constexpr uint32_t S_LO = RING * TILE;            // the keys' remainders
-constexpr uint32_t S_ST = S_LO + TILE;            // the state's copy (state pass: the remainders of odd chunks)
+constexpr uint32_t S_ST = S_LO + TILE;            // the state's copy (state pass: the remainders of odd chunks); third numbers
 constexpr uint32_t S_BAR = S_ST + TILE;
 constexpr uint32_t B_FULL = S_BAR, B_EMPTY = S_BAR + 8 * RING, B_QK = B_EMPTY + 8 * RING, B_S = B_QK + 8, B_P = B_S + 8,
-                   B_PV = B_P + 8, B_K = B_PV + 8, B_DS = B_K + 16, B_DONE = B_DS + 16, S_SLOT = B_DONE + 8, S_FLAG = S_SLOT + 4;
+                   B_PV = B_P + 8, B_K = B_PV + 8, B_DS = B_K + 16, B_DONE = B_DS + 16, B_QS = B_DONE + 8, S_SLOT = B_QS + 8,
+                   S_FLAG = S_SLOT + 4;
+constexpr uint32_t S_FROM = S_FLAG + 4;           // the first chunk whose decayed keys are three numbers
 constexpr uint32_t S_LAM = S_FLAG + 8;            // lambda^128 as two fp32 numbers
 // decays of up to 31 tokens: COL[c] = lambda^(31-c) (rev: lambda^c); DIAG[31 + row - key] = s_kv s_out lambda^|row - key| where
 // the row sees the key, else 0
@@ -64,6 +73,7 @@ static_assert(S_BYTES <= kSmemMost, "shared memory");
 // tensor memory columns: Q K^T and, in its place, P (each 32 columns in the lower half of their own); Q S; P V; the update
 constexpr uint32_t T_QK = 0, T_QS = 128, T_PV = 256, T_DS = 384;
 
+template <int N> struct Int { static constexpr int value = N; };
 template <typename T> struct IsBf16 { static constexpr bool value = false; };
 template <> struct IsBf16<__nv_bfloat16> { static constexpr bool value = true; };
 
@@ -262,7 +272,8 @@ struct Cuts {
 
 // ---------------------------------------------------------------- the kernel
 
-template <typename T, bool STATES>
+// MAY: keys of three numbers.
+template <typename T, bool STATES, bool MAY>
 __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__ LinParams p) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem =
@@ -337,6 +348,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                 umma::mbar_init(sb + B_DS + 8 * i, 1);
             }
             umma::mbar_init(sb + B_DONE, 1);
+            umma::mbar_init(sb + B_QS, 1);
             umma::fence_mbar_init();
             sts32(flag, 0);
         }
@@ -348,6 +360,13 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
         const double l = exp((double)g * LC);
         sts32(sb + S_LAM, __float_as_uint((float)l));
         sts32(sb + S_LAM + 4, __float_as_uint((float)(l - (double)(float)l)));
+        int from = 0x7fffffff;
+        if (w.end) {  // tokens after which an eighth is left, and those behind the segment's first one
+            const float reach = lg < 0.f ? -3.f / lg : 2e9f, ahead = (float)(rev ? seg.t1 - seg.seq0 : seg.seq1 - seg.t0);
+            if (!STATES) from = max((int)((ahead - reach) * (1.f / LC)), 0);
+            else if (ahead - (float)(seg.t1 - seg.t0) < reach) from = 0;
+        }
+        sts32(sb + S_FROM, (uint32_t)from);
     }
     if (tid >= 64 && tid < 96) reinterpret_cast<float *>(smem + S_COL)[lane] = ex2((float)(rev ? lane : 31 - lane) * lg);
     if (tid >= 96 && tid < 160) {
@@ -360,42 +379,56 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
     umma::fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + S_SLOT);
 
+    // Whether chunk c's decayed keys are three numbers (once so, then to the walk's end; the state pass: its whole window).
+    auto three = [&](int c) { return MAY && c >= (int)lds32_now(sb + S_FROM); };
     // The state pass' hand-offs run up to two chunks ahead of one another, so each parity of chunks has its own barriers.
     auto bar_of = [&](uint32_t bar, int c) { return sb + bar + (STATES && (c & 1) ? 8u : 0u); };
     auto par_of = [&](int c) { return (uint32_t)((STATES ? c >> 1 : c) & 1); };
     const int ksteps = (kd + 15) / 16;
     const int NV = (vd + 15) / 16 * 16;
 
+    // The keys' remainders of chunk c.
+    auto lo_of = [&](int c) { return STATES && (c & 1) && !three(c) ? S_ST : S_LO; };
     // The decayed keys of chunk c, eights i0 .. i1 of the columns of row 32 (warp mod 4) + lane; the rounded ones in place of k.
-    auto make_keys = [&](int c, int L, int i0, int i1) {
+    auto make_keys = [&](int c, int L, int i0, int i1, auto all) {
         const int row = (warp & 3) * 32 + lane;
-        const uint32_t kt = sb + slot_of(c, KI) * TILE, lo = sb + (STATES && (c & 1) ? S_ST : S_LO);
+        const uint32_t kt = sb + slot_of(c, KI) * TILE, lo = sb + lo_of(c);
         const bool in = row < L;
-        const float f = in ? w.s_kv * ex2((float)(rev ? row + 1 : L - 1 - row) * lg) : 0.f;  // (behind the end it could be infinite)
+        const float f = in ? w.s_key * ex2((float)(rev ? row + 1 : L - 1 - row) * lg) : 0.f;  // (behind the end it could be infinite)
+        auto place = [&](int i) { return (uint32_t)(i >> 3) * BLK + row * 128 + (((uint32_t)(i & 7) ^ (row & 7)) << 4); };
+        // N eights at a time, as M numbers each
+        auto convert = [&](int from, int to, auto n, auto terms) {
+            constexpr int N = decltype(n)::value, M = decltype(terms)::value;
 #pragma unroll 1
-        for (int i = i0; i < i1; i += 2) {
-            uint4 u[2];
-            uint32_t at[2];
+            for (int i = from; i < to; i += N) {
+                uint4 u[N];
+                uint32_t at[N];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                at[k] = (uint32_t)(i >> 3) * BLK + row * 128 + (((uint32_t)((i & 7) + k) ^ (row & 7)) << 4);
-                u[k] = umma::ld_shared_v4(kt + at[k]);
-                if (!in) u[k] = make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t x[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-                uint32_t h[4], l[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const f2 v = mul2(widen2<T>(x[e]), both(f));
-                    h[e] = narrow2<T>(v);
-                    l[e] = narrow2<T>(fma2(widen2<T>(h[e]), both(-1.f), v));
+                for (int k = 0; k < N; ++k) {
+                    at[k] = (uint32_t)(i >> 3) * BLK + row * 128 + (((uint32_t)((i & 7) + k) ^ (row & 7)) << 4);
+                    u[k] = umma::ld_shared_v4(kt + at[k]);
+                    if (!in) u[k] = make_uint4(0, 0, 0, 0);
                 }
-                umma::st_shared_v4(kt + at[k], h[0], h[1], h[2], h[3]);
-                umma::st_shared_v4(lo + at[k], l[0], l[1], l[2], l[3]);
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    const uint32_t x[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+                    uint32_t h[4], l[4], m[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const f2 v = mul2(widen2<T>(x[e]), both(f));
+                        h[e] = narrow2<T>(v);
+                        const f2 r = fma2(widen2<T>(h[e]), both(-1.f), v);
+                        l[e] = narrow2<T>(r);
+                        if (M == 3) m[e] = narrow2<T>(fma2(widen2<T>(l[e]), both(-1.f), r));
+                    }
+                    umma::st_shared_v4(kt + at[k], h[0], h[1], h[2], h[3]);
+                    umma::st_shared_v4(lo + at[k], l[0], l[1], l[2], l[3]);
+                    if (M == 3) umma::st_shared_v4(sb + S_ST + at[k], m[0], m[1], m[2], m[3]);
+                }
             }
-        }
+        };
+        if (decltype(all)::value && three(c)) convert(0, 8 * kblk, Int<4>(), Int<3>());
+        else convert(i0, i1, Int<2>(), Int<2>());
         umma::fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar_of(B_K, c));
@@ -439,7 +472,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
         const uint32_t quad = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const bool use_s = c > 0 || has_start;
         umma::fence_after();
-        const float rf = use_s ? w.s_out * ex2((float)(rev ? L - 1 - row : row + 1) * lg) : 0.f;
+        const float rf = use_s ? w.s_out * w.s_state * ex2((float)(rev ? L - 1 - row : row + 1) * lg) : 0.f;
         const long long at = (((long long)t + row) * a.H + j) * vd;
         const bool wide = row < L && vd % 16 == 0 && reinterpret_cast<uintptr_t>(w.out) % 32 == 0;
 #pragma unroll 1
@@ -520,7 +553,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
             commit_on(on, sb + B_QK);
             if (lane == 0) mbar_arrive(sb + B_QK);  // (hands on that q and k have landed)
         };
-        // one of the two products of chunk c's state update: with the keys or with their remainders
+        // one of the products of chunk c's state update: with the keys or with one of their remainders
         auto issue_ds = [&](int c, uint32_t keys, int ts, bool more) {
             const uint32_t d = tmem + T_DS - (STATES && (c & 1) ? 128 : 0);
             const uint64_t dv = umma::desc(sb + slot_of(c, VI) * TILE, BLK, 1024), dk = umma::desc(keys, BLK, 1024);
@@ -536,7 +569,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
             int t, L;
             chunk(c, t, L);
             const int ts = (L + 15) / 16;
-            const uint32_t kt = sb + slot_of(c, KI) * TILE, lo = sb + (STATES && (c & 1) ? S_ST : S_LO);
+            const uint32_t kt = sb + slot_of(c, KI) * TILE, lo = sb + lo_of(c);
             const bool upd = want_end || c + 1 < nc, use_s = c > 0 || has_start;
             if (!STATES) {
                 // the state's copy is there, and the accumulators of the chunk before have been read
@@ -552,6 +585,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                     }
                 }
                 commit_on(on, sb + B_EMPTY + 8 * slot_of(c, 0));
+                if (MAY) commit_on(on, sb + B_QS);
                 const uint32_t b = sb + B_FULL + 8 * slot_of(c, VI), f = phase_of(c, VI);
                 ok = ok && __all_sync(0xffffffffu, wait_phases(sb + B_P, c & 1, b, f, b, f, flag, a.err));
                 if (!ok) break;
@@ -569,10 +603,15 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                 // (state pass: its accumulator was read, two chunks before, ahead of these keys)
                 if (!ok) break;
                 umma::fence_after();
-                issue_ds(c, kt, ts, false);
-                if (!STATES && c + 1 < nc) wait_qk(c + 1);
+                const uint32_t first = MAY && three(c) ? sb + S_ST : lo;
+#pragma unroll 1
+                for (uint32_t keys = first;; keys = keys != lo ? lo : kt) {
+                    issue_ds(c, keys, ts, keys != first);
+                    if (keys == kt) break;
+                    if (keys == lo && !STATES && c + 1 < nc) wait_qk(c + 1);
+                    if (!ok) break;
+                }
                 if (!ok) break;
-                issue_ds(c, lo, ts, true);
                 commit_on(on, bar_of(B_DS, c));
             }
             if (!ok) break;
@@ -644,7 +683,8 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                 // (the remainders' place: read by the update of the chunk before)
                 if (want_end || c + 1 < nc) {
                     if (c > 0) ok = ok && wwait(sb + B_DS, (c - 1) & 1, flag, a.err);
-                    if (ok) make_keys(c, L, 10, min(16, 8 * kblk));
+                    if (three(c)) ok = ok && wwait(sb + B_QS, c & 1, flag, a.err);
+                    if (ok) make_keys(c, L, 10, min(16, 8 * kblk), Int<1>());
                 }
                 continue;
             }
@@ -652,8 +692,8 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
             ok = wwait(sb + B_FULL + 8 * slot_of(c, VI), phase_of(c, VI), flag, a.err) &&
                  wwait(sb + B_FULL + 8 * slot_of(c, KI), phase_of(c, KI), flag, a.err);
             if (ok && L < LC) clear_v(c, L);
-            if (c >= 2) ok = ok && wwait(bar_of(B_DS, c), par_of(c - 2), flag, a.err);
-            if (ok) make_keys(c, L, 0, 8);
+            if (three(c) ? c >= 1 : c >= 2) ok = ok && wwait(bar_of(B_DS, three(c) ? c - 1 : c), par_of(three(c) ? c - 1 : c - 2), flag, a.err);
+            if (ok) make_keys(c, L, 0, 8, Int<1>());
         }
     } else {
         // ------------------------------------------------------------ the state and the output rows
@@ -680,6 +720,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                         const long long cs = w.cs;
                         st[2 * i] = pack2(s0[col * cs], s0[(col + 1) * cs]), st[2 * i + 1] = pack2(s0[(col + 2) * cs], s0[(col + 3) * cs]);
                     }
+                    st[2 * i] = mul2(st[2 * i], both(1.f / w.s_state)), st[2 * i + 1] = mul2(st[2 * i + 1], both(1.f / w.s_state));
                 }
             }
             if (!at_start) {
@@ -751,7 +792,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                 int t, L;
                 chunk(0, t, L);
                 ok = make_p(0, L);
-                if (ok && (want_end || nc > 1)) make_keys(0, L, k0, k1);
+                if (ok && (want_end || nc > 1)) make_keys(0, L, k0, three(0) ? k0 : k1, Int<0>());
             }
         }
         int before = 0;  // (state pass) the length of the chunk before
@@ -762,7 +803,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
             if (STATES) {
                 ok = wwait(sb + B_FULL + 8 * slot_of(c, KI), phase_of(c, KI), flag, a.err);
                 if (!ok) break;
-                make_keys(c, L, k0, k1);
+                make_keys(c, L, k0, three(c) ? k0 : k1, Int<0>());
                 if (c > 0) {
                     ok = wwait(bar_of(B_DS, c - 1), par_of(c - 1), flag, a.err);
                     if (!ok) break;
@@ -786,7 +827,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                     int tn, Ln;
                     chunk(c + 1, tn, Ln);
                     ok = make_p(c + 1, Ln);
-                    if (ok && (want_end || c + 2 < nc)) make_keys(c + 1, Ln, k0, k1);
+                    if (ok && (want_end || c + 2 < nc)) make_keys(c + 1, Ln, k0, three(c + 1) ? k0 : k1, Int<0>());
                 }
             }
         }
@@ -802,6 +843,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
             for (int i = 0; i < CW / 4; ++i) {
                 const int col = c0 + 4 * i;
                 if (col >= vd) continue;
+                if (!STATES) st[2 * i] = mul2(st[2 * i], both(w.s_state)), st[2 * i + 1] = mul2(st[2 * i + 1], both(w.s_state));
                 if (!STATES && cs == 1) {
                     *reinterpret_cast<ulonglong2 *>(e + col) = make_ulonglong2(st[2 * i], st[2 * i + 1]);
                 } else {
@@ -816,24 +858,27 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
     if (warp == NS + NK + 1) umma::dealloc(tmem, 512);
 }
 
-template <typename T, bool STATES>
+template <typename T, bool STATES, bool MAY>
 cudaError_t launch_t(const LinParams &p, cudaStream_t s) {
     const long long n = lin_slots(p.a, STATES ? p.a.win_len : p.a.main_len) * p.a.H * p.a.nwalk;
     if (n == 0) return cudaSuccess;
-    auto k = lin_walk_kernel<T, STATES>;
+    auto k = lin_walk_kernel<T, STATES, MAY>;
     const cudaError_t e = allow_smem(k, S_BYTES);
     if (e != cudaSuccess) return e;
     return launch_plain(k, dim3((unsigned)n), dim3(NT), S_BYTES, s, p);
 }
+template <bool STATES>
+cudaError_t launch_any(const LinParams &p, bool bf16, cudaStream_t s) {
+    bool ends = false;
+    for (int i = 0; i < p.a.nwalk; ++i) ends = ends || p.w[i].end;
+    if (!bf16) return launch_t<__half, STATES, false>(p, s);
+    return ends ? launch_t<__nv_bfloat16, STATES, true>(p, s) : launch_t<__nv_bfloat16, STATES, false>(p, s);
+}
 
 }  // namespace
 
-cudaError_t launch_lin_walks(const LinParams &p, bool bf16, cudaStream_t s) {
-    return bf16 ? launch_t<__nv_bfloat16, false>(p, s) : launch_t<__half, false>(p, s);
-}
-cudaError_t launch_lin_states(const LinParams &p, bool bf16, cudaStream_t s) {
-    return bf16 ? launch_t<__nv_bfloat16, true>(p, s) : launch_t<__half, true>(p, s);
-}
+cudaError_t launch_lin_walks(const LinParams &p, bool bf16, cudaStream_t s) { return launch_any<false>(p, bf16, s); }
+cudaError_t launch_lin_states(const LinParams &p, bool bf16, cudaStream_t s) { return launch_any<true>(p, bf16, s); }
 
 }  // namespace lin
 }  // namespace gdr

@@ -10,7 +10,7 @@ from layer_ref import U, ranges
 # Linear attention's 16-bit results carry three roundings: a product's left side (P, or the state's copy) of each term, and
 # the result's own.  One is off by at most U of the value, evenly spread within that, which is U / sqrt(3) in the mean
 # square; three independent ones give U, and a quarter more is for the spread of small samples.  The states are sums of keys
-# held as two 16-bit numbers, each term off by at most U^2, and of fp32 operations (2e-6 together).
+# held as two or three 16-bit numbers, each term off by at most U^2, and of fp32 operations (2e-6 together).
 def attn_bound(t, dt) -> float:
     if t.dtype == torch.float32:
         return U[dt] ** 2 + 2e-6

@@ -125,6 +125,38 @@ def test_decays(decay):
         ref.check(got, leaf.grad, ref.attn_bound(got, BF), "gradient")
 
 
+@DT
+@pytest.mark.parametrize("decay", [0.0, -1e-4, -0.004, -0.5])
+@pytest.mark.parametrize("T", [100, 1100, 9000])
+def test_states_are_fp32(T, decay, dt):
+    """States that are handed on are as good as fp32 sums, whatever the tokens' type.  Of the keys' numbers: 3 bf16 or 2 fp16
+    leave 2^-22 at most, and 2 bf16 (2.5e-6 in the mean square) where the chunk weighs under an eighth, 3.2e-7; the
+    accumulator's eight additions of full size, rounded down, 8 x 2^-24 = 4.8e-7; together under 1e-6."""
+    x = make(1, T, 1, 2, 128, 128, None, True, dt)
+    d = torch.full((2,), decay, device="cuda")
+    _, fin = gdr.linear_attention_fwd(x["q"], x["k"], x["v"], d, initial_state=x["s0"], output_final_state=True)
+    args = [lref.f64(x[n]) for n in ("q", "k", "v", "s0")]
+    ow, fw = ref.attn(*args[:3], d.double().cpu(), 128 ** -0.5, args[3], None)
+    ref.check(fin, fw, 1e-6, "final_state")
+    ((ow * x["do"].double().cpu()).sum() + (fw * x["ds"].double().cpu()).sum()).backward()
+    ds = gdr.linear_attention_bwd(x["q"], x["k"], x["v"], d, x["do"], initial_state=x["s0"], dfinal_state=x["ds"])[3]
+    ref.check(ds, args[3].grad, 1e-6, "dinitial_state")
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.0 ** -30, 4096.0])
+def test_scales(scale):
+    """Scales of any size and sign; a scale of zero leaves the states' gradients alone."""
+    x = make(1, 300, 1, 2, 64, 64)
+    d = torch.tensor([-0.01, -0.3], device="cuda")
+    args = [lref.f64(x[n]) for n in ("q", "k", "v", "s0")]
+    o, fin = gdr.linear_attention_fwd(x["q"], x["k"], x["v"], d, scale=scale, initial_state=x["s0"], output_final_state=True)
+    ow, fw = ref.attn(*args[:3], d.double().cpu(), scale, args[3], None)
+    ((ow * x["do"].double().cpu()).sum() + (fw * x["ds"].double().cpu()).sum()).backward()
+    grads = gdr.linear_attention_bwd(x["q"], x["k"], x["v"], d, x["do"], scale=scale, initial_state=x["s0"], dfinal_state=x["ds"])
+    for got, want in zip((o, fin, *grads), (ow, fw, *(a.grad for a in args))):
+        ref.check(got, want, ref.attn_bound(got, BF), "scale")
+
+
 def test_differences():
     """The gradients against central differences of the fp64 form."""
     x = make(1, 150, 1, 2, 32, 48, dt=FH)
