@@ -199,6 +199,13 @@ def _vectors(t, D, wide, inner):
     return t, ld
 
 
+def _on16(t):
+    """t on a 16-byte boundary, copied there if need be (a slice of a gradient or of a flat parameter may lie anywhere)."""
+    if t is None or t.data_ptr() % 16 == 0:
+        return t
+    return t.clone(memory_format=torch.contiguous_format)
+
+
 def _gated_problem(x, gate, weight, eps, activation):
     xd = _tokens(x, "x")
     if x.dim() < 1:
@@ -215,7 +222,7 @@ def _gated_problem(x, gate, weight, eps, activation):
     x, x_ld = _vectors(x, D, heads * D, inner)
     gate, g_ld = _vectors(gate, D, heads * D, inner)
     p = _lib.GatedNormProblem(x.numel() // (heads * D) if heads * D else 0, x_ld, g_ld, heads, D, xd, wd, _ACT[activation], eps)
-    return p, x, gate
+    return p, x, gate, _on16(weight)
 
 
 def gated_rms_norm_fwd(x, gate, weight, eps=1e-6, activation="silu", out=None):
@@ -224,7 +231,7 @@ def gated_rms_norm_fwd(x, gate, weight, eps=1e-6, activation="silu", out=None):
     x, gate [..., D] bf16 or fp16 (typically [B,T,H,D], a norm a head; slices of a projection are read in place); weight
     [D] of x's type or fp32; ``activation`` "silu" or "sigmoid".  ``out`` must not overlap x or gate.
     """
-    p, x, gate = _gated_problem(x, gate, weight, eps, activation)
+    p, x, gate, weight = _gated_problem(x, gate, weight, eps, activation)
     if out is not None:
         _need(out, "out", x.shape, x.dtype, x)
     y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
@@ -234,9 +241,9 @@ def gated_rms_norm_fwd(x, gate, weight, eps=1e-6, activation="silu", out=None):
 
 def gated_rms_norm_bwd(x, gate, weight, dy, eps=1e-6, activation="silu"):
     """(dx, dgate, dweight); dweight in weight's type."""
-    p, x, gate = _gated_problem(x, gate, weight, eps, activation)
+    p, x, gate, weight = _gated_problem(x, gate, weight, eps, activation)
     _need(dy, "dy", x.shape, x.dtype, x, False)
-    dy = dy.contiguous()
+    dy = _on16(dy.contiguous())
     dx, dg = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for _ in range(2))
     dw = torch.empty_like(weight)
     lib = _lib.load()
@@ -288,7 +295,7 @@ def _block_problem(x, h, name, weight, post_weight, gate, gate_activation, resid
     elif gate_activation is not None:
         raise ValueError("gate_activation without a gate")
     p = _lib.BlockNormProblem(x.numel() // D if D else 0, x_ld, g_ld, D, xd, wd, hd, _ACT[gate_activation], residual_scale, eps)
-    return p, x, gate
+    return p, x, _on16(h), gate, _on16(weight), _on16(post_weight)
 
 
 def block_norm_fwd(x, residual, weight, post_weight=None, gate=None, gate_activation=None, residual_scale=1.0, eps=1e-6,
@@ -303,7 +310,8 @@ def block_norm_fwd(x, residual, weight, post_weight=None, gate=None, gate_activa
     or fp32 (both the same); gate [..., D] of x's type through ``gate_activation`` (None: as it is, "sigmoid", "silu").
     ``out`` (for y) must not overlap the inputs.
     """
-    p, x, gate = _block_problem(x, residual, "residual", weight, post_weight, gate, gate_activation, residual_scale, eps)
+    p, x, residual, gate, weight, post_weight = _block_problem(x, residual, "residual", weight, post_weight, gate,
+                                                               gate_activation, residual_scale, eps)
     if out is not None:
         _need(out, "out", x.shape, x.dtype, x)
     y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
@@ -317,11 +325,13 @@ def block_norm_bwd(x, h, weight, dy, dresidual=None, post_weight=None, gate=None
                    eps=1e-6):
     """(dx, dresidual_in, dweight, dpost_weight, dgate) at h, the forward's residual_out; ``dresidual`` (h's type) is the
     gradient that reaches it from later layers.  The gradients of what was not given are None."""
-    p, x, gate = _block_problem(x, h, "h", weight, post_weight, gate, gate_activation, residual_scale, eps)
+    p, x, h, gate, weight, post_weight = _block_problem(x, h, "h", weight, post_weight, gate, gate_activation,
+                                                        residual_scale, eps)
     _need(dy, "dy", x.shape, x.dtype, x, False)
-    dy = dy.contiguous()
+    dy = _on16(dy.contiguous())
     if dresidual is not None:
         _need(dresidual, "dresidual", h.shape, h.dtype, x)
+        dresidual = _on16(dresidual)
     dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
     dres = torch.empty(h.shape, dtype=h.dtype, device=x.device)
     dg = None if gate is None else torch.empty(x.shape, dtype=x.dtype, device=x.device)

@@ -161,6 +161,29 @@ def test_views(D):
     assert torch.equal(gdr.block_norm_fwd(xm, low, w, gate=gm)[1], a[1])
 
 
+def test_slices_off_16_bytes():
+    """Gradients that are slices of a larger one, streams and weights that are slices of flat tensors: copied, the same bits."""
+    D, n = 67, 5
+    randn = lambda *s: torch.randn(*s, device="cuda")  # noqa: E731
+
+    def at(t):  # the same numbers 2 or 4 bytes past a boundary
+        return torch.cat([t.new_zeros(1), t.reshape(-1)])[1:].view(t.shape)
+
+    x, g, r, w, pw, dy, dh = randn(n, D).half(), randn(n, D).half(), randn(n, D), randn(D), randn(D), randn(n, D).half(), randn(n, D)
+    assert at(dy).data_ptr() % 16 and at(r).data_ptr() % 16 and at(dy).is_contiguous()
+    pairs = [(gdr.gated_rms_norm_fwd(x, g, w), gdr.gated_rms_norm_fwd(at(x), at(g), at(w))),
+             (gdr.gated_rms_norm_bwd(x, g, w, dy), gdr.gated_rms_norm_bwd(at(x), at(g), at(w), at(dy))),
+             (gdr.block_norm_fwd(x, r, w, pw, g), gdr.block_norm_fwd(at(x), at(r), at(w), at(pw), at(g))),
+             (gdr.block_norm_bwd(x, r, w, dy, dh, pw, g), gdr.block_norm_bwd(at(x), at(r), at(w), at(dy), at(dh), at(pw), at(g)))]
+    for a, b in pairs:
+        for s, t in zip(*((z,) if isinstance(z, torch.Tensor) else z for z in (a, b))):
+            assert torch.equal(s, t)
+    leaf = x.clone().requires_grad_()
+    y = torch.cat([gdr.gated_rms_norm(leaf[:3], g[:3], w), gdr.gated_rms_norm(leaf[3:], g[3:], w)])
+    y.backward(dy)
+    assert torch.equal(leaf.grad, pairs[1][0][0])
+
+
 def test_neighbours_stay():
     """Rows of odd width are written to their last element and not beyond."""
     D = 131
