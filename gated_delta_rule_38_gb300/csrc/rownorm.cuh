@@ -40,6 +40,7 @@ struct Rows {
     const RowArgs &a;
     char *smem;
     int t, slot, shift;     // thread of the row, row slot of the block, elements before a row in its first vector
+    bool edge;              // some but not all of a vector's columns lie in the row
     uint32_t own;           // the columns of this thread that lie in the row, a bit each (whole vectors: a bit a group)
     __device__ __forceinline__ Rows(const RowArgs &a_, void *s) : a(a_), smem(static_cast<char *>(s)) {
         slot = threadIdx.x / a.tpr;
@@ -52,6 +53,9 @@ struct Rows {
 #pragma unroll
             for (int e = 0; SHIFT && e < 8; ++e) own |= (uint32_t)(column(g) + e >= 0 && column(g) + e < a.D) << (8 * g + e);
         }
+        edge = false;
+#pragma unroll
+        for (int g = 0; SHIFT && g < NG; ++g) edge = edge || (any(g) && !whole(g));
     }
     __device__ __forceinline__ int column(int g) const { return (g * a.tpr + t) * 8 - (SHIFT ? shift : 0); }
     __device__ __forceinline__ bool any(int g) const { return SHIFT ? own >> (8 * g) & 0xffu : own >> g & 1; }
@@ -130,13 +134,39 @@ struct Rows {
         } else {
             o[0] = widen2<T>(u.x), o[1] = widen2<T>(u.y), o[2] = widen2<T>(u.z), o[3] = widen2<T>(u.w);
         }
-        if (!whole(g)) {  // (a neighbouring row's elements)
+    }
+    // Zeros in place of the neighbouring rows' elements in the vectors at a row's ends, once they are there.  (Left out of
+    // what `get` gives instead, every vector of every pass paid for it: 100000 x 127, block norm's backward 156 us, 136 so.)
+    template <int I>
+    __device__ __forceinline__ void clear_one(int stage, int g) const {
+        if constexpr (has(I)) {
+            if (I == IN_DRES && !a.in[I].p) return;
+            constexpr int W = elem(I) / 2;
+            uint4 *s = reinterpret_cast<uint4 *>(smem + stage * a.place + off(I) + (g * threads() + threadIdx.x) * (16 * W));
+            const uint32_t b = own >> (8 * g);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float v0, v1;
-                unpack2(o[e], v0, v1);
-                o[e] = pack2(has_column(g, 2 * e) ? v0 : 0.f, has_column(g, 2 * e + 1) ? v1 : 0.f);
+            for (int h = 0; h < W; ++h) {
+                uint4 u = s[h];
+                uint32_t *w = &u.x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (W == 2) w[e] = b >> (4 * h + e) & 1 ? w[e] : 0u;
+                    else w[e] &= (b >> (2 * e) & 1 ? 0xffffu : 0u) | (b >> (2 * e + 1) & 1 ? 0xffff0000u : 0u);
+                }
+                s[h] = u;
             }
+        }
+    }
+    __device__ __forceinline__ void clear(int stage) const {
+        if (!SHIFT || !edge) return;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            if (!any(g) || whole(g)) continue;
+            clear_one<0>(stage, g);
+            clear_one<1>(stage, g);
+            clear_one<2>(stage, g);
+            clear_one<3>(stage, g);
+            clear_one<4>(stage, g);
         }
     }
     // a group of an output [rows, D]
@@ -281,6 +311,7 @@ __device__ __forceinline__ void walk(const R &rows, const RowArgs &a, F &&body) 
         if (two) asm volatile("cp.async.wait_group 1;\n" ::: "memory");
         else asm volatile("cp.async.wait_group 0;\n" ::: "memory");
         __syncwarp();  // (what this warp's lanes copied for one another)
+        rows.clear(stage);
         body(row, stage, parity);
     }
     asm volatile("cp.async.wait_group 0;\n" ::: "memory");

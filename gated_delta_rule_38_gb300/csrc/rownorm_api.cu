@@ -7,7 +7,6 @@ namespace {
 
 // How the rows are spread, staged and walked.  A block keeps two rows' places (one on its way while the other is worked on)
 // where both fit; the grid is what is resident at once.  Shifted rows: the same number of blocks for each remainder.
-// (blocks of 256 threads an SM by registers: two, but three of the gated norm's forward and of whole-vector forwards)
 int period_of(int D) {
     int p = 8;
     while (p > 1 && D % 2 == 0) p /= 2, D /= 2;
@@ -27,6 +26,12 @@ norm::NormShape shape_of(int D) {
     s.threads = s.tpr * s.rpb;
     return s;
 }
+// Blocks an SM that the kernels' registers allow: two of 256 threads, but three of the gated norm's forward and of
+// whole-vector forwards; of smaller blocks as many more.
+int blocks_an_sm(const norm::NormShape &s, bool shift, bool two) {
+    if (s.threads > 256) return s.threads > (shift ? 320 : 256) ? 1 : 2;
+    return (two ? 2 : 3) * 256 / s.threads;
+}
 RowForm form_of(RowArgs *a, bool bwd, bool gated) {
     RowForm f = {};
     f.shift = a->D % 8 != 0;
@@ -35,7 +40,7 @@ RowForm form_of(RowArgs *a, bool bwd, bool gated) {
     for (const RowIn &in : a->in)
         if (in.p) place += (size_t)f.s.nv * f.s.threads * 8 * in.elem;
     const size_t all = 227 * 1024;
-    const int most = f.s.threads > (f.shift ? 320 : 256) ? 1 : f.s.threads > 256 || bwd || (f.shift && !gated) ? 2 : 3;
+    const int most = blocks_an_sm(f.s, f.shift, bwd || (f.shift && !gated));
     auto resident = [&](size_t smem) {
         const int n = (int)(all / (smem + 2048));
         return n < most ? n : most;
@@ -53,7 +58,7 @@ RowForm form_of(RowArgs *a, bool bwd, bool gated) {
 size_t parts_bytes(long long rows, int D, int outs) {
     const norm::NormShape s = shape_of(D);
     const int period = period_of(D);
-    const long long each = (rows + period - 1) / period, need = (each + s.rpb - 1) / s.rpb * period, at_once = (long long)kSMs * (s.threads > (D % 8 ? 320 : 256) ? 1 : 2);
+    const long long each = (rows + period - 1) / period, need = (each + s.rpb - 1) / s.rpb * period, at_once = (long long)kSMs * blocks_an_sm(s, D % 8 != 0, true);
     return round_up((size_t)(need < at_once ? need : at_once) * outs * D * sizeof(float), 256);
 }
 
