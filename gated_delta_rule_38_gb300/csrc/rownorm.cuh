@@ -17,7 +17,7 @@
 // rows do not begin on such a boundary (SHIFT: a width that is no multiple of 8, contiguous tensors) the vectors are those of
 // the tensor, not of the row: row r's first element lies r D mod 8 elements into its first vector.  A block walks rows of one
 // remainder only, so that its threads keep their columns, their weights and their sums; the vectors at a row's ends are
-// masked.  (5311 x 4099, gated norm's backward: 167 us with a column of 2 bytes at a time, 93 so.)
+// masked.  (5311 x 4099, gated norm's backward: 167 us with a column of 2 bytes at a time, 90 so.)
 #pragma once
 
 #include "norm.cuh"
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(BT, BT > 320 ? 1 : BT > 256 ? 2 : 3) gated_fwd
     });
 }
 
-// 8192 x 32 x 128 bf16: 59.5 us for 336 MB, 5.6 TB/s, and 8 us of reduction; 5311 x 4099 fp16: 93 us for 218 MB.  (A row more
+// 8192 x 32 x 128 bf16: 59.5 us for 336 MB, 5.6 TB/s, and 8 us of reduction; 5311 x 4099 fp16: 90 us for 218 MB.  (A row more
 // ahead: 62 and 107 us; what is on its way is not what is short.)
 template <typename T, int NG, int BT, bool SHIFT>
 __global__ void __launch_bounds__(BT, BT > 320 ? 1 : 2) gated_bwd_kernel(const __grid_constant__ RowArgs a) {
