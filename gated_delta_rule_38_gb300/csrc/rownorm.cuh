@@ -21,6 +21,7 @@
 #pragma once
 
 #include "norm.cuh"
+#include "rowclip.h"
 #include "rownorm.h"
 
 namespace gdr {
@@ -105,10 +106,7 @@ struct Rows {
                     // (no bytes, zeros: for what lies behind the row's end or the last row; nothing behind the tensor's end)
                     const int c = (g * a.tpr + t - l) * 8 + h * lanes * 4 + l * 4 - shift;
                     int n = in && (W ? c < a.D && c + 4 > 0 : any(g)) ? 16 : 0;
-                    if (SHIFT && n && row == a.rows - 1) {
-                        const long long left = static_cast<const char *>(a.in[I].p) + a.rows * a.D * elem(I) - from;
-                        n = left < 16 ? (int)(left > 0 ? left : 0) : 16;
-                    }
+                    if (SHIFT && n) n = bytes_to_copy(row, a.rows, static_cast<const char *>(a.in[I].p) + a.rows * a.D * elem(I) - from);
                     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(d), "l"(from), "r"(n) : "memory");
                 }
             }
