@@ -61,14 +61,18 @@ constexpr uint32_t S_LO = RING * TILE;            // the keys' remainders
 constexpr uint32_t S_ST = S_LO + TILE;            // the state's copy (state pass: the remainders of odd chunks); third numbers
 constexpr uint32_t S_BAR = S_ST + TILE;
 constexpr uint32_t B_FULL = S_BAR, B_EMPTY = S_BAR + 8 * RING, B_QK = B_EMPTY + 8 * RING, B_S = B_QK + 8, B_P = B_S + 8,
-                   B_PV = B_P + 8, B_K = B_PV + 8, B_DS = B_K + 16, B_DONE = B_DS + 16, B_QS = B_DONE + 8, S_SLOT = B_QS + 8,
+                   B_PV = B_P + 8, B_K = B_PV + 8, B_DS = B_K + 16, B_DONE = B_DS + 16, B_QS = B_DONE + 8, B_MAX = B_QS + 8,
+                   S_SLOT = B_MAX + 16,
                    S_FLAG = S_SLOT + 4;
 constexpr uint32_t S_FROM = S_FLAG + 4;           // the first chunk whose decayed keys are three numbers
 constexpr uint32_t S_LAM = S_FLAG + 8;            // lambda^128 as two fp32 numbers
 // decays of up to 31 tokens: COL[c] = lambda^(31-c) (rev: lambda^c); DIAG[31 + row - key] = s_kv s_out lambda^|row - key| where
 // the row sees the key, else 0
 constexpr uint32_t S_COL = (S_LAM + 8 + 15) / 16 * 16, S_DIAG = S_COL + 128;
-constexpr uint32_t S_BYTES = S_DIAG + 256 + 1024;
+// fp16: the largest magnitude in each state warp's part of the state, by parity of the chunk; four warps of the same columns
+// side by side
+constexpr uint32_t S_MAX = S_DIAG + 256;
+constexpr uint32_t S_BYTES = S_MAX + 8 * NS + 1024;
 static_assert(S_BYTES <= kSmemMost, "shared memory");
 // tensor memory columns: Q K^T and, in its place, P (each 32 columns in the lower half of their own); Q S; P V; the update
 constexpr uint32_t T_QK = 0, T_QS = 128, T_PV = 256, T_DS = 384;
@@ -349,6 +353,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
             }
             umma::mbar_init(sb + B_DONE, 1);
             umma::mbar_init(sb + B_QS, 1);
+            for (int i = 0; i < 2; ++i) umma::mbar_init(sb + B_MAX + 8 * i, 4);
             umma::fence_mbar_init();
             sts32(flag, 0);
         }
@@ -434,6 +439,19 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
         if (lane == 0) mbar_arrive(bar_of(B_K, c));
     };
 
+    // The state's copy is of the tokens' type.  In fp16 it is taken times a power of two that brings the largest of the 64 columns
+    // that four warps share to between 2^14 and 2^15: the state itself may lie far outside that type's range.  The output rows
+    // take the power back; it follows from the warps' maxima, so that no thread has to keep it.  A maximum is of finite numbers:
+    // twice their bits and one more in the exponent, which for the others wraps to zero's or less.  (Capped where fp32's range
+    // ends.  2 x 4096 tokens, 32 heads: 95 us; 87 without, and with states past 65504 infinite.  Maxima of pairs of the rounded
+    // copy, of three numbers an instruction, or asked for only when the copy's product has begun: 95 to 98.)
+    auto maxima = [&](int c) { return sb + S_MAX + (uint32_t)((c & 1) * NS + ((warp >> 2) & 1) * 4) * 4; };
+    auto copy_shift = [&](int c) {
+        const uint4 m = umma::ld_shared_v4(maxima(c));
+        return min(127 + 1 + 14 - (int)(max(max(m.x, m.y), max(m.z, m.w)) >> 24), 100);
+    };
+    auto two_to = [](int e) { return __uint_as_float((uint32_t)(127 + e) << 23); };
+
     // The block of P `dist` blocks of 32 from the diagonal in this warp's rows, if there is one: lambda^|r-s| as a row's factor
     // (distance to the block's near edge) times a column's (from there), both at most 1.
     auto p_beyond = [&](int dist, int L) {
@@ -472,7 +490,8 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
         const uint32_t quad = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const bool use_s = c > 0 || has_start;
         umma::fence_after();
-        const float rf = use_s ? w.s_out * w.s_state * ex2((float)(rev ? L - 1 - row : row + 1) * lg) : 0.f;
+        float rf = use_s ? w.s_out * w.s_state * ex2((float)(rev ? L - 1 - row : row + 1) * lg) : 0.f;
+        if (!IsBf16<T>::value) rf *= two_to(-copy_shift(c));
         const long long at = (((long long)t + row) * a.H + j) * vd;
         const bool wide = row < L && vd % 16 == 0 && reinterpret_cast<uintptr_t>(w.out) % 32 == 0;
 #pragma unroll 1
@@ -742,19 +761,43 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                 }
             }
         }
-        auto put_state = [&]() {
-            if (c0 < NV) {
-#pragma unroll
-                for (int i = 0; i < CW / 8; ++i)
-                    umma::st_shared_v4(sb + S_ST + place(i), narrow2<T>(st[4 * i]), narrow2<T>(st[4 * i + 1]),
-                                       narrow2<T>(st[4 * i + 2]), narrow2<T>(st[4 * i + 3]));
+        uint32_t most = 0;
+        auto see = [&](int i) {  // takes pair i of the state into its maximum
+            float x[2];
+            unpack2(st[i], x[0], x[1]);
+            const uint32_t u = max(__float_as_uint(x[0]) * 2 + 0x01000000u, __float_as_uint(x[1]) * 2 + 0x01000000u);
+            if (!IsBf16<T>::value && c0 + i / 4 * 8 < vd) most = max(most, u);
+        };
+        // the copy for chunk c
+        auto put_state = [&](int c) {
+            if (c0 >= NV) return true;
+            f2 f = both(1.f);
+            if constexpr (!IsBf16<T>::value) {
+                // (columns behind vd and rows behind kd hold what was left in tensor memory and in the tile)
+                const uint32_t m = __reduce_max_sync(0xffffffffu, live ? most : 0u);
+                const uint32_t bar = sb + B_MAX + 8 * (warp >> 2);
+                if (lane == 0) {
+                    sts32(maxima(c) + 4 * (warp & 3), m);
+                    mbar_arrive(bar);
+                }
+                if (!wwait(bar, c & 1, flag, a.err)) return false;
+                f = both(two_to(copy_shift(c)));
             }
+#pragma unroll
+            for (int i = 0; i < CW / 8; ++i) {
+                uint32_t h[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) h[e] = narrow2<T>(IsBf16<T>::value ? st[4 * i + e] : mul2(st[4 * i + e], f));
+                umma::st_shared_v4(sb + S_ST + place(i), h[0], h[1], h[2], h[3]);
+            }
+            return true;
         };
         // the state after chunk c
         auto update = [&](int c, int L) {
             if (c0 >= NV) return;
             umma::fence_after();
             const f2 l1 = both(L == LC ? lds_f(sb + S_LAM) : ex2((float)L * lg)), l2 = both(L == LC ? lds_f(sb + S_LAM + 4) : 0.f);
+            most = 0;
             const uint32_t at = quad + T_DS - (STATES && (c & 1) ? 128 : 0) + c0;
 #pragma unroll
             for (int h = 0; h < CW / 32; ++h) {
@@ -765,6 +808,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                 for (int i = 0; i < 16; ++i) {
                     f2 &v = st[16 * h + i];
                     v = fma2(l1, v, fma2(l2, v, f2_of(x[2 * i], x[2 * i + 1])));
+                    if (!STATES) see(16 * h + i);
                 }
             }
             umma::fence_before();
@@ -784,11 +828,13 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
         const int k0 = STATES ? 8 + c0 / 16 : c0 ? 6 : 0, k1 = min(STATES ? k0 + 4 : c0 ? 10 : 6, 8 * kblk);
         bool ok = true;
         if (!STATES) {
-            put_state();
+#pragma unroll
+            for (int i = 0; i < CW / 2; ++i) see(i);
+            ok = put_state(0);
             umma::fence_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(sb + B_S);
-            if (nc > 0) {
+            if (ok && nc > 0) {
                 int t, L;
                 chunk(0, t, L);
                 ok = make_p(0, L);
@@ -820,7 +866,8 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                     update(c, L);
                 }
                 if (c + 1 < nc) {
-                    put_state();
+                    ok = put_state(c + 1);
+                    if (!ok) break;
                     umma::fence_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sb + B_S);

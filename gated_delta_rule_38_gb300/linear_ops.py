@@ -59,7 +59,8 @@ def linear_attention_fwd(q, k, v, decay, scale=None, initial_state=None, output_
     q, k [B,T,Hk,K] and v [B,T,H,V] bf16 or fp16 (head j reads q/k head j // (H/Hk)), K and V from 8 to 128 in steps of 8;
     ``decay`` [H] fp32, at most 0: a constant of the heads, without a gradient; ``scale`` is K ** -0.5 unless given.
     ``initial_state`` [N,H,K,V] fp32 (None: zeros) and final_state (None unless ``output_final_state``): one a row, or a
-    sequence of a packed batch (``cu_seqlens``).  ``out`` must not overlap q, k or v.
+    sequence of a packed batch (``cu_seqlens``).  ``out`` must not overlap q, k or v.  States may be of any size; with fp16
+    the products scale q.k (backwards also scale do.v) have to stay within 65504.
     """
     cu = _cu(cu_seqlens)
     p, q, k, v, sshape = _problem(q, k, v, decay, scale, cu)
@@ -78,7 +79,7 @@ def linear_attention_fwd(q, k, v, decay, scale=None, initial_state=None, output_
 
 def linear_attention_step(q, k, v, decay, state, scale=None, out=None):
     """o for one new token (or a few) of every row; ``state`` [B,H,K,V] fp32 is updated in place.  Equals
-    linear_attention_fwd over the same tokens."""
+    linear_attention_fwd over the same tokens up to rounding (fp32 throughout: no product of 16-bit numbers)."""
     p, q, k, v, sshape = _problem(q, k, v, decay, scale, None, step=True)
     _need(state, "state", sshape, torch.float32, q)
     if out is not None:

@@ -423,10 +423,11 @@ gdr_status gdr_scan_bwd(const gdr_scan_problem *p, const void *x, const void *dt
  * row strides multiples of 8 (GDR_ERR_ALIGN).  o and state_out overlap no input and not one
  * another (GDR_ERR_UNSUPPORTED).  Packed batches and malformed cu_seqlens as in gdr_conv_fwd.
  * T = 0 passes the states through.  A value that is not finite reaches the outputs of its own
- * sequence and head only, from its chunk of 128 tokens on.  The states are fp32; what enters a
- * product of 16-bit matrices (scale q.k, the decayed keys, the copy of a state that q meets) is in
- * the tokens' type, so with fp16 those have to stay within its range (65504; below 6e-5 they lose
- * bits).  Where sequences and heads do not fill the chip the token axis is cut (workspace:
+ * sequence and head only, from its chunk of 128 tokens on.  The states are fp32 and may be of any
+ * size: the copy that q meets has the tokens' type, in fp16 with a power of two of its own.  The
+ * products scale q.k (backward also scale dout.v), which meet v, are in the tokens' type as they
+ * are, so with fp16 they have to stay within its range (65504; below 6e-5 they lose bits);
+ * gdr_lin_step is fp32 throughout.  Where sequences and heads do not fill the chip the token axis is cut (workspace:
  * gdr_lin_workspace_size, 256-byte aligned).
  * gdr_lin_step: dense rows, the states updated in place; meant for T = 1 or a few tokens; its
  * token tensors are aligned to their elements only.

@@ -353,3 +353,60 @@ def test_refusals():
                  lambda: gdr.linear_attention_fwd(torch.cat([q, q], 2), torch.cat([k, k], 2), torch.cat([v, v[:, :, :1]], 2), slopes(3))):
         with pytest.raises(gdr.GdrError):
             call()
+
+
+@DT
+@pytest.mark.parametrize("size", [3e-7, 300.0, 2e5, 1e9])
+def test_states_past_the_tokens_range(size, dt):
+    """States larger and smaller than the tokens' type holds, under a scale that brings the outputs back into it: the copy of a
+    state that a query meets has a power of two of its own.  (Keys and values are zeros, so that the states alone show.)"""
+    T, H, D = 300, 2, 64
+    randn = gen(7)
+    q, do = randn(1, T, H, D, dtype=dt), randn(1, T, H, D, dtype=dt)
+    zero, s0, d = torch.zeros_like(q), randn(1, H, D, D, scale=size), torch.tensor([0.0, -0.001], device="cuda")
+    leaves = [lref.f64(t) for t in (q, zero, zero, s0)]
+    ow, fw = ref.attn(*leaves[:3], d.double().cpu(), 1 / size, leaves[3], None)
+    (ow * do.double().cpu()).sum().backward()
+    o, fin = gdr.linear_attention_fwd(q, zero, zero, d, scale=1 / size, initial_state=s0, output_final_state=True)
+    ref.check(o, ow, ref.attn_bound(o, dt), "o")
+    ref.check(fin, fw, ref.attn_bound(fin, dt), "final_state")
+    dq, dk, dv, ds = gdr.linear_attention_bwd(q, zero, zero, d, do, scale=1 / size, initial_state=s0)
+    ref.check(dq, leaves[0].grad, ref.attn_bound(dq, dt), "dq")
+    ref.check(ds, leaves[3].grad, ref.attn_bound(ds, dt), "dinitial_state")
+    assert (dk == 0).all() and (dv == 0).all()
+
+
+def test_sums_past_fp16():
+    """Tokens of one sign and no decay: the states (backwards: their gradients) pass 65504 on the way, the outputs do not."""
+    T, D = 3000, 64
+    randn, d = gen(1), torch.zeros(1, device="cuda")
+    full = lambda x: torch.full((1, T, 1, D), x, dtype=FH, device="cuda")  # noqa: E731
+    q, k, v = randn(1, T, 1, D, dtype=FH, scale=1e-3), full(8.0), full(4.0)
+    o, fin = gdr.linear_attention_fwd(q, k, v, d, output_final_state=True)
+    ow, fw = ref.attn(*(lref.f64(t, False) for t in (q, k, v)), d.double().cpu(), D ** -0.5, None, None)
+    assert float(fw.max()) > 65504 and float(ow.abs().max()) < 6e4
+    ref.check(o, ow, ref.attn_bound(o, FH), "o")
+    ref.check(fin, fw, ref.attn_bound(fin, FH), "final_state")
+    q, do = full(32.0), full(16.0)
+    k, v = randn(1, T, 1, D, dtype=FH, scale=1e-3), randn(1, T, 1, D, dtype=FH, scale=1e-3)
+    leaves = [lref.f64(t) for t in (q, k, v)]
+    (ref.attn(*leaves, d.double().cpu(), D ** -0.5, None, None)[0] * do.double().cpu()).sum().backward()
+    for name, got, leaf in zip(("dq", "dk", "dv"), gdr.linear_attention_bwd(q, k, v, d, do), leaves):
+        assert float(leaf.grad.abs().max()) < 6e4
+        ref.check(got, leaf.grad, ref.attn_bound(got, FH), name)
+
+
+@DT
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_one_column_that_is_not_finite(value, dt):
+    """A value of v that is not finite stays in its column: the others' copy of the state is as good as without it."""
+    T, D = 300, 64
+    x, d = make(1, T, 1, 1, D, D, None, True, dt), torch.tensor([-0.01], device="cuda")
+    args = [lref.f64(x[n], False) for n in ("q", "k", "v", "s0")]
+    ow, fw = ref.attn(*args[:3], d.double().cpu(), D ** -0.5, args[3], None)
+    x["v"][0, 40, 0, 5] = value
+    o, fin = gdr.linear_attention_fwd(x["q"], x["k"], x["v"], d, initial_state=x["s0"], output_final_state=True)
+    keep = [c for c in range(D) if c != 5]
+    ref.check(o[..., keep], ow[..., keep], ref.attn_bound(o, dt), "o")
+    ref.check(fin[..., keep], fw[..., keep], ref.attn_bound(fin, dt), "final_state")
+    assert not torch.isfinite(o[0, 128:, 0, 5].float()).any() and not torch.isfinite(fin[..., 5]).any()
