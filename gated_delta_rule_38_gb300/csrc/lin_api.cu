@@ -53,10 +53,15 @@ LinArgs args_of(const gdr_lin_problem *p, const float *decay, int walks) {
     cut(p, walks, &a);
     return a;
 }
-// The scale of a walk's keys, and its power of two (within 2^+-24) apart.
+// The scale of a walk's keys, and its power of two (within 2^+-24) apart; what is left is 1 at most, so that no key leaves its
+// type's range.
 void set_scale(Walk *w, float s) {
     int e = 0;
-    if (std::isfinite(s) && s != 0.f) e = std::ilogb(s), e = e > 24 ? 24 : e < -24 ? -24 : e;
+    if (std::isfinite(s) && s != 0.f) {
+        e = std::ilogb(s);
+        if (std::fabs(s) > std::ldexp(1.f, e)) ++e;
+        e = e > 24 ? 24 : e < -24 ? -24 : e;
+    }
     w->s_kv = s, w->s_state = std::ldexp(1.f, e), w->s_key = s / w->s_state;
 }
 bool split(const LinArgs &a) { return a.main_len < a.T; }

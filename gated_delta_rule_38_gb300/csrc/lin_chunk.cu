@@ -29,7 +29,8 @@
 // in fp16 their remainders would fall below its range.
 // A decayed key is a sum of 16-bit numbers, the rounded one and what that leaves, each with a product of its own, the
 // smallest first: the accumulator loses at each addition by what it holds.  Two of fp16 make 22 bits and states 2e-7 off
-// (of one number: 1e-3).  Two of bf16 make 17 bits and 2.5e-6, which outputs of 8 bits do not show; states that are handed
+// (of one number: 1e-3); the second is held times 2^11, or below a key of 0.1 it would be a subnormal number, and its
+// products' sum is scaled back when the first number's are added (keys of 1e-3: states 2e-5 off without).  Two of bf16 make 17 bits and 2.5e-6, which outputs of 8 bits do not show; states that are handed
 // on get a third where the chunk weighs over an eighth in them (3e-7).  Its place is the state's copy's, free between Q S
 // and the next copy, and warps 8..11 make all the keys of such a chunk: the state's warps have no registers for it.
 // (2 x 4096 tokens, 32 heads of memories of 100 tokens: 88 us with the final states, 79 without; where nothing decays, so
@@ -181,6 +182,14 @@ __device__ __forceinline__ void mma_ss(uint32_t on, uint32_t d, uint64_t a, uint
         "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
         "l"(a), "l"(b), "r"(id), "r"((uint32_t)accumulate), "r"(on));
+}
+// D = A B + D / 2^11.
+constexpr float kLoScale = 2048.f;
+__device__ __forceinline__ void mma_ss_down(uint32_t on, uint32_t d, uint64_t a, uint64_t b, uint32_t id) {
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.eq.b32 p, %4, %4;\nsetp.ne.b32 q, %4, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p, 11;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(id), "r"(on));
 }
 // ... with A in tensor memory.
 __device__ __forceinline__ void mma_ts(uint32_t on, uint32_t d, uint32_t a, uint64_t b, uint32_t id, bool accumulate) {
@@ -423,7 +432,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                         const f2 v = mul2(widen2<T>(x[e]), both(f));
                         h[e] = narrow2<T>(v);
                         const f2 r = fma2(widen2<T>(h[e]), both(-1.f), v);
-                        l[e] = narrow2<T>(r);
+                        l[e] = narrow2<T>(IsBf16<T>::value ? r : mul2(r, both(kLoScale)));
                         if (M == 3) m[e] = narrow2<T>(fma2(widen2<T>(l[e]), both(-1.f), r));
                     }
                     umma::st_shared_v4(kt + at[k], h[0], h[1], h[2], h[3]);
@@ -578,7 +587,10 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
             const uint64_t dv = umma::desc(sb + slot_of(c, VI) * TILE, BLK, 1024), dk = umma::desc(keys, BLK, 1024);
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-                if (ks < ts) mma_ss(on, d, desc_at(dk, ks * 2048u), desc_at(dv, ks * 2048u), i_ds, more || ks > 0);
+                if (ks < ts) {
+                    if (ks == 0 && !bf && more) mma_ss_down(on, d, dk, dv, i_ds);
+                    else mma_ss(on, d, desc_at(dk, ks * 2048u), desc_at(dv, ks * 2048u), i_ds, more || ks > 0);
+                }
         };
         if (!STATES && nc > 0) {
             wait_qk(0);

@@ -410,3 +410,20 @@ def test_one_column_that_is_not_finite(value, dt):
     ref.check(o[..., keep], ow[..., keep], ref.attn_bound(o, dt), "o")
     ref.check(fin[..., keep], fw[..., keep], ref.attn_bound(fin, dt), "final_state")
     assert not torch.isfinite(o[0, 128:, 0, 5].float()).any() and not torch.isfinite(fin[..., 5]).any()
+
+
+@DT
+@pytest.mark.parametrize("size", [0.1, 1e-2, 1e-3, 1e-4])
+def test_states_of_small_keys(size, dt):
+    """As test_states_are_fp32, for keys (backwards: queries) whose second number would be a subnormal one of fp16."""
+    x = make(1, 1100, 1, 2, 128, 128, None, False, dt)
+    d = torch.full((2,), -0.004, device="cuda")
+    q, k = ((x[n].float() * size).to(dt) for n in ("q", "k"))
+    s0 = torch.zeros(1, 2, 128, 128, device="cuda")
+    _, fin = gdr.linear_attention_fwd(q, k, x["v"], d, initial_state=s0, output_final_state=True)
+    args = [lref.f64(t) for t in (q, k, x["v"], s0)]
+    ow, fw = ref.attn(*args[:3], d.double().cpu(), 128 ** -0.5, args[3], None)
+    ref.check(fin, fw, 1e-6, "final_state")
+    (ow * x["do"].double().cpu()).sum().backward()
+    ds = gdr.linear_attention_bwd(q, k, x["v"], d, x["do"], initial_state=s0)[3]
+    ref.check(ds, args[3].grad, 1e-6, "dinitial_state")
