@@ -427,3 +427,16 @@ def test_states_of_small_keys(size, dt):
     (ow * x["do"].double().cpu()).sum().backward()
     ds = gdr.linear_attention_bwd(q, k, x["v"], d, x["do"], initial_state=s0)[3]
     ref.check(ds, args[3].grad, 1e-6, "dinitial_state")
+
+
+@pytest.mark.parametrize("decay", [0.0, -1e-5, -1e-4, -1e-3, -0.03, -0.49, -0.51, -3.0])
+def test_many_steps(decay):
+    """States stepped thousands of times stay as good as their own roundings leave them: two a token, each at most 2^-24 of the
+    state (which grows, or is forgotten, so that none weighs more at the end), in the mean square 2^-24 sqrt(2 T / 3); what a
+    rounded decay would add is T 2^-25 and not random."""
+    T, D = 4000, 32
+    x, d = make(1, T, 1, 2, D, D), torch.full((2,), decay, device="cuda")
+    state = x["s0"].clone()
+    gdr.linear_attention_step(x["q"], x["k"], x["v"], d, state)
+    fw = ref.attn(*(lref.f64(x[n], False) for n in ("q", "k", "v")), d.double().cpu(), 1.0, lref.f64(x["s0"], False), None)[1]
+    ref.check(state, fw, 2.0 ** -24 * (2 * T / 3) ** 0.5, "state")
