@@ -65,11 +65,8 @@ def _cu(cu_seqlens):
     return cu_seqlens.contiguous()
 
 
-def _rows(t, inner=1):
-    """(t, row stride): a tensor whose last ``inner`` dimensions are contiguous and whose rows follow one another at
-    one stride (a slice of a fused projection is one); any other view is copied."""
-    if t.is_contiguous():
-        return t, t.shape[-1] if inner == 1 else t.shape[-1] * t.shape[-2]
+def _row_stride(t, inner=1):
+    """The one stride at which a tensor's rows (its last ``inner`` dimensions, contiguous) follow one another, or None."""
     n = 1
     for d in t.shape[t.dim() - inner:]:
         n *= d
@@ -87,6 +84,15 @@ def _rows(t, inner=1):
         ok = ok and t.stride(i) == step
         step = t.stride(i) * t.shape[i]
     ld = n if ld is None else ld
-    if ok and ld >= n:
-        return t, ld
-    return t.contiguous(), n
+    return ld if ok and ld >= n else None
+
+
+def _rows(t, inner=1):
+    """(t, row stride): a tensor whose last ``inner`` dimensions are contiguous and whose rows follow one another at
+    one stride (a slice of a fused projection is one); any other view is copied."""
+    if not t.is_contiguous():
+        ld = _row_stride(t, inner)
+        if ld is not None:
+            return t, ld
+        t = t.contiguous()
+    return t, t.shape[-1] if inner == 1 else t.shape[-1] * t.shape[-2]

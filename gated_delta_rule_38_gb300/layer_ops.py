@@ -17,7 +17,7 @@ from functools import wraps
 import torch
 
 from . import _lib
-from ._args import _DT, _check, _check_cu, _cu, _need, _rows
+from ._args import _DT, _check, _check_cu, _cu, _need, _row_stride, _rows
 
 __all__ = ["rms_norm", "rms_norm_fwd", "rms_norm_bwd", "short_conv", "short_conv_fwd", "short_conv_bwd",
            "short_conv_step", "selective_scan", "selective_scan_fwd", "selective_scan_bwd", "selective_scan_step",
@@ -216,8 +216,10 @@ def _gated_problem(x, gate, weight, eps, activation):
     _need(weight, "weight", (D,), weight.dtype, x)
     if activation not in ("silu", "sigmoid"):
         raise ValueError(f"activation is {activation!r}, expected 'silu' or 'sigmoid'")
-    # heads of a token lie side by side, tokens at a stride
-    heads = x.shape[-2] if x.dim() > 2 else 1
+    # rows at one stride; or heads of a token side by side, tokens at a stride
+    heads = 1
+    if x.dim() > 2 and not all(t.is_contiguous() or _row_stride(t) is not None for t in (x, gate)):
+        heads = x.shape[-2]
     inner = 2 if heads > 1 else 1
     x, x_ld = _vectors(x, D, heads * D, inner)
     gate, g_ld = _vectors(gate, D, heads * D, inner)

@@ -366,3 +366,31 @@ def test_layer():
             # the same roundings, but those of P and of the state's copy: 2 U / sqrt(3) a layer, damped by the residual scale
             ref.check(got, hh[0, n:], 1e-2, "row %d" % i)
             at += n
+
+
+@pytest.mark.parametrize("shape", [(0, 64), (2, 0, 64), (2, 3, 0, 64), (2, 0, 4, 64), (0, 4, 63)], ids=str)
+def test_gated_without_rows(shape):
+    x, w = torch.empty(*shape, dtype=BF, device="cuda"), torch.ones(shape[-1], device="cuda")
+    assert gdr.gated_rms_norm_fwd(x, x, w).shape == x.shape
+    dx, dg, dw = gdr.gated_rms_norm_bwd(x, x, w, x)
+    assert dx.shape == x.shape and dg.shape == x.shape and (dw == 0).all()
+
+
+@pytest.mark.parametrize("shape", [(3, 50, 64), (150, 64), (2, 3, 25, 64), (3, 50, 2, 64)], ids=str)
+def test_gated_slices_are_read_in_place(shape):
+    """Columns of a wider projection, a norm over the whole width or a head: no copy, the same bits."""
+    from gated_delta_rule_38_gb300 import layer_ops
+    randn = gen(5)
+    width = shape[-1] if shape[-2] != 2 else 2 * shape[-1]
+    lead = shape[:-1] if shape[-2] != 2 else shape[:-2]
+    wide, w = randn(*lead, 2 * width + 16, dtype=BF), 1 + 0.1 * randn(shape[-1])
+    x, g = (wide[..., i:i + width].view(*lead, *shape[len(lead):]) for i in (0, width + 8))
+    p, xr, gr, _ = layer_ops._gated_problem(x, g, w, 1e-6, "silu")
+    assert xr.data_ptr() == x.data_ptr() and gr.data_ptr() == g.data_ptr() and p.x_ld == p.gate_ld == 2 * width + 16
+    dy = randn(*shape, dtype=BF)
+    want = (gdr.gated_rms_norm_fwd(x.contiguous(), g.contiguous(), w), *gdr.gated_rms_norm_bwd(x.contiguous(), g.contiguous(), w, dy))
+    got = (gdr.gated_rms_norm_fwd(x, g, w), *gdr.gated_rms_norm_bwd(x, g, w, dy))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # one of them without gaps, the other a slice
+    got = (gdr.gated_rms_norm_fwd(x, g.contiguous(), w), gdr.gated_rms_norm_fwd(x.contiguous(), g, w))
+    assert all(torch.equal(a, want[0]) for a in got)
