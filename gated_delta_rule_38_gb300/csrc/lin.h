@@ -11,7 +11,6 @@ namespace lin {
 
 constexpr int LC = 128;               // tokens a chunk
 constexpr int LD = 128;               // the largest head dim: the tiles' width
-constexpr int kStateFloats = LD * LD; // one state of the segments' exchange, padded
 
 // One walk over the tokens,  out_r = s_out (sum over s <= r of s_kv lambda^(r-s) (q_r . k_s) v_s + the start's part),
 // or backwards in time (s >= r).  Forward: (q, k, v) -> o.  Backward: (do, v, k) -> dq, and backwards in time
@@ -26,9 +25,9 @@ struct Walk {
     const float *start;      // states before the walk's first token (rev: gradients behind the last), or null
     float *end;              // states behind its last token (rev: gradients before the first), or null
     int rs, cs;              // element (row of kd, column of vd) of start and end: row * rs + column * cs
-    const float *ext;        // the windows' own end states, [place][H][128 x 128], element row * ers + column * ecs
+    const float *ext;        // the windows' own end states, [place][H][kd x vd], element row * ers + column * ecs
     int ers, ecs;
-    float *states;           // the state pass' output: those states, element column * 128 + row
+    float *states;           // the state pass' output: those states, element column * ecs + row
     void *out;               // [tokens][H][vd], 16-bit or fp32
     bool out_f32;
 };
@@ -53,6 +52,9 @@ inline long long lin_slots(const LinArgs &a, int len) {
     const long long per = (a.T + (long long)len - 1) / len;
     return a.cu ? a.N + per : (long long)a.N * (per > 0 ? per : 1);
 }
+
+// Exchanged states of a walk and head: one of every interval of len tokens.
+inline long long lin_places(const LinArgs &a, int len) { return (a.T + (long long)len - 1) / len * (a.cu ? 1 : a.N); }
 
 cudaError_t launch_lin_walks(const LinParams &p, bool bf16, cudaStream_t s);
 cudaError_t launch_lin_states(const LinParams &p, bool bf16, cudaStream_t s);

@@ -74,7 +74,7 @@ Layout layout_of(const gdr_lin_problem *p, bool bwd) {
     Layout l;
     const LinArgs a = args_of(p, nullptr, bwd ? 3 : 1);
     if (split(a)) {
-        l.one = (size_t)lin_slots(a, a.win_len) * p->H * kStateFloats * sizeof(float);
+        l.one = round_up((size_t)lin_places(a, a.win_len) * p->H * p->K * p->V * sizeof(float), 256);
         l.bytes += l.one * (bwd ? 2 : 1);
     }
     if (bwd && p->H != p->Hk) {
@@ -142,7 +142,7 @@ gdr_status gdr_lin_fwd(const gdr_lin_problem *p, const void *q, const void *k, c
     set_scale(&w, 1.f), w.s_out = p->scale;
     w.start = state_in, w.end = state_out, w.rs = p->V, w.cs = 1;
     w.states = static_cast<float *>(workspace);
-    w.ext = w.states, w.ers = 1, w.ecs = LD;
+    w.ext = w.states, w.ers = 1, w.ecs = p->K;
     w.out = o;
     const bool bf = p->dtype == GDR_BF16;
     if (split(lp.a) && (st = timed(K_LIN_STATES, cs, [&] { return launch_lin_states(lp, bf, cs); })) != GDR_OK) return st;
@@ -220,7 +220,7 @@ gdr_status gdr_lin_bwd(const gdr_lin_problem *p, const void *q, const void *k, c
     v_.q_div = v_.k_div = grp, v_.v_div = 1;
     v_.rev = true, set_scale(&v_, p->scale), v_.s_out = 1.f;
     v_.start = dstate_out, v_.end = dstate_in, v_.rs = p->V, v_.cs = 1;
-    v_.states = bw, v_.ext = bw, v_.ers = 1, v_.ecs = LD;
+    v_.states = bw, v_.ext = bw, v_.ers = 1, v_.ecs = p->K;
     v_.out = dv;
     // dk: the same states, transposed
     Walk &k_ = lp.w[2];
@@ -229,7 +229,7 @@ gdr_status gdr_lin_bwd(const gdr_lin_problem *p, const void *q, const void *k, c
     k_.q_div = k_.k_div = 1, k_.v_div = grp;
     k_.rev = true, set_scale(&k_, p->scale), k_.s_out = 1.f;
     k_.start = dstate_out, k_.rs = 1, k_.cs = p->V;
-    k_.ext = bw, k_.ers = LD, k_.ecs = 1;
+    k_.ext = bw, k_.ers = p->K, k_.ecs = 1;
     k_.out = grp > 1 ? static_cast<void *>(pk) : dk, k_.out_f32 = grp > 1;
     // dq: the forward's states, transposed
     Walk &q_ = lp.w[0];
@@ -238,7 +238,7 @@ gdr_status gdr_lin_bwd(const gdr_lin_problem *p, const void *q, const void *k, c
     q_.q_div = q_.k_div = 1, q_.v_div = grp;
     set_scale(&q_, 1.f), q_.s_out = p->scale;
     q_.start = state_in, q_.rs = 1, q_.cs = p->V;
-    q_.states = fw, q_.ext = fw, q_.ers = 1, q_.ecs = LD;
+    q_.states = fw, q_.ext = fw, q_.ers = 1, q_.ecs = p->V;
     q_.out = grp > 1 ? static_cast<void *>(pq) : dq, q_.out_f32 = grp > 1;
     const bool bf = p->dtype == GDR_BF16;
     if (split(lp.a)) {

@@ -270,7 +270,10 @@ struct Cuts {
         if (s.t1 == s.t0 && !(start && s.seq1 == s.seq0)) s.n = -1;
         return s;
     }
-    // Within a sequence: the next cut behind t, the last one at or before it, and the place of the piece that begins at t.
+    // Within a sequence: the next cut behind t, the last one at or before it, and the place of the exchanged state of the piece
+    // that begins at t.  Packed: the interval of the token axis that it lies in (its place in the order, less the starts before).
+    // Of the pieces in one interval a segment only ever wants one, the one whose sequence goes on behind it (backwards: before
+    // it).
     __device__ __forceinline__ int base(const Seg &s) const { return a.cu ? 0 : s.seq0; }
     __device__ __forceinline__ int next(const Seg &s, int t) const {
         const long long c = base(s) + ((long long)(t - base(s)) / len + 1) * len;
@@ -278,8 +281,7 @@ struct Cuts {
     }
     __device__ __forceinline__ int last(const Seg &s, int t) const { return base(s) + (t - base(s)) / len * len; }
     __device__ __forceinline__ long long place(const Seg &s, int t) const {
-        if (!a.cu) return (long long)s.n * per() + (t - s.seq0) / len;
-        return t % len ? (long long)s.n + (s.seq0 + (long long)len - 1) / len : (long long)s.n + 1 + t / len;
+        return a.cu ? t / len : (long long)s.n * per() + (t - s.seq0) / len;
     }
 };
 
@@ -763,7 +765,7 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
                     const int at = pos;
                     const int from = rev ? max(wc.last(seg, pos - 1), seg.seq0) : pos;
                     pos = rev ? from : wc.next(seg, pos);
-                    const float *e = w.ext + (wc.place(seg, from) * a.H + j) * kStateFloats + (long long)row * w.ers;
+                    const float *e = w.ext + (wc.place(seg, from) * a.H + j) * (kd * vd) + (long long)row * w.ers;
                     const f2 d = both(ex2((float)(rev ? at - from : pos - at) * lg));
 #pragma unroll
                     for (int i = 0; i < CW / 2; ++i) {
@@ -895,9 +897,9 @@ __global__ void __launch_bounds__(NT, 1) lin_walk_kernel(const __grid_constant__
             if (ok) update(nc - 1, before);
         }
         if (ok && want_end && live) {
-            const long long n = STATES ? (long long)slot : (long long)seg.n;
-            float *e = STATES ? w.states + (n * a.H + j) * kStateFloats + row : w.end + (n * a.H + j) * kd * vd + (long long)row * w.rs;
-            const long long cs = STATES ? LD : w.cs;
+            const long long n = STATES ? (long long)(a.cu ? slot - seg.n - 1 : slot) : (long long)seg.n;  // (as `place`, which is dearer)
+            float *e = STATES ? w.states + (n * a.H + j) * (kd * vd) + row : w.end + (n * a.H + j) * kd * vd + (long long)row * w.rs;
+            const long long cs = STATES ? w.ecs : w.cs;
 #pragma unroll
             for (int i = 0; i < CW / 4; ++i) {
                 const int col = c0 + 4 * i;

@@ -119,6 +119,24 @@ def test_lin_workspaces(lib):
     assert bwd(lib, long, ws=None) == WORKSPACE and bwd(lib, long, need - 1) == WORKSPACE and bwd(lib, long, need, ws=P + 16) == ALIGN
 
 
+def test_lin_workspace_of_many_sequences(lib):
+    """The states that segments exchange are those of intervals of the token axis, of the heads' own size, however many sequences
+    a packed batch has."""
+    n = ctypes.c_size_t()
+
+    def size(T, N, H=32, K=128, V=128, backward=0):
+        p = _lib.LinProblem(1, T, H, H, K, V, H * K, H * K, H * V, 0, 1.0, P, N)
+        assert lib.gdr_lin_workspace_size(ctypes.byref(p), backward, ctypes.byref(n)) == 0
+        return n.value
+
+    for T, H in ((16384, 32), (8192, 32), (65536, 4), (3000, 2)):
+        for N in (2, 7, 64, 1024, 4096):
+            for b in (0, 1):
+                # at most a state of 64 KB of every chunk, head and walk (q, k, v and o: 128 KB)
+                assert size(T, N, H, backward=b) <= (1 + b) * (T // 128 + 1) * H * 65536, (T, H, N, b)
+    assert size(65536, 3, 4) > 0 and size(65536, 3, 4, 32, 64) <= size(65536, 3, 4) // 8 + 512
+
+
 def gated(**kw):
     p = _lib.GatedNormProblem(7, 256, 256, 4, 64, 0, 2, 2, 1e-6)
     for k, v in kw.items():
