@@ -23,21 +23,29 @@ gdr_status check_lin(const gdr_lin_problem *p) {
     return GDR_OK;
 }
 
-// The cut: tokens of a segment and of a window, with the least estimated time.  In microseconds, as measured: a chunk takes 4
-// in a walk and 2.2 in the state pass, a block's start and end 6 in both, each window before a segment 0.5 where its state is
-// summed up, a second launch 2.  (2 x 4096 tokens, 32 heads: 94 us with 2 segments; 1 x 65536, 16 heads: 312 with 9, 396 with 19.)
+// The cut: tokens of a segment and of a window, with the least estimated time.  In microseconds, as measured with heads of 128
+// (narrower ones are priced alike): a chunk takes 4 in a walk and 2.2 in the state pass, a block's start and end 6 in both, each
+// window before a segment 0.5 where its state is summed up, a second launch 2, a block that finds nothing to do 1.  (2 x 4096
+// tokens, 32 heads: 94 us with 2 segments; 1 x 65536, 16 heads: 312 with 9, 396 with 19.)
+// The lengths of a packed batch's sequences are not known here.  Any of them may be nearly all tokens, so that the longest walk
+// is a segment's; each of the others begins one more block, of a chunk, which fill the SMs that the segments leave idle and,
+// where there are many, are what the call takes, however it is cut.
 void cut(const gdr_lin_problem *p, int walks, LinArgs *a) {
-    const long long nc = (p->T + LC - 1) / LC, heads = (long long)p->H * walks;
-    const long long rows = p->cu_seqlens ? 1 : p->B, more = p->cu_seqlens ? p->num_seqs : 0;
-    auto rounds = [&](long long blocks) { return (double)((blocks + kSMs - 1) / kSMs); };
+    const long long nc = (p->T + LC - 1) / LC, heads = (long long)p->H * walks, pairs = (long long)p->H * (walks > 1 ? 2 : 1);
+    const long long rows = p->cu_seqlens ? 1 : p->B, more = p->cu_seqlens ? p->num_seqs - 1 : 0;
+    // blocks of one length each, and `more` heads' blocks of another
+    auto time = [&](long long blocks, double each, long long others, double other) {
+        const double alone = (double)((blocks + kSMs - 1) / kSMs) * each, all = ((double)blocks * each + (double)others * other) / kSMs;
+        return alone > all ? alone : all;
+    };
     double best = -1;
     a->main_len = a->win_len = (int)((nc > 0 ? nc : 1) * LC);
     for (long long n = 1; n <= nc && n <= 512; ++n) {
         const long long len = (nc + n - 1) / n;
         for (long long d = 1; d <= (n == 1 ? 1 : 4); d *= 2) {
             const long long win = (len + d - 1) / d;
-            const double walk = rounds(rows * n * heads + more) * (4.0 * (double)(win * d) + 6 + 0.5 * (double)((n - 1) * d));
-            const double states = n == 1 ? 0 : rounds(rows * (n - 1) * d * (walks > 1 ? 2 : 1) * p->H + more) * (2.2 * (double)win + 6) + 2;
+            const double walk = time(rows * n * heads, 4.0 * (double)(win * d) + 6 + 0.5 * (double)((n - 1) * d), more * heads, 10);
+            const double states = n == 1 ? 0 : time(rows * (n - 1) * d * pairs, 2.2 * (double)win + 6, more * pairs, 1) + 2;
             if (best < 0 || walk + states < best) best = walk + states, a->main_len = (int)(win * d * LC), a->win_len = (int)(win * LC);
         }
     }

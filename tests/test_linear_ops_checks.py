@@ -121,7 +121,7 @@ def test_lin_workspaces(lib):
 
 def test_lin_workspace_of_many_sequences(lib):
     """The states that segments exchange are those of intervals of the token axis, of the heads' own size, however many sequences
-    a packed batch has."""
+    a packed batch has; and a batch of many short ones is not cut."""
     n = ctypes.c_size_t()
 
     def size(T, N, H=32, K=128, V=128, backward=0):
@@ -135,6 +135,8 @@ def test_lin_workspace_of_many_sequences(lib):
                 # at most a state of 64 KB of every chunk, head and walk (q, k, v and o: 128 KB)
                 assert size(T, N, H, backward=b) <= (1 + b) * (T // 128 + 1) * H * 65536, (T, H, N, b)
     assert size(65536, 3, 4) > 0 and size(65536, 3, 4, 32, 64) <= size(65536, 3, 4) // 8 + 512
+    for T, N in ((16384, 1024), (8192, 4096)):
+        assert size(T, N) == 0 and size(T, N, backward=1) == 0
 
 
 def gated(**kw):
