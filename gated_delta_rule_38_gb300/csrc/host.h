@@ -59,6 +59,7 @@ inline bool touches(const void *p, size_t n, const void *q, size_t rows, size_t 
     if (row >= rows) return false;
     return (a - b) % ld < width || (row + 1 < rows && a + n > b + (row + 1) * ld);
 }
+inline bool overlap(const void *p, size_t n, const void *q, size_t m) { return touches(p, n, q, 1, m, m); }
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 inline size_t esize(gdr_dtype d) { return d == GDR_FP32 ? 4 : 2; }
 inline bool is_half(gdr_dtype d) { return d == GDR_BF16 || d == GDR_FP16; }

@@ -97,6 +97,13 @@ bool token_map(CUtensorMap *m, const gdr_lin_problem *p, const void *t, int64_t 
     return make_tmap_3d(m, t, p->dtype == GDR_BF16, (uint64_t)cols, (uint64_t)heads, (uint64_t)p->B * p->T, (uint64_t)cols * 2,
                         (uint64_t)ld * 2, 64, 1, LC);
 }
+// Whether `n` bytes from `out` touch an input of all calls: tokens, decays or offsets.
+bool over_inputs(const gdr_lin_problem *p, const void *out, size_t n, const void *q, const void *k, const void *v, const float *decay) {
+    const size_t tokens = (size_t)p->B * p->T, qk = (size_t)p->Hk * p->K * 2, vw = (size_t)p->H * p->V * 2;
+    return touches(out, n, q, tokens, qk, (size_t)p->q_ld * 2) || touches(out, n, k, tokens, qk, (size_t)p->k_ld * 2) ||
+           touches(out, n, v, tokens, vw, (size_t)p->v_ld * 2) || overlap(out, n, decay, (size_t)p->H * 4) ||
+           overlap(out, n, p->cu_seqlens, ((size_t)p->num_seqs + 1) * 4);
+}
 // A tensor of tokens: 16-byte aligned, rows on 16-byte boundaries.
 bool tokens_ok(const void *t, int64_t ld) { return aligned16(t) && ld % 8 == 0; }
 
@@ -127,11 +134,10 @@ gdr_status gdr_lin_fwd(const gdr_lin_problem *p, const void *q, const void *k, c
         !aligned16(state_in) || !aligned16(state_out))
         return GDR_ERR_ALIGN;
     const int N = p->cu_seqlens ? p->num_seqs : p->B;
-    const size_t qk = (size_t)p->Hk * p->K * 2, vw = (size_t)p->H * p->V * 2, sb = (size_t)N * p->H * p->K * p->V * 4;
+    const size_t vw = (size_t)p->H * p->V * 2, sb = (size_t)N * p->H * p->K * p->V * 4;
     // segments of a sequence read its start state while another one writes the end state; tiles are read ahead of the output
-    if (touches(state_out, sb, state_in, 1, sb, sb) || touches(o, tokens * vw, state_in, 1, sb, sb) ||
-        touches(o, tokens * vw, state_out, 1, sb, sb) || touches(o, tokens * vw, q, tokens, qk, (size_t)p->q_ld * 2) ||
-        touches(o, tokens * vw, k, tokens, qk, (size_t)p->k_ld * 2) || touches(o, tokens * vw, v, tokens, vw, (size_t)p->v_ld * 2))
+    if (overlap(state_out, sb, state_in, sb) || overlap(o, tokens * vw, state_in, sb) || overlap(o, tokens * vw, state_out, sb) ||
+        over_inputs(p, o, tokens * vw, q, k, v, decay) || over_inputs(p, state_out, sb, q, k, v, decay))
         return GDR_ERR_UNSUPPORTED;
     const Layout l = layout_of(p, false);
     if (l.bytes && (!workspace || workspace_bytes < l.bytes)) return GDR_ERR_WORKSPACE;
@@ -167,11 +173,8 @@ gdr_status gdr_lin_step(const gdr_lin_problem *p, const void *q, const void *k, 
     if (!q || !k || !v || !decay || !state || !o) return GDR_ERR_NULL;
     if (!aligned_to(q, 2) || !aligned_to(k, 2) || !aligned_to(v, 2) || !aligned_to(o, 2) || !aligned_to(decay, 4) || !aligned16(state))
         return GDR_ERR_ALIGN;
-    const size_t tokens = (size_t)p->B * p->T, qk = (size_t)p->Hk * p->K * 2, vw = (size_t)p->H * p->V * 2;
-    const size_t sb = (size_t)p->B * p->H * p->K * p->V * 4;
-    if (touches(o, tokens * vw, q, tokens, qk, (size_t)p->q_ld * 2) || touches(o, tokens * vw, k, tokens, qk, (size_t)p->k_ld * 2) ||
-        touches(o, tokens * vw, v, tokens, vw, (size_t)p->v_ld * 2) || touches(o, tokens * vw, state, 1, sb, sb))
-        return GDR_ERR_UNSUPPORTED;
+    const size_t ob = (size_t)p->B * p->T * p->H * p->V * 2, sb = (size_t)p->B * p->H * p->K * p->V * 4;
+    if (overlap(o, ob, state, sb) || over_inputs(p, o, ob, q, k, v, decay) || over_inputs(p, state, sb, q, k, v, decay)) return GDR_ERR_UNSUPPORTED;
     unsigned *err = nullptr;
     if ((st = device_state(&err)) != GDR_OK) return st;
     StepArgs a = {};
@@ -194,17 +197,16 @@ gdr_status gdr_lin_bwd(const gdr_lin_problem *p, const void *q, const void *k, c
         return GDR_ERR_ALIGN;
     const int N = p->cu_seqlens ? p->num_seqs : p->B;
     const size_t qk = (size_t)p->Hk * p->K * 2, vw = (size_t)p->H * p->V * 2, sb = (size_t)N * p->H * p->K * p->V * 4;
-    if (touches(dq, tokens * qk, dk, 1, tokens * qk, tokens * qk) || touches(dq, tokens * qk, dv, 1, tokens * vw, tokens * vw) ||
-        touches(dk, tokens * qk, dv, 1, tokens * vw, tokens * vw))
-        return GDR_ERR_UNSUPPORTED;
-    for (const void *out : {dq, dk, dv}) {
-        const size_t n = tokens * (out == dv ? vw : qk);
-        if (touches(out, n, q, tokens, qk, (size_t)p->q_ld * 2) || touches(out, n, k, tokens, qk, (size_t)p->k_ld * 2) ||
-            touches(out, n, v, tokens, vw, (size_t)p->v_ld * 2) || touches(out, n, dout, tokens, vw, vw) ||
-            touches(out, n, state_in, 1, sb, sb) || touches(out, n, dstate_out, 1, sb, sb) || touches(out, n, dstate_in, 1, sb, sb))
+    const void *outs[] = {dq, dk, dv, dstate_in};
+    const size_t sizes[] = {tokens * qk, tokens * qk, tokens * vw, sb};
+    for (int i = 0; i < 4; ++i) {
+        const void *out = outs[i];
+        const size_t n = sizes[i];
+        if (over_inputs(p, out, n, q, k, v, decay) || overlap(out, n, dout, tokens * vw) || overlap(out, n, state_in, sb) || overlap(out, n, dstate_out, sb))
             return GDR_ERR_UNSUPPORTED;
+        for (int e = 0; e < i; ++e)
+            if (overlap(out, n, outs[e], sizes[e])) return GDR_ERR_UNSUPPORTED;
     }
-    if (touches(dstate_in, sb, dstate_out, 1, sb, sb) || touches(dstate_in, sb, state_in, 1, sb, sb)) return GDR_ERR_UNSUPPORTED;
     const Layout l = layout_of(p, true);
     if (l.bytes && (!workspace || workspace_bytes < l.bytes)) return GDR_ERR_WORKSPACE;
     if (l.bytes && !aligned_to(workspace, 256)) return GDR_ERR_ALIGN;

@@ -113,7 +113,9 @@ gdr_status gdr_gated_norm_fwd(const gdr_gated_norm_problem *p, const void *x, co
     if (!aligned16(x) || !aligned16(gate) || !aligned16(y) || !aligned16(weight) || !rows_ok(p->D, p->x_ld, row) || !rows_ok(p->D, p->gate_ld, row))
         return GDR_ERR_ALIGN;
     const size_t wide = (size_t)p->heads * p->D * 2;
-    if (over(y, p->tokens, wide, x, p->x_ld * 2) || over(y, p->tokens, wide, gate, p->gate_ld * 2)) return GDR_ERR_UNSUPPORTED;
+    if (over(y, p->tokens, wide, x, p->x_ld * 2) || over(y, p->tokens, wide, gate, p->gate_ld * 2) ||
+        overlap(y, p->tokens * wide, weight, p->D * esize(p->weight_dtype)))
+        return GDR_ERR_UNSUPPORTED;
     unsigned *err = nullptr;
     if ((st = device_state(&err)) != GDR_OK) return st;
     RowArgs a = {};
@@ -143,11 +145,18 @@ gdr_status gdr_gated_norm_bwd(const gdr_gated_norm_problem *p, const void *x, co
     if (!aligned16(x) || !aligned16(gate) || !aligned16(dy) || !aligned16(dx) || !aligned16(dgate) || !aligned16(weight) ||
         !aligned_to(dweight, esize(p->weight_dtype)) || !rows_ok(p->D, p->x_ld, row) || !rows_ok(p->D, p->gate_ld, row))
         return GDR_ERR_ALIGN;
-    const size_t wide = (size_t)p->heads * p->D * 2;
-    for (const void *o : {dx, dgate})
-        if (over(o, p->tokens, wide, x, p->x_ld * 2) || over(o, p->tokens, wide, gate, p->gate_ld * 2) || over(o, p->tokens, wide, dy, wide))
+    const size_t wide = (size_t)p->heads * p->D * 2, all = p->tokens * wide, wb = p->D * esize(p->weight_dtype);
+    const void *outs[] = {dx, dgate, dweight};
+    const size_t sizes[] = {all, all, wb};
+    for (int i = 0; i < 3; ++i) {
+        const void *o = outs[i];
+        const size_t n = sizes[i];
+        if (touches(o, n, x, p->tokens, wide, p->x_ld * 2) || touches(o, n, gate, p->tokens, wide, p->gate_ld * 2) || overlap(o, n, dy, all) ||
+            overlap(o, n, weight, wb))
             return GDR_ERR_UNSUPPORTED;
-    if (over(dx, p->tokens, wide, dgate, wide)) return GDR_ERR_UNSUPPORTED;
+        for (int k = 0; k < i; ++k)
+            if (overlap(o, n, outs[k], sizes[k])) return GDR_ERR_UNSUPPORTED;
+    }
     if (need && (!workspace || workspace_bytes < need)) return GDR_ERR_WORKSPACE;
     if (need && !aligned_to(workspace, 256)) return GDR_ERR_ALIGN;
     unsigned *err = nullptr;
@@ -174,15 +183,16 @@ gdr_status gdr_block_norm_fwd(const gdr_block_norm_problem *p, const void *x, co
     if (st != GDR_OK) return st;
     if (p->rows == 0) return GDR_OK;
     if (!x || !residual || !weight || !y || !residual_out) return GDR_ERR_NULL;
-    const size_t rs = esize(p->residual_dtype), n = (size_t)p->rows, D = p->D;
+    const size_t rs = esize(p->residual_dtype), n = (size_t)p->rows, D = p->D, wb = D * esize(p->weight_dtype);
     if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(post_weight) || !aligned16(gate) || !aligned16(y) ||
         !aligned16(residual_out) || !rows_ok(p->D, p->x_ld, p->D) || (gate && !rows_ok(p->D, p->gate_ld, p->D)))
         return GDR_ERR_ALIGN;
     // (residual_out may be the residual itself: a thread writes what only it has read; not another overlap of the two)
-    if (over(y, n, 2 * D, x, p->x_ld * 2) || over(y, n, 2 * D, gate, p->gate_ld * 2) || touches(y, n * 2 * D, residual, 1, n * rs * D, n * rs * D) ||
-        touches(y, n * 2 * D, residual_out, 1, n * rs * D, n * rs * D) || over(residual_out, n, rs * D, x, p->x_ld * 2) ||
+    if (over(y, n, 2 * D, x, p->x_ld * 2) || over(y, n, 2 * D, gate, p->gate_ld * 2) || overlap(y, n * 2 * D, residual, n * rs * D) ||
+        overlap(y, n * 2 * D, residual_out, n * rs * D) || over(residual_out, n, rs * D, x, p->x_ld * 2) ||
         over(residual_out, n, rs * D, gate, p->gate_ld * 2) ||
-        (residual_out != residual && touches(residual_out, n * rs * D, residual, 1, n * rs * D, n * rs * D)))
+        (residual_out != residual && overlap(residual_out, n * rs * D, residual, n * rs * D)) || overlap(y, n * 2 * D, weight, wb) ||
+        overlap(y, n * 2 * D, post_weight, wb) || overlap(residual_out, n * rs * D, weight, wb) || overlap(residual_out, n * rs * D, post_weight, wb))
         return GDR_ERR_UNSUPPORTED;
     unsigned *err = nullptr;
     if ((st = device_state(&err)) != GDR_OK) return st;
@@ -219,15 +229,17 @@ gdr_status gdr_block_norm_bwd(const gdr_block_norm_problem *p, const void *x, co
         !aligned16(dresidual) || !aligned16(dx) || !aligned16(dresidual_in) || !aligned16(dgate) || !aligned_to(dweight, ws) ||
         !aligned_to(dpost_weight, ws) || !rows_ok(p->D, p->x_ld, p->D) || (gate && !rows_ok(p->D, p->gate_ld, p->D)))
         return GDR_ERR_ALIGN;
-    for (const void *o : {(const void *)dx, (const void *)dresidual_in, (const void *)dgate}) {
-        const size_t w = (o == dresidual_in ? rs : 2) * D;
-        if (over(o, n, w, x, p->x_ld * 2) || over(o, n, w, gate, p->gate_ld * 2) || touches(o, n * w, h, 1, n * rs * D, n * rs * D) ||
-            touches(o, n * w, dy, 1, n * 2 * D, n * 2 * D) || touches(o, n * w, dresidual, 1, n * rs * D, n * rs * D))
+    const void *outs[] = {dx, dresidual_in, dgate, dweight, dpost_weight};
+    const size_t sizes[] = {n * 2 * D, n * rs * D, n * 2 * D, D * ws, D * ws};
+    for (int i = 0; i < 5; ++i) {
+        const void *o = outs[i];
+        const size_t b = sizes[i];
+        if (touches(o, b, x, n, 2 * D, p->x_ld * 2) || touches(o, b, gate, n, 2 * D, p->gate_ld * 2) || overlap(o, b, h, n * rs * D) ||
+            overlap(o, b, dy, n * 2 * D) || overlap(o, b, dresidual, n * rs * D) || overlap(o, b, weight, D * ws) || overlap(o, b, post_weight, D * ws))
             return GDR_ERR_UNSUPPORTED;
+        for (int k = 0; k < i; ++k)
+            if (overlap(o, b, outs[k], sizes[k])) return GDR_ERR_UNSUPPORTED;
     }
-    if (over(dx, n, 2 * D, dgate, 2 * D) || touches(dresidual_in, n * rs * D, dx, 1, n * 2 * D, n * 2 * D) ||
-        touches(dresidual_in, n * rs * D, dgate, 1, n * 2 * D, n * 2 * D))
-        return GDR_ERR_UNSUPPORTED;
     if (need && (!workspace || workspace_bytes < need)) return GDR_ERR_WORKSPACE;
     if (need && !aligned_to(workspace, 256)) return GDR_ERR_ALIGN;
     unsigned *err = nullptr;

@@ -238,3 +238,47 @@ def test_python_surface_needs_cuda_tensors():
               lambda: gdr.block_norm_fwd(x, x, w), lambda: gdr.block_norm(x, x, w), lambda: gdr.block_norm_bwd(x, x, w, x), lambda: gdr.block_norm_fwd(None, x, w)):
         with pytest.raises(ValueError):
             f()
+
+
+def test_outputs_over_small_inputs(lib):
+    """Decays, offsets and weights are inputs too, and states and weights' gradients outputs, as far as the last of their bytes."""
+    cu, nb = P + 40 * FAR, 4  # offsets of three sequences, decays of four heads
+    p, sb = lin(B=1, T=600, cu_seqlens=cu, num_seqs=3), 3 * 4 * 64 * 96 * 4
+    a = far(FWD)
+    last = dict(q=(599 * 128 + 127) * 2, k=(599 * 128 + 127) * 2, v=(599 * 384 + 383) * 2, decay=nb * 4 - 4, s=sb - 4)
+    for n in ("o", "f"):
+        for m, off in last.items():
+            assert fwd(lib, p, **{n: (a[m] + off) // 16 * 16}) == UNSUPPORTED, (n, m)
+        assert fwd(lib, p, **{n: cu}) == UNSUPPORTED, n
+    a = far(BWD)
+    last = dict(last, do=(600 * 384 - 1) * 2, df=sb - 4)
+    for n in ("dq", "dk", "dv", "ds"):
+        for m, off in last.items():
+            assert bwd(lib, p, **{n: (a[m] + off) // 16 * 16}) == UNSUPPORTED, (n, m)
+        assert bwd(lib, p, **{n: cu}) == UNSUPPORTED, n
+        for m in {"dq", "dk", "dv", "ds"} - {n}:
+            assert bwd(lib, p, **{n: a[m]}) == UNSUPPORTED, (n, m)
+    p = lin()
+    step = ("q", "k", "v", "decay", "s", "o")
+    a = far(step)
+    for n in ("o", "s"):
+        for m in ("q", "k", "v", "decay"):
+            assert call(lib.gdr_lin_step, step, p, **{n: a[m]}) == UNSUPPORTED, (n, m)
+    a, p = far(G_FWD), gated()
+    assert call(lib.gdr_gated_norm_fwd, G_FWD, p, y=a["w"] + 64 * 4 - 16) == UNSUPPORTED
+    a = far(G_BWD)
+    for n in ("dx", "dg", "dw"):
+        for m in {"x", "g", "w", "dy", "dx", "dg", "dw"} - {n}:
+            assert call(lib.gdr_gated_norm_bwd, G_BWD, p, 1 << 40, **{n: a[m]}) == UNSUPPORTED, (n, m)
+    a, p = far(B_FWD), block()
+    for n in ("y", "h"):
+        for m in ("w", "pw"):
+            assert call(lib.gdr_block_norm_fwd, B_FWD, p, **{n: a[m] + 64 * 4 - 16}) == UNSUPPORTED, (n, m)
+    a = far(B_BWD)
+    outs = ("dx", "dri", "dw", "dpw", "dg")
+    for n in outs:
+        for m in {"x", "h", "w", "pw", "g", "dy", "dr", *outs} - {n}:
+            assert call(lib.gdr_block_norm_bwd, B_BWD, p, 1 << 40, **{n: a[m]}) == UNSUPPORTED, (n, m)
+    # without a gate or a post_weight their addresses are nobody's
+    none = dict(g=None, dg=None, pw=None, dpw=None)
+    assert call(lib.gdr_block_norm_bwd, B_BWD, p, 1 << 40, dw=a["dpw"], **none) != UNSUPPORTED
