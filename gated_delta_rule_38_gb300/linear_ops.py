@@ -13,7 +13,7 @@ import torch
 
 from . import _lib
 from ._args import _check, _check_cu, _cu, _need, _rows
-from .layer_ops import _once, _p, _s, _tokens
+from .layer_ops import _on16, _once, _p, _s, _tokens
 
 __all__ = ["linear_attention", "linear_attention_fwd", "linear_attention_bwd", "linear_attention_step"]
 
@@ -66,6 +66,7 @@ def linear_attention_fwd(q, k, v, decay, scale=None, initial_state=None, output_
     p, q, k, v, sshape = _problem(q, k, v, decay, scale, cu)
     if initial_state is not None:
         _need(initial_state, "initial_state", sshape, torch.float32, q)
+        initial_state = _on16(initial_state)
     if out is not None:
         _need(out, "out", v.shape, v.dtype, q)
     lib = _lib.load()
@@ -99,6 +100,7 @@ def linear_attention_bwd(q, k, v, decay, do, scale=None, initial_state=None, dfi
     for name, t in (("initial_state", initial_state), ("dfinal_state", dfinal_state)):
         if t is not None:
             _need(t, name, sshape, torch.float32, q)
+    initial_state, dfinal_state = _on16(initial_state), _on16(dfinal_state)
     lib = _lib.load()
     dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
     ds = None if initial_state is None else torch.empty_like(initial_state)

@@ -440,3 +440,35 @@ def test_many_steps(decay):
     gdr.linear_attention_step(x["q"], x["k"], x["v"], d, state)
     fw = ref.attn(*(lref.f64(x[n], False) for n in ("q", "k", "v")), d.double().cpu(), 1.0, lref.f64(x["s0"], False), None)[1]
     ref.check(state, fw, 2.0 ** -24 * (2 * T / 3) ** 0.5, "state")
+
+
+def test_states_off_16_bytes():
+    """States and their gradients that begin anywhere (pieces of a flat buffer, the gradient of a concatenation): copied."""
+    x, d = make(2, 200, 2, 2, 64, 64), slopes(2)
+
+    def off(t):
+        o = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape).copy_(t)
+        assert o.data_ptr() % 16
+        return o
+
+    def both(f):
+        o, fin = gdr.linear_attention_fwd(x["q"], x["k"], x["v"], d, initial_state=f(x["s0"]), output_final_state=True)
+        return o, fin, *gdr.linear_attention_bwd(x["q"], x["k"], x["v"], d, f(x["do"]), initial_state=f(x["s0"]), dfinal_state=f(x["ds"]))
+
+    assert all(torch.equal(a, b) for a, b in zip(both(lambda t: t), both(off)))
+    leaves = [x[n].clone().requires_grad_() for n in ("q", "k", "v", "s0")]
+    grads = []
+    for flat in (True, False):
+        o, fin = gdr.linear_attention(*leaves[:3], d, initial_state=leaves[3], output_final_state=True)
+        w = (x["ds"], x["do"].float())
+        if flat:  # (the gradient of the states then begins 4 bytes into a buffer)
+            both_flat = torch.cat([o.float().sum()[None] * 0, fin.flatten(), o.float().flatten()])
+            loss = (both_flat * torch.cat([torch.zeros(1, device="cuda"), *(t.flatten() for t in w)])).sum()
+        else:
+            loss = (fin * w[0]).sum() + (o.float() * w[1]).sum()
+        grads.append(torch.autograd.grad(loss, leaves))
+    for a, b in zip(*grads):
+        ref.check(a, b, 1e-6, "gradient")
+    # what is updated or written in place cannot be copied: refused
+    with pytest.raises(gdr.GdrError):
+        gdr.linear_attention_step(x["q"][:, :1], x["k"][:, :1], x["v"][:, :1], d, off(x["s0"]))
