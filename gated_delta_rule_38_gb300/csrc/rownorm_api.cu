@@ -26,12 +26,15 @@ norm::NormShape shape_of(int D) {
     s.threads = s.tpr * s.rpb;
     return s;
 }
-// Blocks an SM that the kernels' registers allow: two of 256 threads, but three of the gated norm's forward and of
+// Blocks an SM, as the forms' launch bounds have it: two of 256 threads, but three of the gated norm's forward and of
 // whole-vector forwards; of smaller blocks as many more (8192 x 2560, gated norm's backward: 62 us with two of 160, 54 so).
+// Of more threads one.  (Whole-vector forwards take 80 to 96 registers, which would leave room for a second block of up to 384
+// threads, but their form is one for up to 512: 8192 rows of 4096 columns take 34 us in the gated norm's forward, of 4104 58.)
 // Shifted rows have a form of 320 threads, two an SM with 96 registers (one of 288 with 112 is 4 % faster up to 4600 columns
-// and a quarter slower from there to 5112, where one block is left).
+// and a quarter slower from there to 5112, where one block is left).  Four vectors a thread: one block of any size, with 104 to
+// 128 registers (two of 288 threads, which do not fit, as the grid: 4096 x 8193, gated norm's backward 174 us, 167 so).
 int blocks_an_sm(const norm::NormShape &s, bool shift, bool two) {
-    if (s.threads > 256) return s.threads > (shift ? 320 : 256) ? 1 : 2;
+    if (s.threads > 256) return s.nv == 2 && shift && s.threads <= 320 ? 2 : 1;
     return (two ? 2 : 3) * 256 / s.threads;
 }
 RowForm form_of(RowArgs *a, bool bwd, bool gated) {

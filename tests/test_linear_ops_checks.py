@@ -282,3 +282,13 @@ def test_outputs_over_small_inputs(lib):
     # without a gate or a post_weight their addresses are nobody's
     none = dict(g=None, dg=None, pw=None, dpw=None)
     assert call(lib.gdr_block_norm_bwd, B_BWD, p, 1 << 40, dw=a["dpw"], **none) != UNSUPPORTED
+
+
+@pytest.mark.parametrize("D", [8193, 9001, 10191, 10201, 12288, 16375, 16384])
+def test_partial_rows_are_as_many_as_fit(lib, D):
+    """Four vectors a thread, one block an SM: no more blocks leave partial rows than run at once."""
+    n = ctypes.c_size_t()
+    assert lib.gdr_gated_norm_bwd_workspace_size(ctypes.byref(gated(tokens=100000, heads=1, D=D, x_ld=D, gate_ld=D)), ctypes.byref(n)) == 0
+    assert n.value <= 152 * D * 4 + 255
+    assert lib.gdr_block_norm_bwd_workspace_size(ctypes.byref(block(rows=100000, D=D, x_ld=D, gate_ld=D)), ctypes.byref(n)) == 0
+    assert n.value <= 2 * 152 * D * 4 + 255
