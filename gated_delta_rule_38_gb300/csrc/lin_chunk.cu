@@ -25,17 +25,19 @@
 // to L2.  Loops that can stay loops do: unrolled, a chunk's code no longer fitted the instruction caches next to the
 // schedulers.  (1 x 2048 tokens, 152 heads, one walk a CTA, 318 MB: 156 us with spills, 72 with sixteen warps through all
 // steps together, 60 so, which is 5.3 TB/s, or 3.8 us a chunk; the matrix instructions take half of them.)
-// The states inside are without their scale's power of two (of the gradients' walks), which the keys then need not carry:
-// in fp16 their remainders would fall below its range.
+// The states inside are without their scale's power of two (of the gradients' walks), which the keys then need not carry.
+// P and the state's copy are rounded to 16 bits, as operands of the tensor core: with the output's own rounding that makes
+// outputs 1.4 times as far from 64 bits as one rounding would (bf16 2.3e-3, fp16 2.9e-4).  A second number for each would take
+// two more products a chunk, and a 32 KB tile that shared memory does not have.
 // A decayed key is a sum of 16-bit numbers, the rounded one and what that leaves, each with a product of its own, the
 // smallest first: the accumulator loses at each addition by what it holds.  Two of fp16 make 22 bits and states 2e-7 off
 // (of one number: 1e-3); the second is held times 2^11, or below a key of 0.1 it would be a subnormal number, and its
-// products' sum is scaled back when the first number's are added (keys of 1e-3: states 2e-5 off without).  Two of bf16 make 17 bits and 2.5e-6, which outputs of 8 bits do not show; states that are handed
-// on get a third where the chunk weighs over an eighth in them (3e-7).  Its place is the state's copy's, free between Q S
-// and the next copy, and warps 8..11 make all the keys of such a chunk: the state's warps have no registers for it.
-// (2 x 4096 tokens, 32 heads of memories of 100 tokens: 88 us with the final states, 79 without; where nothing decays, so
-// that every chunk has three, 110.)  The products' loop stays a loop: with its bodies side by side the training step of
-// 2 x 4096 tokens took 296 us, 287 so.
+// products' sum is scaled back when the first number's are added (keys of 1e-3: states 2e-5 off without).  Two of bf16 make
+// 17 bits and 2.5e-6, which outputs of 8 bits do not show; states that are handed on get a third where the chunk weighs over
+// an eighth in them (3e-7).  Its place is the state's copy's, free between Q S and the next copy, and warps 8..11 make all the
+// keys of such a chunk: the state's warps have no registers for it.  (2 x 4096 tokens, 32 heads of memories of 100 tokens: 88
+// us with the final states, 79 without; where nothing decays, so that every chunk has three, 110.)  The products' loop stays
+// a loop: with its bodies side by side the training step of 2 x 4096 tokens took 296 us, 287 so.
 // The accumulators of one chunk's state update start from zero and are added to the state in fp32 registers, rounded to
 // nearest: in the tensor core's own accumulator the additions of a long walk would lose in one direction.
 // lambda^128 is kept as two fp32 numbers, so that a memory of any length is not off by what rounding it once would add up to.
@@ -63,8 +65,7 @@ constexpr uint32_t S_ST = S_LO + TILE;            // the state's copy (state pas
 constexpr uint32_t S_BAR = S_ST + TILE;
 constexpr uint32_t B_FULL = S_BAR, B_EMPTY = S_BAR + 8 * RING, B_QK = B_EMPTY + 8 * RING, B_S = B_QK + 8, B_P = B_S + 8,
                    B_PV = B_P + 8, B_K = B_PV + 8, B_DS = B_K + 16, B_DONE = B_DS + 16, B_QS = B_DONE + 8, B_MAX = B_QS + 8,
-                   S_SLOT = B_MAX + 16,
-                   S_FLAG = S_SLOT + 4;
+                   S_SLOT = B_MAX + 16, S_FLAG = S_SLOT + 4;
 constexpr uint32_t S_FROM = S_FLAG + 4;           // the first chunk whose decayed keys are three numbers
 constexpr uint32_t S_LAM = S_FLAG + 8;            // lambda^128 as two fp32 numbers
 // decays of up to 31 tokens: COL[c] = lambda^(31-c) (rev: lambda^c); DIAG[31 + row - key] = s_kv s_out lambda^|row - key| where

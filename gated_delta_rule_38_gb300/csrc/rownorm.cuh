@@ -317,8 +317,9 @@ __device__ __forceinline__ void walk(const R &rows, const RowArgs &a, F &&body) 
 
 // ---------------------------------------------------------------- gated norm
 
-// 8192 x 32 x 128 bf16: 34.5 us for 201 MB, 5.8 TB/s; 5311 x 4099 fp16: 43 us for 131 MB, 3.0 TB/s, bound by issue (an odd width
-// has 2 more vectors than 256 threads, and a second block of 288 leaves 96 registers).
+// 8192 x 32 x 128 bf16: 34.5 us for 201 MB, 5.8 TB/s; 8192 x 4104: 58 us, 8192 x 8192: 72 for 403 MB, with one block an SM;
+// 5311 x 4099 fp16: 43 us for 131 MB, 3.0 TB/s, bound by issue (an odd width has 2 more vectors than 256 threads, and a second
+// block of 288 leaves 96 registers).
 template <typename T, int NG, int BT, bool SHIFT>
 __global__ void __launch_bounds__(BT, BT > 320 ? 1 : BT > 256 ? 2 : 3) gated_fwd_kernel(const __grid_constant__ RowArgs a) {
     extern __shared__ __align__(16) char s_rows[];
@@ -351,8 +352,9 @@ __global__ void __launch_bounds__(BT, BT > 320 ? 1 : BT > 256 ? 2 : 3) gated_fwd
     });
 }
 
-// 8192 x 32 x 128 bf16: 59.5 us for 336 MB, 5.6 TB/s, and 8 us of reduction; 5311 x 4099 fp16: 90 us for 218 MB.  (A row more
-// ahead: 62 and 107 us; what is on its way is not what is short.)
+// 8192 x 32 x 128 bf16: 59.5 us for 336 MB, 5.6 TB/s, and 8 us of reduction; 8192 x 8192: 137 for 671 MB with it; 5311 x 4099
+// fp16: 90 us for 218 MB, with 120 bytes a thread spilled at 96 registers.  (A row more ahead: 62 and 107 us; what is on its
+// way is not what is short.)  The forms of four vectors spill 196 to 408 bytes: 8192 x 16384 takes 317 us, floor 201.
 template <typename T, int NG, int BT, bool SHIFT>
 __global__ void __launch_bounds__(BT, BT > 320 ? 1 : 2) gated_bwd_kernel(const __grid_constant__ RowArgs a) {
     extern __shared__ __align__(16) char s_rows[];
@@ -410,7 +412,7 @@ __global__ void __launch_bounds__(BT, BT > 320 ? 1 : 2) gated_bwd_kernel(const _
 // ---------------------------------------------------------------- block norm
 
 // 8192 x 4096 bf16 with a gate: 66 us from a bf16 stream (335 MB, 5.1 TB/s), 79 from an fp32 one (470 MB, 5.9 TB/s; 100 with
-// 16 bytes a lane at a stride of 32, which asks for every sector twice).
+// 16 bytes a lane at a stride of 32, which asks for every sector twice).  8192 x 8192: 135 us for 671 MB; 8192 x 4099: 105.
 template <typename T, int NG, int BT, bool SHIFT, bool F32, bool GATE>
 __global__ void __launch_bounds__(BT, BT > 320 ? 1 : BT > 256 || SHIFT ? 2 : 3) block_fwd_kernel(const __grid_constant__ RowArgs a) {
     // Weights come from the L1 cache row by row: held in registers they cost the third block an SM (8192 x 4096 bf16: 71 us with,
@@ -479,7 +481,8 @@ __global__ void __launch_bounds__(BT, BT > 320 ? 1 : BT > 256 || SHIFT ? 2 : 3) 
 }
 
 // 8192 x 4096 bf16 with a gate: 123 us for 537 MB, 4.4 TB/s, bound by issue: some 600 instructions a warp and row, a third of
-// them the sigmoid and its derivative.  (One group a thread in blocks of 512: 181 us.)
+// them the sigmoid and its derivative.  (One group a thread in blocks of 512: 181 us.)  8192 x 8192: 249 us for 1.07 GB; of odd
+// widths the form of 320 threads spills 436 to 536 bytes a thread at 96 registers: 8192 x 4099 takes 265 us, floor 80.
 template <typename T, int NG, int BT, bool SHIFT, bool F32, bool GATE>
 __global__ void __launch_bounds__(BT, BT > 320 ? 1 : 2) block_bwd_kernel(const __grid_constant__ RowArgs a) {
     constexpr bool HOLD = NG <= 2;

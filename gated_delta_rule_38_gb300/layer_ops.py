@@ -306,7 +306,7 @@ def block_norm_fwd(x, residual, weight, post_weight=None, gate=None, gate_activa
 
         b = x / sqrt(mean(x^2) + eps) * post_weight      (x itself without a post_weight)
         residual_out = residual + residual_scale * b * act(gate)
-        y = residual_out / sqrt(mean(residual_out^2) + eps) * weight
+        y = residual_out / sqrt(mean(residual_out^2) + eps) * weight        (from the sum before it is rounded to its type)
 
     x [..., D] bf16 or fp16; residual [..., D] of x's type or fp32, as residual_out; weight and post_weight [D] of x's type
     or fp32 (both the same); gate [..., D] of x's type through ``gate_activation`` (None: as it is, "sigmoid", "silu").
