@@ -472,3 +472,13 @@ def test_states_off_16_bytes():
     # what is updated or written in place cannot be copied: refused
     with pytest.raises(gdr.GdrError):
         gdr.linear_attention_step(x["q"][:, :1], x["k"][:, :1], x["v"][:, :1], d, off(x["s0"]))
+
+
+@pytest.mark.parametrize("case", [(24, 2000, (130, 1000, 0, 870)), (24, 2000, (0, 1999, 1, 0)), (8, 1500, (5, 700, 0, 300, 1, 400, 94)),
+                                  (16, 2000, (256, 768, 512, 464)), (16, 1500, (1, 1, 1, 1497))], ids=str)
+def test_packed_windows(case):
+    """Cut packed batches whose segments have several windows before (backwards: behind) them, in a direction at least, and whose
+    sequences begin and end inside windows, on them and on the cuts: every exchanged state in its place."""
+    H, T, lens = case
+    for dt, K, V in ((BF, 32, 48), (FH, 64, 16)):
+        compare(make(1, T, H, H, K, V, lens, True, dt), torch.full((H,), -0.002, device="cuda"), lens, dt)
